@@ -229,6 +229,144 @@ moe_status moe_backward(const moe_dims* dims, const void* dY, const void* X, con
                         void* dW_up, void* dW_down, float* dS, float* dLogits, void* dW_r,
                         void* ws, size_t ws_bytes, void* stream);
 
+/* moe_backward_aux — moe_backward with further gradients of the router logits, of losses that
+ * look at the logits themselves (moe_router_loss_backward).
+ *  dLogits_aux [T,E] fp32 or NULL (then this is moe_backward): added to the layer's own logit
+ *  gradient, so dLogits receives the sum, dW_r = dLogits^T X and dX includes dLogits W_r.  Its rows
+ *  are dense, so the dX term is a GEMM over all E experts (operands in dtype) that adds to the
+ *  expert-path gradient already rounded to dtype.  Not the dLogits array itself.
+ *  The other arguments and the workspace are those of moe_backward. */
+moe_status moe_backward_aux(const moe_dims* dims, const void* dY, const void* X, const void* W_r,
+                            const void* W_gate, const void* W_up, const void* W_down,
+                            const moe_plan* plan, const void* H_cache, const float* dLogits_aux,
+                            void* dX, void* dW_gate, void* dW_up, void* dW_down, float* dS,
+                            float* dLogits, void* dW_r, void* ws, size_t ws_bytes, void* stream);
+
+/* moe_router_loss — the losses that keep a router's load even and its logits small, with the
+ * per-expert counts they are made of.  dims: T, E and K are used (d, n and dtype only have to be
+ * valid; token rounding does not enter).
+ *  logits [T,E] fp32 (with the bias, as moe_route writes them); topk_idx [T*K] int32: the plain
+ *  top-K choices (plan.topk_idx); an index outside [0, E) is not counted.
+ *  Sequences: n_seq (1 .. 2^20) runs of tokens, sequence s being tokens seq_off[s] ..
+ *  seq_off[s+1] - 1; seq_off [n_seq+1] int32, non-decreasing, within 0 .. T (sequences may be
+ *  empty, and tokens before the first or behind the last belong to none); NULL with n_seq = 1: all
+ *  T tokens.  token_mask [T] uint8 or NULL: a token with 0 (padding) does not count.
+ *  With p_t = softmax(logits_t) over the E experts, lse_t = log sum exp(logits_t), c_se the picks
+ *  of expert e by sequence s's counting tokens, T_s their number, P_se the sum of their p_te and
+ *  N = sum of T_s:
+ *   loss[0] = sum_s (T_s / N) E sum_e (c_se / (K T_s)) (P_se / T_s)    balance loss, 1 when even
+ *   loss[1] = (1 / N) sum_t lse_t^2                                    z-loss
+ *  (0 for N = 0; a sequence without counting tokens adds nothing).  One sequence gives the
+ *  batch-wide loss, several the sequence-wise one, weighted by tokens.
+ *  Outputs: seq_tokens [n_seq] int32 = T_s; seq_counts [n_seq,E] int32 = c_se; prob_sum [n_seq,E]
+ *  fp32 = P_se; lse [T] fp32 (every token's, also of those that do not count); loss [2] fp32.
+ *  A logit of -infinity (a masked expert) has probability 0; a row of -infinity only has lse
+ *  -infinity, counts its picks and adds to neither loss; NaN or +infinity makes its row's
+ *  probabilities, and with them the losses, NaN.
+ *  ws: moe_router_loss_workspace_bytes(dims, n_seq) bytes, contents on entry unused. */
+size_t moe_router_loss_workspace_bytes(const moe_dims* dims, int32_t n_seq);
+moe_status moe_router_loss(const moe_dims* dims, const float* logits, const int32_t* topk_idx,
+                           int32_t n_seq, const int32_t* seq_off, const uint8_t* token_mask,
+                           int32_t* seq_tokens, int32_t* seq_counts, float* prob_sum, float* lse,
+                           float* loss, void* ws, size_t ws_bytes, void* stream);
+
+/* moe_router_loss_backward — the losses' gradient (counts held fixed, as the choice is):
+ *   dLogits[t,e] = p_te (dloss[0] E / (K T_s N) (c_se - sum_j c_sj p_tj) + dloss[1] 2 lse_t / N)
+ *  for counting tokens, 0 for the others and for rows of -infinity only.
+ *  dloss [2] fp32, device: the weights of the two losses (times the loss scale); logits, n_seq,
+ *  seq_off, token_mask as in moe_router_loss; seq_tokens, seq_counts and lse from it.
+ *  dLogits [T,E] fp32, overwritten (not the logits array itself).  Pass it to
+ *  moe_backward_aux. */
+moe_status moe_router_loss_backward(const moe_dims* dims, const float* dloss, const float* logits,
+                                    int32_t n_seq, const int32_t* seq_off,
+                                    const uint8_t* token_mask, const int32_t* seq_tokens,
+                                    const int32_t* seq_counts, const float* lse, float* dLogits,
+                                    void* stream);
+
+/* Dropout.  Whether an element is kept is a function of its row, its column and the two words of
+ * rng, so the mask is never stored: a backward call with the same words drops the same
+ * elements.  Generator: Philox4x32-10 (Salmon, Moraes, Dror, Shaw, SC 2011) with key = seed and
+ * counter = (column / 8, row, offset low word, offset high word); element i of a group of eight
+ * columns takes 16 bits of output word i / 2, the low half for even i, and is kept where they are
+ * >= round(65536 p).  Kept values are scaled by 1 / (1 - round(65536 p) / 65536); a dropped one
+ * contributes 0 whatever it holds.  p in [0, 1].
+ *  rng: device array of 2 uint64, {seed, offset}, read by the kernel, so that a captured graph
+ *  draws a new mask when the caller changes them between replays. */
+
+/* moe_dropout — out = residual + dropout(x), or dropout(x) without a residual, which is also the
+ * gradient: dx = moe_dropout(dout) with the forward's words (the residual's gradient is dout).
+ *  x, residual, out: rows x cols of dtype (any cols >= 1, rows >= 0, rows * ceil(cols / 8) below
+ *  2^31), row strides ldx, ldr, ldo in elements (>= cols; ldr unused without a residual).  Rows
+ *  whose strides keep 16-byte alignment move in 16-byte accesses.  fp32 arithmetic, one
+ *  rounding.  out may be x or residual (with the same stride). */
+moe_status moe_dropout(int64_t rows, int64_t cols, int dtype, const void* x, int64_t ldx,
+                       const void* residual, int64_t ldr, double p, const uint64_t* rng, void* out,
+                       int64_t ldo, void* stream);
+
+/* moe_combine_dropout — moe_combine with dropout and the residual sum on its fp32 sums:
+ * out[t] = residual[t] + dropout(sum over the token's rows of w_r Y_perm[r]), rounded once.  The
+ * mask is moe_dropout's on the [T,d] output, so dY = moe_dropout(dout) is the gradient that
+ * moe_backward takes.  residual [T,d] dtype or NULL; it may be out.  A token with no rows gets its
+ * residual (or zeros). */
+moe_status moe_combine_dropout(const moe_dims* dims, const moe_plan* plan, const void* Y_perm,
+                               int weighted, const void* residual, double p, const uint64_t* rng,
+                               void* out, void* stream);
+
+/* Dense projection with bias, activation and residual in its epilogue: the shared expert or dense
+ * branch beside the routed experts (e.g. gate/up with SwiGLU, then down with the routed experts'
+ * output as residual).
+ *   z = X W^T + bias,  out = residual + act(z)
+ * act: NONE z; RELU; GELU z Phi(z) (the exact form); SILU z / (1 + exp(-z)); SWIGLU: W holds 2 N
+ * rows, N gate rows then N up rows, and act(z) = silu(z[:N]) z[N:].  N' = 2 N for SWIGLU, else N. */
+typedef enum {
+  MOE_ACT_NONE = 0,
+  MOE_ACT_RELU = 1,
+  MOE_ACT_GELU = 2,
+  MOE_ACT_SILU = 3,
+  MOE_ACT_SWIGLU = 4
+} moe_act;
+
+/* Shape (host struct).  M rows (0 .. 2^24), N output and K input features (multiples of 8,
+ * 8 .. 65536).  ldx, ldr, ldy: row strides in elements of X and dX, of residual, and of out and dY
+ * (multiples of 8; 0 = dense).  W, Z and dW are dense.  dtype: type of X, W, residual, Z, out and of the
+ * gradients dY, dX, dW; bias and dbias are fp32; accumulation is fp32.  act: a moe_act.  flags:
+ * reserved, must be 0. */
+typedef struct moe_linear_dims {
+  int64_t M;
+  int64_t N;
+  int64_t K;
+  int64_t ldx;
+  int64_t ldr;
+  int64_t ldy;
+  int32_t dtype;
+  int32_t act;
+  int32_t flags;
+} moe_linear_dims;
+
+enum { MOE_LINEAR_FORWARD = 0, MOE_LINEAR_BACKWARD = 1 };
+
+/* Host: workspace bytes of moe_linear / moe_linear_backward (0 if none; 0 for invalid dims, with
+ * moe_last_error() set). */
+size_t moe_linear_workspace_bytes(const moe_linear_dims* dims, int op);
+
+/* moe_linear — X [M,K], W [N',K], bias [N'] fp32 or NULL, residual [M,N] or NULL (it may be out),
+ * out [M,N].  Z [M,N'] or NULL: receives z rounded to dtype, for the backward.  The activation and
+ * the residual sum work on fp32 values; out is rounded once.  M = 0 does nothing.
+ * ws: moe_linear_workspace_bytes(dims, MOE_LINEAR_FORWARD) bytes. */
+moe_status moe_linear(const moe_linear_dims* dims, const void* X, const void* W, const float* bias,
+                      const void* residual, void* Z, void* out, void* ws, size_t ws_bytes,
+                      void* stream);
+
+/* moe_linear_backward — gradients of moe_linear (the residual's is dY itself):
+ *   dZ = dY act'(Z) (SWIGLU: [dG | dU]),  dX = dZ W,  dW = dZ^T X,  dbias = sum of dZ over rows.
+ *  dY [M,N]; X, W: the forward's; Z [M,N'] from it (unused and may be NULL for NONE).
+ *  dX [M,K], dW [N',K], dbias [N'] fp32: each may be NULL (not all); X is needed for dW, W for dX.
+ *  dZ is rounded to dtype as the products' operand, not in dbias.  M = 0: dW and dbias are zeros.
+ *  ws: moe_linear_workspace_bytes(dims, MOE_LINEAR_BACKWARD) bytes. */
+moe_status moe_linear_backward(const moe_linear_dims* dims, const void* dY, const void* X,
+                               const void* W, const void* Z, void* dX, void* dW, float* dbias,
+                               void* ws, size_t ws_bytes, void* stream);
+
 /* moe_decode — the whole forward layer in one kernel launch, for small token counts (decode /
  * inference): router logits, top-K with softmax, the selected experts' SwiGLU FFNs and the
  * weighted combine.  apxml.com "自定义核与核融合" (the five steps fused into one kernel) and
@@ -364,7 +502,11 @@ typedef enum {
   MOE_STAGE_FP8_QUANT = 14,  /* FP8 row quantisation (moe_quantize_fp8 and the activation's) */
   MOE_STAGE_FP8_UP = 15,     /* FP8 gate/up GEMM + SwiGLU */
   MOE_STAGE_FP8_DOWN = 16,   /* FP8 down GEMM */
-  MOE_STAGE_COUNT = 17
+  MOE_STAGE_ROUTER_LOSS = 17, /* router losses, or their gradient */
+  MOE_STAGE_DROPOUT = 18,     /* moe_dropout (moe_combine_dropout counts as COMBINE) */
+  MOE_STAGE_LINEAR = 19,      /* moe_linear */
+  MOE_STAGE_LINEAR_BWD = 20,  /* each product of moe_linear_backward, and moe_backward_aux's */
+  MOE_STAGE_COUNT = 21
 } moe_stage;
 
 /* Host: stage timing for measurement tools (not thread-safe; for a single host thread).

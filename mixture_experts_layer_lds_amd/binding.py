@@ -5,7 +5,9 @@ becomes the hipStream_t, and non-zero status codes become ``MoEError``.  Every c
 in the library's HIP kernels; if the library is missing, the first call raises.
 The functions keep the C names: ``moe_route``, ``moe_permute``, ``moe_grouped_ffn``,
 ``moe_combine``, ``moe_forward``, ``moe_backward``, ``moe_decode``, ``moe_quantize_fp8``,
-``moe_grouped_ffn_fp8``, ``moe_quantize_mx``, ``moe_grouped_ffn_mx`` (plus sizing helpers).
+``moe_grouped_ffn_fp8``, ``moe_quantize_mx``, ``moe_grouped_ffn_mx``, ``moe_router_loss``,
+``moe_router_loss_backward``, ``moe_backward_aux``, ``moe_dropout``, ``moe_combine_dropout``,
+``moe_linear``, ``moe_linear_backward`` (plus sizing helpers).
 """
 import ctypes
 import os
@@ -19,6 +21,8 @@ MOE_F32, MOE_BF16 = 0, 1
 ROUND_NONE, ROUND_NEAREST, ROUND_UP, ROUND_DOWN, ROUND_STOCHASTIC = 0, 1, 2, 3, 4
 OP_ROUTE, OP_PERMUTE, OP_FFN, OP_COMBINE, OP_FORWARD, OP_BACKWARD, OP_DECODE, OP_FFN_FP8, OP_FFN_MX = range(9)
 FP8_E4M3, FP8_E5M2 = 0, 1
+ACTS = {"none": 0, "relu": 1, "gelu": 2, "silu": 3, "swiglu": 4}
+LINEAR_FORWARD, LINEAR_BACKWARD = 0, 1
 STATUS = {0: "MOE_OK", -1: "MOE_EINVAL", -2: "MOE_ENOTSUP", -3: "MOE_EWORKSPACE", -4: "MOE_EHIP"}
 
 EXPORTS = ["moe_max_rows", "moe_workspace_bytes", "moe_route", "moe_permute", "moe_grouped_ffn",
@@ -27,10 +31,13 @@ EXPORTS = ["moe_max_rows", "moe_workspace_bytes", "moe_route", "moe_permute", "m
            "moe_grouped_ffn_mx",
            "moe_decode_set_spin_limit", "moe_quantize_fp8",
            "moe_grouped_ffn_fp8", "moe_status_string", "moe_last_error",
+           "moe_backward_aux", "moe_router_loss", "moe_router_loss_backward",
+           "moe_router_loss_workspace_bytes", "moe_dropout", "moe_combine_dropout", "moe_linear",
+           "moe_linear_backward", "moe_linear_workspace_bytes",
            "moe_version", "moe_timing_enable", "moe_timing_read"]
 STAGES = ["router_gemm", "route", "tiles", "up_gemm", "down_gemm", "permute", "combine", "dact_gemm",
           "dw_down_gemm", "dw_gu_gemm", "dx_gemm", "router_bwd", "dwr_gemm", "decode", "fp8_quant",
-          "fp8_up_gemm", "fp8_down_gemm"]
+          "fp8_up_gemm", "fp8_down_gemm", "router_loss", "dropout", "linear", "linear_bwd"]
 
 
 class MoEError(RuntimeError):
@@ -44,6 +51,12 @@ class Dims(ctypes.Structure):
                 ("E", ctypes.c_int32), ("K", ctypes.c_int32), ("dtype", ctypes.c_int32),
                 ("round_mode", ctypes.c_int32), ("tile_m", ctypes.c_int32),
                 ("flags", ctypes.c_int32), ("round_rand", ctypes.c_void_p)]
+
+
+class LinearDims(ctypes.Structure):
+    _fields_ = [("M", ctypes.c_int64), ("N", ctypes.c_int64), ("K", ctypes.c_int64), ("ldx", ctypes.c_int64),
+                ("ldr", ctypes.c_int64), ("ldy", ctypes.c_int64), ("dtype", ctypes.c_int32), ("act", ctypes.c_int32),
+                ("flags", ctypes.c_int32)]
 
 
 PLAN_FIELDS = ["topk_idx", "topk_w", "counts", "expert_off", "row_token", "row_w", "tok_off",
@@ -90,6 +103,19 @@ def lib():
         L.moe_quantize_mx.argtypes = [ctypes.c_int64, ctypes.c_int64, ctypes.c_int, ctypes.c_int, vp, vp, vp, vp]
         L.moe_grouped_ffn_mx.argtypes = [pd, pp, ctypes.c_int, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp,
                                          sz, vp]
+        i32, i64, pl = ctypes.c_int32, ctypes.c_int64, ctypes.POINTER(LinearDims)
+        L.moe_backward_aux.argtypes = [pd, vp, vp, vp, vp, vp, vp, pp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp]
+        L.moe_router_loss_workspace_bytes.argtypes, L.moe_router_loss_workspace_bytes.restype = [pd, i32], sz
+        L.moe_router_loss.argtypes = [pd, vp, vp, i32, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp]
+        L.moe_router_loss_backward.argtypes = [pd, vp, vp, i32, vp, vp, vp, vp, vp, vp, vp]
+        L.moe_dropout.argtypes = [i64, i64, ctypes.c_int, vp, i64, vp, i64, ctypes.c_double, vp, vp, i64, vp]
+        L.moe_combine_dropout.argtypes = [pd, pp, vp, ctypes.c_int, vp, ctypes.c_double, vp, vp, vp]
+        L.moe_linear_workspace_bytes.argtypes, L.moe_linear_workspace_bytes.restype = [pl, ctypes.c_int], sz
+        L.moe_linear.argtypes = [pl, vp, vp, vp, vp, vp, vp, vp, sz, vp]
+        L.moe_linear_backward.argtypes = [pl, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp]
+        for f in ("moe_backward_aux", "moe_router_loss", "moe_router_loss_backward", "moe_dropout",
+                  "moe_combine_dropout", "moe_linear", "moe_linear_backward"):
+            getattr(L, f).restype = st
         for f in ("moe_route", "moe_route_noalloc", "moe_permute", "moe_grouped_ffn", "moe_combine", "moe_forward",
                   "moe_backward", "moe_decode", "moe_quantize_fp8", "moe_grouped_ffn_fp8", "moe_quantize_mx",
                   "moe_grouped_ffn_mx"):
@@ -279,6 +305,91 @@ def moe_backward(dims, dY, X, W_r, W_gate, W_up, W_down, plan, H_cache, dX, dW_g
                               _p(W_down), plan.ref(), _p(H_cache), _p(dX), _p(dW_gate), _p(dW_up),
                               _p(dW_down), _p(dS), _p(dLogits), _p(dW_r), _p(ws), ws_bytes,
                               _stream(stream)))
+
+
+def moe_backward_aux(dims, dY, X, W_r, W_gate, W_up, W_down, plan, H_cache, dLogits_aux, dX, dW_gate, dW_up, dW_down,
+                     dS, dLogits, dW_r, ws, ws_bytes, stream=None):
+    """moe_backward with further gradients of the router logits ([T, E] fp32, or None)."""
+    _check(lib().moe_backward_aux(ctypes.byref(dims), _p(dY), _p(X), _p(W_r), _p(W_gate), _p(W_up), _p(W_down),
+                                  plan.ref(), _p(H_cache), _p(dLogits_aux), _p(dX), _p(dW_gate), _p(dW_up),
+                                  _p(dW_down), _p(dS), _p(dLogits), _p(dW_r), _p(ws), ws_bytes, _stream(stream)))
+
+
+def router_loss_workspace(dims, n_seq, device="cuda"):
+    nbytes = lib().moe_router_loss_workspace_bytes(ctypes.byref(dims), int(n_seq))
+    return torch.empty(max(nbytes, 256), dtype=torch.uint8, device=device), nbytes
+
+
+def moe_router_loss(dims, logits, topk_idx, n_seq, seq_off, token_mask, seq_tokens, seq_counts, prob_sum, lse, loss,
+                    ws, ws_bytes, stream=None):
+    """Balance loss and z-loss of a batch of router logits, with the per-sequence expert counts."""
+    _check(lib().moe_router_loss(ctypes.byref(dims), _p(logits), _p(topk_idx), int(n_seq), _p(seq_off),
+                                 _p(token_mask), _p(seq_tokens), _p(seq_counts), _p(prob_sum), _p(lse), _p(loss),
+                                 _p(ws), ws_bytes, _stream(stream)))
+
+
+def moe_router_loss_backward(dims, dloss, logits, n_seq, seq_off, token_mask, seq_tokens, seq_counts, lse, dLogits,
+                             stream=None):
+    """Gradient of the two router losses (weights dloss, fp32 [2] on the device) for the logits."""
+    _check(lib().moe_router_loss_backward(ctypes.byref(dims), _p(dloss), _p(logits), int(n_seq), _p(seq_off),
+                                          _p(token_mask), _p(seq_tokens), _p(seq_counts), _p(lse), _p(dLogits),
+                                          _stream(stream)))
+
+
+def _rows(t, like, name):
+    """Row stride of a 2-D tensor of like's shape and type whose rows are contiguous."""
+    if t.dim() != 2 or t.shape != like.shape or t.dtype != like.dtype or (t.shape[1] > 1 and t.stride(1) != 1):
+        raise MoEError(-1, "%s must be %s of %s with contiguous rows" % (name, tuple(like.shape), like.dtype))
+    return t.stride(0) if t.shape[0] > 1 else max(t.stride(0), t.shape[1])
+
+
+def moe_dropout(x, residual, p, rng, out, stream=None):
+    """out = residual + dropout(x) of 2-D bf16 / fp32 tensors (residual may be None; rows may be
+    strided); rng is a device tensor of two 64-bit words, {seed, offset}.  Without a residual this is
+    also the gradient of dropout."""
+    if x.dtype not in (torch.bfloat16, torch.float32):
+        raise MoEError(-2, "dtype %s not supported" % x.dtype)
+    if rng.numel() < 2 or rng.element_size() != 8:
+        raise MoEError(-1, "rng must hold two 64-bit words")
+    ldx, ldo = _rows(x, x, "x"), _rows(out, x, "out")
+    ldr = _rows(residual, x, "residual") if residual is not None else 0
+    dtype = MOE_BF16 if x.dtype == torch.bfloat16 else MOE_F32
+    _check(lib().moe_dropout(x.shape[0], x.shape[1], dtype, _p(x), ldx, _p(residual), ldr, float(p), _p(rng), _p(out),
+                             ldo, _stream(stream)))
+
+
+def moe_combine_dropout(dims, plan, Y_perm, weighted, residual, p, rng, out, stream=None):
+    """moe_combine with dropout and the residual sum (None: no residual) in its epilogue."""
+    _check(lib().moe_combine_dropout(ctypes.byref(dims), plan.ref(), _p(Y_perm), int(bool(weighted)), _p(residual),
+                                     float(p), _p(rng), _p(out), _stream(stream)))
+
+
+def make_linear_dims(M, N, K, dtype="bf16", act="none", ldx=0, ldr=0, ldy=0):
+    """Shape of a dense projection: M rows, N outputs, K inputs; row strides of X / dX, residual and
+    out / dY in elements (0 = dense)."""
+    dt = {"bf16": MOE_BF16, "f32": MOE_F32, torch.bfloat16: MOE_BF16, torch.float32: MOE_F32}[dtype]
+    return LinearDims(int(M), int(N), int(K), int(ldx), int(ldr), int(ldy), dt, ACTS[act], 0)
+
+
+def moe_linear_workspace_bytes(dims, op):
+    return lib().moe_linear_workspace_bytes(ctypes.byref(dims), op)
+
+
+def linear_workspace(dims, op, device="cuda"):
+    nbytes = moe_linear_workspace_bytes(dims, op)
+    return torch.empty(max(nbytes, 256), dtype=torch.uint8, device=device), nbytes
+
+
+def moe_linear(dims, X, W, bias, residual, Z, out, ws, ws_bytes, stream=None):
+    """out = residual + act(X W^T + bias); bias, residual and Z (the saved pre-activation) may be None."""
+    _check(lib().moe_linear(ctypes.byref(dims), _p(X), _p(W), _p(bias), _p(residual), _p(Z), _p(out), _p(ws),
+                            ws_bytes, _stream(stream)))
+
+
+def moe_linear_backward(dims, dY, X, W, Z, dX, dW, dbias, ws, ws_bytes, stream=None):
+    """Gradients of moe_linear from dY and the saved pre-activation; dX, dW and dbias may be None."""
+    _check(lib().moe_linear_backward(ctypes.byref(dims), _p(dY), _p(X), _p(W), _p(Z), _p(dX), _p(dW), _p(dbias),
+                                     _p(ws), ws_bytes, _stream(stream)))
 
 
 def moe_timing_enable(on):

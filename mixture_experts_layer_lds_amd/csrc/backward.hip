@@ -554,12 +554,14 @@ __device__ __forceinline__ int expert_of_row(const int32_t* soff, int E, int r) 
   return lo;
 }
 
-template <typename T, int CPL, int RB>
+// AUX: logit gradients of other losses (the balance loss) are added to the row's before it is
+// written; those rows are dense, so W_r is null then and the dX term follows as a GEMM.
+template <typename T, int CPL, int RB, bool AUX>
 __global__ __launch_bounds__(256) void k_router_bwd(
     const int32_t* __restrict__ tok_off, const int32_t* __restrict__ tok_row,
     const int32_t* __restrict__ expert_off, const float* __restrict__ row_w,
     const float* __restrict__ dS_part, int ntiles, int64_t R_max, const T* __restrict__ dXp,
-    const T* __restrict__ Wr, float* __restrict__ dS, float* __restrict__ dLogits,
+    const T* __restrict__ Wr, const float* __restrict__ aux, float* __restrict__ dS, float* __restrict__ dLogits,
     T* __restrict__ dLop, int E_pad, T* __restrict__ dX, int T_, int d, int E) {
   // per wave: the dense dL row [E_pad], the token's rows and their experts (at most E of each);
   // per block: expert_off [E + 1]
@@ -613,7 +615,8 @@ __global__ __launch_bounds__(256) void k_router_bwd(
   __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup");
   __builtin_amdgcn_wave_barrier();
   for (int e = lane; e < E_pad; e += 64) {
-    const float v = sdl[e];
+    float v = sdl[e];
+    if (AUX && e < E) v += aux[(int64_t)t * E + e];
     if (e < E) dLogits[(int64_t)t * E + e] = v;
     if (dLop) dLop[(int64_t)t * E_pad + e] = from_f32<T>(v);
   }
@@ -669,26 +672,32 @@ __global__ __launch_bounds__(256) void k_router_bwd(
 
 template <typename T, int CPL, int RB>
 static void router_bwd_for(const Shape& s, const PlanPtrs& p, const float* dS_part, int ntiles, const void* dX_perm,
-                           const void* W_r, float* dS, float* dLogits, void* dLop, int E_pad, void* dX,
+                           const void* W_r, const float* aux, float* dS, float* dLogits, void* dLop, int E_pad, void* dX,
                            hipStream_t st) {
   const int grid = (int)cdiv(s.T, 4);
   const size_t lds = ((size_t)4 * 3 * E_pad + s.E + 1) * sizeof(float);  // <= 53 KiB for E <= 1024
-  k_router_bwd<T, CPL, RB><<<grid, 256, lds, st>>>(p.tok_off, p.tok_row, p.expert_off, p.row_w, dS_part, ntiles,
-                                                   s.R_max, static_cast<const T*>(dX_perm), static_cast<const T*>(W_r),
-                                                   dS, dLogits, static_cast<T*>(dLop), E_pad, static_cast<T*>(dX),
-                                                   (int)s.T, (int)s.d, s.E);
+  if (aux)
+    k_router_bwd<T, CPL, RB, true><<<grid, 256, lds, st>>>(
+        p.tok_off, p.tok_row, p.expert_off, p.row_w, dS_part, ntiles, s.R_max, static_cast<const T*>(dX_perm),
+        static_cast<const T*>(W_r), aux, dS, dLogits, static_cast<T*>(dLop), E_pad, static_cast<T*>(dX), (int)s.T,
+        (int)s.d, s.E);
+  else
+    k_router_bwd<T, CPL, RB, false><<<grid, 256, lds, st>>>(
+        p.tok_off, p.tok_row, p.expert_off, p.row_w, dS_part, ntiles, s.R_max, static_cast<const T*>(dX_perm),
+        static_cast<const T*>(W_r), nullptr, dS, dLogits, static_cast<T*>(dLop), E_pad, static_cast<T*>(dX), (int)s.T,
+        (int)s.d, s.E);
 }
 
 hipError_t launch_router_bwd(const Shape& s, const PlanPtrs& p, const float* dS_part, int ntiles,
-                             const void* dX_perm, const void* W_r, float* dS, float* dLogits,
+                             const void* dX_perm, const void* W_r, const float* aux, float* dS, float* dLogits,
                              void* dLop, int E_pad, void* dX, hipStream_t st) {
   // chunks per lane: the whole row in one pass up to 4 * 64 16-byte chunks, else passes of that
   const int64_t nch = s.d / (s.bf16 ? 8 : 4);
 #define MOE_RBWD(TT)                                                                                    \
-  if (nch <= 64) router_bwd_for<TT, 1, 8>(s, p, dS_part, ntiles, dX_perm, W_r, dS, dLogits, dLop, E_pad, dX, st); \
-  else if (nch <= 128) router_bwd_for<TT, 2, 4>(s, p, dS_part, ntiles, dX_perm, W_r, dS, dLogits, dLop, E_pad, dX, st); \
-  else if (nch <= 192) router_bwd_for<TT, 3, 2>(s, p, dS_part, ntiles, dX_perm, W_r, dS, dLogits, dLop, E_pad, dX, st); \
-  else router_bwd_for<TT, 4, 2>(s, p, dS_part, ntiles, dX_perm, W_r, dS, dLogits, dLop, E_pad, dX, st);
+  if (nch <= 64) router_bwd_for<TT, 1, 8>(s, p, dS_part, ntiles, dX_perm, W_r, aux, dS, dLogits, dLop, E_pad, dX, st); \
+  else if (nch <= 128) router_bwd_for<TT, 2, 4>(s, p, dS_part, ntiles, dX_perm, W_r, aux, dS, dLogits, dLop, E_pad, dX, st); \
+  else if (nch <= 192) router_bwd_for<TT, 3, 2>(s, p, dS_part, ntiles, dX_perm, W_r, aux, dS, dLogits, dLop, E_pad, dX, st); \
+  else router_bwd_for<TT, 4, 2>(s, p, dS_part, ntiles, dX_perm, W_r, aux, dS, dLogits, dLop, E_pad, dX, st);
   if (s.bf16) { MOE_RBWD(bf16) } else { MOE_RBWD(float) }
 #undef MOE_RBWD
   return hipGetLastError();

@@ -12,6 +12,7 @@
 // combine gathers the token's rows and accumulates them in fp32 in ascending expert order,
 // rounding once.
 #include "internal.h"
+#include "philox.h"
 
 namespace moe {
 
@@ -60,16 +61,13 @@ hipError_t launch_permute(const Shape& s, const PlanPtrs& p, const void* X, void
 // d is small enough; otherwise the row goes in several passes).  Per pass the rows are read in
 // batches of RBATCH: every chunk of every row of a batch is requested before any is used, so a
 // wave reads whole rows at once (RBATCH * CPL loads in flight per lane) instead of one chunk of
-// each row per round trip.  fp32 accumulation in ascending expert order, one rounding.
-template <typename T, bool WEIGHTED, int CPL, int RBATCH>
-__global__ __launch_bounds__(256) void k_combine(const int32_t* __restrict__ tok_off,
-                                                 const int32_t* __restrict__ tok_row,
-                                                 const float* __restrict__ row_w,
-                                                 const T* __restrict__ Y, T* __restrict__ out,
-                                                 int T_, int d, int rmax) {
-  const int t = blockIdx.x * 4 + (threadIdx.x >> 6);
+// each row per round trip.  fp32 accumulation in ascending expert order, one rounding.  epi is
+// applied to the fp32 sums of each chunk (token, first column) before that rounding.
+template <typename T, bool WEIGHTED, int CPL, int RBATCH, class Epi>
+__device__ __forceinline__ void combine_token(const int32_t* __restrict__ tok_off, const int32_t* __restrict__ tok_row,
+                                              const float* __restrict__ row_w, const T* __restrict__ Y, T* out, int t,
+                                              int d, int rmax, Epi epi) {
   const int lane = threadIdx.x & 63;
-  if (t >= T_) return;
   const int base = tok_off[t], cnt = tok_off[t + 1] - base;
   constexpr int VEC = 16 / sizeof(T);
   const int nch = d / VEC;
@@ -109,8 +107,51 @@ __global__ __launch_bounds__(256) void k_combine(const int32_t* __restrict__ tok
     }
 #pragma unroll
     for (int j = 0; j < CPL; ++j)
-      if (ok[j]) st16(out + (int64_t)t * d + (int64_t)(c0 + lane + 64 * j) * VEC, pack16<T>(acc[j]));
+      if (ok[j]) {
+        epi(t, (c0 + lane + 64 * j) * VEC, acc[j]);
+        st16(out + (int64_t)t * d + (int64_t)(c0 + lane + 64 * j) * VEC, pack16<T>(acc[j]));
+      }
   }
+}
+
+template <typename T, bool WEIGHTED, int CPL, int RBATCH>
+__global__ __launch_bounds__(256) void k_combine(const int32_t* __restrict__ tok_off,
+                                                 const int32_t* __restrict__ tok_row,
+                                                 const float* __restrict__ row_w,
+                                                 const T* __restrict__ Y, T* __restrict__ out,
+                                                 int T_, int d, int rmax) {
+  const int t = blockIdx.x * 4 + (threadIdx.x >> 6);
+  if (t >= T_) return;
+  combine_token<T, WEIGHTED, CPL, RBATCH>(tok_off, tok_row, row_w, Y, out, t, d, rmax, [](int, int, float*) {});
+}
+
+// out[t] = residual[t] + keep(sum_r w_r Y[r]) * scale: dropout and the residual sum on the fp32
+// sums, in the same pass (a separate dropout would write and read the layer's output once more
+// and round it twice).  The mask is that of k_dropout on the [T, d] output: a lane's chunk is one
+// group of eight bf16 columns, or half a group in fp32.  res may be null, or out itself.
+template <typename T, bool WEIGHTED, int CPL, int RBATCH>
+__global__ __launch_bounds__(256) void k_combine_dropout(const int32_t* __restrict__ tok_off,
+                                                         const int32_t* __restrict__ tok_row,
+                                                         const float* __restrict__ row_w, const T* __restrict__ Y,
+                                                         const T* res, T* out, int T_, int d, int rmax, DropArgs a) {
+  const int t = blockIdx.x * 4 + (threadIdx.x >> 6);
+  if (t >= T_) return;
+  const PhiloxKey key = philox_key(a.rng);
+  constexpr int VEC = 16 / sizeof(T);
+  combine_token<T, WEIGHTED, CPL, RBATCH>(tok_off, tok_row, row_w, Y, out, t, d, rmax, [&](int tt, int c, float* f) {
+    float r[VEC];
+#pragma unroll
+    for (int k = 0; k < VEC; ++k) r[k] = 0.0f;
+    if (res) unpack16<T>(ld16(res + (int64_t)tt * d + c), r);
+    const u32x4 w = philox10(key, (uint32_t)c >> 3, (uint32_t)tt);
+    const bool upper = VEC == 4 && (c & 4);  // fp32: the second half of the group
+#pragma unroll
+    for (int k = 0; k < VEC; ++k) {
+      const bool keep = VEC == 8 ? drop_keep(w, k, a.threshold)
+                                 : (upper ? drop_keep(w, 4 + (k & 3), a.threshold) : drop_keep(w, k & 3, a.threshold));
+      f[k] = (keep ? f[k] * a.scale : 0.0f) + r[k];
+    }
+  });
 }
 
 template <typename T, bool W>
@@ -131,6 +172,30 @@ hipError_t launch_combine(const Shape& s, const PlanPtrs& p, const void* Y_perm,
                           void* out, hipStream_t st) {
   if (s.bf16) { if (weighted) combine_for<bf16, true>(s, p, Y_perm, out, st); else combine_for<bf16, false>(s, p, Y_perm, out, st); }
   else { if (weighted) combine_for<float, true>(s, p, Y_perm, out, st); else combine_for<float, false>(s, p, Y_perm, out, st); }
+  return hipGetLastError();
+}
+
+template <typename T, bool W>
+static void combine_dropout_for(const Shape& s, const PlanPtrs& p, const void* Y_perm, const void* residual, void* out,
+                                const DropArgs& a, hipStream_t st) {
+  const int grid = (int)cdiv(s.T, 4);
+  const int64_t nch = s.d / (16 / (int)sizeof(T));
+  const T* Y = static_cast<const T*>(Y_perm);
+  const T* r = static_cast<const T*>(residual);
+  T* o = static_cast<T*>(out);
+  // the chunk and batch sizes of combine_for
+#define MOE_CD(CPL, RB) k_combine_dropout<T, W, CPL, RB><<<grid, 256, 0, st>>>(p.tok_off, p.tok_row, p.row_w, Y, r, o, (int)s.T, (int)s.d, (int)s.R_max, a)
+  if (nch <= 64) MOE_CD(1, 8);
+  else if (nch <= 128) MOE_CD(2, 8);
+  else if (nch <= 192) MOE_CD(3, 4);
+  else MOE_CD(4, 4);
+#undef MOE_CD
+}
+
+hipError_t launch_combine_dropout(const Shape& s, const PlanPtrs& p, const void* Y_perm, bool weighted,
+                                  const void* residual, void* out, const DropArgs& a, hipStream_t st) {
+  if (s.bf16) { if (weighted) combine_dropout_for<bf16, true>(s, p, Y_perm, residual, out, a, st); else combine_dropout_for<bf16, false>(s, p, Y_perm, residual, out, a, st); }
+  else { if (weighted) combine_dropout_for<float, true>(s, p, Y_perm, residual, out, a, st); else combine_dropout_for<float, false>(s, p, Y_perm, residual, out, a, st); }
   return hipGetLastError();
 }
 

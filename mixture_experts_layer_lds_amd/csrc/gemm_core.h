@@ -624,6 +624,25 @@ struct RowLoaderF32 {                       // K-major rows: thread owns rows ti
   }
 };
 
+// The same with rows that end inside a stage (K any multiple of 4).
+struct RowLoaderF32Tail : RowLoaderF32 {
+  int klim;
+  template <class RowPtr>
+  __device__ void init(RowPtr row_ptr, int klen) {
+    RowLoaderF32::init(row_ptr);
+    klim = klen;
+  }
+  __device__ void load(int kt) {
+    const int chunk = threadIdx.x & 7;
+    const bool in = kt * 32 + chunk * 4 < klim;
+#pragma unroll
+    for (int q = 0; q < 8; ++q) {
+      if (rp[q] && in) v[q] = ld16(rp[q] + (int64_t)kt * 128 + chunk * 16);
+      else v[q] = u32x4{0u, 0u, 0u, 0u};
+    }
+  }
+};
+
 // MN-major fp32 operand, transposed in registers into the K-major layout: thread owns two 4 (k)
 // x 4 (mn) blocks, mn = 4 (tid % 64), k = 4 (tid / 64) and 4 (tid / 64 + 4).  kbase / klim as
 // for MNDma.
@@ -892,6 +911,39 @@ struct KDmaW8 {
     dma16(g[q] + (int64_t)ps[q] * step[q], dst + (8 * q + w) * 1024);
   }
   __device__ static bf16x8 frag(const char* t, int row0, int s) { return KDma::frag(t, row0, s); }
+};
+
+// K-major operand whose rows may end inside a stage (K any multiple of 8): in the last stage the
+// chunks past the row's end come from the zero page, chosen per lane with one v_cndmask per address
+// half on a scalar mask (written out for the reason given at MNDma).
+struct KDmaW8Tail : KDmaW8 {
+  int last;        // index of the last stage
+  uint64_t live;   // lanes whose chunk lies inside the row in that stage
+  uint64_t src[2];
+  template <class RowPtr>
+  __device__ void init(RowPtr row_ptr, int klen) {
+    KDmaW8::init(row_ptr);
+    const int lane = threadIdx.x & 63;
+    const int chunk = (lane & 3) ^ (lane >> 4);
+    last = (klen + 31) / 32 - 1;
+    live = __builtin_amdgcn_ballot_w64(32 * last + chunk * 8 < klen);
+  }
+  template <int P>
+  __device__ void prepare_q(int s, int q) {
+    const int lane = threadIdx.x & 63;
+    const uint64_t a = reinterpret_cast<uint64_t>(g[q] + (int64_t)s * step[q]);
+    const uint64_t zero = reinterpret_cast<uint64_t>(g_zero_page) + (lane & 3) * 16;
+    const uint32_t zl = (uint32_t)zero, zh = (uint32_t)(zero >> 32);
+    const uint64_t m = __builtin_amdgcn_readfirstlane(s) == __builtin_amdgcn_readfirstlane(last) ? live : ~0ull;
+    uint32_t sl = (uint32_t)a, sh = (uint32_t)(a >> 32);
+    asm("v_cndmask_b32_e64 %0, %1, %0, %2" : "+v"(sl) : "v"(zl), "s"(m));
+    asm("v_cndmask_b32_e64 %0, %1, %0, %2" : "+v"(sh) : "v"(zh), "s"(m));
+    src[q] = ((uint64_t)sh << 32) | sl;
+  }
+  __device__ void issue_q(int q, char* dst) const {
+    const int w = threadIdx.x >> 6;
+    dma16(reinterpret_cast<const void*>(src[q]), dst + (8 * q + w) * 1024);
+  }
 };
 
 // MN-major operand (layout as MNDma).  The row ids of a stage are fetched into one of two

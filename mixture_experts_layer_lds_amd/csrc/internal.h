@@ -114,13 +114,52 @@ hipError_t launch_dw_gu_gemm(const Shape& s, const PlanPtrs& p, const int32_t* o
 // Router backward + dX gather-sum, one wave per token:
 //   dS[r] = sum of partials; dL = w (dS - <w, dS>); dLogits row; dLop[t][e] (GEMM operand);
 //   dX[t] = sum_r dX_perm[r] (+ sum_r dL_r W_r[e_r] if W_r)
+// aux (may be null): [T][E] further logit gradients added to dLogits and dLop (not to dX: their
+// rows are dense, so their dX term is a GEMM of its own, launch_logit_dx)
 hipError_t launch_router_bwd(const Shape& s, const PlanPtrs& p, const float* dS_part, int ntiles,
-                             const void* dX_perm, const void* W_r, float* dS, float* dLogits,
+                             const void* dX_perm, const void* W_r, const float* aux, float* dS, float* dLogits,
                              void* dLop, int E_pad, void* dX, hipStream_t st);
 // dW_r[E,d] = dL^T X (split over tokens, fp32 partials, fixed-order reduction)
 size_t dwr_workspace_bytes(const Shape& s);
 hipError_t launch_dwr_gemm(const Shape& s, const void* dLop, int E_pad, const void* X, void* dW_r,
                            void* ws, hipStream_t st);
+
+// ---- dropout (dropout.hip, combine.hip) ----
+struct DropArgs;  // philox.h
+// out = residual + keep(x) * scale over rows x cols with row strides (elements); rows * ceil(cols
+// / 8) below 2^31.  residual may be null; out may be x or residual.
+hipError_t launch_dropout(bool is_bf16, int64_t rows, int64_t cols, const void* x, int64_t ldx, const void* residual,
+                          int64_t ldr, void* out, int64_t ldo, const DropArgs& a, hipStream_t st);
+hipError_t launch_combine_dropout(const Shape& s, const PlanPtrs& p, const void* Y_perm, bool weighted,
+                                  const void* residual, void* out, const DropArgs& a, hipStream_t st);
+
+// ---- router losses (router_loss.hip) ----
+size_t router_loss_workspace_bytes(int64_t T, int E, int n_seq);
+hipError_t launch_router_loss(const float* logits, const int32_t* topk_idx, int64_t T, int E, int K, int n_seq,
+                              const int32_t* seq_off, const uint8_t* mask, int32_t* seq_tokens, int32_t* seq_counts,
+                              float* prob_sum, float* lse, float* loss, void* ws, hipStream_t st);
+hipError_t launch_router_loss_bwd(const float* dloss, const float* logits, int64_t T, int E, int K, int n_seq,
+                                  const int32_t* seq_off, const uint8_t* mask, const int32_t* seq_tokens,
+                                  const int32_t* seq_counts, const float* lse, float* dLogits, hipStream_t st);
+
+// ---- dense projection (linear.hip) ----
+struct LinShape {
+  int64_t M, N, K;
+  int64_t ldx, ldr, ldy;  // row strides in elements: X and dX, residual, out and dY
+  int act;                // moe_act
+  bool bf16;
+};
+size_t linear_fwd_workspace_bytes(const LinShape& s);
+size_t linear_bwd_workspace_bytes(const LinShape& s);
+// out = residual + act(X W^T + bias), Z = X W^T + bias; bias, residual and Z may be null
+hipError_t launch_linear(const LinShape& s, const void* X, const void* W, const float* bias, const void* residual,
+                         void* Z, void* out, void* ws, hipStream_t st);
+// the backward's steps, in this order on one workspace: dZ (and dbias when given), then the products
+hipError_t launch_linear_dz(const LinShape& s, const void* dY, const void* Z, float* dbias, void* ws, hipStream_t st);
+hipError_t launch_linear_dx(const LinShape& s, const void* dY, const void* W, void* dX, void* ws, hipStream_t st);
+hipError_t launch_linear_dw(const LinShape& s, const void* dY, const void* X, void* dW, void* ws, hipStream_t st);
+// dX += dL W_r for dense logit gradients dL [T][E_pad] in the element type
+hipError_t launch_logit_dx(const Shape& s, const void* dL, int E_pad, const void* W_r, void* dX, hipStream_t st);
 
 // single-launch forward for small T (decode.hip)
 size_t decode_workspace_bytes(int64_t T, int64_t d, int64_t n, int E, int K);

@@ -10,6 +10,7 @@
 
 #include "../../include/moe.h"
 #include "internal.h"
+#include "philox.h"
 
 using namespace moe;
 
@@ -578,6 +579,15 @@ moe_status moe_backward(const moe_dims* dims, const void* dY, const void* X, con
                         const moe_plan* plan, const void* H_cache, void* dX, void* dW_gate,
                         void* dW_up, void* dW_down, float* dS, float* dLogits, void* dW_r,
                         void* ws, size_t ws_bytes, void* stream) {
+  return moe_backward_aux(dims, dY, X, W_r, W_gate, W_up, W_down, plan, H_cache, nullptr, dX, dW_gate, dW_up, dW_down,
+                          dS, dLogits, dW_r, ws, ws_bytes, stream);
+}
+
+moe_status moe_backward_aux(const moe_dims* dims, const void* dY, const void* X, const void* W_r,
+                            const void* W_gate, const void* W_up, const void* W_down,
+                            const moe_plan* plan, const void* H_cache, const float* dLogits_aux, void* dX,
+                            void* dW_gate, void* dW_up, void* dW_down, float* dS, float* dLogits, void* dW_r,
+                            void* ws, size_t ws_bytes, void* stream) {
   MOE_TRY(check_dims(dims));
   MOE_TRY(check_plan(plan));
   MOE_TRY(need_ptr(dY, "dY"));
@@ -587,6 +597,7 @@ moe_status moe_backward(const moe_dims* dims, const void* dY, const void* X, con
   MOE_TRY(need_ptr(W_up, "W_up"));
   MOE_TRY(need_ptr(W_down, "W_down"));
   MOE_TRY(opt_ptr(H_cache, "H_cache"));
+  MOE_TRY(opt_ptr(dLogits_aux, "dLogits_aux"));
   MOE_TRY(need_ptr(dX, "dX"));
   MOE_TRY(need_ptr(dW_gate, "dW_gate"));
   MOE_TRY(need_ptr(dW_up, "dW_up"));
@@ -617,12 +628,211 @@ moe_status moe_backward(const moe_dims* dims, const void* dY, const void* X, con
   MOE_STAGE(MOE_STAGE_DX_GEMM, st, launch_dx_gemm(s, p, w.mtile_off, w.dH, W_gate, W_up, w.dX_perm, st),
             "dX GEMM");
   MOE_STAGE(MOE_STAGE_ROUTER_BWD, st,
-            launch_router_bwd(s, p, w.dS_part, dact_ntiles(dims->n), w.dX_perm, W_r, dS, dLogits,
-                              dW_r ? w.dLop : nullptr, e_pad(dims->E), dX, st),
+            launch_router_bwd(s, p, w.dS_part, dact_ntiles(dims->n), w.dX_perm, dLogits_aux ? nullptr : W_r,
+                              dLogits_aux, dS, dLogits, dW_r || (dLogits_aux && W_r) ? w.dLop : nullptr,
+                              e_pad(dims->E), dX, st),
             "router backward");
+  if (dLogits_aux && W_r)  // dense logit gradients: their dX term is a GEMM that adds to the gathered sum
+    MOE_STAGE(MOE_STAGE_LINEAR_BWD, st, launch_logit_dx(s, w.dLop, e_pad(dims->E), W_r, dX, st), "logit dX GEMM");
   if (dW_r)
     MOE_STAGE(MOE_STAGE_DWR_GEMM, st, launch_dwr_gemm(s, w.dLop, e_pad(dims->E), X, dW_r, w.dwr, st),
               "dW_r GEMM");
+  return MOE_OK;
+}
+
+// ---- router losses ----
+static moe_status check_n_seq(int32_t n_seq) {
+  if (n_seq < 1 || n_seq > (1 << 20)) return fail(MOE_EINVAL, "n_seq=%d out of range [1, 2^20]", n_seq);
+  return MOE_OK;
+}
+static moe_status check_sequences(int32_t n_seq, const int32_t* seq_off, const uint8_t* mask) {
+  MOE_TRY(check_n_seq(n_seq));
+  if (n_seq > 1 && !seq_off) return fail(MOE_EINVAL, "n_seq=%d needs seq_off", n_seq);
+  MOE_TRY(opt_ptr(seq_off, "seq_off"));
+  return opt_ptr(mask, "token_mask");
+}
+
+size_t moe_router_loss_workspace_bytes(const moe_dims* dims, int32_t n_seq) {
+  if (check_dims(dims) != MOE_OK || check_n_seq(n_seq) != MOE_OK) return 0;
+  return router_loss_workspace_bytes(dims->T, dims->E, n_seq);
+}
+
+moe_status moe_router_loss(const moe_dims* dims, const float* logits, const int32_t* topk_idx, int32_t n_seq,
+                           const int32_t* seq_off, const uint8_t* token_mask, int32_t* seq_tokens,
+                           int32_t* seq_counts, float* prob_sum, float* lse, float* loss, void* ws, size_t ws_bytes,
+                           void* stream) {
+  MOE_TRY(check_dims(dims));
+  MOE_TRY(check_sequences(n_seq, seq_off, token_mask));
+  MOE_TRY(need_ptr(logits, "logits"));
+  MOE_TRY(need_ptr(topk_idx, "topk_idx"));
+  MOE_TRY(need_ptr(seq_tokens, "seq_tokens"));
+  MOE_TRY(need_ptr(seq_counts, "seq_counts"));
+  MOE_TRY(need_ptr(prob_sum, "prob_sum"));
+  MOE_TRY(need_ptr(lse, "lse"));
+  MOE_TRY(need_ptr(loss, "loss"));
+  const size_t need = router_loss_workspace_bytes(dims->T, dims->E, n_seq);
+  if (ws_bytes < need) return fail(MOE_EWORKSPACE, "workspace of %zu bytes < %zu needed", ws_bytes, need);
+  MOE_TRY(need_ptr(ws, "ws"));
+  hipStream_t st = static_cast<hipStream_t>(stream);
+  MOE_STAGE(MOE_STAGE_ROUTER_LOSS, st,
+            launch_router_loss(logits, topk_idx, dims->T, dims->E, dims->K, n_seq, seq_off, token_mask, seq_tokens,
+                               seq_counts, prob_sum, lse, loss, ws, st),
+            "router loss");
+  return MOE_OK;
+}
+
+moe_status moe_router_loss_backward(const moe_dims* dims, const float* dloss, const float* logits, int32_t n_seq,
+                                    const int32_t* seq_off, const uint8_t* token_mask, const int32_t* seq_tokens,
+                                    const int32_t* seq_counts, const float* lse, float* dLogits, void* stream) {
+  MOE_TRY(check_dims(dims));
+  MOE_TRY(check_sequences(n_seq, seq_off, token_mask));
+  MOE_TRY(need_ptr(dloss, "dloss"));
+  MOE_TRY(need_ptr(logits, "logits"));
+  MOE_TRY(need_ptr(seq_tokens, "seq_tokens"));
+  MOE_TRY(need_ptr(seq_counts, "seq_counts"));
+  MOE_TRY(need_ptr(lse, "lse"));
+  MOE_TRY(need_ptr(dLogits, "dLogits"));
+  hipStream_t st = static_cast<hipStream_t>(stream);
+  MOE_STAGE(MOE_STAGE_ROUTER_LOSS, st,
+            launch_router_loss_bwd(dloss, logits, dims->T, dims->E, dims->K, n_seq, seq_off, token_mask, seq_tokens,
+                                   seq_counts, lse, dLogits, st),
+            "router loss backward");
+  return MOE_OK;
+}
+
+// ---- dropout ----
+static moe_status drop_args(double p, const uint64_t* rng, DropArgs* a) {
+  if (!(p >= 0.0 && p <= 1.0)) return fail(MOE_EINVAL, "dropout probability %g out of range [0, 1]", p);
+  MOE_TRY(need_ptr(rng, "rng"));
+  a->rng = rng;
+  a->threshold = static_cast<uint32_t>(p * 65536.0 + 0.5);
+  a->scale = a->threshold < 65536u ? static_cast<float>(65536.0 / (65536.0 - a->threshold)) : 0.0f;
+  return MOE_OK;
+}
+
+static moe_status check_ld(int64_t ld, int64_t cols, const char* name) {
+  if (ld < cols || ld > ((int64_t)1 << 40)) return fail(MOE_EINVAL, "%s=%lld is less than the row's %lld elements (or above 2^40)", name, (long long)ld, (long long)cols);
+  return MOE_OK;
+}
+
+moe_status moe_dropout(int64_t rows, int64_t cols, int dtype, const void* x, int64_t ldx, const void* residual,
+                       int64_t ldr, double p, const uint64_t* rng, void* out, int64_t ldo, void* stream) {
+  if (rows < 0 || cols < 1 || cols > ((int64_t)1 << 30))
+    return fail(MOE_EINVAL, "rows=%lld / cols=%lld out of range", (long long)rows, (long long)cols);
+  if (rows > 0x7fffffffll || rows * ((cols + 7) / 8) > 0x7fffffffll)
+    return fail(MOE_ENOTSUP, "rows=%lld x cols=%lld is more than 2^31 groups of 8", (long long)rows, (long long)cols);
+  if (dtype != MOE_BF16 && dtype != MOE_F32) return fail(MOE_ENOTSUP, "dtype %d not supported", dtype);
+  MOE_TRY(check_ld(ldx, cols, "ldx"));
+  MOE_TRY(check_ld(ldo, cols, "ldo"));
+  if (residual) MOE_TRY(check_ld(ldr, cols, "ldr"));
+  DropArgs a;
+  MOE_TRY(drop_args(p, rng, &a));
+  if (rows == 0) return MOE_OK;
+  MOE_TRY(need_ptr(x, "x"));
+  MOE_TRY(opt_ptr(residual, "residual"));
+  MOE_TRY(need_ptr(out, "out"));
+  hipStream_t st = static_cast<hipStream_t>(stream);
+  MOE_STAGE(MOE_STAGE_DROPOUT, st, launch_dropout(dtype == MOE_BF16, rows, cols, x, ldx, residual, ldr, out, ldo, a, st),
+            "dropout");
+  return MOE_OK;
+}
+
+moe_status moe_combine_dropout(const moe_dims* dims, const moe_plan* plan, const void* Y_perm, int weighted,
+                               const void* residual, double p, const uint64_t* rng, void* out, void* stream) {
+  MOE_TRY(check_dims(dims));
+  MOE_TRY(check_plan(plan));
+  MOE_TRY(need_ptr(Y_perm, "Y_perm"));
+  MOE_TRY(opt_ptr(residual, "residual"));
+  MOE_TRY(need_ptr(out, "out"));
+  DropArgs a;
+  MOE_TRY(drop_args(p, rng, &a));
+  hipStream_t st = static_cast<hipStream_t>(stream);
+  MOE_STAGE(MOE_STAGE_COMBINE, st,
+            launch_combine_dropout(shape_of(dims), plan_ptrs(plan), Y_perm, weighted != 0, residual, out, a, st),
+            "combine with dropout");
+  return MOE_OK;
+}
+
+// ---- dense projection ----
+static moe_status check_linear(const moe_linear_dims* dm, LinShape* s) {
+  if (!dm) return fail(MOE_EINVAL, "dims is NULL");
+  if (dm->M < 0 || dm->M > (1 << 24)) return fail(MOE_EINVAL, "M=%lld out of range [0, 2^24]", (long long)dm->M);
+  if (dm->N < 8 || dm->N > 65536 || dm->K < 8 || dm->K > 65536)
+    return fail(MOE_EINVAL, "N=%lld / K=%lld out of range [8, 65536]", (long long)dm->N, (long long)dm->K);
+  if (dm->N % 8 || dm->K % 8)
+    return fail(MOE_ENOTSUP, "N=%lld and K=%lld must be multiples of 8", (long long)dm->N, (long long)dm->K);
+  if (dm->dtype != MOE_F32 && dm->dtype != MOE_BF16) return fail(MOE_ENOTSUP, "dtype %d not supported", dm->dtype);
+  if (dm->act < MOE_ACT_NONE || dm->act > MOE_ACT_SWIGLU) return fail(MOE_EINVAL, "activation %d invalid", dm->act);
+  if (dm->flags != 0) return fail(MOE_EINVAL, "flags must be 0");
+  s->M = dm->M;
+  s->N = dm->N;
+  s->K = dm->K;
+  s->ldx = dm->ldx ? dm->ldx : dm->K;
+  s->ldr = dm->ldr ? dm->ldr : dm->N;
+  s->ldy = dm->ldy ? dm->ldy : dm->N;
+  s->act = dm->act;
+  s->bf16 = dm->dtype == MOE_BF16;
+  MOE_TRY(check_ld(s->ldx, s->K, "ldx"));
+  MOE_TRY(check_ld(s->ldr, s->N, "ldr"));
+  MOE_TRY(check_ld(s->ldy, s->N, "ldy"));
+  if (s->ldx % 8 || s->ldr % 8 || s->ldy % 8)
+    return fail(MOE_ENOTSUP, "ldx=%lld, ldr=%lld and ldy=%lld must be multiples of 8", (long long)s->ldx,
+                (long long)s->ldr, (long long)s->ldy);
+  return MOE_OK;
+}
+
+size_t moe_linear_workspace_bytes(const moe_linear_dims* dims, int op) {
+  LinShape s;
+  if (check_linear(dims, &s) != MOE_OK) return 0;
+  if (op == MOE_LINEAR_FORWARD) return linear_fwd_workspace_bytes(s);
+  if (op == MOE_LINEAR_BACKWARD) return linear_bwd_workspace_bytes(s);
+  fail(MOE_EINVAL, "unknown op %d", op);
+  return 0;
+}
+
+static moe_status check_linear_ws(size_t need, void* ws, size_t ws_bytes) {
+  if (need == 0) return MOE_OK;
+  if (ws_bytes < need) return fail(MOE_EWORKSPACE, "workspace of %zu bytes < %zu needed", ws_bytes, need);
+  return need_ptr(ws, "ws");
+}
+
+moe_status moe_linear(const moe_linear_dims* dims, const void* X, const void* W, const float* bias,
+                      const void* residual, void* Z, void* out, void* ws, size_t ws_bytes, void* stream) {
+  LinShape s;
+  MOE_TRY(check_linear(dims, &s));
+  if (s.M == 0) return MOE_OK;
+  MOE_TRY(need_ptr(X, "X"));
+  MOE_TRY(need_ptr(W, "W"));
+  MOE_TRY(opt_ptr(bias, "bias"));
+  MOE_TRY(opt_ptr(residual, "residual"));
+  MOE_TRY(opt_ptr(Z, "Z"));
+  MOE_TRY(need_ptr(out, "out"));
+  MOE_TRY(check_linear_ws(linear_fwd_workspace_bytes(s), ws, ws_bytes));
+  hipStream_t st = static_cast<hipStream_t>(stream);
+  MOE_STAGE(MOE_STAGE_LINEAR, st, launch_linear(s, X, W, bias, residual, Z, out, ws, st), "linear");
+  return MOE_OK;
+}
+
+moe_status moe_linear_backward(const moe_linear_dims* dims, const void* dY, const void* X, const void* W,
+                               const void* Z, void* dX, void* dW, float* dbias, void* ws, size_t ws_bytes,
+                               void* stream) {
+  LinShape s;
+  MOE_TRY(check_linear(dims, &s));
+  if (!dX && !dW && !dbias) return fail(MOE_EINVAL, "dX, dW and dbias are all NULL");
+  if (s.M > 0) {
+    MOE_TRY(need_ptr(dY, "dY"));
+    if (dW) MOE_TRY(need_ptr(X, "X"));
+    if (dX) MOE_TRY(need_ptr(W, "W"));
+    if (s.act != MOE_ACT_NONE) MOE_TRY(need_ptr(Z, "Z"));
+  }
+  MOE_TRY(opt_ptr(dX, "dX"));
+  MOE_TRY(opt_ptr(dW, "dW"));
+  MOE_TRY(opt_ptr(dbias, "dbias"));
+  MOE_TRY(check_linear_ws(linear_bwd_workspace_bytes(s), ws, ws_bytes));
+  hipStream_t st = static_cast<hipStream_t>(stream);
+  MOE_STAGE(MOE_STAGE_LINEAR_BWD, st, launch_linear_dz(s, dY, Z, dbias, ws, st), "linear dZ");
+  if (dX && s.M > 0) MOE_STAGE(MOE_STAGE_LINEAR_BWD, st, launch_linear_dx(s, dY, W, dX, ws, st), "linear dX GEMM");
+  if (dW) MOE_STAGE(MOE_STAGE_LINEAR_BWD, st, launch_linear_dw(s, dY, X, dW, ws, st), "linear dW GEMM");
   return MOE_OK;
 }
 

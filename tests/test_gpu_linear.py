@@ -1,0 +1,246 @@
+"""moe_linear and moe_linear_backward against the float64 oracle.
+
+Bounds (elementwise, u = 2^-23 a step of an fp32 sum, h = half a step of the type): a product of
+length n is off by (n + 8) u times the sum of its terms' sizes; an activation passes that on times
+its steepest slope (below 1.13) and adds its own error, 2^-19 of 1 + |z| (exponential, reciprocal and
+error function are a few steps of fp32 off, the exponential's argument by |z| 2^-24); storing
+rounds by h.  In the backward dZ is rounded by h as an operand of the products, not in dbias."""
+import numpy as np
+import pytest
+import torch
+
+from block_util import DT, HALF, U32, assert_guards, assert_within, check_replays, f64, strided
+from conftest import announce_case
+from mixture_experts_layer_lds_amd import binding as B
+from oracle import block as ob
+
+pytestmark = pytest.mark.gpu
+ACT_ERR = 2.0 ** -19
+
+
+@pytest.fixture(autouse=True)
+def announce(request):
+    announce_case(request.node.nodeid)
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU visible")
+    yield
+
+
+class Proj:
+    def __init__(self, M, N, K, dtype, act, bias, residual, save, pad, seed=0):
+        g = torch.Generator().manual_seed(seed * 7919 + M * 31 + N * 7 + K)
+        rn = lambda *s: torch.randn(*s, generator=g)  # noqa: E731
+        self.M, self.N, self.K, self.dtype, self.act, self.pad = M, N, K, dtype, act, pad
+        self.NW = 2 * N if act == "swiglu" else N
+        dt = DT[dtype]
+        self.X, _ = strided(M, K, pad, dtype, rn(M, K))
+        self.W = (rn(self.NW, K) / max(K, 1) ** 0.5).cuda().to(dt)
+        self.bias = rn(self.NW).cuda() if bias else None
+        self.res = strided(M, N, pad, dtype, rn(M, N))[0] if residual else None
+        self.out, self.out_base = strided(M, N, pad, dtype, extra_rows=2)
+        self.Z = torch.full((M + 1, self.NW), 777.0, device="cuda", dtype=dt) if save else None
+        self.dY, _ = strided(M, N, pad, dtype, rn(M, N))
+        self.dX, self.dX_base = strided(M, K, pad, dtype, extra_rows=2)
+        self.dW = torch.full((self.NW + 1, K), 777.0, device="cuda", dtype=dt)
+        self.db = torch.full((self.NW + 8,), 777.0, device="cuda")
+        ld = lambda n: (n + pad) if pad else 0  # noqa: E731
+        self.dims = B.make_linear_dims(M, N, K, dtype, act, ld(K), ld(N), ld(N))
+        self.wf, self.nf = B.linear_workspace(self.dims, B.LINEAR_FORWARD)
+        self.wb, self.nbk = B.linear_workspace(self.dims, B.LINEAR_BACKWARD)
+        self.wf.fill_(0xFF)
+        self.wb.fill_(0xFF)
+
+    def forward(self):
+        B.moe_linear(self.dims, self.X, self.W, self.bias, self.res, self.Z, self.out, self.wf, self.nf)
+
+    def z_parts(self):
+        """The exact z and the bound of its fp32 error."""
+        X, W = f64(self.X), f64(self.W)
+        b = f64(self.bias) if self.bias is not None else np.zeros(self.NW)
+        z = X @ W.T + b
+        return z, (self.K + 8) * U32 * (np.abs(X) @ np.abs(W).T + np.abs(b))
+
+    def check_forward(self):
+        self.forward()
+        torch.cuda.synchronize()
+        z, ze = self.z_parts()
+        h, N = HALF[self.dtype], self.N
+        res = f64(self.res) if self.res is not None else np.zeros((self.M, N))
+        a = ob.activation(z, self.act)
+        if self.act == "swiglu":
+            g, u, ge, ue = z[:, :N], z[:, N:], ze[:, :N], ze[:, N:]
+            ae = (1.13 * ge + ACT_ERR * (1 + np.abs(g))) * (np.abs(u) + ue) + np.abs(ob.activation(g, "silu")) * ue
+        elif self.act in ("gelu", "silu"):
+            ae = 1.13 * ze + ACT_ERR * (1 + np.abs(z))
+        else:
+            ae = ze
+        ref = a + res
+        assert_within("out", f64(self.out), ref, h * (np.abs(ref) + ae) + ae + 2 * U32 * (np.abs(a) + np.abs(res)))
+        assert_guards(self.out_base, self.M, N, "out")
+        if self.Z is not None:
+            assert_within("Z", f64(self.Z[:self.M]), z, h * (np.abs(z) + ze) + ze)
+            assert bool((self.Z[self.M] == 777.0).all())
+
+    def backward(self, dX=True, dW=True, db=True):
+        B.moe_linear_backward(self.dims, self.dY, self.X, self.W, self.Zs, self.dX if dX else None,
+                              self.dW if dW else None, self.db if db else None, self.wb, self.nbk)
+
+    def check_backward(self):
+        z, _ = self.z_parts()
+        self.Zs = torch.from_numpy(z).cuda().to(DT[self.dtype]) if self.act != "none" else None
+        zs = f64(self.Zs) if self.Zs is not None else z
+        self.backward()
+        torch.cuda.synchronize()
+        dY, X, W = f64(self.dY), f64(self.X), f64(self.W)
+        rX, rW, rb, dz = ob.linear_backward(dY, X, W, zs, self.act)
+        h, N = HALF[self.dtype], self.N
+        if self.act == "swiglu":
+            g, u = np.abs(zs[:, :N]), np.abs(zs[:, N:])
+            de = ACT_ERR * np.concatenate([np.abs(dY) * u * (1 + g) ** 2, np.abs(dY) * (1 + g) ** 2], 1)
+        elif self.act in ("gelu", "silu"):
+            de = ACT_ERR * np.abs(dY) * (1 + np.abs(zs)) ** 2
+        else:
+            de = np.zeros_like(dz)
+        op = de + (h * (np.abs(dz) + de) if self.act != "none" else 0)  # the operand as stored
+        size = np.abs(dz) + op
+        tX = op @ np.abs(W) + (self.NW + 8) * U32 * (size @ np.abs(W))
+        tW = op.T @ np.abs(X) + (self.M + 8) * U32 * (size.T @ np.abs(X))
+        assert_within("dX", f64(self.dX), rX, tX + h * (np.abs(rX) + tX))
+        assert_within("dW", f64(self.dW[:self.NW]), rW, tW + h * (np.abs(rW) + tW))
+        tb = de.sum(0) + (self.M + 8) * U32 * (np.abs(dz) + de).sum(0)
+        assert_within("dbias", f64(self.db[:self.NW]), rb, tb)
+        assert_guards(self.dX_base, self.M, self.K, "dX")
+        assert bool((self.dW[self.NW] == 777.0).all()) and bool((self.db[self.NW:] == 777.0).all())
+        # each gradient alone has the same bits
+        want = [t.clone() for t in (self.dX, self.dW, self.db)]
+        for k, t in enumerate((self.dX, self.dW, self.db)):
+            t.fill_(777.0) if k else self.dX_base.fill_(777.0)
+            self.backward(*[j == k for j in range(3)])
+            assert torch.equal(t, want[k]), ("dX", "dW", "dbias")[k]
+
+
+SIZES = [(1, 8, 8), (1, 264, 40), (1, 2048, 712), (2, 16, 4096), (3, 64, 1032), (7, 1000, 64), (16, 256, 512), (17, 520, 96),
+         (31, 24, 2000), (33, 128, 136), (48, 392, 264), (64, 128, 1544), (65, 256, 320), (130, 72, 200), (255, 256, 256),
+         (257, 264, 264), (300, 1000, 328), (513, 136, 72), (1000, 640, 1032), (1, 40, 8192), (129, 8, 24)]
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("M,N,K", SIZES)
+def test_forward_sizes(M, N, K, dtype):
+    """Every size with two activations, bias, residual, saved z and row strides in turn."""
+    n = SIZES.index((M, N, K))
+    for k, act in enumerate((ob.ACTS[n % 5], ob.ACTS[(n + 3) % 5])):
+        Proj(M, N, K, dtype, act, bias=(n + k) % 3 != 0, residual=(n + k) % 2 == 0, save=(n // 2 + k) % 2 == 0,
+             pad=(0, 8, 24)[(n + k) % 3], seed=k).check_forward()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("act", ob.ACTS)
+@pytest.mark.parametrize("bias,residual,save", [(0, 0, 0), (1, 0, 1), (0, 1, 0), (1, 1, 1)])
+def test_forward_epilogues(act, bias, residual, save, dtype):
+    """One row, a few rows, a split reduction and a whole grid of tiles, with every epilogue."""
+    for M, N, K in ((1, 136, 256), (5, 72, 328), (300, 264, 520), (4100, 1096, 40)):
+        if dtype == "f32" and M > 4000:
+            M, N = 2100, 2056
+        Proj(M, N, K, dtype, act, bias, residual, save, pad=8 * bias).check_forward()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("M,N,K", SIZES)
+def test_backward_sizes(M, N, K, dtype):
+    n = SIZES.index((M, N, K))
+    for k, act in enumerate((ob.ACTS[(n + 1) % 5], ob.ACTS[(n + 4) % 5])):
+        Proj(M, N, K, dtype, act, bias=False, residual=False, save=False, pad=(8, 0, 24)[(n + k) % 3], seed=k).check_backward()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("act", ob.ACTS)
+def test_backward_whole_grids(act, dtype):
+    """Products with enough tiles to go straight to their outputs (dX: many rows; dW: wide)."""
+    Proj(4100, 72, 1928, dtype, act, False, False, False, pad=0).check_backward()
+    Proj(96, 1800 if act == "swiglu" else 3600, 2312, dtype, act, False, False, False, pad=8).check_backward()
+
+
+@pytest.mark.parametrize("act", ob.ACTS)
+def test_backward_against_differences(act):
+    """<dY, out(X + h v) - out(X - h v)> / 2 h against <dX, v>, and the same for W and bias, in fp32:
+    fp32 noise 2^-20 / h of the sizes, truncation h^2."""
+    p = Proj(40, 48, 56, "f32", act, True, True, True, pad=0)
+    p.forward()
+    p.Zs = p.Z[:40].clone()
+    p.backward()
+    h = 2.0 ** -7
+    for var, grad in ((p.X, p.dX), (p.W, p.dW[:p.NW]), (p.bias, p.db[:p.NW])):
+        v = torch.randn(var.shape, generator=torch.Generator(device="cuda").manual_seed(2), device="cuda")
+        v /= v.double().norm()
+        x0, val = var.clone(), []
+        for s in (1, -1):
+            var.copy_(x0 + s * h * v)
+            p.forward()
+            val.append((p.out.double() * p.dY.double()).sum().item())
+        var.copy_(x0)
+        size = p.dY.double().norm().item() * 4 * (1 + p.out.double().norm().item() / 40)
+        if act == "relu":
+            size += 4 * h ** -1 * h  # kinks: at most a few of the 1920 elements cross zero, each by h |v|
+        assert abs((val[0] - val[1]) / (2 * h) - (grad.double() * v.double()).sum().item()) <= size * (h * h + 2.0 ** -20 / h)
+
+
+def test_residual_may_be_the_output():
+    for M, N, K in ((3, 264, 512), (200, 264, 512), (4200, 2056, 64)):
+        for dtype in ("bf16", "f32"):
+            p = Proj(M, N, K, dtype, "silu", True, True, False, pad=0)
+            p.forward()
+            want = p.out.clone()
+            alias = p.res.clone()
+            B.moe_linear(p.dims, p.X, p.W, p.bias, alias, None, alias, p.wf, p.nf)
+            assert torch.equal(alias, want)
+
+
+def test_no_rows():
+    for dtype in ("bf16", "f32"):
+        p = Proj(0, 264, 40, dtype, "gelu", True, False, False, pad=0)
+        p.forward()
+        assert_guards(p.out_base, 0, 264, "out")
+        p.Zs = torch.empty(0, 264, dtype=DT[dtype], device="cuda")
+        p.backward()
+        assert not p.dW[:264].any() and not p.db[:264].any()
+        assert bool((p.dW[264] == 777.0).all()) and bool((p.dX_base == 777.0).all())
+
+
+def test_infinities_and_nans_stay_in_their_rows():
+    """A row of X that holds a NaN or an infinity leaves every other row as it was."""
+    for M in (5, 300, 4100):
+        p = Proj(M, 1096, 72, "bf16", "silu", True, True, False, pad=0)
+        p.forward()
+        want = p.out.clone()
+        p.X[1, 3], p.X[2, 70] = float("nan"), float("inf")
+        p.forward()
+        keep = torch.ones(M, dtype=torch.bool, device="cuda")
+        keep[[1, 2]] = False
+        assert torch.equal(p.out[keep], want[keep]) and p.out[1].isnan().all()
+
+
+@pytest.mark.parametrize("M,N,K,act", [(1, 520, 1032, "swiglu"), (40, 264, 1032, "gelu"), (300, 264, 520, "silu"), (4100, 1096, 40, "relu")])
+def test_graph_replays_and_streams(M, N, K, act):
+    p = Proj(M, N, K, "bf16", act, True, True, True, pad=0)
+    p.forward()
+    p.Zs = p.Z[:M].clone()
+
+    def step():
+        p.forward()
+        p.backward()
+
+    check_replays(step, dict(out=p.out, Z=p.Z[:M], dX=p.dX, dW=p.dW[:p.NW], db=p.db[:p.NW]))
+    want = [t.clone() for t in (p.out, p.dX, p.dW, p.db)]
+    qs = [Proj(M, N, K, "bf16", act, True, True, True, pad=0) for _ in range(2)]
+    for q in qs:
+        q.Zs = p.Zs
+    torch.cuda.synchronize()
+    for q in qs:
+        with torch.cuda.stream(torch.cuda.Stream()):
+            for _ in range(4):
+                q.forward()
+                q.backward()
+    torch.cuda.synchronize()
+    for q in qs:
+        assert all(torch.equal(a, b) for a, b in zip((q.out, q.dX, q.dW, q.db), want))
