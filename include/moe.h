@@ -328,7 +328,7 @@ typedef enum {
 
 /* Shape (host struct).  M rows (0 .. 2^24), N output and K input features (multiples of 8,
  * 8 .. 65536).  ldx, ldr, ldy: row strides in elements of X and dX, of residual, and of out and dY
- * (multiples of 8; 0 = dense).  W, Z and dW are dense.  dtype: type of X, W, residual, Z, out and of the
+ * (multiples of 8, at most 2^22; 0 = dense).  W, Z and dW are dense.  dtype: type of X, W, residual, Z, out and of the
  * gradients dY, dX, dW; bias and dbias are fp32; accumulation is fp32.  act: a moe_act.  flags:
  * reserved, must be 0. */
 typedef struct moe_linear_dims {

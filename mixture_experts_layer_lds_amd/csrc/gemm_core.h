@@ -913,39 +913,6 @@ struct KDmaW8 {
   __device__ static bf16x8 frag(const char* t, int row0, int s) { return KDma::frag(t, row0, s); }
 };
 
-// K-major operand whose rows may end inside a stage (K any multiple of 8): in the last stage the
-// chunks past the row's end come from the zero page, chosen per lane with one v_cndmask per address
-// half on a scalar mask (written out for the reason given at MNDma).
-struct KDmaW8Tail : KDmaW8 {
-  int last;        // index of the last stage
-  uint64_t live;   // lanes whose chunk lies inside the row in that stage
-  uint64_t src[2];
-  template <class RowPtr>
-  __device__ void init(RowPtr row_ptr, int klen) {
-    KDmaW8::init(row_ptr);
-    const int lane = threadIdx.x & 63;
-    const int chunk = (lane & 3) ^ (lane >> 4);
-    last = (klen + 31) / 32 - 1;
-    live = __builtin_amdgcn_ballot_w64(32 * last + chunk * 8 < klen);
-  }
-  template <int P>
-  __device__ void prepare_q(int s, int q) {
-    const int lane = threadIdx.x & 63;
-    const uint64_t a = reinterpret_cast<uint64_t>(g[q] + (int64_t)s * step[q]);
-    const uint64_t zero = reinterpret_cast<uint64_t>(g_zero_page) + (lane & 3) * 16;
-    const uint32_t zl = (uint32_t)zero, zh = (uint32_t)(zero >> 32);
-    const uint64_t m = __builtin_amdgcn_readfirstlane(s) == __builtin_amdgcn_readfirstlane(last) ? live : ~0ull;
-    uint32_t sl = (uint32_t)a, sh = (uint32_t)(a >> 32);
-    asm("v_cndmask_b32_e64 %0, %1, %0, %2" : "+v"(sl) : "v"(zl), "s"(m));
-    asm("v_cndmask_b32_e64 %0, %1, %0, %2" : "+v"(sh) : "v"(zh), "s"(m));
-    src[q] = ((uint64_t)sh << 32) | sl;
-  }
-  __device__ void issue_q(int q, char* dst) const {
-    const int w = threadIdx.x >> 6;
-    dma16(reinterpret_cast<const void*>(src[q]), dst + (8 * q + w) * 1024);
-  }
-};
-
 // MN-major operand (layout as MNDma).  The row ids of a stage are fetched into one of two
 // buffers by the stage's parity P, so that the ids of the next stage can be read while the
 // current one's second half is still to be prepared.

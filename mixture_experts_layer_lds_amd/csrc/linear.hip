@@ -5,10 +5,9 @@
 //   backward   dZ = dY act'(z),  dX = dZ W,  dW = dZ^T X,  db = sum of dZ over rows
 // N' = N, except SwiGLU: N' = 2 N, W = [W_gate; W_up], act(z) = silu(z_gate) z_up.
 //
-// All three products run on the layer's MFMA engine (gemm_core.h: bf16 on eight waves, 256 x 256
-// tiles, the DMA ring; fp32 on the register-staged ring): X and W are K-major in the forward;
-// dX reads W with its rows along the reduction, dW reads both operands so.  Reductions
-// may end inside a stage (any multiple of 8).  Where the output has too few tiles for 256 CUs the
+// All three products run on MFMA main loops (bf16: gemm_dense.h; fp32: the register-staged ring of
+// gemm_core.h): X and W are K-major in the forward; dX reads W with its rows along the reduction,
+// dW reads both operands so.  Reductions may end inside a stage (any multiple of 8).  Where the output has too few tiles for 256 CUs the
 // reduction is cut into slices whose fp32 partial products a second kernel adds in slice order
 // before the epilogue (k_lin_finish).
 //
@@ -16,7 +15,9 @@
 // 16-byte chunks of a row, so that residual, saved pre-activation and output are read and written in
 // whole segments and rounded once.
 #include "gemm_core.h"
+#include "gemm_dense.h"
 #include "internal.h"
+#include "skinny.h"
 
 namespace moe {
 
@@ -72,123 +73,116 @@ struct LinGemm {
   const void* B;
   int64_t ldb;
   int m, n, red, bred;
-  int MT, NT, SK, klen;  // tiles, slices and values of k per slice (a multiple of 32)
+  int MT, NT, SK, klen;  // tiles, slices and values of k per slice (a multiple of 64; fp32: 32)
+  int mid;               // bf16: 128 x 128 tiles
   float* part;           // [SK][m][n] when the output goes there
 };
 
 enum { LIN_FWD = 0, LIN_DX = 1, LIN_DW = 2 };            // operand layouts
 enum { LIN_OUT_EPI = 0, LIN_OUT_GLU = 1, LIN_OUT_PART = 2 };  // where the tile goes
 
-// The tile half held in LDS as fp32 rows (frow), walked in 16-byte chunks: thread owns 8 columns
-// (tid % 16) and rows tid / 16 + 32 k.
-constexpr int LIN_FROW = 128 * 4 + 16;
-static_assert(64 * LIN_FROW <= LDS_BUF, "fp32 staging");
-__device__ __forceinline__ char* lin_frow(LdsBufs L, int r) { return epi_buf(L, r) + (r & 63) * LIN_FROW; }
-
-template <class Val>
-__device__ __forceinline__ void lin_dump(LdsBufs L, int wm, int wn, Val val) {
+// A tile half held in LDS as fp32 rows (row r in slot r / (TM / 2)), walked in 16-byte chunks: a
+// thread owns 8 columns and every 32nd row.
+template <class TI>
+__device__ __forceinline__ char* lin_frow(char* b0, char* b1, int r) {
+  return r < TI::SPLIT ? b0 + r * TI::EPITCH : b1 + (r - TI::SPLIT) * TI::EPITCH;
+}
+template <class TI, class Val>
+__device__ __forceinline__ void lin_dump(char* b0, char* b1, int wm, int wn, Val val) {
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
+  for (int i = 0; i < TI::MI; ++i)
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
       const f32x4 v4 = {val(i, 4 * q), val(i, 4 * q + 1), val(i, 4 * q + 2), val(i, 4 * q + 3)};
-      *reinterpret_cast<f32x4*>(lin_frow(L, acc_m(wm, i)) + (wn * 32 + acc_n(4 * q)) * 4) = v4;
+      const int r = (wm * TI::MI + i) * 32 + (threadIdx.x & 31);
+      *reinterpret_cast<f32x4*>(lin_frow<TI>(b0, b1, r) + (wn * 32 + acc_n(4 * q)) * 4) = v4;
     }
 }
-template <class Row>
-__device__ __forceinline__ void lin_walk(LdsBufs L, int mrows, int valid, Row row) {
-  const int c = (threadIdx.x & 15) * 8;
+template <class TI, class Row>
+__device__ __forceinline__ void lin_walk(char* b0, char* b1, int mrows, int valid, Row row) {
+  const int c = (threadIdx.x % (TI::HC / 8)) * 8;
 #pragma unroll
-  for (int k = 0; k < 8; ++k) {
-    const int r = (int)(threadIdx.x >> 4) + 32 * k;
+  for (int k = 0; k < TI::TM_ / 32; ++k) {
+    const int r = (int)(threadIdx.x / (TI::HC / 8)) + 32 * k;
     if (r >= mrows || c >= valid) continue;
-    const char* p = lin_frow(L, r) + c * 4;
+    const char* p = lin_frow<TI>(b0, b1, r) + c * 4;
     const f32x4 a = *reinterpret_cast<const f32x4*>(p), b = *reinterpret_cast<const f32x4*>(p + 16);
     float f[8] = {a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]};
     row(k, r, c, f);
   }
 }
 
-// bf16: eight waves, 256 x 256 tiles (SwiGLU: 128 output columns, gate rows over up rows in the B
-// tile, so a lane holds both of a column).  Wave column wn has column block j at j 128 + 32 wn, so
-// that block j of every wave is half j of the tile.
-template <int MODE, bool TAIL, int OUT>
-__global__ __launch_bounds__(GEMM8_THREADS, 1) void k_lin_w8(LinGemm g, LinEpi<bf16> ep) {
-  MOE_GEMM_LDS(L);
+// bf16 on the dense main loop (gemm_dense.h).  SwiGLU (LIN_OUT_GLU): a tile has TN / 2 output
+// columns, the B tile stacks their gate rows over their up rows, so a lane holds both of a column.
+template <class TI, int MODE, bool TAIL, int OUT>
+__global__ __launch_bounds__(TI::THREADS, TI::NW == 8 ? 1 : 2) void k_lin_bf16(LinGemm g, LinEpi<bf16> ep) {
+  __shared__ __attribute__((aligned(1024))) char b0[TI::SLOT];
+  __shared__ __attribute__((aligned(1024))) char b1[TI::SLOT];
   const int lin = xcd_remap(blockIdx.x, gridDim.x);
   const int per = g.MT * g.NT;
   const int sl = lin / per;
   if (sl >= g.SK) return;
   int mt, nt;
   raster_tile(lin % per, g.MT, g.NT, mt, nt);
-  constexpr int TN = OUT == LIN_OUT_GLU ? 128 : BN;
-  const int m0 = mt * BM, n0 = nt * TN;
+  constexpr int HC = TI::HC, TN = OUT == LIN_OUT_GLU ? HC : 2 * HC;
+  const int m0 = mt * TI::TM_, n0 = nt * TN;
   const int wave = threadIdx.x >> 6;
-  const int wm = wave >> 2, wn = wave & 3;
+  const int wm = wave / TI::WN_, wn = wave % TI::WN_;
   const int k0 = sl * g.klen, klen = min(g.klen, g.red - k0), blen = max(min(g.klen, g.bred - k0), 1);
-  const int mrows = min(BM, g.m - m0);
+  const int mrows = min(TI::TM_, g.m - m0);
   const int64_t ldab = g.lda * (int64_t)sizeof(bf16), ldbb = g.ldb * (int64_t)sizeof(bf16);
   const char* Ab = static_cast<const char*>(g.A);
   const char* Bb = static_cast<const char*>(g.B);
-  auto bsub = [&](int j) { return j * 128 + wn * 32; };
-  AccW8 acc;
-  const int nkt = (int)cdiv(klen, Mma<bf16>::BK);
-  typedef typename std::conditional<TAIL, KDmaW8Tail, KDmaW8>::type KD;
-  auto krows = [&](auto row_ptr) {
-    KD l;
-    if constexpr (TAIL) l.init(row_ptr, klen);
-    else l.init(row_ptr);
-    return l;
-  };
-  auto arow = [&](int i) -> const char* { return i < mrows ? Ab + (m0 + i) * ldab + (int64_t)k0 * 2 : nullptr; };
-  if constexpr (MODE == LIN_FWD) {
-    auto la = krows(arow);
-    auto lb = krows([&](int i) -> const char* {
-      int r = n0 + i;
-      if (OUT == LIN_OUT_GLU) {
-        if (n0 + (i & 127) >= g.n) return nullptr;
-        r = n0 + (i & 127) + (i < 128 ? 0 : g.n);
-      } else if (r >= g.n) {
-        return nullptr;
-      }
-      return Bb + r * ldbb + (int64_t)k0 * 2;
-    });
-    gemm_mainloop_w8_rows(la, lb, nkt, acc, L, wm, bsub, mrows);
-  } else if constexpr (MODE == LIN_DX) {
-    auto la = krows(arow);
-    const char* bk = Bb + k0 * ldbb + (int64_t)n0 * 2;
-    auto lb = mn_rows_w8([=](int k) { return bk + k * ldbb; }, blen, n0, g.n);
-    gemm_mainloop_w8_rows(la, lb, nkt, acc, L, wm, bsub, mrows);
+  DnAcc<TI::MI> acc;
+  const int nkt = (int)cdiv(klen, DN_BK);
+  if constexpr (MODE == LIN_DW) {
+    DnMN<TI::TM_, TI::NW, TAIL> la;
+    DnMN<2 * HC, TI::NW, TAIL> lb;
+    la.init(Ab + k0 * ldab + (int64_t)m0 * 2, ldab, klen, mrows);
+    lb.init(Bb + k0 * ldbb + (int64_t)n0 * 2, ldbb, blen, min(2 * HC, g.n - n0));
+    dn_mainloop<TI>(la, lb, nkt, acc, b0, b1, wm, wn);
   } else {
-    const char* ak = Ab + k0 * ldab + (int64_t)m0 * 2;
-    const char* bk = Bb + k0 * ldbb + (int64_t)n0 * 2;
-    auto la = mn_rows_w8([=](int k) { return ak + k * ldab; }, klen, m0, g.m);
-    auto lb = mn_rows_w8([=](int k) { return bk + k * ldbb; }, blen, n0, g.n);
-    gemm_mainloop_w8_rows(la, lb, nkt, acc, L, wm, bsub, mrows);
+    DnK<TI::TM_, TI::NW, TAIL> la;
+    la.init(Ab + m0 * ldab + (int64_t)k0 * 2, ldab, klen, [&](int i) { return (int64_t)min(i, mrows - 1); });
+    if constexpr (MODE == LIN_DX) {
+      DnMN<2 * HC, TI::NW, TAIL> lb;
+      lb.init(Bb + k0 * ldbb + (int64_t)n0 * 2, ldbb, blen, min(2 * HC, g.n - n0));
+      dn_mainloop<TI>(la, lb, nkt, acc, b0, b1, wm, wn);
+    } else {
+      DnK<2 * HC, TI::NW, TAIL> lb;
+      const int ncols = min(TN, g.n - n0);
+      // SwiGLU: the tile's upper half holds the up rows, N rows behind the gate rows
+      lb.init(Bb + n0 * ldbb + (int64_t)k0 * 2, ldbb, klen,
+              [&](int i) { return (int64_t)min(OUT == LIN_OUT_GLU ? i % HC : i, ncols - 1); },
+              OUT == LIN_OUT_GLU ? g.n * ldbb : 0);
+      dn_mainloop<TI>(la, lb, nkt, acc, b0, b1, wm, wn);
+    }
   }
+  constexpr int MI = TI::MI;
   if constexpr (OUT == LIN_OUT_PART) {
     float* dst = g.part + (int64_t)sl * g.m * g.n;
 #pragma unroll
     for (int j = 0; j < 2; ++j)
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
-        const int c = n0 + bsub(j) + acc_n(4 * q);  // n is a multiple of 4
+        const int c = n0 + j * HC + wn * 32 + acc_n(4 * q);  // n is a multiple of 4
         if (c >= g.n) continue;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int r = acc_m(wm, i);
+        for (int i = 0; i < MI; ++i) {
+          const int r = (wm * MI + i) * 32 + (threadIdx.x & 31);
           if (r >= mrows) continue;
           *reinterpret_cast<f32x4*>(dst + (int64_t)(m0 + r) * g.n + c) =
               f32x4{acc.c[i][j][4 * q], acc.c[i][j][4 * q + 1], acc.c[i][j][4 * q + 2], acc.c[i][j][4 * q + 3]};
         }
       }
   } else if constexpr (OUT == LIN_OUT_EPI) {
-    const int cw = (threadIdx.x & 15) * 8;
+    constexpr int NR = TI::TM_ / 32;
+    const int cw = (threadIdx.x % (HC / 8)) * 8;
 #pragma unroll
     for (int half = 0; half < 2; ++half) {
-      const int c0 = n0 + half * 128, valid = min(128, g.n - c0);
+      const int c0 = n0 + half * HC, valid = min(HC, g.n - c0);
       if (valid <= 0) break;  // (uniform)
-      u32x4 rv[8];
+      u32x4 rv[NR];
       float b[8] = {0, 0, 0, 0, 0, 0, 0, 0};
       if (cw < valid) {
         if (ep.bias) {
@@ -197,15 +191,15 @@ __global__ __launch_bounds__(GEMM8_THREADS, 1) void k_lin_w8(LinGemm g, LinEpi<b
         }
         if (ep.res) {
 #pragma unroll
-          for (int k = 0; k < 8; ++k) {
-            const int r = min((int)(threadIdx.x >> 4) + 32 * k, mrows - 1);
+          for (int k = 0; k < NR; ++k) {
+            const int r = min((int)(threadIdx.x / (HC / 8)) + 32 * k, mrows - 1);
             rv[k] = ld16_nt(ep.res + (m0 + r) * ep.ldr + c0 + cw);
           }
         }
       }
-      lin_dump(L, wm, wn, [&](int i, int v) { return acc.c[i][half][v]; });
+      lin_dump<TI>(b0, b1, wm, wn, [&](int i, int v) { return acc.c[i][half][v]; });
       __syncthreads();
-      lin_walk(L, mrows, valid, [&](int k, int r, int c, float (&f)[8]) {
+      lin_walk<TI>(b0, b1, mrows, valid, [&](int k, int r, int c, float (&f)[8]) {
 #pragma unroll
         for (int u = 0; u < 8; ++u) f[u] += b[u];
         if (ep.Z) st16_nt(ep.Z + (m0 + r) * ep.ldz + c0 + c, pack16<bf16>(f));
@@ -221,7 +215,7 @@ __global__ __launch_bounds__(GEMM8_THREADS, 1) void k_lin_w8(LinGemm g, LinEpi<b
       __syncthreads();
     }
   } else {  // SwiGLU: block 0 is the gate, block 1 the up projection of the same columns
-    const int valid = min(128, g.n - n0);
+    const int valid = min(HC, g.n - n0);
     if (ep.bias) {
 #pragma unroll
       for (int j = 0; j < 2; ++j)
@@ -231,7 +225,7 @@ __global__ __launch_bounds__(GEMM8_THREADS, 1) void k_lin_w8(LinGemm g, LinEpi<b
           f32x4 b = {0.0f, 0.0f, 0.0f, 0.0f};
           if (c < g.n) b = *reinterpret_cast<const f32x4*>(ep.bias + (int64_t)j * g.n + c);
 #pragma unroll
-          for (int i = 0; i < 4; ++i)
+          for (int i = 0; i < MI; ++i)
 #pragma unroll
             for (int u = 0; u < 4; ++u) acc.c[i][j][4 * q + u] += b[u];
         }
@@ -239,20 +233,20 @@ __global__ __launch_bounds__(GEMM8_THREADS, 1) void k_lin_w8(LinGemm g, LinEpi<b
     if (ep.Z) {
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
-        lin_dump(L, wm, wn, [&](int i, int v) { return acc.c[i][j][v]; });
+        lin_dump<TI>(b0, b1, wm, wn, [&](int i, int v) { return acc.c[i][j][v]; });
         __syncthreads();
-        lin_walk(L, mrows, valid, [&](int, int r, int c, float (&f)[8]) {
+        lin_walk<TI>(b0, b1, mrows, valid, [&](int, int r, int c, float (&f)[8]) {
           st16_nt(ep.Z + (m0 + r) * ep.ldz + (int64_t)j * g.n + n0 + c, pack16<bf16>(f));
         });
         __syncthreads();
       }
     }
-    lin_dump(L, wm, wn, [&](int i, int v) {
+    lin_dump<TI>(b0, b1, wm, wn, [&](int i, int v) {
       const float gv = acc.c[i][0][v];
       return gv * sigmoid_f32(gv) * acc.c[i][1][v];
     });
     __syncthreads();
-    lin_walk(L, mrows, valid, [&](int, int r, int c, float (&f)[8]) {
+    lin_walk<TI>(b0, b1, mrows, valid, [&](int, int r, int c, float (&f)[8]) {
       if (ep.res) {
         float rr[8];
         unpack16<bf16>(ld16_nt(ep.res + (m0 + r) * ep.ldr + n0 + c), rr);
@@ -334,73 +328,149 @@ __global__ __launch_bounds__(GEMM_THREADS, 1) void k_lin_f32(LinGemm g, LinEpi<f
     }
 }
 
-// Adds the SK slices in slice order and applies the epilogue; a thread takes 8 consecutive output
-// columns.  n: output columns; np: columns of the partial products (2 n for SwiGLU).
+// Four consecutive elements of T as fp32.
+template <typename T> __device__ __forceinline__ f32x4 lin_ld4(const T* p) {
+  if constexpr (sizeof(T) == 4) {
+    return *reinterpret_cast<const f32x4*>(p);
+  } else {
+    const u32x2 v = *reinterpret_cast<const u32x2*>(p);
+    return f32x4{__uint_as_float(v[0] << 16), __uint_as_float(v[0] & 0xffff0000u), __uint_as_float(v[1] << 16),
+                 __uint_as_float(v[1] & 0xffff0000u)};
+  }
+}
+template <typename T> __device__ __forceinline__ void lin_st4(T* p, f32x4 v) {
+  if constexpr (sizeof(T) == 4) *reinterpret_cast<f32x4*>(p) = v;
+  else *reinterpret_cast<u32x2*>(p) = u32x2{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
+}
+
+// The epilogue of four consecutive columns c of row r: z is z there (bias not yet added), for
+// SwiGLU the gate's, zu the up projection's.
+template <typename T>
+__device__ __forceinline__ void lin_epi4(const LinEpi<T>& ep, int64_t r, int c, int n, bool glu, f32x4 z, f32x4 zu) {
+  if (ep.bias) {
+    z += *reinterpret_cast<const f32x4*>(ep.bias + c);
+    if (glu) zu += *reinterpret_cast<const f32x4*>(ep.bias + n + c);
+  }
+  if (ep.Z) {
+    lin_st4(ep.Z + r * ep.ldz + c, z);
+    if (glu) lin_st4(ep.Z + r * ep.ldz + n + c, zu);
+  }
+  float f[4] = {z[0], z[1], z[2], z[3]};
+  if (glu) {
+#pragma unroll
+    for (int u = 0; u < 4; ++u) f[u] = f[u] * sigmoid_f32(f[u]) * zu[u];
+  } else {
+    lin_act<4>(f, ep.act);
+  }
+  f32x4 o = {f[0], f[1], f[2], f[3]};
+  if (ep.res) o += lin_ld4(ep.res + r * ep.ldr + c);
+  lin_st4(ep.out + r * ep.ldo + c, o);
+}
+
+// Adds the SK slices in slice order and applies the epilogue; a thread takes four consecutive
+// output columns and requests the slices four at a time.  n: output columns; np: columns of the
+// partial products (2 n for SwiGLU).
 template <typename T>
 __global__ __launch_bounds__(256) void k_lin_finish(const float* __restrict__ part, int SK, int m, int n, int np,
                                                     LinEpi<T> ep) {
   const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  const int cpr = n / 8;
+  const int cpr = n / 4;
   if (i >= (int64_t)m * cpr) return;
-  const int r = (int)(i / cpr), c = (int)(i - (int64_t)r * cpr) * 8;
-  auto sum8 = [&](int col, float (&f)[8]) {
-    f32x4 a = {0.0f, 0.0f, 0.0f, 0.0f}, b = a;
-    const float* p = part + (int64_t)r * np + col;
-    for (int s = 0; s < SK; ++s, p += (int64_t)m * np) {
-      a += __builtin_nontemporal_load(reinterpret_cast<const f32x4*>(p));
-      b += __builtin_nontemporal_load(reinterpret_cast<const f32x4*>(p + 4));
+  const int64_t r = i / cpr;
+  const int c = (int)(i - r * cpr) * 4;
+  const int64_t slice = (int64_t)m * np;
+  const bool glu = np != n;
+  const float* p = part + r * np + c;
+  f32x4 z = {0.0f, 0.0f, 0.0f, 0.0f}, zu = z;
+  auto ld = [](const float* q) { return __builtin_nontemporal_load(reinterpret_cast<const f32x4*>(q)); };
+  int s = 0;
+  for (; s + 4 <= SK; s += 4, p += 4 * slice) {
+    f32x4 v[4], w[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      v[k] = ld(p + k * slice);
+      if (glu) w[k] = ld(p + k * slice + n);
     }
 #pragma unroll
-    for (int u = 0; u < 4; ++u) {
-      f[u] = a[u];
-      f[4 + u] = b[u];
+    for (int k = 0; k < 4; ++k) {
+      z += v[k];
+      if (glu) zu += w[k];
     }
-    if (ep.bias)
-#pragma unroll
-      for (int u = 0; u < 8; ++u) f[u] += ep.bias[col + u];
-    if (ep.Z) {
-      T* z = ep.Z + r * ep.ldz + col;
-#pragma unroll
-      for (int u = 0; u < 8; u += 16 / (int)sizeof(T)) st16_nt(z + u, pack16<T>(f + u));
-    }
-  };
-  float f[8];
-  sum8(c, f);
-  if (np != n) {
-    float up[8];
-    sum8(n + c, up);
-#pragma unroll
-    for (int u = 0; u < 8; ++u) f[u] = f[u] * sigmoid_f32(f[u]) * up[u];
-  } else {
-    lin_act<8>(f, ep.act);
   }
-  T* o = ep.out + r * ep.ldo + c;
+  for (; s < SK; ++s, p += slice) {
+    z += ld(p);
+    if (glu) zu += ld(p + n);
+  }
+  lin_epi4(ep, r, c, n, glu, z, zu);
+}
+
+// A few rows (single tokens, small decode batches): one workgroup per 16 rows of W (SwiGLU: 8 gate
+// and the 8 matching up rows), its waves sharing the reduction; W is streamed from memory straight
+// into the MFMA's A operand (two batches of 1 KB loads in flight per wave) and X, which stays in
+// the caches, into B, NG groups of 16 rows.  The waves' partial tiles meet in LDS, are added in
+// wave order, and wave g finishes group g in the same launch.  Bound by reading W once.
+template <typename T, int NG, bool GLU>
+__global__ __launch_bounds__(1024) void k_lin_skinny(const T* __restrict__ X, int64_t ldx, const T* __restrict__ W,
+                                                     int m, int n, int K, LinEpi<T> ep) {
+  extern __shared__ f32x4 sk_part[];  // [wave][NG][64]
+  constexpr int S = DecMma<T>::S, V = DecMma<T>::V;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), W_ = blockDim.x >> 6;
+  const int r16 = lane & 15, q = lane >> 4, ko = q * V;
+  constexpr int TC = GLU ? 8 : 16;  // output columns per tile
+  const int c0 = blockIdx.x * TC;
+  const int row = GLU ? (r16 < 8 ? c0 + r16 : n + c0 + r16 - 8) : min(c0 + r16, n - 1);
+  DecStream<T, NG> ds;
+  ds.w = W + (int64_t)row * K + ko;
 #pragma unroll
-  for (int u = 0; u < 8; u += 16 / (int)sizeof(T)) {
-    if (ep.res) {
-      float rr[16 / sizeof(T)];
-      unpack16<T>(ld16(ep.res + r * ep.ldr + c + u), rr);
+  for (int g = 0; g < NG; ++g) ds.x[g] = X + (int64_t)min(g * 16 + r16, m - 1) * ldx + ko;
+  f32x4 acc[NG];
 #pragma unroll
-      for (int k = 0; k < 16 / (int)sizeof(T); ++k) f[u + k] += rr[k];
+  for (int g = 0; g < NG; ++g) acc[g] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+  const int ns = K / S, a = (int)((int64_t)ns * wave / W_), b = (int)((int64_t)ns * (wave + 1) / W_);
+  dec_stream<T, NG>(ds, a, b, acc);
+  if (wave == W_ - 1 && K % S) {  // the last, partial step: lanes past K supply zeros on both sides
+    const bool in = ns * S + ko < K;
+    const u32x4 zero = {0u, 0u, 0u, 0u};
+    const u32x4 wv = in ? ld16(ds.w + ns * S) : zero;
+#pragma unroll
+    for (int g = 0; g < NG; ++g) {
+      const u32x4 xv = in ? ld16(ds.x[g] + ns * S) : zero;
+      acc[g] = DecMma<T>::mma(wv, xv, acc[g]);
     }
-    st16_nt(o + u, pack16<T>(f + u));
+  }
+#pragma unroll
+  for (int g = 0; g < NG; ++g) sk_part[(wave * NG + g) * 64 + lane] = acc[g];
+  __syncthreads();
+  for (int g = wave; g < NG; g += W_) {
+    f32x4 v = sk_part[g * 64 + lane];
+    for (int w = 1; w < W_; ++w) v += sk_part[(w * NG + g) * 64 + lane];
+    const int r = g * 16 + r16;
+    if constexpr (GLU) {  // gate rows in lanes 0-31, the same columns' up rows 32 lanes above
+      f32x4 up;
+#pragma unroll
+      for (int u = 0; u < 4; ++u) up[u] = __shfl_xor(v[u], 32, 64);
+      if (q < 2 && r < m) lin_epi4(ep, (int64_t)r, c0 + 4 * q, n, true, v, up);
+    } else {
+      const int c = c0 + 4 * q;
+      if (r < m && c < n) lin_epi4(ep, (int64_t)r, c, n, false, v, v);
+    }
   }
 }
 
 // dZ = dY act'(z) (SwiGLU: [dG | dU]) and the bias gradient's partial sums: a workgroup takes 256
-// columns (32 lanes of 8) and LIN_DZ_ROWS rows (8 at a time); db_part[row block][column].  dZ may
-// be null (only the sums), db_part too.
-constexpr int LIN_DZ_ROWS = 64;
+// columns (32 lanes of 8) and `rows` rows (8 at a time); db_part[row block][column].  dZ may be
+// null (only the sums), db_part too.
 template <typename T>
 __global__ __launch_bounds__(256) void k_lin_dz(const T* __restrict__ dY, int64_t ldy, const T* __restrict__ Z, int m,
-                                                int n, int act, T* __restrict__ dZ, float* __restrict__ db_part) {
+                                                int n, int act, int rows, T* __restrict__ dZ,
+                                                float* __restrict__ db_part) {
   constexpr int VEC = 16 / sizeof(T);
   __shared__ float red[8][256 + 4];
   const int glu = act == LIN_SWIGLU, np = glu ? 2 * n : n;
   const int cl = (threadIdx.x & 31) * 8, rl = threadIdx.x >> 5;
   const int cbs = (n + 255) / 256, cb = blockIdx.x % cbs, rb = blockIdx.x / cbs;
   const int c = cb * 256 + cl;
-  const int r0 = rb * LIN_DZ_ROWS, r1 = min(m, r0 + LIN_DZ_ROWS);
+  const int r0 = rb * rows, r1 = min(m, r0 + rows);
   float s0[8], s1[8];
 #pragma unroll
   for (int u = 0; u < 8; ++u) s0[u] = s1[u] = 0.0f;
@@ -454,40 +524,67 @@ __global__ __launch_bounds__(256) void k_lin_dz(const T* __restrict__ dY, int64_
   }
 }
 
-// db = the row blocks' sums in order (fp64): 64 columns by 4 runs of row blocks per workgroup.
-__global__ __launch_bounds__(256) void k_lin_db(const float* __restrict__ db_part, int blocks, int np,
-                                                float* __restrict__ db) {
-  __shared__ double red[4][64];
-  const int cl = threadIdx.x & 63, run = threadIdx.x >> 6;
-  const int c = blockIdx.x * 64 + cl;
+// db = the row blocks' sums (fp64): 32 columns by 32 runs of row blocks per workgroup, then the runs
+// in order.
+__global__ __launch_bounds__(1024) void k_lin_db(const float* __restrict__ db_part, int blocks, int np,
+                                                 float* __restrict__ db) {
+  __shared__ double red[32][33];
+  const int cl = threadIdx.x & 31, run = threadIdx.x >> 5;
+  const int c = blockIdx.x * 32 + cl;
   double v = 0.0;
-  if (c < np)
-    for (int b = run; b < blocks; b += 4) v += (double)db_part[(int64_t)b * np + c];
+  if (c < np) {
+#pragma unroll 4
+    for (int b = run; b < blocks; b += 32) v += (double)db_part[(int64_t)b * np + c];
+  }
   red[run][cl] = v;
   __syncthreads();
-  if (run == 0 && c < np) db[c] = (float)((red[0][cl] + red[1][cl]) + (red[2][cl] + red[3][cl]));
+  if (run == 0 && c < np) {
+    for (int q = 1; q < 32; ++q) v += red[q][cl];
+    db[c] = (float)v;
+  }
 }
 
 // ---------------------------------------------------------------------------------------------
 // Host side
 // ---------------------------------------------------------------------------------------------
-// Slices of a product's reduction: one where the tiles fill half the chip, else as many as fill
-// it, each of at least four stages.
-static void lin_plan(LinGemm& g, int tn, bool may_split) {
-  g.MT = (int)cdiv(g.m, BM);
-  g.NT = (int)cdiv(g.n, tn);
+// The bf16 tiles: 256 x 256 on eight waves, and 128 x 128 on four (two workgroups per CU) where the
+// larger ones are too few to fill the chip.
+typedef DnTile<256, 256, 2, 4> LinBig;
+typedef DnTile<128, 128, 2, 2> LinMid;
+
+// Tile size and slices of a product's reduction: one where the tiles fill half the chip, else as
+// many as fill it, each of at least four stages.
+static void lin_plan(LinGemm& g, bool bf16_, bool may_split) {
+  const int64_t big = cdiv(g.m, 256) * cdiv(g.n, 256);
+  g.mid = bf16_ && big < 192;
+  const int t = g.mid ? 128 : 256;
+  const int bk = bf16_ ? DN_BK : 32;
+  g.MT = (int)cdiv(g.m, t);
+  g.NT = (int)cdiv(g.n, t);
   const int64_t tiles = g.m ? (int64_t)g.MT * g.NT : 1;
-  const int stages = (int)cdiv(g.red, 32);
+  const int slots = g.mid ? 512 : 256;
+  const int stages = (int)cdiv(g.red, bk);
   int sk = 1;
-  if (may_split && tiles < 128) {
-    sk = (int)(256 / tiles);
+  if (may_split && tiles < slots / 2) {
+    sk = (int)(slots / tiles);
     if (sk > stages / 4) sk = stages / 4;
     if (sk > 64) sk = 64;
     if (sk < 1) sk = 1;
   }
-  g.klen = (int)cdiv(stages, sk) * 32;
+  g.klen = (int)cdiv(stages, sk) * bk;
   g.SK = g.red > 0 ? (int)cdiv(g.red, g.klen) : 1;
 }
+
+// Rows per workgroup of k_lin_dz: 64 where that gives four workgroups per CU, fewer (at least 8) for
+// small inputs, whose time is the length of one workgroup's row loop.
+static int lin_dz_rows(const LinShape& s) {
+  int rows = 64;
+  while (rows > 8 && cdiv(s.N, 256) * cdiv(s.M, rows) < 1024) rows /= 2;
+  return rows;
+}
+
+// Rows up to which the forward streams W through k_lin_skinny.
+constexpr int LIN_SKINNY_M = 32;
 
 static LinGemm lin_gemm(const LinShape& s, int mode) {
   LinGemm g{};
@@ -506,7 +603,7 @@ static LinGemm lin_gemm(const LinShape& s, int mode) {
     g.red = (int)s.M;
   }
   g.bred = g.red;
-  lin_plan(g, BN, true);
+  lin_plan(g, s.bf16, true);
   return g;
 }
 
@@ -517,7 +614,7 @@ static bool lin_fwd_part(const LinShape& s, const LinGemm& g) { return g.SK > 1 
 static size_t lin_part_bytes(const LinGemm& g) { return (size_t)g.SK * g.m * g.n * sizeof(float); }
 
 size_t linear_fwd_workspace_bytes(const LinShape& s) {
-  if (s.M == 0) return 0;
+  if (s.M <= LIN_SKINNY_M) return 0;
   const LinGemm g = lin_gemm(s, LIN_FWD);
   return lin_fwd_part(s, g) ? lin_part_bytes(g) : 0;
 }
@@ -538,7 +635,7 @@ static size_t lin_carve_bwd(const LinShape& s, void* base, LinBwdWs* w) {
   const int64_t NW = s.act == LIN_SWIGLU ? 2 * s.N : s.N;
   LinBwdWs q;
   q.dZ = take(s.act == LIN_NONE ? 0 : (size_t)s.M * NW * (s.bf16 ? 2 : 4));
-  q.db_part = reinterpret_cast<float*>(take((size_t)cdiv(s.M, LIN_DZ_ROWS) * NW * 4));
+  q.db_part = reinterpret_cast<float*>(take((size_t)cdiv(s.M, lin_dz_rows(s)) * NW * 4));
   const LinGemm gx = lin_gemm(s, LIN_DX), gw = lin_gemm(s, LIN_DW);
   const size_t px = gx.SK > 1 ? lin_part_bytes(gx) : 0, pw = gw.SK > 1 ? lin_part_bytes(gw) : 0;
   q.part = reinterpret_cast<float*>(take(px > pw ? px : pw));
@@ -548,15 +645,21 @@ static size_t lin_carve_bwd(const LinShape& s, void* base, LinBwdWs* w) {
 
 size_t linear_bwd_workspace_bytes(const LinShape& s) { return lin_carve_bwd(s, nullptr, nullptr); }
 
+template <class TI, int MODE, int OUT>
+static void lin_launch_bf16(const LinGemm& g, const LinEpi<bf16>& ep, hipStream_t st) {
+  const int grid = grid8((int64_t)g.MT * g.NT * g.SK);
+  if (g.red % DN_BK || g.bred != g.red) k_lin_bf16<TI, MODE, true, OUT><<<grid, TI::THREADS, 0, st>>>(g, ep);
+  else k_lin_bf16<TI, MODE, false, OUT><<<grid, TI::THREADS, 0, st>>>(g, ep);
+}
 template <int MODE, int OUT>
 static void lin_launch(const LinShape& s, const LinGemm& g, const LinEpi<bf16>& eb, const LinEpi<float>& ef,
                        hipStream_t st) {
-  const int grid = grid8((int64_t)g.MT * g.NT * g.SK);
   if (s.bf16) {
-    if (MODE != LIN_DW && g.red % 32) k_lin_w8<MODE, MODE != LIN_DW, OUT><<<grid, GEMM8_THREADS, 0, st>>>(g, eb);
-    else k_lin_w8<MODE, false, OUT><<<grid, GEMM8_THREADS, 0, st>>>(g, eb);
+    if (g.mid) lin_launch_bf16<LinMid, MODE, OUT>(g, eb, st);
+    else lin_launch_bf16<LinBig, MODE, OUT>(g, eb, st);
   } else {
-    if constexpr (OUT != LIN_OUT_GLU) k_lin_f32<MODE, OUT><<<grid, GEMM_THREADS, 0, st>>>(g, ef);
+    if constexpr (OUT != LIN_OUT_GLU)
+      k_lin_f32<MODE, OUT><<<grid8((int64_t)g.MT * g.NT * g.SK), GEMM_THREADS, 0, st>>>(g, ef);
   }
 }
 
@@ -569,7 +672,7 @@ static hipError_t lin_run(const LinShape& s, LinGemm g, float* part, const LinEp
     if constexpr (MODE == LIN_FWD) {
       if (eb.act == LIN_SWIGLU) {
         g.n = (int)s.N;
-        g.NT = (int)cdiv(g.n, 128);
+        g.NT = (int)cdiv(g.n, g.mid ? 64 : 128);
         lin_launch<MODE, LIN_OUT_GLU>(s, g, eb, ef, st);
         return hipGetLastError();
       }
@@ -582,7 +685,7 @@ static hipError_t lin_run(const LinShape& s, LinGemm g, float* part, const LinEp
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
   const int n = eb.act == LIN_SWIGLU ? g.n / 2 : g.n;
-  const int grid = (int)cdiv((int64_t)g.m * (n / 8), 256);
+  const int grid = (int)cdiv((int64_t)g.m * (n / 4), 256);
   if (s.bf16) k_lin_finish<bf16><<<grid, 256, 0, st>>>(part, g.SK, g.m, n, g.n, eb);
   else k_lin_finish<float><<<grid, 256, 0, st>>>(part, g.SK, g.m, n, g.n, ef);
   return hipGetLastError();
@@ -594,6 +697,26 @@ static LinEpi<T> lin_epi(const float* bias, const void* res, int64_t ldr, void* 
   return LinEpi<T>{bias, static_cast<const T*>(res), ldr, static_cast<T*>(Z), ldz, static_cast<T*>(out), ldo, act};
 }
 
+template <typename T, int NG>
+static void lin_skinny_ng(const LinShape& s, const void* X, const void* W, const LinEpi<T>& ep, hipStream_t st) {
+  const bool glu = s.act == LIN_SWIGLU;
+  const int tiles = (int)cdiv(s.N, glu ? 8 : 16);
+  // waves per tile: enough that the grid has 8 per CU, each with at least four steps to read
+  int w = 4;
+  while (w < 16 && tiles * w < 2048 && s.K / (w * DecMma<T>::S) >= 8) w *= 2;
+  const size_t lds = (size_t)w * NG * 64 * sizeof(f32x4);
+  const T* x = static_cast<const T*>(X);
+  const T* wt = static_cast<const T*>(W);
+  if (glu) k_lin_skinny<T, NG, true><<<tiles, w * 64, lds, st>>>(x, s.ldx, wt, (int)s.M, (int)s.N, (int)s.K, ep);
+  else k_lin_skinny<T, NG, false><<<tiles, w * 64, lds, st>>>(x, s.ldx, wt, (int)s.M, (int)s.N, (int)s.K, ep);
+}
+template <typename T>
+static hipError_t lin_skinny(const LinShape& s, const void* X, const void* W, const LinEpi<T>& ep, hipStream_t st) {
+  if (s.M <= 16) lin_skinny_ng<T, 1>(s, X, W, ep, st);
+  else lin_skinny_ng<T, 2>(s, X, W, ep, st);
+  return hipGetLastError();
+}
+
 hipError_t launch_linear(const LinShape& s, const void* X, const void* W, const float* bias, const void* residual,
                          void* Z, void* out, void* ws, hipStream_t st) {
   if (s.M == 0) return hipSuccess;
@@ -602,27 +725,29 @@ hipError_t launch_linear(const LinShape& s, const void* X, const void* W, const 
   g.lda = s.ldx;
   g.B = W;
   g.ldb = s.K;
-  return lin_run<LIN_FWD>(s, g, static_cast<float*>(ws), lin_epi<bf16>(bias, residual, s.ldr, Z, g.n, out, s.ldy, s.act),
-                          lin_epi<float>(bias, residual, s.ldr, Z, g.n, out, s.ldy, s.act), lin_fwd_part(s, g), st);
+  const LinEpi<bf16> eb = lin_epi<bf16>(bias, residual, s.ldr, Z, g.n, out, s.ldy, s.act);
+  const LinEpi<float> ef = lin_epi<float>(bias, residual, s.ldr, Z, g.n, out, s.ldy, s.act);
+  if (s.M <= LIN_SKINNY_M) return s.bf16 ? lin_skinny(s, X, W, eb, st) : lin_skinny(s, X, W, ef, st);
+  return lin_run<LIN_FWD>(s, g, static_cast<float*>(ws), eb, ef, lin_fwd_part(s, g), st);
 }
 
 hipError_t launch_linear_dz(const LinShape& s, const void* dY, const void* Z, float* dbias, void* ws, hipStream_t st) {
   LinBwdWs w;
   lin_carve_bwd(s, ws, &w);
   const int NW = (int)(s.act == LIN_SWIGLU ? 2 * s.N : s.N);
-  const int blocks = (int)cdiv(s.M, LIN_DZ_ROWS);
+  const int rows = lin_dz_rows(s), blocks = (int)cdiv(s.M, rows);
   if (s.M > 0 && (dbias || s.act != LIN_NONE)) {
     const int grid = (int)(cdiv(s.N, 256) * blocks);
     void* dZ = s.act == LIN_NONE ? nullptr : w.dZ;
     float* db = dbias ? w.db_part : nullptr;
     if (s.bf16)
-      k_lin_dz<bf16><<<grid, 256, 0, st>>>((const bf16*)dY, s.ldy, (const bf16*)Z, (int)s.M, (int)s.N, s.act, (bf16*)dZ, db);
+      k_lin_dz<bf16><<<grid, 256, 0, st>>>((const bf16*)dY, s.ldy, (const bf16*)Z, (int)s.M, (int)s.N, s.act, rows, (bf16*)dZ, db);
     else
-      k_lin_dz<float><<<grid, 256, 0, st>>>((const float*)dY, s.ldy, (const float*)Z, (int)s.M, (int)s.N, s.act, (float*)dZ, db);
+      k_lin_dz<float><<<grid, 256, 0, st>>>((const float*)dY, s.ldy, (const float*)Z, (int)s.M, (int)s.N, s.act, rows, (float*)dZ, db);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
-  if (dbias) k_lin_db<<<(int)cdiv(NW, 64), 256, 0, st>>>(w.db_part, blocks, NW, dbias);
+  if (dbias) k_lin_db<<<(int)cdiv(NW, 32), 1024, 0, st>>>(w.db_part, blocks, NW, dbias);
   return hipGetLastError();
 }
 
@@ -662,7 +787,7 @@ hipError_t launch_logit_dx(const Shape& s, const void* dL, int E_pad, const void
   g.n = (int)s.d;
   g.red = E_pad;
   g.bred = s.E;
-  lin_plan(g, BN, false);
+  lin_plan(g, s.bf16, false);
   return lin_run<LIN_DX>(ls, g, nullptr, lin_epi<bf16>(nullptr, dX, s.d, nullptr, 0, dX, s.d, LIN_NONE),
                          lin_epi<float>(nullptr, dX, s.d, nullptr, 0, dX, s.d, LIN_NONE), false, st);
 }

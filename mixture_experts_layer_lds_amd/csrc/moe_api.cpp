@@ -710,10 +710,13 @@ static moe_status drop_args(double p, const uint64_t* rng, DropArgs* a) {
   return MOE_OK;
 }
 
-static moe_status check_ld(int64_t ld, int64_t cols, const char* name) {
-  if (ld < cols || ld > ((int64_t)1 << 40)) return fail(MOE_EINVAL, "%s=%lld is less than the row's %lld elements (or above 2^40)", name, (long long)ld, (long long)cols);
+static moe_status check_ld(int64_t ld, int64_t cols, int64_t most, const char* name) {
+  if (ld < cols || ld > most)
+    return fail(MOE_EINVAL, "%s=%lld out of range [%lld, %lld]", name, (long long)ld, (long long)cols, (long long)most);
   return MOE_OK;
 }
+constexpr int64_t kMaxStride = (int64_t)1 << 40;        // dropout: 64-bit offsets throughout
+constexpr int64_t kMaxLinearStride = (int64_t)1 << 22;  // dense projection: a tile's offsets are 32-bit
 
 moe_status moe_dropout(int64_t rows, int64_t cols, int dtype, const void* x, int64_t ldx, const void* residual,
                        int64_t ldr, double p, const uint64_t* rng, void* out, int64_t ldo, void* stream) {
@@ -722,9 +725,9 @@ moe_status moe_dropout(int64_t rows, int64_t cols, int dtype, const void* x, int
   if (rows > 0x7fffffffll || rows * ((cols + 7) / 8) > 0x7fffffffll)
     return fail(MOE_ENOTSUP, "rows=%lld x cols=%lld is more than 2^31 groups of 8", (long long)rows, (long long)cols);
   if (dtype != MOE_BF16 && dtype != MOE_F32) return fail(MOE_ENOTSUP, "dtype %d not supported", dtype);
-  MOE_TRY(check_ld(ldx, cols, "ldx"));
-  MOE_TRY(check_ld(ldo, cols, "ldo"));
-  if (residual) MOE_TRY(check_ld(ldr, cols, "ldr"));
+  MOE_TRY(check_ld(ldx, cols, kMaxStride, "ldx"));
+  MOE_TRY(check_ld(ldo, cols, kMaxStride, "ldo"));
+  if (residual) MOE_TRY(check_ld(ldr, cols, kMaxStride, "ldr"));
   DropArgs a;
   MOE_TRY(drop_args(p, rng, &a));
   if (rows == 0) return MOE_OK;
@@ -772,9 +775,9 @@ static moe_status check_linear(const moe_linear_dims* dm, LinShape* s) {
   s->ldy = dm->ldy ? dm->ldy : dm->N;
   s->act = dm->act;
   s->bf16 = dm->dtype == MOE_BF16;
-  MOE_TRY(check_ld(s->ldx, s->K, "ldx"));
-  MOE_TRY(check_ld(s->ldr, s->N, "ldr"));
-  MOE_TRY(check_ld(s->ldy, s->N, "ldy"));
+  MOE_TRY(check_ld(s->ldx, s->K, kMaxLinearStride, "ldx"));
+  MOE_TRY(check_ld(s->ldr, s->N, kMaxLinearStride, "ldr"));
+  MOE_TRY(check_ld(s->ldy, s->N, kMaxLinearStride, "ldy"));
   if (s->ldx % 8 || s->ldr % 8 || s->ldy % 8)
     return fail(MOE_ENOTSUP, "ldx=%lld, ldr=%lld and ldy=%lld must be multiples of 8", (long long)s->ldx,
                 (long long)s->ldr, (long long)s->ldy);

@@ -9,12 +9,16 @@
 // A sequence is a run of tokens seq_off[s] .. seq_off[s+1] - 1; a token counts if it lies in one
 // and its mask byte is not zero.
 //
-// Forward: one workgroup per chunk of 64 tokens reads the logits once (the only large operand).
+// Forward: one workgroup of 16 waves per chunk of tokens (64, more where rows are short) reads the
+// logits once (the only large operand); it requests the whole chunk, its choices and the sequence
+// table together before it uses any, since at these sizes the length of the chain of dependent
+// loads, not their bytes, sets the time.
 // Where a chunk holds several sequences it is cut into pieces, and the piece of chunk c and
 // sequence s leaves its partial sums in slot c + s: along the tokens either c or s grows from one
 // piece to the next, so slots never collide, and the number of pieces needs no host knowledge.  A
 // second launch adds the slots of a sequence in chunk order (in 64 bits), and its last workgroup
-// forms the two losses.  No floating-point atomics: the order of every sum is fixed.
+// forms the two losses.  Where one chunk holds the whole batch, its workgroup writes the results
+// itself and there is no second launch.  No floating-point atomics: the order of every sum is fixed.
 //
 // A token is taken by G lanes, each holding up to 4 NV of its logits (four consecutive ones per
 // 16-byte load where E is a multiple of 4), so that a wave reads whole rows whatever E is; the
@@ -24,11 +28,11 @@
 
 namespace moe {
 
-constexpr int RL_CHUNK = 64;     // tokens per workgroup
-constexpr int RL_THREADS = 256;
+constexpr int RL_BWD_CHUNK = 64;  // tokens per workgroup of the backward
+constexpr int RL_THREADS = 1024;
 constexpr int RL_WAVES = RL_THREADS / 64;
 constexpr int RL_JOIN_COLS = 32;      // columns per workgroup of the joining launch
-constexpr int RL_JOIN_THREADS = 1024;
+constexpr int RL_BWD_THREADS = 256;
 
 struct RlossWs {
   unsigned* ticket;  // workgroups of the joining launch that have finished
@@ -40,7 +44,28 @@ struct RlossWs {
   double* zs;        // [n_seq]
 };
 
-static int64_t rl_chunks(int64_t T) { return cdiv(T, RL_CHUNK); }
+// Lanes per token (G) and 4-logit chunks per lane (NV) for E: the fewest idle lanes, at most 16
+// logits a lane.
+struct RlLayout {
+  int G, NV;
+};
+static RlLayout rl_layout(int E) {
+  const int q = (E + 3) / 4;  // chunks per row
+  if (q <= 2) return {2, 1};
+  if (q <= 4) return {4, 1};
+  if (q <= 8) return {8, 1};
+  if (q <= 16) return {16, 1};
+  if (q <= 32) return {16, 2};
+  if (q <= 48) return {16, 3};
+  if (q <= 64) return {32, 2};
+  if (q <= 96) return {32, 3};
+  if (q <= 128) return {64, 2};
+  return {64, 4};
+}
+// Steps of the forward's workgroup over its chunk, and the chunk's tokens.
+__host__ __device__ constexpr int rl_steps(int G) { return G > 16 ? G / 16 : 1; }
+__host__ __device__ constexpr int rl_chunk(int G) { return RL_WAVES * (64 / G) * rl_steps(G); }
+static int64_t rl_chunks(int64_t T, int E) { return cdiv(T, rl_chunk(rl_layout(E).G)); }
 static int rl_colblocks(int E) { return (E + RL_JOIN_COLS - 1) / RL_JOIN_COLS; }
 
 static size_t rl_carve(void* base, int64_t T, int E, int n_seq, RlossWs* w) {
@@ -51,7 +76,7 @@ static size_t rl_carve(void* base, int64_t T, int E, int n_seq, RlossWs* w) {
     off = align_up(off + bytes, 256);
     return p;
   };
-  const size_t slots = (size_t)(rl_chunks(T) + n_seq);
+  const size_t slots = (size_t)(rl_chunks(T, E) + n_seq);
   RlossWs q;
   q.ticket = reinterpret_cast<unsigned*>(take(sizeof(unsigned)));
   q.prob = reinterpret_cast<float*>(take(slots * E * 4));
@@ -71,26 +96,37 @@ __device__ __forceinline__ int rl_off(const int32_t* seq_off, int s, int T) {
   return seq_off ? min(max(seq_off[s], 0), T) : (s ? T : 0);
 }
 
-// The piece of the chunk [.., end) that starts at token t: its sequence (-1: outside all of them)
-// and its end.
-__device__ __forceinline__ int rl_piece(const int32_t* seq_off, int n_seq, int T, int t, int end, int& stop) {
-  int lo = 0, hi = n_seq;  // the first s with seq_off[s + 1] > t
+// The piece of a chunk that starts at token t: its sequence (-1: outside all of them) and its end,
+// at most `end`.  off(s) gives the table's entries.
+template <class Off>
+__device__ __forceinline__ int rl_piece(Off off, int n_seq, int t, int end, int& stop) {
+  int lo = 0, hi = n_seq;  // the first s with off(s + 1) > t
   while (lo < hi) {
     const int mid = (lo + hi) >> 1;
-    if (rl_off(seq_off, mid + 1, T) > t) hi = mid;
+    if (off(mid + 1) > t) hi = mid;
     else lo = mid + 1;
   }
   if (lo >= n_seq) {
     stop = end;
     return -1;
   }
-  const int b = rl_off(seq_off, lo, T);
+  const int b = off(lo);
   if (t < b) {
     stop = min(end, b);
     return -1;
   }
-  stop = min(end, max(rl_off(seq_off, lo + 1, T), t + 1));
+  stop = min(end, max(off(lo + 1), t + 1));
   return lo;
+}
+
+// The sequence table in LDS where it fits, else read in place.
+constexpr int RL_TABLE = 1024;
+struct RlTable {
+  int off[RL_TABLE + 1];
+};
+__device__ __forceinline__ void rl_table_load(RlTable& L, const int32_t* seq_off, int n_seq, int T) {
+  if (n_seq <= RL_TABLE)
+    for (int i = threadIdx.x; i <= n_seq; i += blockDim.x) L.off[i] = rl_off(seq_off, i, T);
 }
 
 __device__ __forceinline__ float rl_exp(float x) { return __builtin_amdgcn_exp2f(x * 1.44269504088896f); }
@@ -142,70 +178,235 @@ __device__ __forceinline__ float rl_group_max(float v) {
   return v;
 }
 
-template <int G, int NV, bool V4>
+// Where the sums end up.
+struct RlossOut {
+  int32_t* seq_tokens;
+  int32_t* seq_counts;
+  float* prob_sum;
+  float* loss;
+};
+
+constexpr int RL_RUNS = RL_THREADS / RL_JOIN_COLS;
+struct RlJoinLds {
+  double p[RL_RUNS][RL_JOIN_COLS + 1];
+  int c[RL_RUNS][RL_JOIN_COLS + 1];
+  double z[RL_WAVES], b[RL_WAVES];
+  long long n[RL_WAVES];
+  int last;
+};
+
+__device__ __forceinline__ void rl_write_loss(const RlossOut& o, int E, int K, double bal, double z, long long n) {
+  o.loss[0] = n ? (float)(bal * (double)E / ((double)K * (double)n)) : 0.0f;
+  o.loss[1] = n ? (float)(z / (double)n) : 0.0f;
+}
+
+// Adds sequence s's slots for columns block cb in chunk order: 32 columns by 32 runs of chunks, then
+// the runs in order.  Also the sequence's tokens and z sum when cb is 0.
+__device__ __forceinline__ void rl_join(RlJoinLds& L, int s, int cb, int chunk, int T, int E,
+                                        const int32_t* __restrict__ seq_off, const RlossWs& w, const RlossOut& o) {
+  const int cbs = (E + RL_JOIN_COLS - 1) / RL_JOIN_COLS;
+  const int lo = rl_off(seq_off, s, T), hi = rl_off(seq_off, s + 1, T);
+  const int c0 = lo / chunk, c1 = hi > lo ? (hi - 1) / chunk + 1 : c0;  // chunks c0 .. c1 - 1
+  const int ci = threadIdx.x % RL_JOIN_COLS, run = threadIdx.x / RL_JOIN_COLS;
+  const int e = cb * RL_JOIN_COLS + ci;
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  double p = 0.0;
+  int cnt = 0;
+  if (e < E) {
+#pragma unroll 4
+    for (int c = c0 + run; c < c1; c += RL_RUNS) {
+      const int64_t i = (int64_t)(c + s) * E + e;
+      p += (double)w.prob[i];
+      cnt += w.cnt[i];
+    }
+  }
+  L.p[run][ci] = p;
+  L.c[run][ci] = cnt;
+  if (cb == 0) {
+    double z = 0.0;
+    long long n = 0;
+    for (int c = c0 + (int)threadIdx.x; c < c1; c += RL_THREADS) {
+      z += (double)w.z[c + s];
+      n += w.tok[c + s];
+    }
+#pragma unroll
+    for (int k = 32; k > 0; k >>= 1) {
+      z += __shfl_xor(z, k, 64);
+      n += __shfl_xor(n, k, 64);
+    }
+    if (lane == 0) {
+      L.z[wave] = z;
+      L.n[wave] = n;
+    }
+  }
+  __syncthreads();
+  if (threadIdx.x < RL_JOIN_COLS) {
+    double ps = 0.0;
+    int cs = 0;
+#pragma unroll 8
+    for (int r = 0; r < RL_RUNS; ++r) {
+      ps += L.p[r][ci];
+      cs += L.c[r][ci];
+    }
+    if (e < E) {
+      o.prob_sum[(int64_t)s * E + e] = (float)ps;
+      o.seq_counts[(int64_t)s * E + e] = cs;
+    }
+    double bsum = e < E ? ps * (double)cs : 0.0;
+#pragma unroll
+    for (int k = RL_JOIN_COLS / 2; k > 0; k >>= 1) bsum += __shfl_xor(bsum, k, 64);
+    if (threadIdx.x == 0) w.bal[(int64_t)s * cbs + cb] = bsum;
+  }
+  if (cb == 0 && threadIdx.x == 64) {
+    double z = 0.0;
+    long long n = 0;
+    for (int q = 0; q < RL_WAVES; ++q) {
+      z += L.z[q];
+      n += L.n[q];
+    }
+    w.zs[s] = z;
+    o.seq_tokens[s] = (int)n;
+  }
+  __syncthreads();
+}
+
+// The two losses from the sequences' sums (one workgroup).
+__device__ __forceinline__ void rl_losses(RlJoinLds& L, int E, int K, int n_seq, const RlossWs& w, const RlossOut& o) {
+  const int cbs = (E + RL_JOIN_COLS - 1) / RL_JOIN_COLS;
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  double bsum = 0.0, zsum = 0.0;
+  long long n = 0;
+  for (int q = threadIdx.x; q < n_seq; q += RL_THREADS) {
+    double bq = 0.0;
+    for (int k = 0; k < cbs; ++k) bq += w.bal[(int64_t)q * cbs + k];
+    const int tq = o.seq_tokens[q];
+    if (tq > 0) bsum += bq / (double)tq;
+    zsum += w.zs[q];
+    n += tq;
+  }
+#pragma unroll
+  for (int k = 32; k > 0; k >>= 1) {
+    bsum += __shfl_xor(bsum, k, 64);
+    zsum += __shfl_xor(zsum, k, 64);
+    n += __shfl_xor(n, k, 64);
+  }
+  if (lane == 0) {
+    L.b[wave] = bsum;
+    L.z[wave] = zsum;
+    L.n[wave] = n;
+  }
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    bsum = zsum = 0.0;
+    n = 0;
+    for (int q = 0; q < RL_WAVES; ++q) {
+      bsum += L.b[q];
+      zsum += L.z[q];
+      n += L.n[q];
+    }
+    rl_write_loss(o, E, K, bsum, zsum, n);
+  }
+}
+
+template <int G, int NV, bool V4, bool ONE>
 __global__ __launch_bounds__(RL_THREADS) void k_rloss_part(const float* __restrict__ logits,
                                                            const int32_t* __restrict__ topk_idx, int T, int E, int K,
                                                            int n_seq, const int32_t* __restrict__ seq_off,
                                                            const uint8_t* __restrict__ mask, float* __restrict__ lse,
-                                                           RlossWs w) {
+                                                           RlossWs w, RlossOut o) {
   using Row = RlRow<G, NV, V4>;
-  constexpr int N = Row::N, TPW = 64 / G;
+  constexpr int N = Row::N, TPW = 64 / G, STEPS = rl_steps(G), CHUNK = rl_chunk(G);
   extern __shared__ float rl_lds[];  // [waves][E] probability sums, [E] counts
   int* hist = reinterpret_cast<int*>(rl_lds + RL_WAVES * E);
   __shared__ float sz[RL_WAVES];
   __shared__ int sn[RL_WAVES];
+  __shared__ double sb[RL_WAVES];
+  __shared__ RlTable tab;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, li = lane % G, grp = lane / G;
-  const int t_begin = blockIdx.x * RL_CHUNK, t_end = min(T, t_begin + RL_CHUNK);
-  if (blockIdx.x == 0 && threadIdx.x == 0) *w.ticket = 0u;
+  const int t_begin = blockIdx.x * CHUNK, t_end = min(T, t_begin + CHUNK);
+  // everything the chunk needs is requested here
+  float x[STEPS][N];
+  bool live[STEPS];
+#pragma unroll
+  for (int i = 0; i < STEPS; ++i) {
+    const int t = min(t_begin + (i * RL_WAVES + wave) * TPW + grp, T - 1);
+    Row::load(logits + (int64_t)t * E, li, E, x[i]);
+    live[i] = !mask || mask[t];
+  }
+  const int picks = (t_end - t_begin) * K;  // the chunk's choices, one per thread and round
+  const int first = (int)threadIdx.x < picks ? topk_idx[(int64_t)t_begin * K + threadIdx.x] : -1;
+  rl_table_load(tab, seq_off, n_seq, T);
+  if (!ONE && blockIdx.x == 0 && threadIdx.x == 0) *w.ticket = 0u;
+  for (int e = threadIdx.x; e < E; e += RL_THREADS) hist[e] = 0;
+  if constexpr (ONE) {  // sequences without tokens have no piece
+    for (int i = threadIdx.x; i < n_seq * E; i += RL_THREADS) {
+      const int s = i / E;
+      if (rl_off(seq_off, s + 1, T) <= rl_off(seq_off, s, T)) {
+        o.prob_sum[i] = 0.0f;
+        o.seq_counts[i] = 0;
+        if (i == s * E) o.seq_tokens[s] = 0;
+      }
+    }
+  }
+  // softmax of every token of the chunk
+  float l2[STEPS];
+#pragma unroll
+  for (int i = 0; i < STEPS; ++i) {
+    float m = x[i][0];
+#pragma unroll
+    for (int k = 1; k < N; ++k) m = fmaxf(m, x[i][k]);
+    m = rl_group_max<G>(m);
+    // a row of -infinity only (every expert masked) has no probabilities: its sum is zero, its
+    // log-sum-exp -infinity, and it adds to neither loss; a NaN or +infinity makes the row NaN
+    m = m == -INFINITY ? 0.0f : m;
+    float sum = 0.0f;
+#pragma unroll
+    for (int k = 0; k < N; ++k) {
+      x[i][k] = rl_exp(x[i][k] - m);
+      sum += x[i][k];
+    }
+    sum = rl_group_sum<G>(sum);
+    const float l = m + __logf(sum);
+    const int t = t_begin + (i * RL_WAVES + wave) * TPW + grp;
+    if (li == 0 && t < t_end) lse[t] = l;
+    const float inv = sum != 0.0f ? 1.0f / sum : 0.0f;
+    l2[i] = sum != 0.0f ? l * l : 0.0f;
+#pragma unroll
+    for (int k = 0; k < N; ++k) x[i][k] *= inv;
+  }
+  __syncthreads();
+  auto off = [&](int s) { return n_seq <= RL_TABLE ? tab.off[s] : rl_off(seq_off, s, T); };
+  double bsum = 0.0, zsum = 0.0;  // ONE: thread 0's sums over the sequences
+  long long nsum = 0;
   for (int a = t_begin, b; a < t_end; a = b) {
-    const int s = rl_piece(seq_off, n_seq, T, a, t_end, b);
-    for (int e = threadIdx.x; e < E; e += RL_THREADS) hist[e] = 0;
+    const int s = rl_piece(off, n_seq, a, t_end, b);
+    if (s < 0) continue;  // (uniform) tokens outside every sequence only get their log-sum-exp
     float acc[N];
 #pragma unroll
-    for (int i = 0; i < N; ++i) acc[i] = 0.0f;
+    for (int k = 0; k < N; ++k) acc[k] = 0.0f;
     float z = 0.0f;
     int n = 0;
-    for (int t = a + wave * TPW + grp; t < b; t += RL_WAVES * TPW) {  // uniform within a group of G lanes
-      float x[N];
-      Row::load(logits + (int64_t)t * E, li, E, x);
-      float m = x[0];
 #pragma unroll
-      for (int i = 1; i < N; ++i) m = fmaxf(m, x[i]);
-      m = rl_group_max<G>(m);
-      // a row of -infinity only (every expert masked) has no probabilities: its sum is zero, its
-      // log-sum-exp -infinity, and it adds to neither loss; a NaN or +infinity makes the row NaN
-      m = m == -INFINITY ? 0.0f : m;
-      float sum = 0.0f;
-#pragma unroll
-      for (int i = 0; i < N; ++i) {
-        x[i] = rl_exp(x[i] - m);
-        sum += x[i];
-      }
-      sum = rl_group_sum<G>(sum);
-      const float l = m + __logf(sum);
-      if (li == 0) lse[t] = l;
-      if (s >= 0 && (!mask || mask[t])) {
+    for (int i = 0; i < STEPS; ++i) {
+      const int t = t_begin + (i * RL_WAVES + wave) * TPW + grp;
+      if (t >= a && t < b && live[i]) {
         ++n;
-        if (sum != 0.0f) {
-          const float inv = 1.0f / sum;
+        z += l2[i];
 #pragma unroll
-          for (int i = 0; i < N; ++i) acc[i] += x[i] * inv;
-          z += l * l;
-        }
+        for (int k = 0; k < N; ++k) acc[k] += x[i][k];
       }
     }
-    if (s < 0) continue;  // (uniform) tokens outside every sequence only get their log-sum-exp
-    __syncthreads();      // the histogram is clear
-    for (int i = threadIdx.x; i < (b - a) * K; i += RL_THREADS) {
-      const int t = a + i / K;
-      const int e = topk_idx[(int64_t)a * K + i];
-      if ((uint32_t)e < (uint32_t)E && (!mask || mask[t])) atomicAdd(&hist[e], 1);
+    for (int i = threadIdx.x, e = first; i < picks;) {
+      const int t = t_begin + i / K;
+      if (t >= a && t < b && (uint32_t)e < (uint32_t)E && (!mask || mask[t])) atomicAdd(&hist[e], 1);
+      i += RL_THREADS;
+      if (i < picks) e = topk_idx[(int64_t)t_begin * K + i];
     }
 #pragma unroll
-    for (int i = 0; i < N; ++i) {
+    for (int k = 0; k < N; ++k) {
 #pragma unroll
-      for (int o = G; o < 64; o <<= 1) acc[i] += __shfl_xor(acc[i], o, 64);
-      if (grp == 0 && Row::col(li, i) < E) rl_lds[wave * E + Row::col(li, i)] = acc[i];
+      for (int h = G; h < 64; h <<= 1) acc[k] += __shfl_xor(acc[k], h, 64);
+      if (grp == 0 && Row::col(li, k) < E) rl_lds[wave * E + Row::col(li, k)] = acc[k];
     }
     // every lane of a group holds its tokens' count and z: take one lane per group
     z = wave_sum(li == 0 ? z : 0.0f);
@@ -216,142 +417,77 @@ __global__ __launch_bounds__(RL_THREADS) void k_rloss_part(const float* __restri
     }
     __syncthreads();
     const int64_t slot = (int64_t)blockIdx.x + s;
+    double bal = 0.0;
     for (int e = threadIdx.x; e < E; e += RL_THREADS) {
-      w.prob[slot * E + e] = (rl_lds[e] + rl_lds[E + e]) + (rl_lds[2 * E + e] + rl_lds[3 * E + e]);
-      w.cnt[slot * E + e] = hist[e];
+      float v = 0.0f;
+#pragma unroll
+      for (int q = 0; q < RL_WAVES; ++q) v += rl_lds[q * E + e];
+      const int c = hist[e];
+      hist[e] = 0;
+      if constexpr (ONE) {
+        o.prob_sum[(int64_t)s * E + e] = v;
+        o.seq_counts[(int64_t)s * E + e] = c;
+        bal += (double)v * (double)c;
+      } else {
+        w.prob[slot * E + e] = v;
+        w.cnt[slot * E + e] = c;
+      }
+    }
+    if constexpr (ONE) {
+#pragma unroll
+      for (int h = 32; h > 0; h >>= 1) bal += __shfl_xor(bal, h, 64);
+      if (lane == 0) sb[wave] = bal;
+      __syncthreads();
     }
     if (threadIdx.x == 0) {
-      w.z[slot] = (sz[0] + sz[1]) + (sz[2] + sz[3]);
-      w.tok[slot] = sn[0] + sn[1] + sn[2] + sn[3];
+      float zs = 0.0f;
+      int ns = 0;
+#pragma unroll
+      for (int q = 0; q < RL_WAVES; ++q) {
+        zs += sz[q];
+        ns += sn[q];
+      }
+      if constexpr (ONE) {
+        double bs = 0.0;
+#pragma unroll
+        for (int q = 0; q < RL_WAVES; ++q) bs += sb[q];
+        o.seq_tokens[s] = ns;
+        if (ns > 0) bsum += bs / (double)ns;
+        zsum += (double)zs;
+        nsum += ns;
+      } else {
+        w.z[slot] = zs;
+        w.tok[slot] = ns;
+      }
     }
     __syncthreads();  // the LDS is free for the next piece
   }
+  if (ONE && threadIdx.x == 0) rl_write_loss(o, E, K, bsum, zsum, nsum);
 }
 
-// Adds a sequence's slots in chunk order: 32 columns by 32 runs of chunks per workgroup, then the
-// runs in order.  The last workgroup to finish forms the losses.
-__global__ __launch_bounds__(RL_JOIN_THREADS) void k_rloss_join(int T, int E, int K, int n_seq,
-                                                                const int32_t* __restrict__ seq_off, RlossWs w,
-                                                                int32_t* __restrict__ seq_tokens,
-                                                                int32_t* __restrict__ seq_counts,
-                                                                float* __restrict__ prob_sum, float* __restrict__ loss) {
-  constexpr int RUNS = RL_JOIN_THREADS / RL_JOIN_COLS;
-  __shared__ double sp[RUNS][RL_JOIN_COLS + 1];
-  __shared__ int sc[RUNS][RL_JOIN_COLS + 1];
-  __shared__ double rz[16], rb[16];
-  __shared__ long long rn[16];
-  __shared__ int last;
+// The joining launch, one workgroup per sequence and block of 32 columns; the last one to finish
+// forms the losses.
+__global__ __launch_bounds__(RL_THREADS) void k_rloss_join(int T, int E, int K, int n_seq, int chunk,
+                                                           const int32_t* __restrict__ seq_off, RlossWs w, RlossOut o) {
+  __shared__ RlJoinLds L;
   const int cbs = (E + RL_JOIN_COLS - 1) / RL_JOIN_COLS;
-  const int s = blockIdx.x / cbs, cb = blockIdx.x % cbs;
-  const int lo = rl_off(seq_off, s, T), hi = rl_off(seq_off, s + 1, T);
-  const int c0 = lo / RL_CHUNK, c1 = hi > lo ? (hi - 1) / RL_CHUNK + 1 : c0;  // chunks c0 .. c1 - 1
-  const int ci = threadIdx.x % RL_JOIN_COLS, run = threadIdx.x / RL_JOIN_COLS;
-  const int e = cb * RL_JOIN_COLS + ci;
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  double p = 0.0;
-  int cnt = 0;
-  if (e < E)
-    for (int c = c0 + run; c < c1; c += RUNS) {
-      const int64_t i = (int64_t)(c + s) * E + e;
-      p += (double)w.prob[i];
-      cnt += w.cnt[i];
-    }
-  sp[run][ci] = p;
-  sc[run][ci] = cnt;
-  if (cb == 0) {  // the sequence's tokens and z sum
-    double z = 0.0;
-    long long n = 0;
-    for (int c = c0 + (int)threadIdx.x; c < c1; c += RL_JOIN_THREADS) {
-      z += (double)w.z[c + s];
-      n += w.tok[c + s];
-    }
-#pragma unroll
-    for (int o = 32; o > 0; o >>= 1) {
-      z += __shfl_xor(z, o, 64);
-      n += __shfl_xor(n, o, 64);
-    }
-    if (lane == 0) {
-      rz[wave] = z;
-      rn[wave] = n;
-    }
-  }
-  __syncthreads();
-  if (threadIdx.x < RL_JOIN_COLS) {
-    double ps = 0.0;
-    int cs = 0;
-    for (int r = 0; r < RUNS; ++r) {
-      ps += sp[r][ci];
-      cs += sc[r][ci];
-    }
-    if (e < E) {
-      prob_sum[(int64_t)s * E + e] = (float)ps;
-      seq_counts[(int64_t)s * E + e] = cs;
-    }
-    double bsum = e < E ? ps * (double)cs : 0.0;
-#pragma unroll
-    for (int o = RL_JOIN_COLS / 2; o > 0; o >>= 1) bsum += __shfl_xor(bsum, o, 64);
-    if (threadIdx.x == 0) w.bal[(int64_t)s * cbs + cb] = bsum;
-  }
-  if (cb == 0 && threadIdx.x == 0) {
-    double z = 0.0;
-    long long n = 0;
-    for (int q = 0; q < 16; ++q) {
-      z += rz[q];
-      n += rn[q];
-    }
-    w.zs[s] = z;
-    seq_tokens[s] = (int)n;
-  }
-  // the last workgroup sums over the sequences
-  __syncthreads();
+  rl_join(L, blockIdx.x / cbs, blockIdx.x % cbs, chunk, T, E, seq_off, w, o);
   if (threadIdx.x == 0) {
     __builtin_amdgcn_fence(__ATOMIC_RELEASE, "agent");
     const unsigned v = __hip_atomic_fetch_add(w.ticket, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-    last = v == gridDim.x - 1;
+    L.last = v == gridDim.x - 1;
   }
   __syncthreads();
-  if (!last) return;
+  if (!L.last) return;
   __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "agent");
-  double bsum = 0.0, zsum = 0.0;
-  long long n = 0;
-  for (int q = threadIdx.x; q < n_seq; q += RL_JOIN_THREADS) {
-    double bq = 0.0;
-    for (int k = 0; k < cbs; ++k) bq += w.bal[(int64_t)q * cbs + k];
-    const int tq = seq_tokens[q];
-    if (tq > 0) bsum += bq / (double)tq;
-    zsum += w.zs[q];
-    n += tq;
-  }
-#pragma unroll
-  for (int o = 32; o > 0; o >>= 1) {
-    bsum += __shfl_xor(bsum, o, 64);
-    zsum += __shfl_xor(zsum, o, 64);
-    n += __shfl_xor(n, o, 64);
-  }
-  if (lane == 0) {
-    rb[wave] = bsum;
-    rz[wave] = zsum;
-    rn[wave] = n;
-  }
-  __syncthreads();
-  if (threadIdx.x == 0) {
-    bsum = zsum = 0.0;
-    n = 0;
-    for (int q = 0; q < 16; ++q) {
-      bsum += rb[q];
-      zsum += rz[q];
-      n += rn[q];
-    }
-    loss[0] = n ? (float)(bsum * (double)E / ((double)K * (double)n)) : 0.0f;
-    loss[1] = n ? (float)(zsum / (double)n) : 0.0f;
-  }
+  rl_losses(L, E, K, n_seq, w, o);
 }
 
 // dLogits, piece by piece as the forward.  The counts enter less their mean K T_s / E: the
 // probabilities of a row sum to one, so the mean drops out of the difference, and without it the
 // difference of two nearly equal numbers would lose the leading bits.
 template <int G, int NV, bool V4>
-__global__ __launch_bounds__(RL_THREADS) void k_rloss_bwd(const float* __restrict__ dloss,
+__global__ __launch_bounds__(RL_BWD_THREADS) void k_rloss_bwd(const float* __restrict__ dloss,
                                                           const float* __restrict__ logits, int T, int E, int K,
                                                           int n_seq, const int32_t* __restrict__ seq_off,
                                                           const uint8_t* __restrict__ mask,
@@ -359,12 +495,15 @@ __global__ __launch_bounds__(RL_THREADS) void k_rloss_bwd(const float* __restric
                                                           const int32_t* __restrict__ seq_counts,
                                                           const float* __restrict__ lse, float* __restrict__ dLogits) {
   using Row = RlRow<G, NV, V4>;
-  constexpr int N = Row::N, TPW = 64 / G;
-  __shared__ long long rn[RL_WAVES];
+  constexpr int N = Row::N, TPW = 64 / G, WAVES = RL_BWD_THREADS / 64;
+  __shared__ long long rn[WAVES];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, li = lane % G, grp = lane / G;
-  const int t_begin = blockIdx.x * RL_CHUNK, t_end = min(T, t_begin + RL_CHUNK);
+  const int t_begin = blockIdx.x * RL_BWD_CHUNK, t_end = min(T, t_begin + RL_BWD_CHUNK);
+  __shared__ RlTable tab;
+  rl_table_load(tab, seq_off, n_seq, T);
+  auto off = [&](int s) { return n_seq <= RL_TABLE ? tab.off[s] : rl_off(seq_off, s, T); };
   long long n = 0;
-  for (int q = threadIdx.x; q < n_seq; q += RL_THREADS) n += seq_tokens[q];
+  for (int q = threadIdx.x; q < n_seq; q += RL_BWD_THREADS) n += seq_tokens[q];
 #pragma unroll
   for (int o = 32; o > 0; o >>= 1) n += __shfl_xor(n, o, 64);
   if (lane == 0) rn[wave] = n;
@@ -373,7 +512,7 @@ __global__ __launch_bounds__(RL_THREADS) void k_rloss_bwd(const float* __restric
   const float inv_n = n > 0 ? 1.0f / (float)n : 0.0f;
   const float gb = dloss[0] * inv_n * (float)E / (float)K, gz = dloss[1] * 2.0f * inv_n;
   for (int a = t_begin, b; a < t_end; a = b) {
-    const int s = rl_piece(seq_off, n_seq, T, a, t_end, b);
+    const int s = rl_piece(off, n_seq, a, t_end, b);
     float ex[N];
     float coef = 0.0f;
     if (s >= 0) {
@@ -389,7 +528,7 @@ __global__ __launch_bounds__(RL_THREADS) void k_rloss_bwd(const float* __restric
 #pragma unroll
       for (int i = 0; i < N; ++i) ex[i] = 0.0f;
     }
-    for (int t = a + wave * TPW + grp; t < b; t += RL_WAVES * TPW) {
+    for (int t = a + wave * TPW + grp; t < b; t += WAVES * TPW) {
       const float l = lse[t];
       float x[N];
       if (s >= 0 && (!mask || mask[t]) && l != -INFINITY) {
@@ -413,22 +552,22 @@ __global__ __launch_bounds__(RL_THREADS) void k_rloss_bwd(const float* __restric
   }
 }
 
-// Lanes per token and 4-logit chunks per lane for E: one chunk where that leaves few idle lanes,
-// else up to four.  V4 needs 16-byte aligned rows.
+// Calls f<G, NV, V4> for E's layout; V4 needs 16-byte aligned rows.
 template <class F>
 static void rl_dispatch(int E, F f) {
-#define RL_CASE(GG, NN) (E % 4 == 0 ? f.template operator()<GG, NN, true>() : f.template operator()<GG, NN, false>())
-  const int q = (E + 3) / 4;  // chunks per row
-  if (q <= 2) RL_CASE(2, 1);
-  else if (q <= 4) RL_CASE(4, 1);
-  else if (q <= 8) RL_CASE(8, 1);
-  else if (q <= 16) RL_CASE(16, 1);
-  else if (q <= 32) RL_CASE(16, 2);
-  else if (q <= 48) RL_CASE(16, 3);
-  else if (q <= 64) RL_CASE(32, 2);
-  else if (q <= 96) RL_CASE(32, 3);
-  else if (q <= 128) RL_CASE(64, 2);
-  else RL_CASE(64, 4);
+  const RlLayout l = rl_layout(E);
+#define RL_CASE(GG, NN) \
+  if (l.G == GG && l.NV == NN) return E % 4 == 0 ? f.template operator()<GG, NN, true>() : f.template operator()<GG, NN, false>()
+  RL_CASE(2, 1);
+  RL_CASE(4, 1);
+  RL_CASE(8, 1);
+  RL_CASE(16, 1);
+  RL_CASE(16, 2);
+  RL_CASE(16, 3);
+  RL_CASE(32, 2);
+  RL_CASE(32, 3);
+  RL_CASE(64, 2);
+  RL_CASE(64, 4);
 #undef RL_CASE
 }
 
@@ -441,11 +580,16 @@ struct RlossFwd {
   const uint8_t* mask;
   float* lse;
   RlossWs w;
+  RlossOut o;
   hipStream_t st;
   template <int G, int NV, bool V4>
   void operator()() const {
-    k_rloss_part<G, NV, V4><<<(int)rl_chunks(T), RL_THREADS, (size_t)(RL_WAVES + 1) * E * 4, st>>>(
-        logits, topk_idx, T, E, K, n_seq, seq_off, mask, lse, w);
+    const size_t lds = (size_t)(RL_WAVES + 1) * E * 4;
+    if (rl_chunks(T, E) == 1)
+      k_rloss_part<G, NV, V4, true><<<1, RL_THREADS, lds, st>>>(logits, topk_idx, T, E, K, n_seq, seq_off, mask, lse, w, o);
+    else
+      k_rloss_part<G, NV, V4, false><<<(int)rl_chunks(T, E), RL_THREADS, lds, st>>>(logits, topk_idx, T, E, K, n_seq, seq_off,
+                                                                                 mask, lse, w, o);
   }
 };
 struct RlossBwd {
@@ -459,7 +603,7 @@ struct RlossBwd {
   hipStream_t st;
   template <int G, int NV, bool V4>
   void operator()() const {
-    k_rloss_bwd<G, NV, V4><<<(int)rl_chunks(T), RL_THREADS, 0, st>>>(dloss, logits, T, E, K, n_seq, seq_off, mask,
+    k_rloss_bwd<G, NV, V4><<<(int)cdiv(T, RL_BWD_CHUNK), RL_BWD_THREADS, 0, st>>>(dloss, logits, T, E, K, n_seq, seq_off, mask,
                                                                       seq_tokens, seq_counts, lse, dLogits);
   }
 };
@@ -470,11 +614,11 @@ hipError_t launch_router_loss(const float* logits, const int32_t* topk_idx, int6
                               float* prob_sum, float* lse, float* loss, void* ws, hipStream_t st) {
   RlossWs w;
   rl_carve(ws, T, E, n_seq, &w);
-  rl_dispatch(E, RlossFwd{logits, topk_idx, (int)T, E, K, n_seq, seq_off, mask, lse, w, st});
+  const RlossOut o{seq_tokens, seq_counts, prob_sum, loss};
+  rl_dispatch(E, RlossFwd{logits, topk_idx, (int)T, E, K, n_seq, seq_off, mask, lse, w, o, st});
   const hipError_t e = hipGetLastError();
-  if (e != hipSuccess) return e;
-  k_rloss_join<<<n_seq * rl_colblocks(E), RL_JOIN_THREADS, 0, st>>>((int)T, E, K, n_seq, seq_off, w, seq_tokens,
-                                                                    seq_counts, prob_sum, loss);
+  if (e != hipSuccess || rl_chunks(T, E) == 1) return e;
+  k_rloss_join<<<n_seq * rl_colblocks(E), RL_THREADS, 0, st>>>((int)T, E, K, n_seq, rl_chunk(rl_layout(E).G), seq_off, w, o);
   return hipGetLastError();
 }
 
