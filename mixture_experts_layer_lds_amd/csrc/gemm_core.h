@@ -624,25 +624,6 @@ struct RowLoaderF32 {                       // K-major rows: thread owns rows ti
   }
 };
 
-// The same with rows that end inside a stage (K any multiple of 4).
-struct RowLoaderF32Tail : RowLoaderF32 {
-  int klim;
-  template <class RowPtr>
-  __device__ void init(RowPtr row_ptr, int klen) {
-    RowLoaderF32::init(row_ptr);
-    klim = klen;
-  }
-  __device__ void load(int kt) {
-    const int chunk = threadIdx.x & 7;
-    const bool in = kt * 32 + chunk * 4 < klim;
-#pragma unroll
-    for (int q = 0; q < 8; ++q) {
-      if (rp[q] && in) v[q] = ld16(rp[q] + (int64_t)kt * 128 + chunk * 16);
-      else v[q] = u32x4{0u, 0u, 0u, 0u};
-    }
-  }
-};
-
 // MN-major fp32 operand, transposed in registers into the K-major layout: thread owns two 4 (k)
 // x 4 (mn) blocks, mn = 4 (tid % 64), k = 4 (tid / 64) and 4 (tid / 64 + 4).  kbase / klim as
 // for MNDma.

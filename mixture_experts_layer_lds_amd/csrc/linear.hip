@@ -5,9 +5,9 @@
 //   backward   dZ = dY act'(z),  dX = dZ W,  dW = dZ^T X,  db = sum of dZ over rows
 // N' = N, except SwiGLU: N' = 2 N, W = [W_gate; W_up], act(z) = silu(z_gate) z_up.
 //
-// All three products run on MFMA main loops (bf16: gemm_dense.h; fp32: the register-staged ring of
-// gemm_core.h): X and W are K-major in the forward; dX reads W with its rows along the reduction,
-// dW reads both operands so.  Reductions may end inside a stage (any multiple of 8).  Where the output has too few tiles for 256 CUs the
+// All three products run on the MFMA main loop of gemm_dense.h: X and W are K-major in the forward;
+// dX reads W with its rows along the reduction, dW reads both operands so.  Reductions may end
+// inside a stage (any multiple of 8).  Where the output has too few tiles for 256 CUs the
 // reduction is cut into slices whose fp32 partial products a second kernel adds in slice order
 // before the epilogue (k_lin_finish).
 //
@@ -25,31 +25,57 @@ static inline int grid8(int64_t n) { return (int)((n + 7) / 8 * 8); }
 
 enum { LIN_NONE = 0, LIN_RELU = 1, LIN_GELU = 2, LIN_SILU = 3, LIN_SWIGLU = 4 };
 
-// act(z) of N elements in place (not SwiGLU).  GELU is the exact form z Phi(z).
+// The normal distribution's upper tail at |z| and, through *e, exp(-z^2 / 2):
+// erfc(x) = (a1 t + .. + a5 t^5) exp(-x^2), t = 1 / (1 + p x) (Abramowitz and Stegun 7.1.26, off by
+// at most 1.5e-7), a third of the instructions of the library's erf, which cost the GELU epilogue
+// 0.10 of 0.90 ms on the 8192 x 14336 x 4096 product.
+__device__ __forceinline__ float normal_tail(float z, float* e) {
+  const float x = fabsf(z) * 0.70710678118654752f;
+  const float t = __builtin_amdgcn_rcpf(1.0f + 0.3275911f * x);
+  *e = __expf(-0.5f * z * z);
+  return 0.5f * t * (0.254829592f + t * (-0.284496736f + t * (1.421413741f + t * (-1.453152027f + t * 1.061405429f)))) * *e;
+}
+
+// act(z) of one element and its derivative (not SwiGLU).  GELU is the exact form z Phi(z).
+template <int ACT>
+__device__ __forceinline__ float lin_act1(float z) {
+  if constexpr (ACT == LIN_RELU) return z < 0.0f ? 0.0f : z;  // a NaN stays
+  if constexpr (ACT == LIN_GELU) {
+    float e;
+    const float q = normal_tail(z, &e);
+    return z < 0.0f ? z * q : z - z * q;
+  }
+  if constexpr (ACT == LIN_SILU) return z * sigmoid_f32(z);
+  return z;
+}
+template <int ACT>
+__device__ __forceinline__ float lin_grad1(float z) {
+  if constexpr (ACT == LIN_RELU) return z > 0.0f ? 1.0f : 0.0f;
+  if constexpr (ACT == LIN_GELU) {
+    float e;
+    const float q = normal_tail(z, &e);
+    return (z < 0.0f ? q : 1.0f - q) + z * e * 0.39894228040143268f;
+  }
+  if constexpr (ACT == LIN_SILU) {
+    const float s = sigmoid_f32(z);
+    return s * (1.0f + z * (1.0f - s));
+  }
+  return 1.0f;
+}
+// f(integral_constant<int, act>) for the activation act (SwiGLU as NONE: it is not elementwise).
+template <class F>
+__device__ __forceinline__ void lin_by_act(int act, F f) {
+  if (act == LIN_RELU) f(std::integral_constant<int, LIN_RELU>{});
+  else if (act == LIN_GELU) f(std::integral_constant<int, LIN_GELU>{});
+  else if (act == LIN_SILU) f(std::integral_constant<int, LIN_SILU>{});
+  else f(std::integral_constant<int, LIN_NONE>{});
+}
 template <int N>
 __device__ __forceinline__ void lin_act(float* z, int act) {
-  if (act == LIN_RELU) {
+  lin_by_act(act, [&](auto A) {
 #pragma unroll
-    for (int u = 0; u < N; ++u) z[u] = z[u] < 0.0f ? 0.0f : z[u];  // a NaN stays
-  } else if (act == LIN_GELU) {
-#pragma unroll
-    for (int u = 0; u < N; ++u) z[u] = 0.5f * z[u] * (1.0f + erff(z[u] * 0.70710678118654752f));
-  } else if (act == LIN_SILU) {
-#pragma unroll
-    for (int u = 0; u < N; ++u) z[u] *= sigmoid_f32(z[u]);
-  }
-}
-__device__ __forceinline__ float lin_act_grad(float z, int act) {
-  switch (act) {
-    case LIN_RELU: return z > 0.0f ? 1.0f : 0.0f;
-    case LIN_GELU:
-      return 0.5f * (1.0f + erff(z * 0.70710678118654752f)) + z * __expf(-0.5f * z * z) * 0.39894228040143268f;
-    case LIN_SILU: {
-      const float s = sigmoid_f32(z);
-      return s * (1.0f + z * (1.0f - s));
-    }
-    default: return 1.0f;
-  }
+    for (int u = 0; u < N; ++u) z[u] = lin_act1<decltype(A)::value>(z[u]);
+  });
 }
 
 // What the epilogue does with z [m][n]; pointers may be null, res may be out.
@@ -87,35 +113,55 @@ template <class TI>
 __device__ __forceinline__ char* lin_frow(char* b0, char* b1, int r) {
   return r < TI::SPLIT ? b0 + r * TI::EPITCH : b1 + (r - TI::SPLIT) * TI::EPITCH;
 }
+// val(i, h): the four accumulators of row block i and column block h of the half.
 template <class TI, class Val>
 __device__ __forceinline__ void lin_dump(char* b0, char* b1, int wm, int wn, Val val) {
 #pragma unroll
-  for (int i = 0; i < TI::MI; ++i)
+  for (int i = 0; i < TI::MI; ++i) {
+    char* row = lin_frow<TI>(b0, b1, (wm * TI::MI + i) * 16 + (threadIdx.x & 15));
 #pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      const f32x4 v4 = {val(i, 4 * q), val(i, 4 * q + 1), val(i, 4 * q + 2), val(i, 4 * q + 3)};
-      const int r = (wm * TI::MI + i) * 32 + (threadIdx.x & 31);
-      *reinterpret_cast<f32x4*>(lin_frow<TI>(b0, b1, r) + (wn * 32 + acc_n(4 * q)) * 4) = v4;
-    }
+    for (int h = 0; h < 2; ++h) *reinterpret_cast<f32x4*>(row + dn_col(wn, h) * 4) = val(i, h);
+  }
 }
-template <class TI, class Row>
-__device__ __forceinline__ void lin_walk(char* b0, char* b1, int mrows, int valid, Row row) {
-  const int c = (threadIdx.x % (TI::HC / 8)) * 8;
+// Eight values to and from 16-byte chunks (one of bf16, two of fp32).
+template <typename T> __device__ __forceinline__ void lin_st8(T* p, const float* f) {
 #pragma unroll
-  for (int k = 0; k < TI::TM_ / 32; ++k) {
-    const int r = (int)(threadIdx.x / (TI::HC / 8)) + 32 * k;
-    if (r >= mrows || c >= valid) continue;
-    const char* p = lin_frow<TI>(b0, b1, r) + c * 4;
-    const f32x4 a = *reinterpret_cast<const f32x4*>(p), b = *reinterpret_cast<const f32x4*>(p + 16);
-    float f[8] = {a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]};
-    row(k, r, c, f);
+  for (int u = 0; u < 8; u += Vec<T>::N) st16_nt(p + u, pack16<T>(f + u));
+}
+
+// Walks the staged half: row(r, c, f, res) with 8 fp32 values f of tile row r, columns c .., and 8
+// of the residual (zeros without one).  Rows go in batches of four whose residual chunks are
+// requested together; res_row(r) is row r's residual at the half's first column.
+template <class TI, typename T, class ResRow, class Row>
+__device__ __forceinline__ void lin_walk(char* b0, char* b1, int mrows, int valid, bool has_res, ResRow res_row, Row row) {
+  constexpr int NV = 8 / Vec<T>::N;
+  const int c = (threadIdx.x % (TI::HC / 8)) * 8, r0 = threadIdx.x / (TI::HC / 8);
+  if (c >= valid) return;
+#pragma unroll
+  for (int k0 = 0; k0 < TI::TM_ / 32; k0 += 4) {
+    u32x4 rv[4][NV];
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+#pragma unroll
+      for (int v = 0; v < NV; ++v)
+        rv[k][v] = has_res ? ld16_nt(res_row(min(r0 + 32 * (k0 + k), mrows - 1)) + c + v * Vec<T>::N) : u32x4{0u, 0u, 0u, 0u};
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int r = r0 + 32 * (k0 + k);
+      const char* p = lin_frow<TI>(b0, b1, r) + c * 4;
+      const f32x4 a = *reinterpret_cast<const f32x4*>(p), b = *reinterpret_cast<const f32x4*>(p + 16);
+      float f[8] = {a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]}, rr[8];
+#pragma unroll
+      for (int v = 0; v < NV; ++v) unpack16<T>(rv[k][v], rr + v * Vec<T>::N);
+      if (r < mrows) row(r, c, f, rr);
+    }
   }
 }
 
-// bf16 on the dense main loop (gemm_dense.h).  SwiGLU (LIN_OUT_GLU): a tile has TN / 2 output
+// One product on the dense main loop (gemm_dense.h).  SwiGLU (LIN_OUT_GLU): a tile has TN / 2 output
 // columns, the B tile stacks their gate rows over their up rows, so a lane holds both of a column.
-template <class TI, int MODE, bool TAIL, int OUT>
-__global__ __launch_bounds__(TI::THREADS, TI::NW == 8 ? 1 : 2) void k_lin_bf16(LinGemm g, LinEpi<bf16> ep) {
+template <typename T, class TI, int MODE, bool TAIL, int OUT>
+__global__ __launch_bounds__(TI::THREADS, TI::NW == 8 ? 1 : 2) void k_lin(LinGemm g, LinEpi<T> ep) {
   __shared__ __attribute__((aligned(1024))) char b0[TI::SLOT];
   __shared__ __attribute__((aligned(1024))) char b1[TI::SLOT];
   const int lin = xcd_remap(blockIdx.x, gridDim.x);
@@ -130,29 +176,29 @@ __global__ __launch_bounds__(TI::THREADS, TI::NW == 8 ? 1 : 2) void k_lin_bf16(L
   const int wm = wave / TI::WN_, wn = wave % TI::WN_;
   const int k0 = sl * g.klen, klen = min(g.klen, g.red - k0), blen = max(min(g.klen, g.bred - k0), 1);
   const int mrows = min(TI::TM_, g.m - m0);
-  const int64_t ldab = g.lda * (int64_t)sizeof(bf16), ldbb = g.ldb * (int64_t)sizeof(bf16);
+  const int64_t ldab = g.lda * (int64_t)sizeof(T), ldbb = g.ldb * (int64_t)sizeof(T);
   const char* Ab = static_cast<const char*>(g.A);
   const char* Bb = static_cast<const char*>(g.B);
   DnAcc<TI::MI> acc;
-  const int nkt = (int)cdiv(klen, DN_BK);
+  const int nkt = (int)cdiv(klen, dn_bk<T>());
   if constexpr (MODE == LIN_DW) {
-    DnMN<TI::TM_, TI::NW, TAIL> la;
-    DnMN<2 * HC, TI::NW, TAIL> lb;
-    la.init(Ab + k0 * ldab + (int64_t)m0 * 2, ldab, klen, mrows);
-    lb.init(Bb + k0 * ldbb + (int64_t)n0 * 2, ldbb, blen, min(2 * HC, g.n - n0));
+    DnMN<T, TI::TM_, TI::NW, TAIL> la;
+    DnMN<T, 2 * HC, TI::NW, TAIL> lb;
+    la.init(Ab + k0 * ldab + (int64_t)m0 * sizeof(T), ldab, klen, mrows);
+    lb.init(Bb + k0 * ldbb + (int64_t)n0 * sizeof(T), ldbb, blen, min(2 * HC, g.n - n0));
     dn_mainloop<TI>(la, lb, nkt, acc, b0, b1, wm, wn);
   } else {
-    DnK<TI::TM_, TI::NW, TAIL> la;
-    la.init(Ab + m0 * ldab + (int64_t)k0 * 2, ldab, klen, [&](int i) { return (int64_t)min(i, mrows - 1); });
+    DnK<T, TI::TM_, TI::NW, TAIL> la;
+    la.init(Ab + m0 * ldab + (int64_t)k0 * sizeof(T), ldab, klen, [&](int i) { return (int64_t)min(i, mrows - 1); });
     if constexpr (MODE == LIN_DX) {
-      DnMN<2 * HC, TI::NW, TAIL> lb;
-      lb.init(Bb + k0 * ldbb + (int64_t)n0 * 2, ldbb, blen, min(2 * HC, g.n - n0));
+      DnMN<T, 2 * HC, TI::NW, TAIL> lb;
+      lb.init(Bb + k0 * ldbb + (int64_t)n0 * sizeof(T), ldbb, blen, min(2 * HC, g.n - n0));
       dn_mainloop<TI>(la, lb, nkt, acc, b0, b1, wm, wn);
     } else {
-      DnK<2 * HC, TI::NW, TAIL> lb;
+      DnK<T, 2 * HC, TI::NW, TAIL> lb;
       const int ncols = min(TN, g.n - n0);
       // SwiGLU: the tile's upper half holds the up rows, N rows behind the gate rows
-      lb.init(Bb + n0 * ldbb + (int64_t)k0 * 2, ldbb, klen,
+      lb.init(Bb + n0 * ldbb + (int64_t)k0 * sizeof(T), ldbb, klen,
               [&](int i) { return (int64_t)min(OUT == LIN_OUT_GLU ? i % HC : i, ncols - 1); },
               OUT == LIN_OUT_GLU ? g.n * ldbb : 0);
       dn_mainloop<TI>(la, lb, nkt, acc, b0, b1, wm, wn);
@@ -162,170 +208,89 @@ __global__ __launch_bounds__(TI::THREADS, TI::NW == 8 ? 1 : 2) void k_lin_bf16(L
   if constexpr (OUT == LIN_OUT_PART) {
     float* dst = g.part + (int64_t)sl * g.m * g.n;
 #pragma unroll
-    for (int j = 0; j < 2; ++j)
+    for (int j = 0; j < 4; ++j) {
+      const int c = n0 + (j >> 1) * HC + dn_col(wn, j & 1);  // n is a multiple of 4
+      if (c >= g.n) continue;
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        const int c = n0 + j * HC + wn * 32 + acc_n(4 * q);  // n is a multiple of 4
-        if (c >= g.n) continue;
-#pragma unroll
-        for (int i = 0; i < MI; ++i) {
-          const int r = (wm * MI + i) * 32 + (threadIdx.x & 31);
-          if (r >= mrows) continue;
-          *reinterpret_cast<f32x4*>(dst + (int64_t)(m0 + r) * g.n + c) =
-              f32x4{acc.c[i][j][4 * q], acc.c[i][j][4 * q + 1], acc.c[i][j][4 * q + 2], acc.c[i][j][4 * q + 3]};
-        }
+      for (int i = 0; i < MI; ++i) {
+        const int r = (wm * MI + i) * 16 + (threadIdx.x & 15);
+        if (r < mrows) *reinterpret_cast<f32x4*>(dst + (int64_t)(m0 + r) * g.n + c) = acc.c[i][j];
       }
+    }
   } else if constexpr (OUT == LIN_OUT_EPI) {
-    constexpr int NR = TI::TM_ / 32;
     const int cw = (threadIdx.x % (HC / 8)) * 8;
 #pragma unroll
     for (int half = 0; half < 2; ++half) {
       const int c0 = n0 + half * HC, valid = min(HC, g.n - c0);
       if (valid <= 0) break;  // (uniform)
-      u32x4 rv[NR];
-      float b[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-      if (cw < valid) {
-        if (ep.bias) {
+      lin_dump<TI>(b0, b1, wm, wn, [&](int i, int h) { return acc.c[i][2 * half + h]; });
+      __syncthreads();
+      const T* res = ep.res ? ep.res + m0 * ep.ldr + c0 : nullptr;
+      T* out = ep.out + m0 * ep.ldo + c0;
+      auto res_row = [&](int r) { return res + r * ep.ldr; };
+      if constexpr (MODE == LIN_FWD) {
+        float b[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+        if (ep.bias && cw < valid) {
 #pragma unroll
           for (int u = 0; u < 8; ++u) b[u] = ep.bias[c0 + cw + u];
         }
-        if (ep.res) {
+        T* Z = ep.Z ? ep.Z + m0 * ep.ldz + c0 : nullptr;
+        lin_by_act(ep.act, [&](auto A) {
+          lin_walk<TI, T>(b0, b1, mrows, valid, res != nullptr, res_row, [&](int r, int c, float (&f)[8], const float (&rr)[8]) {
 #pragma unroll
-          for (int k = 0; k < NR; ++k) {
-            const int r = min((int)(threadIdx.x / (HC / 8)) + 32 * k, mrows - 1);
-            rv[k] = ld16_nt(ep.res + (m0 + r) * ep.ldr + c0 + cw);
-          }
-        }
-      }
-      lin_dump<TI>(b0, b1, wm, wn, [&](int i, int v) { return acc.c[i][half][v]; });
-      __syncthreads();
-      lin_walk<TI>(b0, b1, mrows, valid, [&](int k, int r, int c, float (&f)[8]) {
+            for (int u = 0; u < 8; ++u) f[u] += b[u];
+            if (Z) lin_st8(Z + r * ep.ldz + c, f);
 #pragma unroll
-        for (int u = 0; u < 8; ++u) f[u] += b[u];
-        if (ep.Z) st16_nt(ep.Z + (m0 + r) * ep.ldz + c0 + c, pack16<bf16>(f));
-        lin_act<8>(f, ep.act);
-        if (ep.res) {
-          float rr[8];
-          unpack16<bf16>(rv[k], rr);
+            for (int u = 0; u < 8; ++u) f[u] = lin_act1<decltype(A)::value>(f[u]) + rr[u];
+            lin_st8(out + r * ep.ldo + c, f);
+          });
+        });
+      } else {
+        lin_walk<TI, T>(b0, b1, mrows, valid, res != nullptr, res_row, [&](int r, int c, float (&f)[8], const float (&rr)[8]) {
 #pragma unroll
           for (int u = 0; u < 8; ++u) f[u] += rr[u];
-        }
-        st16_nt(ep.out + (m0 + r) * ep.ldo + c0 + c, pack16<bf16>(f));
-      });
+          lin_st8(out + r * ep.ldo + c, f);
+        });
+      }
       __syncthreads();
     }
   } else {  // SwiGLU: block 0 is the gate, block 1 the up projection of the same columns
     const int valid = min(HC, g.n - n0);
     if (ep.bias) {
 #pragma unroll
-      for (int j = 0; j < 2; ++j)
+      for (int j = 0; j < 4; ++j) {
+        const int c = n0 + dn_col(wn, j & 1);
+        f32x4 b = {0.0f, 0.0f, 0.0f, 0.0f};
+        if (c < g.n) b = *reinterpret_cast<const f32x4*>(ep.bias + (int64_t)(j >> 1) * g.n + c);
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          const int c = n0 + wn * 32 + acc_n(4 * q);
-          f32x4 b = {0.0f, 0.0f, 0.0f, 0.0f};
-          if (c < g.n) b = *reinterpret_cast<const f32x4*>(ep.bias + (int64_t)j * g.n + c);
-#pragma unroll
-          for (int i = 0; i < MI; ++i)
-#pragma unroll
-            for (int u = 0; u < 4; ++u) acc.c[i][j][4 * q + u] += b[u];
-        }
+        for (int i = 0; i < MI; ++i) acc.c[i][j] += b;
+      }
     }
     if (ep.Z) {
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
-        lin_dump<TI>(b0, b1, wm, wn, [&](int i, int v) { return acc.c[i][j][v]; });
+        lin_dump<TI>(b0, b1, wm, wn, [&](int i, int h) { return acc.c[i][2 * j + h]; });
         __syncthreads();
-        lin_walk<TI>(b0, b1, mrows, valid, [&](int, int r, int c, float (&f)[8]) {
-          st16_nt(ep.Z + (m0 + r) * ep.ldz + (int64_t)j * g.n + n0 + c, pack16<bf16>(f));
+        lin_walk<TI, T>(b0, b1, mrows, valid, false, [&](int) { return ep.res; }, [&](int r, int c, float (&f)[8], const float (&)[8]) {
+          lin_st8(ep.Z + (m0 + r) * ep.ldz + (int64_t)j * g.n + n0 + c, f);
         });
         __syncthreads();
       }
     }
-    lin_dump<TI>(b0, b1, wm, wn, [&](int i, int v) {
-      const float gv = acc.c[i][0][v];
-      return gv * sigmoid_f32(gv) * acc.c[i][1][v];
+    lin_dump<TI>(b0, b1, wm, wn, [&](int i, int h) {
+      f32x4 v = acc.c[i][h];
+#pragma unroll
+      for (int u = 0; u < 4; ++u) v[u] = v[u] * sigmoid_f32(v[u]) * acc.c[i][2 + h][u];
+      return v;
     });
     __syncthreads();
-    lin_walk<TI>(b0, b1, mrows, valid, [&](int, int r, int c, float (&f)[8]) {
-      if (ep.res) {
-        float rr[8];
-        unpack16<bf16>(ld16_nt(ep.res + (m0 + r) * ep.ldr + n0 + c), rr);
+    lin_walk<TI, T>(b0, b1, mrows, valid, ep.res != nullptr, [&](int r) { return ep.res + (m0 + r) * ep.ldr + n0; },
+                 [&](int r, int c, float (&f)[8], const float (&rr)[8]) {
 #pragma unroll
-        for (int u = 0; u < 8; ++u) f[u] += rr[u];
-      }
-      st16_nt(ep.out + (m0 + r) * ep.ldo + n0 + c, pack16<bf16>(f));
+      for (int u = 0; u < 8; ++u) f[u] += rr[u];
+      lin_st8(ep.out + (m0 + r) * ep.ldo + n0 + c, f);
     });
   }
-}
-
-// fp32: four waves, 256 x 256 tiles, the register-staged ring; a lane's accumulators 4 q .. 4 q + 3
-// are four consecutive columns, one 16-byte access each.
-template <int MODE, int OUT>
-__global__ __launch_bounds__(GEMM_THREADS, 1) void k_lin_f32(LinGemm g, LinEpi<float> ep) {
-  MOE_GEMM_LDS(L);
-  const int lin = xcd_remap(blockIdx.x, gridDim.x);
-  const int per = g.MT * g.NT;
-  const int sl = lin / per;
-  if (sl >= g.SK) return;
-  int mt, nt;
-  raster_tile(lin % per, g.MT, g.NT, mt, nt);
-  const int m0 = mt * BM, n0 = nt * BN;
-  const int wave = threadIdx.x >> 6;
-  const int wm = wave >> 1, wn = wave & 1;
-  const int k0 = sl * g.klen, klen = min(g.klen, g.red - k0), blen = min(g.klen, g.bred - k0);
-  const int mrows = min(BM, g.m - m0);
-  const int64_t ldab = g.lda * 4, ldbb = g.ldb * 4;
-  const char* Ab = static_cast<const char*>(g.A);
-  const char* Bb = static_cast<const char*>(g.B);
-  auto bsub = [&](int j) { return bsub_plain(wn, j); };
-  WaveAcc acc;
-  const int nkt = (int)cdiv(klen, Mma<float>::BK);
-  auto arow = [&](int i) -> const char* { return i < mrows ? Ab + (m0 + i) * ldab + (int64_t)k0 * 4 : nullptr; };
-  if constexpr (MODE == LIN_FWD) {
-    RowLoaderF32Tail la, lb;
-    la.init(arow, klen);
-    lb.init([&](int i) -> const char* { return n0 + i < g.n ? Bb + (n0 + i) * ldbb + (int64_t)k0 * 4 : nullptr; }, klen);
-    gemm_mainloop_reg(la, lb, nkt, acc, L, wm, bsub);
-  } else if constexpr (MODE == LIN_DX) {
-    RowLoaderF32Tail la;
-    la.init(arow, klen);
-    const char* bk = Bb + k0 * ldbb + (int64_t)n0 * 4;
-    auto lb = mn_rows<float>([=](int k) { return bk + k * ldbb; }, blen, n0, g.n);
-    gemm_mainloop_reg(la, lb, nkt, acc, L, wm, bsub);
-  } else {
-    const char* ak = Ab + k0 * ldab + (int64_t)m0 * 4;
-    const char* bk = Bb + k0 * ldbb + (int64_t)n0 * 4;
-    auto la = mn_rows<float>([=](int k) { return ak + k * ldab; }, klen, m0, g.m);
-    auto lb = mn_rows<float>([=](int k) { return bk + k * ldbb; }, blen, n0, g.n);
-    gemm_mainloop_reg(la, lb, nkt, acc, L, wm, bsub);
-  }
-  float* dst = OUT == LIN_OUT_PART ? g.part + (int64_t)sl * g.m * g.n : nullptr;
-#pragma unroll
-  for (int j = 0; j < 4; ++j)
-#pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      const int c = n0 + bsub(j) + acc_n(4 * q);  // n is a multiple of 4
-      if (c >= g.n) continue;
-      f32x4 b = {0.0f, 0.0f, 0.0f, 0.0f};
-      if (OUT == LIN_OUT_EPI && ep.bias) b = *reinterpret_cast<const f32x4*>(ep.bias + c);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int r = acc_m(wm, i);
-        if (r >= mrows) continue;
-        f32x4 v = {acc.c[i][j][4 * q], acc.c[i][j][4 * q + 1], acc.c[i][j][4 * q + 2], acc.c[i][j][4 * q + 3]};
-        if (OUT == LIN_OUT_PART) {
-          *reinterpret_cast<f32x4*>(dst + (int64_t)(m0 + r) * g.n + c) = v;
-          continue;
-        }
-        v += b;
-        if (ep.Z) *reinterpret_cast<f32x4*>(ep.Z + (m0 + r) * ep.ldz + c) = v;
-        float f[4] = {v[0], v[1], v[2], v[3]};
-        lin_act<4>(f, ep.act);
-        v = f32x4{f[0], f[1], f[2], f[3]};
-        if (ep.res) v += *reinterpret_cast<const f32x4*>(ep.res + (m0 + r) * ep.ldr + c);
-        *reinterpret_cast<f32x4*>(ep.out + (m0 + r) * ep.ldo + c) = v;
-      }
-    }
 }
 
 // Four consecutive elements of T as fp32.
@@ -493,11 +458,13 @@ __global__ __launch_bounds__(256) void k_lin_dz(const T* __restrict__ dY, int64_
           s1[u] += zu[u];
         }
       } else {
+        lin_by_act(act, [&](auto A) {
 #pragma unroll
-        for (int u = 0; u < 8; ++u) {
-          if (act != LIN_NONE) dy[u] *= lin_act_grad(z[u], act);
-          s0[u] += dy[u];
-        }
+          for (int u = 0; u < 8; ++u) {
+            if constexpr (decltype(A)::value != LIN_NONE) dy[u] *= lin_grad1<decltype(A)::value>(z[u]);
+            s0[u] += dy[u];
+          }
+        });
       }
       if (dZ) {
 #pragma unroll
@@ -547,30 +514,38 @@ __global__ __launch_bounds__(1024) void k_lin_db(const float* __restrict__ db_pa
 // ---------------------------------------------------------------------------------------------
 // Host side
 // ---------------------------------------------------------------------------------------------
-// The bf16 tiles: 256 x 256 on eight waves, and 128 x 128 on four (two workgroups per CU) where the
-// larger ones are too few to fill the chip.
+// The tiles: 256 x 256 on eight waves (bf16), and 128 x 128 on four, two workgroups per CU.
 typedef DnTile<256, 256, 2, 4> LinBig;
 typedef DnTile<128, 128, 2, 2> LinMid;
 
-// Tile size and slices of a product's reduction: one where the tiles fill half the chip, else as
-// many as fill it, each of at least four stages.
+// Tile size and slices of a product's reduction: the cheapest by a model of the time in
+// microseconds.  A round of 256 large tiles takes 1.4 per stage and 10 besides; 128 x 128 tiles
+// take 0.5 per stage where every CU has one and 0.95 where it has two, and 4 besides; fp32 stages
+// take eight times the MFMA time.  Slices cost a second launch and the writing and reading of their
+// fp32 partial products at 4 TB/s.  Measured (4096 x 4096 weights, bf16): 64 rows 13.6 us with 8
+// slices, 16.9 with 16, 30 with one; 256 rows 20.9 with 4, 31 with one; 512 rows 29 with 2, 32 with
+// one; 1024 rows 36 with one; 2048 rows 66 on the small tile.
 static void lin_plan(LinGemm& g, bool bf16_, bool may_split) {
-  const int64_t big = cdiv(g.m, 256) * cdiv(g.n, 256);
-  g.mid = bf16_ && big < 192;
-  const int t = g.mid ? 128 : 256;
-  const int bk = bf16_ ? DN_BK : 32;
-  g.MT = (int)cdiv(g.m, t);
-  g.NT = (int)cdiv(g.n, t);
-  const int64_t tiles = g.m ? (int64_t)g.MT * g.NT : 1;
-  const int slots = g.mid ? 512 : 256;
-  const int stages = (int)cdiv(g.red, bk);
+  const int stages = (int)cdiv(g.red, bf16_ ? dn_bk<bf16>() : dn_bk<float>());
+  const int64_t big = cdiv(g.m, 256) * cdiv(g.n, 256), mid = cdiv(g.m, 128) * cdiv(g.n, 128);
+  double best = bf16_ ? cdiv(big, 256) * (stages * 1.4 + 10.0) : 1e30;
   int sk = 1;
-  if (may_split && tiles < slots / 2) {
-    sk = (int)(slots / tiles);
-    if (sk > stages / 4) sk = stages / 4;
-    if (sk > 64) sk = 64;
-    if (sk < 1) sk = 1;
+  g.mid = 0;
+  static const int kSlices[] = {1, 2, 3, 4, 6, 8, 12, 16, 24, 32};
+  for (int q : kSlices) {
+    if (q > 1 && (!may_split || q > stages)) break;
+    const int64_t wgs = mid * q, rounds = cdiv(wgs, 512);
+    const double stage = bf16_ ? (wgs <= 256 ? 0.5 : 0.95) : (wgs <= 256 ? 1.9 : 3.6);
+    const double t = rounds * (cdiv(stages, q) * stage + 4.0) + (q > 1 ? 2.5 + 2e-6 * q * g.m * g.n : 0.0);
+    if (t < best) {
+      best = t;
+      sk = q;
+      g.mid = 1;
+    }
   }
+  g.MT = (int)cdiv(g.m, g.mid ? 128 : 256);
+  g.NT = (int)cdiv(g.n, g.mid ? 128 : 256);
+  const int bk = bf16_ ? dn_bk<bf16>() : dn_bk<float>();
   g.klen = (int)cdiv(stages, sk) * bk;
   g.SK = g.red > 0 ? (int)cdiv(g.red, g.klen) : 1;
 }
@@ -607,16 +582,12 @@ static LinGemm lin_gemm(const LinShape& s, int mode) {
   return g;
 }
 
-// Whether the forward's SwiGLU goes through partial products: where they are split anyway, and in
-// fp32, whose four-wave kernel keeps gate and up in different lanes.
-static bool lin_fwd_part(const LinShape& s, const LinGemm& g) { return g.SK > 1 || (s.act == LIN_SWIGLU && !s.bf16); }
-
 static size_t lin_part_bytes(const LinGemm& g) { return (size_t)g.SK * g.m * g.n * sizeof(float); }
 
 size_t linear_fwd_workspace_bytes(const LinShape& s) {
   if (s.M <= LIN_SKINNY_M) return 0;
   const LinGemm g = lin_gemm(s, LIN_FWD);
-  return lin_fwd_part(s, g) ? lin_part_bytes(g) : 0;
+  return g.SK > 1 ? lin_part_bytes(g) : 0;
 }
 
 struct LinBwdWs {
@@ -645,30 +616,26 @@ static size_t lin_carve_bwd(const LinShape& s, void* base, LinBwdWs* w) {
 
 size_t linear_bwd_workspace_bytes(const LinShape& s) { return lin_carve_bwd(s, nullptr, nullptr); }
 
-template <class TI, int MODE, int OUT>
-static void lin_launch_bf16(const LinGemm& g, const LinEpi<bf16>& ep, hipStream_t st) {
+template <typename T, class TI, int MODE, int OUT>
+static void lin_launch_t(const LinGemm& g, const LinEpi<T>& ep, hipStream_t st) {
   const int grid = grid8((int64_t)g.MT * g.NT * g.SK);
-  if (g.red % DN_BK || g.bred != g.red) k_lin_bf16<TI, MODE, true, OUT><<<grid, TI::THREADS, 0, st>>>(g, ep);
-  else k_lin_bf16<TI, MODE, false, OUT><<<grid, TI::THREADS, 0, st>>>(g, ep);
+  if (g.red % dn_bk<T>() || g.bred != g.red) k_lin<T, TI, MODE, true, OUT><<<grid, TI::THREADS, 0, st>>>(g, ep);
+  else k_lin<T, TI, MODE, false, OUT><<<grid, TI::THREADS, 0, st>>>(g, ep);
 }
 template <int MODE, int OUT>
 static void lin_launch(const LinShape& s, const LinGemm& g, const LinEpi<bf16>& eb, const LinEpi<float>& ef,
                        hipStream_t st) {
-  if (s.bf16) {
-    if (g.mid) lin_launch_bf16<LinMid, MODE, OUT>(g, eb, st);
-    else lin_launch_bf16<LinBig, MODE, OUT>(g, eb, st);
-  } else {
-    if constexpr (OUT != LIN_OUT_GLU)
-      k_lin_f32<MODE, OUT><<<grid8((int64_t)g.MT * g.NT * g.SK), GEMM_THREADS, 0, st>>>(g, ef);
-  }
+  if (!s.bf16) lin_launch_t<float, LinMid, MODE, OUT>(g, ef, st);
+  else if (g.mid) lin_launch_t<bf16, LinMid, MODE, OUT>(g, eb, st);
+  else if constexpr (OUT != LIN_OUT_PART) lin_launch_t<bf16, LinBig, MODE, OUT>(g, eb, st);  // never sliced
 }
 
-// A product whose epilogue is ep: directly, or through partial products.
+// A product whose epilogue is ep: directly, or through partial products where it is sliced.
 template <int MODE>
 static hipError_t lin_run(const LinShape& s, LinGemm g, float* part, const LinEpi<bf16>& eb, const LinEpi<float>& ef,
-                          bool through_part, hipStream_t st) {
+                          hipStream_t st) {
   if (g.m == 0) return hipSuccess;
-  if (!through_part) {
+  if (g.SK == 1) {
     if constexpr (MODE == LIN_FWD) {
       if (eb.act == LIN_SWIGLU) {
         g.n = (int)s.N;
@@ -728,7 +695,7 @@ hipError_t launch_linear(const LinShape& s, const void* X, const void* W, const 
   const LinEpi<bf16> eb = lin_epi<bf16>(bias, residual, s.ldr, Z, g.n, out, s.ldy, s.act);
   const LinEpi<float> ef = lin_epi<float>(bias, residual, s.ldr, Z, g.n, out, s.ldy, s.act);
   if (s.M <= LIN_SKINNY_M) return s.bf16 ? lin_skinny(s, X, W, eb, st) : lin_skinny(s, X, W, ef, st);
-  return lin_run<LIN_FWD>(s, g, static_cast<float*>(ws), eb, ef, lin_fwd_part(s, g), st);
+  return lin_run<LIN_FWD>(s, g, static_cast<float*>(ws), eb, ef, st);
 }
 
 hipError_t launch_linear_dz(const LinShape& s, const void* dY, const void* Z, float* dbias, void* ws, hipStream_t st) {
@@ -760,7 +727,7 @@ hipError_t launch_linear_dx(const LinShape& s, const void* dY, const void* W, vo
   g.B = W;
   g.ldb = s.K;
   return lin_run<LIN_DX>(s, g, w.part, lin_epi<bf16>(nullptr, nullptr, 0, nullptr, 0, dX, s.ldx, LIN_NONE),
-                         lin_epi<float>(nullptr, nullptr, 0, nullptr, 0, dX, s.ldx, LIN_NONE), g.SK > 1, st);
+                         lin_epi<float>(nullptr, nullptr, 0, nullptr, 0, dX, s.ldx, LIN_NONE), st);
 }
 
 hipError_t launch_linear_dw(const LinShape& s, const void* dY, const void* X, void* dW, void* ws, hipStream_t st) {
@@ -772,7 +739,7 @@ hipError_t launch_linear_dw(const LinShape& s, const void* dY, const void* X, vo
   g.B = X;
   g.ldb = s.ldx;
   return lin_run<LIN_DW>(s, g, w.part, lin_epi<bf16>(nullptr, nullptr, 0, nullptr, 0, dW, s.K, LIN_NONE),
-                         lin_epi<float>(nullptr, nullptr, 0, nullptr, 0, dW, s.K, LIN_NONE), g.SK > 1, st);
+                         lin_epi<float>(nullptr, nullptr, 0, nullptr, 0, dW, s.K, LIN_NONE), st);
 }
 
 hipError_t launch_logit_dx(const Shape& s, const void* dL, int E_pad, const void* W_r, void* dX, hipStream_t st) {
@@ -789,7 +756,7 @@ hipError_t launch_logit_dx(const Shape& s, const void* dL, int E_pad, const void
   g.bred = s.E;
   lin_plan(g, s.bf16, false);
   return lin_run<LIN_DX>(ls, g, nullptr, lin_epi<bf16>(nullptr, dX, s.d, nullptr, 0, dX, s.d, LIN_NONE),
-                         lin_epi<float>(nullptr, dX, s.d, nullptr, 0, dX, s.d, LIN_NONE), false, st);
+                         lin_epi<float>(nullptr, dX, s.d, nullptr, 0, dX, s.d, LIN_NONE), st);
 }
 
 }  // namespace moe
