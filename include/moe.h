@@ -505,7 +505,7 @@ typedef enum {
   MOE_STAGE_ROUTER_LOSS = 17, /* router losses, or their gradient */
   MOE_STAGE_DROPOUT = 18,     /* moe_dropout (moe_combine_dropout counts as COMBINE) */
   MOE_STAGE_LINEAR = 19,      /* moe_linear */
-  MOE_STAGE_LINEAR_BWD = 20,  /* each product of moe_linear_backward, and moe_backward_aux's */
+  MOE_STAGE_LINEAR_BWD = 20,  /* moe_linear_backward, and moe_backward_aux's logit dX GEMM */
   MOE_STAGE_COUNT = 21
 } moe_stage;
 

@@ -150,9 +150,14 @@ def _p(t):
     return t.data_ptr()
 
 
+# the current stream's handle without building a torch stream object (2.8 us a call)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _stream(stream=None):
-    s = stream if stream is not None else torch.cuda.current_stream()
-    return s.cuda_stream
+    if stream is None and _raw_stream is not None:
+        return _raw_stream(torch.cuda.current_device())
+    return (stream if stream is not None else torch.cuda.current_stream()).cuda_stream
 
 
 def _check(status):
@@ -336,26 +341,31 @@ def moe_router_loss_backward(dims, dloss, logits, n_seq, seq_off, token_mask, se
                                           _stream(stream)))
 
 
-def _rows(t, like, name):
-    """Row stride of a 2-D tensor of like's shape and type whose rows are contiguous."""
-    if t.dim() != 2 or t.shape != like.shape or t.dtype != like.dtype or (t.shape[1] > 1 and t.stride(1) != 1):
-        raise MoEError(-1, "%s must be %s of %s with contiguous rows" % (name, tuple(like.shape), like.dtype))
-    return t.stride(0) if t.shape[0] > 1 else max(t.stride(0), t.shape[1])
+def _row_stride(t, shape, dtype, name):
+    """Row stride of a 2-D tensor of this shape and type whose rows are contiguous."""
+    if t.shape != shape or t.dtype is not dtype:
+        raise MoEError(-1, "%s must be %s of %s" % (name, tuple(shape), dtype))
+    ld, step = t.stride()
+    if step != 1 and shape[1] > 1:
+        raise MoEError(-1, "%s must have contiguous rows" % name)
+    return ld if shape[0] > 1 else shape[1]
 
 
 def moe_dropout(x, residual, p, rng, out, stream=None):
     """out = residual + dropout(x) of 2-D bf16 / fp32 tensors (residual may be None; rows may be
     strided); rng is a device tensor of two 64-bit words, {seed, offset}.  Without a residual this is
     also the gradient of dropout."""
-    if x.dtype not in (torch.bfloat16, torch.float32):
-        raise MoEError(-2, "dtype %s not supported" % x.dtype)
+    dtype, shape = x.dtype, x.shape
+    if dtype not in (torch.bfloat16, torch.float32):
+        raise MoEError(-2, "dtype %s not supported" % dtype)
+    if len(shape) != 2:
+        raise MoEError(-1, "x must have two dimensions")
     if rng.numel() < 2 or rng.element_size() != 8:
         raise MoEError(-1, "rng must hold two 64-bit words")
-    ldx, ldo = _rows(x, x, "x"), _rows(out, x, "out")
-    ldr = _rows(residual, x, "residual") if residual is not None else 0
-    dtype = MOE_BF16 if x.dtype == torch.bfloat16 else MOE_F32
-    _check(lib().moe_dropout(x.shape[0], x.shape[1], dtype, _p(x), ldx, _p(residual), ldr, float(p), _p(rng), _p(out),
-                             ldo, _stream(stream)))
+    ldx, ldo = _row_stride(x, shape, dtype, "x"), _row_stride(out, shape, dtype, "out")
+    ldr = _row_stride(residual, shape, dtype, "residual") if residual is not None else 0
+    _check(lib().moe_dropout(shape[0], shape[1], MOE_BF16 if dtype is torch.bfloat16 else MOE_F32, x.data_ptr(), ldx,
+                             _p(residual), ldr, p, rng.data_ptr(), out.data_ptr(), ldo, _stream(stream)))
 
 
 def moe_combine_dropout(dims, plan, Y_perm, weighted, residual, p, rng, out, stream=None):

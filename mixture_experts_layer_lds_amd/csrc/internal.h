@@ -154,10 +154,9 @@ size_t linear_bwd_workspace_bytes(const LinShape& s);
 // out = residual + act(X W^T + bias), Z = X W^T + bias; bias, residual and Z may be null
 hipError_t launch_linear(const LinShape& s, const void* X, const void* W, const float* bias, const void* residual,
                          void* Z, void* out, void* ws, hipStream_t st);
-// the backward's steps, in this order on one workspace: dZ (and dbias when given), then the products
-hipError_t launch_linear_dz(const LinShape& s, const void* dY, const void* Z, float* dbias, void* ws, hipStream_t st);
-hipError_t launch_linear_dx(const LinShape& s, const void* dY, const void* W, void* dX, void* ws, hipStream_t st);
-hipError_t launch_linear_dw(const LinShape& s, const void* dY, const void* X, void* dW, void* ws, hipStream_t st);
+// dX, dW and dbias, each of which may be null
+hipError_t launch_linear_bwd(const LinShape& s, const void* dY, const void* X, const void* W, const void* Z, void* dX,
+                             void* dW, float* dbias, void* ws, hipStream_t st);
 // dX += dL W_r for dense logit gradients dL [T][E_pad] in the element type
 hipError_t launch_logit_dx(const Shape& s, const void* dL, int E_pad, const void* W_r, void* dX, hipStream_t st);
 

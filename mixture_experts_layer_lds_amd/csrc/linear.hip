@@ -27,23 +27,25 @@ enum { LIN_NONE = 0, LIN_RELU = 1, LIN_GELU = 2, LIN_SILU = 3, LIN_SWIGLU = 4 };
 
 // The normal distribution's upper tail at |z| and, through *e, exp(-z^2 / 2):
 // erfc(x) = (a1 t + .. + a5 t^5) exp(-x^2), t = 1 / (1 + p x) (Abramowitz and Stegun 7.1.26, off by
-// at most 1.5e-7), a third of the instructions of the library's erf, which cost the GELU epilogue
-// 0.10 of 0.90 ms on the 8192 x 14336 x 4096 product.
+// at most 1.5e-7), with 1/2 and x = |z| / sqrt 2 folded into the constants: a third of the
+// instructions of the library's erf, which cost the GELU epilogue 0.10 of 0.90 ms on the
+// 8192 x 14336 x 4096 product.
 __device__ __forceinline__ float normal_tail(float z, float* e) {
-  const float x = fabsf(z) * 0.70710678118654752f;
-  const float t = __builtin_amdgcn_rcpf(1.0f + 0.3275911f * x);
-  *e = __expf(-0.5f * z * z);
-  return 0.5f * t * (0.254829592f + t * (-0.284496736f + t * (1.421413741f + t * (-1.453152027f + t * 1.061405429f)))) * *e;
+  const float t = __builtin_amdgcn_rcpf(fmaf(fabsf(z), 0.23164189f, 1.0f));
+  *e = __builtin_amdgcn_exp2f(z * z * -0.72134752f);
+  const float p = fmaf(t, fmaf(t, fmaf(t, fmaf(t, 0.5307027145f, -0.7265760135f), 0.7107068705f), -0.142248368f), 0.127414796f);
+  return p * t * *e;
 }
 
-// act(z) of one element and its derivative (not SwiGLU).  GELU is the exact form z Phi(z).
+// act(z) of one element and its derivative (not SwiGLU).  GELU is the exact form
+// z Phi(z) = max(z, 0) - |z| tail(|z|).
 template <int ACT>
 __device__ __forceinline__ float lin_act1(float z) {
   if constexpr (ACT == LIN_RELU) return z < 0.0f ? 0.0f : z;  // a NaN stays
   if constexpr (ACT == LIN_GELU) {
     float e;
     const float q = normal_tail(z, &e);
-    return z < 0.0f ? z * q : z - z * q;
+    return fmaf(-fabsf(z), q, z < 0.0f ? 0.0f : z);
   }
   if constexpr (ACT == LIN_SILU) return z * sigmoid_f32(z);
   return z;
@@ -161,10 +163,7 @@ __device__ __forceinline__ void lin_walk(char* b0, char* b1, int mrows, int vali
 // One product on the dense main loop (gemm_dense.h).  SwiGLU (LIN_OUT_GLU): a tile has TN / 2 output
 // columns, the B tile stacks their gate rows over their up rows, so a lane holds both of a column.
 template <typename T, class TI, int MODE, bool TAIL, int OUT>
-__global__ __launch_bounds__(TI::THREADS, TI::NW == 8 ? 1 : 2) void k_lin(LinGemm g, LinEpi<T> ep) {
-  __shared__ __attribute__((aligned(1024))) char b0[TI::SLOT];
-  __shared__ __attribute__((aligned(1024))) char b1[TI::SLOT];
-  const int lin = xcd_remap(blockIdx.x, gridDim.x);
+__device__ __forceinline__ void lin_tile(int lin, const LinGemm& g, const LinEpi<T>& ep, char* b0, char* b1) {
   const int per = g.MT * g.NT;
   const int sl = lin / per;
   if (sl >= g.SK) return;
@@ -293,6 +292,23 @@ __global__ __launch_bounds__(TI::THREADS, TI::NW == 8 ? 1 : 2) void k_lin(LinGem
   }
 }
 
+template <typename T, class TI, int MODE, bool TAIL, int OUT>
+__global__ __launch_bounds__(TI::THREADS, TI::NW == 8 ? 1 : 2) void k_lin(LinGemm g, LinEpi<T> ep) {
+  __shared__ __attribute__((aligned(1024))) char b0[TI::SLOT];
+  __shared__ __attribute__((aligned(1024))) char b1[TI::SLOT];
+  lin_tile<T, TI, MODE, TAIL, OUT>(xcd_remap(blockIdx.x, gridDim.x), g, ep, b0, b1);
+}
+
+// The backward's two products in one launch, where neither fills the chip: workgroups below nx take
+// dX's tiles, the others dW's.
+template <typename T, class TI, int OUT>
+__global__ __launch_bounds__(TI::THREADS, 2) void k_lin_pair(LinGemm gx, LinEpi<T> ex, int nx, LinGemm gw, LinEpi<T> ew) {
+  __shared__ __attribute__((aligned(1024))) char b0[TI::SLOT];
+  __shared__ __attribute__((aligned(1024))) char b1[TI::SLOT];
+  if ((int)blockIdx.x < nx) lin_tile<T, TI, LIN_DX, true, OUT>(xcd_remap(blockIdx.x, nx), gx, ex, b0, b1);
+  else lin_tile<T, TI, LIN_DW, true, OUT>(xcd_remap(blockIdx.x - nx, gridDim.x - nx), gw, ew, b0, b1);
+}
+
 // Four consecutive elements of T as fp32.
 template <typename T> __device__ __forceinline__ f32x4 lin_ld4(const T* p) {
   if constexpr (sizeof(T) == 4) {
@@ -336,9 +352,8 @@ __device__ __forceinline__ void lin_epi4(const LinEpi<T>& ep, int64_t r, int c, 
 // output columns and requests the slices four at a time.  n: output columns; np: columns of the
 // partial products (2 n for SwiGLU).
 template <typename T>
-__global__ __launch_bounds__(256) void k_lin_finish(const float* __restrict__ part, int SK, int m, int n, int np,
-                                                    LinEpi<T> ep) {
-  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+__device__ __forceinline__ void lin_finish(int64_t i, const float* __restrict__ part, int SK, int m, int n, int np,
+                                           const LinEpi<T>& ep) {
   const int cpr = n / 4;
   if (i >= (int64_t)m * cpr) return;
   const int64_t r = i / cpr;
@@ -368,56 +383,169 @@ __global__ __launch_bounds__(256) void k_lin_finish(const float* __restrict__ pa
   }
   lin_epi4(ep, r, c, n, glu, z, zu);
 }
+template <typename T>
+__global__ __launch_bounds__(256) void k_lin_finish(const float* __restrict__ part, int SK, int m, int n, int np,
+                                                    LinEpi<T> ep) {
+  lin_finish<T>((int64_t)blockIdx.x * 256 + threadIdx.x, part, SK, m, n, np, ep);
+}
 
-// A few rows (single tokens, small decode batches): one workgroup per 16 rows of W (SwiGLU: 8 gate
-// and the 8 matching up rows), its waves sharing the reduction; W is streamed from memory straight
-// into the MFMA's A operand (two batches of 1 KB loads in flight per wave) and X, which stays in
-// the caches, into B, NG groups of 16 rows.  The waves' partial tiles meet in LDS, are added in
-// wave order, and wave g finishes group g in the same launch.  Bound by reading W once.
-template <typename T, int NG, bool GLU>
-__global__ __launch_bounds__(1024) void k_lin_skinny(const T* __restrict__ X, int64_t ldx, const T* __restrict__ W,
-                                                     int m, int n, int K, LinEpi<T> ep) {
-  extern __shared__ f32x4 sk_part[];  // [wave][NG][64]
+// db = the row blocks' sums (fp64) for 32 columns: RUNS runs of row blocks, then the runs in order.
+constexpr int LIN_DB_RUNS = 8;
+__device__ __forceinline__ void lin_db(int block, const float* __restrict__ db_part, int blocks, int np,
+                                       float* __restrict__ db) {
+  __shared__ double red[LIN_DB_RUNS][33];
+  const int cl = threadIdx.x & 31, run = threadIdx.x >> 5;
+  const int c = block * 32 + cl;
+  double v = 0.0;
+  if (c < np) {
+#pragma unroll 8
+    for (int b = run; b < blocks; b += LIN_DB_RUNS) v += (double)db_part[(int64_t)b * np + c];
+  }
+  red[run][cl] = v;
+  __syncthreads();
+  if (run == 0 && c < np) {
+#pragma unroll
+    for (int q = 1; q < LIN_DB_RUNS; ++q) v += red[q][cl];
+    db[c] = (float)v;
+  }
+}
+__global__ __launch_bounds__(256) void k_lin_db(const float* __restrict__ db_part, int blocks, int np,
+                                                float* __restrict__ db) {
+  lin_db(blockIdx.x, db_part, blocks, np, db);
+}
+
+// What is left after k_lin_pair's partial products, in one launch: dX, dW and db (when given).
+struct LinDb {
+  const float* part;
+  int blocks, np;
+  float* db;
+};
+template <typename T>
+__global__ __launch_bounds__(256) void k_lin_finish_pair(LinGemm gx, LinEpi<T> ex, int nx, LinGemm gw, LinEpi<T> ew, int nw,
+                                                         LinDb d) {
+  const int b = blockIdx.x;
+  if (b < nx) lin_finish<T>((int64_t)b * 256 + threadIdx.x, gx.part, gx.SK, gx.m, gx.n, gx.n, ex);
+  else if (b < nx + nw) lin_finish<T>((int64_t)(b - nx) * 256 + threadIdx.x, gw.part, gw.SK, gw.m, gw.n, gw.n, ew);
+  else lin_db(b - nx - nw, d.part, d.blocks, d.np, d.db);
+}
+
+// A few rows (single tokens, small decode batches): one workgroup per 16 RT rows of W, its waves
+// sharing the reduction; W is streamed from memory straight into the MFMA's A operand (two batches
+// of loads in flight per wave) and X, which stays in the caches, into B, NG groups of 16 rows.  The
+// waves' partial tiles meet in LDS, are added in wave order, and the epilogue runs in the same
+// launch.  Bound by reading W once.
+// SwiGLU with RT = 1 takes 8 gate rows and the 8 matching up rows, so that a column's two halves lie
+// 32 lanes apart; with RT = 2 16 gate rows and their 16 up rows, in the same lane.
+template <typename T, int NG, int RT>
+struct LinStream {
+  static constexpr int U = NG + RT <= 3 ? 4 : 2;  // steps per batch: two batches fit the registers
+  const T* w[RT];  // lane's W rows at its k offset
+  const T* x[NG];
+  u32x4 wv[2][U][RT], xv[2][U][NG];
+  __device__ __forceinline__ void load(int buf, int st, int last) {
+    constexpr int S = DecMma<T>::S;
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int k = min(st + u, last) * S;
+#pragma unroll
+      for (int r = 0; r < RT; ++r) wv[buf][u][r] = ld16(w[r] + k);
+#pragma unroll
+      for (int g = 0; g < NG; ++g) xv[buf][u][g] = ld16(x[g] + k);
+    }
+  }
+  __device__ __forceinline__ void mma(int buf, int live, f32x4 (&acc)[RT][NG]) const {
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+      if (u < live) {
+#pragma unroll
+        for (int r = 0; r < RT; ++r)
+#pragma unroll
+          for (int g = 0; g < NG; ++g) acc[r][g] = DecMma<T>::mma(wv[buf][u][r], xv[buf][u][g], acc[r][g]);
+      }
+  }
+  // steps [a, b), a < b: batches of U with the next batch's loads issued before the current one's
+  // MFMAs; steps past b repeat the last one and are not used
+  __device__ __forceinline__ void run(int a, int b, f32x4 (&acc)[RT][NG]) {
+    load(0, a, b - 1);
+    int st = a;
+    for (; st + 2 * U < b; st += 2 * U) {  // steady state: both batches whole
+      load(1, st + U, b - 1);
+      mma(0, U, acc);
+      load(0, st + 2 * U, b - 1);
+      mma(1, U, acc);
+    }
+    if (st + U < b) {
+      load(1, st + U, b - 1);
+      mma(0, U, acc);
+      mma(1, b - st - U, acc);
+    } else {
+      mma(0, b - st, acc);
+    }
+  }
+};
+
+template <typename T, int NG, int RT, bool GLU>
+__global__ __launch_bounds__(512) void k_lin_skinny(const T* __restrict__ X, int64_t ldx, const T* __restrict__ W,
+                                                    int m, int n, int K, LinEpi<T> ep) {
+  extern __shared__ f32x4 sk_part[];  // [wave][RT][NG][64]
   constexpr int S = DecMma<T>::S, V = DecMma<T>::V;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), W_ = blockDim.x >> 6;
   const int r16 = lane & 15, q = lane >> 4, ko = q * V;
-  constexpr int TC = GLU ? 8 : 16;  // output columns per tile
+  constexpr int TC = GLU ? 8 * RT : 16 * RT;  // output columns per tile
   const int c0 = blockIdx.x * TC;
-  const int row = GLU ? (r16 < 8 ? c0 + r16 : n + c0 + r16 - 8) : min(c0 + r16, n - 1);
-  DecStream<T, NG> ds;
-  ds.w = W + (int64_t)row * K + ko;
+  LinStream<T, NG, RT> ds;
+#pragma unroll
+  for (int r = 0; r < RT; ++r) {
+    const int row = !GLU ? min(c0 + 16 * r + r16, n - 1)
+                         : (RT == 1 ? (r16 < 8 ? c0 + r16 : n + c0 + r16 - 8) : r * n + min(c0 + r16, n - 1));
+    ds.w[r] = W + (int64_t)row * K + ko;
+  }
 #pragma unroll
   for (int g = 0; g < NG; ++g) ds.x[g] = X + (int64_t)min(g * 16 + r16, m - 1) * ldx + ko;
-  f32x4 acc[NG];
+  f32x4 acc[RT][NG];
 #pragma unroll
-  for (int g = 0; g < NG; ++g) acc[g] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+  for (int r = 0; r < RT; ++r)
+#pragma unroll
+    for (int g = 0; g < NG; ++g) acc[r][g] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
   const int ns = K / S, a = (int)((int64_t)ns * wave / W_), b = (int)((int64_t)ns * (wave + 1) / W_);
-  dec_stream<T, NG>(ds, a, b, acc);
+  if (a < b) ds.run(a, b, acc);
   if (wave == W_ - 1 && K % S) {  // the last, partial step: lanes past K supply zeros on both sides
     const bool in = ns * S + ko < K;
     const u32x4 zero = {0u, 0u, 0u, 0u};
-    const u32x4 wv = in ? ld16(ds.w + ns * S) : zero;
 #pragma unroll
     for (int g = 0; g < NG; ++g) {
       const u32x4 xv = in ? ld16(ds.x[g] + ns * S) : zero;
-      acc[g] = DecMma<T>::mma(wv, xv, acc[g]);
+#pragma unroll
+      for (int r = 0; r < RT; ++r) acc[r][g] = DecMma<T>::mma(in ? ld16(ds.w[r] + ns * S) : zero, xv, acc[r][g]);
     }
   }
 #pragma unroll
-  for (int g = 0; g < NG; ++g) sk_part[(wave * NG + g) * 64 + lane] = acc[g];
-  __syncthreads();
-  for (int g = wave; g < NG; g += W_) {
-    f32x4 v = sk_part[g * 64 + lane];
-    for (int w = 1; w < W_; ++w) v += sk_part[(w * NG + g) * 64 + lane];
-    const int r = g * 16 + r16;
-    if constexpr (GLU) {  // gate rows in lanes 0-31, the same columns' up rows 32 lanes above
-      f32x4 up;
+  for (int r = 0; r < RT; ++r)
 #pragma unroll
-      for (int u = 0; u < 4; ++u) up[u] = __shfl_xor(v[u], 32, 64);
-      if (q < 2 && r < m) lin_epi4(ep, (int64_t)r, c0 + 4 * q, n, true, v, up);
-    } else {
+    for (int g = 0; g < NG; ++g) sk_part[((wave * RT + r) * NG + g) * 64 + lane] = acc[r][g];
+  __syncthreads();
+  auto total = [&](int r, int g) {
+    f32x4 v = sk_part[(r * NG + g) * 64 + lane];
+    for (int w = 1; w < W_; ++w) v += sk_part[((w * RT + r) * NG + g) * 64 + lane];
+    return v;
+  };
+  constexpr int ITEMS = (GLU ? 1 : RT) * NG;  // 16 x 16 (SwiGLU: 8 RT x 16) output blocks
+  for (int it = wave; it < ITEMS; it += W_) {
+    const int g = it % NG, r = it / NG, t = g * 16 + r16;
+    if constexpr (GLU) {
+      f32x4 z = total(0, g), up;
+      if constexpr (RT == 1) {
+#pragma unroll
+        for (int u = 0; u < 4; ++u) up[u] = __shfl_xor(z[u], 32, 64);
+      } else {
+        up = total(1, g);
+      }
       const int c = c0 + 4 * q;
-      if (r < m && c < n) lin_epi4(ep, (int64_t)r, c, n, false, v, v);
+      if ((RT == 2 || q < 2) && t < m && c < n) lin_epi4(ep, (int64_t)t, c, n, true, z, up);
+    } else {
+      const int c = c0 + 16 * r + 4 * q;
+      const f32x4 z = total(r, g);
+      if (t < m && c < n) lin_epi4(ep, (int64_t)t, c, n, false, z, z);
     }
   }
 }
@@ -491,26 +619,6 @@ __global__ __launch_bounds__(256) void k_lin_dz(const T* __restrict__ dY, int64_
   }
 }
 
-// db = the row blocks' sums (fp64): 32 columns by 32 runs of row blocks per workgroup, then the runs
-// in order.
-__global__ __launch_bounds__(1024) void k_lin_db(const float* __restrict__ db_part, int blocks, int np,
-                                                 float* __restrict__ db) {
-  __shared__ double red[32][33];
-  const int cl = threadIdx.x & 31, run = threadIdx.x >> 5;
-  const int c = blockIdx.x * 32 + cl;
-  double v = 0.0;
-  if (c < np) {
-#pragma unroll 4
-    for (int b = run; b < blocks; b += 32) v += (double)db_part[(int64_t)b * np + c];
-  }
-  red[run][cl] = v;
-  __syncthreads();
-  if (run == 0 && c < np) {
-    for (int q = 1; q < 32; ++q) v += red[q][cl];
-    db[c] = (float)v;
-  }
-}
-
 // ---------------------------------------------------------------------------------------------
 // Host side
 // ---------------------------------------------------------------------------------------------
@@ -520,34 +628,42 @@ typedef DnTile<128, 128, 2, 2> LinMid;
 
 // Tile size and slices of a product's reduction: the cheapest by a model of the time in
 // microseconds.  A round of 256 large tiles takes 1.4 per stage and 10 besides; 128 x 128 tiles
-// take 0.5 per stage where every CU has one and 0.95 where it has two, and 4 besides; fp32 stages
-// take eight times the MFMA time.  Slices cost a second launch and the writing and reading of their
-// fp32 partial products at 4 TB/s.  Measured (4096 x 4096 weights, bf16): 64 rows 13.6 us with 8
-// slices, 16.9 with 16, 30 with one; 256 rows 20.9 with 4, 31 with one; 512 rows 29 with 2, 32 with
-// one; 1024 rows 36 with one; 2048 rows 66 on the small tile.
+// take 0.5 per stage where every CU has one (0.8 in the backward's pair, whose operands are read
+// with their rows along the reduction) and 0.95 where it has two, and 4 besides; an fp32 stage 1.9
+// and 3.6.  Slices cost a second launch (2.5) and 1.2 per million partial products written and read
+// back (fp32, whose stores pass beside longer stages, 0.4).  Measured (4096 x 4096 weights, bf16): 64 rows 13.6 us with 8 slices, 16.9 with 16, 30
+// with one; 256 rows 20.9 with 4, 31 with one; 512 rows 29 with 2, 32 with one; 1024 rows 36 with
+// one; 2048 rows 66 on the small tile.
+constexpr int kLinSlices[] = {1, 2, 3, 4, 6, 8, 12, 16, 24, 32};
+static int lin_stages(const LinGemm& g, bool bf16_) { return (int)cdiv(g.red, bf16_ ? dn_bk<bf16>() : dn_bk<float>()); }
+static int64_t lin_mid_tiles(const LinGemm& g) { return cdiv(g.m, 128) * cdiv(g.n, 128); }
+// Model of 128 x 128 tiles: wgs workgroups of `stages` stages, out partial products in all.
+static double lin_mid_time(int64_t wgs, int64_t stages, double out, bool bf16_, bool pair) {
+  const double stage = bf16_ ? (wgs > 256 ? 0.95 : (pair ? 0.8 : 0.5)) : (wgs > 256 ? 3.6 : 1.9);
+  const double rounds = wgs <= 512 ? 1.0 : wgs / 512.0;
+  return rounds * (stages * stage + 4.0) + (out > 0 ? 2.5 + (bf16_ ? 1.2e-6 : 0.4e-6) * out : 0.0);
+}
+static void lin_set(LinGemm& g, bool bf16_, int mid, int sk) {
+  g.mid = mid;
+  g.MT = (int)cdiv(g.m, mid ? 128 : 256);
+  g.NT = (int)cdiv(g.n, mid ? 128 : 256);
+  g.klen = (int)cdiv(lin_stages(g, bf16_), sk) * (bf16_ ? dn_bk<bf16>() : dn_bk<float>());
+  g.SK = g.red > 0 ? (int)cdiv(g.red, g.klen) : 1;
+}
 static void lin_plan(LinGemm& g, bool bf16_, bool may_split) {
-  const int stages = (int)cdiv(g.red, bf16_ ? dn_bk<bf16>() : dn_bk<float>());
-  const int64_t big = cdiv(g.m, 256) * cdiv(g.n, 256), mid = cdiv(g.m, 128) * cdiv(g.n, 128);
-  double best = bf16_ ? cdiv(big, 256) * (stages * 1.4 + 10.0) : 1e30;
-  int sk = 1;
-  g.mid = 0;
-  static const int kSlices[] = {1, 2, 3, 4, 6, 8, 12, 16, 24, 32};
-  for (int q : kSlices) {
+  const int stages = lin_stages(g, bf16_);
+  double best = bf16_ ? cdiv(cdiv(g.m, 256) * cdiv(g.n, 256), 256) * (stages * 1.4 + 10.0) : 1e30;
+  int mid = 0, sk = 1;
+  for (int q : kLinSlices) {
     if (q > 1 && (!may_split || q > stages)) break;
-    const int64_t wgs = mid * q, rounds = cdiv(wgs, 512);
-    const double stage = bf16_ ? (wgs <= 256 ? 0.5 : 0.95) : (wgs <= 256 ? 1.9 : 3.6);
-    const double t = rounds * (cdiv(stages, q) * stage + 4.0) + (q > 1 ? 2.5 + 2e-6 * q * g.m * g.n : 0.0);
+    const double t = lin_mid_time(lin_mid_tiles(g) * q, cdiv(stages, q), q > 1 ? (double)q * g.m * g.n : 0.0, bf16_, false);
     if (t < best) {
       best = t;
+      mid = 1;
       sk = q;
-      g.mid = 1;
     }
   }
-  g.MT = (int)cdiv(g.m, g.mid ? 128 : 256);
-  g.NT = (int)cdiv(g.n, g.mid ? 128 : 256);
-  const int bk = bf16_ ? dn_bk<bf16>() : dn_bk<float>();
-  g.klen = (int)cdiv(stages, sk) * bk;
-  g.SK = g.red > 0 ? (int)cdiv(g.red, g.klen) : 1;
+  lin_set(g, bf16_, mid, sk);
 }
 
 // Rows per workgroup of k_lin_dz: 64 where that gives four workgroups per CU, fewer (at least 8) for
@@ -558,8 +674,10 @@ static int lin_dz_rows(const LinShape& s) {
   return rows;
 }
 
-// Rows up to which the forward streams W through k_lin_skinny.
-constexpr int LIN_SKINNY_M = 32;
+// Whether the forward streams W through k_lin_skinny: up to 16 rows, and up to 32 while K keeps the
+// repeated reads of X short (7168 x 2048 weights, 32 rows: 10.5 us against 12.3 tiled; 4096 x 4096:
+// 13.6 against 12.2).
+static bool lin_is_skinny(const LinShape& s) { return s.M <= 16 || (s.M <= 32 && s.K <= 2048); }
 
 static LinGemm lin_gemm(const LinShape& s, int mode) {
   LinGemm g{};
@@ -585,15 +703,40 @@ static LinGemm lin_gemm(const LinShape& s, int mode) {
 static size_t lin_part_bytes(const LinGemm& g) { return (size_t)g.SK * g.m * g.n * sizeof(float); }
 
 size_t linear_fwd_workspace_bytes(const LinShape& s) {
-  if (s.M <= LIN_SKINNY_M) return 0;
+  if (lin_is_skinny(s)) return 0;
   const LinGemm g = lin_gemm(s, LIN_FWD);
   return g.SK > 1 ? lin_part_bytes(g) : 0;
+}
+
+// The backward's two products where both are small: 128 x 128 tiles of both side by side in one
+// launch, the same number of slices for each (999 x 1000 x 264, ReLU with a bias: 26 us in six
+// launches, 20 in three; 25.9 unsliced, 20.8 with 2, 20.2 with 3, 24.8 with 8).  False: they are launched one after the other, each with a plan of its own.
+static bool lin_pair_plan(const LinShape& s, LinGemm& gx, LinGemm& gw, bool* parts) {
+  const int64_t tiles = lin_mid_tiles(gx) + lin_mid_tiles(gw);
+  if (s.M == 0 || tiles > 256) return false;
+  const int sx = lin_stages(gx, s.bf16), sw = lin_stages(gw, s.bf16), most = sx > sw ? sx : sw;
+  const double out = (double)gx.m * gx.n + (double)gw.m * gw.n;
+  double best = 1e30;
+  int sk = 1;
+  for (int q : kLinSlices) {
+    if (q > most) break;
+    const double t = lin_mid_time(tiles * q, cdiv(most, q), q > 1 ? q * out : 0.0, s.bf16, true);
+    if (t < best) {
+      best = t;
+      sk = q;
+    }
+  }
+  lin_set(gx, s.bf16, 1, sk < sx ? sk : sx);
+  lin_set(gw, s.bf16, 1, sk < sw ? sk : sw);
+  *parts = sk > 1;
+  return true;
 }
 
 struct LinBwdWs {
   void* dZ;
   float* db_part;
-  float* part;
+  float* part;    // of a product on its own, or dX's of a pair
+  float* part_w;  // dW's of a pair
 };
 static size_t lin_carve_bwd(const LinShape& s, void* base, LinBwdWs* w) {
   char* b = static_cast<char*>(base);
@@ -607,9 +750,17 @@ static size_t lin_carve_bwd(const LinShape& s, void* base, LinBwdWs* w) {
   LinBwdWs q;
   q.dZ = take(s.act == LIN_NONE ? 0 : (size_t)s.M * NW * (s.bf16 ? 2 : 4));
   q.db_part = reinterpret_cast<float*>(take((size_t)cdiv(s.M, lin_dz_rows(s)) * NW * 4));
-  const LinGemm gx = lin_gemm(s, LIN_DX), gw = lin_gemm(s, LIN_DW);
+  LinGemm gx = lin_gemm(s, LIN_DX), gw = lin_gemm(s, LIN_DW);
   const size_t px = gx.SK > 1 ? lin_part_bytes(gx) : 0, pw = gw.SK > 1 ? lin_part_bytes(gw) : 0;
-  q.part = reinterpret_cast<float*>(take(px > pw ? px : pw));
+  size_t alone = px > pw ? px : pw;
+  bool parts = false;
+  if (lin_pair_plan(s, gx, gw, &parts) && parts) {
+    q.part_w = reinterpret_cast<float*>(take(lin_part_bytes(gw)));
+    if (lin_part_bytes(gx) > alone) alone = lin_part_bytes(gx);
+  } else {
+    q.part_w = nullptr;
+  }
+  q.part = reinterpret_cast<float*>(take(alone));
   if (w) *w = q;
   return off;
 }
@@ -622,39 +773,35 @@ static void lin_launch_t(const LinGemm& g, const LinEpi<T>& ep, hipStream_t st) 
   if (g.red % dn_bk<T>() || g.bred != g.red) k_lin<T, TI, MODE, true, OUT><<<grid, TI::THREADS, 0, st>>>(g, ep);
   else k_lin<T, TI, MODE, false, OUT><<<grid, TI::THREADS, 0, st>>>(g, ep);
 }
-template <int MODE, int OUT>
-static void lin_launch(const LinShape& s, const LinGemm& g, const LinEpi<bf16>& eb, const LinEpi<float>& ef,
-                       hipStream_t st) {
-  if (!s.bf16) lin_launch_t<float, LinMid, MODE, OUT>(g, ef, st);
-  else if (g.mid) lin_launch_t<bf16, LinMid, MODE, OUT>(g, eb, st);
-  else if constexpr (OUT != LIN_OUT_PART) lin_launch_t<bf16, LinBig, MODE, OUT>(g, eb, st);  // never sliced
+template <int MODE, int OUT, typename T>
+static void lin_launch(const LinGemm& g, const LinEpi<T>& ep, hipStream_t st) {
+  if constexpr (sizeof(T) == 4) lin_launch_t<T, LinMid, MODE, OUT>(g, ep, st);
+  else if (g.mid) lin_launch_t<T, LinMid, MODE, OUT>(g, ep, st);
+  else if constexpr (OUT != LIN_OUT_PART) lin_launch_t<T, LinBig, MODE, OUT>(g, ep, st);  // never sliced
 }
 
 // A product whose epilogue is ep: directly, or through partial products where it is sliced.
-template <int MODE>
-static hipError_t lin_run(const LinShape& s, LinGemm g, float* part, const LinEpi<bf16>& eb, const LinEpi<float>& ef,
-                          hipStream_t st) {
+template <int MODE, typename T>
+static hipError_t lin_run(LinGemm g, float* part, const LinEpi<T>& ep, hipStream_t st) {
   if (g.m == 0) return hipSuccess;
   if (g.SK == 1) {
     if constexpr (MODE == LIN_FWD) {
-      if (eb.act == LIN_SWIGLU) {
-        g.n = (int)s.N;
+      if (ep.act == LIN_SWIGLU) {
+        g.n /= 2;
         g.NT = (int)cdiv(g.n, g.mid ? 64 : 128);
-        lin_launch<MODE, LIN_OUT_GLU>(s, g, eb, ef, st);
+        lin_launch<MODE, LIN_OUT_GLU>(g, ep, st);
         return hipGetLastError();
       }
     }
-    lin_launch<MODE, LIN_OUT_EPI>(s, g, eb, ef, st);
+    lin_launch<MODE, LIN_OUT_EPI>(g, ep, st);
     return hipGetLastError();
   }
   g.part = part;
-  lin_launch<MODE, LIN_OUT_PART>(s, g, eb, ef, st);
+  lin_launch<MODE, LIN_OUT_PART>(g, ep, st);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  const int n = eb.act == LIN_SWIGLU ? g.n / 2 : g.n;
-  const int grid = (int)cdiv((int64_t)g.m * (n / 4), 256);
-  if (s.bf16) k_lin_finish<bf16><<<grid, 256, 0, st>>>(part, g.SK, g.m, n, g.n, eb);
-  else k_lin_finish<float><<<grid, 256, 0, st>>>(part, g.SK, g.m, n, g.n, ef);
+  const int n = ep.act == LIN_SWIGLU ? g.n / 2 : g.n;
+  k_lin_finish<T><<<(int)cdiv((int64_t)g.m * (n / 4), 256), 256, 0, st>>>(part, g.SK, g.m, n, g.n, ep);
   return hipGetLastError();
 }
 
@@ -664,18 +811,27 @@ static LinEpi<T> lin_epi(const float* bias, const void* res, int64_t ldr, void* 
   return LinEpi<T>{bias, static_cast<const T*>(res), ldr, static_cast<T*>(Z), ldz, static_cast<T*>(out), ldo, act};
 }
 
-template <typename T, int NG>
-static void lin_skinny_ng(const LinShape& s, const void* X, const void* W, const LinEpi<T>& ep, hipStream_t st) {
+template <typename T, int NG, int RT>
+static void lin_skinny_rt(const LinShape& s, const void* X, const void* W, const LinEpi<T>& ep, hipStream_t st) {
   const bool glu = s.act == LIN_SWIGLU;
-  const int tiles = (int)cdiv(s.N, glu ? 8 : 16);
-  // waves per tile: enough that the grid has 8 per CU, each with at least four steps to read
+  const int tiles = (int)cdiv(s.N, (glu ? 8 : 16) * RT);
+  // waves per tile: more while a wave has over 16 steps to read, or while the grid has fewer than 6
+  // waves per CU and a wave at least 8 steps (16384 x 4096 weights, one row: 32.0 us with 2 waves,
+  // 26.3 with 8; 7168 x 2048: 7.6 with 4, 8.1 with 8)
+  const int steps = (int)(s.K / DecMma<T>::S);
   int w = 4;
-  while (w < 16 && tiles * w < 2048 && s.K / (w * DecMma<T>::S) >= 8) w *= 2;
-  const size_t lds = (size_t)w * NG * 64 * sizeof(f32x4);
+  while (w < 8 && (steps / w > 16 || (tiles * w < 1536 && steps / w >= 8))) w *= 2;
+  const size_t lds = (size_t)w * RT * NG * 64 * sizeof(f32x4);
   const T* x = static_cast<const T*>(X);
   const T* wt = static_cast<const T*>(W);
-  if (glu) k_lin_skinny<T, NG, true><<<tiles, w * 64, lds, st>>>(x, s.ldx, wt, (int)s.M, (int)s.N, (int)s.K, ep);
-  else k_lin_skinny<T, NG, false><<<tiles, w * 64, lds, st>>>(x, s.ldx, wt, (int)s.M, (int)s.N, (int)s.K, ep);
+  if (glu) k_lin_skinny<T, NG, RT, true><<<tiles, w * 64, lds, st>>>(x, s.ldx, wt, (int)s.M, (int)s.N, (int)s.K, ep);
+  else k_lin_skinny<T, NG, RT, false><<<tiles, w * 64, lds, st>>>(x, s.ldx, wt, (int)s.M, (int)s.N, (int)s.K, ep);
+}
+// Two row blocks per wave halve the reads of X, where that still leaves a workgroup for nearly every CU.
+template <typename T, int NG>
+static void lin_skinny_ng(const LinShape& s, const void* X, const void* W, const LinEpi<T>& ep, hipStream_t st) {
+  if (s.M > 1 && cdiv(s.N, s.act == LIN_SWIGLU ? 16 : 32) >= 224) lin_skinny_rt<T, NG, 2>(s, X, W, ep, st);
+  else lin_skinny_rt<T, NG, 1>(s, X, W, ep, st);
 }
 template <typename T>
 static hipError_t lin_skinny(const LinShape& s, const void* X, const void* W, const LinEpi<T>& ep, hipStream_t st) {
@@ -684,67 +840,87 @@ static hipError_t lin_skinny(const LinShape& s, const void* X, const void* W, co
   return hipGetLastError();
 }
 
-hipError_t launch_linear(const LinShape& s, const void* X, const void* W, const float* bias, const void* residual,
-                         void* Z, void* out, void* ws, hipStream_t st) {
-  if (s.M == 0) return hipSuccess;
+template <typename T>
+static hipError_t lin_forward(const LinShape& s, const void* X, const void* W, const LinEpi<T>& ep, void* ws, hipStream_t st) {
+  if (lin_is_skinny(s)) return lin_skinny(s, X, W, ep, st);
   LinGemm g = lin_gemm(s, LIN_FWD);
   g.A = X;
   g.lda = s.ldx;
   g.B = W;
   g.ldb = s.K;
-  const LinEpi<bf16> eb = lin_epi<bf16>(bias, residual, s.ldr, Z, g.n, out, s.ldy, s.act);
-  const LinEpi<float> ef = lin_epi<float>(bias, residual, s.ldr, Z, g.n, out, s.ldy, s.act);
-  if (s.M <= LIN_SKINNY_M) return s.bf16 ? lin_skinny(s, X, W, eb, st) : lin_skinny(s, X, W, ef, st);
-  return lin_run<LIN_FWD>(s, g, static_cast<float*>(ws), eb, ef, st);
+  return lin_run<LIN_FWD>(g, static_cast<float*>(ws), ep, st);
 }
 
-hipError_t launch_linear_dz(const LinShape& s, const void* dY, const void* Z, float* dbias, void* ws, hipStream_t st) {
+hipError_t launch_linear(const LinShape& s, const void* X, const void* W, const float* bias, const void* residual,
+                         void* Z, void* out, void* ws, hipStream_t st) {
+  if (s.M == 0) return hipSuccess;
+  const int64_t NW = s.act == LIN_SWIGLU ? 2 * s.N : s.N;
+  if (s.bf16) return lin_forward<bf16>(s, X, W, lin_epi<bf16>(bias, residual, s.ldr, Z, NW, out, s.ldy, s.act), ws, st);
+  return lin_forward<float>(s, X, W, lin_epi<float>(bias, residual, s.ldr, Z, NW, out, s.ldy, s.act), ws, st);
+}
+
+template <typename T>
+static hipError_t lin_backward(const LinShape& s, const T* dY, const T* X, const T* W, const T* Z, T* dX, T* dW,
+                               float* dbias, void* ws, hipStream_t st) {
   LinBwdWs w;
   lin_carve_bwd(s, ws, &w);
+  const bool none = s.act == LIN_NONE;
   const int NW = (int)(s.act == LIN_SWIGLU ? 2 * s.N : s.N);
   const int rows = lin_dz_rows(s), blocks = (int)cdiv(s.M, rows);
-  if (s.M > 0 && (dbias || s.act != LIN_NONE)) {
-    const int grid = (int)(cdiv(s.N, 256) * blocks);
-    void* dZ = s.act == LIN_NONE ? nullptr : w.dZ;
-    float* db = dbias ? w.db_part : nullptr;
-    if (s.bf16)
-      k_lin_dz<bf16><<<grid, 256, 0, st>>>((const bf16*)dY, s.ldy, (const bf16*)Z, (int)s.M, (int)s.N, s.act, rows, (bf16*)dZ, db);
-    else
-      k_lin_dz<float><<<grid, 256, 0, st>>>((const float*)dY, s.ldy, (const float*)Z, (int)s.M, (int)s.N, s.act, rows, (float*)dZ, db);
+  if (s.M > 0 && (dbias || (!none && (dX || dW)))) {
+    k_lin_dz<T><<<(int)(cdiv(s.N, 256) * blocks), 256, 0, st>>>(dY, s.ldy, Z, (int)s.M, (int)s.N, s.act, rows,
+                                                               none || !(dX || dW) ? nullptr : static_cast<T*>(w.dZ),
+                                                               dbias ? w.db_part : nullptr);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
-  if (dbias) k_lin_db<<<(int)cdiv(NW, 32), 1024, 0, st>>>(w.db_part, blocks, NW, dbias);
-  return hipGetLastError();
+  LinGemm gx = lin_gemm(s, LIN_DX), gw = lin_gemm(s, LIN_DW);
+  gx.A = gw.A = none ? static_cast<const void*>(dY) : w.dZ;
+  gx.lda = gw.lda = none ? s.ldy : NW;
+  gx.B = W;
+  gw.B = X;
+  gx.ldb = s.K;
+  gw.ldb = s.ldx;
+  const LinEpi<T> ex = lin_epi<T>(nullptr, nullptr, 0, nullptr, 0, dX, s.ldx, LIN_NONE);
+  const LinEpi<T> ew = lin_epi<T>(nullptr, nullptr, 0, nullptr, 0, dW, s.K, LIN_NONE);
+  const LinDb db{w.db_part, blocks, NW, dbias};
+  // (the plan goes by the shape alone: a gradient asked for on its own has the pair's bits)
+  bool parts = false;
+  const bool pair = lin_pair_plan(s, gx, gw, &parts);
+  if (pair && dX && dW) {
+    gx.part = w.part;
+    gw.part = w.part_w;
+    const int nx = grid8((int64_t)gx.MT * gx.NT * gx.SK), nw = grid8((int64_t)gw.MT * gw.NT * gw.SK);
+    if (parts) k_lin_pair<T, LinMid, LIN_OUT_PART><<<nx + nw, LinMid::THREADS, 0, st>>>(gx, ex, nx, gw, ew);
+    else k_lin_pair<T, LinMid, LIN_OUT_EPI><<<nx + nw, LinMid::THREADS, 0, st>>>(gx, ex, nx, gw, ew);
+    hipError_t e = hipGetLastError();
+    if (e != hipSuccess || (!parts && !dbias)) return e;
+    const int fx = parts ? (int)cdiv((int64_t)gx.m * (gx.n / 4), 256) : 0, fw = parts ? (int)cdiv((int64_t)gw.m * (gw.n / 4), 256) : 0;
+    k_lin_finish_pair<T><<<fx + fw + (dbias ? (int)cdiv(NW, 32) : 0), 256, 0, st>>>(gx, ex, fx, gw, ew, fw, db);
+    return hipGetLastError();
+  }
+  if (dbias) k_lin_db<<<(int)cdiv(NW, 32), 256, 0, st>>>(db.part, db.blocks, db.np, db.db);
+  hipError_t e = hipGetLastError();
+  if (e == hipSuccess && dX) e = lin_run<LIN_DX>(gx, w.part, ex, st);
+  if (e == hipSuccess && dW) e = lin_run<LIN_DW>(gw, parts ? w.part_w : w.part, ew, st);
+  return e;
 }
 
-hipError_t launch_linear_dx(const LinShape& s, const void* dY, const void* W, void* dX, void* ws, hipStream_t st) {
-  LinBwdWs w;
-  lin_carve_bwd(s, ws, &w);
-  LinGemm g = lin_gemm(s, LIN_DX);
-  g.A = s.act == LIN_NONE ? dY : w.dZ;
-  g.lda = s.act == LIN_NONE ? s.ldy : g.red;
-  g.B = W;
-  g.ldb = s.K;
-  return lin_run<LIN_DX>(s, g, w.part, lin_epi<bf16>(nullptr, nullptr, 0, nullptr, 0, dX, s.ldx, LIN_NONE),
-                         lin_epi<float>(nullptr, nullptr, 0, nullptr, 0, dX, s.ldx, LIN_NONE), st);
+hipError_t launch_linear_bwd(const LinShape& s, const void* dY, const void* X, const void* W, const void* Z, void* dX,
+                             void* dW, float* dbias, void* ws, hipStream_t st) {
+  if (s.bf16)
+    return lin_backward<bf16>(s, static_cast<const bf16*>(dY), static_cast<const bf16*>(X), static_cast<const bf16*>(W),
+                              static_cast<const bf16*>(Z), static_cast<bf16*>(dX), static_cast<bf16*>(dW), dbias, ws, st);
+  return lin_backward<float>(s, static_cast<const float*>(dY), static_cast<const float*>(X), static_cast<const float*>(W),
+                             static_cast<const float*>(Z), static_cast<float*>(dX), static_cast<float*>(dW), dbias, ws, st);
 }
 
-hipError_t launch_linear_dw(const LinShape& s, const void* dY, const void* X, void* dW, void* ws, hipStream_t st) {
-  LinBwdWs w;
-  lin_carve_bwd(s, ws, &w);
-  LinGemm g = lin_gemm(s, LIN_DW);
-  g.A = s.act == LIN_NONE ? dY : w.dZ;
-  g.lda = s.act == LIN_NONE ? s.ldy : g.m;
-  g.B = X;
-  g.ldb = s.ldx;
-  return lin_run<LIN_DW>(s, g, w.part, lin_epi<bf16>(nullptr, nullptr, 0, nullptr, 0, dW, s.K, LIN_NONE),
-                         lin_epi<float>(nullptr, nullptr, 0, nullptr, 0, dW, s.K, LIN_NONE), st);
+template <typename T>
+static hipError_t lin_logit_dx(LinGemm g, const Shape& s, void* dX, hipStream_t st) {
+  return lin_run<LIN_DX>(g, nullptr, lin_epi<T>(nullptr, dX, s.d, nullptr, 0, dX, s.d, LIN_NONE), st);
 }
 
 hipError_t launch_logit_dx(const Shape& s, const void* dL, int E_pad, const void* W_r, void* dX, hipStream_t st) {
-  LinShape ls{};
-  ls.bf16 = s.bf16;
   LinGemm g{};
   g.A = dL;
   g.lda = E_pad;
@@ -755,8 +931,7 @@ hipError_t launch_logit_dx(const Shape& s, const void* dL, int E_pad, const void
   g.red = E_pad;
   g.bred = s.E;
   lin_plan(g, s.bf16, false);
-  return lin_run<LIN_DX>(ls, g, nullptr, lin_epi<bf16>(nullptr, dX, s.d, nullptr, 0, dX, s.d, LIN_NONE),
-                         lin_epi<float>(nullptr, dX, s.d, nullptr, 0, dX, s.d, LIN_NONE), st);
+  return s.bf16 ? lin_logit_dx<bf16>(g, s, dX, st) : lin_logit_dx<float>(g, s, dX, st);
 }
 
 }  // namespace moe

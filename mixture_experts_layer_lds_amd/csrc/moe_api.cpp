@@ -833,9 +833,8 @@ moe_status moe_linear_backward(const moe_linear_dims* dims, const void* dY, cons
   MOE_TRY(opt_ptr(dbias, "dbias"));
   MOE_TRY(check_linear_ws(linear_bwd_workspace_bytes(s), ws, ws_bytes));
   hipStream_t st = static_cast<hipStream_t>(stream);
-  MOE_STAGE(MOE_STAGE_LINEAR_BWD, st, launch_linear_dz(s, dY, Z, dbias, ws, st), "linear dZ");
-  if (dX && s.M > 0) MOE_STAGE(MOE_STAGE_LINEAR_BWD, st, launch_linear_dx(s, dY, W, dX, ws, st), "linear dX GEMM");
-  if (dW) MOE_STAGE(MOE_STAGE_LINEAR_BWD, st, launch_linear_dw(s, dY, X, dW, ws, st), "linear dW GEMM");
+  MOE_STAGE(MOE_STAGE_LINEAR_BWD, st,
+            launch_linear_bwd(s, dY, X, W, Z, s.M > 0 ? dX : nullptr, dW, dbias, ws, st), "linear backward");
   return MOE_OK;
 }
 

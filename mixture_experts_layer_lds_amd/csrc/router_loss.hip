@@ -165,17 +165,32 @@ struct RlRow {
     }
   }
 };
-template <int G>
-__device__ __forceinline__ float rl_group_sum(float v) {
-#pragma unroll
-  for (int o = G / 2; o > 0; o >>= 1) v += __shfl_xor(v, o, 64);
+// Exchange within aligned groups of 2, 4, 8 and 16 lanes by DPP (quad permutations, then mirrors of
+// half rows and rows, whose lanes already agree), between 16-lane rows by shuffles: an add with a
+// DPP operand costs a few cycles, a shuffle an LDS round trip, and these chains are what a token's
+// softmax waits for.
+template <int CTRL>
+__device__ __forceinline__ float rl_dpp(float v) {
+  const int i = __float_as_int(v);
+  return __int_as_float(__builtin_amdgcn_update_dpp(i, i, CTRL, 0xf, 0xf, true));
+}
+template <int G, class Op>
+__device__ __forceinline__ float rl_group(float v, Op op) {
+  if (G >= 2) v = op(v, rl_dpp<0xB1>(v));    // quad_perm [1, 0, 3, 2]
+  if (G >= 4) v = op(v, rl_dpp<0x4E>(v));    // quad_perm [2, 3, 0, 1]
+  if (G >= 8) v = op(v, rl_dpp<0x141>(v));   // row_half_mirror
+  if (G >= 16) v = op(v, rl_dpp<0x140>(v));  // row_mirror
+  if (G >= 32) v = op(v, __shfl_xor(v, 16, 64));
+  if (G >= 64) v = op(v, __shfl_xor(v, 32, 64));
   return v;
 }
 template <int G>
+__device__ __forceinline__ float rl_group_sum(float v) {
+  return rl_group<G>(v, [](float a, float b) { return a + b; });
+}
+template <int G>
 __device__ __forceinline__ float rl_group_max(float v) {
-#pragma unroll
-  for (int o = G / 2; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor(v, o, 64));
-  return v;
+  return rl_group<G>(v, [](float a, float b) { return fmaxf(a, b); });
 }
 
 // Where the sums end up.
@@ -188,8 +203,8 @@ struct RlossOut {
 
 constexpr int RL_RUNS = RL_THREADS / RL_JOIN_COLS;
 struct RlJoinLds {
-  double p[RL_RUNS][RL_JOIN_COLS + 1];
-  int c[RL_RUNS][RL_JOIN_COLS + 1];
+  double p[RL_WAVES][RL_JOIN_COLS];
+  int c[RL_WAVES][RL_JOIN_COLS];
   double z[RL_WAVES], b[RL_WAVES];
   long long n[RL_WAVES];
   int last;
@@ -200,8 +215,8 @@ __device__ __forceinline__ void rl_write_loss(const RlossOut& o, int E, int K, d
   o.loss[1] = n ? (float)(z / (double)n) : 0.0f;
 }
 
-// Adds sequence s's slots for columns block cb in chunk order: 32 columns by 32 runs of chunks, then
-// the runs in order.  Also the sequence's tokens and z sum when cb is 0.
+// Adds sequence s's slots for columns block cb in a fixed order: 32 columns by 32 runs of chunks, then
+// the runs by waves (two each).  Also the sequence's tokens and z sum when cb is 0.
 __device__ __forceinline__ void rl_join(RlJoinLds& L, int s, int cb, int chunk, int T, int E,
                                         const int32_t* __restrict__ seq_off, const RlossWs& w, const RlossOut& o) {
   const int cbs = (E + RL_JOIN_COLS - 1) / RL_JOIN_COLS;
@@ -220,8 +235,12 @@ __device__ __forceinline__ void rl_join(RlJoinLds& L, int s, int cb, int chunk, 
       cnt += w.cnt[i];
     }
   }
-  L.p[run][ci] = p;
-  L.c[run][ci] = cnt;
+  p += __shfl_xor(p, 32, 64);
+  cnt += __shfl_xor(cnt, 32, 64);
+  if (lane < 32) {
+    L.p[wave][ci] = p;
+    L.c[wave][ci] = cnt;
+  }
   if (cb == 0) {
     double z = 0.0;
     long long n = 0;
@@ -243,8 +262,8 @@ __device__ __forceinline__ void rl_join(RlJoinLds& L, int s, int cb, int chunk, 
   if (threadIdx.x < RL_JOIN_COLS) {
     double ps = 0.0;
     int cs = 0;
-#pragma unroll 8
-    for (int r = 0; r < RL_RUNS; ++r) {
+#pragma unroll
+    for (int r = 0; r < RL_WAVES; ++r) {
       ps += L.p[r][ci];
       cs += L.c[r][ci];
     }
@@ -409,8 +428,8 @@ __global__ __launch_bounds__(RL_THREADS) void k_rloss_part(const float* __restri
       if (grp == 0 && Row::col(li, k) < E) rl_lds[wave * E + Row::col(li, k)] = acc[k];
     }
     // every lane of a group holds its tokens' count and z: take one lane per group
-    z = wave_sum(li == 0 ? z : 0.0f);
-    n = wave_sum_i(li == 0 ? n : 0);
+    z = rl_group_sum<64>(li == 0 ? z : 0.0f);
+    n = (int)rl_group_sum<64>(li == 0 ? (float)n : 0.0f);
     if (lane == 0) {
       sz[wave] = z;
       sn[wave] = n;
