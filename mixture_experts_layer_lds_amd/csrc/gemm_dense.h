@@ -39,8 +39,11 @@ template <typename T> struct DnMma;
 template <> struct DnMma<bf16> {
   typedef bf16x8 frag;
   __device__ static f32x4 mma(frag a, frag b, f32x4 c) { return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0); }
-  // swizzle of k-row k of an MN-major operand
-  __device__ static int swz(int k) { return (4 * (k & 3)) ^ (2 * ((k >> 3) & 1)); }
+  // swizzle of k-row k of an MN-major operand of PITCH bytes per k-row (128: two rows to 256 bytes)
+  template <int PITCH>
+  __device__ static int swz(int k) {
+    return PITCH == 128 ? (2 * ((k >> 1) & 1)) ^ (4 * ((k >> 3) & 1)) : (4 * (k & 3)) ^ (2 * ((k >> 3) & 1));
+  }
 };
 template <> struct DnMma<float> {
   typedef f32x4 frag;
@@ -49,6 +52,7 @@ template <> struct DnMma<float> {
     for (int i = 0; i < 4; ++i) c = __builtin_amdgcn_mfma_f32_16x16x4f32(a[i], b[i], c, 0, 0, 0);
     return c;
   }
+  template <int PITCH>
   __device__ static int swz(int k) { return 4 * ((k >> 2) & 3); }
 };
 
@@ -126,7 +130,7 @@ struct DnMN {
     ld = ldb;
 #pragma unroll
     for (int q = 0; q < 2; ++q) {
-      const int chunk = (lane % LPR) ^ DnMma<T>::swz(kl + q * NW * RPI);
+      const int chunk = (lane % LPR) ^ DnMma<T>::template swz<PITCH>(kl + q * NW * RPI);
       off[q] = (uint32_t)(kl * ldb) + min(chunk * 16, cols * SZ - 16);
     }
     klen = klen_;
@@ -144,10 +148,10 @@ struct DnMN {
     const int lane = threadIdx.x & 63, i = lane & 15, g = lane >> 4;
     if constexpr (SZ == 2) {
       const int k = g * 8 + (i >> 2), mn = mn0 + 4 * (i & 3);
-      return k * PITCH + ((mn >> 3) ^ DnMma<T>::swz(k)) * 16 + (mn & 7) * 2;
+      return k * PITCH + ((mn >> 3) ^ DnMma<T>::template swz<PITCH>(k)) * 16 + (mn & 7) * 2;
     } else {
       const int k = g * 4, mn = mn0 + i;
-      return k * PITCH + ((mn >> 2) ^ DnMma<T>::swz(k)) * 16 + (mn & 3) * 4;
+      return k * PITCH + ((mn >> 2) ^ DnMma<T>::template swz<PITCH>(k)) * 16 + (mn & 3) * 4;
     }
   }
   __device__ static Frag frag(const char* t, uint32_t base, int at, int ks) {
@@ -208,8 +212,8 @@ __device__ __forceinline__ void dn_read_b(const char* slot, int ks, const DnLds&
   for (int j = 0; j < 4; ++j) F.f[j] = BL::frag(slot + TI::A_BYTES, d.b, (j >> 1) * TI::HC + (j & 1) * 16, ks);
 }
 
-// The 4 MH MFMAs of one half k-step, FROM .. TO - 1 of them, with DMA instructions N0 .. N1 - 1
-// spread between them.
+// The 4 MH MFMA blocks of one half k-step, FROM .. TO - 1 of them, with DMA instructions N0 ..
+// N1 - 1 spread between them.
 template <class TI, int HALF, int FROM, int TO, int N0 = 0, int N1 = 0, class Frag, class Issue>
 __device__ __forceinline__ void dn_mma(const DnFragA<TI, Frag>& A, const DnFragB<Frag>& B, DnAcc<TI::MI>& acc, Issue issue) {
   typedef DnMma<typename std::conditional<std::is_same<Frag, bf16x8>::value, bf16, float>::type> M;

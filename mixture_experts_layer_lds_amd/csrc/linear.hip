@@ -102,7 +102,7 @@ struct LinGemm {
   int64_t ldb;
   int m, n, red, bred;
   int MT, NT, SK, klen;  // tiles, slices and values of k per slice (a multiple of 64; fp32: 32)
-  int mid;               // bf16: 128 x 128 tiles
+  int tile;              // LIN_BIG, LIN_MID or LIN_SMALL
   float* part;           // [SK][m][n] when the output goes there
 };
 
@@ -132,23 +132,23 @@ template <typename T> __device__ __forceinline__ void lin_st8(T* p, const float*
 }
 
 // Walks the staged half: row(r, c, f, res) with 8 fp32 values f of tile row r, columns c .., and 8
-// of the residual (zeros without one).  Rows go in batches of four whose residual chunks are
+// of the residual (zeros without one).  Rows go in batches of KB whose residual chunks are
 // requested together; res_row(r) is row r's residual at the half's first column.
 template <class TI, typename T, class ResRow, class Row>
 __device__ __forceinline__ void lin_walk(char* b0, char* b1, int mrows, int valid, bool has_res, ResRow res_row, Row row) {
-  constexpr int NV = 8 / Vec<T>::N;
+  constexpr int NV = 8 / Vec<T>::N, KB = TI::TM_ / 32 < 4 ? TI::TM_ / 32 : 4;
   const int c = (threadIdx.x % (TI::HC / 8)) * 8, r0 = threadIdx.x / (TI::HC / 8);
   if (c >= valid) return;
 #pragma unroll
-  for (int k0 = 0; k0 < TI::TM_ / 32; k0 += 4) {
-    u32x4 rv[4][NV];
+  for (int k0 = 0; k0 < TI::TM_ / 32; k0 += KB) {
+    u32x4 rv[KB][NV];
 #pragma unroll
-    for (int k = 0; k < 4; ++k)
+    for (int k = 0; k < KB; ++k)
 #pragma unroll
       for (int v = 0; v < NV; ++v)
         rv[k][v] = has_res ? ld16_nt(res_row(min(r0 + 32 * (k0 + k), mrows - 1)) + c + v * Vec<T>::N) : u32x4{0u, 0u, 0u, 0u};
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
+    for (int k = 0; k < KB; ++k) {
       const int r = r0 + 32 * (k0 + k);
       const char* p = lin_frow<TI>(b0, b1, r) + c * 4;
       const f32x4 a = *reinterpret_cast<const f32x4*>(p), b = *reinterpret_cast<const f32x4*>(p + 16);
@@ -622,48 +622,66 @@ __global__ __launch_bounds__(256) void k_lin_dz(const T* __restrict__ dY, int64_
 // ---------------------------------------------------------------------------------------------
 // Host side
 // ---------------------------------------------------------------------------------------------
-// The tiles: 256 x 256 on eight waves (bf16), and 128 x 128 on four, two workgroups per CU.
+// The tiles: 256 x 256 on eight waves (bf16), 128 x 128 on four with two workgroups per CU, and
+// 64 x 64 on two with up to five.
+enum { LIN_BIG = 256, LIN_MID = 128, LIN_SMALL = 64 };
 typedef DnTile<256, 256, 2, 4> LinBig;
 typedef DnTile<128, 128, 2, 2> LinMid;
+typedef DnTile<64, 64, 2, 1> LinSmall;
 
 // Tile size and slices of a product's reduction: the cheapest by a model of the time in
-// microseconds.  A round of 256 large tiles takes 1.4 per stage and 10 besides; 128 x 128 tiles
-// take 0.5 per stage where every CU has one (0.8 in the backward's pair, whose operands are read
-// with their rows along the reduction) and 0.95 where it has two, and 4 besides; an fp32 stage 1.9
-// and 3.6.  Slices cost a second launch (2.5) and 1.2 per million partial products written and read
-// back (fp32, whose stores pass beside longer stages, 0.4).  Measured (4096 x 4096 weights, bf16): 64 rows 13.6 us with 8 slices, 16.9 with 16, 30
-// with one; 256 rows 20.9 with 4, 31 with one; 512 rows 29 with 2, 32 with one; 1024 rows 36 with
-// one; 2048 rows 66 on the small tile.
+// microseconds, fitted to measured times.  A round of 256 large tiles takes 1.4 per stage and 10
+// besides.  The smaller tiles take 4 besides and per stage: 128 x 128 0.5 where every CU has one
+// workgroup and 0.95 where it has two; 64 x 64 0.29, and 0.165 per workgroup of the CU beyond that;
+// where an operand is read with its rows along the reduction in a launch of two products 0.8 and
+// 0.45 at least.  In fp32 a stage takes 2.05 and 3.8, or 1.05, 2.0 and 0.61 per workgroup (and
+// 128 x 128 tiles 5.5 besides).  Slices cost a second launch (2.5) and 1.2 per million partial
+// products written and read back.  Measured (4096 x 4096 weights, bf16; 64 x 64 | 128 x 128 tiles):
+// 64 rows 12.4 us with 4 slices, 22.1 with one | 13.6 with 8, 30 with one; 256 rows 20.4 with 2 |
+// 19.9 with 4, 31.7 with one; 300 x 512 x 512 6.0 | 8.7; 100 x 4096 x 512 fp32 15.2 with 2 | 18.1
+// with 6; 1237 x 904 x 1544 fp32 47 with 3 | 46 with 3, 104 with one.
 constexpr int kLinSlices[] = {1, 2, 3, 4, 6, 8, 12, 16, 24, 32};
 static int lin_stages(const LinGemm& g, bool bf16_) { return (int)cdiv(g.red, bf16_ ? dn_bk<bf16>() : dn_bk<float>()); }
-static int64_t lin_mid_tiles(const LinGemm& g) { return cdiv(g.m, 128) * cdiv(g.n, 128); }
-// Model of 128 x 128 tiles: wgs workgroups of `stages` stages, out partial products in all.
-static double lin_mid_time(int64_t wgs, int64_t stages, double out, bool bf16_, bool pair) {
-  const double stage = bf16_ ? (wgs > 256 ? 0.95 : (pair ? 0.8 : 0.5)) : (wgs > 256 ? 3.6 : 1.9);
-  const double rounds = wgs <= 512 ? 1.0 : wgs / 512.0;
-  return rounds * (stages * stage + 4.0) + (out > 0 ? 2.5 + (bf16_ ? 1.2e-6 : 0.4e-6) * out : 0.0);
+static int64_t lin_tiles(const LinGemm& g, int tile) { return cdiv(g.m, tile) * cdiv(g.n, tile); }
+// wgs workgroups of `stages` stages on tiles below the largest, out partial products in all.
+static double lin_time(int tile, int64_t wgs, int64_t stages, double out, bool bf16_, bool pair) {
+  const double per = wgs / 256.0;  // workgroups per CU
+  double stage, most;              // per stage; workgroups that a CU holds
+  const double besides = !bf16_ && tile == LIN_MID ? 5.5 : 4.0;
+  if (tile == LIN_MID) {
+    stage = bf16_ ? (per > 1 ? 0.95 : (pair ? 0.8 : 0.5)) : (per > 1 ? 3.8 : 2.05);
+    most = 2;
+  } else {
+    const double share = bf16_ ? 0.165 : 0.61, least = bf16_ ? (pair ? 0.45 : 0.29) : (per > 1 ? 2.0 : 1.05);
+    stage = share * per > least ? share * per : least;
+    most = 5;
+    if (per > most) stage = share * most;
+  }
+  const double rounds = per <= most ? 1.0 : per / most;
+  return rounds * (stages * stage + besides) + (out > 0 ? 2.5 + 1.2e-6 * out : 0.0);
 }
-static void lin_set(LinGemm& g, bool bf16_, int mid, int sk) {
-  g.mid = mid;
-  g.MT = (int)cdiv(g.m, mid ? 128 : 256);
-  g.NT = (int)cdiv(g.n, mid ? 128 : 256);
+static void lin_set(LinGemm& g, bool bf16_, int tile, int sk) {
+  g.tile = tile;
+  g.MT = (int)cdiv(g.m, tile);
+  g.NT = (int)cdiv(g.n, tile);
   g.klen = (int)cdiv(lin_stages(g, bf16_), sk) * (bf16_ ? dn_bk<bf16>() : dn_bk<float>());
   g.SK = g.red > 0 ? (int)cdiv(g.red, g.klen) : 1;
 }
 static void lin_plan(LinGemm& g, bool bf16_, bool may_split) {
   const int stages = lin_stages(g, bf16_);
-  double best = bf16_ ? cdiv(cdiv(g.m, 256) * cdiv(g.n, 256), 256) * (stages * 1.4 + 10.0) : 1e30;
-  int mid = 0, sk = 1;
-  for (int q : kLinSlices) {
-    if (q > 1 && (!may_split || q > stages)) break;
-    const double t = lin_mid_time(lin_mid_tiles(g) * q, cdiv(stages, q), q > 1 ? (double)q * g.m * g.n : 0.0, bf16_, false);
-    if (t < best) {
-      best = t;
-      mid = 1;
-      sk = q;
+  double best = bf16_ ? cdiv(lin_tiles(g, LIN_BIG), 256) * (stages * 1.4 + 10.0) : 1e30;
+  int tile = LIN_BIG, sk = 1;
+  for (int t : {LIN_MID, LIN_SMALL})
+    for (int q : kLinSlices) {
+      if (q > 1 && (!may_split || q > stages)) break;
+      const double us = lin_time(t, lin_tiles(g, t) * q, cdiv(stages, q), q > 1 ? (double)q * g.m * g.n : 0.0, bf16_, false);
+      if (us < best) {
+        best = us;
+        tile = t;
+        sk = q;
+      }
     }
-  }
-  lin_set(g, bf16_, mid, sk);
+  lin_set(g, bf16_, tile, sk);
 }
 
 // Rows per workgroup of k_lin_dz: 64 where that gives four workgroups per CU, fewer (at least 8) for
@@ -708,26 +726,27 @@ size_t linear_fwd_workspace_bytes(const LinShape& s) {
   return g.SK > 1 ? lin_part_bytes(g) : 0;
 }
 
-// The backward's two products where both are small: 128 x 128 tiles of both side by side in one
-// launch, the same number of slices for each (999 x 1000 x 264, ReLU with a bias: 26 us in six
+// The backward's two products where both are small: their tiles side by side in one launch, the same number of slices for each (999 x 1000 x 264, ReLU with a bias: 26 us in six
 // launches, 20 in three; 25.9 unsliced, 20.8 with 2, 20.2 with 3, 24.8 with 8).  False: they are launched one after the other, each with a plan of its own.
 static bool lin_pair_plan(const LinShape& s, LinGemm& gx, LinGemm& gw, bool* parts) {
-  const int64_t tiles = lin_mid_tiles(gx) + lin_mid_tiles(gw);
-  if (s.M == 0 || tiles > 256) return false;
-  const int sx = lin_stages(gx, s.bf16), sw = lin_stages(gw, s.bf16), most = sx > sw ? sx : sw;
+  if (s.M == 0 || lin_tiles(gx, LIN_MID) + lin_tiles(gw, LIN_MID) > 256) return false;
+  const int sx = lin_stages(gx, s.bf16), sw = lin_stages(gw, s.bf16), longest = sx > sw ? sx : sw;
   const double out = (double)gx.m * gx.n + (double)gw.m * gw.n;
   double best = 1e30;
-  int sk = 1;
-  for (int q : kLinSlices) {
-    if (q > most) break;
-    const double t = lin_mid_time(tiles * q, cdiv(most, q), q > 1 ? q * out : 0.0, s.bf16, true);
-    if (t < best) {
-      best = t;
-      sk = q;
+  int tile = LIN_MID, sk = 1;
+  for (int t : {LIN_MID, LIN_SMALL})
+    for (int q : kLinSlices) {
+      if (q > longest) break;
+      const int64_t wgs = (lin_tiles(gx, t) + lin_tiles(gw, t)) * q;
+      const double us = lin_time(t, wgs, cdiv(longest, q), q > 1 ? q * out : 0.0, s.bf16, true);
+      if (us < best) {
+        best = us;
+        tile = t;
+        sk = q;
+      }
     }
-  }
-  lin_set(gx, s.bf16, 1, sk < sx ? sk : sx);
-  lin_set(gw, s.bf16, 1, sk < sw ? sk : sw);
+  lin_set(gx, s.bf16, tile, sk < sx ? sk : sx);
+  lin_set(gw, s.bf16, tile, sk < sw ? sk : sw);
   *parts = sk > 1;
   return true;
 }
@@ -775,9 +794,9 @@ static void lin_launch_t(const LinGemm& g, const LinEpi<T>& ep, hipStream_t st) 
 }
 template <int MODE, int OUT, typename T>
 static void lin_launch(const LinGemm& g, const LinEpi<T>& ep, hipStream_t st) {
-  if constexpr (sizeof(T) == 4) lin_launch_t<T, LinMid, MODE, OUT>(g, ep, st);
-  else if (g.mid) lin_launch_t<T, LinMid, MODE, OUT>(g, ep, st);
-  else if constexpr (OUT != LIN_OUT_PART) lin_launch_t<T, LinBig, MODE, OUT>(g, ep, st);  // never sliced
+  if (g.tile == LIN_SMALL) lin_launch_t<T, LinSmall, MODE, OUT>(g, ep, st);
+  else if (g.tile == LIN_MID) lin_launch_t<T, LinMid, MODE, OUT>(g, ep, st);
+  else if constexpr (sizeof(T) == 2 && OUT != LIN_OUT_PART) lin_launch_t<T, LinBig, MODE, OUT>(g, ep, st);  // never sliced
 }
 
 // A product whose epilogue is ep: directly, or through partial products where it is sliced.
@@ -788,7 +807,7 @@ static hipError_t lin_run(LinGemm g, float* part, const LinEpi<T>& ep, hipStream
     if constexpr (MODE == LIN_FWD) {
       if (ep.act == LIN_SWIGLU) {
         g.n /= 2;
-        g.NT = (int)cdiv(g.n, g.mid ? 64 : 128);
+        g.NT = (int)cdiv(g.n, g.tile / 2);
         lin_launch<MODE, LIN_OUT_GLU>(g, ep, st);
         return hipGetLastError();
       }
@@ -859,6 +878,13 @@ hipError_t launch_linear(const LinShape& s, const void* X, const void* W, const 
   return lin_forward<float>(s, X, W, lin_epi<float>(bias, residual, s.ldr, Z, NW, out, s.ldy, s.act), ws, st);
 }
 
+template <typename T, class TI>
+static void lin_pair_launch(const LinGemm& gx, const LinEpi<T>& ex, int nx, const LinGemm& gw, const LinEpi<T>& ew, int nw,
+                            bool parts, hipStream_t st) {
+  if (parts) k_lin_pair<T, TI, LIN_OUT_PART><<<nx + nw, TI::THREADS, 0, st>>>(gx, ex, nx, gw, ew);
+  else k_lin_pair<T, TI, LIN_OUT_EPI><<<nx + nw, TI::THREADS, 0, st>>>(gx, ex, nx, gw, ew);
+}
+
 template <typename T>
 static hipError_t lin_backward(const LinShape& s, const T* dY, const T* X, const T* W, const T* Z, T* dX, T* dW,
                                float* dbias, void* ws, hipStream_t st) {
@@ -891,8 +917,8 @@ static hipError_t lin_backward(const LinShape& s, const T* dY, const T* X, const
     gx.part = w.part;
     gw.part = w.part_w;
     const int nx = grid8((int64_t)gx.MT * gx.NT * gx.SK), nw = grid8((int64_t)gw.MT * gw.NT * gw.SK);
-    if (parts) k_lin_pair<T, LinMid, LIN_OUT_PART><<<nx + nw, LinMid::THREADS, 0, st>>>(gx, ex, nx, gw, ew);
-    else k_lin_pair<T, LinMid, LIN_OUT_EPI><<<nx + nw, LinMid::THREADS, 0, st>>>(gx, ex, nx, gw, ew);
+    if (gx.tile == LIN_SMALL) lin_pair_launch<T, LinSmall>(gx, ex, nx, gw, ew, nw, parts, st);
+    else lin_pair_launch<T, LinMid>(gx, ex, nx, gw, ew, nw, parts, st);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess || (!parts && !dbias)) return e;
     const int fx = parts ? (int)cdiv((int64_t)gx.m * (gx.n / 4), 256) : 0, fw = parts ? (int)cdiv((int64_t)gw.m * (gw.n / 4), 256) : 0;
