@@ -193,6 +193,17 @@ __device__ __forceinline__ float rl_group_max(float v) {
   return rl_group<G>(v, [](float a, float b) { return fmaxf(a, b); });
 }
 
+// What one workgroup of the joining launch leaves for the last: stored and loaded past the caches of
+// the XCDs (agent scope), so that no cache has to be written back or invalidated as a whole.
+template <typename V>
+__device__ __forceinline__ void rl_put(V* p, V v) {
+  __hip_atomic_store(p, v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+template <typename V>
+__device__ __forceinline__ V rl_get(const V* p) {
+  return __hip_atomic_load(p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+
 // Where the sums end up.
 struct RlossOut {
   int32_t* seq_tokens;
@@ -274,7 +285,7 @@ __device__ __forceinline__ void rl_join(RlJoinLds& L, int s, int cb, int chunk, 
     double bsum = e < E ? ps * (double)cs : 0.0;
 #pragma unroll
     for (int k = RL_JOIN_COLS / 2; k > 0; k >>= 1) bsum += __shfl_xor(bsum, k, 64);
-    if (threadIdx.x == 0) w.bal[(int64_t)s * cbs + cb] = bsum;
+    if (threadIdx.x == 0) rl_put(&w.bal[(int64_t)s * cbs + cb], bsum);
   }
   if (cb == 0 && threadIdx.x == 64) {
     double z = 0.0;
@@ -283,9 +294,11 @@ __device__ __forceinline__ void rl_join(RlJoinLds& L, int s, int cb, int chunk, 
       z += L.z[q];
       n += L.n[q];
     }
-    w.zs[s] = z;
-    o.seq_tokens[s] = (int)n;
+    rl_put(&w.zs[s], z);
+    rl_put(&o.seq_tokens[s], (int32_t)n);
   }
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup");
+  __builtin_amdgcn_s_waitcnt(0);  // this wave's stores have arrived
   __syncthreads();
 }
 
@@ -297,10 +310,10 @@ __device__ __forceinline__ void rl_losses(RlJoinLds& L, int E, int K, int n_seq,
   long long n = 0;
   for (int q = threadIdx.x; q < n_seq; q += RL_THREADS) {
     double bq = 0.0;
-    for (int k = 0; k < cbs; ++k) bq += w.bal[(int64_t)q * cbs + k];
-    const int tq = o.seq_tokens[q];
+    for (int k = 0; k < cbs; ++k) bq += rl_get(&w.bal[(int64_t)q * cbs + k]);
+    const int tq = rl_get(&o.seq_tokens[q]);
     if (tq > 0) bsum += bq / (double)tq;
-    zsum += w.zs[q];
+    zsum += rl_get(&w.zs[q]);
     n += tq;
   }
 #pragma unroll
@@ -354,6 +367,8 @@ __global__ __launch_bounds__(RL_THREADS) void k_rloss_part(const float* __restri
   }
   const int picks = (t_end - t_begin) * K;  // the chunk's choices, one per thread and round
   const int first = (int)threadIdx.x < picks ? topk_idx[(int64_t)t_begin * K + threadIdx.x] : -1;
+  const int first_t = t_begin + (int)threadIdx.x / K;
+  const bool first_live = !mask || ((int)threadIdx.x < picks && mask[first_t]);
   rl_table_load(tab, seq_off, n_seq, T);
   if (!ONE && blockIdx.x == 0 && threadIdx.x == 0) *w.ticket = 0u;
   for (int e = threadIdx.x; e < E; e += RL_THREADS) hist[e] = 0;
@@ -415,11 +430,11 @@ __global__ __launch_bounds__(RL_THREADS) void k_rloss_part(const float* __restri
         for (int k = 0; k < N; ++k) acc[k] += x[i][k];
       }
     }
-    for (int i = threadIdx.x, e = first; i < picks;) {
-      const int t = t_begin + i / K;
+    if ((int)threadIdx.x < picks && first_t >= a && first_t < b && (uint32_t)first < (uint32_t)E && first_live)
+      atomicAdd(&hist[first], 1);
+    for (int i = threadIdx.x + RL_THREADS; i < picks; i += RL_THREADS) {
+      const int t = t_begin + i / K, e = topk_idx[(int64_t)t_begin * K + i];
       if (t >= a && t < b && (uint32_t)e < (uint32_t)E && (!mask || mask[t])) atomicAdd(&hist[e], 1);
-      i += RL_THREADS;
-      if (i < picks) e = topk_idx[(int64_t)t_begin * K + i];
     }
 #pragma unroll
     for (int k = 0; k < N; ++k) {
@@ -492,13 +507,11 @@ __global__ __launch_bounds__(RL_THREADS) void k_rloss_join(int T, int E, int K, 
   const int cbs = (E + RL_JOIN_COLS - 1) / RL_JOIN_COLS;
   rl_join(L, blockIdx.x / cbs, blockIdx.x % cbs, chunk, T, E, seq_off, w, o);
   if (threadIdx.x == 0) {
-    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "agent");
     const unsigned v = __hip_atomic_fetch_add(w.ticket, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
     L.last = v == gridDim.x - 1;
   }
   __syncthreads();
   if (!L.last) return;
-  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "agent");
   rl_losses(L, E, K, n_seq, w, o);
 }
 
