@@ -28,11 +28,17 @@
 
 namespace moe {
 
-constexpr int RL_BWD_CHUNK = 64;  // tokens per workgroup of the backward
+constexpr int RL_BWD_CHUNK = 64;  // tokens per workgroup of the backward, less where T gives under two per CU
 constexpr int RL_THREADS = 1024;
 constexpr int RL_WAVES = RL_THREADS / 64;
 constexpr int RL_JOIN_COLS = 32;      // columns per workgroup of the joining launch
 constexpr int RL_BWD_THREADS = 256;
+// A chunk of more than RL_FEW pieces leaves those of up to RL_SHORT rounds of a wave's tokens to single
+// waves: a piece that the whole workgroup takes costs two to three barriers and as many LDS round
+// trips whatever its length (35 tokens of 379 logits in 46 sequences: 84 us so, 21 by waves; 64 x 128 in
+// 64: 130 against 17).
+constexpr int RL_FEW = 3;
+constexpr int RL_SHORT = 8;
 
 struct RlossWs {
   unsigned* ticket;  // workgroups of the joining launch that have finished
@@ -96,16 +102,24 @@ __device__ __forceinline__ int rl_off(const int32_t* seq_off, int s, int T) {
   return seq_off ? min(max(seq_off[s], 0), T) : (s ? T : 0);
 }
 
-// The piece of a chunk that starts at token t: its sequence (-1: outside all of them) and its end,
-// at most `end`.  off(s) gives the table's entries.
+// The first sequence from lo on that ends after token t (n_seq: none).  off(s) gives the table's
+// entries.
 template <class Off>
-__device__ __forceinline__ int rl_piece(Off off, int n_seq, int t, int end, int& stop) {
-  int lo = 0, hi = n_seq;  // the first s with off(s + 1) > t
+__device__ __forceinline__ int rl_find(Off off, int n_seq, int t, int lo) {
+  int hi = n_seq;
+  if (lo < hi && off(lo + 1) > t) return lo;
   while (lo < hi) {
     const int mid = (lo + hi) >> 1;
     if (off(mid + 1) > t) hi = mid;
     else lo = mid + 1;
   }
+  return lo;
+}
+// The piece of a chunk that starts at token t: its sequence (-1: outside all of them) and its end,
+// at most `end`.  lo: a sequence that does not lie behind t; left at the one found.
+template <class Off>
+__device__ __forceinline__ int rl_piece(Off off, int n_seq, int t, int end, int& stop, int& lo) {
+  lo = rl_find(off, n_seq, t, lo);
   if (lo >= n_seq) {
     stop = end;
     return -1;
@@ -117,6 +131,24 @@ __device__ __forceinline__ int rl_piece(Off off, int n_seq, int t, int end, int&
   }
   stop = min(end, max(off(lo + 1), t + 1));
   return lo;
+}
+
+// The next piece of more than `least` tokens from token a on, among the sequences s0 .. s1 of a
+// chunk: a wave looks at 64 sequences at once.  Its sequence (-1: none), a and b.
+template <class Off>
+__device__ __forceinline__ int rl_long_piece(Off off, int s0, int s1, int begin, int end, int least, int& a, int& b) {
+  for (int base = s0; base <= s1; base += 64) {
+    const int s = base + (int)(threadIdx.x & 63), c = min(s, s1);
+    const int lo = max(off(c), begin), hi = min(off(c + 1), end);
+    const uint64_t hit = __builtin_amdgcn_ballot_w64(s <= s1 && lo >= a && hi - lo > least);
+    if (hit) {
+      const int l = __builtin_ctzll(hit);
+      a = __shfl(lo, l, 64);
+      b = __shfl(hi, l, 64);
+      return base + l;
+    }
+  }
+  return -1;
 }
 
 // The sequence table in LDS where it fits, else read in place.
@@ -191,6 +223,31 @@ __device__ __forceinline__ float rl_group_sum(float v) {
 template <int G>
 __device__ __forceinline__ float rl_group_max(float v) {
   return rl_group<G>(v, [](float a, float b) { return fmaxf(a, b); });
+}
+
+// The softmax of a token's row in place; returns the log-sum-exp, and in l2 its square.  A row of
+// -infinity only (every expert masked) has no probabilities: its sum is zero, its log-sum-exp
+// -infinity, and it adds to neither loss; a NaN or +infinity makes the row NaN.
+template <int G, int N>
+__device__ __forceinline__ float rl_softmax(float (&x)[N], float& l2) {
+  float m = x[0];
+#pragma unroll
+  for (int k = 1; k < N; ++k) m = fmaxf(m, x[k]);
+  m = rl_group_max<G>(m);
+  m = m == -INFINITY ? 0.0f : m;
+  float sum = 0.0f;
+#pragma unroll
+  for (int k = 0; k < N; ++k) {
+    x[k] = rl_exp(x[k] - m);
+    sum += x[k];
+  }
+  sum = rl_group_sum<G>(sum);
+  const float l = m + __logf(sum);
+  const float inv = sum != 0.0f ? 1.0f / sum : 0.0f;
+  l2 = sum != 0.0f ? l * l : 0.0f;
+#pragma unroll
+  for (int k = 0; k < N; ++k) x[k] *= inv;
+  return l;
 }
 
 // What one workgroup of the joining launch leaves for the last: stored and loaded past the caches of
@@ -302,19 +359,21 @@ __device__ __forceinline__ void rl_join(RlJoinLds& L, int s, int cb, int chunk, 
   __syncthreads();
 }
 
-// The two losses from the sequences' sums (one workgroup).
-__device__ __forceinline__ void rl_losses(RlJoinLds& L, int E, int K, int n_seq, const RlossWs& w, const RlossOut& o) {
-  const int cbs = (E + RL_JOIN_COLS - 1) / RL_JOIN_COLS;
+// The two losses from the sequences' sums (one workgroup), cbs of them per sequence in w.bal.
+__device__ __forceinline__ void rl_losses(RlJoinLds& L, int E, int K, int n_seq, int cbs, const RlossWs& w, const RlossOut& o) {
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   double bsum = 0.0, zsum = 0.0;
   long long n = 0;
   for (int q = threadIdx.x; q < n_seq; q += RL_THREADS) {
+    const int tq = rl_get(&o.seq_tokens[q]);
     double bq = 0.0;
     for (int k = 0; k < cbs; ++k) bq += rl_get(&w.bal[(int64_t)q * cbs + k]);
-    const int tq = rl_get(&o.seq_tokens[q]);
-    if (tq > 0) bsum += bq / (double)tq;
-    zsum += rl_get(&w.zs[q]);
-    n += tq;
+    const double zq = rl_get(&w.zs[q]);
+    if (tq > 0) {  // (a sequence without tokens may have left no sums)
+      bsum += bq / (double)tq;
+      zsum += zq;
+      n += tq;
+    }
   }
 #pragma unroll
   for (int k = 32; k > 0; k >>= 1) {
@@ -386,35 +445,28 @@ __global__ __launch_bounds__(RL_THREADS) void k_rloss_part(const float* __restri
   float l2[STEPS];
 #pragma unroll
   for (int i = 0; i < STEPS; ++i) {
-    float m = x[i][0];
-#pragma unroll
-    for (int k = 1; k < N; ++k) m = fmaxf(m, x[i][k]);
-    m = rl_group_max<G>(m);
-    // a row of -infinity only (every expert masked) has no probabilities: its sum is zero, its
-    // log-sum-exp -infinity, and it adds to neither loss; a NaN or +infinity makes the row NaN
-    m = m == -INFINITY ? 0.0f : m;
-    float sum = 0.0f;
-#pragma unroll
-    for (int k = 0; k < N; ++k) {
-      x[i][k] = rl_exp(x[i][k] - m);
-      sum += x[i][k];
-    }
-    sum = rl_group_sum<G>(sum);
-    const float l = m + __logf(sum);
+    const float l = rl_softmax<G>(x[i], l2[i]);
     const int t = t_begin + (i * RL_WAVES + wave) * TPW + grp;
     if (li == 0 && t < t_end) lse[t] = l;
-    const float inv = sum != 0.0f ? 1.0f / sum : 0.0f;
-    l2[i] = sum != 0.0f ? l * l : 0.0f;
-#pragma unroll
-    for (int k = 0; k < N; ++k) x[i][k] *= inv;
   }
   __syncthreads();
   auto off = [&](int s) { return n_seq <= RL_TABLE ? tab.off[s] : rl_off(seq_off, s, T); };
   double bsum = 0.0, zsum = 0.0;  // ONE: thread 0's sums over the sequences
   long long nsum = 0;
+  // a chunk of many pieces: the workgroup takes the longer ones, its waves one short one each
+  const int s0 = __builtin_amdgcn_readfirstlane(rl_find(off, n_seq, t_begin, 0));
+  const bool many = n_seq - s0 > RL_FEW && off(s0 + RL_FEW) < t_end;
+  const int s1 = many ? __builtin_amdgcn_readfirstlane(min(rl_find(off, n_seq, t_end - 1, s0), n_seq - 1)) : s0;
+  int at = s0;
   for (int a = t_begin, b; a < t_end; a = b) {
-    const int s = rl_piece(off, n_seq, a, t_end, b);
-    if (s < 0) continue;  // (uniform) tokens outside every sequence only get their log-sum-exp
+    int s;
+    if (many) {
+      s = rl_long_piece(off, s0, s1, t_begin, t_end, RL_SHORT * TPW, a, b);
+      if (s < 0) break;
+    } else {
+      s = rl_piece(off, n_seq, a, t_end, b, at);
+      if (s < 0) continue;  // (uniform) tokens outside every sequence only get their log-sum-exp
+    }
     float acc[N];
 #pragma unroll
     for (int k = 0; k < N; ++k) acc[k] = 0.0f;
@@ -485,10 +537,16 @@ __global__ __launch_bounds__(RL_THREADS) void k_rloss_part(const float* __restri
         double bs = 0.0;
 #pragma unroll
         for (int q = 0; q < RL_WAVES; ++q) bs += sb[q];
-        o.seq_tokens[s] = ns;
-        if (ns > 0) bsum += bs / (double)ns;
-        zsum += (double)zs;
-        nsum += ns;
+        if (many) {
+          rl_put(&w.bal[s], bs);
+          rl_put(&w.zs[s], (double)zs);
+          rl_put(&o.seq_tokens[s], (int32_t)ns);
+        } else {
+          o.seq_tokens[s] = ns;
+          if (ns > 0) bsum += bs / (double)ns;
+          zsum += (double)zs;
+          nsum += ns;
+        }
       } else {
         w.z[slot] = zs;
         w.tok[slot] = ns;
@@ -496,7 +554,76 @@ __global__ __launch_bounds__(RL_THREADS) void k_rloss_part(const float* __restri
     }
     __syncthreads();  // the LDS is free for the next piece
   }
-  if (ONE && threadIdx.x == 0) rl_write_loss(o, E, K, bsum, zsum, nsum);
+  if (many) {
+    int* cnt = reinterpret_cast<int*>(rl_lds) + wave * E;  // the wave's own counts
+    for (int s = s0 + wave; s <= s1; s += RL_WAVES) {
+      const int a = __builtin_amdgcn_readfirstlane(max(off(s), t_begin)), b = __builtin_amdgcn_readfirstlane(min(off(s + 1), t_end));
+      if (b <= a || b - a > RL_SHORT * TPW) continue;
+      for (int e = lane; e < E; e += 64) cnt[e] = 0;
+      const int32_t* pick = topk_idx + (int64_t)a * K;
+      for (int i = lane; i < (b - a) * K; i += 64) {
+        const int e = pick[i];
+        if ((uint32_t)e < (uint32_t)E && (!mask || mask[a + i / K])) atomicAdd(&cnt[e], 1);
+      }
+      float acc[N];
+#pragma unroll
+      for (int k = 0; k < N; ++k) acc[k] = 0.0f;
+      float z = 0.0f, n = 0.0f;
+      for (int t0 = a; t0 < b; t0 += TPW) {
+        const int t = min(t0 + grp, b - 1);
+        float y[N], q;
+        Row::load(logits + (int64_t)t * E, li, E, y);
+        rl_softmax<G>(y, q);
+        if (t0 + grp < b && (!mask || mask[t])) {
+          n += 1.0f;
+          z += q;
+#pragma unroll
+          for (int k = 0; k < N; ++k) acc[k] += y[k];
+        }
+      }
+      const int64_t slot = ONE ? (int64_t)s : (int64_t)blockIdx.x + s;
+      float* prob = (ONE ? o.prob_sum : w.prob) + slot * E;
+      int32_t* out_cnt = (ONE ? o.seq_counts : w.cnt) + slot * E;
+      double bal = 0.0;
+#pragma unroll
+      for (int k = 0; k < N; ++k) {
+#pragma unroll
+        for (int h = G; h < 64; h <<= 1) acc[k] += __shfl_xor(acc[k], h, 64);
+        const int e = Row::col(li, k);
+        if (grp == 0 && e < E) {
+          const int c = cnt[e];
+          prob[e] = acc[k];
+          out_cnt[e] = c;
+          if (ONE) bal += (double)acc[k] * (double)c;
+        }
+      }
+      z = rl_group_sum<64>(li == 0 ? z : 0.0f);
+      n = rl_group_sum<64>(li == 0 ? n : 0.0f);
+      if constexpr (ONE) {
+#pragma unroll
+        for (int h = 32; h > 0; h >>= 1) bal += __shfl_xor(bal, h, 64);
+      }
+      if (lane == 0) {
+        if constexpr (ONE) {
+          rl_put(&w.bal[s], bal);
+          rl_put(&w.zs[s], (double)z);
+          rl_put(&o.seq_tokens[s], (int32_t)n);
+        } else {
+          w.z[slot] = z;
+          w.tok[slot] = (int)n;
+        }
+      }
+    }
+    if constexpr (ONE) {
+      __shared__ RlJoinLds L;
+      __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup");
+      __builtin_amdgcn_s_waitcnt(0);  // this wave's sums have arrived
+      __syncthreads();
+      rl_losses(L, E, K, n_seq, 1, w, o);
+    }
+  } else if (ONE && threadIdx.x == 0) {
+    rl_write_loss(o, E, K, bsum, zsum, nsum);
+  }
 }
 
 // The joining launch, one workgroup per sequence and block of 32 columns; the last one to finish
@@ -512,10 +639,10 @@ __global__ __launch_bounds__(RL_THREADS) void k_rloss_join(int T, int E, int K, 
   }
   __syncthreads();
   if (!L.last) return;
-  rl_losses(L, E, K, n_seq, w, o);
+  rl_losses(L, E, K, n_seq, cbs, w, o);
 }
 
-// dLogits, piece by piece as the forward.  The counts enter less their mean K T_s / E: the
+// dLogits.  A group of lanes keeps its sequence's counts as long as its tokens stay in it.  The counts enter less their mean K T_s / E: the
 // probabilities of a row sum to one, so the mean drops out of the difference, and without it the
 // difference of two nearly equal numbers would lose the leading bits.
 template <int G, int NV, bool V4>
@@ -525,12 +652,13 @@ __global__ __launch_bounds__(RL_BWD_THREADS) void k_rloss_bwd(const float* __res
                                                           const uint8_t* __restrict__ mask,
                                                           const int32_t* __restrict__ seq_tokens,
                                                           const int32_t* __restrict__ seq_counts,
-                                                          const float* __restrict__ lse, float* __restrict__ dLogits) {
+                                                          const float* __restrict__ lse, float* __restrict__ dLogits,
+                                                          int chunk) {
   using Row = RlRow<G, NV, V4>;
   constexpr int N = Row::N, TPW = 64 / G, WAVES = RL_BWD_THREADS / 64;
   __shared__ long long rn[WAVES];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, li = lane % G, grp = lane / G;
-  const int t_begin = blockIdx.x * RL_BWD_CHUNK, t_end = min(T, t_begin + RL_BWD_CHUNK);
+  const int t_begin = blockIdx.x * chunk, t_end = min(T, t_begin + chunk);
   __shared__ RlTable tab;
   rl_table_load(tab, seq_off, n_seq, T);
   auto off = [&](int s) { return n_seq <= RL_TABLE ? tab.off[s] : rl_off(seq_off, s, T); };
@@ -543,44 +671,42 @@ __global__ __launch_bounds__(RL_BWD_THREADS) void k_rloss_bwd(const float* __res
   n = rn[0] + rn[1] + rn[2] + rn[3];
   const float inv_n = n > 0 ? 1.0f / (float)n : 0.0f;
   const float gb = dloss[0] * inv_n * (float)E / (float)K, gz = dloss[1] * 2.0f * inv_n;
-  for (int a = t_begin, b; a < t_end; a = b) {
-    const int s = rl_piece(off, n_seq, a, t_end, b);
-    float ex[N];
-    float coef = 0.0f;
-    if (s >= 0) {
-      const int ts = seq_tokens[s];
-      coef = ts > 0 ? gb / (float)ts : 0.0f;
-      const float mean = (float)((double)K * (double)ts / (double)E);
-#pragma unroll
-      for (int i = 0; i < N; ++i) {
-        const int c = Row::col(li, i);
-        ex[i] = c < E ? (float)seq_counts[(int64_t)s * E + c] - mean : 0.0f;
-      }
-    } else {
-#pragma unroll
-      for (int i = 0; i < N; ++i) ex[i] = 0.0f;
-    }
-    for (int t = a + wave * TPW + grp; t < b; t += WAVES * TPW) {
-      const float l = lse[t];
-      float x[N];
-      if (s >= 0 && (!mask || mask[t]) && l != -INFINITY) {
-        Row::load(logits + (int64_t)t * E, li, E, x);
-        float dot = 0.0f;
+  int s = -1, stop = t_begin, at = 0;  // the sequence of this lane group's tokens before `stop`
+  float ex[N], coef = 0.0f;
+  for (int t = t_begin + wave * TPW + grp; t < t_end; t += WAVES * TPW) {
+    float x[N];
+    Row::load(logits + (int64_t)t * E, li, E, x);
+    const float l = lse[t];
+    const bool live = !mask || mask[t];
+    if (t >= stop) {
+      s = rl_piece(off, n_seq, t, T, stop, at);
+      if (s >= 0) {
+        const int ts = seq_tokens[s];
+        coef = ts > 0 ? gb / (float)ts : 0.0f;
+        const float mean = (float)((double)K * (double)ts / (double)E);
 #pragma unroll
         for (int i = 0; i < N; ++i) {
-          x[i] = rl_exp(x[i] - l);
-          dot += x[i] * ex[i];
+          const int c = Row::col(li, i);
+          ex[i] = c < E ? (float)seq_counts[(int64_t)s * E + c] - mean : 0.0f;
         }
-        dot = rl_group_sum<G>(dot);
-        const float zt = gz * l;
-#pragma unroll
-        for (int i = 0; i < N; ++i) x[i] *= coef * (ex[i] - dot) + zt;
-      } else {
-#pragma unroll
-        for (int i = 0; i < N; ++i) x[i] = 0.0f;
       }
-      Row::store(dLogits + (int64_t)t * E, li, E, x);
     }
+    if (s >= 0 && live && l != -INFINITY) {
+      float dot = 0.0f;
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        x[i] = rl_exp(x[i] - l);
+        dot += x[i] * ex[i];
+      }
+      dot = rl_group_sum<G>(dot);
+      const float zt = gz * l;
+#pragma unroll
+      for (int i = 0; i < N; ++i) x[i] *= coef * (ex[i] - dot) + zt;
+    } else {
+#pragma unroll
+      for (int i = 0; i < N; ++i) x[i] = 0.0f;
+    }
+    Row::store(dLogits + (int64_t)t * E, li, E, x);
   }
 }
 
@@ -635,8 +761,11 @@ struct RlossBwd {
   hipStream_t st;
   template <int G, int NV, bool V4>
   void operator()() const {
-    k_rloss_bwd<G, NV, V4><<<(int)cdiv(T, RL_BWD_CHUNK), RL_BWD_THREADS, 0, st>>>(dloss, logits, T, E, K, n_seq, seq_off, mask,
-                                                                      seq_tokens, seq_counts, lse, dLogits);
+    constexpr int LEAST = RL_BWD_THREADS / G;  // one token per lane group
+    int chunk = RL_BWD_CHUNK > LEAST ? RL_BWD_CHUNK : LEAST;
+    while (chunk > LEAST && cdiv(T, chunk) < 512) chunk /= 2;
+    k_rloss_bwd<G, NV, V4><<<(int)cdiv(T, chunk), RL_BWD_THREADS, 0, st>>>(dloss, logits, T, E, K, n_seq, seq_off, mask,
+                                                                      seq_tokens, seq_counts, lse, dLogits, chunk);
   }
 };
 }  // namespace

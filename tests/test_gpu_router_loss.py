@@ -206,3 +206,38 @@ def test_determinism_streams_and_graph():
     for o in others:
         for k, v in o.outs().items():
             assert torch.equal(v, ref[k]), k
+
+
+def _cuts(T, lengths):
+    """A table whose sequences have these lengths (the last one ends where they do, at most at T)."""
+    off = [0]
+    for n in lengths:
+        off.append(min(T, off[-1] + n))
+    return off
+
+
+# chunks of many short sequences beside long ones: waves take the short pieces, the workgroup the long
+@pytest.mark.parametrize("E,K", [(5, 2), (24, 4), (128, 8), (250, 3), (379, 6), (1000, 8)])
+@pytest.mark.parametrize("lengths", [
+    [1] * 64, [0, 3, 0, 0, 2, 1, 0, 7, 20, 5, 0, 4], [1, 1, 1, 40, 1, 1, 2, 30, 1, 1, 1, 50, 1], [5] * 40, [2, 300, 1, 1, 1, 1, 250, 3, 3, 3, 3],
+], ids=["ones", "gaps", "mixed", "fives", "long"])
+def test_many_sequences_in_a_chunk(E, K, lengths):
+    T = sum(lengths) + 9
+    Case(T=T, E=E, K=K, n_seq=len(lengths), off=_cuts(T, lengths), masked=0.2, seed=E + len(lengths)).check()
+
+
+@pytest.mark.parametrize("T,E", [(40, 16), (1300, 16), (700, 300)])
+def test_more_sequences_than_the_table_in_shared_memory_holds(T, E):
+    off = np.sort(np.random.default_rng(T).integers(0, T + 1, 1500)).tolist()
+    Case(T=T, E=E, K=2, n_seq=1499, off=off, masked=0.1, seed=T).check()
+
+
+@pytest.mark.parametrize("T,lengths", [(60, [2] * 25), (900, [1, 2, 70, 3] * 11)])
+def test_many_sequences_replayed(T, lengths):
+    c = Case(T=T, E=48, K=4, n_seq=len(lengths), off=_cuts(T, lengths), masked=0.2, seed=T)
+
+    def step():
+        c.forward()
+        c.backward()
+
+    check_replays(step, c.outs())
