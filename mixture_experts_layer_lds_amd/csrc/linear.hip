@@ -301,12 +301,12 @@ __global__ __launch_bounds__(TI::THREADS, TI::NW == 8 ? 1 : 2) void k_lin(LinGem
 
 // The backward's two products in one launch, where neither fills the chip: workgroups below nx take
 // dX's tiles, the others dW's.
-template <typename T, class TI, int OUT>
+template <typename T, class TI, int OUT_X, int OUT_W>
 __global__ __launch_bounds__(TI::THREADS, 2) void k_lin_pair(LinGemm gx, LinEpi<T> ex, int nx, LinGemm gw, LinEpi<T> ew) {
   __shared__ __attribute__((aligned(1024))) char b0[TI::SLOT];
   __shared__ __attribute__((aligned(1024))) char b1[TI::SLOT];
-  if ((int)blockIdx.x < nx) lin_tile<T, TI, LIN_DX, true, OUT>(xcd_remap(blockIdx.x, nx), gx, ex, b0, b1);
-  else lin_tile<T, TI, LIN_DW, true, OUT>(xcd_remap(blockIdx.x - nx, gridDim.x - nx), gw, ew, b0, b1);
+  if ((int)blockIdx.x < nx) lin_tile<T, TI, LIN_DX, true, OUT_X>(xcd_remap(blockIdx.x, nx), gx, ex, b0, b1);
+  else lin_tile<T, TI, LIN_DW, true, OUT_W>(xcd_remap(blockIdx.x - nx, gridDim.x - nx), gw, ew, b0, b1);
 }
 
 // Four consecutive elements of T as fp32.
@@ -389,21 +389,20 @@ __global__ __launch_bounds__(256) void k_lin_finish(const float* __restrict__ pa
   lin_finish<T>((int64_t)blockIdx.x * 256 + threadIdx.x, part, SK, m, n, np, ep);
 }
 
-// db = the row blocks' sums (fp64) for 32 columns: RUNS runs of row blocks, then the runs in order.
-constexpr int LIN_DB_RUNS = 8;
+// db = the row blocks' sums (fp64) for 8 columns: 32 runs of row blocks, then the runs in order (many
+// rows and few columns leave hundreds of row blocks: 5875 x 24 takes 735, 12 us by 8 runs).
+constexpr int LIN_DB_COLS = 8, LIN_DB_RUNS = 32;
 __device__ __forceinline__ void lin_db(int block, const float* __restrict__ db_part, int blocks, int np,
                                        float* __restrict__ db) {
-  __shared__ double red[LIN_DB_RUNS][33];
-  const int cl = threadIdx.x & 31, run = threadIdx.x >> 5;
-  const int c = block * 32 + cl;
+  __shared__ double red[LIN_DB_RUNS][LIN_DB_COLS + 1];
+  const int cl = threadIdx.x % LIN_DB_COLS, run = threadIdx.x / LIN_DB_COLS;
+  const int c = block * LIN_DB_COLS + cl;  // np is a multiple of 8
   double v = 0.0;
-  if (c < np) {
 #pragma unroll 8
-    for (int b = run; b < blocks; b += LIN_DB_RUNS) v += (double)db_part[(int64_t)b * np + c];
-  }
+  for (int b = run; b < blocks; b += LIN_DB_RUNS) v += (double)db_part[(int64_t)b * np + c];
   red[run][cl] = v;
   __syncthreads();
-  if (run == 0 && c < np) {
+  if (run == 0) {
 #pragma unroll
     for (int q = 1; q < LIN_DB_RUNS; ++q) v += red[q][cl];
     db[c] = (float)v;
@@ -644,7 +643,7 @@ constexpr int kLinSlices[] = {1, 2, 3, 4, 6, 8, 12, 16, 24, 32};
 static int lin_stages(const LinGemm& g, bool bf16_) { return (int)cdiv(g.red, bf16_ ? dn_bk<bf16>() : dn_bk<float>()); }
 static int64_t lin_tiles(const LinGemm& g, int tile) { return cdiv(g.m, tile) * cdiv(g.n, tile); }
 // wgs workgroups of `stages` stages on tiles below the largest, out partial products in all.
-static double lin_time(int tile, int64_t wgs, int64_t stages, double out, bool bf16_, bool pair) {
+static double lin_time(int tile, double wgs, int64_t stages, double out, bool bf16_, bool pair) {
   const double per = wgs / 256.0;  // workgroups per CU
   double stage, most;              // per stage; workgroups that a CU holds
   const double besides = !bf16_ && tile == LIN_MID ? 5.5 : 4.0;
@@ -667,7 +666,8 @@ static void lin_set(LinGemm& g, bool bf16_, int tile, int sk) {
   g.klen = (int)cdiv(lin_stages(g, bf16_), sk) * (bf16_ ? dn_bk<bf16>() : dn_bk<float>());
   g.SK = g.red > 0 ? (int)cdiv(g.red, g.klen) : 1;
 }
-static void lin_plan(LinGemm& g, bool bf16_, bool may_split) {
+// Sets g's plan and returns its time by the model.
+static double lin_plan(LinGemm& g, bool bf16_, bool may_split) {
   const int stages = lin_stages(g, bf16_);
   double best = bf16_ ? cdiv(lin_tiles(g, LIN_BIG), 256) * (stages * 1.4 + 10.0) : 1e30;
   int tile = LIN_BIG, sk = 1;
@@ -682,6 +682,7 @@ static void lin_plan(LinGemm& g, bool bf16_, bool may_split) {
       }
     }
   lin_set(g, bf16_, tile, sk);
+  return best;
 }
 
 // Rows per workgroup of k_lin_dz: 64 where that gives four workgroups per CU, fewer (at least 8) for
@@ -726,28 +727,37 @@ size_t linear_fwd_workspace_bytes(const LinShape& s) {
   return g.SK > 1 ? lin_part_bytes(g) : 0;
 }
 
-// The backward's two products where both are small: their tiles side by side in one launch, the same number of slices for each (999 x 1000 x 264, ReLU with a bias: 26 us in six
-// launches, 20 in three; 25.9 unsliced, 20.8 with 2, 20.2 with 3, 24.8 with 8).  False: they are launched one after the other, each with a plan of its own.
-static bool lin_pair_plan(const LinShape& s, LinGemm& gx, LinGemm& gw, bool* parts) {
-  if (s.M == 0 || lin_tiles(gx, LIN_MID) + lin_tiles(gw, LIN_MID) > 256) return false;
+// The backward's two products in one launch, each cut so that no workgroup has more than `most` stages
+// (a batch of many rows has a short reduction for dX and a long one for dW): where the model says
+// that this beats one after the other.  999 x 1000 x 264, ReLU with a bias: 26 us in six launches,
+// 20 in three; 25.9 unsliced, 20.8 with 2 slices, 20.2 with 3, 24.8 with 8.  12062 x 296 x 424:
+// 50 us apart, 41 together; 2048 x 2048 x 2048: 54 and 47.  False: one after the other, each with a plan of its own, in gx
+// and gw.
+static bool lin_pair_plan(const LinShape& s, LinGemm& gx, LinGemm& gw) {
+  // with over four rounds of tiles each product fills the chip by itself (16384 x 512 x 2048: 91 us
+  // apart, 98 together)
+  if (s.M == 0 || lin_tiles(gx, LIN_MID) + lin_tiles(gw, LIN_MID) > 1024) return false;
+  const double apart = lin_plan(gx, s.bf16, true) + lin_plan(gw, s.bf16, true);
   const int sx = lin_stages(gx, s.bf16), sw = lin_stages(gw, s.bf16), longest = sx > sw ? sx : sw;
-  const double out = (double)gx.m * gx.n + (double)gw.m * gw.n;
-  double best = 1e30;
-  int tile = LIN_MID, sk = 1;
+  double best = 0.9 * apart;  // (its error, within which the simpler launches stay)
+  int tile = 0, most = 0;
   for (int t : {LIN_MID, LIN_SMALL})
     for (int q : kLinSlices) {
       if (q > longest) break;
-      const int64_t wgs = (lin_tiles(gx, t) + lin_tiles(gw, t)) * q;
-      const double us = lin_time(t, wgs, cdiv(longest, q), q > 1 ? q * out : 0.0, s.bf16, true);
+      const int len = (int)cdiv(longest, q), qx = (int)cdiv(sx, len), qw = (int)cdiv(sw, len);
+      const double out = (qx > 1 ? (double)qx * gx.m * gx.n : 0.0) + (qw > 1 ? (double)qw * gw.m * gw.n : 0.0);
+      // the shorter product's workgroups count by their share of the longest
+      const double wgs = ((double)lin_tiles(gx, t) * sx + (double)lin_tiles(gw, t) * sw) / len;
+      const double us = lin_time(t, wgs, len, out, s.bf16, true);
       if (us < best) {
         best = us;
         tile = t;
-        sk = q;
+        most = len;
       }
     }
-  lin_set(gx, s.bf16, tile, sk < sx ? sk : sx);
-  lin_set(gw, s.bf16, tile, sk < sw ? sk : sw);
-  *parts = sk > 1;
+  if (!tile) return false;
+  lin_set(gx, s.bf16, tile, (int)cdiv(sx, most));
+  lin_set(gw, s.bf16, tile, (int)cdiv(sw, most));
   return true;
 }
 
@@ -770,15 +780,10 @@ static size_t lin_carve_bwd(const LinShape& s, void* base, LinBwdWs* w) {
   q.dZ = take(s.act == LIN_NONE ? 0 : (size_t)s.M * NW * (s.bf16 ? 2 : 4));
   q.db_part = reinterpret_cast<float*>(take((size_t)cdiv(s.M, lin_dz_rows(s)) * NW * 4));
   LinGemm gx = lin_gemm(s, LIN_DX), gw = lin_gemm(s, LIN_DW);
+  const bool pair = lin_pair_plan(s, gx, gw);
   const size_t px = gx.SK > 1 ? lin_part_bytes(gx) : 0, pw = gw.SK > 1 ? lin_part_bytes(gw) : 0;
-  size_t alone = px > pw ? px : pw;
-  bool parts = false;
-  if (lin_pair_plan(s, gx, gw, &parts) && parts) {
-    q.part_w = reinterpret_cast<float*>(take(lin_part_bytes(gw)));
-    if (lin_part_bytes(gx) > alone) alone = lin_part_bytes(gx);
-  } else {
-    q.part_w = nullptr;
-  }
+  q.part_w = pair ? reinterpret_cast<float*>(take(pw)) : nullptr;
+  const size_t alone = pair || px > pw ? px : pw;
   q.part = reinterpret_cast<float*>(take(alone));
   if (w) *w = q;
   return off;
@@ -879,10 +884,13 @@ hipError_t launch_linear(const LinShape& s, const void* X, const void* W, const 
 }
 
 template <typename T, class TI>
-static void lin_pair_launch(const LinGemm& gx, const LinEpi<T>& ex, int nx, const LinGemm& gw, const LinEpi<T>& ew, int nw,
-                            bool parts, hipStream_t st) {
-  if (parts) k_lin_pair<T, TI, LIN_OUT_PART><<<nx + nw, TI::THREADS, 0, st>>>(gx, ex, nx, gw, ew);
-  else k_lin_pair<T, TI, LIN_OUT_EPI><<<nx + nw, TI::THREADS, 0, st>>>(gx, ex, nx, gw, ew);
+static void lin_pair_launch(const LinGemm& gx, const LinEpi<T>& ex, const LinGemm& gw, const LinEpi<T>& ew, hipStream_t st) {
+  const int nx = grid8((int64_t)gx.MT * gx.NT * gx.SK), grid = nx + grid8((int64_t)gw.MT * gw.NT * gw.SK);
+  const bool px = gx.SK > 1, pw = gw.SK > 1;
+  if (px && pw) k_lin_pair<T, TI, LIN_OUT_PART, LIN_OUT_PART><<<grid, TI::THREADS, 0, st>>>(gx, ex, nx, gw, ew);
+  else if (px) k_lin_pair<T, TI, LIN_OUT_PART, LIN_OUT_EPI><<<grid, TI::THREADS, 0, st>>>(gx, ex, nx, gw, ew);
+  else if (pw) k_lin_pair<T, TI, LIN_OUT_EPI, LIN_OUT_PART><<<grid, TI::THREADS, 0, st>>>(gx, ex, nx, gw, ew);
+  else k_lin_pair<T, TI, LIN_OUT_EPI, LIN_OUT_EPI><<<grid, TI::THREADS, 0, st>>>(gx, ex, nx, gw, ew);
 }
 
 template <typename T>
@@ -911,24 +919,23 @@ static hipError_t lin_backward(const LinShape& s, const T* dY, const T* X, const
   const LinEpi<T> ew = lin_epi<T>(nullptr, nullptr, 0, nullptr, 0, dW, s.K, LIN_NONE);
   const LinDb db{w.db_part, blocks, NW, dbias};
   // (the plan goes by the shape alone: a gradient asked for on its own has the pair's bits)
-  bool parts = false;
-  const bool pair = lin_pair_plan(s, gx, gw, &parts);
+  const bool pair = lin_pair_plan(s, gx, gw);
   if (pair && dX && dW) {
     gx.part = w.part;
     gw.part = w.part_w;
-    const int nx = grid8((int64_t)gx.MT * gx.NT * gx.SK), nw = grid8((int64_t)gw.MT * gw.NT * gw.SK);
-    if (gx.tile == LIN_SMALL) lin_pair_launch<T, LinSmall>(gx, ex, nx, gw, ew, nw, parts, st);
-    else lin_pair_launch<T, LinMid>(gx, ex, nx, gw, ew, nw, parts, st);
+    if (gx.tile == LIN_SMALL) lin_pair_launch<T, LinSmall>(gx, ex, gw, ew, st);
+    else lin_pair_launch<T, LinMid>(gx, ex, gw, ew, st);
+    const int fx = gx.SK > 1 ? (int)cdiv((int64_t)gx.m * (gx.n / 4), 256) : 0;
+    const int fw = gw.SK > 1 ? (int)cdiv((int64_t)gw.m * (gw.n / 4), 256) : 0;
     hipError_t e = hipGetLastError();
-    if (e != hipSuccess || (!parts && !dbias)) return e;
-    const int fx = parts ? (int)cdiv((int64_t)gx.m * (gx.n / 4), 256) : 0, fw = parts ? (int)cdiv((int64_t)gw.m * (gw.n / 4), 256) : 0;
-    k_lin_finish_pair<T><<<fx + fw + (dbias ? (int)cdiv(NW, 32) : 0), 256, 0, st>>>(gx, ex, fx, gw, ew, fw, db);
+    if (e != hipSuccess || fx + fw + (dbias ? 1 : 0) == 0) return e;
+    k_lin_finish_pair<T><<<fx + fw + (dbias ? NW / LIN_DB_COLS : 0), 256, 0, st>>>(gx, ex, fx, gw, ew, fw, db);
     return hipGetLastError();
   }
-  if (dbias) k_lin_db<<<(int)cdiv(NW, 32), 256, 0, st>>>(db.part, db.blocks, db.np, db.db);
+  if (dbias) k_lin_db<<<NW / LIN_DB_COLS, 256, 0, st>>>(db.part, db.blocks, db.np, db.db);
   hipError_t e = hipGetLastError();
   if (e == hipSuccess && dX) e = lin_run<LIN_DX>(gx, w.part, ex, st);
-  if (e == hipSuccess && dW) e = lin_run<LIN_DW>(gw, parts ? w.part_w : w.part, ew, st);
+  if (e == hipSuccess && dW) e = lin_run<LIN_DW>(gw, pair ? w.part_w : w.part, ew, st);
   return e;
 }
 
