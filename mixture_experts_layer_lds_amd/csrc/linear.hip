@@ -45,7 +45,7 @@ __device__ __forceinline__ float lin_act1(float z) {
   if constexpr (ACT == LIN_GELU) {
     float e;
     const float q = normal_tail(z, &e);
-    return fmaf(-fabsf(z), q, z < 0.0f ? 0.0f : z);
+    return fmaf(q != 0.0f ? -fabsf(z) : 0.0f, q, z < 0.0f ? 0.0f : z);  // (infinity times a tail of 0 is 0)
   }
   if constexpr (ACT == LIN_SILU) return z * sigmoid_f32(z);
   return z;
@@ -56,7 +56,7 @@ __device__ __forceinline__ float lin_grad1(float z) {
   if constexpr (ACT == LIN_GELU) {
     float e;
     const float q = normal_tail(z, &e);
-    return (z < 0.0f ? q : 1.0f - q) + z * e * 0.39894228040143268f;
+    return (z < 0.0f ? q : 1.0f - q) + (e != 0.0f ? z : 0.0f) * e * 0.39894228040143268f;
   }
   if constexpr (ACT == LIN_SILU) {
     const float s = sigmoid_f32(z);

@@ -598,6 +598,7 @@ moe_status moe_backward_aux(const moe_dims* dims, const void* dY, const void* X,
   MOE_TRY(need_ptr(W_down, "W_down"));
   MOE_TRY(opt_ptr(H_cache, "H_cache"));
   MOE_TRY(opt_ptr(dLogits_aux, "dLogits_aux"));
+  if (dLogits_aux && dLogits_aux == dLogits) return fail(MOE_EINVAL, "dLogits_aux must not be the dLogits array");
   MOE_TRY(need_ptr(dX, "dX"));
   MOE_TRY(need_ptr(dW_gate, "dW_gate"));
   MOE_TRY(need_ptr(dW_up, "dW_up"));
@@ -692,6 +693,7 @@ moe_status moe_router_loss_backward(const moe_dims* dims, const float* dloss, co
   MOE_TRY(need_ptr(seq_counts, "seq_counts"));
   MOE_TRY(need_ptr(lse, "lse"));
   MOE_TRY(need_ptr(dLogits, "dLogits"));
+  if (dLogits == logits) return fail(MOE_EINVAL, "dLogits must not be the logits array");
   hipStream_t st = static_cast<hipStream_t>(stream);
   MOE_STAGE(MOE_STAGE_ROUTER_LOSS, st,
             launch_router_loss_bwd(dloss, logits, dims->T, dims->E, dims->K, n_seq, seq_off, token_mask, seq_tokens,

@@ -129,3 +129,13 @@ def test_backward_aux_refuses_a_misaligned_gradient(lib):
     r = lib.moe_backward_aux(ctypes.byref(d), FAKE, FAKE, FAKE, FAKE, FAKE, FAKE, ctypes.byref(plan), None, FAKE + 4, FAKE,
                              FAKE, FAKE, FAKE, FAKE, FAKE, FAKE, FAKE, BIG, None)
     assert r == -1 and b"dLogits_aux" in lib.moe_last_error()
+
+
+def test_gradients_refuse_the_array_they_read(lib):
+    d = B.make_dims(64, 64, 64, 8, 2)
+    plan = B.PlanStruct(*([FAKE] * 9))
+    r = lib.moe_backward_aux(ctypes.byref(d), FAKE, FAKE, FAKE, FAKE, FAKE, FAKE, ctypes.byref(plan), None, FAKE + 64, FAKE,
+                             FAKE, FAKE, FAKE, FAKE, FAKE + 64, FAKE, FAKE, BIG, None)
+    assert r == -1 and b"dLogits_aux" in lib.moe_last_error()
+    r = lib.moe_router_loss_backward(ctypes.byref(d), FAKE, FAKE + 64, 1, None, None, FAKE, FAKE, FAKE, FAKE + 64, None)
+    assert r == -1 and b"logits" in lib.moe_last_error()

@@ -244,3 +244,46 @@ def test_graph_replays_and_streams(M, N, K, act):
     torch.cuda.synchronize()
     for q in qs:
         assert all(torch.equal(a, b) for a, b in zip((q.out, q.dX, q.dW, q.db), want))
+
+
+@pytest.mark.parametrize("M", [3, 40])
+def test_gelu_at_infinities(M):
+    """z Phi(z) tends to z and to 0, its derivative to 1 and to 0."""
+    X = torch.zeros(M, 64, device="cuda")
+    X[0], X[1] = float("inf"), -float("inf")
+    W = torch.full((72, 64), 0.5, device="cuda")
+    dims = B.make_linear_dims(M, 72, 64, "f32", "gelu")
+    ws, nb = B.linear_workspace(dims, B.LINEAR_BACKWARD)
+    out, Z, db = torch.empty(M, 72, device="cuda"), torch.empty(M, 72, device="cuda"), torch.empty(72, device="cuda")
+    B.moe_linear(dims, X, W, None, None, Z, out, ws, nb)
+    assert (out[0] == float("inf")).all() and (out[1:] == 0).all()
+    dY = torch.zeros(M, 72, device="cuda")
+    dY[0], dY[1] = 3.0, 5.0
+    B.moe_linear_backward(dims, dY, X, W, Z, None, None, db, ws, nb)
+    assert (db == 3.0).all()
+
+
+# few rows with a long reduction for dX, many rows with one for dW: products of the pair cut apart
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("M,N,K,act", [(25, 1152, 232, "swiglu"), (3011, 72, 104, "relu"), (1100, 24, 1720, "gelu"), (700, 520, 16, "none")])
+def test_backward_of_unequal_reductions(M, N, K, act, dtype):
+    p = Proj(M, N, K, dtype, act, bias=True, residual=False, save=True, pad=8)
+    p.check_backward()
+
+
+@pytest.mark.parametrize("M,N,K", [(4096, 4096, 1096), (4090, 4096, 328), (4096, 1096, 4096), (1100, 4096, 4096), (4000, 2000, 4040)])
+def test_large_tiles_with_partial_stages(M, N, K):
+    """Small whole numbers: every product and sum is exact, so the results are the exact ones rounded."""
+    g = torch.Generator(device="cuda").manual_seed(M + N + K)
+    ints = lambda *s: torch.randint(-2, 3, s, generator=g, device="cuda").float()  # noqa: E731
+    X, W, dY = ints(M, K), ints(N, K), ints(M, N)
+    Xb, Wb, dYb = X.bfloat16(), W.bfloat16(), dY.bfloat16()
+    out, dX, dW = torch.empty_like(dYb), torch.empty_like(Xb), torch.empty_like(Wb)
+    dims = B.make_linear_dims(M, N, K, "bf16")
+    wf, nf = B.linear_workspace(dims, B.LINEAR_FORWARD)
+    wb, nb = B.linear_workspace(dims, B.LINEAR_BACKWARD)
+    B.moe_linear(dims, Xb, Wb, None, None, None, out, wf, nf)
+    B.moe_linear_backward(dims, dYb, Xb, Wb, None, dX, dW, None, wb, nb)
+    assert torch.equal(out, (X @ W.t()).bfloat16())
+    assert torch.equal(dX, (dY @ W).bfloat16())
+    assert torch.equal(dW, (dY.t() @ X).bfloat16())
