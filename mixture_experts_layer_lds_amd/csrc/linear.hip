@@ -11,6 +11,13 @@
 // reduction is cut into slices whose fp32 partial products a second kernel adds in slice order
 // before the epilogue (k_lin_finish).
 //
+// Large products are bound by the matrix cores at the clock that the chip's power allows
+// (8192 x 14336 x 4096 bf16: 690 us, 1390 TFLOP/s, of which the loop alone 650; 735 with GELU, whose
+// epilogue is 14 vector operations an element; a library product of that size 620 to 710), small
+// ones by launches and the length of one workgroup's loop.  The two products of a large backward go
+// out apart: together their last rounds filled up, but 16384 x 7168 x 4096 took 1578 us against
+// 1537, as idle CUs leave the others a higher clock.
+//
 // The epilogue works on the fp32 accumulators: a tile half is laid out in LDS and walked in
 // 16-byte chunks of a row, so that residual, saved pre-activation and output are read and written in
 // whole segments and rounded once.
@@ -432,7 +439,8 @@ __global__ __launch_bounds__(256) void k_lin_finish_pair(LinGemm gx, LinEpi<T> e
 // sharing the reduction; W is streamed from memory straight into the MFMA's A operand (two batches
 // of loads in flight per wave) and X, which stays in the caches, into B, NG groups of 16 rows.  The
 // waves' partial tiles meet in LDS, are added in wave order, and the epilogue runs in the same
-// launch.  Bound by reading W once.
+// launch.  Bound by reading W once: one row, SwiGLU, 4096 x 7168 weights 10.8 us (5.4 TB/s); 13 rows,
+// 7168 x 2048 weights with a residual 8.6 us, of which a launch is about 3.
 // SwiGLU with RT = 1 takes 8 gate rows and the 8 matching up rows, so that a column's two halves lie
 // 32 lanes apart; with RT = 2 16 gate rows and their 16 up rows, in the same lane.
 template <typename T, int NG, int RT>
@@ -551,7 +559,7 @@ __global__ __launch_bounds__(512) void k_lin_skinny(const T* __restrict__ X, int
 
 // dZ = dY act'(z) (SwiGLU: [dG | dU]) and the bias gradient's partial sums: a workgroup takes 256
 // columns (32 lanes of 8) and `rows` rows (8 at a time); db_part[row block][column].  dZ may be
-// null (only the sums), db_part too.
+// null (only the sums), db_part too.  Bound by memory: 16384 x 2048 SwiGLU, 336 MB, 61 us.
 template <typename T>
 __global__ __launch_bounds__(256) void k_lin_dz(const T* __restrict__ dY, int64_t ldy, const T* __restrict__ Z, int m,
                                                 int n, int act, int rows, T* __restrict__ dZ,
@@ -948,6 +956,9 @@ hipError_t launch_linear_bwd(const LinShape& s, const void* dY, const void* X, c
                              static_cast<const float*>(Z), static_cast<float*>(dX), static_cast<float*>(dW), dbias, ws, st);
 }
 
+// dX += dL W_r, after the gather-sum has rounded dX to the element type: the sum is rounded twice,
+// which its bound counts, where keeping the first part in fp32 would cost [T, d] floats of workspace
+// and traffic.
 template <typename T>
 static hipError_t lin_logit_dx(LinGemm g, const Shape& s, void* dX, hipStream_t st) {
   return lin_run<LIN_DX>(g, nullptr, lin_epi<T>(nullptr, dX, s.d, nullptr, 0, dX, s.d, LIN_NONE), st);

@@ -19,6 +19,8 @@
 // second launch adds the slots of a sequence in chunk order (in 64 bits), and its last workgroup
 // forms the two losses.  Where one chunk holds the whole batch, its workgroup writes the results
 // itself and there is no second launch.  No floating-point atomics: the order of every sum is fixed.
+// Measured: 16384 x 256 in 7 sequences 16.9 us (9.8 and 6.7 for the two launches; the 17.4 MB would
+// take 3.5), 256 x 8 in one launch 5.2; backward 32768 x 384, 101 MB, 19.3 us (5.2 TB/s).
 //
 // A token is taken by G lanes, each holding up to 4 NV of its logits (four consecutive ones per
 // 16-byte load where E is a multiple of 4), so that a wave reads whole rows whatever E is; the
