@@ -18,7 +18,8 @@ Everything here is plain float64 numpy, written from the pages' description of t
 ``oracle/fp8.py`` adds the FP8 (OCP E4M3) row quantisation and the quantised expert FFN, and
 ``oracle/mx.py`` the block-scaled variant (E4M3 or E5M2 elements, one power-of-two scale per 32
 elements along K), both from the apxml.com page's section "利用稀疏性和量化" (quantisation of
-weights and activations).
+weights and activations).  ``oracle/block.py`` holds the operators of the block around the layer
+(dense projection, router losses, dropout), which the pages do not describe.
 
 Where the pages leave a step open, the reading taken is stated at the function that takes it.
 Every function's result is pinned by tests under ``tests/`` (brute force, closed forms,
