@@ -110,6 +110,7 @@ struct LinGemm {
   int m, n, red, bred;
   int MT, NT, SK, klen;  // tiles, slices and values of k per slice (a multiple of 64; fp32: 32)
   int tile;              // LIN_BIG, LIN_MID or LIN_SMALL
+  bool off_lines;        // rows that do not start on 128-byte lines
   float* part;           // [SK][m][n] when the output goes there
 };
 
@@ -651,7 +652,7 @@ constexpr int kLinSlices[] = {1, 2, 3, 4, 6, 8, 12, 16, 24, 32};
 static int lin_stages(const LinGemm& g, bool bf16_) { return (int)cdiv(g.red, bf16_ ? dn_bk<bf16>() : dn_bk<float>()); }
 static int64_t lin_tiles(const LinGemm& g, int tile) { return cdiv(g.m, tile) * cdiv(g.n, tile); }
 // wgs workgroups of `stages` stages on tiles below the largest, out partial products in all.
-static double lin_time(int tile, double wgs, int64_t stages, double out, bool bf16_, bool pair) {
+static double lin_time(int tile, double wgs, int64_t stages, double out, bool bf16_, bool pair, double slow) {
   const double per = wgs / 256.0;  // workgroups per CU
   double stage, most;              // per stage; workgroups that a CU holds
   const double besides = !bf16_ && tile == LIN_MID ? 5.5 : 4.0;
@@ -659,7 +660,7 @@ static double lin_time(int tile, double wgs, int64_t stages, double out, bool bf
     stage = bf16_ ? (per > 1 ? 0.95 : (pair ? 0.8 : 0.5)) : (per > 1 ? 3.8 : 2.05);
     most = 2;
   } else {
-    const double share = bf16_ ? 0.165 : 0.61, least = bf16_ ? (pair ? 0.45 : 0.29) : (per > 1 ? 2.0 : 1.05);
+    const double share = bf16_ ? 0.165 * slow : 0.61, least = bf16_ ? (pair ? 0.45 : 0.29) : (per > 1 ? 2.0 : 1.05);
     stage = share * per > least ? share * per : least;
     most = 5;
     if (per > most) stage = share * most;
@@ -674,15 +675,23 @@ static void lin_set(LinGemm& g, bool bf16_, int tile, int sk) {
   g.klen = (int)cdiv(lin_stages(g, bf16_), sk) * (bf16_ ? dn_bk<bf16>() : dn_bk<float>());
   g.SK = g.red > 0 ? (int)cdiv(g.red, g.klen) : 1;
 }
+// What bf16 64 x 64 tiles lose, as they load twice as much per product as 128 x 128 ones, where the
+// operands leave the L2s and where rows do not start on 128-byte lines (2560 x 1024 x 7168: 78 us on
+// them, 55 on 128 x 128; 3000 x 1000 x 2000: 30.6 and 23.7).
+static double lin_slow(const LinGemm& g) {
+  const double mb = 2e-6 * g.red * ((double)g.m + g.n);
+  return (mb > 40 ? 1.6 : mb > 24 ? 1.2 : 1.0) * (g.off_lines ? 1.3 : 1.0);
+}
 // Sets g's plan and returns its time by the model.
 static double lin_plan(LinGemm& g, bool bf16_, bool may_split) {
   const int stages = lin_stages(g, bf16_);
+  const double slow = lin_slow(g);
   double best = bf16_ ? cdiv(lin_tiles(g, LIN_BIG), 256) * (stages * 1.4 + 10.0) : 1e30;
   int tile = LIN_BIG, sk = 1;
   for (int t : {LIN_MID, LIN_SMALL})
     for (int q : kLinSlices) {
       if (q > 1 && (!may_split || q > stages)) break;
-      const double us = lin_time(t, lin_tiles(g, t) * q, cdiv(stages, q), q > 1 ? (double)q * g.m * g.n : 0.0, bf16_, false);
+      const double us = lin_time(t, lin_tiles(g, t) * q, cdiv(stages, q), q > 1 ? (double)q * g.m * g.n : 0.0, bf16_, false, slow);
       if (us < best) {
         best = us;
         tile = t;
@@ -723,6 +732,7 @@ static LinGemm lin_gemm(const LinShape& s, int mode) {
     g.red = (int)s.M;
   }
   g.bred = g.red;
+  g.off_lines = s.K % 64 || (mode != LIN_FWD && NW % 64);
   lin_plan(g, s.bf16, true);
   return g;
 }
@@ -756,7 +766,7 @@ static bool lin_pair_plan(const LinShape& s, LinGemm& gx, LinGemm& gw) {
       const double out = (qx > 1 ? (double)qx * gx.m * gx.n : 0.0) + (qw > 1 ? (double)qw * gw.m * gw.n : 0.0);
       // the shorter product's workgroups count by their share of the longest
       const double wgs = ((double)lin_tiles(gx, t) * sx + (double)lin_tiles(gw, t) * sw) / len;
-      const double us = lin_time(t, wgs, len, out, s.bf16, true);
+      const double us = lin_time(t, wgs, len, out, s.bf16, true, 1.0);
       if (us < best) {
         best = us;
         tile = t;
