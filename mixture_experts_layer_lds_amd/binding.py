@@ -341,14 +341,12 @@ def moe_router_loss_backward(dims, dloss, logits, n_seq, seq_off, token_mask, se
                                           _stream(stream)))
 
 
-def _row_stride(t, shape, dtype, name):
-    """Row stride of a 2-D tensor of this shape and type whose rows are contiguous."""
-    if t.shape != shape or t.dtype is not dtype:
-        raise MoEError(-1, "%s must be %s of %s" % (name, tuple(shape), dtype))
+def _row_stride(t, rows, cols, name):
+    """Row stride of a rows x cols tensor whose rows are contiguous."""
     ld, step = t.stride()
-    if step != 1 and shape[1] > 1:
+    if step != 1 and cols > 1:
         raise MoEError(-1, "%s must have contiguous rows" % name)
-    return ld if shape[0] > 1 else shape[1]
+    return ld if rows > 1 else cols
 
 
 def moe_dropout(x, residual, p, rng, out, stream=None):
@@ -356,16 +354,28 @@ def moe_dropout(x, residual, p, rng, out, stream=None):
     strided); rng is a device tensor of two 64-bit words, {seed, offset}.  Without a residual this is
     also the gradient of dropout."""
     dtype, shape = x.dtype, x.shape
-    if dtype not in (torch.bfloat16, torch.float32):
+    if dtype is torch.bfloat16:
+        code = MOE_BF16
+    elif dtype is torch.float32:
+        code = MOE_F32
+    else:
         raise MoEError(-2, "dtype %s not supported" % dtype)
     if len(shape) != 2:
         raise MoEError(-1, "x must have two dimensions")
+    if out.shape != shape or out.dtype is not dtype:
+        raise MoEError(-1, "out must be %s of %s" % (tuple(shape), dtype))
     if rng.numel() < 2 or rng.element_size() != 8:
         raise MoEError(-1, "rng must hold two 64-bit words")
-    ldx, ldo = _row_stride(x, shape, dtype, "x"), _row_stride(out, shape, dtype, "out")
-    ldr = _row_stride(residual, shape, dtype, "residual") if residual is not None else 0
-    _check(lib().moe_dropout(shape[0], shape[1], MOE_BF16 if dtype is torch.bfloat16 else MOE_F32, x.data_ptr(), ldx,
-                             _p(residual), ldr, p, rng.data_ptr(), out.data_ptr(), ldo, _stream(stream)))
+    rows, cols = shape
+    res, ldr = None, 0
+    if residual is not None:
+        if residual.shape != shape or residual.dtype is not dtype:
+            raise MoEError(-1, "residual must be %s of %s" % (tuple(shape), dtype))
+        res, ldr = residual.data_ptr(), _row_stride(residual, rows, cols, "residual")
+    status = lib().moe_dropout(rows, cols, code, x.data_ptr(), _row_stride(x, rows, cols, "x"), res, ldr, p, rng.data_ptr(),
+                               out.data_ptr(), _row_stride(out, rows, cols, "out"), _stream(stream))
+    if status:
+        _check(status)
 
 
 def moe_combine_dropout(dims, plan, Y_perm, weighted, residual, p, rng, out, stream=None):
