@@ -111,6 +111,7 @@ struct LinGemm {
   int MT, NT, SK, klen;  // tiles, slices and values of k per slice (a multiple of 64; fp32: 32)
   int tile;              // LIN_BIG, LIN_MID or LIN_SMALL
   bool off_lines;        // rows that do not start on 128-byte lines
+  double us;             // the plan's time by the model
   float* part;           // [SK][m][n] when the output goes there
 };
 
@@ -682,8 +683,7 @@ static double lin_slow(const LinGemm& g) {
   const double mb = 2e-6 * g.red * ((double)g.m + g.n);
   return (mb > 40 ? 1.6 : mb > 24 ? 1.2 : 1.0) * (g.off_lines ? 1.3 : 1.0);
 }
-// Sets g's plan and returns its time by the model.
-static double lin_plan(LinGemm& g, bool bf16_, bool may_split) {
+static void lin_plan(LinGemm& g, bool bf16_, bool may_split) {
   const int stages = lin_stages(g, bf16_);
   const double slow = lin_slow(g);
   double best = bf16_ ? cdiv(lin_tiles(g, LIN_BIG), 256) * (stages * 1.4 + 10.0) : 1e30;
@@ -699,7 +699,7 @@ static double lin_plan(LinGemm& g, bool bf16_, bool may_split) {
       }
     }
   lin_set(g, bf16_, tile, sk);
-  return best;
+  g.us = best;
 }
 
 // Rows per workgroup of k_lin_dz: 64 where that gives four workgroups per CU, fewer (at least 8) for
@@ -755,7 +755,7 @@ static bool lin_pair_plan(const LinShape& s, LinGemm& gx, LinGemm& gw) {
   // with over four rounds of tiles each product fills the chip by itself (16384 x 512 x 2048: 91 us
   // apart, 98 together)
   if (s.M == 0 || lin_tiles(gx, LIN_MID) + lin_tiles(gw, LIN_MID) > 1024) return false;
-  const double apart = lin_plan(gx, s.bf16, true) + lin_plan(gw, s.bf16, true);
+  const double apart = gx.us + gw.us;
   const int sx = lin_stages(gx, s.bf16), sw = lin_stages(gw, s.bf16), longest = sx > sw ? sx : sw;
   double best = 0.9 * apart;  // (its error, within which the simpler launches stay)
   int tile = 0, most = 0;
@@ -780,6 +780,8 @@ static bool lin_pair_plan(const LinShape& s, LinGemm& gx, LinGemm& gw) {
 }
 
 struct LinBwdWs {
+  LinGemm gx, gw;  // the plans
+  bool pair;
   void* dZ;
   float* db_part;
   float* part;    // of a product on its own, or dX's of a pair
@@ -797,11 +799,12 @@ static size_t lin_carve_bwd(const LinShape& s, void* base, LinBwdWs* w) {
   LinBwdWs q;
   q.dZ = take(s.act == LIN_NONE ? 0 : (size_t)s.M * NW * (s.bf16 ? 2 : 4));
   q.db_part = reinterpret_cast<float*>(take((size_t)cdiv(s.M, lin_dz_rows(s)) * NW * 4));
-  LinGemm gx = lin_gemm(s, LIN_DX), gw = lin_gemm(s, LIN_DW);
-  const bool pair = lin_pair_plan(s, gx, gw);
-  const size_t px = gx.SK > 1 ? lin_part_bytes(gx) : 0, pw = gw.SK > 1 ? lin_part_bytes(gw) : 0;
-  q.part_w = pair ? reinterpret_cast<float*>(take(pw)) : nullptr;
-  const size_t alone = pair || px > pw ? px : pw;
+  q.gx = lin_gemm(s, LIN_DX);
+  q.gw = lin_gemm(s, LIN_DW);
+  q.pair = lin_pair_plan(s, q.gx, q.gw);
+  const size_t px = q.gx.SK > 1 ? lin_part_bytes(q.gx) : 0, pw = q.gw.SK > 1 ? lin_part_bytes(q.gw) : 0;
+  q.part_w = q.pair ? reinterpret_cast<float*>(take(pw)) : nullptr;
+  const size_t alone = q.pair || px > pw ? px : pw;
   q.part = reinterpret_cast<float*>(take(alone));
   if (w) *w = q;
   return off;
@@ -926,7 +929,7 @@ static hipError_t lin_backward(const LinShape& s, const T* dY, const T* X, const
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
-  LinGemm gx = lin_gemm(s, LIN_DX), gw = lin_gemm(s, LIN_DW);
+  LinGemm gx = w.gx, gw = w.gw;
   gx.A = gw.A = none ? static_cast<const void*>(dY) : w.dZ;
   gx.lda = gw.lda = none ? s.ldy : NW;
   gx.B = W;
@@ -937,8 +940,7 @@ static hipError_t lin_backward(const LinShape& s, const T* dY, const T* X, const
   const LinEpi<T> ew = lin_epi<T>(nullptr, nullptr, 0, nullptr, 0, dW, s.K, LIN_NONE);
   const LinDb db{w.db_part, blocks, NW, dbias};
   // (the plan goes by the shape alone: a gradient asked for on its own has the pair's bits)
-  const bool pair = lin_pair_plan(s, gx, gw);
-  if (pair && dX && dW) {
+  if (w.pair && dX && dW) {
     gx.part = w.part;
     gw.part = w.part_w;
     if (gx.tile == LIN_SMALL) lin_pair_launch<T, LinSmall>(gx, ex, gw, ew, st);
@@ -953,7 +955,7 @@ static hipError_t lin_backward(const LinShape& s, const T* dY, const T* X, const
   if (dbias) k_lin_db<<<NW / LIN_DB_COLS, 256, 0, st>>>(db.part, db.blocks, db.np, db.db);
   hipError_t e = hipGetLastError();
   if (e == hipSuccess && dX) e = lin_run<LIN_DX>(gx, w.part, ex, st);
-  if (e == hipSuccess && dW) e = lin_run<LIN_DW>(gw, pair ? w.part_w : w.part, ew, st);
+  if (e == hipSuccess && dW) e = lin_run<LIN_DW>(gw, w.pair ? w.part_w : w.part, ew, st);
   return e;
 }
 
