@@ -9,8 +9,8 @@
 // A sequence is a run of tokens seq_off[s] .. seq_off[s+1] - 1; a token counts if it lies in one
 // and its mask byte is not zero.
 //
-// Forward: one workgroup of 16 waves per chunk of tokens (64, more where rows are short) reads the
-// logits once (the only large operand); it requests the whole chunk, its choices and the sequence
+// Forward: one workgroup per chunk of tokens (32 or 64, more where rows are short) reads the logits
+// once (the only large operand); it requests the whole chunk, its choices and the sequence
 // table together before it uses any, since at these sizes the length of the chain of dependent
 // loads, not their bytes, sets the time.
 // Where a chunk holds several sequences it is cut into pieces, and the piece of chunk c and
@@ -19,7 +19,7 @@
 // second launch adds the slots of a sequence in chunk order (in 64 bits), and its last workgroup
 // forms the two losses.  Where one chunk holds the whole batch, its workgroup writes the results
 // itself and there is no second launch.  No floating-point atomics: the order of every sum is fixed.
-// Measured: 16384 x 256 in 7 sequences 16.9 us (9.8 and 6.7 for the two launches; the 17.4 MB would
+// Measured: 16384 x 256 in 7 sequences 16.2 us (9.8 and 6.0 for the two launches; the 17.4 MB would
 // take 3.5), 256 x 8 in one launch 5.2; backward 32768 x 384, 101 MB, 19.3 us (5.2 TB/s).
 //
 // A token is taken by G lanes, each holding up to 4 NV of its logits (four consecutive ones per
@@ -31,8 +31,8 @@
 namespace moe {
 
 constexpr int RL_BWD_CHUNK = 64;  // tokens per workgroup of the backward, less where T gives under two per CU
-constexpr int RL_THREADS = 1024;
-constexpr int RL_WAVES = RL_THREADS / 64;
+constexpr int RL_JOIN_THREADS = 512;  // (1024 threads in both launches: 16384 x 256 16.7 us, 15.9 so)
+constexpr int RL_MAX_WAVES = 16;
 constexpr int RL_JOIN_COLS = 32;      // columns per workgroup of the joining launch
 constexpr int RL_BWD_THREADS = 256;
 // A chunk of more than RL_FEW pieces leaves those of up to RL_SHORT rounds of a wave's tokens to single
@@ -70,10 +70,24 @@ static RlLayout rl_layout(int E) {
   if (q <= 128) return {64, 2};
   return {64, 4};
 }
-// Steps of the forward's workgroup over its chunk, and the chunk's tokens.
-__host__ __device__ constexpr int rl_steps(int G) { return G > 16 ? G / 16 : 1; }
-__host__ __device__ constexpr int rl_chunk(int G) { return RL_WAVES * (64 / G) * rl_steps(G); }
-static int64_t rl_chunks(int64_t T, int E) { return cdiv(T, rl_chunk(rl_layout(E).G)); }
+// The forward's workgroup: 16 waves where it holds the whole batch (one per short sequence), else 8.
+// It takes its chunk in steps of a token per lane group; where rows are long and the longer chunks
+// still give every CU one, twice as many (fewer sums to join: 32768 x 384 22.7 us against 26.4, but
+// 4096 x 256 in 64 sequences 23.6 against 19.6).
+__host__ __device__ constexpr int rl_waves(bool one) { return one ? 16 : 8; }
+__host__ __device__ constexpr int rl_steps(int G, bool longer) { return G > 16 ? (longer ? G / 8 : G / 16) : 1; }
+__host__ __device__ constexpr int rl_chunk(int G, bool one, bool longer) { return rl_waves(one) * (64 / G) * rl_steps(G, longer); }
+struct RlGrid {
+  bool one, longer;
+  int chunk;
+};
+static RlGrid rl_grid(int64_t T, int E) {
+  const int G = rl_layout(E).G;
+  if (T <= rl_chunk(G, true, false)) return {true, false, rl_chunk(G, true, false)};
+  const bool longer = G > 16 && cdiv(T, rl_chunk(G, false, true)) >= 256;
+  return {false, longer, rl_chunk(G, false, longer)};
+}
+static int64_t rl_chunks(int64_t T, int E) { return cdiv(T, rl_grid(T, E).chunk); }
 static int rl_colblocks(int E) { return (E + RL_JOIN_COLS - 1) / RL_JOIN_COLS; }
 
 static size_t rl_carve(void* base, int64_t T, int E, int n_seq, RlossWs* w) {
@@ -271,12 +285,12 @@ struct RlossOut {
   float* loss;
 };
 
-constexpr int RL_RUNS = RL_THREADS / RL_JOIN_COLS;
+constexpr int RL_RUNS = RL_JOIN_THREADS / RL_JOIN_COLS;
 struct RlJoinLds {
-  double p[RL_WAVES][RL_JOIN_COLS];
-  int c[RL_WAVES][RL_JOIN_COLS];
-  double z[RL_WAVES], b[RL_WAVES];
-  long long n[RL_WAVES];
+  double p[RL_JOIN_THREADS / 64][RL_JOIN_COLS];
+  int c[RL_JOIN_THREADS / 64][RL_JOIN_COLS];
+  double z[RL_MAX_WAVES], b[RL_MAX_WAVES];
+  long long n[RL_MAX_WAVES];
   int last;
 };
 
@@ -285,7 +299,7 @@ __device__ __forceinline__ void rl_write_loss(const RlossOut& o, int E, int K, d
   o.loss[1] = n ? (float)(z / (double)n) : 0.0f;
 }
 
-// Adds sequence s's slots for columns block cb in a fixed order: 32 columns by 32 runs of chunks, then
+// Adds sequence s's slots for columns block cb in a fixed order: 32 columns by 16 runs of chunks, then
 // the runs by waves (two each).  Also the sequence's tokens and z sum when cb is 0.
 __device__ __forceinline__ void rl_join(RlJoinLds& L, int s, int cb, int chunk, int T, int E,
                                         const int32_t* __restrict__ seq_off, const RlossWs& w, const RlossOut& o) {
@@ -314,7 +328,7 @@ __device__ __forceinline__ void rl_join(RlJoinLds& L, int s, int cb, int chunk, 
   if (cb == 0) {
     double z = 0.0;
     long long n = 0;
-    for (int c = c0 + (int)threadIdx.x; c < c1; c += RL_THREADS) {
+    for (int c = c0 + (int)threadIdx.x; c < c1; c += RL_JOIN_THREADS) {
       z += (double)w.z[c + s];
       n += w.tok[c + s];
     }
@@ -333,7 +347,7 @@ __device__ __forceinline__ void rl_join(RlJoinLds& L, int s, int cb, int chunk, 
     double ps = 0.0;
     int cs = 0;
 #pragma unroll
-    for (int r = 0; r < RL_WAVES; ++r) {
+    for (int r = 0; r < RL_JOIN_THREADS / 64; ++r) {
       ps += L.p[r][ci];
       cs += L.c[r][ci];
     }
@@ -349,7 +363,7 @@ __device__ __forceinline__ void rl_join(RlJoinLds& L, int s, int cb, int chunk, 
   if (cb == 0 && threadIdx.x == 64) {
     double z = 0.0;
     long long n = 0;
-    for (int q = 0; q < RL_WAVES; ++q) {
+    for (int q = 0; q < RL_JOIN_THREADS / 64; ++q) {
       z += L.z[q];
       n += L.n[q];
     }
@@ -366,7 +380,7 @@ __device__ __forceinline__ void rl_losses(RlJoinLds& L, int E, int K, int n_seq,
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   double bsum = 0.0, zsum = 0.0;
   long long n = 0;
-  for (int q = threadIdx.x; q < n_seq; q += RL_THREADS) {
+  for (int q = threadIdx.x; q < n_seq; q += blockDim.x) {
     const int tq = rl_get(&o.seq_tokens[q]);
     double bq = 0.0;
     for (int k = 0; k < cbs; ++k) bq += rl_get(&w.bal[(int64_t)q * cbs + k]);
@@ -392,7 +406,7 @@ __device__ __forceinline__ void rl_losses(RlJoinLds& L, int E, int K, int n_seq,
   if (threadIdx.x == 0) {
     bsum = zsum = 0.0;
     n = 0;
-    for (int q = 0; q < RL_WAVES; ++q) {
+    for (int q = 0; q < (int)blockDim.x / 64; ++q) {
       bsum += L.b[q];
       zsum += L.z[q];
       n += L.n[q];
@@ -401,19 +415,20 @@ __device__ __forceinline__ void rl_losses(RlJoinLds& L, int E, int K, int n_seq,
   }
 }
 
-template <int G, int NV, bool V4, bool ONE>
-__global__ __launch_bounds__(RL_THREADS) void k_rloss_part(const float* __restrict__ logits,
+template <int G, int NV, bool V4, bool ONE, bool LONGER>
+__global__ __launch_bounds__(rl_waves(ONE) * 64) void k_rloss_part(const float* __restrict__ logits,
                                                            const int32_t* __restrict__ topk_idx, int T, int E, int K,
                                                            int n_seq, const int32_t* __restrict__ seq_off,
                                                            const uint8_t* __restrict__ mask, float* __restrict__ lse,
                                                            RlossWs w, RlossOut o) {
   using Row = RlRow<G, NV, V4>;
-  constexpr int N = Row::N, TPW = 64 / G, STEPS = rl_steps(G), CHUNK = rl_chunk(G);
+  constexpr int N = Row::N, TPW = 64 / G, WAVES = rl_waves(ONE), THREADS = 64 * WAVES;
+  constexpr int STEPS = rl_steps(G, LONGER), CHUNK = rl_chunk(G, ONE, LONGER);
   extern __shared__ float rl_lds[];  // [waves][E] probability sums, [E] counts
-  int* hist = reinterpret_cast<int*>(rl_lds + RL_WAVES * E);
-  __shared__ float sz[RL_WAVES];
-  __shared__ int sn[RL_WAVES];
-  __shared__ double sb[RL_WAVES];
+  int* hist = reinterpret_cast<int*>(rl_lds + WAVES * E);
+  __shared__ float sz[WAVES];
+  __shared__ int sn[WAVES];
+  __shared__ double sb[WAVES];
   __shared__ RlTable tab;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, li = lane % G, grp = lane / G;
   const int t_begin = blockIdx.x * CHUNK, t_end = min(T, t_begin + CHUNK);
@@ -422,7 +437,7 @@ __global__ __launch_bounds__(RL_THREADS) void k_rloss_part(const float* __restri
   bool live[STEPS];
 #pragma unroll
   for (int i = 0; i < STEPS; ++i) {
-    const int t = min(t_begin + (i * RL_WAVES + wave) * TPW + grp, T - 1);
+    const int t = min(t_begin + (i * WAVES + wave) * TPW + grp, T - 1);
     Row::load(logits + (int64_t)t * E, li, E, x[i]);
     live[i] = !mask || mask[t];
   }
@@ -432,9 +447,9 @@ __global__ __launch_bounds__(RL_THREADS) void k_rloss_part(const float* __restri
   const bool first_live = !mask || ((int)threadIdx.x < picks && mask[first_t]);
   rl_table_load(tab, seq_off, n_seq, T);
   if (!ONE && blockIdx.x == 0 && threadIdx.x == 0) *w.ticket = 0u;
-  for (int e = threadIdx.x; e < E; e += RL_THREADS) hist[e] = 0;
+  for (int e = threadIdx.x; e < E; e += THREADS) hist[e] = 0;
   if constexpr (ONE) {  // sequences without tokens have no piece
-    for (int i = threadIdx.x; i < n_seq * E; i += RL_THREADS) {
+    for (int i = threadIdx.x; i < n_seq * E; i += THREADS) {
       const int s = i / E;
       if (rl_off(seq_off, s + 1, T) <= rl_off(seq_off, s, T)) {
         o.prob_sum[i] = 0.0f;
@@ -448,7 +463,7 @@ __global__ __launch_bounds__(RL_THREADS) void k_rloss_part(const float* __restri
 #pragma unroll
   for (int i = 0; i < STEPS; ++i) {
     const float l = rl_softmax<G>(x[i], l2[i]);
-    const int t = t_begin + (i * RL_WAVES + wave) * TPW + grp;
+    const int t = t_begin + (i * WAVES + wave) * TPW + grp;
     if (li == 0 && t < t_end) lse[t] = l;
   }
   __syncthreads();
@@ -476,7 +491,7 @@ __global__ __launch_bounds__(RL_THREADS) void k_rloss_part(const float* __restri
     int n = 0;
 #pragma unroll
     for (int i = 0; i < STEPS; ++i) {
-      const int t = t_begin + (i * RL_WAVES + wave) * TPW + grp;
+      const int t = t_begin + (i * WAVES + wave) * TPW + grp;
       if (t >= a && t < b && live[i]) {
         ++n;
         z += l2[i];
@@ -486,7 +501,7 @@ __global__ __launch_bounds__(RL_THREADS) void k_rloss_part(const float* __restri
     }
     if ((int)threadIdx.x < picks && first_t >= a && first_t < b && (uint32_t)first < (uint32_t)E && first_live)
       atomicAdd(&hist[first], 1);
-    for (int i = threadIdx.x + RL_THREADS; i < picks; i += RL_THREADS) {
+    for (int i = threadIdx.x + THREADS; i < picks; i += THREADS) {
       const int t = t_begin + i / K, e = topk_idx[(int64_t)t_begin * K + i];
       if (t >= a && t < b && (uint32_t)e < (uint32_t)E && (!mask || mask[t])) atomicAdd(&hist[e], 1);
     }
@@ -506,10 +521,10 @@ __global__ __launch_bounds__(RL_THREADS) void k_rloss_part(const float* __restri
     __syncthreads();
     const int64_t slot = (int64_t)blockIdx.x + s;
     double bal = 0.0;
-    for (int e = threadIdx.x; e < E; e += RL_THREADS) {
+    for (int e = threadIdx.x; e < E; e += THREADS) {
       float v = 0.0f;
 #pragma unroll
-      for (int q = 0; q < RL_WAVES; ++q) v += rl_lds[q * E + e];
+      for (int q = 0; q < WAVES; ++q) v += rl_lds[q * E + e];
       const int c = hist[e];
       hist[e] = 0;
       if constexpr (ONE) {
@@ -531,14 +546,14 @@ __global__ __launch_bounds__(RL_THREADS) void k_rloss_part(const float* __restri
       float zs = 0.0f;
       int ns = 0;
 #pragma unroll
-      for (int q = 0; q < RL_WAVES; ++q) {
+      for (int q = 0; q < WAVES; ++q) {
         zs += sz[q];
         ns += sn[q];
       }
       if constexpr (ONE) {
         double bs = 0.0;
 #pragma unroll
-        for (int q = 0; q < RL_WAVES; ++q) bs += sb[q];
+        for (int q = 0; q < WAVES; ++q) bs += sb[q];
         if (many) {
           rl_put(&w.bal[s], bs);
           rl_put(&w.zs[s], (double)zs);
@@ -558,7 +573,7 @@ __global__ __launch_bounds__(RL_THREADS) void k_rloss_part(const float* __restri
   }
   if (many) {
     int* cnt = reinterpret_cast<int*>(rl_lds) + wave * E;  // the wave's own counts
-    for (int s = s0 + wave; s <= s1; s += RL_WAVES) {
+    for (int s = s0 + wave; s <= s1; s += WAVES) {
       const int a = __builtin_amdgcn_readfirstlane(max(off(s), t_begin)), b = __builtin_amdgcn_readfirstlane(min(off(s + 1), t_end));
       if (b <= a || b - a > RL_SHORT * TPW) continue;
       for (int e = lane; e < E; e += 64) cnt[e] = 0;
@@ -630,7 +645,7 @@ __global__ __launch_bounds__(RL_THREADS) void k_rloss_part(const float* __restri
 
 // The joining launch, one workgroup per sequence and block of 32 columns; the last one to finish
 // forms the losses.
-__global__ __launch_bounds__(RL_THREADS) void k_rloss_join(int T, int E, int K, int n_seq, int chunk,
+__global__ __launch_bounds__(RL_JOIN_THREADS) void k_rloss_join(int T, int E, int K, int n_seq, int chunk,
                                                            const int32_t* __restrict__ seq_off, RlossWs w, RlossOut o) {
   __shared__ RlJoinLds L;
   const int cbs = (E + RL_JOIN_COLS - 1) / RL_JOIN_COLS;
@@ -744,12 +759,16 @@ struct RlossFwd {
   hipStream_t st;
   template <int G, int NV, bool V4>
   void operator()() const {
-    const size_t lds = (size_t)(RL_WAVES + 1) * E * 4;
-    if (rl_chunks(T, E) == 1)
-      k_rloss_part<G, NV, V4, true><<<1, RL_THREADS, lds, st>>>(logits, topk_idx, T, E, K, n_seq, seq_off, mask, lse, w, o);
-    else
-      k_rloss_part<G, NV, V4, false><<<(int)rl_chunks(T, E), RL_THREADS, lds, st>>>(logits, topk_idx, T, E, K, n_seq, seq_off,
-                                                                                 mask, lse, w, o);
+    const RlGrid g = rl_grid(T, E);
+    const int grid = (int)cdiv(T, g.chunk), threads = 64 * rl_waves(g.one);
+    const size_t lds = (size_t)(rl_waves(g.one) + 1) * E * 4;
+    auto go = [&](auto kernel) {
+      kernel<<<grid, threads, lds, st>>>(logits, topk_idx, T, E, K, n_seq, seq_off, mask, lse, w, o);
+    };
+    if (g.one) return go(k_rloss_part<G, NV, V4, true, false>);
+    if constexpr (G > 16)
+      if (g.longer) return go(k_rloss_part<G, NV, V4, false, true>);
+    go(k_rloss_part<G, NV, V4, false, false>);
   }
 };
 struct RlossBwd {
@@ -780,8 +799,9 @@ hipError_t launch_router_loss(const float* logits, const int32_t* topk_idx, int6
   const RlossOut o{seq_tokens, seq_counts, prob_sum, loss};
   rl_dispatch(E, RlossFwd{logits, topk_idx, (int)T, E, K, n_seq, seq_off, mask, lse, w, o, st});
   const hipError_t e = hipGetLastError();
-  if (e != hipSuccess || rl_chunks(T, E) == 1) return e;
-  k_rloss_join<<<n_seq * rl_colblocks(E), RL_THREADS, 0, st>>>((int)T, E, K, n_seq, rl_chunk(rl_layout(E).G), seq_off, w, o);
+  const RlGrid g = rl_grid(T, E);
+  if (e != hipSuccess || g.one) return e;
+  k_rloss_join<<<n_seq * rl_colblocks(E), RL_JOIN_THREADS, 0, st>>>((int)T, E, K, n_seq, g.chunk, seq_off, w, o);
   return hipGetLastError();
 }
 
