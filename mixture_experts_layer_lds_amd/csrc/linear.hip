@@ -748,9 +748,9 @@ size_t linear_fwd_workspace_bytes(const LinShape& s) {
 // The backward's two products in one launch, each cut so that no workgroup has more than `most` stages
 // (a batch of many rows has a short reduction for dX and a long one for dW): where the model says
 // that this beats one after the other.  999 x 1000 x 264, ReLU with a bias: 26 us in six launches,
-// 20 in three; 25.9 unsliced, 20.8 with 2 slices, 20.2 with 3, 24.8 with 8.  12062 x 296 x 424:
-// 50 us apart, 41 together; 2048 x 2048 x 2048: 54 and 47.  False: one after the other, each with a plan of its own, in gx
-// and gw.
+// 17 in three (on 128 x 128 tiles 25.9 unsliced, 20.8 with 2 slices, 20.2 with 3, 24.8 with 8);
+// 12062 x 296 x 424: 50 us apart, 41 together; 2048 x 2048 x 2048: 54 and 47.  False: one after the
+// other, each with a plan of its own, in gx and gw.
 static bool lin_pair_plan(const LinShape& s, LinGemm& gx, LinGemm& gw) {
   // with over four rounds of tiles each product fills the chip by itself (16384 x 512 x 2048: 91 us
   // apart, 98 together)

@@ -659,9 +659,10 @@ __global__ __launch_bounds__(RL_JOIN_THREADS) void k_rloss_join(int T, int E, in
   rl_losses(L, E, K, n_seq, cbs, w, o);
 }
 
-// dLogits.  A group of lanes keeps its sequence's counts as long as its tokens stay in it.  The counts enter less their mean K T_s / E: the
-// probabilities of a row sum to one, so the mean drops out of the difference, and without it the
-// difference of two nearly equal numbers would lose the leading bits.
+// dLogits.  A group of lanes keeps its sequence's counts as long as its tokens stay in it.  The
+// counts enter less their mean K T_s / E: the probabilities of a row sum to one, so the mean drops
+// out of the difference, and without it the difference of two nearly equal numbers would lose the
+// leading bits.
 template <int G, int NV, bool V4>
 __global__ __launch_bounds__(RL_BWD_THREADS) void k_rloss_bwd(const float* __restrict__ dloss,
                                                           const float* __restrict__ logits, int T, int E, int K,
