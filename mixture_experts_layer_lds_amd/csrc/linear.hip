@@ -44,7 +44,7 @@ __device__ __forceinline__ float normal_tail(float z, float* e) {
   return p * t * *e;
 }
 
-// act(z) of one element and its derivative (not SwiGLU).  GELU is the exact form
+// act(z) of one element (not SwiGLU).  GELU is the exact form
 // z Phi(z) = max(z, 0) - |z| tail(|z|).
 template <int ACT>
 __device__ __forceinline__ float lin_act1(float z) {
@@ -57,19 +57,20 @@ __device__ __forceinline__ float lin_act1(float z) {
   if constexpr (ACT == LIN_SILU) return z * sigmoid_f32(z);
   return z;
 }
+// dy act'(z).  ReLU selects: where its unit is off, dy adds nothing even if it is infinite or NaN.
 template <int ACT>
-__device__ __forceinline__ float lin_grad1(float z) {
-  if constexpr (ACT == LIN_RELU) return z > 0.0f ? 1.0f : 0.0f;
+__device__ __forceinline__ float lin_bwd1(float dy, float z) {
+  if constexpr (ACT == LIN_RELU) return z > 0.0f ? dy : 0.0f;
   if constexpr (ACT == LIN_GELU) {
     float e;
     const float q = normal_tail(z, &e);
-    return (z < 0.0f ? q : 1.0f - q) + (e != 0.0f ? z : 0.0f) * e * 0.39894228040143268f;
+    return dy * ((z < 0.0f ? q : 1.0f - q) + (e != 0.0f ? z : 0.0f) * e * 0.39894228040143268f);
   }
   if constexpr (ACT == LIN_SILU) {
     const float s = sigmoid_f32(z);
-    return s * (1.0f + z * (1.0f - s));
+    return dy * (s * (1.0f + z * (1.0f - s)));
   }
-  return 1.0f;
+  return dy;
 }
 // f(integral_constant<int, act>) for the activation act (SwiGLU as NONE: it is not elementwise).
 template <class F>
@@ -598,7 +599,7 @@ __global__ __launch_bounds__(256) void k_lin_dz(const T* __restrict__ dY, int64_
         lin_by_act(act, [&](auto A) {
 #pragma unroll
           for (int u = 0; u < 8; ++u) {
-            if constexpr (decltype(A)::value != LIN_NONE) dy[u] *= lin_grad1<decltype(A)::value>(z[u]);
+            dy[u] = lin_bwd1<decltype(A)::value>(dy[u], z[u]);
             s0[u] += dy[u];
           }
         });

@@ -34,7 +34,7 @@ def activation(z, act):
 def activation_backward(dy, z, act):
     """dL/dz from dL/d act(z)."""
     if act == "relu":
-        return dy * (z > 0)
+        return np.where(z > 0, dy, 0.0)  # a unit that is off passes nothing on, whatever dy holds
     if act == "gelu":
         return dy * (_phi(z) + z * np.exp(-0.5 * z * z) / math.sqrt(2.0 * math.pi))
     if act == "silu":

@@ -287,3 +287,21 @@ def test_large_tiles_with_partial_stages(M, N, K):
     assert torch.equal(out, (X @ W.t()).bfloat16())
     assert torch.equal(dX, (dY @ W).bfloat16())
     assert torch.equal(dW, (dY.t() @ X).bfloat16())
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("M,N,K", [(3, 72, 64), (300, 264, 136)])
+def test_relu_gradient_of_units_that_are_off(M, N, K, dtype):
+    """An infinite or NaN dY where z <= 0 adds nothing to any gradient: the same bits as with zeros there."""
+    p = Proj(M, N, K, dtype, "relu", True, False, False, pad=8)
+    p.Zs = torch.randn(M, N, generator=torch.Generator(device="cuda").manual_seed(6), device="cuda").to(DT[dtype])
+    p.Zs[0, :8] = 0.0
+    off = p.Zs <= 0
+    p.dY[off] = 0.0
+    p.backward()
+    want = [t.clone() for t in (p.dX, p.dW[:p.NW], p.db[:p.NW])]
+    bad = torch.tensor([float("inf"), float("nan"), -float("inf")], device="cuda").to(DT[dtype])
+    p.dY[off] = bad[torch.arange(int(off.sum()), device="cuda") % 3]
+    p.backward()
+    for got, ref in zip((p.dX, p.dW[:p.NW], p.db[:p.NW]), want):
+        assert ref.isfinite().all() and torch.equal(got, ref)

@@ -43,6 +43,16 @@ def test_activations_match_torch(act):
     assert np.allclose(ob.activation(z, act), ref.numpy(), rtol=1e-13, atol=1e-15)
 
 
+def test_relu_gradient_selects():
+    """Where a unit is off its gradient is 0 for any dy, as torch's own."""
+    z = np.array([[-1.0, 0.0, 2.0, -3.0, -0.0, 1.0]])
+    dy = np.array([[np.inf, np.nan, np.inf, -np.inf, 5.0, -2.0]])
+    x = torch.tensor(z, requires_grad=True)
+    torch.relu(x).backward(torch.tensor(dy))
+    got = ob.activation_backward(dy, z, "relu")
+    assert np.array_equal(got, [[0.0, 0.0, np.inf, 0.0, 0.0, -2.0]]) and np.array_equal(got, x.grad.numpy())
+
+
 def test_router_losses_even_load_is_one_and_matches_autograd():
     T, E, K = 24, 6, 2
     logits = torch.zeros(T, E, dtype=torch.float64)
