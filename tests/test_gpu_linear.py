@@ -305,3 +305,38 @@ def test_relu_gradient_of_units_that_are_off(M, N, K, dtype):
     p.backward()
     for got, ref in zip((p.dX, p.dW[:p.NW], p.db[:p.NW]), want):
         assert ref.isfinite().all() and torch.equal(got, ref)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("M", [16, 4096])
+def test_gelu_keeps_its_digits(M, dtype):
+    """GELU and its derivative relative to the tail Q(|z|) = Phi(-|z|), which both are made of.  With one
+    column of ones as W, z is X exactly.  The tail is a reciprocal, nine multiply-adds, an exponential
+    and two products, 16 roundings of 2^-24 at most, and the exponential's argument z^2 / 2 has three of its
+    own: Q is off by Q (2^-20 + z^2 2^-23), and where it goes into a bf16 result by 2^-17 more (its
+    polynomial is then cut at 4.7e-6).  out = max(z, 0) - |z| Q adds a rounding of 2^-24 (and that of
+    the type); the derivative's z exp(-z^2 / 2) / sqrt(2 pi) three products and the exponential, and the
+    sum is rounded."""
+    z = torch.linspace(-12, 12, M + 1)[:M].to(DT[dtype])
+    X, W = torch.zeros(M, 8, dtype=DT[dtype], device="cuda"), torch.zeros(8, 8, dtype=DT[dtype], device="cuda")
+    X[:, 0], W[:, 0] = z.cuda(), 1.0
+    dims = B.make_linear_dims(M, 8, 8, dtype, "gelu")
+    ws, nb = B.linear_workspace(dims, B.LINEAR_FORWARD)
+    out = torch.empty(M, 8, dtype=DT[dtype], device="cuda")
+    B.moe_linear(dims, X, W, None, None, None, out, ws, nb)
+    v = f64(z)[:, None]
+    q, a = ob._phi(-np.abs(v)), np.abs(v)
+    rel = 2.0 ** -20 + v * v * 2.0 ** -23
+    cut = rel + (2.0 ** -17 if dtype == "bf16" else 0.0)
+    ref = ob.activation(v, "gelu")
+    assert_within("out", f64(out), np.repeat(ref, 8, 1), (a * q * cut + (HALF[dtype] + U32) * np.abs(ref)) * np.ones(8) + 1e-36)
+    # the derivative through the bias gradient of single rows (fp32 whatever the type)
+    phi = np.exp(-0.5 * v * v) / np.sqrt(2 * np.pi)
+    want = ob.activation_backward(np.ones_like(v), v, "gelu")
+    tol = q * rel + a * phi * (2.0 ** -21 + v * v * 2.0 ** -23) + U32 * (np.where(v < 0, q, 1.0) + a * phi) + 1e-36
+    one = B.make_linear_dims(1, M, 8, dtype, "gelu")
+    wb, nbb = B.linear_workspace(one, B.LINEAR_BACKWARD)
+    db, dY = torch.empty(M, device="cuda"), torch.ones(1, M, dtype=DT[dtype], device="cuda")
+    B.moe_linear_backward(one, dY, X[:1], torch.zeros(M, 8, dtype=DT[dtype], device="cuda"), z.cuda()[None].contiguous(),
+                          None, None, db, wb, nbb)
+    assert_within("derivative", f64(db)[:, None], want, tol)
