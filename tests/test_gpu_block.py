@@ -146,3 +146,38 @@ def test_backward_aux_without_router_weights_and_with_null_aux():
 def test_block_graph_replays_match_eager():
     b = Block(wl.small_shape(T=400, d=256, E=8, K=2, n=128, dtype="bf16", backward=True, seed=12))
     check_replays(b.step, b.outs())
+
+
+# E a multiple of the stage's 64 (32) rows of W_r and not, one stage to sixteen; 4096 x 4096 in bf16 fills the
+# chip with 256 x 256 tiles
+@pytest.mark.parametrize("T,d,E,dtype", [
+    (500, 256, 67, "f32"), (500, 256, 130, "f32"), (333, 320, 250, "f32"), (500, 256, 256, "f32"), (300, 192, 384, "f32"), (200, 128, 1001, "f32"),
+    (500, 256, 67, "bf16"), (500, 256, 130, "bf16"), (333, 320, 250, "bf16"), (500, 256, 256, "bf16"), (300, 192, 384, "bf16"), (200, 128, 1001, "bf16"),
+    (4096, 4096, 379, "bf16"), (4090, 4096, 384, "bf16"),
+])
+def test_backward_aux_of_many_experts(T, d, E, dtype):
+    """dX is the expert path's (the call without W_r) plus dLogits W_r with dLogits rounded to the type: a
+    product of E terms on top of a rounded value, rounded once more."""
+    cfg = wl.small_shape(T=T, d=d, E=E, K=2, n=64, dtype=dtype, backward=True, seed=E)
+    b = Block(cfg)
+    b.step()
+    i, aux = b.inp, torch.randn(T, E, generator=torch.Generator(device="cuda").manual_seed(E), device="cuda")
+
+    def run(W_r, dWr):
+        o = [torch.full_like(t, 7.0) for t in (b.dX, b.dWg, b.dWu, b.dWdn, b.dS, b.dL, b.dWr)]
+        B.moe_backward_aux(b.dims, b.dYm, i["X"], W_r, i["W_gate"], i["W_up"], i["W_down"], b.plan, b.H, aux, *o[:6],
+                           o[6] if dWr else None, *b.ws[B.OP_BACKWARD])
+        return o
+
+    only, full = run(None, False), run(i["W_r"], True)
+    assert torch.equal(only[5], full[5])
+    X = i["X"].double()
+    L, W, base = full[5].to(cfg.torch_dtype).double(), i["W_r"].double(), only[0].double()
+    h = 2.0 ** -8 if dtype == "bf16" else 2.0 ** -24
+    for name, got, first, A, C in (("dX", full[0], base, L, W), ("dW_r", full[6], 0 * W, L.t(), X)):
+        ref = first + A @ C
+        err = (A.shape[1] + 8) * 2.0 ** -23 * (first.abs() + A.abs() @ C.abs())
+        off, tol = (got.double() - ref).abs(), h * (ref.abs() + err) + err
+        assert bool((off <= tol).all()), "%s: worst %.3g" % (name, (off / tol.clamp(min=1e-30)).max().item())
+        # the product is not lost among the rounding
+        assert ((A @ C).abs() > tol).float().mean().item() > 0.5
