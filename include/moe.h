@@ -349,6 +349,13 @@ enum { MOE_LINEAR_FORWARD = 0, MOE_LINEAR_BACKWARD = 1 };
  * moe_last_error() set). */
 size_t moe_linear_workspace_bytes(const moe_linear_dims* dims, int op);
 
+/* Host: how a product is cut into workgroups, for measurement tools and tests.  Returns the edge of its
+ * output tiles (0: the streaming kernel of a few rows), or a negative moe_status; *slices (may be
+ * NULL) receives the parts that its reduction is cut into, *paired (may be NULL) 1 where the
+ * backward's two products go out in one launch. */
+enum { MOE_LINEAR_OUT = 0, MOE_LINEAR_DX = 1, MOE_LINEAR_DW = 2 };
+int moe_linear_plan(const moe_linear_dims* dims, int product, int32_t* slices, int32_t* paired);
+
 /* moe_linear — X [M,K], W [N',K], bias [N'] fp32 or NULL, residual [M,N] or NULL (it may be out, with
  * the same stride), out [M,N].  out and Z overlap no other argument.  Z [M,N'] or NULL: receives z rounded to dtype, for the backward.  The activation and
  * the residual sum work on fp32 values; out is rounded once.  M = 0 does nothing.

@@ -23,6 +23,7 @@ OP_ROUTE, OP_PERMUTE, OP_FFN, OP_COMBINE, OP_FORWARD, OP_BACKWARD, OP_DECODE, OP
 FP8_E4M3, FP8_E5M2 = 0, 1
 ACTS = {"none": 0, "relu": 1, "gelu": 2, "silu": 3, "swiglu": 4}
 LINEAR_FORWARD, LINEAR_BACKWARD = 0, 1
+LINEAR_OUT, LINEAR_DX, LINEAR_DW = 0, 1, 2
 STATUS = {0: "MOE_OK", -1: "MOE_EINVAL", -2: "MOE_ENOTSUP", -3: "MOE_EWORKSPACE", -4: "MOE_EHIP"}
 
 EXPORTS = ["moe_max_rows", "moe_workspace_bytes", "moe_route", "moe_permute", "moe_grouped_ffn",
@@ -33,7 +34,7 @@ EXPORTS = ["moe_max_rows", "moe_workspace_bytes", "moe_route", "moe_permute", "m
            "moe_grouped_ffn_fp8", "moe_status_string", "moe_last_error",
            "moe_backward_aux", "moe_router_loss", "moe_router_loss_backward",
            "moe_router_loss_workspace_bytes", "moe_dropout", "moe_combine_dropout", "moe_linear",
-           "moe_linear_backward", "moe_linear_workspace_bytes",
+           "moe_linear_backward", "moe_linear_workspace_bytes", "moe_linear_plan",
            "moe_version", "moe_timing_enable", "moe_timing_read"]
 STAGES = ["router_gemm", "route", "tiles", "up_gemm", "down_gemm", "permute", "combine", "dact_gemm",
           "dw_down_gemm", "dw_gu_gemm", "dx_gemm", "router_bwd", "dwr_gemm", "decode", "fp8_quant",
@@ -111,6 +112,8 @@ def lib():
         L.moe_dropout.argtypes = [i64, i64, ctypes.c_int, vp, i64, vp, i64, ctypes.c_double, vp, vp, i64, vp]
         L.moe_combine_dropout.argtypes = [pd, pp, vp, ctypes.c_int, vp, ctypes.c_double, vp, vp, vp]
         L.moe_linear_workspace_bytes.argtypes, L.moe_linear_workspace_bytes.restype = [pl, ctypes.c_int], sz
+        L.moe_linear_plan.argtypes = [pl, ctypes.c_int, ctypes.POINTER(i32), ctypes.POINTER(i32)]
+        L.moe_linear_plan.restype = ctypes.c_int
         L.moe_linear.argtypes = [pl, vp, vp, vp, vp, vp, vp, vp, sz, vp]
         L.moe_linear_backward.argtypes = [pl, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp]
         for f in ("moe_backward_aux", "moe_router_loss", "moe_router_loss_backward", "moe_dropout",
@@ -398,6 +401,15 @@ def moe_linear_workspace_bytes(dims, op):
 def linear_workspace(dims, op, device="cuda"):
     nbytes = moe_linear_workspace_bytes(dims, op)
     return torch.empty(max(nbytes, 256), dtype=torch.uint8, device=device), nbytes
+
+
+def moe_linear_plan(dims, product):
+    """(tile edge, slices of the reduction, whether dX and dW share a launch) of one product."""
+    slices, paired = ctypes.c_int32(), ctypes.c_int32()
+    tile = lib().moe_linear_plan(ctypes.byref(dims), product, ctypes.byref(slices), ctypes.byref(paired))
+    if tile < 0:
+        _check(tile)
+    return tile, slices.value, bool(paired.value)
 
 
 def moe_linear(dims, X, W, bias, residual, Z, out, ws, ws_bytes, stream=None):

@@ -151,6 +151,8 @@ struct LinShape {
 };
 size_t linear_fwd_workspace_bytes(const LinShape& s);
 size_t linear_bwd_workspace_bytes(const LinShape& s);
+// product 0 (forward), 1 (dX) or 2 (dW): tile edge (0: streamed), slices, and whether dX and dW are paired
+int linear_plan(const LinShape& s, int product, int* slices, bool* paired);
 // out = residual + act(X W^T + bias), Z = X W^T + bias; bias, residual and Z may be null
 hipError_t launch_linear(const LinShape& s, const void* X, const void* W, const float* bias, const void* residual,
                          void* Z, void* out, void* ws, hipStream_t st);

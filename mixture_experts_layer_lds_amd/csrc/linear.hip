@@ -836,6 +836,23 @@ static size_t lin_carve_bwd(const LinShape& s, void* base, LinBwdWs* w) {
 
 size_t linear_bwd_workspace_bytes(const LinShape& s) { return lin_carve_bwd(s, nullptr, nullptr); }
 
+int linear_plan(const LinShape& s, int product, int* slices, bool* paired) {
+  *slices = 1;
+  *paired = false;
+  if (product == LIN_FWD && lin_is_skinny(s)) return 0;
+  LinBwdWs w;
+  LinGemm g;
+  if (product == LIN_FWD) {
+    g = lin_gemm(s, LIN_FWD);
+  } else {
+    lin_carve_bwd(s, nullptr, &w);
+    g = product == LIN_DX ? w.gx : w.gw;
+    *paired = w.pair;
+  }
+  *slices = g.SK;
+  return g.tile;
+}
+
 template <typename T, class TI, int MODE, int OUT>
 static void lin_launch_t(const LinGemm& g, const LinEpi<T>& ep, hipStream_t st) {
   const int grid = grid8((int64_t)g.MT * g.NT * g.SK);

@@ -795,6 +795,18 @@ size_t moe_linear_workspace_bytes(const moe_linear_dims* dims, int op) {
   return 0;
 }
 
+int moe_linear_plan(const moe_linear_dims* dims, int product, int32_t* slices, int32_t* paired) {
+  LinShape s;
+  MOE_TRY(check_linear(dims, &s));
+  if (product < MOE_LINEAR_OUT || product > MOE_LINEAR_DW) return fail(MOE_EINVAL, "unknown product %d", product);
+  int parts;
+  bool both;
+  const int tile = linear_plan(s, product, &parts, &both);
+  if (slices) *slices = parts;
+  if (paired) *paired = both ? 1 : 0;
+  return tile;
+}
+
 static moe_status check_linear_ws(size_t need, void* ws, size_t ws_bytes) {
   if (need == 0) return MOE_OK;
   if (ws_bytes < need) return fail(MOE_EWORKSPACE, "workspace of %zu bytes < %zu needed", ws_bytes, need);

@@ -139,3 +139,12 @@ def test_gradients_refuse_the_array_they_read(lib):
     assert r == -1 and b"dLogits_aux" in lib.moe_last_error()
     r = lib.moe_router_loss_backward(ctypes.byref(d), FAKE, FAKE + 64, 1, None, None, FAKE, FAKE, FAKE, FAKE + 64, None)
     assert r == -1 and b"logits" in lib.moe_last_error()
+
+
+def test_linear_plan_query(lib):
+    d = ldims(M=1)
+    assert B.moe_linear_plan(d, B.LINEAR_OUT) == (0, 1, False)
+    assert B.moe_linear_plan(ldims(M=8192, N=8192, K=8192), B.LINEAR_OUT) == (256, 1, False)
+    assert lib.moe_linear_plan(ctypes.byref(d), B.LINEAR_DW, None, None) in (64, 128, 256)
+    assert lib.moe_linear_plan(ctypes.byref(d), 3, None, None) == -1 and lib.moe_linear_plan(None, 0, None, None) == -1
+    assert lib.moe_linear_plan(ctypes.byref(ldims(N=100)), 0, None, None) == -2

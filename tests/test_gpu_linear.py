@@ -340,3 +340,75 @@ def test_gelu_keeps_its_digits(M, dtype):
     B.moe_linear_backward(one, dY, X[:1], torch.zeros(M, 8, dtype=DT[dtype], device="cuda"), z.cuda()[None].contiguous(),
                           None, None, db, wb, nbb)
     assert_within("derivative", f64(db)[:, None], want, tol)
+
+
+# ragged last tiles: 250 of 256 rows; 136, 8 (of the first half only) and all 256 columns; 4090 x 1992 SwiGLU: 72 of 128
+@pytest.mark.parametrize("M,N,K,act,bias,residual,save,alias", [
+    (4090, 3976, 328, "gelu", True, True, True, False), (4090, 4096, 328, "silu", True, True, False, True),
+    (3850, 3848, 1096, "relu", False, True, True, False), (4090, 3976, 320, "none", True, False, True, False),
+    (4090, 1992, 328, "swiglu", True, True, True, False), (4090, 1928, 1096, "swiglu", False, True, False, True),
+    (4090, 2048, 320, "swiglu", True, False, True, False),
+])
+def test_large_tiles_with_every_epilogue(M, N, K, act, bias, residual, save, alias):
+    """X, bias and residual small whole numbers, W sixteenths of them: z is exact in fp32 (at most 4 K + 4
+    sixteenths), so out is off by the activation's own error, 2^-19 of 1 + |z| times what multiplies it,
+    one sum and one rounding, and Z is z rounded."""
+    NW = 2 * N if act == "swiglu" else N
+    pad, dt = 8, torch.bfloat16
+    dims = B.make_linear_dims(M, N, K, "bf16", act, K + pad, N + pad, N + pad)
+    assert B.moe_linear_plan(dims, B.LINEAR_OUT)[:2] == (256, 1)
+    g = torch.Generator(device="cuda").manual_seed(M + N + K)
+    ints = lambda *s: torch.randint(-2, 3, s, generator=g, device="cuda").float()  # noqa: E731
+    X, _ = strided(M, K, pad, "bf16", ints(M, K))
+    W = (ints(NW, K) / 16).to(dt)
+    b = ints(NW) if bias else None
+    out, base = strided(M, N, pad, "bf16", extra_rows=2)
+    res = ints(M, N).to(dt) if residual else None
+    keep = res
+    if alias:
+        out.copy_(res)
+        res = out
+    elif residual:
+        res = strided(M, N, pad, "bf16", res)[0]
+    Z = torch.full((M + 1, NW), 777.0, dtype=dt, device="cuda") if save else None
+    ws, nb = B.linear_workspace(dims, B.LINEAR_FORWARD)
+    B.moe_linear(dims, X, W, b, res, Z, out, ws, nb)
+    z = X.float() @ W.float().t()
+    z = (z + b if bias else z).double()
+    if save:
+        assert torch.equal(Z[:M], z.to(dt)) and bool((Z[M] == 777.0).all())
+    if act == "swiglu":
+        gate, up = z[:, :N], z[:, N:]
+        a, ae = gate * torch.sigmoid(gate) * up, ACT_ERR * (1 + gate.abs()) * up.abs()
+    elif act == "silu":
+        a, ae = z * torch.sigmoid(z), ACT_ERR * (1 + z.abs())
+    elif act == "gelu":
+        a, ae = z * torch.special.ndtr(z), ACT_ERR * (1 + z.abs())
+    else:
+        a, ae = z.clamp(min=0) if act == "relu" else z, torch.zeros_like(z)
+    r = keep.double() if residual else torch.zeros_like(a)
+    ref = a + r
+    tol = HALF["bf16"] * (ref.abs() + ae) + ae + 2 * U32 * (a.abs() + r.abs())
+    off = (out.double() - ref).abs()
+    assert bool((off <= tol).all()), "worst %.3g" % (off / tol.clamp(min=1e-30)).max().item()
+    assert_guards(base, M, N, "out")
+
+
+@pytest.mark.parametrize("M,N,K,product", [(4088, 1096, 4088, B.LINEAR_DX), (4000, 1096, 3848, B.LINEAR_DX), (1100, 4088, 3976, B.LINEAR_DW)])
+def test_large_tiles_backward_with_an_activation(M, N, K, product):
+    """ReLU with whole numbers: dZ, the products (below 2^24) and dbias are exact, rounded once."""
+    dims = B.make_linear_dims(M, N, K, "bf16", "relu", K + 8, 0, N + 24)
+    assert B.moe_linear_plan(dims, product)[0] == 256
+    g = torch.Generator(device="cuda").manual_seed(M + N + K)
+    ints = lambda *s: torch.randint(-2, 3, s, generator=g, device="cuda").float()  # noqa: E731
+    X, W, dY, Z = ints(M, K), ints(N, K), ints(M, N), ints(M, N)
+    Xs, dYs = strided(M, K, 8, "bf16", X)[0], strided(M, N, 24, "bf16", dY)[0]
+    dX, base = strided(M, K, 8, "bf16", extra_rows=1)
+    dW, db = torch.full((N + 1, K), 777.0, dtype=torch.bfloat16, device="cuda"), torch.full((N + 8,), 777.0, device="cuda")
+    ws, nb = B.linear_workspace(dims, B.LINEAR_BACKWARD)
+    B.moe_linear_backward(dims, dYs, Xs, W.bfloat16(), Z.bfloat16(), dX, dW[:N], db[:N], ws, nb)
+    dZ = torch.where(Z > 0, dY, torch.zeros_like(dY))
+    assert torch.equal(dX, (dZ @ W).bfloat16()) and torch.equal(dW[:N], (dZ.t() @ X).bfloat16())
+    assert torch.equal(db[:N], dZ.sum(0))
+    assert_guards(base, M, K, "dX")
+    assert bool((dW[N] == 777.0).all()) and bool((db[N:] == 777.0).all())
