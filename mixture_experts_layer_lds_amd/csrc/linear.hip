@@ -771,15 +771,17 @@ size_t linear_fwd_workspace_bytes(const LinShape& s) {
 
 // The backward's two products in one launch, each cut so that no workgroup has more than `most` stages
 // (a batch of many rows has a short reduction for dX and a long one for dW): where the model says
-// that this beats one after the other.  999 x 1000 x 264, ReLU with a bias: 26 us in six launches,
-// 17 in three (on 128 x 128 tiles 25.9 unsliced, 20.8 with 2 slices, 20.2 with 3, 24.8 with 8);
-// 12062 x 296 x 424: 50 us apart, 41 together; 2048 x 2048 x 2048: 54 and 47.  False: one after the
-// other, each with a plan of its own, in gx and gw.
+// that this beats one after the other.  Replayed from a graph: 999 x 1000 x 264, ReLU with a bias, 28.5 us in
+// six launches, 18.7 in three; 12062 x 296 x 424 29 us apart, 25.5 together; 2048 x 2048 x 2048 46 and 40.
+// What small tiles lose (lin_slow) counts for the pair too: on 64 x 64 tiles 12062 x 296 x 424 takes 32
+// together, 3000 x 2000 x 1000 65 (49 apart), 1500 x 1000 x 2000 33 (26 together on 128 x 128).  False: one
+// after the other, each with a plan of its own, in gx and gw.
 static bool lin_pair_plan(const LinShape& s, LinGemm& gx, LinGemm& gw) {
   // with over four rounds of tiles each product fills the chip by itself (16384 x 512 x 2048: 91 us
   // apart, 98 together)
   if (s.M == 0 || lin_tiles(gx, LIN_MID) + lin_tiles(gw, LIN_MID) > 1024) return false;
-  const double apart = gx.us + gw.us;
+  const double apart = gx.us + gw.us, sx_slow = lin_slow(gx), sw_slow = lin_slow(gw);
+  const double slow = sx_slow > sw_slow ? sx_slow : sw_slow;  // as for the products apart
   const int sx = lin_stages(gx, s.bf16), sw = lin_stages(gw, s.bf16), longest = sx > sw ? sx : sw;
   double best = 0.9 * apart;  // (its error, within which the simpler launches stay)
   int tile = 0, most = 0;
@@ -790,7 +792,7 @@ static bool lin_pair_plan(const LinShape& s, LinGemm& gx, LinGemm& gw) {
       const double out = (qx > 1 ? (double)qx * gx.m * gx.n : 0.0) + (qw > 1 ? (double)qw * gw.m * gw.n : 0.0);
       // the shorter product's workgroups count by their share of the longest
       const double wgs = ((double)lin_tiles(gx, t) * sx + (double)lin_tiles(gw, t) * sw) / len;
-      const double us = lin_time(t, wgs, len, out, s.bf16, true, 1.0);
+      const double us = lin_time(t, wgs, len, out, s.bf16, true, slow);
       if (us < best) {
         best = us;
         tile = t;

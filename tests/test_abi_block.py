@@ -148,3 +148,12 @@ def test_linear_plan_query(lib):
     assert lib.moe_linear_plan(ctypes.byref(d), B.LINEAR_DW, None, None) in (64, 128, 256)
     assert lib.moe_linear_plan(ctypes.byref(d), 3, None, None) == -1 and lib.moe_linear_plan(None, 0, None, None) == -1
     assert lib.moe_linear_plan(ctypes.byref(ldims(N=100)), 0, None, None) == -2
+
+
+@pytest.mark.parametrize("M,N,K", [(3000, 2000, 1000), (2904, 1800, 1000), (2504, 1496, 1496), (1500, 1000, 2000), (5000, 328, 1000)])
+def test_pairs_off_the_lines_avoid_small_tiles(lib, M, N, K):
+    """Rows that do not start on 128-byte lines cost small tiles as much in a pair of products as apart."""
+    d = B.make_linear_dims(M, N, K)
+    for product in (B.LINEAR_DX, B.LINEAR_DW):
+        tile, _, paired = B.moe_linear_plan(d, product)
+        assert not paired or tile == 128
