@@ -352,6 +352,17 @@ def _row_stride(t, rows, cols, name):
     return ld if rows > 1 else cols
 
 
+def _rng_ptr(rng, device):
+    """Address of the generator's two words, which the kernels read on ``device`` (None: not known)."""
+    if isinstance(rng, int):
+        return rng
+    if rng.numel() < 2 or rng.dtype not in (torch.int64, torch.uint64) or not rng.is_contiguous():
+        raise MoEError(-1, "rng must hold two consecutive 64-bit words")
+    if rng.device.type != "cuda" or (device is not None and rng.device != device):
+        raise MoEError(-1, "rng is on %s and the tensors on %s: they must be on one GPU" % (rng.device, device))
+    return rng.data_ptr()
+
+
 def moe_dropout(x, residual, p, rng, out, stream=None):
     """out = residual + dropout(x) of 2-D bf16 / fp32 tensors (residual may be None; rows may be
     strided); rng is a device tensor of two 64-bit words, {seed, offset}.  Without a residual this is
@@ -367,24 +378,26 @@ def moe_dropout(x, residual, p, rng, out, stream=None):
         raise MoEError(-1, "x must have two dimensions")
     if out.shape != shape or out.dtype is not dtype:
         raise MoEError(-1, "out must be %s of %s" % (tuple(shape), dtype))
-    if rng.numel() < 2 or rng.element_size() != 8:
-        raise MoEError(-1, "rng must hold two 64-bit words")
     rows, cols = shape
     res, ldr = None, 0
     if residual is not None:
         if residual.shape != shape or residual.dtype is not dtype:
             raise MoEError(-1, "residual must be %s of %s" % (tuple(shape), dtype))
         res, ldr = residual.data_ptr(), _row_stride(residual, rows, cols, "residual")
-    status = lib().moe_dropout(rows, cols, code, x.data_ptr(), _row_stride(x, rows, cols, "x"), res, ldr, p, rng.data_ptr(),
-                               out.data_ptr(), _row_stride(out, rows, cols, "out"), _stream(stream))
+    ldx, ldo, device = _row_stride(x, rows, cols, "x"), _row_stride(out, rows, cols, "out"), x.device
+    words = _rng_ptr(rng, device)
+    if out.device != device or (residual is not None and residual.device != device):
+        raise MoEError(-1, "x, residual and out must be on one GPU")
+    status = lib().moe_dropout(rows, cols, code, x.data_ptr(), ldx, res, ldr, p, words, out.data_ptr(), ldo, _stream(stream))
     if status:
         _check(status)
 
 
 def moe_combine_dropout(dims, plan, Y_perm, weighted, residual, p, rng, out, stream=None):
     """moe_combine with dropout and the residual sum (None: no residual) in its epilogue."""
+    words = _rng_ptr(rng, getattr(out, "device", None))
     _check(lib().moe_combine_dropout(ctypes.byref(dims), plan.ref(), _p(Y_perm), int(bool(weighted)), _p(residual),
-                                     float(p), _p(rng), _p(out), _stream(stream)))
+                                     float(p), words, _p(out), _stream(stream)))
 
 
 def make_linear_dims(M, N, K, dtype="bf16", act="none", ldx=0, ldr=0, ldy=0):

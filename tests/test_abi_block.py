@@ -157,3 +157,21 @@ def test_pairs_off_the_lines_avoid_small_tiles(lib, M, N, K):
     for product in (B.LINEAR_DX, B.LINEAR_DW):
         tile, _, paired = B.moe_linear_plan(d, product)
         assert not paired or tile == 128
+
+
+def test_dropout_binding_refuses_generator_words_that_the_kernel_cannot_read():
+    """The kernel dereferences rng: words in host memory (where seeds are made), on another device, apart
+    from each other, or of another kind are refused before any launch."""
+    x, words = torch.zeros(4, 16), torch.zeros(2, dtype=torch.int64)
+    d = B.make_dims(64, 64, 64, 8, 2)
+
+    class NoPlan:
+        def ref(self):
+            raise AssertionError("reached the library")
+
+    for rng, where in ((words, "cpu"), (words.to("meta"), "meta"), (torch.zeros(4, dtype=torch.int64)[::2], "consecutive"),
+                       (torch.zeros(2, dtype=torch.float64), "64-bit"), (torch.zeros(1, dtype=torch.int64), "64-bit")):
+        with pytest.raises(B.MoEError, match=where):
+            B.moe_dropout(x, None, 0.1, rng, torch.zeros(4, 16))
+        with pytest.raises((B.MoEError, AssertionError), match=where):
+            B.moe_combine_dropout(d, NoPlan(), x, True, None, 0.1, rng, torch.zeros(64, 64))
