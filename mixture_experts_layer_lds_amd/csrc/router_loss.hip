@@ -34,6 +34,7 @@ constexpr int RL_BWD_CHUNK = 64;  // tokens per workgroup of the backward, less 
 constexpr int RL_JOIN_THREADS = 512;  // (1024 threads in both launches: 16384 x 256 16.7 us, 15.9 so)
 constexpr int RL_MAX_WAVES = 16;
 constexpr int RL_JOIN_COLS = 32;      // columns per workgroup of the joining launch
+constexpr int RL_JOIN_SEQS = 1 << 16; // sequences per grid row of it (a grid's x extent stays below 2^32 threads)
 constexpr int RL_BWD_THREADS = 256;
 // A chunk of more than RL_FEW pieces leaves those of up to RL_SHORT rounds of a wave's tokens to single
 // waves: a piece that the whole workgroup takes costs two to three barriers and as many LDS round
@@ -649,10 +650,12 @@ __global__ __launch_bounds__(RL_JOIN_THREADS) void k_rloss_join(int T, int E, in
                                                            const int32_t* __restrict__ seq_off, RlossWs w, RlossOut o) {
   __shared__ RlJoinLds L;
   const int cbs = (E + RL_JOIN_COLS - 1) / RL_JOIN_COLS;
-  rl_join(L, blockIdx.x / cbs, blockIdx.x % cbs, chunk, T, E, seq_off, w, o);
+  const int s = blockIdx.y * RL_JOIN_SEQS + blockIdx.x / cbs;
+  if (s >= n_seq) return;
+  rl_join(L, s, blockIdx.x % cbs, chunk, T, E, seq_off, w, o);
   if (threadIdx.x == 0) {
     const unsigned v = __hip_atomic_fetch_add(w.ticket, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-    L.last = v == gridDim.x - 1;
+    L.last = v == (unsigned)(n_seq * cbs) - 1;
   }
   __syncthreads();
   if (!L.last) return;
@@ -802,7 +805,8 @@ hipError_t launch_router_loss(const float* logits, const int32_t* topk_idx, int6
   const hipError_t e = hipGetLastError();
   const RlGrid g = rl_grid(T, E);
   if (e != hipSuccess || g.one) return e;
-  k_rloss_join<<<n_seq * rl_colblocks(E), RL_JOIN_THREADS, 0, st>>>((int)T, E, K, n_seq, g.chunk, seq_off, w, o);
+  const dim3 join((unsigned)((n_seq < RL_JOIN_SEQS ? n_seq : RL_JOIN_SEQS) * rl_colblocks(E)), (unsigned)cdiv(n_seq, RL_JOIN_SEQS));
+  k_rloss_join<<<join, RL_JOIN_THREADS, 0, st>>>((int)T, E, K, n_seq, g.chunk, seq_off, w, o);
   return hipGetLastError();
 }
 

@@ -241,3 +241,30 @@ def test_many_sequences_replayed(T, lengths):
         c.backward()
 
     check_replays(step, c.outs())
+
+
+@pytest.mark.parametrize("E,n_seq", [(256, 1 << 20), (16, 1 << 20), (40, (1 << 16) + 1)])
+def test_as_many_sequences_as_allowed(E, n_seq):
+    """Nearly all of them empty: the others give what they give in a table without the empty ones."""
+    T, K = 3000, 4
+    at = [0, 5, (1 << 16) - 1, n_seq // 2 + 3 if n_seq > 1 << 17 else 1 << 15, n_seq - 1]
+    at, cuts = sorted(at), [0, 10, 700, 701, 2000, 2990]
+    small = Case(T=T, E=E, K=K, n_seq=5, off=cuts, masked=0.1, seed=3)
+    small.check()
+    off = np.zeros(n_seq + 1, np.int32)
+    for s, cut in zip(at, cuts[1:]):
+        off[s + 1:] = cut
+    big = Case(T=T, E=E, K=K, n_seq=n_seq, off=off, masked=0.1, seed=3)
+    big.forward()
+    big.backward()
+    torch.cuda.synchronize()
+    rows = torch.tensor(at, device="cuda")
+    assert torch.equal(big.tokens[rows], small.tokens) and big.tokens.sum() == small.tokens.sum() and (big.tokens >= 0).all()
+    assert torch.equal(big.counts[rows], small.counts) and big.counts.sum() == small.counts.sum() and (big.counts >= 0).all()
+    # the order of additions may differ: each sum of at most T terms twice within its bound
+    for name in ("prob", "lse", "loss", "dlogits"):
+        a, b = getattr(big, name), getattr(small, name)
+        if name == "prob":
+            assert ((a != 0).any(1).sum() == 5) and bool((a >= 0).all())
+            a = a[rows]
+        assert_within(name, f64(a), f64(b), (2 * EXP + 2 * (E + 70) * U32) * np.abs(f64(b)) + 1e-30)
