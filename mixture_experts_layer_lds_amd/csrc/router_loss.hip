@@ -267,6 +267,12 @@ __device__ __forceinline__ float rl_softmax(float (&x)[N], float& l2) {
   return l;
 }
 
+// What a wave's lanes have put into LDS is there for its other lanes.
+__device__ __forceinline__ void rl_wave_sync() {
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "workgroup");
+  __builtin_amdgcn_wave_barrier();
+}
+
 // What one workgroup of the joining launch leaves for the last: stored and loaded past the caches of
 // the XCDs (agent scope), so that no cache has to be written back or invalidated as a whole.
 template <typename V>
@@ -577,7 +583,9 @@ __global__ __launch_bounds__(rl_waves(ONE) * 64) void k_rloss_part(const float* 
     for (int s = s0 + wave; s <= s1; s += WAVES) {
       const int a = __builtin_amdgcn_readfirstlane(max(off(s), t_begin)), b = __builtin_amdgcn_readfirstlane(min(off(s + 1), t_end));
       if (b <= a || b - a > RL_SHORT * TPW) continue;
+      rl_wave_sync();  // (the last piece's counts have been read)
       for (int e = lane; e < E; e += 64) cnt[e] = 0;
+      rl_wave_sync();
       const int32_t* pick = topk_idx + (int64_t)a * K;
       for (int i = lane; i < (b - a) * K; i += 64) {
         const int e = pick[i];
@@ -599,6 +607,7 @@ __global__ __launch_bounds__(rl_waves(ONE) * 64) void k_rloss_part(const float* 
           for (int k = 0; k < N; ++k) acc[k] += y[k];
         }
       }
+      rl_wave_sync();  // the counts are whole
       const int64_t slot = ONE ? (int64_t)s : (int64_t)blockIdx.x + s;
       float* prob = (ONE ? o.prob_sum : w.prob) + slot * E;
       int32_t* out_cnt = (ONE ? o.seq_counts : w.cnt) + slot * E;
