@@ -412,3 +412,54 @@ def test_large_tiles_backward_with_an_activation(M, N, K, product):
     assert torch.equal(db[:N], dZ.sum(0))
     assert_guards(base, M, K, "dX")
     assert bool((dW[N] == 777.0).all()) and bool((db[N:] == 777.0).all())
+
+
+@pytest.mark.parametrize("dtype,M", [("bf16", 300), ("f32", 140), ("bf16", 9)])
+def test_row_strides_at_the_limit(dtype, M):
+    """Strides of 2^22 elements: a tile's row offsets pass 2^31 bytes.  Whole numbers, so every result is exact."""
+    N, K, ld = 72, 136, 1 << 22
+    g = torch.Generator(device="cuda").manual_seed(M)
+    ints = lambda *s: torch.randint(-2, 3, s, generator=g, device="cuda").float()  # noqa: E731
+
+    def far(rows, cols, fill=None):
+        v = torch.empty(rows * ld, dtype=DT[dtype], device="cuda").view(rows, ld)[:, :cols]
+        if fill is not None:
+            v.copy_(fill)
+        return v
+
+    X, W, R, dY = ints(M, K), ints(N, K), ints(M, N), ints(M, N)
+    dims = B.make_linear_dims(M, N, K, dtype, "none", ld, ld, ld)
+    wf, nf = B.linear_workspace(dims, B.LINEAR_FORWARD)
+    wb, nb = B.linear_workspace(dims, B.LINEAR_BACKWARD)
+    x, w, out, dX = far(M, K, X), W.to(DT[dtype]), far(M, N), far(M, K)
+    B.moe_linear(dims, x, w, None, far(M, N, R), None, out, wf, nf)
+    assert torch.equal(out, (X @ W.t() + R).to(DT[dtype]))
+    dW, db = torch.empty_like(w), torch.empty(N, device="cuda")
+    B.moe_linear_backward(dims, far(M, N, dY), x, w, None, dX, dW, db, wb, nb)
+    assert torch.equal(dX, (dY @ W).to(DT[dtype])) and torch.equal(dW, (dY.t() @ X).to(DT[dtype])) and torch.equal(db, dY.sum(0))
+
+
+def test_more_outputs_than_32_bits_count():
+    """2^31 outputs and more: the last rows, and the sums over all of them, of whole numbers."""
+    M, N, K = (1 << 20) + 8, 2056, 8
+    g = torch.Generator(device="cuda").manual_seed(1)
+    ints = lambda *s: torch.randint(-1, 2, s, generator=g, device="cuda").bfloat16()  # noqa: E731
+    X, W = ints(M, K), ints(N, K)
+    dims = B.make_linear_dims(M, N, K, "bf16", "relu")
+    ws, nb = B.linear_workspace(dims, B.LINEAR_BACKWARD)
+    out, Z = torch.empty(M, N, dtype=torch.bfloat16, device="cuda"), torch.empty(M, N, dtype=torch.bfloat16, device="cuda")
+    B.moe_linear(dims, X, W, None, None, Z, out, *B.linear_workspace(dims, B.LINEAR_FORWARD))
+    dY = torch.ones(1, N, dtype=torch.bfloat16, device="cuda").expand(M, N).contiguous()
+    dX, dW, db = torch.empty_like(X), torch.empty_like(W), torch.empty(N, device="cuda")
+    B.moe_linear_backward(dims, dY, X, W, Z, dX, dW, db, ws, nb)
+    tW, tb = torch.zeros(N, K, dtype=torch.float64, device="cuda"), torch.zeros(N, dtype=torch.float64, device="cuda")
+    for a in range(0, M, 1 << 16):
+        x = X[a:a + (1 << 16)].float()
+        z = x @ W.float().t()
+        assert torch.equal(Z[a:a + (1 << 16)].float(), z) and torch.equal(out[a:a + (1 << 16)].float(), z.clamp(min=0))
+        on = (z > 0).float()
+        assert torch.equal(dX[a:a + (1 << 16)], (on @ W.float()).bfloat16())
+        tW += (on.t() @ x).double()
+        tb += on.sum(0).double()
+    # counts stay below 2^24: exact in fp32, then dW is rounded once
+    assert torch.equal(db.double(), tb) and torch.equal(dW, tW.float().bfloat16())
