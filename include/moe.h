@@ -329,8 +329,8 @@ typedef enum {
 /* Shape (host struct).  M rows (0 .. 2^24), N output and K input features (multiples of 8,
  * 8 .. 65536).  ldx, ldr, ldy: row strides in elements of X and dX, of residual, and of out and dY
  * (multiples of 8, at most 2^22; 0 = dense).  W, Z and dW are dense.  dtype: type of X, W,
- * residual, Z, out and of the gradients dY, dX, dW; bias and dbias are fp32; accumulation is fp32.  act: a moe_act.  flags:
- * reserved, must be 0. */
+ * residual, Z, out and of the gradients dY, dX, dW; bias and dbias are fp32; accumulation is fp32.
+ * act: a moe_act.  flags: reserved, must be 0. */
 typedef struct moe_linear_dims {
   int64_t M;
   int64_t N;
@@ -357,8 +357,9 @@ enum { MOE_LINEAR_OUT = 0, MOE_LINEAR_DX = 1, MOE_LINEAR_DW = 2 };
 int moe_linear_plan(const moe_linear_dims* dims, int product, int32_t* slices, int32_t* paired);
 
 /* moe_linear — X [M,K], W [N',K], bias [N'] fp32 or NULL, residual [M,N] or NULL (it may be out, with
- * the same stride), out [M,N].  out and Z overlap no other argument.  Z [M,N'] or NULL: receives z rounded to dtype, for the backward.  The activation and
- * the residual sum work on fp32 values; out is rounded once.  M = 0 does nothing.
+ * the same stride), out [M,N].  out and Z overlap no other argument.  Z [M,N'] or NULL: receives z
+ * rounded to dtype, for the backward.  The activation and the residual sum work on fp32 values; out
+ * is rounded once.  M = 0 does nothing.
  * ws: moe_linear_workspace_bytes(dims, MOE_LINEAR_FORWARD) bytes. */
 moe_status moe_linear(const moe_linear_dims* dims, const void* X, const void* W, const float* bias,
                       const void* residual, void* Z, void* out, void* ws, size_t ws_bytes,
@@ -366,9 +367,11 @@ moe_status moe_linear(const moe_linear_dims* dims, const void* X, const void* W,
 
 /* moe_linear_backward — gradients of moe_linear (the residual's is dY itself):
  *   dZ = dY act'(Z) (SWIGLU: [dG | dU]),  dX = dZ W,  dW = dZ^T X,  dbias = sum of dZ over rows.
+ *  RELU selects: dZ is dY where Z > 0 and 0 elsewhere, whatever dY holds there.
  *  dY [M,N]; X, W: the forward's; Z [M,N'] from it (unused and may be NULL for NONE).
  *  dX [M,K], dW [N',K], dbias [N'] fp32: each may be NULL (not all); X is needed for dW, W for dX.
- *  No output overlaps an input.  dZ is rounded to dtype as the products' operand, not in dbias.  M = 0: dW and dbias are zeros.
+ *  No output overlaps an input.  dZ is rounded to dtype as the products' operand, not in dbias.
+ *  M = 0: dW and dbias are zeros.
  *  ws: moe_linear_workspace_bytes(dims, MOE_LINEAR_BACKWARD) bytes. */
 moe_status moe_linear_backward(const moe_linear_dims* dims, const void* dY, const void* X,
                                const void* W, const void* Z, void* dX, void* dW, float* dbias,

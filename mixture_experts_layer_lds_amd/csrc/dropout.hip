@@ -7,9 +7,9 @@
 // goes element by element, as do all groups of rows that are not aligned.  A dropped element is
 // selected away, not multiplied by zero, so it adds nothing even where x is infinite or NaN.
 // Bound by memory (x and residual read once, out written once): 32768 x 7168 bf16, 940 MB, 150 us
-// (6.3 TB/s; a library copy of 2 GiB reaches 4.9); 257 x 1003 fp32
-// rows with a residual 3.7 us, a launch's length.  16 random bits an element keep the generator at
-// 8 multiplications each, below what memory takes.
+// (6.3 TB/s; a library copy of 2 GiB reaches 4.9); 257 x 1003 fp32 rows with a residual 3.7 us, a launch's
+// length.  16 random bits an element keep the generator at 20 products of 32 x 32 -> 64 bits per group of
+// eight, 2.5 an element, below what memory takes.
 #include "internal.h"
 #include "philox.h"
 

@@ -11,12 +11,13 @@
 // reduction is cut into slices whose fp32 partial products a second kernel adds in slice order
 // before the epilogue (k_lin_finish).
 //
-// Large products are bound by the matrix cores at the clock that the chip's power allows
-// (8192 x 14336 x 4096 bf16: 690 us, 1390 TFLOP/s, of which the loop alone 650; 735 with GELU, whose
-// epilogue is 14 vector operations an element; a library product of that size 620 to 710), small
-// ones by launches and the length of one workgroup's loop.  The two products of a large backward go
-// out apart: together their last rounds filled up, but 16384 x 7168 x 4096 took 1578 us against
-// 1537, as idle CUs leave the others a higher clock.
+// Large products are bound by the matrix cores at the clock that the chip's power allows.  8192 x
+// 14336 x 4096 bf16, many passes on end: 700 to 730 us without an activation (1320 to 1370 TFLOP/s, of which
+// the loop alone 650), 745 to 755 with GELU (15 vector operations an element), 765 to 780 with bias and
+// Z kept too; a library product of that size alone 615 to 630.  Small ones are bound by launches and the
+// length of one workgroup's loop.  The two products of a large backward go out apart: together their
+// last rounds filled up, but 16384 x 7168 x 4096 took 1578 us against 1537, as idle CUs leave the others
+// a higher clock.
 //
 // The epilogue works on the fp32 accumulators: a tile half is laid out in LDS and walked in
 // 16-byte chunks of a row, so that residual, saved pre-activation and output are read and written in
