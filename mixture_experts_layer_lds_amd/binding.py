@@ -352,14 +352,16 @@ def _row_stride(t, rows, cols, name):
     return ld if rows > 1 else cols
 
 
-def _rng_ptr(rng, device):
-    """Address of the generator's two words, which the kernels read on ``device`` (None: not known)."""
+def _rng_ptr(rng, dev):
+    """Address of the generator's two words, which the kernels read on GPU ``dev`` (None: not known)."""
     if isinstance(rng, int):
         return rng
-    if rng.numel() < 2 or rng.dtype not in (torch.int64, torch.uint64) or not rng.is_contiguous():
+    dtype = rng.dtype
+    if rng.numel() < 2 or (dtype is not torch.int64 and dtype is not torch.uint64) or not rng.is_contiguous():
         raise MoEError(-1, "rng must hold two consecutive 64-bit words")
-    if rng.device.type != "cuda" or (device is not None and rng.device != device):
-        raise MoEError(-1, "rng is on %s and the tensors on %s: they must be on one GPU" % (rng.device, device))
+    on = rng.get_device()  # -1: not a GPU's memory
+    if on < 0 or (dev is not None and on != dev):
+        raise MoEError(-1, "rng is on %s: it must be on the GPU that holds the tensors" % rng.device)
     return rng.data_ptr()
 
 
@@ -384,9 +386,9 @@ def moe_dropout(x, residual, p, rng, out, stream=None):
         if residual.shape != shape or residual.dtype is not dtype:
             raise MoEError(-1, "residual must be %s of %s" % (tuple(shape), dtype))
         res, ldr = residual.data_ptr(), _row_stride(residual, rows, cols, "residual")
-    ldx, ldo, device = _row_stride(x, rows, cols, "x"), _row_stride(out, rows, cols, "out"), x.device
-    words = _rng_ptr(rng, device)
-    if out.device != device or (residual is not None and residual.device != device):
+    ldx, ldo, dev = _row_stride(x, rows, cols, "x"), _row_stride(out, rows, cols, "out"), x.get_device()
+    words = _rng_ptr(rng, dev)
+    if out.get_device() != dev or (residual is not None and residual.get_device() != dev):
         raise MoEError(-1, "x, residual and out must be on one GPU")
     status = lib().moe_dropout(rows, cols, code, x.data_ptr(), ldx, res, ldr, p, words, out.data_ptr(), ldo, _stream(stream))
     if status:
@@ -395,7 +397,7 @@ def moe_dropout(x, residual, p, rng, out, stream=None):
 
 def moe_combine_dropout(dims, plan, Y_perm, weighted, residual, p, rng, out, stream=None):
     """moe_combine with dropout and the residual sum (None: no residual) in its epilogue."""
-    words = _rng_ptr(rng, getattr(out, "device", None))
+    words = _rng_ptr(rng, out.get_device() if isinstance(out, torch.Tensor) else None)
     _check(lib().moe_combine_dropout(ctypes.byref(dims), plan.ref(), _p(Y_perm), int(bool(weighted)), _p(residual),
                                      float(p), words, _p(out), _stream(stream)))
 
