@@ -377,6 +377,91 @@ moe_status moe_linear_backward(const moe_linear_dims* dims, const void* dY, cons
                                const void* W, const void* Z, void* dX, void* dW, float* dbias,
                                void* ws, size_t ws_bytes, void* stream);
 
+/* Layer norm and RMS norm, with the sum of a residual stream in front: what stands before the layer in
+ * a pre-norm block.
+ *   s = x + residual,  y = (s - mu) rstd weight + bias,  rstd = 1 / sqrt(var + eps)
+ * LAYER: mu and var are the row's mean and mean squared deviation from it; RMS: mu = 0, var the mean
+ * square. */
+typedef enum { MOE_NORM_LAYER = 0, MOE_NORM_RMS = 1 } moe_norm_kind;
+
+/* Shape (host struct).  rows (0 .. 2^31 - 1) of cols elements (1 .. 65536, any number).  ldx: row stride
+ * in elements of x and dx; ldr: of residual and dsum; lds: of sum; ldy: of y and dy (>= cols, at most
+ * 2^40; 0 = dense; rows whose strides keep 16-byte alignment move in 16-byte accesses).
+ * dtype: type of x, residual, sum, y and of the gradients dy, dsum, dx.  wtype: type of weight and bias
+ * (their gradients are fp32).  kind: a moe_norm_kind.  eps: finite, >= 0.  flags: reserved, must be 0. */
+typedef struct moe_norm_dims {
+  int64_t rows;
+  int64_t cols;
+  int64_t ldx;
+  int64_t ldr;
+  int64_t lds;
+  int64_t ldy;
+  int32_t dtype;
+  int32_t wtype;
+  int32_t kind;
+  int32_t flags;
+  float eps;
+} moe_norm_dims;
+
+/* moe_norm — x [rows,cols]; residual [rows,cols] or NULL; weight, bias [cols] or NULL (1 and 0).
+ *  sum [rows,cols] or NULL (NULL without a residual): s rounded to dtype, for the next residual and the
+ *  backward.  What is normalised is the rounded s, whether sum is given or not.
+ *  y [rows,cols]; mean (LAYER; unused for RMS) and rstd [rows] fp32, or NULL where no backward follows.
+ *  fp32 arithmetic, y is rounded once.  sum and y may each be x or residual (with the same stride), but
+ *  not one another.  A row with infinities or NaN has NaN in y; other rows are untouched by it.  rows = 0
+ *  does nothing. */
+moe_status moe_norm(const moe_norm_dims* dims, const void* x, const void* residual, const void* weight,
+                    const void* bias, void* sum, void* y, float* mean, float* rstd, void* stream);
+
+/* Host: workspace bytes of moe_norm_backward (0 for invalid dims, with moe_last_error() set). */
+size_t moe_norm_workspace_bytes(const moe_norm_dims* dims);
+
+/* moe_norm_backward — with xh = (s - mu) rstd and g = dy weight:
+ *   dx = rstd (g - mean(g) - xh mean(g xh)) + dsum   (RMS: without mean(g)),
+ *   dweight = sum over rows of dy xh,  dbias = sum over rows of dy.
+ *  dy [rows,cols]; s [rows,cols] (stride lds): the forward's sum, or its x where it had no residual;
+ *  weight as in the forward; mean (LAYER) and rstd [rows] from it.
+ *  dsum [rows,cols] or NULL: the gradient that reaches s directly (the residual stream's).  dx is the
+ *  gradient of x and of residual alike.
+ *  dx [rows,cols], dweight, dbias [cols] fp32: each may be NULL (not all).  dx may be dy, s or dsum (with the
+ *  same stride).  fp32 sums in a fixed order.  rows = 0: dweight and dbias are zeros.
+ *  ws: moe_norm_workspace_bytes(dims) bytes, unused where dweight and dbias are NULL. */
+moe_status moe_norm_backward(const moe_norm_dims* dims, const void* dy, const void* s, const void* weight,
+                             const float* mean, const float* rstd, const void* dsum, void* dx,
+                             float* dweight, float* dbias, void* ws, size_t ws_bytes, void* stream);
+
+/* One gradient tensor (host struct): n consecutive elements of dtype at src (n >= 0).  dst: where
+ * moe_grad_clip writes the scaled ones: src itself (in place; also meant by NULL) or n elements that
+ * overlap no tensor of the list.  src and dst need only the element's own alignment; those on 16-byte
+ * borders move in 16-byte accesses.  reserved: 0. */
+typedef struct moe_grad {
+  const void* src;
+  void* dst;
+  int64_t n;
+  int32_t dtype;
+  int32_t reserved;
+} moe_grad;
+
+/* Host: workspace bytes for a list of count tensors (count 0 .. 2^16; 0 for an invalid count). */
+size_t moe_grad_workspace_bytes(int32_t count);
+
+/* moe_grad_norm — norm [1] fp32 = sqrt(sum of squares over all tensors), summed in fp64 in a fixed
+ * order, so that it is exact to its rounding for any fp32 values.  Infinities and NaN reach it.
+ * grads: host array, read during the call only.  It may hold any mix of sizes and types; one
+ * tensor must not stand in it twice (it would count twice).  No tensors: 0.
+ * ws: moe_grad_workspace_bytes(count) bytes. */
+moe_status moe_grad_norm(const moe_grad* grads, int32_t count, float* norm, void* ws, size_t ws_bytes,
+                         void* stream);
+
+/* moe_grad_clip — dst = c src with c = max_norm / norm where norm > max_norm, else 1; products in
+ * fp32, rounded once.  max_norm >= 0 (infinity: never cut).
+ *  norm_in NULL: the norm is computed first (moe_grad_norm's sums) and written to norm [1].
+ *  norm_in [1] fp32, device: the norm to use, e.g. joined over ranks; norm is then unused and may be NULL,
+ *  as may ws.
+ *  A norm that is infinite or NaN leaves c = 1: the caller sees it in norm and skips the step. */
+moe_status moe_grad_clip(const moe_grad* grads, int32_t count, double max_norm, const float* norm_in,
+                         float* norm, void* ws, size_t ws_bytes, void* stream);
+
 /* moe_decode — the whole forward layer in one kernel launch, for small token counts (decode /
  * inference): router logits, top-K with softmax, the selected experts' SwiGLU FFNs and the
  * weighted combine.  apxml.com "自定义核与核融合" (the five steps fused into one kernel) and
@@ -516,7 +601,9 @@ typedef enum {
   MOE_STAGE_DROPOUT = 18,     /* moe_dropout (moe_combine_dropout counts as COMBINE) */
   MOE_STAGE_LINEAR = 19,      /* moe_linear */
   MOE_STAGE_LINEAR_BWD = 20,  /* moe_linear_backward, and moe_backward_aux's logit dX GEMM */
-  MOE_STAGE_COUNT = 21
+  MOE_STAGE_NORM = 21,        /* moe_norm, moe_norm_backward */
+  MOE_STAGE_GRAD = 22,        /* moe_grad_norm, moe_grad_clip */
+  MOE_STAGE_COUNT = 23
 } moe_stage;
 
 /* Host: stage timing for measurement tools (not thread-safe; for a single host thread).

@@ -7,7 +7,8 @@ The functions keep the C names: ``moe_route``, ``moe_permute``, ``moe_grouped_ff
 ``moe_combine``, ``moe_forward``, ``moe_backward``, ``moe_decode``, ``moe_quantize_fp8``,
 ``moe_grouped_ffn_fp8``, ``moe_quantize_mx``, ``moe_grouped_ffn_mx``, ``moe_router_loss``,
 ``moe_router_loss_backward``, ``moe_backward_aux``, ``moe_dropout``, ``moe_combine_dropout``,
-``moe_linear``, ``moe_linear_backward`` (plus sizing helpers).
+``moe_linear``, ``moe_linear_backward``, ``moe_norm``, ``moe_norm_backward``, ``moe_grad_norm``,
+``moe_grad_clip`` (plus sizing helpers).
 """
 import ctypes
 import os
@@ -23,6 +24,7 @@ OP_ROUTE, OP_PERMUTE, OP_FFN, OP_COMBINE, OP_FORWARD, OP_BACKWARD, OP_DECODE, OP
 FP8_E4M3, FP8_E5M2 = 0, 1
 ACTS = {"none": 0, "relu": 1, "gelu": 2, "silu": 3, "swiglu": 4}
 LINEAR_FORWARD, LINEAR_BACKWARD = 0, 1
+NORM_KINDS = {"layer": 0, "rms": 1}
 LINEAR_OUT, LINEAR_DX, LINEAR_DW = 0, 1, 2
 STATUS = {0: "MOE_OK", -1: "MOE_EINVAL", -2: "MOE_ENOTSUP", -3: "MOE_EWORKSPACE", -4: "MOE_EHIP"}
 
@@ -35,10 +37,13 @@ EXPORTS = ["moe_max_rows", "moe_workspace_bytes", "moe_route", "moe_permute", "m
            "moe_backward_aux", "moe_router_loss", "moe_router_loss_backward",
            "moe_router_loss_workspace_bytes", "moe_dropout", "moe_combine_dropout", "moe_linear",
            "moe_linear_backward", "moe_linear_workspace_bytes", "moe_linear_plan",
+           "moe_norm", "moe_norm_workspace_bytes", "moe_norm_backward", "moe_grad_workspace_bytes", "moe_grad_norm",
+           "moe_grad_clip",
            "moe_version", "moe_timing_enable", "moe_timing_read"]
 STAGES = ["router_gemm", "route", "tiles", "up_gemm", "down_gemm", "permute", "combine", "dact_gemm",
           "dw_down_gemm", "dw_gu_gemm", "dx_gemm", "router_bwd", "dwr_gemm", "decode", "fp8_quant",
-          "fp8_up_gemm", "fp8_down_gemm", "router_loss", "dropout", "linear", "linear_bwd"]
+          "fp8_up_gemm", "fp8_down_gemm", "router_loss", "dropout", "linear", "linear_bwd", "norm",
+          "grad"]
 
 
 class MoEError(RuntimeError):
@@ -58,6 +63,16 @@ class LinearDims(ctypes.Structure):
     _fields_ = [("M", ctypes.c_int64), ("N", ctypes.c_int64), ("K", ctypes.c_int64), ("ldx", ctypes.c_int64),
                 ("ldr", ctypes.c_int64), ("ldy", ctypes.c_int64), ("dtype", ctypes.c_int32), ("act", ctypes.c_int32),
                 ("flags", ctypes.c_int32)]
+
+
+class NormDims(ctypes.Structure):
+    _fields_ = [(k, ctypes.c_int64) for k in ("rows", "cols", "ldx", "ldr", "lds", "ldy")] + [
+        (k, ctypes.c_int32) for k in ("dtype", "wtype", "kind", "flags")] + [("eps", ctypes.c_float)]
+
+
+class GradStruct(ctypes.Structure):
+    _fields_ = [("src", ctypes.c_void_p), ("dst", ctypes.c_void_p), ("n", ctypes.c_int64), ("dtype", ctypes.c_int32),
+                ("reserved", ctypes.c_int32)]
 
 
 PLAN_FIELDS = ["topk_idx", "topk_w", "counts", "expert_off", "row_token", "row_w", "tok_off",
@@ -116,6 +131,15 @@ def lib():
         L.moe_linear_plan.restype = ctypes.c_int
         L.moe_linear.argtypes = [pl, vp, vp, vp, vp, vp, vp, vp, sz, vp]
         L.moe_linear_backward.argtypes = [pl, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp]
+        pn, pg = ctypes.POINTER(NormDims), ctypes.POINTER(GradStruct)
+        L.moe_norm.argtypes = [pn, vp, vp, vp, vp, vp, vp, vp, vp, vp]
+        L.moe_norm_workspace_bytes.argtypes, L.moe_norm_workspace_bytes.restype = [pn], sz
+        L.moe_norm_backward.argtypes = [pn, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp]
+        L.moe_grad_workspace_bytes.argtypes, L.moe_grad_workspace_bytes.restype = [i32], sz
+        L.moe_grad_norm.argtypes = [pg, i32, vp, vp, sz, vp]
+        L.moe_grad_clip.argtypes = [pg, i32, ctypes.c_double, vp, vp, vp, sz, vp]
+        for f in ("moe_norm", "moe_norm_backward", "moe_grad_norm", "moe_grad_clip"):
+            getattr(L, f).restype = st
         for f in ("moe_backward_aux", "moe_router_loss", "moe_router_loss_backward", "moe_dropout",
                   "moe_combine_dropout", "moe_linear", "moe_linear_backward"):
             getattr(L, f).restype = st
@@ -161,6 +185,14 @@ def _stream(stream=None):
     if stream is None and _raw_stream is not None:
         return _raw_stream(torch.cuda.current_device())
     return (stream if stream is not None else torch.cuda.current_stream()).cuda_stream
+
+
+def _on_gpu(*tensors):
+    """Refuses tensors that the current GPU's kernels could not read (None and addresses pass)."""
+    dev = torch.cuda.current_device()
+    for t in tensors:
+        if t is not None and not isinstance(t, int) and t.get_device() != dev:
+            raise MoEError(-1, "a tensor is on %s: it must be on the current GPU, cuda:%d" % (t.device, dev))
 
 
 def _check(status):
@@ -437,6 +469,88 @@ def moe_linear_backward(dims, dY, X, W, Z, dX, dW, dbias, ws, ws_bytes, stream=N
     """Gradients of moe_linear from dY and the saved pre-activation; dX, dW and dbias may be None."""
     _check(lib().moe_linear_backward(ctypes.byref(dims), _p(dY), _p(X), _p(W), _p(Z), _p(dX), _p(dW), _p(dbias),
                                      _p(ws), ws_bytes, _stream(stream)))
+
+
+def make_norm_dims(rows, cols, dtype="bf16", kind="layer", eps=1e-5, wtype="f32", ldx=0, ldr=0, lds=0, ldy=0):
+    """Shape of a layer / RMS norm; wtype: type of weight and bias; row strides in elements of x / dx, residual /
+    dsum, sum and y / dy (0 = dense)."""
+    types = {"bf16": MOE_BF16, "f32": MOE_F32, torch.bfloat16: MOE_BF16, torch.float32: MOE_F32}
+    return NormDims(int(rows), int(cols), int(ldx), int(ldr), int(lds), int(ldy), types[dtype], types[wtype],
+                    NORM_KINDS[kind], 0, float(eps))
+
+
+def norm_workspace(dims, device="cuda"):
+    nbytes = lib().moe_norm_workspace_bytes(ctypes.byref(dims))
+    return torch.empty(max(nbytes, 256), dtype=torch.uint8, device=device), nbytes
+
+
+def moe_norm(dims, x, residual, weight, bias, sum, y, mean, rstd, stream=None):
+    """sum = x + residual, y = norm(sum) weight + bias, with the rows' mean and 1 / deviation; residual, weight,
+    bias, sum, mean and rstd may be None."""
+    _on_gpu(x, residual, weight, bias, sum, y, mean, rstd)
+    status = lib().moe_norm(ctypes.byref(dims), _p(x), _p(residual), _p(weight), _p(bias), _p(sum), _p(y), _p(mean),
+                            _p(rstd), _stream(stream))
+    if status:
+        _check(status)
+
+
+def moe_norm_backward(dims, dy, s, weight, mean, rstd, dsum, dx, dweight, dbias, ws, ws_bytes, stream=None):
+    """Gradients of moe_norm from dy and the normalised sum s (x without a residual); dsum: the gradient that
+    reaches s directly, or None; dx, dweight and dbias may be None."""
+    _on_gpu(dy, s, weight, mean, rstd, dsum, dx, dweight, dbias, ws)
+    _check(lib().moe_norm_backward(ctypes.byref(dims), _p(dy), _p(s), _p(weight), _p(mean), _p(rstd), _p(dsum), _p(dx),
+                                   _p(dweight), _p(dbias), _p(ws), ws_bytes, _stream(stream)))
+
+
+class Gradients:
+    """A list of gradient tensors (contiguous, bf16 or fp32, on one GPU) and where moe_grad_clip writes the
+    scaled ones: ``dst``, tensors of the same sizes and types, or in place without it."""
+
+    def __init__(self, src, dst=None):
+        self.src, self.dst = list(src), list(src if dst is None else dst)
+        if len(self.src) != len(self.dst):
+            raise MoEError(-1, "%d gradients but %d destinations" % (len(self.src), len(self.dst)))
+        self.count = len(self.src)
+        self.array = (GradStruct * max(self.count, 1))()
+        spans = []
+        for i, (s, d) in enumerate(zip(self.src, self.dst)):
+            if s.dtype not in (torch.bfloat16, torch.float32):
+                raise MoEError(-2, "gradient %d: dtype %s not supported" % (i, s.dtype))
+            if d.dtype != s.dtype or d.numel() != s.numel():
+                raise MoEError(-1, "gradient %d: its destination must be %d elements of %s" % (i, s.numel(), s.dtype))
+            if not (s.is_contiguous() and d.is_contiguous()):
+                raise MoEError(-1, "gradient %d must be contiguous" % i)
+            if s.device != self.src[0].device or d.device != s.device:
+                raise MoEError(-1, "gradient %d is on another device" % i)
+            n = s.numel()
+            self.array[i] = GradStruct(s.data_ptr(), d.data_ptr(), n, MOE_BF16 if s.dtype is torch.bfloat16 else MOE_F32, 0)
+            if n:
+                spans.append((s.data_ptr(), s.data_ptr() + n * s.element_size(), i))
+                if d.data_ptr() != s.data_ptr():
+                    spans.append((d.data_ptr(), d.data_ptr() + n * s.element_size(), i))
+        spans.sort()
+        for (_, end, i), (start, _, j) in zip(spans, spans[1:]):
+            if start < end:
+                raise MoEError(-1, "gradients %d and %d share memory" % (i, j))
+
+
+def grad_workspace(grads, device="cuda"):
+    nbytes = lib().moe_grad_workspace_bytes(grads.count)
+    return torch.empty(max(nbytes, 256), dtype=torch.uint8, device=device), nbytes
+
+
+def moe_grad_norm(grads, norm, ws, ws_bytes, stream=None):
+    """The global norm (fp32 [1]) of a list of gradients."""
+    _on_gpu(*grads.src[:1], norm, ws)
+    _check(lib().moe_grad_norm(grads.array, grads.count, _p(norm), _p(ws), ws_bytes, _stream(stream)))
+
+
+def moe_grad_clip(grads, max_norm, norm_in, norm, ws, ws_bytes, stream=None):
+    """Gradients scaled down to a global norm of max_norm.  norm_in (fp32 [1]): the norm to use; None: it is
+    computed and written to norm."""
+    _on_gpu(*grads.src[:1], norm_in, norm, ws)
+    _check(lib().moe_grad_clip(grads.array, grads.count, float(max_norm), _p(norm_in), _p(norm), _p(ws), ws_bytes,
+                               _stream(stream)))
 
 
 def moe_timing_enable(on):

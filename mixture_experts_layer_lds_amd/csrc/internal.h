@@ -133,6 +133,35 @@ hipError_t launch_dropout(bool is_bf16, int64_t rows, int64_t cols, const void* 
 hipError_t launch_combine_dropout(const Shape& s, const PlanPtrs& p, const void* Y_perm, bool weighted,
                                   const void* residual, void* out, const DropArgs& a, hipStream_t st);
 
+// ---- layer / RMS norm (norm.hip) ----
+struct NormShape {
+  int64_t rows, cols;
+  int64_t ldx, ldr, lds, ldy;  // row strides in elements: x and dx, residual and dsum, sum, y and dy
+  float eps;
+  bool bf16, wbf16, rms;  // element type, type of weight and bias, kind
+};
+// sum = x + residual, y = norm(sum) weight + bias; residual, weight, bias, sum, mean and rstd may be null
+hipError_t launch_norm(const NormShape& s, const void* x, const void* residual, const void* weight, const void* bias,
+                       void* sum, void* y, float* mean, float* rstd, hipStream_t st);
+size_t norm_bwd_workspace_bytes(const NormShape& s);
+// dx, dweight and dbias may be null each; weight and dsum too; mean is not read for RMS
+hipError_t launch_norm_bwd(const NormShape& s, const void* dy, const void* sum, const void* weight, const float* mean,
+                           const float* rstd, const void* dsum, void* dx, float* dweight, float* dbias, void* ws,
+                           hipStream_t st);
+
+// ---- gradient norm and clipping (grads.hip) ----
+struct GradTensor {
+  const void* src;
+  void* dst;
+  int64_t n;
+  bool bf16;
+};
+size_t grad_workspace_bytes(int count);
+hipError_t launch_grad_norm(const GradTensor* list, int count, float* norm, void* ws, hipStream_t st);
+// norm_in (device) or, where it is null, the norm computed first and written to norm
+hipError_t launch_grad_clip(const GradTensor* list, int count, double max_norm, const float* norm_in, float* norm, void* ws,
+                            hipStream_t st);
+
 // ---- router losses (router_loss.hip) ----
 size_t router_loss_workspace_bytes(int64_t T, int E, int n_seq);
 hipError_t launch_router_loss(const float* logits, const int32_t* topk_idx, int64_t T, int E, int K, int n_seq,

@@ -5,7 +5,9 @@
 
 #include <cstdarg>
 #include <cstdio>
+#include <memory>
 #include <mutex>
+#include <new>
 #include <string>
 
 #include "../../include/moe.h"
@@ -849,6 +851,163 @@ moe_status moe_linear_backward(const moe_linear_dims* dims, const void* dY, cons
   hipStream_t st = static_cast<hipStream_t>(stream);
   MOE_STAGE(MOE_STAGE_LINEAR_BWD, st,
             launch_linear_bwd(s, dY, X, W, Z, s.M > 0 ? dX : nullptr, dW, dbias, ws, st), "linear backward");
+  return MOE_OK;
+}
+
+// ---- layer / RMS norm ----
+static moe_status check_norm(const moe_norm_dims* dm, NormShape* s) {
+  if (!dm) return fail(MOE_EINVAL, "dims is NULL");
+  if (dm->rows < 0 || dm->rows > 0x7fffffffll) return fail(MOE_EINVAL, "rows=%lld out of range [0, 2^31)", (long long)dm->rows);
+  if (dm->cols < 1 || dm->cols > 65536) return fail(MOE_EINVAL, "cols=%lld out of range [1, 65536]", (long long)dm->cols);
+  if (dm->dtype != MOE_F32 && dm->dtype != MOE_BF16) return fail(MOE_ENOTSUP, "dtype %d not supported", dm->dtype);
+  if (dm->wtype != MOE_F32 && dm->wtype != MOE_BF16) return fail(MOE_ENOTSUP, "wtype %d not supported", dm->wtype);
+  if (dm->kind != MOE_NORM_LAYER && dm->kind != MOE_NORM_RMS) return fail(MOE_EINVAL, "norm kind %d invalid", dm->kind);
+  if (!(dm->eps >= 0.0f && dm->eps <= 3.4e38f)) return fail(MOE_EINVAL, "eps=%g must be finite and >= 0", (double)dm->eps);
+  if (dm->flags != 0) return fail(MOE_EINVAL, "flags must be 0");
+  s->rows = dm->rows;
+  s->cols = dm->cols;
+  s->ldx = dm->ldx ? dm->ldx : dm->cols;
+  s->ldr = dm->ldr ? dm->ldr : dm->cols;
+  s->lds = dm->lds ? dm->lds : dm->cols;
+  s->ldy = dm->ldy ? dm->ldy : dm->cols;
+  s->eps = dm->eps;
+  s->bf16 = dm->dtype == MOE_BF16;
+  s->wbf16 = dm->wtype == MOE_BF16;
+  s->rms = dm->kind == MOE_NORM_RMS;
+  MOE_TRY(check_ld(s->ldx, s->cols, kMaxStride, "ldx"));
+  MOE_TRY(check_ld(s->ldr, s->cols, kMaxStride, "ldr"));
+  MOE_TRY(check_ld(s->lds, s->cols, kMaxStride, "lds"));
+  return check_ld(s->ldy, s->cols, kMaxStride, "ldy");
+}
+// An output that is an input's array takes its rows from the same places.
+static moe_status check_alias(const void* out, int64_t ldo, const void* in, int64_t ldi, const char* name) {
+  if (out && out == in && ldo != ldi) return fail(MOE_EINVAL, "%s is an input's array with another row stride", name);
+  return MOE_OK;
+}
+
+moe_status moe_norm(const moe_norm_dims* dims, const void* x, const void* residual, const void* weight,
+                    const void* bias, void* sum, void* y, float* mean, float* rstd, void* stream) {
+  NormShape s;
+  MOE_TRY(check_norm(dims, &s));
+  if (s.rows == 0) return MOE_OK;
+  MOE_TRY(need_ptr(x, "x"));
+  MOE_TRY(opt_ptr(residual, "residual"));
+  MOE_TRY(opt_ptr(weight, "weight"));
+  MOE_TRY(opt_ptr(bias, "bias"));
+  MOE_TRY(opt_ptr(sum, "sum"));
+  MOE_TRY(need_ptr(y, "y"));
+  MOE_TRY(opt_ptr(mean, "mean"));
+  MOE_TRY(opt_ptr(rstd, "rstd"));
+  if (sum && !residual) return fail(MOE_EINVAL, "sum requested without a residual");
+  if (sum == y) return fail(MOE_EINVAL, "sum and y are the same array");
+  MOE_TRY(check_alias(y, s.ldy, x, s.ldx, "y"));
+  MOE_TRY(check_alias(y, s.ldy, residual, s.ldr, "y"));
+  MOE_TRY(check_alias(sum, s.lds, x, s.ldx, "sum"));
+  MOE_TRY(check_alias(sum, s.lds, residual, s.ldr, "sum"));
+  hipStream_t st = static_cast<hipStream_t>(stream);
+  MOE_STAGE(MOE_STAGE_NORM, st, launch_norm(s, x, residual, weight, bias, sum, y, mean, rstd, st), "norm");
+  return MOE_OK;
+}
+
+size_t moe_norm_workspace_bytes(const moe_norm_dims* dims) {
+  NormShape s;
+  return check_norm(dims, &s) == MOE_OK ? norm_bwd_workspace_bytes(s) : 0;
+}
+
+moe_status moe_norm_backward(const moe_norm_dims* dims, const void* dy, const void* sum, const void* weight,
+                             const float* mean, const float* rstd, const void* dsum, void* dx, float* dweight,
+                             float* dbias, void* ws, size_t ws_bytes, void* stream) {
+  NormShape s;
+  MOE_TRY(check_norm(dims, &s));
+  if (!dx && !dweight && !dbias) return fail(MOE_EINVAL, "dx, dweight and dbias are all NULL");
+  if (s.rows > 0) {
+    MOE_TRY(need_ptr(dy, "dy"));
+    MOE_TRY(need_ptr(sum, "s"));
+    MOE_TRY(opt_ptr(weight, "weight"));
+    if (!s.rms) MOE_TRY(need_ptr(mean, "mean"));
+    MOE_TRY(need_ptr(rstd, "rstd"));
+    MOE_TRY(opt_ptr(dsum, "dsum"));
+  }
+  MOE_TRY(opt_ptr(dx, "dx"));
+  MOE_TRY(opt_ptr(dweight, "dweight"));
+  MOE_TRY(opt_ptr(dbias, "dbias"));
+  MOE_TRY(check_alias(dx, s.ldx, dy, s.ldy, "dx"));
+  MOE_TRY(check_alias(dx, s.ldx, sum, s.lds, "dx"));
+  MOE_TRY(check_alias(dx, s.ldx, dsum, s.ldr, "dx"));
+  if (dweight && dweight == dbias) return fail(MOE_EINVAL, "dweight and dbias are the same array");
+  if (dweight || dbias) {
+    const size_t need = norm_bwd_workspace_bytes(s);
+    if (need > 0) {
+      if (ws_bytes < need) return fail(MOE_EWORKSPACE, "workspace of %zu bytes < %zu needed", ws_bytes, need);
+      MOE_TRY(need_ptr(ws, "ws"));
+    }
+  }
+  hipStream_t st = static_cast<hipStream_t>(stream);
+  MOE_STAGE(MOE_STAGE_NORM, st,
+            launch_norm_bwd(s, dy, sum, weight, mean, rstd, dsum, dx, dweight, dbias, ws, st), "norm backward");
+  return MOE_OK;
+}
+
+// ---- gradient norm and clipping ----
+constexpr int32_t kMaxGrads = 1 << 16;
+static moe_status check_grads(const moe_grad* g, int32_t count, GradTensor* out) {
+  for (int32_t i = 0; i < count; ++i) {
+    if (g[i].dtype != MOE_F32 && g[i].dtype != MOE_BF16) return fail(MOE_ENOTSUP, "tensor %d: dtype %d not supported", i, g[i].dtype);
+    if (g[i].n < 0 || g[i].n > ((int64_t)1 << 36)) return fail(MOE_EINVAL, "tensor %d: n=%lld out of range [0, 2^36]", i, (long long)g[i].n);
+    if (g[i].reserved != 0) return fail(MOE_EINVAL, "tensor %d: reserved must be 0", i);
+    GradTensor t;
+    t.src = g[i].src;
+    t.dst = g[i].dst ? g[i].dst : const_cast<void*>(g[i].src);
+    t.n = g[i].n;
+    t.bf16 = g[i].dtype == MOE_BF16;
+    const uintptr_t both = reinterpret_cast<uintptr_t>(t.src) | reinterpret_cast<uintptr_t>(t.dst);
+    if (t.n > 0 && !t.src) return fail(MOE_EINVAL, "tensor %d: src is NULL", i);
+    if (t.n > 0 && both % (t.bf16 ? 2 : 4)) return fail(MOE_EINVAL, "tensor %d is not aligned to its elements", i);
+    out[i] = t;
+  }
+  return MOE_OK;
+}
+static moe_status check_grad_list(const moe_grad* g, int32_t count) {
+  if (count < 0 || count > kMaxGrads) return fail(MOE_EINVAL, "count=%d out of range [0, 2^16]", count);
+  if (count > 0 && !g) return fail(MOE_EINVAL, "grads is NULL");
+  return MOE_OK;
+}
+static moe_status check_grad_ws(int32_t count, void* ws, size_t ws_bytes) {
+  const size_t need = grad_workspace_bytes(count);
+  if (ws_bytes < need) return fail(MOE_EWORKSPACE, "workspace of %zu bytes < %zu needed", ws_bytes, need);
+  return need_ptr(ws, "ws");
+}
+
+size_t moe_grad_workspace_bytes(int32_t count) {
+  return count < 0 || count > kMaxGrads ? (fail(MOE_EINVAL, "count=%d out of range [0, 2^16]", count), 0) : grad_workspace_bytes(count);
+}
+
+moe_status moe_grad_norm(const moe_grad* grads, int32_t count, float* norm, void* ws, size_t ws_bytes, void* stream) {
+  MOE_TRY(check_grad_list(grads, count));
+  const std::unique_ptr<GradTensor[]> list(new (std::nothrow) GradTensor[count + 1]);
+  if (!list) return fail(MOE_EINVAL, "no host memory for %d tensors", count);
+  MOE_TRY(check_grads(grads, count, list.get()));
+  MOE_TRY(need_ptr(norm, "norm"));
+  MOE_TRY(check_grad_ws(count, ws, ws_bytes));
+  hipStream_t st = static_cast<hipStream_t>(stream);
+  MOE_STAGE(MOE_STAGE_GRAD, st, launch_grad_norm(list.get(), count, norm, ws, st), "gradient norm");
+  return MOE_OK;
+}
+
+moe_status moe_grad_clip(const moe_grad* grads, int32_t count, double max_norm, const float* norm_in, float* norm,
+                         void* ws, size_t ws_bytes, void* stream) {
+  MOE_TRY(check_grad_list(grads, count));
+  if (!(max_norm >= 0.0)) return fail(MOE_EINVAL, "max_norm=%g must be >= 0", max_norm);
+  const std::unique_ptr<GradTensor[]> list(new (std::nothrow) GradTensor[count + 1]);
+  if (!list) return fail(MOE_EINVAL, "no host memory for %d tensors", count);
+  MOE_TRY(check_grads(grads, count, list.get()));
+  MOE_TRY(opt_ptr(norm_in, "norm_in"));
+  if (!norm_in) {
+    MOE_TRY(need_ptr(norm, "norm"));
+    MOE_TRY(check_grad_ws(count, ws, ws_bytes));
+  }
+  hipStream_t st = static_cast<hipStream_t>(stream);
+  MOE_STAGE(MOE_STAGE_GRAD, st, launch_grad_clip(list.get(), count, max_norm, norm_in, norm, ws, st), "gradient clipping");
   return MOE_OK;
 }
 

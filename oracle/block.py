@@ -150,3 +150,29 @@ def dropout(x, p, seed, offset, residual=None):
     t = dropout_threshold(p)
     y = np.where(keep, x, 0.0) * (65536.0 / (65536 - t) if t < 65536 else 0.0)
     return y if residual is None else residual + y
+
+
+# ---- layer / RMS norm ----
+def norm_stats(s, eps, kind="layer"):
+    """Row means (zeros for "rms") and 1 / sqrt(mean squared deviation + eps)."""
+    mean = s.mean(axis=1) if kind == "layer" else np.zeros(s.shape[0])
+    return mean, 1.0 / np.sqrt(((s - mean[:, None]) ** 2).mean(axis=1) + eps)
+
+
+def norm(s, weight=None, bias=None, eps=1e-5, kind="layer"):
+    """y = (s - mean) rstd weight + bias of each row."""
+    mean, rstd = norm_stats(s, eps, kind)
+    y = (s - mean[:, None]) * rstd[:, None]
+    y = y if weight is None else y * weight
+    return y if bias is None else y + bias
+
+
+def norm_backward(dy, s, weight, mean, rstd, dsum=None, kind="layer"):
+    """dx, dweight, dbias for the statistics given (mean is ignored for "rms")."""
+    xh = (s - (mean[:, None] if kind == "layer" else 0.0)) * rstd[:, None]
+    g = dy if weight is None else dy * weight
+    dx = g - xh * (g * xh).mean(axis=1)[:, None]
+    if kind == "layer":
+        dx = dx - g.mean(axis=1)[:, None]
+    dx = dx * rstd[:, None]
+    return (dx if dsum is None else dx + dsum), (dy * xh).sum(axis=0), dy.sum(axis=0)
