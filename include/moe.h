@@ -462,6 +462,51 @@ moe_status moe_grad_norm(const moe_grad* grads, int32_t count, float* norm, void
 moe_status moe_grad_clip(const moe_grad* grads, int32_t count, double max_norm, const float* norm_in,
                          float* norm, void* ws, size_t ws_bytes, void* stream);
 
+/* 4-bit weights with group scales, for serving: each row of K elements is cut into groups of consecutive
+ * elements with one scale each.
+ *  codes  [rows, K / 2] uint8: byte i of a row holds element 2 i in its low half, 2 i + 1 in its high half.
+ *  INT4   value (c - 8) s for code c = 0 .. 15; s bf16 (any sign, finite), group 32, 64 or 128;
+ *         scales [K / group, rows]: plane g holds every row's scale of group g.
+ *  FP4    OCP E2M1 codes (sign, 2 bits of exponent, 1 of mantissa: 0 0.5 1 1.5 2 3 4 6) times
+ *         2^(e - 127), e an E8M0 byte (0 .. 254); group 32; scales as in the block-scaled FP8 calls: the byte of
+ *         group g of row r is at (g / 4) rows 4 + 4 r + g % 4, ceil(K / 128) rows 4 bytes in all.  Bytes of
+ *         groups past K / 32 are not used.
+ *  K: a multiple of group, at most 65536. */
+typedef enum { MOE_W4_INT4 = 0, MOE_W4_FP4 = 1 } moe_w4_format;
+
+typedef struct moe_w4 {
+  uint8_t* codes;
+  void* scales;
+  int32_t format;
+  int32_t group;
+} moe_w4;
+
+/* Host: bytes of scales for rows x K weights (0 if invalid). */
+int64_t moe_w4_scale_bytes(int64_t rows, int64_t K, int32_t format, int32_t group);
+
+/* moe_quantize_w4 — codes and scales of src [rows, K] dtype (MOE_BF16 or MOE_F32), finite values, into
+ * the arrays of w.  INT4: s = max|group| / 7 rounded to bf16 (1 for a group of zeros), c the nearest integer
+ * to x / s, ties to even, plus 8 (1 .. 15).  FP4: the smallest power of two s with max|group| / s <= 6, within
+ * 2^-127 .. 2^127 (1 for zeros), c the nearest value to x / s, ties to the even code.  rows >= 0. */
+moe_status moe_quantize_w4(int64_t rows, int64_t K, int dtype, const void* src, const moe_w4* w, void* stream);
+
+/* moe_dequantize_w4 — the values of w as out [rows, K] dtype, each rounded once (FP4 values are exact in
+ * either type, but for those below bf16's smallest step): for calls that take no 4-bit weights, e.g.
+ * moe_grouped_ffn on a prompt. */
+moe_status moe_dequantize_w4(int64_t rows, int64_t K, int dtype, const moe_w4* w, void* out, void* stream);
+
+/* moe_linear_w4 — moe_linear without Z, on 4-bit weights W (N' rows of K): out = residual + act(X W^T + bias).
+ *  dims.dtype must be MOE_BF16 (X, residual, out); K a multiple of the group.  Up to 64 rows the codes are
+ *  streamed, products are exact and sums fp32 (INT4: a group's sum is multiplied by its scale in
+ *  fp32); with more rows W is expanded to bf16 in the workspace first, where an INT4 value is rounded to
+ *  bf16 (half a step, 2^-9 of it).
+ *  An infinite element of X may make its row's results NaN where the exact sum is infinite (INT4).
+ *  residual may be out (with the same stride).  M = 0 does nothing.
+ *  ws: moe_linear_w4_workspace_bytes(dims) bytes. */
+size_t moe_linear_w4_workspace_bytes(const moe_linear_dims* dims);
+moe_status moe_linear_w4(const moe_linear_dims* dims, const void* X, const moe_w4* W, const float* bias,
+                         const void* residual, void* out, void* ws, size_t ws_bytes, void* stream);
+
 /* moe_decode — the whole forward layer in one kernel launch, for small token counts (decode /
  * inference): router logits, top-K with softmax, the selected experts' SwiGLU FFNs and the
  * weighted combine.  apxml.com "自定义核与核融合" (the five steps fused into one kernel) and
@@ -494,6 +539,16 @@ moe_status moe_decode(const moe_dims* dims, const void* X, const void* W_r, cons
                       const void* W_gate, const void* W_up, const void* W_down, float* logits,
                       int32_t* topk_idx, float* topk_w, void* out, void* ws, size_t ws_bytes,
                       void* stream);
+
+/* moe_decode_w4 — moe_decode with the experts' weights in 4 bits: W_gate, W_up (E n rows of d) and W_down
+ * (E d rows of n), all three of one format and group.  dims.dtype must be MOE_BF16 (X, W_r, out); d and n
+ * multiples of the group.  Products are exact and sums fp32, as in moe_linear_w4's streaming form; the
+ * SwiGLU activation is rounded to bf16 between the projections.  Everything else, the workspace
+ * (MOE_OP_DECODE), the bounded barriers and moe_decode_status() among it, is as for moe_decode. */
+moe_status moe_decode_w4(const moe_dims* dims, const void* X, const void* W_r, const float* bias,
+                         const moe_w4* W_gate, const moe_w4* W_up, const moe_w4* W_down, float* logits,
+                         int32_t* topk_idx, float* topk_w, void* out, void* ws, size_t ws_bytes,
+                         void* stream);
 
 /* moe_decode_status — host: waits for `stream` (hipStreamSynchronize), then reads and clears the
  * current device's decode status word.  Returns MOE_EHIP (with a message) if a moe_decode kernel
@@ -593,7 +648,7 @@ typedef enum {
   MOE_STAGE_DX_GEMM = 10,
   MOE_STAGE_ROUTER_BWD = 11, /* dS, dLogits and the dX gather-sum */
   MOE_STAGE_DWR_GEMM = 12,
-  MOE_STAGE_DECODE = 13,     /* the single-launch forward of moe_decode */
+  MOE_STAGE_DECODE = 13,     /* the single-launch forward of moe_decode, moe_decode_w4 */
   MOE_STAGE_FP8_QUANT = 14,  /* FP8 row quantisation (moe_quantize_fp8 and the activation's) */
   MOE_STAGE_FP8_UP = 15,     /* FP8 gate/up GEMM + SwiGLU */
   MOE_STAGE_FP8_DOWN = 16,   /* FP8 down GEMM */
@@ -603,7 +658,9 @@ typedef enum {
   MOE_STAGE_LINEAR_BWD = 20,  /* moe_linear_backward, and moe_backward_aux's logit dX GEMM */
   MOE_STAGE_NORM = 21,        /* moe_norm, moe_norm_backward */
   MOE_STAGE_GRAD = 22,        /* moe_grad_norm, moe_grad_clip */
-  MOE_STAGE_COUNT = 23
+  MOE_STAGE_W4 = 23,          /* moe_quantize_w4, moe_dequantize_w4 */
+  MOE_STAGE_LINEAR_W4 = 24,   /* moe_linear_w4 */
+  MOE_STAGE_COUNT = 25
 } moe_stage;
 
 /* Host: stage timing for measurement tools (not thread-safe; for a single host thread).

@@ -8,7 +8,8 @@ The functions keep the C names: ``moe_route``, ``moe_permute``, ``moe_grouped_ff
 ``moe_grouped_ffn_fp8``, ``moe_quantize_mx``, ``moe_grouped_ffn_mx``, ``moe_router_loss``,
 ``moe_router_loss_backward``, ``moe_backward_aux``, ``moe_dropout``, ``moe_combine_dropout``,
 ``moe_linear``, ``moe_linear_backward``, ``moe_norm``, ``moe_norm_backward``, ``moe_grad_norm``,
-``moe_grad_clip`` (plus sizing helpers).
+``moe_grad_clip``, ``moe_quantize_w4``, ``moe_dequantize_w4``, ``moe_linear_w4``, ``moe_decode_w4`` (plus
+sizing helpers).
 """
 import ctypes
 import os
@@ -24,6 +25,7 @@ OP_ROUTE, OP_PERMUTE, OP_FFN, OP_COMBINE, OP_FORWARD, OP_BACKWARD, OP_DECODE, OP
 FP8_E4M3, FP8_E5M2 = 0, 1
 ACTS = {"none": 0, "relu": 1, "gelu": 2, "silu": 3, "swiglu": 4}
 LINEAR_FORWARD, LINEAR_BACKWARD = 0, 1
+W4_FORMATS = {"int4": 0, "fp4": 1}
 NORM_KINDS = {"layer": 0, "rms": 1}
 LINEAR_OUT, LINEAR_DX, LINEAR_DW = 0, 1, 2
 STATUS = {0: "MOE_OK", -1: "MOE_EINVAL", -2: "MOE_ENOTSUP", -3: "MOE_EWORKSPACE", -4: "MOE_EHIP"}
@@ -38,12 +40,13 @@ EXPORTS = ["moe_max_rows", "moe_workspace_bytes", "moe_route", "moe_permute", "m
            "moe_router_loss_workspace_bytes", "moe_dropout", "moe_combine_dropout", "moe_linear",
            "moe_linear_backward", "moe_linear_workspace_bytes", "moe_linear_plan",
            "moe_norm", "moe_norm_workspace_bytes", "moe_norm_backward", "moe_grad_workspace_bytes", "moe_grad_norm",
-           "moe_grad_clip",
+           "moe_grad_clip", "moe_w4_scale_bytes", "moe_quantize_w4", "moe_dequantize_w4", "moe_linear_w4_workspace_bytes",
+           "moe_linear_w4", "moe_decode_w4",
            "moe_version", "moe_timing_enable", "moe_timing_read"]
 STAGES = ["router_gemm", "route", "tiles", "up_gemm", "down_gemm", "permute", "combine", "dact_gemm",
           "dw_down_gemm", "dw_gu_gemm", "dx_gemm", "router_bwd", "dwr_gemm", "decode", "fp8_quant",
           "fp8_up_gemm", "fp8_down_gemm", "router_loss", "dropout", "linear", "linear_bwd", "norm",
-          "grad"]
+          "grad", "w4", "linear_w4"]
 
 
 class MoEError(RuntimeError):
@@ -73,6 +76,10 @@ class NormDims(ctypes.Structure):
 class GradStruct(ctypes.Structure):
     _fields_ = [("src", ctypes.c_void_p), ("dst", ctypes.c_void_p), ("n", ctypes.c_int64), ("dtype", ctypes.c_int32),
                 ("reserved", ctypes.c_int32)]
+
+
+class W4Struct(ctypes.Structure):
+    _fields_ = [("codes", ctypes.c_void_p), ("scales", ctypes.c_void_p), ("format", ctypes.c_int32), ("group", ctypes.c_int32)]
 
 
 PLAN_FIELDS = ["topk_idx", "topk_w", "counts", "expert_off", "row_token", "row_w", "tok_off",
@@ -138,7 +145,15 @@ def lib():
         L.moe_grad_workspace_bytes.argtypes, L.moe_grad_workspace_bytes.restype = [i32], sz
         L.moe_grad_norm.argtypes = [pg, i32, vp, vp, sz, vp]
         L.moe_grad_clip.argtypes = [pg, i32, ctypes.c_double, vp, vp, vp, sz, vp]
-        for f in ("moe_norm", "moe_norm_backward", "moe_grad_norm", "moe_grad_clip"):
+        pw, ci = ctypes.POINTER(W4Struct), ctypes.c_int
+        L.moe_w4_scale_bytes.argtypes, L.moe_w4_scale_bytes.restype = [i64, i64, i32, i32], i64
+        L.moe_quantize_w4.argtypes = [i64, i64, ci, vp, pw, vp]
+        L.moe_dequantize_w4.argtypes = [i64, i64, ci, pw, vp, vp]
+        L.moe_linear_w4_workspace_bytes.argtypes, L.moe_linear_w4_workspace_bytes.restype = [pl], sz
+        L.moe_linear_w4.argtypes = [pl, vp, pw, vp, vp, vp, vp, sz, vp]
+        L.moe_decode_w4.argtypes = [pd, vp, vp, vp, pw, pw, pw, vp, vp, vp, vp, vp, sz, vp]
+        for f in ("moe_norm", "moe_norm_backward", "moe_grad_norm", "moe_grad_clip", "moe_quantize_w4", "moe_dequantize_w4",
+                  "moe_linear_w4", "moe_decode_w4"):
             getattr(L, f).restype = st
         for f in ("moe_backward_aux", "moe_router_loss", "moe_router_loss_backward", "moe_dropout",
                   "moe_combine_dropout", "moe_linear", "moe_linear_backward"):
@@ -551,6 +566,89 @@ def moe_grad_clip(grads, max_norm, norm_in, norm, ws, ws_bytes, stream=None):
     _on_gpu(*grads.src[:1], norm_in, norm, ws)
     _check(lib().moe_grad_clip(grads.array, grads.count, float(max_norm), _p(norm_in), _p(norm), _p(ws), ws_bytes,
                                _stream(stream)))
+
+
+class W4:
+    """4-bit weights: codes uint8 [..., K / 2] (the even element in the low half) and their group scales, "int4"
+    (bf16 [K / group, rows]) or "fp4" (bytes [ceil(K / 128), rows, 4]; group 32).  The leading dimensions of codes
+    make up the rows."""
+
+    def __init__(self, codes, scales, format="int4", group=128):
+        self.codes, self.scales, self.format, self.group = codes, scales, format, int(group)
+        self.K = 2 * codes.shape[-1]
+        self.rows = codes.numel() // max(codes.shape[-1], 1)
+        if codes.dtype is not torch.uint8 or not codes.is_contiguous():
+            raise MoEError(-1, "codes must be contiguous bytes")
+        if scales.dtype is not (torch.bfloat16 if format == "int4" else torch.uint8) or not scales.is_contiguous():
+            raise MoEError(-1, "scales must be contiguous %s" % ("bf16" if format == "int4" else "bytes"))
+        need = lib().moe_w4_scale_bytes(self.rows, self.K, W4_FORMATS[format], self.group)
+        if need == 0 and self.rows > 0:
+            raise MoEError(-2, lib().moe_last_error().decode())
+        if scales.numel() * scales.element_size() != need:
+            raise MoEError(-1, "scales hold %d bytes, %d x %d weights need %d" % (scales.numel() * scales.element_size(),
+                                                                                  self.rows, self.K, need))
+        if scales.device != codes.device:
+            raise MoEError(-1, "codes are on %s but scales on %s" % (codes.device, scales.device))
+        self.struct = W4Struct(codes.data_ptr(), scales.data_ptr(), W4_FORMATS[format], self.group)
+        self._ref = ctypes.byref(self.struct)
+
+
+def make_w4(rows, K, format="int4", group=128, device="cuda"):
+    """Room for rows x K 4-bit weights, for moe_quantize_w4 to fill."""
+    codes = torch.empty(rows, K // 2, dtype=torch.uint8, device=device)
+    if format == "int4":
+        return W4(codes, torch.empty(K // group, rows, dtype=torch.bfloat16, device=device), format, group)
+    return W4(codes, torch.full((-(-K // 128), rows, 4), 127, dtype=torch.uint8, device=device), format, group)
+
+
+def _w4_matrix(t, w4, name):
+    if t.dtype not in (torch.bfloat16, torch.float32) or not t.is_contiguous() or t.numel() != w4.rows * w4.K:
+        raise MoEError(-1, "%s must be %d x %d contiguous bf16 or fp32" % (name, w4.rows, w4.K))
+    return MOE_BF16 if t.dtype is torch.bfloat16 else MOE_F32
+
+
+def moe_quantize_w4(src, w4, stream=None):
+    """4-bit codes and scales of a bf16 / fp32 tensor of w4's size."""
+    dtype = _w4_matrix(src, w4, "src")
+    _on_gpu(src, w4.codes)
+    _check(lib().moe_quantize_w4(w4.rows, w4.K, dtype, _p(src), w4._ref, _stream(stream)))
+
+
+def moe_dequantize_w4(w4, out, stream=None):
+    """The values of 4-bit weights as bf16 or fp32."""
+    dtype = _w4_matrix(out, w4, "out")
+    _on_gpu(out, w4.codes)
+    _check(lib().moe_dequantize_w4(w4.rows, w4.K, dtype, w4._ref, _p(out), _stream(stream)))
+
+
+def linear_w4_workspace(dims, device="cuda"):
+    nbytes = lib().moe_linear_w4_workspace_bytes(ctypes.byref(dims))
+    return torch.empty(max(nbytes, 256), dtype=torch.uint8, device=device), nbytes
+
+
+def _w4_rows(w4, rows, K, name):
+    if w4.rows != rows or w4.K != K:
+        raise MoEError(-1, "%s holds %d x %d weights, %d x %d expected" % (name, w4.rows, w4.K, rows, K))
+
+
+def moe_linear_w4(dims, X, W, bias, residual, out, ws, ws_bytes, stream=None):
+    """out = residual + act(X W^T + bias) with 4-bit weights W (a W4); bias and residual may be None."""
+    _w4_rows(W, 2 * dims.N if dims.act == ACTS["swiglu"] else dims.N, dims.K, "W")
+    _on_gpu(X, W.codes, bias, residual, out, ws)
+    status = lib().moe_linear_w4(ctypes.byref(dims), _p(X), W._ref, _p(bias), _p(residual), _p(out), _p(ws), ws_bytes,
+                                 _stream(stream))
+    if status:
+        _check(status)
+
+
+def moe_decode_w4(dims, X, W_r, bias, W_gate, W_up, W_down, logits, topk_idx, topk_w, out, ws, ws_bytes, stream=None):
+    """moe_decode with 4-bit expert weights (W4 of E n, E n and E d rows)."""
+    _w4_rows(W_gate, dims.E * dims.n, dims.d, "W_gate")
+    _w4_rows(W_up, dims.E * dims.n, dims.d, "W_up")
+    _w4_rows(W_down, dims.E * dims.d, dims.n, "W_down")
+    _on_gpu(X, W_r, bias, W_gate.codes, W_up.codes, W_down.codes, logits, topk_idx, topk_w, out, ws)
+    _check(lib().moe_decode_w4(ctypes.byref(dims), _p(X), _p(W_r), _p(bias), W_gate._ref, W_up._ref, W_down._ref, _p(logits),
+                               _p(topk_idx), _p(topk_w), _p(out), _p(ws), ws_bytes, _stream(stream)))
 
 
 def moe_timing_enable(on):

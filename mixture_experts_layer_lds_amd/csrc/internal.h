@@ -191,6 +191,23 @@ hipError_t launch_linear_bwd(const LinShape& s, const void* dY, const void* X, c
 // dX += dL W_r for dense logit gradients dL [T][E_pad] in the element type
 hipError_t launch_logit_dx(const Shape& s, const void* dL, int E_pad, const void* W_r, void* dX, hipStream_t st);
 
+// ---- 4-bit weights (w4.hip, decode.hip) ----
+struct W4View {
+  const uint8_t* codes;
+  const void* scales;
+  int format, group;  // moe_w4_format; elements per scale
+};
+hipError_t launch_quant_w4(const void* src, bool is_bf16, int format, int group, int64_t rows, int64_t K, uint8_t* codes,
+                           void* scales, hipStream_t st);
+hipError_t launch_expand_w4(const W4View& w, int64_t rows, int64_t K, bool is_bf16, void* out, hipStream_t st);
+size_t linear_w4_workspace_bytes(const LinShape& s);
+hipError_t launch_linear_w4(const LinShape& s, const void* X, const W4View& w, const float* bias, const void* residual, void* out,
+                            void* ws, hipStream_t st);
+// launch_decode with the experts' weights in 4 bits (one format and group for the three)
+hipError_t launch_decode_w4(const Shape& s, const void* X, const void* W_r, const float* bias, const W4View& W_gate,
+                            const W4View& W_up, const W4View& W_down, float* logits, int32_t* topk_idx, float* topk_w, void* out,
+                            void* ws, hipStream_t st);
+
 // single-launch forward for small T (decode.hip)
 size_t decode_workspace_bytes(int64_t T, int64_t d, int64_t n, int E, int K);
 hipError_t launch_decode(const Shape& s, const void* X, const void* W_r, const float* bias,

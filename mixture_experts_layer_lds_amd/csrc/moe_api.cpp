@@ -13,6 +13,7 @@
 #include "../../include/moe.h"
 #include "internal.h"
 #include "philox.h"
+#include "w4.h"
 
 using namespace moe;
 
@@ -979,7 +980,8 @@ static moe_status check_grad_ws(int32_t count, void* ws, size_t ws_bytes) {
 }
 
 size_t moe_grad_workspace_bytes(int32_t count) {
-  return count < 0 || count > kMaxGrads ? (fail(MOE_EINVAL, "count=%d out of range [0, 2^16]", count), 0) : grad_workspace_bytes(count);
+  if (count < 0 || count > kMaxGrads) return fail(MOE_EINVAL, "count=%d out of range [0, 2^16]", count), 0;
+  return grad_workspace_bytes(count);
 }
 
 moe_status moe_grad_norm(const moe_grad* grads, int32_t count, float* norm, void* ws, size_t ws_bytes, void* stream) {
@@ -1008,6 +1010,121 @@ moe_status moe_grad_clip(const moe_grad* grads, int32_t count, double max_norm, 
   }
   hipStream_t st = static_cast<hipStream_t>(stream);
   MOE_STAGE(MOE_STAGE_GRAD, st, launch_grad_clip(list.get(), count, max_norm, norm_in, norm, ws, st), "gradient clipping");
+  return MOE_OK;
+}
+
+// ---- 4-bit weights ----
+static_assert((int)MOE_W4_INT4 == W4_INT && (int)MOE_W4_FP4 == W4_FP, "format codes");
+static moe_status check_w4_format(int64_t K, int32_t format, int32_t group) {
+  if (format != MOE_W4_INT4 && format != MOE_W4_FP4) return fail(MOE_EINVAL, "4-bit format %d invalid", format);
+  if (format == MOE_W4_FP4 ? group != 32 : group != 32 && group != 64 && group != 128)
+    return fail(MOE_ENOTSUP, "group of %d not supported", group);
+  if (K < 1 || K > 65536) return fail(MOE_EINVAL, "K=%lld out of range [1, 65536]", (long long)K);
+  if (K % group) return fail(MOE_ENOTSUP, "K=%lld is not a multiple of the group %d", (long long)K, group);
+  return MOE_OK;
+}
+static moe_status check_w4(int64_t K, const moe_w4* w, const char* name, W4View* v) {
+  if (!w) return fail(MOE_EINVAL, "%s is NULL", name);
+  MOE_TRY(check_w4_format(K, w->format, w->group));
+  if (!w->codes || !aligned16(w->codes)) return fail(MOE_EINVAL, "codes of %s are NULL or not 16-byte aligned", name);
+  if (!w->scales || !aligned16(w->scales)) return fail(MOE_EINVAL, "scales of %s are NULL or not 16-byte aligned", name);
+  *v = W4View{w->codes, w->scales, w->format, w->group};
+  return MOE_OK;
+}
+constexpr int64_t kMaxW4Rows = (int64_t)1 << 31;
+static moe_status check_w4_matrix(int64_t rows, int64_t K, int dtype, const moe_w4* w) {
+  if (rows < 0 || rows > kMaxW4Rows) return fail(MOE_EINVAL, "rows=%lld out of range [0, 2^31]", (long long)rows);
+  if (dtype != MOE_BF16 && dtype != MOE_F32) return fail(MOE_ENOTSUP, "dtype %d not supported", dtype);
+  if (!w) return fail(MOE_EINVAL, "w is NULL");
+  return check_w4_format(K, w->format, w->group);
+}
+
+int64_t moe_w4_scale_bytes(int64_t rows, int64_t K, int32_t format, int32_t group) {
+  if (rows < 0 || rows > kMaxW4Rows) return fail(MOE_EINVAL, "rows=%lld out of range [0, 2^31]", (long long)rows), 0;
+  if (check_w4_format(K, format, group) != MOE_OK) return 0;
+  return format == MOE_W4_INT4 ? K / group * rows * 2 : mx_scale_bytes(rows, K);
+}
+
+moe_status moe_quantize_w4(int64_t rows, int64_t K, int dtype, const void* src, const moe_w4* w, void* stream) {
+  MOE_TRY(check_w4_matrix(rows, K, dtype, w));
+  if (rows == 0) return MOE_OK;
+  W4View v;
+  MOE_TRY(need_ptr(src, "src"));
+  MOE_TRY(check_w4(K, w, "w", &v));
+  hipStream_t st = static_cast<hipStream_t>(stream);
+  MOE_STAGE(MOE_STAGE_W4, st, launch_quant_w4(src, dtype == MOE_BF16, v.format, v.group, rows, K, w->codes, w->scales, st),
+            "4-bit quantisation");
+  return MOE_OK;
+}
+
+moe_status moe_dequantize_w4(int64_t rows, int64_t K, int dtype, const moe_w4* w, void* out, void* stream) {
+  MOE_TRY(check_w4_matrix(rows, K, dtype, w));
+  if (rows == 0) return MOE_OK;
+  W4View v;
+  MOE_TRY(check_w4(K, w, "w", &v));
+  MOE_TRY(need_ptr(out, "out"));
+  hipStream_t st = static_cast<hipStream_t>(stream);
+  MOE_STAGE(MOE_STAGE_W4, st, launch_expand_w4(v, rows, K, dtype == MOE_BF16, out, st), "4-bit expansion");
+  return MOE_OK;
+}
+
+moe_status moe_decode_w4(const moe_dims* dims, const void* X, const void* W_r, const float* bias, const moe_w4* W_gate,
+                         const moe_w4* W_up, const moe_w4* W_down, float* logits, int32_t* topk_idx, float* topk_w, void* out,
+                         void* ws, size_t ws_bytes, void* stream) {
+  MOE_TRY(check_dims(dims));
+  if (dims->dtype != MOE_BF16) return fail(MOE_ENOTSUP, "4-bit weights need dtype MOE_BF16");
+  if (dims->round_mode != MOE_ROUND_NONE)
+    return fail(MOE_ENOTSUP, "moe_decode_w4 routes with plain top-K (round_mode must be NONE)");
+  if (dims->T > 1024) return fail(MOE_ENOTSUP, "moe_decode_w4 handles T <= 1024 (got %lld)", (long long)dims->T);
+  W4View gate, up, down;
+  MOE_TRY(check_w4(dims->d, W_gate, "W_gate", &gate));
+  MOE_TRY(check_w4(dims->d, W_up, "W_up", &up));
+  MOE_TRY(check_w4(dims->n, W_down, "W_down", &down));
+  if (up.format != gate.format || up.group != gate.group || down.format != gate.format || down.group != gate.group)
+    return fail(MOE_ENOTSUP, "W_gate, W_up and W_down must have one format and group");
+  MOE_TRY(need_ptr(X, "X"));
+  MOE_TRY(need_ptr(W_r, "W_r"));
+  MOE_TRY(opt_ptr(bias, "bias"));
+  MOE_TRY(need_ptr(logits, "logits"));
+  MOE_TRY(need_ptr(topk_idx, "topk_idx"));
+  MOE_TRY(need_ptr(topk_w, "topk_w"));
+  MOE_TRY(need_ptr(out, "out"));
+  MOE_TRY(check_ws(dims, MOE_OP_DECODE, ws, ws_bytes));
+  hipStream_t st = static_cast<hipStream_t>(stream);
+  MOE_STAGE(MOE_STAGE_DECODE, st,
+            launch_decode_w4(shape_of(dims), X, W_r, bias, gate, up, down, logits, topk_idx, topk_w, out, ws, st),
+            "decode on 4-bit weights");
+  return MOE_OK;
+}
+
+static moe_status check_linear_w4(const moe_linear_dims* dims, LinShape* s) {
+  MOE_TRY(check_linear(dims, s));
+  if (!s->bf16) return fail(MOE_ENOTSUP, "4-bit weights need dtype MOE_BF16");
+  if (s->K % 32) return fail(MOE_ENOTSUP, "K=%lld must be a multiple of 32", (long long)s->K);
+  return MOE_OK;
+}
+
+size_t moe_linear_w4_workspace_bytes(const moe_linear_dims* dims) {
+  LinShape s;
+  return check_linear_w4(dims, &s) == MOE_OK ? linear_w4_workspace_bytes(s) : 0;
+}
+
+moe_status moe_linear_w4(const moe_linear_dims* dims, const void* X, const moe_w4* W, const float* bias,
+                         const void* residual, void* out, void* ws, size_t ws_bytes, void* stream) {
+  LinShape s;
+  MOE_TRY(check_linear_w4(dims, &s));
+  if (s.M == 0) return MOE_OK;
+  W4View w;
+  MOE_TRY(check_w4(s.K, W, "W", &w));
+  MOE_TRY(need_ptr(X, "X"));
+  MOE_TRY(opt_ptr(bias, "bias"));
+  MOE_TRY(opt_ptr(residual, "residual"));
+  MOE_TRY(need_ptr(out, "out"));
+  MOE_TRY(check_alias(out, s.ldy, residual, s.ldr, "out"));
+  if (out == X) return fail(MOE_EINVAL, "out is the X array");
+  MOE_TRY(check_linear_ws(linear_w4_workspace_bytes(s), ws, ws_bytes));
+  hipStream_t st = static_cast<hipStream_t>(stream);
+  MOE_STAGE(MOE_STAGE_LINEAR_W4, st, launch_linear_w4(s, X, w, bias, residual, out, ws, st), "linear on 4-bit weights");
   return MOE_OK;
 }
 
