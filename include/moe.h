@@ -542,9 +542,11 @@ moe_status moe_decode(const moe_dims* dims, const void* X, const void* W_r, cons
 
 /* moe_decode_w4 — moe_decode with the experts' weights in 4 bits: W_gate, W_up (E n rows of d) and W_down
  * (E d rows of n), all three of one format and group.  dims.dtype must be MOE_BF16 (X, W_r, out); d and n
- * multiples of the group.  Products are exact and sums fp32, as in moe_linear_w4's streaming form; the
- * SwiGLU activation is rounded to bf16 between the projections.  Everything else, the workspace
- * (MOE_OP_DECODE), the bounded barriers and moe_decode_status() among it, is as for moe_decode. */
+ * multiples of the group; plain top-K, T <= 1024.  Products are exact and sums fp32, as in moe_linear_w4's
+ * streaming form; the SwiGLU activation is rounded to bf16 between the projections.  Routing is the same
+ * function of the logits as moe_decode's.  It is a chain of three to five launches without grid-wide
+ * barriers, so nothing has to be resident at once and there is no status to ask for.
+ *  ws: moe_workspace_bytes(dims, MOE_OP_DECODE) bytes, contents on entry unused. */
 moe_status moe_decode_w4(const moe_dims* dims, const void* X, const void* W_r, const float* bias,
                          const moe_w4* W_gate, const moe_w4* W_up, const moe_w4* W_down, float* logits,
                          int32_t* topk_idx, float* topk_w, void* out, void* ws, size_t ws_bytes,
@@ -648,7 +650,7 @@ typedef enum {
   MOE_STAGE_DX_GEMM = 10,
   MOE_STAGE_ROUTER_BWD = 11, /* dS, dLogits and the dX gather-sum */
   MOE_STAGE_DWR_GEMM = 12,
-  MOE_STAGE_DECODE = 13,     /* the single-launch forward of moe_decode, moe_decode_w4 */
+  MOE_STAGE_DECODE = 13,     /* the single-launch forward of moe_decode; all of moe_decode_w4 */
   MOE_STAGE_FP8_QUANT = 14,  /* FP8 row quantisation (moe_quantize_fp8 and the activation's) */
   MOE_STAGE_FP8_UP = 15,     /* FP8 gate/up GEMM + SwiGLU */
   MOE_STAGE_FP8_DOWN = 16,   /* FP8 down GEMM */

@@ -12,7 +12,7 @@ CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libmoe_mi355x.so")
 BUILD = os.path.join(HERE, "_build")
 SOURCES = ["route.hip", "gemm_fwd.hip", "backward.hip", "combine.hip", "decode.hip", "fp8.hip",
-           "router_loss.hip", "dropout.hip", "linear.hip", "norm.hip", "grads.hip", "w4.hip",
+           "router_loss.hip", "dropout.hip", "linear.hip", "norm.hip", "grads.hip", "w4.hip", "decode_w4.hip",
            "moe_api.cpp"]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")

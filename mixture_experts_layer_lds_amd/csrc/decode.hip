@@ -42,7 +42,7 @@
 
 #include "internal.h"
 #include "skinny.h"
-#include "w4.h"
+#include "topk_wave.h"
 
 namespace moe {
 
@@ -57,7 +57,6 @@ struct DecodeArgs {
   const void* W_gate;
   const void* W_up;
   const void* W_down;
-  const void *s_gate, *s_up, *s_down;  // scales of 4-bit weights
   float* logits;
   int32_t* topk_idx;
   float* topk_w;
@@ -122,42 +121,19 @@ __device__ __forceinline__ int dec_pick_w(int items, int ns) {
   return best_w;
 }
 
-// The group's tile of ng token groups: member m streams its share of ns steps, stream(a, b, acc); the
+// The group's tile: member m streams its share of steps [s0, s1) for ng token groups; the
 // epilogue epi(v) runs on member 0 with the tile summed over members (v[g], rows 4 (lane / 16)
 // + i, column lane % 16 of token group g).
-template <class Stream, class Epi>
-__device__ __forceinline__ void dec_group_run(DecGroup& G, DecLds& L, int ng, int ns, Stream stream, Epi epi) {
+template <typename T, class Epi>
+__device__ __forceinline__ void dec_group_tile(DecGroup& G, DecLds& L, const T* wrow, const T* const* xrow,
+                                               int ng, int s0, int s1, Epi epi) {
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int a = ns * G.m / G.W, b = ns * (G.m + 1) / G.W;
+  const int ko = (lane >> 4) * DecMma<T>::V;
+  const int ns = s1 - s0;
+  const int a = s0 + ns * G.m / G.W, b = s0 + ns * (G.m + 1) / G.W;
   f32x4 acc[DEC_NG];
 #pragma unroll
   for (int g = 0; g < DEC_NG; ++g) acc[g] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-  stream(a, b, acc);
-  if (G.W == 1) {
-    epi(acc);
-    return;
-  }
-  const int buf = G.seq & 1, use = G.seq >> 1;
-  ++G.seq;
-  dec_lds_wait_ge(&L.consumed[G.grp][buf], use);  // the buffer's previous tile has been read
-  for (int g = 0; g < ng; ++g) L.part[((wave * 2 + buf) * DEC_NG + g) * 64 + lane] = acc[g];
-  if (lane == 0) __hip_atomic_fetch_add(&L.arrive[G.grp][buf], 1, __ATOMIC_RELEASE, __HIP_MEMORY_SCOPE_WORKGROUP);
-  if (G.m == 0) {
-    dec_lds_wait_ge(&L.arrive[G.grp][buf], (use + 1) * G.W);
-    f32x4 v[DEC_NG];
-    for (int g = 0; g < ng; ++g) {
-      v[g] = L.part[((wave * 2 + buf) * DEC_NG + g) * 64 + lane];
-      for (int mm = 1; mm < G.W; ++mm) v[g] += L.part[(((wave + mm) * 2 + buf) * DEC_NG + g) * 64 + lane];
-    }
-    if (lane == 0) __hip_atomic_store(&L.consumed[G.grp][buf], use + 1, __ATOMIC_RELEASE, __HIP_MEMORY_SCOPE_WORKGROUP);
-    epi(v);
-  }
-}
-
-// Weights of the element type: steps [a, b) of the rows at wrow against the vectors at xrow.
-template <typename T>
-__device__ __forceinline__ void dec_rows(const T* wrow, const T* const* xrow, int ng, int a, int b, f32x4* acc) {
-  const int ko = ((threadIdx.x & 63) >> 4) * DecMma<T>::V;
   if (ng == 3) {
     DecStream<T, 3> ds;
     ds.w = wrow + ko;
@@ -176,56 +152,24 @@ __device__ __forceinline__ void dec_rows(const T* wrow, const T* const* xrow, in
     ds.x[0] = xrow[0] + ko;
     dec_stream<T, 1>(ds, a, b, acc);
   }
-}
-
-// The experts' weights: in the element type, or 4-bit codes (bf16 layers).
-// NG: token groups of 16 per pass over a tile's rows, as many as the 128 registers of 16 waves hold.
-struct DecPlain { static constexpr bool W4 = false; static constexpr int FMT = 0, GROUP = 32, NG = DEC_NG; };
-template <int F, int G> struct DecW4 { static constexpr bool W4 = true; static constexpr int FMT = F, GROUP = G, NG = F == W4_FP ? 2 : 1; };
-
-// 4-bit weights: blocks [a, b) of the rows; code and scale as W4Stream's w and s.
-template <int FMT, int GROUP, int NG>
-__device__ __forceinline__ void dec_rows_w4_ng(const uint8_t* code, const uint8_t* scale, int64_t plane, const bf16* const* xrow,
-                                               int K, int a, int b, f32x4* acc) {
-  W4Stream<FMT, GROUP, NG, 1, 1> ws;
-  ws.w[0] = code;
-  ws.s[0] = scale;
-  ws.plane = plane;
-  ws.K = K;
-#pragma unroll
-  for (int g = 0; g < NG; ++g) ws.x[g] = xrow[g] + (FMT == W4_INT ? 8 : 32) * ((threadIdx.x & 63) >> 4);
-  f32x4 (&ac)[1][NG] = *reinterpret_cast<f32x4(*)[1][NG]>(acc);
-  if (a < b) ws.run(a, b, ac);
-#pragma unroll
-  for (int g = 0; g < NG; ++g) acc[g] *= w4_factor<FMT>();
-}
-template <int FMT, int GROUP>
-__device__ __forceinline__ void dec_rows_w4(const uint8_t* code, const uint8_t* scale, int64_t plane, const bf16* const* xrow,
-                                            int ng, int K, int a, int b, f32x4* acc) {
-  if constexpr (DecW4<FMT, GROUP>::NG == 2)
-    if (ng == 2) return dec_rows_w4_ng<FMT, GROUP, 2>(code, scale, plane, xrow, K, a, b, acc);
-  dec_rows_w4_ng<FMT, GROUP, 1>(code, scale, plane, xrow, K, a, b, acc);
-}
-
-__device__ __forceinline__ uint32_t dec_order_key(float x) {
-  if (x != x) return 0u;
-  const uint32_t u = __float_as_uint(x == 0.0f ? 0.0f : x);
-  return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
-}
-__device__ __forceinline__ float dec_key_value(uint32_t k) {
-  return __uint_as_float((k & 0x80000000u) ? (k & 0x7fffffffu) : ~k);
-}
-
-template <typename T>
-__device__ __forceinline__ void dec_store4(T* p, f32x4 v) {
-  if constexpr (sizeof(T) == 2) {
-    const uint32_t lo = (uint32_t)__builtin_bit_cast(uint16_t, from_f32<bf16>(v[0])) |
-                        ((uint32_t)__builtin_bit_cast(uint16_t, from_f32<bf16>(v[1])) << 16);
-    const uint32_t hi = (uint32_t)__builtin_bit_cast(uint16_t, from_f32<bf16>(v[2])) |
-                        ((uint32_t)__builtin_bit_cast(uint16_t, from_f32<bf16>(v[3])) << 16);
-    *reinterpret_cast<u32x2*>(p) = u32x2{lo, hi};
-  } else {
-    *reinterpret_cast<f32x4*>(p) = v;
+  if (G.W == 1) {
+    epi(acc);
+    return;
+  }
+  const int buf = G.seq & 1, use = G.seq >> 1;
+  ++G.seq;
+  dec_lds_wait_ge(&L.consumed[G.grp][buf], use);  // the buffer's previous tile has been read
+  for (int g = 0; g < ng; ++g) L.part[((wave * 2 + buf) * DEC_NG + g) * 64 + lane] = acc[g];
+  if (lane == 0) __hip_atomic_fetch_add(&L.arrive[G.grp][buf], 1, __ATOMIC_RELEASE, __HIP_MEMORY_SCOPE_WORKGROUP);
+  if (G.m == 0) {
+    dec_lds_wait_ge(&L.arrive[G.grp][buf], (use + 1) * G.W);
+    f32x4 v[DEC_NG];
+    for (int g = 0; g < ng; ++g) {
+      v[g] = L.part[((wave * 2 + buf) * DEC_NG + g) * 64 + lane];
+      for (int mm = 1; mm < G.W; ++mm) v[g] += L.part[(((wave + mm) * 2 + buf) * DEC_NG + g) * 64 + lane];
+    }
+    if (lane == 0) __hip_atomic_store(&L.consumed[G.grp][buf], use + 1, __ATOMIC_RELEASE, __HIP_MEMORY_SCOPE_WORKGROUP);
+    epi(v);
   }
 }
 
@@ -294,7 +238,7 @@ __global__ __launch_bounds__(256) void k_dec_clear(unsigned long long* bar, int3
   for (int i = threadIdx.x; i < E; i += 256) cnt[i] = 0;
 }
 
-template <typename T, class Q>
+template <typename T>
 __global__ __launch_bounds__(DEC_THREADS) void k_decode(DecodeArgs a) {
   unsigned long long* bar = a.bar;
   __shared__ DecLds L;
@@ -322,7 +266,7 @@ __global__ __launch_bounds__(DEC_THREADS) void k_decode(DecodeArgs a) {
       const T* xr[DEC_NG];
 #pragma unroll
       for (int g = 0; g < DEC_NG; ++g) xr[g] = X + (int64_t)min((g0 + g) * 16 + r16, T_ - 1) * d;
-      dec_group_run(G, L, ng, d / S, [&](int sa, int sb, f32x4* acc) { dec_rows<T>(wrow, xr, ng, sa, sb, acc); }, [&](const f32x4* v) {
+      dec_group_tile<T>(G, L, wrow, xr, ng, 0, d / S, [&](const f32x4* v) {
         for (int g = 0; g < ng; ++g) {
           const int t = (g0 + g) * 16 + r16;
 #pragma unroll
@@ -340,40 +284,9 @@ __global__ __launch_bounds__(DEC_THREADS) void k_decode(DecodeArgs a) {
   {
     const int nw = gridDim.x * DEC_WAVES;
     for (int t = blockIdx.x * DEC_WAVES + wave; t < T_; t += nw) {
-      // lane i holds the order keys of experts i + 64 j (E <= 1024); each round takes the largest
-      // key still in play (a DPP wave maximum) and, among the experts holding it, the lowest id
-      // (ballots in ascending e): logit descending, then expert id ascending
-      const int ej = (E + 63) >> 6;
-      uint32_t key[16];
-      uint32_t alive = 0;
-#pragma unroll
-      for (int j = 0; j < 16; ++j) {
-        const int e = lane + 64 * j;
-        key[j] = e < E ? dec_order_key(a.logits[(int64_t)t * E + e]) : 0u;
-        alive |= e < E ? (1u << j) : 0u;
-      }
-      int my_e = 0;
-      float my_v = 0.0f;
-      for (int k = 0; k < K; ++k) {
-        uint32_t lm = 0;  // NaN keys are 0 too; ties at 0 are settled among live candidates
-#pragma unroll
-        for (int j = 0; j < 16; ++j)
-          if (j < ej && ((alive >> j) & 1u)) lm = key[j] > lm ? key[j] : lm;
-        const uint32_t kmax = wave_max_u32(lm);
-        int win = -1;
-#pragma unroll
-        for (int j = 0; j < 16; ++j) {
-          if (j >= ej) break;
-          const uint64_t m = __builtin_amdgcn_ballot_w64(((alive >> j) & 1u) && key[j] == kmax);
-          if (win < 0 && m != 0ull) win = 64 * j + (int)__builtin_ctzll(m);
-        }
-        win = __builtin_amdgcn_readfirstlane(win);
-        if (lane == (win & 63)) alive &= ~(1u << (win >> 6));
-        if (lane == k) {
-          my_e = win;
-          my_v = dec_key_value(kmax);
-        }
-      }
+      int my_e;
+      float my_v;
+      wave_select(a.logits + (int64_t)t * E, E, K, my_e, my_v);
       const float vmax = __shfl(my_v, 0, 64);
       const float ex = lane < K ? __expf(my_v - vmax) : 0.0f;
       const float sum = wave_sum(ex);
@@ -395,33 +308,20 @@ __global__ __launch_bounds__(DEC_THREADS) void k_decode(DecodeArgs a) {
     const T* Wu = reinterpret_cast<const T*>(a.W_up);
     T* act = reinterpret_cast<T*>(a.act);
     const int tiles = n / 8;
-    const int items = nact * tiles, steps = Q::W4 ? w4_blocks(d) : d / S;
-    G.setup(dec_pick_w(items, steps));
+    const int items = nact * tiles;
+    G.setup(dec_pick_w(items, d / S));
     for (int u = G.gid; u < items; u += G.ngroups) {
       const int e = L.active[u / tiles], j0 = (u % tiles) * 8;
       const int c = __builtin_amdgcn_readfirstlane(a.cnt[e]);
       const int32_t* lst = a.list + (int64_t)e * T_;
       const T* wrow = r16 < 8 ? Wg + ((int64_t)e * n + j0 + r16) * d : Wu + ((int64_t)e * n + j0 + r16 - 8) * d;
-      const uint8_t *code = nullptr, *scale = nullptr;
-      if constexpr (Q::W4) {
-        const int64_t row = (int64_t)e * n + j0;
-        code = static_cast<const uint8_t*>(r16 < 8 ? a.W_gate : a.W_up) + (row + (r16 & 7)) * (d / 2) + 16 * q;
-        // INT: scales of tile rows 4 q + i (gate for q < 2); FP: the byte of the lane's row and group
-        if (Q::FMT == W4_INT) scale = static_cast<const uint8_t*>(q < 2 ? a.s_gate : a.s_up) + (row + 4 * (q & 1)) * 2;
-        else scale = static_cast<const uint8_t*>(r16 < 8 ? a.s_gate : a.s_up) + (row + (r16 & 7)) * 4 + q;
-      }
-      const int64_t plane = (int64_t)E * n * (Q::FMT == W4_INT ? 2 : 4);
       const int groups = (c + 15) / 16;
-      for (int g0 = 0; g0 < groups; g0 += Q::NG) {
-        const int ng = min(Q::NG, groups - g0);
-        const T* xr[Q::NG];
+      for (int g0 = 0; g0 < groups; g0 += DEC_NG) {
+        const int ng = min(DEC_NG, groups - g0);
+        const T* xr[DEC_NG];
 #pragma unroll
-        for (int g = 0; g < Q::NG; ++g) xr[g] = X + (int64_t)(lst[min((g0 + g) * 16 + r16, c - 1)] / K) * d;
-        auto stream = [&](int sa, int sb, f32x4* acc) {
-          if constexpr (Q::W4) dec_rows_w4<Q::FMT, Q::GROUP>(code, scale, plane, xr, ng, d, sa, sb, acc);
-          else dec_rows<T>(wrow, xr, ng, sa, sb, acc);
-        };
-        dec_group_run(G, L, ng, steps, stream, [&](const f32x4* v) {
+        for (int g = 0; g < DEC_NG; ++g) xr[g] = X + (int64_t)(lst[min((g0 + g) * 16 + r16, c - 1)] / K) * d;
+        dec_group_tile<T>(G, L, wrow, xr, ng, 0, d / S, [&](const f32x4* v) {
           for (int g = 0; g < ng; ++g) {
             f32x4 o;
 #pragma unroll
@@ -445,31 +345,20 @@ __global__ __launch_bounds__(DEC_THREADS) void k_decode(DecodeArgs a) {
     const T* Wd = reinterpret_cast<const T*>(a.W_down);
     const T* act = reinterpret_cast<const T*>(a.act);
     const int tiles = d / 16;
-    const int items = nact * tiles, steps = Q::W4 ? w4_blocks(n) : n / S;
-    G.setup(dec_pick_w(items, steps));
+    const int items = nact * tiles;
+    G.setup(dec_pick_w(items, n / S));
     for (int u = G.gid; u < items; u += G.ngroups) {
       const int e = L.active[u / tiles], col0 = (u % tiles) * 16;
       const int c = __builtin_amdgcn_readfirstlane(a.cnt[e]);
       const int32_t* lst = a.list + (int64_t)e * T_;
       const T* wrow = Wd + ((int64_t)e * d + col0 + r16) * n;
-      const uint8_t *code = nullptr, *scale = nullptr;
-      if constexpr (Q::W4) {
-        const int64_t row = (int64_t)e * d + col0;
-        code = static_cast<const uint8_t*>(a.W_down) + (row + r16) * (n / 2) + 16 * q;
-        scale = static_cast<const uint8_t*>(a.s_down) + (Q::FMT == W4_INT ? (row + 4 * q) * 2 : (row + r16) * 4 + q);
-      }
-      const int64_t plane = (int64_t)E * d * (Q::FMT == W4_INT ? 2 : 4);
       const int groups = (c + 15) / 16;
-      for (int g0 = 0; g0 < groups; g0 += Q::NG) {
-        const int ng = min(Q::NG, groups - g0);
-        const T* xr[Q::NG];
+      for (int g0 = 0; g0 < groups; g0 += DEC_NG) {
+        const int ng = min(DEC_NG, groups - g0);
+        const T* xr[DEC_NG];
 #pragma unroll
-        for (int g = 0; g < Q::NG; ++g) xr[g] = act + (int64_t)lst[min((g0 + g) * 16 + r16, c - 1)] * n;
-        auto stream = [&](int sa, int sb, f32x4* acc) {
-          if constexpr (Q::W4) dec_rows_w4<Q::FMT, Q::GROUP>(code, scale, plane, xr, ng, n, sa, sb, acc);
-          else dec_rows<T>(wrow, xr, ng, sa, sb, acc);
-        };
-        dec_group_run(G, L, ng, steps, stream, [&](const f32x4* v) {
+        for (int g = 0; g < DEC_NG; ++g) xr[g] = act + (int64_t)lst[min((g0 + g) * 16 + r16, c - 1)] * n;
+        dec_group_tile<T>(G, L, wrow, xr, ng, 0, n / S, [&](const f32x4* v) {
           for (int g = 0; g < ng; ++g) {
             const int slot = (g0 + g) * 16 + r16;
             if (slot < c) *reinterpret_cast<f32x4*>(a.y + (int64_t)lst[slot] * d + col0 + 4 * q) = v[g];
@@ -533,9 +422,9 @@ size_t decode_workspace_bytes(int64_t T, int64_t d, int64_t n, int E, int K) {
 }
 
 static long long g_dec_spin_limit = 1ll << 20;  // about a second of polling
-// Grid size per device and kernel (0 until the first call on that device computes it).
-constexpr int DEC_MAX_DEVICES = 64, DEC_KERNELS = 6;
-static std::atomic<int> g_dec_grid[DEC_MAX_DEVICES][DEC_KERNELS];
+// Grid size per device and dtype (0 until the first call on that device computes it).
+constexpr int DEC_MAX_DEVICES = 64;
+static std::atomic<int> g_dec_grid[DEC_MAX_DEVICES][2];
 
 long long decode_set_spin_limit(long long limit) {
   const long long prev = g_dec_spin_limit;
@@ -557,23 +446,11 @@ hipError_t decode_read_status(hipStream_t st, int* failed) {
   return e;
 }
 
-// The kernel of a weight format, and its place in g_dec_grid.
-static const void* dec_kernel(const Shape& s, const W4View* w, int* index) {
-  const int i = !w ? (s.bf16 ? 1 : 0) : w->format == W4_FP ? 2 : w->group == 32 ? 3 : w->group == 64 ? 4 : 5;
-  *index = i;
-  switch (i) {
-    case 0: return reinterpret_cast<const void*>(&k_decode<float, DecPlain>);
-    case 1: return reinterpret_cast<const void*>(&k_decode<bf16, DecPlain>);
-    case 2: return reinterpret_cast<const void*>(&k_decode<bf16, DecW4<W4_FP, 32>>);
-    case 3: return reinterpret_cast<const void*>(&k_decode<bf16, DecW4<W4_INT, 32>>);
-    case 4: return reinterpret_cast<const void*>(&k_decode<bf16, DecW4<W4_INT, 64>>);
-    default: return reinterpret_cast<const void*>(&k_decode<bf16, DecW4<W4_INT, 128>>);
-  }
-}
-
-static hipError_t dec_launch(const Shape& s, DecodeArgs a, const W4View* w4, const void* X, const void* W_r, const float* bias,
-                             float* logits, int32_t* topk_idx, float* topk_w, void* out, void* ws, hipStream_t st) {
-  a.X = X; a.W_r = W_r; a.bias = bias;
+hipError_t launch_decode(const Shape& s, const void* X, const void* W_r, const float* bias,
+                         const void* W_gate, const void* W_up, const void* W_down, float* logits,
+                         int32_t* topk_idx, float* topk_w, void* out, void* ws, hipStream_t st) {
+  DecodeArgs a;
+  a.X = X; a.W_r = W_r; a.bias = bias; a.W_gate = W_gate; a.W_up = W_up; a.W_down = W_down;
   a.logits = logits; a.topk_idx = topk_idx; a.topk_w = topk_w; a.out = out;
   char* w = static_cast<char*>(ws);
   a.bar = reinterpret_cast<unsigned long long*>(w);
@@ -587,15 +464,15 @@ static hipError_t dec_launch(const Shape& s, DecodeArgs a, const W4View* w4, con
   a.y = reinterpret_cast<float*>(w);
   a.T = (int)s.T; a.d = (int)s.d; a.n = (int)s.n; a.E = s.E; a.K = s.K;
   a.spin_limit = g_dec_spin_limit;
-  int index;
-  const void* fn = dec_kernel(s, w4, &index);
+  const void* fn = s.bf16 ? reinterpret_cast<const void*>(&k_decode<bf16>)
+                          : reinterpret_cast<const void*>(&k_decode<float>);
   int dev = 0;
   hipError_t e = hipGetDevice(&dev);
   if (e != hipSuccess) return e;
   // every workgroup must be resident at once for the grid barriers: the grid is the device's CU
-  // count times the kernel's occupancy, queried once per device and kernel
+  // count times the kernel's occupancy, queried once per device and dtype
   if (dev < 0 || dev >= DEC_MAX_DEVICES) return hipErrorInvalidDevice;
-  std::atomic<int>& cached = g_dec_grid[dev][index];
+  std::atomic<int>& cached = g_dec_grid[dev][s.bf16 ? 1 : 0];
   int grid = cached.load(std::memory_order_relaxed);
   if (grid == 0) {
     int cus = 0, per_cu = 0;
@@ -617,23 +494,6 @@ static hipError_t dec_launch(const Shape& s, DecodeArgs a, const W4View* w4, con
   // a third of a small decode step.
   void* params[] = {&a};
   return hipLaunchKernel(fn, dim3(grid), dim3(DEC_THREADS), params, 0u, st);
-}
-
-hipError_t launch_decode(const Shape& s, const void* X, const void* W_r, const float* bias,
-                         const void* W_gate, const void* W_up, const void* W_down, float* logits,
-                         int32_t* topk_idx, float* topk_w, void* out, void* ws, hipStream_t st) {
-  DecodeArgs a{};
-  a.W_gate = W_gate; a.W_up = W_up; a.W_down = W_down;
-  return dec_launch(s, a, nullptr, X, W_r, bias, logits, topk_idx, topk_w, out, ws, st);
-}
-
-hipError_t launch_decode_w4(const Shape& s, const void* X, const void* W_r, const float* bias, const W4View& W_gate,
-                            const W4View& W_up, const W4View& W_down, float* logits, int32_t* topk_idx, float* topk_w, void* out,
-                            void* ws, hipStream_t st) {
-  DecodeArgs a{};
-  a.W_gate = W_gate.codes; a.W_up = W_up.codes; a.W_down = W_down.codes;
-  a.s_gate = W_gate.scales; a.s_up = W_up.scales; a.s_down = W_down.scales;
-  return dec_launch(s, a, &W_gate, X, W_r, bias, logits, topk_idx, topk_w, out, ws, st);
 }
 
 }  // namespace moe

@@ -1,0 +1,376 @@
+// The MoE layer for a few tokens with 4-bit expert weights (w4.h): router logits, top-K with softmax, the
+// chosen experts' SwiGLU FFNs, the weighted combine.
+//
+// A few short launches on the caller's stream, not one with grid-wide barriers: a launch that waits for
+// the one before costs about 2 us, a barrier of the whole chip and the phases' uneven ends cost more.
+//
+// By pairs (few tokens for the experts, so that hardly two choose the same one): three launches.
+//   1. router logits;
+//   2. gate/up: a workgroup takes 8 columns of one (token, choice) pair.  Its first wave finds the pair's
+//      expert from the token's logits while the others copy the token to LDS, so that top-K needs no launch;
+//      one workgroup of a token writes its choices and weights;
+//   3. down: a workgroup takes 16 output columns of a token, its waves the token's experts; their results are
+//      added in ascending expert order with their weights, in LDS.
+// By experts (more tokens): five launches.  1. router logits, which also clear the experts' counters; 2. top-K,
+// each pair appended to its expert's list (the order inside a list reaches no value); 3. gate/up and
+// 4. down on groups of 16 of an expert's tokens; 5. combine in ascending expert order.
+#include "internal.h"
+#include "skinny.h"
+#include "topk_wave.h"
+#include "w4.h"
+
+namespace moe {
+
+struct DecW4 {
+  const bf16 *X, *W_r;
+  const float* bias;
+  const uint8_t *gate, *up, *down;
+  const uint8_t *s_gate, *s_up, *s_down;
+  float* logits;
+  int32_t* topk_idx;
+  float* topk_w;
+  bf16* out;
+  int32_t* cnt;   // [E]
+  int32_t* list;  // [E][T] pair ids t * K + k
+  bf16* act;      // [T * K][n]
+  float* y;       // [T * K][d]
+  int T, d, n, E, K;
+};
+
+// ---- 1. router logits: a workgroup takes 16 experts and up to 48 tokens, its waves share d ----
+constexpr int DW_LOGIT_WAVES = 16, DW_NG = 3;
+
+template <int NG>
+__device__ __forceinline__ void dw_logit_rows(const bf16* wrow, const bf16* const* xrow, int a, int b, f32x4* acc) {
+  const int ko = ((threadIdx.x & 63) >> 4) * DecMma<bf16>::V;
+  DecStream<bf16, NG> ds;
+  ds.w = wrow + ko;
+#pragma unroll
+  for (int g = 0; g < NG; ++g) ds.x[g] = xrow[g] + ko;
+  dec_stream<bf16, NG>(ds, a, b, acc);
+}
+
+__global__ __launch_bounds__(DW_LOGIT_WAVES * 64) void k_dw4_logits(DecW4 a, bool lists) {
+  __shared__ f32x4 part[DW_LOGIT_WAVES][DW_NG][64];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), r16 = lane & 15, q = lane >> 4;
+  if (lists && blockIdx.x == 0 && blockIdx.y == 0 && (int)threadIdx.x < a.E) a.cnt[threadIdx.x] = 0;  // (E <= 1024)
+  const int e0 = blockIdx.x * 16, g0 = blockIdx.y * DW_NG;
+  const int ng = min(DW_NG, (a.T + 15) / 16 - g0);
+  const bf16* wrow = a.W_r + (int64_t)min(e0 + r16, a.E - 1) * a.d;
+  const bf16* xrow[DW_NG];
+#pragma unroll
+  for (int g = 0; g < DW_NG; ++g) xrow[g] = a.X + (int64_t)min((g0 + g) * 16 + r16, a.T - 1) * a.d;
+  f32x4 acc[DW_NG];
+#pragma unroll
+  for (int g = 0; g < DW_NG; ++g) acc[g] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+  const int ns = a.d / DecMma<bf16>::S, s0 = ns * wave / DW_LOGIT_WAVES, s1 = ns * (wave + 1) / DW_LOGIT_WAVES;
+  if (ng == 3) dw_logit_rows<3>(wrow, xrow, s0, s1, acc);
+  else if (ng == 2) dw_logit_rows<2>(wrow, xrow, s0, s1, acc);
+  else dw_logit_rows<1>(wrow, xrow, s0, s1, acc);
+#pragma unroll
+  for (int g = 0; g < DW_NG; ++g) part[wave][g][lane] = acc[g];
+  __syncthreads();
+  if (wave < ng) {
+    f32x4 v = part[0][wave][lane];
+    for (int w = 1; w < DW_LOGIT_WAVES; ++w) v += part[w][wave][lane];
+    const int t = (g0 + wave) * 16 + r16;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int e = e0 + 4 * q + i;
+      if (t < a.T && e < a.E) a.logits[(int64_t)t * a.E + e] = v[i] + (a.bias ? a.bias[e] : 0.0f);
+    }
+  }
+}
+
+// A token's choices and weights by one wave; lane k returns the k-th expert.
+__device__ __forceinline__ int dw_choose(const DecW4& a, int t) {
+  const int lane = threadIdx.x & 63;
+  int e;
+  float v;
+  wave_select(a.logits + (int64_t)t * a.E, a.E, a.K, e, v);
+  const float ex = lane < a.K ? __expf(v - __shfl(v, 0, WAVE)) : 0.0f;
+  const float sum = wave_sum(ex);
+  if (lane < a.K) {
+    a.topk_idx[(int64_t)t * a.K + lane] = e;
+    a.topk_w[(int64_t)t * a.K + lane] = ex / sum;
+  }
+  return e;
+}
+
+// The ranks of a token's choices by expert id: order[r] is the choice of the r-th smallest expert.
+__device__ __forceinline__ void dw_order(const int32_t* idx, int K, int (&order)[16]) {
+  int ids[16];
+#pragma unroll
+  for (int k = 0; k < 16; ++k) ids[k] = k < K ? __builtin_amdgcn_readfirstlane(idx[k]) : 0x7fffffff;
+  int prev = -1;
+#pragma unroll
+  for (int r = 0; r < 16; ++r) {
+    int best = 0x7fffffff, b = 0;
+#pragma unroll
+    for (int k = 0; k < 16; ++k)
+      if (ids[k] > prev && ids[k] < best) {
+        best = ids[k];
+        b = k;
+      }
+    order[r] = b;
+    prev = best;
+  }
+}
+
+// ---- by pairs ----
+// gate/up of a pair: 8 gate rows and their up rows in one tile
+template <int FMT, int G, bool XLDS>
+__global__ __launch_bounds__(512) void k_dw4_up_pair(DecW4 a) {
+  extern __shared__ __attribute__((aligned(16))) char dw_lds[];
+  __shared__ int chosen;
+  typedef W4Stream<FMT, G, 1, 1, 1, XLDS, FMT == W4_INT && G < 128 ? 1 : 2> Stream;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), W_ = blockDim.x >> 6;
+  const int lane = threadIdx.x & 63, r16 = lane & 15, q = lane >> 4;
+  const int pair = blockIdx.y, t = pair / a.K, k = pair - t * a.K, j0 = blockIdx.x * 8;
+  const bf16* x = a.X + (int64_t)t * a.d;
+  bf16* xl = reinterpret_cast<bf16*>(dw_lds);
+  const int nb = w4_blocks(a.d), b0 = nb * wave / W_, b1 = nb * (wave + 1) / W_;
+  if constexpr (XLDS) w4_stage<FMT>(x, xl, b0 * W4_BLOCK, min(b1 * W4_BLOCK, a.d));
+  if (wave == 0) {
+    int e;
+    float v;
+    if (blockIdx.x == 0 && k == 0) e = dw_choose(a, t);
+    else wave_select(a.logits + (int64_t)t * a.E, a.E, k + 1, e, v);
+    if (lane == k) chosen = e;
+  }
+  __syncthreads();
+  const int e = __builtin_amdgcn_readfirstlane(chosen);
+  const int64_t row = (int64_t)e * a.n + j0 + (r16 & 7);
+  Stream ws;
+  ws.w[0] = (r16 < 8 ? a.gate : a.up) + row * (a.d / 2) + 16 * q;
+  ws.s[0] = (r16 < 8 ? a.s_gate : a.s_up) + (FMT == W4_INT ? row * 2 : row * 4 + q);
+  ws.plane = (int64_t)a.E * a.n * (FMT == W4_INT ? 2 : 4);
+  ws.x[0] = (XLDS ? xl : x) + Stream::XQ * q;
+  ws.K = a.d;
+  f32x4 acc[1][1] = {{{0.0f, 0.0f, 0.0f, 0.0f}}};
+  if (b0 < b1) ws.run(b0, b1, acc);
+  __syncthreads();
+  float* res = reinterpret_cast<float*>(dw_lds);  // [wave][16]
+  if (q == 0) res[wave * 16 + r16] = acc[0][0][0];
+  __syncthreads();
+  if (threadIdx.x < 8) {
+    float g = 0.0f, u = 0.0f;
+    for (int w = 0; w < W_; ++w) {
+      g += res[w * 16 + threadIdx.x];
+      u += res[w * 16 + 8 + threadIdx.x];
+    }
+    a.act[(int64_t)pair * a.n + j0 + threadIdx.x] = from_f32<bf16>(g * sigmoid_f32(g) * u);
+  }
+}
+
+// down and combine of a token: 16 output columns, `splits` waves per choice
+template <int FMT, int G, bool XLDS>
+__global__ __launch_bounds__(1024) void k_dw4_down_pair(DecW4 a, int splits) {
+  extern __shared__ __attribute__((aligned(16))) char dw_lds[];
+  typedef W4Stream<FMT, G, 1, 1, 1, XLDS, FMT == W4_INT && G < 128 ? 1 : 2> Stream;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int lane = threadIdx.x & 63, r16 = lane & 15, q = lane >> 4;
+  const int t = blockIdx.y, c0 = blockIdx.x * 16, k = wave / splits, part = wave - k * splits;
+  const bf16* x = a.act + ((int64_t)t * a.K + k) * a.n;
+  bf16* xl = reinterpret_cast<bf16*>(dw_lds) + (int64_t)k * a.n;
+  const int nb = w4_blocks(a.n), b0 = nb * part / splits, b1 = nb * (part + 1) / splits;
+  if constexpr (XLDS) w4_stage<FMT>(x, xl, b0 * W4_BLOCK, min(b1 * W4_BLOCK, a.n));
+  const int32_t* idx = a.topk_idx + (int64_t)t * a.K;
+  const int64_t row = (int64_t)__builtin_amdgcn_readfirstlane(idx[k]) * a.d + c0 + r16;
+  Stream ws;
+  ws.w[0] = a.down + row * (a.n / 2) + 16 * q;
+  ws.s[0] = a.s_down + (FMT == W4_INT ? row * 2 : row * 4 + q);
+  ws.plane = (int64_t)a.E * a.d * (FMT == W4_INT ? 2 : 4);
+  ws.x[0] = (XLDS ? xl : x) + Stream::XQ * q;
+  ws.K = a.n;
+  f32x4 acc[1][1] = {{{0.0f, 0.0f, 0.0f, 0.0f}}};
+  if (b0 < b1) ws.run(b0, b1, acc);
+  __syncthreads();
+  float* res = reinterpret_cast<float*>(dw_lds);  // [wave][16]
+  if (q == 0) res[wave * 16 + r16] = acc[0][0][0];
+  __syncthreads();
+  if (threadIdx.x < 16) {
+    int order[16];
+    dw_order(idx, a.K, order);
+    float o = 0.0f;
+#pragma unroll
+    for (int r = 0; r < 16; ++r)
+      if (r < a.K) {
+        float y = 0.0f;
+        for (int s = 0; s < splits; ++s) y += res[(order[r] * splits + s) * 16 + threadIdx.x];
+        o = fmaf(a.topk_w[(int64_t)t * a.K + order[r]], y, o);
+      }
+    a.out[(int64_t)t * a.d + c0 + threadIdx.x] = from_f32<bf16>(o);
+  }
+}
+
+// ---- by experts ----
+__global__ __launch_bounds__(256) void k_dw4_topk(DecW4 a) {
+  const int t = blockIdx.x * 4 + (threadIdx.x >> 6), lane = threadIdx.x & 63;
+  if (t >= a.T) return;
+  const int e = dw_choose(a, t);
+  if (lane < a.K) a.list[(int64_t)e * a.T + atomicAdd(&a.cnt[e], 1)] = t * a.K + lane;  // (a token picks an expert at most once)
+}
+
+// A tile of an expert against groups of 16 of its tokens, the waves sharing the reduction.  UP: 16 gate rows
+// and their up rows -> act; else 32 rows of W_down -> y.
+template <int FMT, int G, bool UP>
+__global__ __launch_bounds__(512) void k_dw4_expert(DecW4 a) {
+  extern __shared__ __attribute__((aligned(16))) char dw_lds[];
+  constexpr int RT = 2, TILE = 256;
+  typedef W4Stream<FMT, G, 1, RT, 4, false, 1> Stream;
+  const int e = blockIdx.y, c = __builtin_amdgcn_readfirstlane(a.cnt[e]);
+  if (c == 0) return;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), W_ = blockDim.x >> 6;
+  const int lane = threadIdx.x & 63, r16 = lane & 15, q = lane >> 4;
+  const int rows = UP ? a.n : a.d, K = UP ? a.d : a.n;  // of an expert
+  const int c0 = blockIdx.x * (UP ? 16 : 32);
+  const int32_t* lst = a.list + (int64_t)e * a.T;
+  Stream ws;
+#pragma unroll
+  for (int r = 0; r < RT; ++r) {
+    const int64_t row = (int64_t)e * rows + c0 + r16 + (UP ? 0 : 16 * r);  // (n and d are multiples of 64)
+    const uint8_t* w = UP ? (r == 0 ? a.gate : a.up) : a.down;
+    const uint8_t* s = UP ? (r == 0 ? a.s_gate : a.s_up) : a.s_down;
+    ws.w[r] = w + row * (K / 2) + 16 * q;
+    ws.s[r] = s + (FMT == W4_INT ? row * 2 : row * 4 + q);
+  }
+  ws.plane = (int64_t)a.E * rows * (FMT == W4_INT ? 2 : 4);
+  ws.K = K;
+  const int nb = w4_blocks(K), b0 = nb * wave / W_, b1 = nb * (wave + 1) / W_;
+  float* res = reinterpret_cast<float*>(dw_lds);  // [wave][RT][token][16]
+  for (int g0 = 0; g0 < c; g0 += 16) {
+    const int pair = lst[min(g0 + r16, c - 1)];
+    ws.x[0] = (UP ? a.X + (int64_t)(pair / a.K) * a.d : a.act + (int64_t)pair * a.n) + Stream::XQ * q;
+    f32x4 acc[RT][1] = {{{0.0f, 0.0f, 0.0f, 0.0f}}, {{0.0f, 0.0f, 0.0f, 0.0f}}};
+    if (b0 < b1) ws.run(b0, b1, acc);
+    __syncthreads();  // (the last group's results have been read)
+#pragma unroll
+    for (int r = 0; r < RT; ++r) w4_put<4>(res + (wave * RT + r) * TILE, acc[r][0]);
+    __syncthreads();
+    auto total = [&](int r, int at) {
+      const float* p = res + r * TILE + at;
+      f32x4 v = *reinterpret_cast<const f32x4*>(p);
+      for (int w = 1; w < W_; ++w) v += *reinterpret_cast<const f32x4*>(p + w * RT * TILE);
+      return v;
+    };
+    constexpr int QUADS = UP ? 4 : 8;
+    for (int it = threadIdx.x; it < 16 * QUADS; it += blockDim.x) {
+      const int quad = it % QUADS, tok = it / QUADS, col = c0 + 4 * quad;
+      if (g0 + tok >= c) continue;
+      const int64_t to = lst[g0 + tok];
+      if constexpr (UP) {
+        const f32x4 g = total(0, tok * 16 + 4 * quad), u = total(1, tok * 16 + 4 * quad);
+        f32x4 h;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) h[i] = g[i] * sigmoid_f32(g[i]) * u[i];
+        dec_store4<bf16>(a.act + to * a.n + col, h);
+      } else {
+        *reinterpret_cast<f32x4*>(a.y + to * a.d + col) = total(quad >> 2, tok * 16 + 4 * (quad & 3));
+      }
+    }
+  }
+}
+
+__global__ __launch_bounds__(256) void k_dw4_combine(DecW4 a) {
+  const int t = blockIdx.y, c = (blockIdx.x * 256 + threadIdx.x) * 4;
+  int order[16];
+  dw_order(a.topk_idx + (int64_t)t * a.K, a.K, order);
+  if (c >= a.d) return;
+  f32x4 yv[16];
+  float wv[16];
+#pragma unroll
+  for (int r = 0; r < 16; ++r)
+    if (r < a.K) {
+      const int64_t p = (int64_t)t * a.K + order[r];
+      wv[r] = a.topk_w[p];
+      yv[r] = *reinterpret_cast<const f32x4*>(a.y + p * a.d + c);
+    }
+  f32x4 s = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+  for (int r = 0; r < 16; ++r)
+    if (r < a.K) s += wv[r] * yv[r];
+  dec_store4<bf16>(a.out + (int64_t)t * a.d + c, s);
+}
+
+constexpr int64_t DW_LDS = 65536;
+
+template <int FMT, int G>
+static hipError_t dw4_run(const DecW4& a, hipStream_t st) {
+  const bool pairs = a.T * a.K * 2 <= a.E || a.T == 1;
+  const dim3 lg((unsigned)cdiv(a.E, 16), (unsigned)cdiv(a.T, 16 * DW_NG));
+  k_dw4_logits<<<lg, DW_LOGIT_WAVES * 64, 0, st>>>(a, !pairs);
+  hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  if (pairs) {
+    const int nb = w4_blocks(a.d);
+    int waves = 4;
+    while (waves > 1 && nb / waves < 4) waves /= 2;
+    const dim3 ug((unsigned)(a.n / 8), (unsigned)(a.T * a.K));
+    const int64_t xl = (int64_t)a.d * 2;
+    if (xl <= DW_LDS) k_dw4_up_pair<FMT, G, true><<<ug, waves * 64, xl < 1024 ? 1024 : xl, st>>>(a);
+    else k_dw4_up_pair<FMT, G, false><<<ug, waves * 64, 1024, st>>>(a);
+    e = hipGetLastError();
+    if (e != hipSuccess) return e;
+    const int nd = w4_blocks(a.n);
+    int splits = 1;
+    while (a.K * splits * 2 <= 16 && nd / (splits * 2) >= 4) splits *= 2;
+    const dim3 dg((unsigned)(a.d / 16), (unsigned)a.T);
+    const int64_t al = (int64_t)a.K * a.n * 2;
+    if (al <= DW_LDS) k_dw4_down_pair<FMT, G, true><<<dg, a.K * splits * 64, al < 1024 ? 1024 : al, st>>>(a, splits);
+    else k_dw4_down_pair<FMT, G, false><<<dg, a.K * splits * 64, 1024, st>>>(a, splits);
+    return hipGetLastError();
+  }
+  k_dw4_topk<<<(unsigned)cdiv(a.T, 4), 256, 0, st>>>(a);
+  e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  auto waves_of = [](int K) {
+    int w = 8;
+    while (w > 1 && w4_blocks(K) / w < 2) w /= 2;
+    return w;
+  };
+  const int wu = waves_of(a.d), wd = waves_of(a.n);
+  k_dw4_expert<FMT, G, true><<<dim3((unsigned)(a.n / 16), (unsigned)a.E), wu * 64, wu * 2048, st>>>(a);
+  e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  k_dw4_expert<FMT, G, false><<<dim3((unsigned)(a.d / 32), (unsigned)a.E), wd * 64, wd * 2048, st>>>(a);
+  e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  k_dw4_combine<<<dim3((unsigned)cdiv(a.d, 1024), (unsigned)a.T), 256, 0, st>>>(a);
+  return hipGetLastError();
+}
+
+static size_t dw_align(size_t b) { return (b + 255) / 256 * 256; }
+hipError_t launch_decode_w4(const Shape& s, const void* X, const void* W_r, const float* bias, const W4View& W_gate,
+                            const W4View& W_up, const W4View& W_down, float* logits, int32_t* topk_idx, float* topk_w, void* out,
+                            void* ws, hipStream_t st) {
+  DecW4 a;
+  a.X = static_cast<const bf16*>(X);
+  a.W_r = static_cast<const bf16*>(W_r);
+  a.bias = bias;
+  a.gate = W_gate.codes;
+  a.up = W_up.codes;
+  a.down = W_down.codes;
+  a.s_gate = static_cast<const uint8_t*>(W_gate.scales);
+  a.s_up = static_cast<const uint8_t*>(W_up.scales);
+  a.s_down = static_cast<const uint8_t*>(W_down.scales);
+  a.logits = logits;
+  a.topk_idx = topk_idx;
+  a.topk_w = topk_w;
+  a.out = static_cast<bf16*>(out);
+  char* w = static_cast<char*>(ws);  // (moe_decode's workspace holds more)
+  a.cnt = reinterpret_cast<int32_t*>(w);
+  w += dw_align((size_t)s.E * 4);
+  a.list = reinterpret_cast<int32_t*>(w);
+  w += dw_align((size_t)s.E * s.T * 4);
+  a.act = reinterpret_cast<bf16*>(w);
+  w += dw_align((size_t)s.T * s.K * s.n * 2);
+  a.y = reinterpret_cast<float*>(w);
+  a.T = (int)s.T; a.d = (int)s.d; a.n = (int)s.n; a.E = s.E; a.K = s.K;
+  if (W_gate.format == W4_FP) return dw4_run<W4_FP, 32>(a, st);
+  if (W_gate.group == 32) return dw4_run<W4_INT, 32>(a, st);
+  if (W_gate.group == 64) return dw4_run<W4_INT, 64>(a, st);
+  return dw4_run<W4_INT, 128>(a, st);
+}
+
+}  // namespace moe

@@ -141,44 +141,8 @@ __device__ __forceinline__ void lin_epi4(const LinEpi<T>& ep, int64_t r, int c, 
   lin_st4(ep.out + r * ep.ldo + c, o);
 }
 
-// The end of a streaming kernel of a few rows: the waves' partial tiles acc [RT][NG] meet in LDS
-// (sk_part [wave][RT][NG][64]), are added in wave order, and the epilogue runs.  16 RT rows of W from c0
-// on (SwiGLU: 8 RT gate rows with their up rows, 32 lanes apart for RT = 1, the other tile for RT = 2)
-// against the rows t0 .. t0 + 16 NG - 1 of m.
-template <typename T, int NG, int RT, bool GLU>
-__device__ __forceinline__ void lin_skinny_join(const f32x4 (&acc)[RT][NG], f32x4* sk_part, const LinEpi<T>& ep, int t0, int m,
-                                                int n, int c0) {
-  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), W_ = blockDim.x >> 6;
-  const int r16 = lane & 15, q = lane >> 4;
-#pragma unroll
-  for (int r = 0; r < RT; ++r)
-#pragma unroll
-    for (int g = 0; g < NG; ++g) sk_part[((wave * RT + r) * NG + g) * 64 + lane] = acc[r][g];
-  __syncthreads();
-  auto total = [&](int r, int g) {
-    f32x4 v = sk_part[(r * NG + g) * 64 + lane];
-    for (int w = 1; w < W_; ++w) v += sk_part[((w * RT + r) * NG + g) * 64 + lane];
-    return v;
-  };
-  constexpr int ITEMS = (GLU ? 1 : RT) * NG;  // 16 x 16 (SwiGLU: 8 RT x 16) output blocks
-  for (int it = wave; it < ITEMS; it += W_) {
-    const int g = it % NG, r = it / NG, t = t0 + g * 16 + r16;
-    if constexpr (GLU) {
-      f32x4 z = total(0, g), up;
-      if constexpr (RT == 1) {
-#pragma unroll
-        for (int u = 0; u < 4; ++u) up[u] = __shfl_xor(z[u], 32, 64);
-      } else {
-        up = total(1, g);
-      }
-      const int c = c0 + 4 * q;
-      if ((RT == 2 || q < 2) && t < m && c < n) lin_epi4(ep, (int64_t)t, c, n, true, z, up);
-    } else {
-      const int c = c0 + 16 * r + 4 * q;
-      const f32x4 z = total(r, g);
-      if (t < m && c < n) lin_epi4(ep, (int64_t)t, c, n, false, z, z);
-    }
-  }
-}
+// Adds SK partial products [SK][m][np] in slice order and applies the epilogue (linear.hip); np: n, or 2 n for
+// SwiGLU.
+hipError_t launch_lin_finish(const float* part, int SK, int m, int n, int np, const LinEpi<bf16>& ep, hipStream_t st);
 
 }  // namespace moe

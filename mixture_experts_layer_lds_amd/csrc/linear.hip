@@ -421,7 +421,35 @@ __global__ __launch_bounds__(512) void k_lin_skinny(const T* __restrict__ X, int
       for (int r = 0; r < RT; ++r) acc[r][g] = DecMma<T>::mma(in ? ld16(ds.w[r] + ns * S) : zero, xv, acc[r][g]);
     }
   }
-  lin_skinny_join<T, NG, RT, GLU>(acc, sk_part, ep, 0, m, n, c0);
+#pragma unroll
+  for (int r = 0; r < RT; ++r)
+#pragma unroll
+    for (int g = 0; g < NG; ++g) sk_part[((wave * RT + r) * NG + g) * 64 + lane] = acc[r][g];
+  __syncthreads();
+  auto total = [&](int r, int g) {
+    f32x4 v = sk_part[(r * NG + g) * 64 + lane];
+    for (int w = 1; w < W_; ++w) v += sk_part[((w * RT + r) * NG + g) * 64 + lane];
+    return v;
+  };
+  constexpr int ITEMS = (GLU ? 1 : RT) * NG;  // 16 x 16 (SwiGLU: 8 RT x 16) output blocks
+  for (int it = wave; it < ITEMS; it += W_) {
+    const int g = it % NG, r = it / NG, t = g * 16 + r16;
+    if constexpr (GLU) {
+      f32x4 z = total(0, g), up;
+      if constexpr (RT == 1) {
+#pragma unroll
+        for (int u = 0; u < 4; ++u) up[u] = __shfl_xor(z[u], 32, 64);
+      } else {
+        up = total(1, g);
+      }
+      const int c = c0 + 4 * q;
+      if ((RT == 2 || q < 2) && t < m && c < n) lin_epi4(ep, (int64_t)t, c, n, true, z, up);
+    } else {
+      const int c = c0 + 16 * r + 4 * q;
+      const f32x4 z = total(r, g);
+      if (t < m && c < n) lin_epi4(ep, (int64_t)t, c, n, false, z, z);
+    }
+  }
 }
 
 // dZ = dY act'(z) (SwiGLU: [dG | dU]) and the bias gradient's partial sums: a workgroup takes 256
@@ -707,6 +735,11 @@ static void lin_launch(const LinGemm& g, const LinEpi<T>& ep, hipStream_t st) {
   if (g.tile == LIN_SMALL) lin_launch_t<T, LinSmall, MODE, OUT>(g, ep, st);
   else if (g.tile == LIN_MID) lin_launch_t<T, LinMid, MODE, OUT>(g, ep, st);
   else if constexpr (sizeof(T) == 2 && OUT != LIN_OUT_PART) lin_launch_t<T, LinBig, MODE, OUT>(g, ep, st);  // never sliced
+}
+
+hipError_t launch_lin_finish(const float* part, int SK, int m, int n, int np, const LinEpi<bf16>& ep, hipStream_t st) {
+  k_lin_finish<bf16><<<(int)cdiv((int64_t)m * (n / 4), 256), 256, 0, st>>>(part, SK, m, n, np, ep);
+  return hipGetLastError();
 }
 
 // A product whose epilogue is ep: directly, or through partial products where it is sliced.

@@ -1,20 +1,23 @@
-// 4-bit weights with group scales as the A operand of 16 x 16 x 32 MFMAs: shared by the dense projection
-// of a few rows (w4.hip) and the single-launch decode kernel (decode.hip).
+// 4-bit weights with group scales as the B operand of 16 x 16 x 32 MFMAs, the tokens being A: shared by the
+// dense projection of a few rows (w4.hip) and the decode of the routed experts (decode_w4.hip).
 //
 // A row of K codes lies in K / 2 bytes, the even element in the low half.  A lane loads 16 bytes, 32
 // codes, of its weight row at a time; the four lanes of a row cover a block of 128.
 //
-// FP (E2M1 values times 2^(e - 127), one scale byte per 32): lane q's codes are scale group q of the
+// FP (E2M1 values times 2^(e - 127), one scale byte per 32): lane group q's codes are scale group q of the
 // block, and one conversion instruction makes two codes with their scale into two bf16 values, exactly.
 // Step j of the block takes the lane's codes 8 j .. 8 j + 7, against the same elements of the tokens.
 //
-// INT (value (c - 8) s, s bf16 per group of G = 32, 64 or 128): four lane swaps transpose the block, so
-// that step j holds elements 32 j .. 32 j + 31 of the row in the MFMA's own order and a group is G / 32
-// whole steps.  A code is put into the mantissa of 1.0 (1 + c / 16, one shift and one and-or for two codes)
-// and the excess of 1.5 is taken off by a second product of the tokens with -1.5, which is exact in
-// bf16: both sums are exact products accumulated in fp32, and the group's scale multiplies their sum in
-// fp32.  So no weight is rounded.  Two codes that share a register are four apart; the tokens'
-// elements are put into the same order (0 4 1 5 2 6 3 7) by four byte permutations.
+// INT (value (c - 8) s, s bf16 per group of G = 32, 64 or 128): a group has to be whole steps, since its
+// scale multiplies their sum.  With G = 128 the block is one group and steps are as above; with less, four
+// lane swaps transpose the block so that step j holds elements 32 j .. 32 j + 31.  A code is put into the
+// mantissa of 1.0 (1 + c / 16: one shift and one and-or for two codes) and the excess of 1.5 is taken off by
+// a product of the tokens with -1.5, from which the group's sum starts: all products are exact, sums fp32,
+// and the weights are never rounded.  Two codes that share a register are four apart; the tokens' elements
+// are put into the same order, 0 4 1 5 2 6 3 7, by four byte permutations.
+//
+// With the weights as B a lane's results all belong to one weight row, so a group costs one scale conversion
+// and NI multiply-adds a lane: 4 for up to 16 tokens, 1 for up to 4, which then lie in every fourth row of A.
 #pragma once
 
 #include "common.h"
@@ -25,12 +28,11 @@ enum { W4_INT = 0, W4_FP = 1 };
 
 constexpr int W4_BLOCK = 128;  // elements of a row per block
 
-// Whole blocks and the part of a last one (a multiple of 32 elements).
 __host__ __device__ __forceinline__ int w4_blocks(int K) { return (K + W4_BLOCK - 1) / W4_BLOCK; }
 
-__device__ __forceinline__ bf16x8 w4_bf16x8(u32x4 v) { return __builtin_bit_cast(bf16x8, v); }
+// a: tokens, b: weights
 __device__ __forceinline__ f32x4 w4_mfma(u32x4 a, u32x4 b, f32x4 c) {
-  return __builtin_amdgcn_mfma_f32_16x16x32_bf16(w4_bf16x8(a), w4_bf16x8(b), c, 0, 0, 0);
+  return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
 }
 
 // Word j of lane group i becomes word i of lane group j (lane groups: lane / 16).
@@ -58,24 +60,32 @@ __device__ __forceinline__ u32x4 w4_unpack_fp(uint32_t w, float s) {
                __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, s, 3))};
 }
 
-// One wave's stream over blocks of RT tiles of 16 weight rows against NG groups of 16 tokens.
-template <int FMT, int G, int NG, int RT, int U>  // U: blocks per batch of loads
+// One wave's stream over blocks of RT tiles of 16 weight rows against NG groups of tokens.
+// XLDS: the tokens lie in LDS (w4_stage), in the order that the steps take them; else in memory.
+// U: blocks per batch of loads.
+template <int FMT, int G, int NG, int RT, int NI, bool XLDS, int U>
 struct W4Stream {
   static constexpr bool INT = FMT == W4_INT;
-  static constexpr int GS = INT ? G / 32 : 1;                  // steps per group
-  static constexpr int NS = INT ? W4_BLOCK / G : 1;            // scale words per block and tile
-  static constexpr int XS = INT ? 32 : 8;                      // elements between a lane's steps in x
+  static constexpr bool TR = INT && G < W4_BLOCK;     // blocks are transposed
+  static constexpr int GS = INT ? G / 32 : 1;         // steps per group
+  static constexpr int NS = INT ? W4_BLOCK / G : 1;   // scales per block and lane
+  static constexpr int XQ = TR ? 8 : 32, XS = TR ? 32 : 8;  // a lane's elements of step j: block + XQ (lane / 16) + XS j
 
-  const uint8_t* w[RT];  // lane's weight row, at byte 16 (lane / 16)
-  const uint8_t* s[RT];  // INT: scales of rows 4 (lane / 16) .. + 3 of the tile; FP: scale byte (lane / 16) of the lane's row
+  const uint8_t* w[RT];  // lane's weight row (lane % 16 of the tile), at byte 16 (lane / 16)
+  const uint8_t* s[RT];  // INT: its scales' first bytes; FP: its scale byte of group lane / 16
   int64_t plane;         // bytes between scale planes (INT: per group; FP: per block)
-  const bf16* x[NG];     // lane's token, at element 8 (lane / 16) (INT) or 32 (lane / 16) (FP)
+  const bf16* x[NG];     // lane's token, at element XQ (lane / 16); XLDS: in LDS
   int K;
 
   struct Codes {
     u32x4 c[RT];
-    u32x2 s[RT][NS];  // INT: four bf16; FP: one byte
+    uint32_t s[RT][NS];
   };
+  struct Batch {
+    Codes c[U];
+    u32x4 x[XLDS ? 1 : U][NG][4];
+  };
+
   // the codes and scales of a block's first `left` elements (a multiple of 32)
   __device__ __forceinline__ void load_codes(Codes& b, int blk, int left = W4_BLOCK) const {
     const int q = (threadIdx.x & 63) >> 4;
@@ -87,9 +97,10 @@ struct W4Stream {
       if constexpr (INT) {
 #pragma unroll
         for (int g = 0; g < NS; ++g)
-          if (left == W4_BLOCK || g * G < left) b.s[r][g] = *reinterpret_cast<const u32x2*>(s[r] + ((int64_t)blk * NS + g) * plane);
+          if (left == W4_BLOCK || g * G < left)
+            b.s[r][g] = *reinterpret_cast<const uint16_t*>(s[r] + ((int64_t)blk * NS + g) * plane);
       } else {
-        b.s[r][0][0] = in ? s[r][blk * plane] : 127;
+        b.s[r][0] = in ? s[r][blk * plane] : 127;
       }
     }
   }
@@ -104,35 +115,39 @@ struct W4Stream {
     if constexpr (INT) {
       constexpr uint32_t NEG = 0xbfc0bfc0u;  // -1.5, twice
       const u32x4 neg = {NEG, NEG, NEG, NEG};
-      const f32x4 zero = {0.0f, 0.0f, 0.0f, 0.0f};
+      if constexpr (TR) {
 #pragma unroll
-      for (int r = 0; r < RT; ++r) w4_transpose(b.c[r]);
-      f32x4 corr[NG], part[RT][NG];
+        for (int r = 0; r < RT; ++r) w4_transpose(b.c[r]);
+      }
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        if (j >= steps) break;
-        const bool first = j % GS == 0;
-        u32x4 a[RT];
-#pragma unroll
-        for (int r = 0; r < RT; ++r) a[r] = w4_unpack_int(b.c[r][j]);
+      for (int h = 0; h < NS; ++h) {
+        if (h * GS >= steps) break;
+        u32x4 xo[NG][GS];
+        f32x4 part[RT][NG];
 #pragma unroll
         for (int g = 0; g < NG; ++g) {
-          const u32x4 xo = w4_order_int(xv[g][j]);
-          corr[g] = w4_mfma(neg, xo, first ? zero : corr[g]);
+          f32x4 corr = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-          for (int r = 0; r < RT; ++r) part[r][g] = w4_mfma(a[r], xo, first ? zero : part[r][g]);
-        }
-        if (j % GS == GS - 1) {
-#pragma unroll
-          for (int r = 0; r < RT; ++r) {
-            const u32x2 sv = b.s[r][j / GS];
-            const float f[4] = {__uint_as_float(sv[0] << 16), __uint_as_float(sv[0] & 0xffff0000u), __uint_as_float(sv[1] << 16),
-                                __uint_as_float(sv[1] & 0xffff0000u)};
-#pragma unroll
-            for (int g = 0; g < NG; ++g)
-#pragma unroll
-              for (int i = 0; i < 4; ++i) acc[r][g][i] = fmaf(f[i], part[r][g][i] + corr[g][i], acc[r][g][i]);
+          for (int j = 0; j < GS; ++j) {
+            xo[g][j] = XLDS ? xv[g][h * GS + j] : w4_order_int(xv[g][h * GS + j]);
+            corr = w4_mfma(xo[g][j], neg, corr);
           }
+#pragma unroll
+          for (int r = 0; r < RT; ++r) part[r][g] = corr;
+        }
+#pragma unroll
+        for (int r = 0; r < RT; ++r) {
+#pragma unroll
+          for (int j = 0; j < GS; ++j) {
+            const u32x4 c = w4_unpack_int(b.c[r][h * GS + j]);
+#pragma unroll
+            for (int g = 0; g < NG; ++g) part[r][g] = w4_mfma(xo[g][j], c, part[r][g]);
+          }
+          const float f = __uint_as_float(b.s[r][h] << 16);
+#pragma unroll
+          for (int g = 0; g < NG; ++g)
+#pragma unroll
+            for (int i = 0; i < NI; ++i) acc[r][g][i] = fmaf(f, part[r][g][i], acc[r][g][i]);
         }
       }
     } else {
@@ -140,46 +155,64 @@ struct W4Stream {
 #pragma unroll
       for (int r = 0; r < RT; ++r) {
         // 2^(e - 127); e = 0 is below the normal range
-        const uint32_t e = b.s[r][0][0];
+        const uint32_t e = b.s[r][0];
         const float sc = __uint_as_float(e ? e << 23 : 0x00400000u);
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          const u32x4 a = w4_unpack_fp(b.c[r][j], sc);
+          const u32x4 c = w4_unpack_fp(b.c[r][j], sc);
 #pragma unroll
-          for (int g = 0; g < NG; ++g) acc[r][g] = w4_mfma(a, xv[g][j], acc[r][g]);
+          for (int g = 0; g < NG; ++g) acc[r][g] = w4_mfma(xv[g][j], c, acc[r][g]);
         }
       }
     }
   }
-  // blocks [a, b) of the row's w4_blocks(K); the last one may be a part
+
+  __device__ __forceinline__ void load(Batch& t, int blk, int last) const {
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int k = min(blk + u, last);
+      load_codes(t.c[u], k);
+      if constexpr (!XLDS) load_x(t.x[u], k);
+    }
+  }
+  __device__ __forceinline__ void mma(Batch& t, int blk, int live, f32x4 (&acc)[RT][NG]) const {
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      if (u >= live) break;
+      if constexpr (XLDS) load_x(t.x[0], blk + u);
+      mma(t.c[u], t.x[XLDS ? 0 : u], 4, acc);
+    }
+  }
+  // Blocks [a, b) of the row's w4_blocks(K); the last one may be a part.  Batches of U blocks, the next
+  // batch's loads issued before the current one's products; blocks past the last whole one repeat it and
+  // are not used.
   __device__ __forceinline__ void run(int a, int b, f32x4 (&acc)[RT][NG]) const {
     const int whole = min(b, K / W4_BLOCK);
     if (a < whole) {
-      Codes c0[U], c1[U];
-      u32x4 x0[U][NG][4];
-      auto codes = [&](Codes (&c)[U], int blk) {
-#pragma unroll
-        for (int u = 0; u < U; ++u) load_codes(c[u], min(blk + u, whole - 1));
-      };
-      // a batch: its tokens are requested before the next batch's codes, since loads return in order
-      auto batch = [&](Codes (&c)[U], Codes (&next)[U], int blk, bool more) {
-#pragma unroll
-        for (int u = 0; u < U; ++u) load_x(x0[u], min(blk + u, whole - 1));
-        if (more) codes(next, blk + U);
-#pragma unroll
-        for (int u = 0; u < U; ++u)
-          if (blk + u < whole) mma(c[u], x0[u], 4, acc);
-      };
-      codes(c0, a);
-      int blk = a;
-      for (; blk + 2 * U < whole; blk += 2 * U) {
-        batch(c0, c1, blk, true);
-        batch(c1, c0, blk + U, true);
+      Batch t0, t1;
+      load(t0, a, whole - 1);
+      int st = a;
+      for (; st + 2 * U < whole; st += 2 * U) {  // steady state: both batches whole
+        load(t1, st + U, whole - 1);
+        mma(t0, st, U, acc);
+        load(t0, st + 2 * U, whole - 1);
+        mma(t1, st + U, U, acc);
       }
-      batch(c0, c1, blk, blk + U < whole);
-      if (blk + U < whole) batch(c1, c0, blk + U, false);
+      if (st + U < whole) {
+        load(t1, st + U, whole - 1);
+        mma(t0, st, U, acc);
+        mma(t1, st + U, whole - st - U, acc);
+      } else {
+        mma(t0, st, whole - st, acc);
+      }
     }
-    if (b > whole && b * W4_BLOCK > K && a < b) tail(b - 1, acc);
+    if (b > whole && a < b) tail(b - 1, acc);
+    if constexpr (INT) {
+#pragma unroll
+      for (int r = 0; r < RT; ++r)
+#pragma unroll
+        for (int g = 0; g < NG; ++g) acc[r][g] *= 16.0f;  // codes went in as c / 16
+    }
   }
   // the part of a last block: K - 128 blk = 32, 64 or 96 elements
   __device__ __forceinline__ void tail(int blk, f32x4 (&acc)[RT][NG]) const {
@@ -192,14 +225,32 @@ struct W4Stream {
     for (int g = 0; g < NG; ++g)
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        const bool in = INT ? 32 * j < left : 32 * q < left;
+        const bool in = TR ? 32 * j < left : 32 * q < left;
         v[g][j] = in ? ld16(x[g] + blk * W4_BLOCK + j * XS) : zero;
       }
     mma(c, v, left / 32, acc);
   }
 };
 
-// What a sum over blocks is still to be multiplied by (INT: codes went in as c / 16).
-template <int FMT> __device__ __forceinline__ constexpr float w4_factor() { return FMT == W4_INT ? 16.0f : 1.0f; }
+// Copies elements [k0, k1) (multiples of 32) of a token to LDS, for the calling wave's own use: INT in the
+// order of the codes.
+template <int FMT>
+__device__ __forceinline__ void w4_stage(const bf16* x, bf16* lds, int k0, int k1) {
+  for (int k = k0 + (threadIdx.x & 63) * 8; k < k1; k += 64 * 8) {
+    const u32x4 v = ld16(x + k);
+    st16(lds + k, FMT == W4_INT ? w4_order_int(v) : v);
+  }
+}
+
+// A wave's results of one tile and token group to LDS as [token][16 rows] floats: 16 tokens, or 4 with NI = 1.
+template <int NI> constexpr int w4_tokens() { return NI == 1 ? 4 : 16; }
+template <int NI>
+__device__ __forceinline__ void w4_put(float* p, f32x4 v) {
+  const int r16 = threadIdx.x & 15, q = (threadIdx.x & 63) >> 4;
+#pragma unroll
+  for (int i = 0; i < NI; ++i) p[(NI * q + i) * 16 + r16] = v[i];
+}
+// A lane's token in a group: of the 16 rows of A.
+template <int NI> __device__ __forceinline__ int w4_token() { return NI == 1 ? (threadIdx.x & 15) >> 2 : threadIdx.x & 15; }
 
 }  // namespace moe

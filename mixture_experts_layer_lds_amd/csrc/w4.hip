@@ -1,9 +1,8 @@
 // 4-bit weights with group scales (w4.h has the formats): quantisation, expansion, and the dense
 // projection on them, out = residual + act(X W^T + bias) with bf16 X.
 //
-// A few rows: one workgroup per 16 RT rows of W, its waves sharing the reduction, the codes streamed from
-// memory straight into registers (k_w4_skinny); the waves' partial tiles meet in LDS and the epilogue runs in
-// the same launch.  More rows: W expanded to bf16 in the workspace, then the dense projection's own tiles.
+// Few rows: the codes are streamed from memory straight into registers (k_w4_rows).  More rows: W expanded to
+// bf16 in the workspace, then the dense projection's own tiles.
 #include "internal.h"
 #include "lin_epi.h"
 #include "w4.h"
@@ -92,75 +91,190 @@ __global__ __launch_bounds__(256) void k_expand_w4(const uint8_t* __restrict__ c
 }
 
 // ---- a few rows ----
-// Dynamic LDS: [wave][RT][NG][64] partial tiles.
-template <int FMT, int G, int NG, int RT, bool GLU>
-__global__ __launch_bounds__(512) void k_w4_skinny(const bf16* __restrict__ X, int64_t ldx, const uint8_t* __restrict__ codes,
-                                                   const uint8_t* __restrict__ scales, int64_t plane, int m, int n, int K,
-                                                   LinEpi<bf16> ep) {
-  extern __shared__ f32x4 sk_part[];
-  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), W_ = blockDim.x >> 6;
-  const int r16 = lane & 15, q = lane >> 4;
-  constexpr int TC = GLU ? 8 * RT : 16 * RT;  // output columns per tile
-  constexpr bool INT = FMT == W4_INT;
-  const int c0 = blockIdx.x * TC, t0 = blockIdx.y * 16 * NG;
-  W4Stream<FMT, G, NG, RT, NG == 1 && RT == 1 ? 2 : 1> ws;
+enum { W4_OUT = 0, W4_GLU = 1, W4_PART = 2 };  // the epilogue; SwiGLU's; partial products of a slice
+
+// One workgroup per 16 RT rows of W (SwiGLU: 8 RT columns, their gate rows in the first half of the tiles, the
+// up rows in the second; with RT = 1 in the halves of one tile), NG groups of tokens and one slice of the
+// reduction, which its waves share: blocks of 128 elements in contiguous runs.  The waves' results meet in LDS,
+// [wave][RT][NG][token][16], are added in wave order, and the epilogue runs on four columns of a token a thread.
+//
+// Up to 4 tokens (NI = 1) each wave copies its run of X to LDS, in the order that the products take it, so that
+// the memory path carries little but codes.  With more, X (16 tokens of a block: 4 KB for a tile's 1 KB of
+// codes) comes from L2, which bounds the kernel unless a wave takes several tiles of rows with each block of X:
+// 13 x 14336 -> 4096 took 17.3 us with RT = 1 and the whole reduction in a workgroup, 11.7 with RT = 4 and four
+// slices (to which joining them adds about 2.5).
+template <int FMT, int G, int NG, int RT, int NI, bool XLDS, int U, int OUT>
+__global__ __launch_bounds__(512) void k_w4_rows(const bf16* __restrict__ X, int64_t ldx, const uint8_t* __restrict__ codes,
+                                                 const uint8_t* __restrict__ scales, int64_t plane, int m, int n, int K,
+                                                 float* __restrict__ part, LinEpi<bf16> ep) {
+  extern __shared__ __attribute__((aligned(16))) char w4_lds[];
+  typedef W4Stream<FMT, G, NG, RT, NI, XLDS, U> Stream;
+  constexpr int TOK = w4_tokens<NI>();
+  constexpr bool GLU = OUT == W4_GLU;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), W_ = blockDim.x >> 6;
+  const int lane = threadIdx.x & 63, r16 = lane & 15, q = lane >> 4;
+  const int c0 = blockIdx.x * (GLU ? 8 : 16) * RT, t0 = blockIdx.y * TOK * NG;
+  Stream ws;
 #pragma unroll
   for (int r = 0; r < RT; ++r) {
-    // row i of the tile: (rows behind the last read valid ones, unused)
-    auto row = [&](int i, int rows) {
-      if constexpr (!GLU) return min(c0 + 16 * r + i, n - rows);
-      else if constexpr (RT == 1) return i < 8 ? c0 + i : n + c0 + i - 8;
-      else return r * n + min(c0 + i, n - rows);
-    };
-    ws.w[r] = codes + (int64_t)row(r16, 1) * (K / 2) + 16 * q;
-    ws.s[r] = INT ? scales + (int64_t)row(4 * q, 4) * 2 : scales + (int64_t)row(r16, 1) * 4 + q;
+    int row;  // (rows behind the last read it, unused)
+    if constexpr (!GLU) row = min(c0 + 16 * r + r16, n - 1);
+    else if constexpr (RT == 1) row = r16 < 8 ? c0 + r16 : n + c0 + r16 - 8;
+    else row = (r < RT / 2 ? 0 : n) + min(c0 + 16 * (r % (RT / 2)) + r16, n - 1);
+    ws.w[r] = codes + (int64_t)row * (K / 2) + 16 * q;
+    ws.s[r] = scales + (FMT == W4_INT ? (int64_t)row * 2 : (int64_t)row * 4 + q);
   }
   ws.plane = plane;
   ws.K = K;
+  const int nb = w4_blocks(K);
+  const int z0 = (int)((int64_t)nb * blockIdx.z / gridDim.z), z1 = (int)((int64_t)nb * (blockIdx.z + 1) / gridDim.z);
+  const int a = z0 + (z1 - z0) * wave / W_, b = z0 + (z1 - z0) * (wave + 1) / W_;
+  bf16* xl = reinterpret_cast<bf16*>(w4_lds);
+  const int xp = K + 8;  // LDS pitch of a token
 #pragma unroll
-  for (int g = 0; g < NG; ++g) ws.x[g] = X + (int64_t)min(t0 + g * 16 + r16, m - 1) * ldx + (INT ? 8 : 32) * q;
+  for (int g = 0; g < NG; ++g) {
+    const int t = min(t0 + g * TOK + w4_token<NI>(), m - 1);
+    ws.x[g] = (XLDS ? xl + t * xp : X + (int64_t)t * ldx) + Stream::XQ * q;
+  }
+  if constexpr (XLDS)
+    for (int t = 0; t < m; ++t) w4_stage<FMT>(X + t * ldx, xl + t * xp, a * W4_BLOCK, min(b * W4_BLOCK, K));
   f32x4 acc[RT][NG];
 #pragma unroll
   for (int r = 0; r < RT; ++r)
 #pragma unroll
     for (int g = 0; g < NG; ++g) acc[r][g] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-  const int nb = w4_blocks(K), a = (int)((int64_t)nb * wave / W_), b = (int)((int64_t)nb * (wave + 1) / W_);
   if (a < b) ws.run(a, b, acc);
+  if constexpr (XLDS) __syncthreads();  // (the results take the tokens' place)
+  float* res = reinterpret_cast<float*>(w4_lds);
+  constexpr int TILE = TOK * 16;
 #pragma unroll
   for (int r = 0; r < RT; ++r)
 #pragma unroll
-    for (int g = 0; g < NG; ++g) acc[r][g] *= w4_factor<FMT>();
-  lin_skinny_join<bf16, NG, RT, GLU>(acc, sk_part, ep, t0, m, n, c0);
+    for (int g = 0; g < NG; ++g) w4_put<NI>(res + ((wave * RT + r) * NG + g) * TILE, acc[r][g]);
+  __syncthreads();
+  auto total = [&](int r, int g, int at) {
+    const float* p = res + (r * NG + g) * TILE + at;
+    f32x4 v = *reinterpret_cast<const f32x4*>(p);
+    for (int w = 1; w < W_; ++w) v += *reinterpret_cast<const f32x4*>(p + w * RT * NG * TILE);
+    return v;
+  };
+  constexpr int QUADS = GLU ? 2 * RT : 4 * RT;  // of a token's columns
+  for (int it = threadIdx.x; it < NG * TOK * QUADS; it += blockDim.x) {
+    const int quad = it % QUADS, tok = it / QUADS % TOK, g = it / QUADS / TOK;
+    const int c = c0 + 4 * quad, t = t0 + g * TOK + tok;
+    if (t >= m || c >= n) continue;
+    const int r = quad >> 2, at = tok * 16 + 4 * (quad & 3);
+    const f32x4 z = total(r, g, at);
+    if constexpr (GLU) {
+      const f32x4 up = RT == 1 ? total(0, g, at + 8) : total(r + RT / 2, g, at);
+      lin_epi4(ep, (int64_t)t, c, n, true, z, up);
+    } else if constexpr (OUT == W4_OUT) {
+      lin_epi4(ep, (int64_t)t, c, n, false, z, z);
+    } else {
+      *reinterpret_cast<f32x4*>(part + ((int64_t)blockIdx.z * m + t) * n + c) = z;
+    }
+  }
 }
 
 // Rows up to which the codes are streamed; more go through an expanded copy of W.
 constexpr int W4_STREAM_ROWS = 64;
+constexpr int64_t W4_LDS = 65536;
 
-template <int FMT, int G, int NG, int RT>
-static void w4_skinny_rt(const LinShape& s, const W4View& w, const bf16* X, const LinEpi<bf16>& ep, hipStream_t st) {
+// How a product is cut: by the shape alone, so that the workspace is known without the weights.
+struct W4Plan {
+  bool lds;         // up to 4 tokens, which lie in LDS
+  int ng, rt;       // token groups of 16 and row tiles of a workgroup
+  int slices, waves;
+};
+static W4Plan w4_plan(const LinShape& s) {
   const bool glu = s.act == LIN_SWIGLU;
   const int64_t rows = glu ? 2 * s.N : s.N;
-  const dim3 grid((unsigned)cdiv(s.N, (glu ? 8 : 16) * RT), (unsigned)cdiv(s.M, 16 * NG));
   const int blocks = w4_blocks((int)s.K);
-  int waves = 1;
-  while (waves < 8 && blocks / waves >= 4) waves *= 2;
-  const size_t lds = (size_t)waves * RT * NG * 64 * sizeof(f32x4);
+  W4Plan p;
+  p.lds = s.M <= 4 && s.M * (s.K + 8) * 2 <= W4_LDS;
+  p.ng = s.M <= 16 ? 1 : 2;
+  p.rt = 1;
+  p.slices = 1;
+  if (p.lds) {
+    // 8 waves where the grid would not fill the chip otherwise (2 x 2048 x 7168: 5.9 us, 6.6 with 4;
+    // 2 x 14336 x 4096: 14.8, 14.0)
+    const int64_t tiles = rows / 16;
+    p.waves = 4;
+    while (p.waves < 8 && tiles * p.waves < 2048) p.waves *= 2;
+    while (p.waves > 1 && blocks / p.waves < 4) p.waves /= 2;
+    return p;
+  }
+  // X costs its bytes once per workgroup, at about 13 TB/s over all L2s; fewer, taller workgroups need
+  // slices to fill the chip, and a second launch of about 2.5 us to join them
+  const int64_t groups = cdiv(s.M, 16 * p.ng);
+  const double x_us = 32.0 * p.ng * s.K * groups / 13e6;  // per row tile of a workgroup
+  int best = 1;
+  for (int rt : {4, 2}) {
+    if (cdiv(rows, 16 * rt) * groups >= 200) {
+      best = rt;
+      break;
+    }
+  }
+  const double whole = x_us * cdiv(rows, 16 * best), sliced = x_us * cdiv(rows, 64) + 2.5;
+  p.rt = best;
+  if (best < 4 && sliced < whole) {
+    p.rt = 4;
+    while (p.slices < 8 && cdiv(rows, 64) * groups * p.slices < 200 && blocks / (2 * p.slices) >= 8) p.slices *= 2;
+    if (p.slices == 1) p.rt = best;
+  }
+  p.waves = 8;
+  while (p.waves > 1 && blocks / p.slices / p.waves < 2) p.waves /= 2;
+  return p;
+}
+
+template <int FMT, int G, int NG, int RT, int NI, bool XLDS, int U>
+static void w4_rows(const LinShape& s, const W4Plan& p, const W4View& w, const bf16* X, const LinEpi<bf16>& ep, float* part,
+                    hipStream_t st) {
+  const bool glu = s.act == LIN_SWIGLU;
+  const int64_t rows = glu ? 2 * s.N : s.N;
+  constexpr int TOK = w4_tokens<NI>();
+  size_t lds = (size_t)p.waves * RT * NG * TOK * 16 * sizeof(float);
+  const size_t xl = XLDS ? (size_t)s.M * (s.K + 8) * sizeof(bf16) : 0;
+  if (xl > lds) lds = xl;
+  const dim3 grid((unsigned)cdiv(rows, 16 * RT), (unsigned)cdiv(s.M, TOK * NG), (unsigned)p.slices);
   const uint8_t* sc = static_cast<const uint8_t*>(w.scales);
   const int64_t plane = rows * (FMT == W4_INT ? 2 : 4);
-  if (glu) k_w4_skinny<FMT, G, NG, RT, true><<<grid, waves * 64, lds, st>>>(X, s.ldx, w.codes, sc, plane, (int)s.M, (int)s.N, (int)s.K, ep);
-  else k_w4_skinny<FMT, G, NG, RT, false><<<grid, waves * 64, lds, st>>>(X, s.ldx, w.codes, sc, plane, (int)s.M, (int)s.N, (int)s.K, ep);
+  const int m = (int)s.M, K = (int)s.K, threads = p.waves * 64;
+  if (p.slices > 1) {
+    if constexpr (!XLDS && RT == 4)
+      k_w4_rows<FMT, G, NG, RT, NI, XLDS, U, W4_PART><<<grid, threads, lds, st>>>(X, s.ldx, w.codes, sc, plane, m, (int)rows, K, part, ep);
+  } else if (glu) {
+    k_w4_rows<FMT, G, NG, RT, NI, XLDS, U, W4_GLU><<<grid, threads, lds, st>>>(X, s.ldx, w.codes, sc, plane, m, (int)s.N, K, part, ep);
+  } else {
+    k_w4_rows<FMT, G, NG, RT, NI, XLDS, U, W4_OUT><<<grid, threads, lds, st>>>(X, s.ldx, w.codes, sc, plane, m, (int)s.N, K, part, ep);
+  }
+}
+template <int FMT, int G, int NG>
+static void w4_rows_rt(const LinShape& s, const W4Plan& p, const W4View& w, const bf16* X, const LinEpi<bf16>& ep, float* part,
+                       hipStream_t st) {
+  if (p.rt == 4) w4_rows<FMT, G, NG, 4, 4, false, 1>(s, p, w, X, ep, part, st);
+  else if (p.rt == 2) w4_rows<FMT, G, NG, 2, 4, false, 1>(s, p, w, X, ep, part, st);
+  else w4_rows<FMT, G, NG, 1, 4, false, 1>(s, p, w, X, ep, part, st);
 }
 template <int FMT, int G>
-static void w4_skinny(const LinShape& s, const W4View& w, const bf16* X, const LinEpi<bf16>& ep, hipStream_t st) {
-  if (s.M <= 16) w4_skinny_rt<FMT, G, 1, 1>(s, w, X, ep, st);
-  else w4_skinny_rt<FMT, G, 2, 1>(s, w, X, ep, st);
+static hipError_t w4_stream(const LinShape& s, const W4View& w, const bf16* X, const LinEpi<bf16>& ep, float* part, hipStream_t st) {
+  const W4Plan p = w4_plan(s);
+  // (small groups leave no registers for two blocks a batch)
+  if (p.lds) w4_rows<FMT, G, 1, 1, 1, true, FMT == W4_INT && G < 128 ? 1 : 2>(s, p, w, X, ep, part, st);
+  else if (p.ng == 1) w4_rows_rt<FMT, G, 1>(s, p, w, X, ep, part, st);
+  else w4_rows_rt<FMT, G, 2>(s, p, w, X, ep, part, st);
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess || p.slices == 1) return e;
+  return launch_lin_finish(part, p.slices, (int)s.M, (int)s.N, (int)(s.act == LIN_SWIGLU ? 2 * s.N : s.N), ep, st);
 }
 
 static size_t w4_expanded_bytes(const LinShape& s) {
   return align_up((size_t)(s.act == LIN_SWIGLU ? 2 * s.N : s.N) * s.K * sizeof(bf16), 256);
 }
 size_t linear_w4_workspace_bytes(const LinShape& s) {
-  return s.M <= W4_STREAM_ROWS ? 0 : w4_expanded_bytes(s) + linear_fwd_workspace_bytes(s);
+  if (s.M > W4_STREAM_ROWS) return w4_expanded_bytes(s) + linear_fwd_workspace_bytes(s);
+  const int slices = s.M > 0 ? w4_plan(s).slices : 1;
+  return slices > 1 ? (size_t)slices * s.M * (s.act == LIN_SWIGLU ? 2 * s.N : s.N) * sizeof(float) : 0;
 }
 
 hipError_t launch_quant_w4(const void* src, bool is_bf16, int format, int group, int64_t rows, int64_t K, uint8_t* codes,
@@ -207,11 +321,11 @@ hipError_t launch_linear_w4(const LinShape& s, const void* X, const W4View& w, c
   }
   const LinEpi<bf16> ep{bias, static_cast<const bf16*>(residual), s.ldr, nullptr, 0, static_cast<bf16*>(out), s.ldy, s.act};
   const bf16* x = static_cast<const bf16*>(X);
-  if (w.format == W4_FP) w4_skinny<W4_FP, 32>(s, w, x, ep, st);
-  else if (w.group == 32) w4_skinny<W4_INT, 32>(s, w, x, ep, st);
-  else if (w.group == 64) w4_skinny<W4_INT, 64>(s, w, x, ep, st);
-  else w4_skinny<W4_INT, 128>(s, w, x, ep, st);
-  return hipGetLastError();
+  float* part = static_cast<float*>(ws);
+  if (w.format == W4_FP) return w4_stream<W4_FP, 32>(s, w, x, ep, part, st);
+  if (w.group == 32) return w4_stream<W4_INT, 32>(s, w, x, ep, part, st);
+  if (w.group == 64) return w4_stream<W4_INT, 64>(s, w, x, ep, part, st);
+  return w4_stream<W4_INT, 128>(s, w, x, ep, part, st);
 }
 
 }  // namespace moe

@@ -89,7 +89,7 @@ def test_every_fp4_code_and_scale_byte():
     for k0 in (0, 16):
         x = torch.zeros(16, K, dtype=torch.bfloat16, device="cuda")
         x[torch.arange(16), k0 + torch.arange(16)] = 1.0
-        B.moe_linear_w4(dims, x, w, None, None, y, None, 0)
+        B.moe_linear_w4(dims, x, w, None, None, y, *B.linear_w4_workspace(dims))
         got = f64(y).T
         ok = (np.abs(V) >= 2.0 ** -126) & (np.abs(V) < 3.3e38) | (V == 0)
         # (a row with weights beyond the range has infinities times zero)
@@ -176,16 +176,19 @@ def test_rows_are_independent(fmt, group):
     M, N, K = 16, 128, 512
     w = random_w4(N, K, fmt, group, 5)[0]
     x = torch.randn(M, K, generator=torch.Generator().manual_seed(1)).bfloat16().cuda()
-    dims, one = B.make_linear_dims(M, N, K), B.make_linear_dims(1, N, K)
-    y, y1 = torch.empty(M, N, dtype=torch.bfloat16, device="cuda"), torch.empty(1, N, dtype=torch.bfloat16, device="cuda")
-    B.moe_linear_w4(dims, x, w, None, None, y, None, 0)
+    dims = B.make_linear_dims(M, N, K)
+    y, y1 = (torch.empty(M, N, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    ws, nb = B.linear_w4_workspace(dims)
+    B.moe_linear_w4(dims, x, w, None, None, y, ws, nb)
     for t in (0, 7, 15):
-        B.moe_linear_w4(one, x[t:t + 1], w, None, None, y1, None, 0)
-        assert torch.equal(y1[0], y[t])
+        other = torch.randn(M, K, generator=torch.Generator().manual_seed(t + 2)).bfloat16().cuda()
+        other[t] = x[t]
+        B.moe_linear_w4(dims, other, w, None, None, y1, ws, nb)
+        assert torch.equal(y1[t], y[t])
     bad = x.clone()
     bad[3, 5], bad[9, 500] = float("nan"), float("inf")
     z = torch.empty_like(y)
-    B.moe_linear_w4(dims, bad, w, None, None, z, None, 0)
+    B.moe_linear_w4(dims, bad, w, None, None, z, ws, nb)
     keep = [t for t in range(M) if t not in (3, 9)]
     assert torch.equal(z[keep], y[keep]) and bool(z[3].isnan().all()) and not bool(z[9].isfinite().any())
 
