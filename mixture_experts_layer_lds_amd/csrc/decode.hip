@@ -286,7 +286,7 @@ __global__ __launch_bounds__(DEC_THREADS) void k_decode(DecodeArgs a) {
     for (int t = blockIdx.x * DEC_WAVES + wave; t < T_; t += nw) {
       int my_e;
       float my_v;
-      wave_select(a.logits + (int64_t)t * E, E, K, my_e, my_v);
+      wave_select<16>([&](int e) { return a.logits[(int64_t)t * E + e]; }, E, K, my_e, my_v);
       const float vmax = __shfl(my_v, 0, 64);
       const float ex = lane < K ? __expf(my_v - vmax) : 0.0f;
       const float sum = wave_sum(ex);

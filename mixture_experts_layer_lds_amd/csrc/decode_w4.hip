@@ -5,10 +5,10 @@
 // the one before costs about 2 us, a barrier of the whole chip and the phases' uneven ends cost more.
 //
 // By pairs (few tokens for the experts, so that hardly two choose the same one): three launches.
-//   1. router logits;
-//   2. gate/up: a workgroup takes 8 columns of one (token, choice) pair.  Its first wave finds the pair's
+//   1. router logits, the reduction cut into slices whose sums the next launch adds;
+//   2. gate/up: a workgroup takes 16 columns of one (token, choice) pair.  Its first wave finds the pair's
 //      expert from the token's logits while the others copy the token to LDS, so that top-K needs no launch;
-//      one workgroup of a token writes its choices and weights;
+//      one workgroup of a token writes its logits, choices and weights;
 //   3. down: a workgroup takes 16 output columns of a token, its waves the token's experts; their results are
 //      added in ascending expert order with their weights, in LDS.
 // By experts (more tokens): five launches.  1. router logits, which also clear the experts' counters; 2. top-K,
@@ -34,11 +34,12 @@ struct DecW4 {
   int32_t* list;  // [E][T] pair ids t * K + k
   bf16* act;      // [T * K][n]
   float* y;       // [T * K][d]
-  int T, d, n, E, K;
+  float* part;    // [slices][T][E] sums of slices of the router logits (one slice: they are the logits)
+  int T, d, n, E, K, slices;
 };
 
-// ---- 1. router logits: a workgroup takes 16 experts and up to 48 tokens, its waves share d ----
-constexpr int DW_LOGIT_WAVES = 16, DW_NG = 3;
+// ---- 1. router logits: a workgroup takes 16 experts, up to 48 tokens and a slice of d, its waves share it ----
+constexpr int DW_LOGIT_WAVES = 4, DW_NG = 3, DW_SLICES = 8;
 
 template <int NG>
 __device__ __forceinline__ void dw_logit_rows(const bf16* wrow, const bf16* const* xrow, int a, int b, f32x4* acc) {
@@ -51,9 +52,10 @@ __device__ __forceinline__ void dw_logit_rows(const bf16* wrow, const bf16* cons
 }
 
 __global__ __launch_bounds__(DW_LOGIT_WAVES * 64) void k_dw4_logits(DecW4 a, bool lists) {
-  __shared__ f32x4 part[DW_LOGIT_WAVES][DW_NG][64];
+  __shared__ f32x4 red[DW_LOGIT_WAVES][DW_NG][64];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), r16 = lane & 15, q = lane >> 4;
-  if (lists && blockIdx.x == 0 && blockIdx.y == 0 && (int)threadIdx.x < a.E) a.cnt[threadIdx.x] = 0;  // (E <= 1024)
+  if (lists && blockIdx.x == 0 && blockIdx.y == 0 && blockIdx.z == 0)
+    for (int i = threadIdx.x; i < a.E; i += DW_LOGIT_WAVES * 64) a.cnt[i] = 0;
   const int e0 = blockIdx.x * 16, g0 = blockIdx.y * DW_NG;
   const int ng = min(DW_NG, (a.T + 15) / 16 - g0);
   const bf16* wrow = a.W_r + (int64_t)min(e0 + r16, a.E - 1) * a.d;
@@ -63,38 +65,64 @@ __global__ __launch_bounds__(DW_LOGIT_WAVES * 64) void k_dw4_logits(DecW4 a, boo
   f32x4 acc[DW_NG];
 #pragma unroll
   for (int g = 0; g < DW_NG; ++g) acc[g] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-  const int ns = a.d / DecMma<bf16>::S, s0 = ns * wave / DW_LOGIT_WAVES, s1 = ns * (wave + 1) / DW_LOGIT_WAVES;
+  const int ns = a.d / DecMma<bf16>::S, parts = gridDim.z * DW_LOGIT_WAVES, p = blockIdx.z * DW_LOGIT_WAVES + wave;
+  const int s0 = ns * p / parts, s1 = ns * (p + 1) / parts;
   if (ng == 3) dw_logit_rows<3>(wrow, xrow, s0, s1, acc);
   else if (ng == 2) dw_logit_rows<2>(wrow, xrow, s0, s1, acc);
   else dw_logit_rows<1>(wrow, xrow, s0, s1, acc);
 #pragma unroll
-  for (int g = 0; g < DW_NG; ++g) part[wave][g][lane] = acc[g];
+  for (int g = 0; g < DW_NG; ++g) red[wave][g][lane] = acc[g];
   __syncthreads();
   if (wave < ng) {
-    f32x4 v = part[0][wave][lane];
-    for (int w = 1; w < DW_LOGIT_WAVES; ++w) v += part[w][wave][lane];
+    f32x4 v = red[0][wave][lane];
+    for (int w = 1; w < DW_LOGIT_WAVES; ++w) v += red[w][wave][lane];
     const int t = (g0 + wave) * 16 + r16;
+    const bool whole = gridDim.z == 1;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const int e = e0 + 4 * q + i;
-      if (t < a.T && e < a.E) a.logits[(int64_t)t * a.E + e] = v[i] + (a.bias ? a.bias[e] : 0.0f);
+      if (t >= a.T || e >= a.E) continue;
+      if (whole) a.logits[(int64_t)t * a.E + e] = v[i] + (a.bias ? a.bias[e] : 0.0f);
+      else a.part[((int64_t)blockIdx.z * a.T + t) * a.E + e] = v[i];
     }
   }
 }
 
-// A token's choices and weights by one wave; lane k returns the k-th expert.
-__device__ __forceinline__ int dw_choose(const DecW4& a, int t) {
+// The first K choices of token t by one wave; lane k returns the k-th expert.  WRITE (then K is the layer's):
+// also writes the logits where they lie in slices, the choices and the weights.
+template <int EJ, bool WRITE>
+__device__ __forceinline__ int dw_choose_ej(const DecW4& a, int t, int K) {
   const int lane = threadIdx.x & 63;
   int e;
   float v;
-  wave_select(a.logits + (int64_t)t * a.E, a.E, a.K, e, v);
-  const float ex = lane < a.K ? __expf(v - __shfl(v, 0, WAVE)) : 0.0f;
-  const float sum = wave_sum(ex);
-  if (lane < a.K) {
-    a.topk_idx[(int64_t)t * a.K + lane] = e;
-    a.topk_w[(int64_t)t * a.K + lane] = ex / sum;
+  wave_select<EJ>([&](int i) {
+    const int64_t at = (int64_t)t * a.E + i;
+    if (a.slices == 1) return a.logits[at];
+    float p[DW_SLICES];
+#pragma unroll
+    for (int s = 0; s < DW_SLICES; ++s) p[s] = s < a.slices ? a.part[(int64_t)s * a.T * a.E + at] : 0.0f;
+    float l = p[0];
+#pragma unroll
+    for (int s = 1; s < DW_SLICES; ++s) l += p[s];
+    if (a.bias) l += a.bias[i];
+    if (WRITE) a.logits[at] = l;
+    return l;
+  }, a.E, K, e, v);
+  if (WRITE) {
+    const float ex = lane < K ? __expf(v - __shfl(v, 0, WAVE)) : 0.0f;
+    const float sum = wave_sum(ex);
+    if (lane < K) {
+      a.topk_idx[(int64_t)t * K + lane] = e;
+      a.topk_w[(int64_t)t * K + lane] = ex / sum;
+    }
   }
   return e;
+}
+template <bool WRITE>
+__device__ __forceinline__ int dw_choose(const DecW4& a, int t, int K) {
+  if (a.E <= 128) return dw_choose_ej<2, WRITE>(a, t, K);
+  if (a.E <= 256) return dw_choose_ej<4, WRITE>(a, t, K);
+  return dw_choose_ej<16, WRITE>(a, t, K);
 }
 
 // The ranks of a token's choices by expert id: order[r] is the choice of the r-th smallest expert.
@@ -118,46 +146,50 @@ __device__ __forceinline__ void dw_order(const int32_t* idx, int K, int (&order)
 }
 
 // ---- by pairs ----
-// gate/up of a pair: 8 gate rows and their up rows in one tile
+// gate/up of a pair: 16 gate rows and their up rows
 template <int FMT, int G, bool XLDS>
-__global__ __launch_bounds__(512) void k_dw4_up_pair(DecW4 a) {
+__global__ __launch_bounds__(256) void k_dw4_up_pair(DecW4 a) {
   extern __shared__ __attribute__((aligned(16))) char dw_lds[];
   __shared__ int chosen;
-  typedef W4Stream<FMT, G, 1, 1, 1, XLDS, FMT == W4_INT && G < 128 ? 1 : 2> Stream;
+  typedef W4Stream<FMT, G, 1, 2, 1, XLDS, FMT == W4_INT && G < 128 ? 1 : 2> Stream;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), W_ = blockDim.x >> 6;
   const int lane = threadIdx.x & 63, r16 = lane & 15, q = lane >> 4;
-  const int pair = blockIdx.y, t = pair / a.K, k = pair - t * a.K, j0 = blockIdx.x * 8;
+  const int pair = blockIdx.y, t = pair / a.K, k = pair - t * a.K, j0 = blockIdx.x * 16;
   const bf16* x = a.X + (int64_t)t * a.d;
   bf16* xl = reinterpret_cast<bf16*>(dw_lds);
   const int nb = w4_blocks(a.d), b0 = nb * wave / W_, b1 = nb * (wave + 1) / W_;
-  if constexpr (XLDS) w4_stage<FMT>(x, xl, b0 * W4_BLOCK, min(b1 * W4_BLOCK, a.d));
   if (wave == 0) {
-    int e;
-    float v;
-    if (blockIdx.x == 0 && k == 0) e = dw_choose(a, t);
-    else wave_select(a.logits + (int64_t)t * a.E, a.E, k + 1, e, v);
+    const int e = blockIdx.x == 0 && k == 0 ? dw_choose<true>(a, t, a.K) : dw_choose<false>(a, t, k + 1);
     if (lane == k) chosen = e;
+  }
+  if constexpr (XLDS) {
+    W4Stage<FMT, 1> stage;
+    stage.request(x, xl, b0 * W4_BLOCK, min(b1 * W4_BLOCK, a.d));
+    stage.write();
   }
   __syncthreads();
   const int e = __builtin_amdgcn_readfirstlane(chosen);
-  const int64_t row = (int64_t)e * a.n + j0 + (r16 & 7);
+  const int64_t row = (int64_t)e * a.n + j0 + r16;
   Stream ws;
-  ws.w[0] = (r16 < 8 ? a.gate : a.up) + row * (a.d / 2) + 16 * q;
-  ws.s[0] = (r16 < 8 ? a.s_gate : a.s_up) + (FMT == W4_INT ? row * 2 : row * 4 + q);
+#pragma unroll
+  for (int r = 0; r < 2; ++r) {
+    ws.w[r] = (r == 0 ? a.gate : a.up) + row * (a.d / 2) + 16 * q;
+    ws.s[r] = (r == 0 ? a.s_gate : a.s_up) + (FMT == W4_INT ? row * 2 : row * 4 + q);
+  }
   ws.plane = (int64_t)a.E * a.n * (FMT == W4_INT ? 2 : 4);
   ws.x[0] = (XLDS ? xl : x) + Stream::XQ * q;
   ws.K = a.d;
-  f32x4 acc[1][1] = {{{0.0f, 0.0f, 0.0f, 0.0f}}};
+  f32x4 acc[2][1] = {{{0.0f, 0.0f, 0.0f, 0.0f}}, {{0.0f, 0.0f, 0.0f, 0.0f}}};
   if (b0 < b1) ws.run(b0, b1, acc);
   __syncthreads();
-  float* res = reinterpret_cast<float*>(dw_lds);  // [wave][16]
-  if (q == 0) res[wave * 16 + r16] = acc[0][0][0];
+  float* res = reinterpret_cast<float*>(dw_lds);  // [wave][gate, up][16]
+  if (q < 2) res[(wave * 2 + q) * 16 + r16] = q == 0 ? acc[0][0][0] : acc[1][0][0];
   __syncthreads();
-  if (threadIdx.x < 8) {
+  if (threadIdx.x < 16) {
     float g = 0.0f, u = 0.0f;
     for (int w = 0; w < W_; ++w) {
-      g += res[w * 16 + threadIdx.x];
-      u += res[w * 16 + 8 + threadIdx.x];
+      g += res[w * 32 + threadIdx.x];
+      u += res[w * 32 + 16 + threadIdx.x];
     }
     a.act[(int64_t)pair * a.n + j0 + threadIdx.x] = from_f32<bf16>(g * sigmoid_f32(g) * u);
   }
@@ -171,12 +203,14 @@ __global__ __launch_bounds__(1024) void k_dw4_down_pair(DecW4 a, int splits) {
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int lane = threadIdx.x & 63, r16 = lane & 15, q = lane >> 4;
   const int t = blockIdx.y, c0 = blockIdx.x * 16, k = wave / splits, part = wave - k * splits;
+  const int32_t* idx = a.topk_idx + (int64_t)t * a.K;
+  const int e = idx[k];
   const bf16* x = a.act + ((int64_t)t * a.K + k) * a.n;
   bf16* xl = reinterpret_cast<bf16*>(dw_lds) + (int64_t)k * a.n;
   const int nb = w4_blocks(a.n), b0 = nb * part / splits, b1 = nb * (part + 1) / splits;
-  if constexpr (XLDS) w4_stage<FMT>(x, xl, b0 * W4_BLOCK, min(b1 * W4_BLOCK, a.n));
-  const int32_t* idx = a.topk_idx + (int64_t)t * a.K;
-  const int64_t row = (int64_t)__builtin_amdgcn_readfirstlane(idx[k]) * a.d + c0 + r16;
+  W4Stage<FMT, 4> stage;
+  if constexpr (XLDS) stage.request(x, xl, b0 * W4_BLOCK, min(b1 * W4_BLOCK, a.n));
+  const int64_t row = (int64_t)__builtin_amdgcn_readfirstlane(e) * a.d + c0 + r16;
   Stream ws;
   ws.w[0] = a.down + row * (a.n / 2) + 16 * q;
   ws.s[0] = a.s_down + (FMT == W4_INT ? row * 2 : row * 4 + q);
@@ -184,7 +218,10 @@ __global__ __launch_bounds__(1024) void k_dw4_down_pair(DecW4 a, int splits) {
   ws.x[0] = (XLDS ? xl : x) + Stream::XQ * q;
   ws.K = a.n;
   f32x4 acc[1][1] = {{{0.0f, 0.0f, 0.0f, 0.0f}}};
-  if (b0 < b1) ws.run(b0, b1, acc);
+  if (b0 < b1)
+    ws.run(b0, b1, acc, [&] {
+      if constexpr (XLDS) stage.write();
+    });
   __syncthreads();
   float* res = reinterpret_cast<float*>(dw_lds);  // [wave][16]
   if (q == 0) res[wave * 16 + r16] = acc[0][0][0];
@@ -208,7 +245,7 @@ __global__ __launch_bounds__(1024) void k_dw4_down_pair(DecW4 a, int splits) {
 __global__ __launch_bounds__(256) void k_dw4_topk(DecW4 a) {
   const int t = blockIdx.x * 4 + (threadIdx.x >> 6), lane = threadIdx.x & 63;
   if (t >= a.T) return;
-  const int e = dw_choose(a, t);
+  const int e = dw_choose<true>(a, t, a.K);
   if (lane < a.K) a.list[(int64_t)e * a.T + atomicAdd(&a.cnt[e], 1)] = t * a.K + lane;  // (a token picks an expert at most once)
 }
 
@@ -295,26 +332,30 @@ __global__ __launch_bounds__(256) void k_dw4_combine(DecW4 a) {
 
 constexpr int64_t DW_LDS = 65536;
 
+// Whether the call goes by pairs.
+static bool dw4_pairs(int64_t T, int E, int K) { return T == 1 || T * K * 2 <= E; }
+
 template <int FMT, int G>
 static hipError_t dw4_run(const DecW4& a, hipStream_t st) {
-  const bool pairs = a.T * a.K * 2 <= a.E || a.T == 1;
-  const dim3 lg((unsigned)cdiv(a.E, 16), (unsigned)cdiv(a.T, 16 * DW_NG));
+  const bool pairs = dw4_pairs(a.T, a.E, a.K);
+  const dim3 lg((unsigned)cdiv(a.E, 16), (unsigned)cdiv(a.T, 16 * DW_NG), (unsigned)a.slices);
   k_dw4_logits<<<lg, DW_LOGIT_WAVES * 64, 0, st>>>(a, !pairs);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
   if (pairs) {
     const int nb = w4_blocks(a.d);
     int waves = 4;
-    while (waves > 1 && nb / waves < 4) waves /= 2;
-    const dim3 ug((unsigned)(a.n / 8), (unsigned)(a.T * a.K));
+    while (waves > 1 && nb / waves < 3) waves /= 2;
+    const dim3 ug((unsigned)(a.n / 16), (unsigned)(a.T * a.K));
     const int64_t xl = (int64_t)a.d * 2;
     if (xl <= DW_LDS) k_dw4_up_pair<FMT, G, true><<<ug, waves * 64, xl < 1024 ? 1024 : xl, st>>>(a);
     else k_dw4_up_pair<FMT, G, false><<<ug, waves * 64, 1024, st>>>(a);
     e = hipGetLastError();
     if (e != hipSuccess) return e;
+    // waves per choice: up to 8 waves in all, so that the chip holds three workgroups a CU
     const int nd = w4_blocks(a.n);
     int splits = 1;
-    while (a.K * splits * 2 <= 16 && nd / (splits * 2) >= 4) splits *= 2;
+    while (a.K * splits * 2 <= 8 && nd / (splits * 2) >= 4) splits *= 2;
     const dim3 dg((unsigned)(a.d / 16), (unsigned)a.T);
     const int64_t al = (int64_t)a.K * a.n * 2;
     if (al <= DW_LDS) k_dw4_down_pair<FMT, G, true><<<dg, a.K * splits * 64, al < 1024 ? 1024 : al, st>>>(a, splits);
@@ -358,15 +399,21 @@ hipError_t launch_decode_w4(const Shape& s, const void* X, const void* W_r, cons
   a.topk_idx = topk_idx;
   a.topk_w = topk_w;
   a.out = static_cast<bf16*>(out);
+  a.T = (int)s.T; a.d = (int)s.d; a.n = (int)s.n; a.E = s.E; a.K = s.K;
   char* w = static_cast<char*>(ws);  // (moe_decode's workspace holds more)
   a.cnt = reinterpret_cast<int32_t*>(w);
   w += dw_align((size_t)s.E * 4);
-  a.list = reinterpret_cast<int32_t*>(w);
-  w += dw_align((size_t)s.E * s.T * 4);
   a.act = reinterpret_cast<bf16*>(w);
   w += dw_align((size_t)s.T * s.K * s.n * 2);
+  a.list = reinterpret_cast<int32_t*>(w);
+  w += dw_align((size_t)s.E * s.T * 4);
   a.y = reinterpret_cast<float*>(w);
-  a.T = (int)s.T; a.d = (int)s.d; a.n = (int)s.n; a.E = s.E; a.K = s.K;
+  // slices of the logits lie where y will be written, by pairs over the unused lists too; each has at least 8
+  // steps of the reduction
+  a.part = dw4_pairs(s.T, s.E, s.K) ? reinterpret_cast<float*>(a.list) : a.y;
+  const int64_t room = (int64_t)s.K * s.d + (dw4_pairs(s.T, s.E, s.K) ? s.E : 0);  // floats per token
+  a.slices = 1;
+  while (a.slices < DW_SLICES && s.d / 32 / (a.slices * 2) >= 8 && (int64_t)s.E * a.slices * 2 <= room) a.slices *= 2;
   if (W_gate.format == W4_FP) return dw4_run<W4_FP, 32>(a, st);
   if (W_gate.group == 32) return dw4_run<W4_INT, 32>(a, st);
   if (W_gate.group == 64) return dw4_run<W4_INT, 64>(a, st);

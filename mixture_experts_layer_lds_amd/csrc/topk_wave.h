@@ -14,19 +14,20 @@ __device__ __forceinline__ float dec_key_value(uint32_t k) {
   return __uint_as_float((k & 0x80000000u) ? (k & 0x7fffffffu) : ~k);
 }
 
-// The K largest of E logits (E <= 1024): lane k receives the k-th expert and its logit.
-__device__ __forceinline__ void wave_select(const float* logits, int E, int K, int& my_e, float& my_v) {
+// The K largest of E <= 64 EJ logits, logit(e) each: lane k receives the k-th expert and its logit.
+template <int EJ, class Logit>
+__device__ __forceinline__ void wave_select(Logit logit, int E, int K, int& my_e, float& my_v) {
   const int lane = threadIdx.x & 63;
   // lane i holds the order keys of experts i + 64 j (E <= 1024); each round takes the largest
   // key still in play (a DPP wave maximum) and, among the experts holding it, the lowest id
   // (ballots in ascending e): logit descending, then expert id ascending
   const int ej = (E + 63) >> 6;
-  uint32_t key[16];
+  uint32_t key[EJ];
   uint32_t alive = 0;
 #pragma unroll
-  for (int j = 0; j < 16; ++j) {
+  for (int j = 0; j < EJ; ++j) {
     const int e = lane + 64 * j;
-    key[j] = e < E ? dec_order_key(logits[e]) : 0u;
+    key[j] = e < E ? dec_order_key(logit(e)) : 0u;
     alive |= e < E ? (1u << j) : 0u;
   }
   my_e = 0;
@@ -34,12 +35,12 @@ __device__ __forceinline__ void wave_select(const float* logits, int E, int K, i
   for (int k = 0; k < K; ++k) {
     uint32_t lm = 0;  // NaN keys are 0 too; ties at 0 are settled among live candidates
 #pragma unroll
-    for (int j = 0; j < 16; ++j)
+    for (int j = 0; j < EJ; ++j)
       if (j < ej && ((alive >> j) & 1u)) lm = key[j] > lm ? key[j] : lm;
     const uint32_t kmax = wave_max_u32(lm);
     int win = -1;
 #pragma unroll
-    for (int j = 0; j < 16; ++j) {
+    for (int j = 0; j < EJ; ++j) {
       if (j >= ej) break;
       const uint64_t m = __builtin_amdgcn_ballot_w64(((alive >> j) & 1u) && key[j] == kmax);
       if (win < 0 && m != 0ull) win = 64 * j + (int)__builtin_ctzll(m);

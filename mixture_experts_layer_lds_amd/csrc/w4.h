@@ -186,11 +186,16 @@ struct W4Stream {
   // Blocks [a, b) of the row's w4_blocks(K); the last one may be a part.  Batches of U blocks, the next
   // batch's loads issued before the current one's products; blocks past the last whole one repeat it and
   // are not used.
-  __device__ __forceinline__ void run(int a, int b, f32x4 (&acc)[RT][NG]) const {
+  // ready() is called once, when the first codes have been requested: what it does to the tokens' place in LDS
+  // costs no time of its own.
+  template <class Ready>
+  __device__ __forceinline__ void run(int a, int b, f32x4 (&acc)[RT][NG], Ready ready) const {
     const int whole = min(b, K / W4_BLOCK);
+    if (a >= whole) ready();
     if (a < whole) {
       Batch t0, t1;
       load(t0, a, whole - 1);
+      ready();
       int st = a;
       for (; st + 2 * U < whole; st += 2 * U) {  // steady state: both batches whole
         load(t1, st + U, whole - 1);
@@ -214,6 +219,7 @@ struct W4Stream {
         for (int g = 0; g < NG; ++g) acc[r][g] *= 16.0f;  // codes went in as c / 16
     }
   }
+  __device__ __forceinline__ void run(int a, int b, f32x4 (&acc)[RT][NG]) const { run(a, b, acc, [] {}); }
   // the part of a last block: K - 128 blk = 32, 64 or 96 elements
   __device__ __forceinline__ void tail(int blk, f32x4 (&acc)[RT][NG]) const {
     const int q = (threadIdx.x & 63) >> 4, left = K - blk * W4_BLOCK;
@@ -233,14 +239,33 @@ struct W4Stream {
 };
 
 // Copies elements [k0, k1) (multiples of 32) of a token to LDS, for the calling wave's own use: INT in the
-// order of the codes.
-template <int FMT>
-__device__ __forceinline__ void w4_stage(const bf16* x, bf16* lds, int k0, int k1) {
-  for (int k = k0 + (threadIdx.x & 63) * 8; k < k1; k += 64 * 8) {
-    const u32x4 v = ld16(x + k);
-    st16(lds + k, FMT == W4_INT ? w4_order_int(v) : v);
+// order of the codes.  The first 64 x 8 R elements pass through registers, so that other loads can be
+// issued between request() and write().
+template <int FMT, int R>
+struct W4Stage {
+  u32x4 v[R];
+  const bf16* x;
+  bf16* lds;
+  int k0, k1;
+  __device__ __forceinline__ void request(const bf16* x_, bf16* lds_, int a, int b) {
+    x = x_;
+    lds = lds_;
+    k0 = a + (threadIdx.x & 63) * 8;
+    k1 = b;
+#pragma unroll
+    for (int i = 0; i < R; ++i)
+      if (k0 + 512 * i < k1) v[i] = ld16(x + k0 + 512 * i);
   }
-}
+  __device__ __forceinline__ void write() const {
+#pragma unroll
+    for (int i = 0; i < R; ++i)
+      if (k0 + 512 * i < k1) st16(lds + k0 + 512 * i, FMT == W4_INT ? w4_order_int(v[i]) : v[i]);
+    for (int k = k0 + 512 * R; k < k1; k += 512) {
+      const u32x4 u = ld16(x + k);
+      st16(lds + k, FMT == W4_INT ? w4_order_int(u) : u);
+    }
+  }
+};
 
 // A wave's results of one tile and token group to LDS as [token][16 rows] floats: 16 tokens, or 4 with NI = 1.
 template <int NI> constexpr int w4_tokens() { return NI == 1 ? 4 : 16; }

@@ -56,37 +56,31 @@ __global__ __launch_bounds__(256) void k_quant_w4(const T* __restrict__ src, int
   }
 }
 
-// ---- expansion: a thread takes 32 codes ----
+// ---- expansion: a thread takes 8 codes of a word, so that a wave writes whole lines ----
 template <typename T, int FMT>
 __global__ __launch_bounds__(256) void k_expand_w4(const uint8_t* __restrict__ codes, const void* __restrict__ scales, int64_t rows,
                                                    int K, int group, T* __restrict__ out) {
-  const int nb = K / 32;
-  const int64_t items = rows * nb;
-  for (int64_t it = (int64_t)blockIdx.x * 256 + threadIdx.x; it < items; it += (int64_t)gridDim.x * 256) {
-    const int64_t row = it / nb;
-    const int b = (int)(it - row * nb);
-    const u32x4 w = ld16_nt(codes + row * (K / 2) + b * 16);
-    float s = 0.0f;
-    int e = 0;
-    if constexpr (FMT == W4_INT) s = (float)static_cast<const bf16*>(scales)[(int64_t)(b * 32 / group) * rows + row];
-    else e = static_cast<const uint8_t*>(scales)[((int64_t)(b >> 2) * rows + row) * 4 + (b & 3)];
+  const int words = K / 8;  // of a row
+  for (int64_t row = blockIdx.y; row < rows; row += gridDim.y) {
+    const int i = blockIdx.x * 256 + threadIdx.x;
+    if (i >= words) return;
+    const uint32_t w = __builtin_nontemporal_load(reinterpret_cast<const uint32_t*>(codes + row * (K / 2)) + i);
+    float f[8];
+    if constexpr (FMT == W4_INT) {
+      const float s = (float)static_cast<const bf16*>(scales)[(int64_t)(i * 8 / group) * rows + row];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      float f[8];
+      for (int k = 0; k < 8; ++k) f[k] = (float)((int)(w >> (4 * k) & 15) - 8) * s;
+    } else {
+      const int e = static_cast<const uint8_t*>(scales)[((int64_t)(i >> 4) * rows + row) * 4 + ((i >> 2) & 3)];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const int c = (int)(w[j] >> (4 * i)) & 15;
-        if constexpr (FMT == W4_INT) {
-          f[i] = (float)(c - 8) * s;
-        } else {
-          // twice the magnitude: 0 1 2 3 4 6 8 12
-          const int m = c & 7, t = m < 4 ? m : (2 + (m & 1)) << ((m >> 1) - 1);
-          f[i] = ldexpf((float)(c & 8 ? -t : t), e - 128);
-        }
+      for (int k = 0; k < 8; ++k) {
+        // twice the magnitude: 0 1 2 3 4 6 8 12
+        const int c = (int)(w >> (4 * k)) & 15, m = c & 7, t = m < 4 ? m : (2 + (m & 1)) << ((m >> 1) - 1);
+        f[k] = ldexpf((float)(c & 8 ? -t : t), e - 128);
       }
-#pragma unroll
-      for (int u = 0; u < 8; u += Vec<T>::N) st16(out + row * K + b * 32 + j * 8 + u, pack16<T>(f + u));
     }
+#pragma unroll
+    for (int u = 0; u < 8; u += Vec<T>::N) st16(out + row * K + i * 8 + u, pack16<T>(f + u));
   }
 }
 
@@ -136,14 +130,24 @@ __global__ __launch_bounds__(512) void k_w4_rows(const bf16* __restrict__ X, int
     const int t = min(t0 + g * TOK + w4_token<NI>(), m - 1);
     ws.x[g] = (XLDS ? xl + t * xp : X + (int64_t)t * ldx) + Stream::XQ * q;
   }
-  if constexpr (XLDS)
-    for (int t = 0; t < m; ++t) w4_stage<FMT>(X + t * ldx, xl + t * xp, a * W4_BLOCK, min(b * W4_BLOCK, K));
+  W4Stage<FMT, 2> first;
+  if constexpr (XLDS) first.request(X, xl, a * W4_BLOCK, min(b * W4_BLOCK, K));
   f32x4 acc[RT][NG];
 #pragma unroll
   for (int r = 0; r < RT; ++r)
 #pragma unroll
     for (int g = 0; g < NG; ++g) acc[r][g] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-  if (a < b) ws.run(a, b, acc);
+  if (a < b)
+    ws.run(a, b, acc, [&] {
+      if constexpr (XLDS) {
+        first.write();
+        for (int t = 1; t < m; ++t) {
+          W4Stage<FMT, 1> s;
+          s.request(X + t * ldx, xl + t * xp, a * W4_BLOCK, min(b * W4_BLOCK, K));
+          s.write();
+        }
+      }
+    });
   if constexpr (XLDS) __syncthreads();  // (the results take the tokens' place)
   float* res = reinterpret_cast<float*>(w4_lds);
   constexpr int TILE = TOK * 16;
@@ -296,8 +300,7 @@ hipError_t launch_quant_w4(const void* src, bool is_bf16, int format, int group,
 
 hipError_t launch_expand_w4(const W4View& w, int64_t rows, int64_t K, bool is_bf16, void* out, hipStream_t st) {
   if (rows <= 0) return hipSuccess;
-  const int64_t need = cdiv(rows * (K / 32), 256);
-  const int grid = (int)(need < (1 << 20) ? need : 1 << 20);
+  const dim3 grid((unsigned)cdiv(K / 8, 256), (unsigned)(rows < 32768 ? rows : 32768));
   const int k = (int)K;
   if (is_bf16) {
     bf16* o = static_cast<bf16*>(out);
