@@ -14,6 +14,8 @@
 // By experts (more tokens): five launches.  1. router logits, which also clear the experts' counters; 2. top-K,
 // each pair appended to its expert's list (the order inside a list reaches no value); 3. gate/up and
 // 4. down on groups of 16 of an expert's tokens; 5. combine in ascending expert order.
+#include <cmath>
+
 #include "internal.h"
 #include "skinny.h"
 #include "topk_wave.h"
@@ -125,11 +127,12 @@ __device__ __forceinline__ int dw_choose(const DecW4& a, int t, int K) {
   return dw_choose_ej<16, WRITE>(a, t, K);
 }
 
-// The ranks of a token's choices by expert id: order[r] is the choice of the r-th smallest expert.
-__device__ __forceinline__ void dw_order(const int32_t* idx, int K, int (&order)[16]) {
+// The ranks of a token's choices by expert id: order[r] is the choice of the r-th smallest expert.  mine: lane
+// k holds the k-th choice.
+__device__ __forceinline__ void dw_order(int mine, int K, int (&order)[16]) {
   int ids[16];
 #pragma unroll
-  for (int k = 0; k < 16; ++k) ids[k] = k < K ? __builtin_amdgcn_readfirstlane(idx[k]) : 0x7fffffff;
+  for (int k = 0; k < 16; ++k) ids[k] = k < K ? __builtin_amdgcn_readlane(mine, k) : 0x7fffffff;
   int prev = -1;
 #pragma unroll
   for (int r = 0; r < 16; ++r) {
@@ -151,7 +154,7 @@ template <int FMT, int G, bool XLDS>
 __global__ __launch_bounds__(256) void k_dw4_up_pair(DecW4 a) {
   extern __shared__ __attribute__((aligned(16))) char dw_lds[];
   __shared__ int chosen;
-  typedef W4Stream<FMT, G, 1, 2, 1, XLDS, FMT == W4_INT && G < 128 ? 1 : 2> Stream;
+  typedef W4Stream<FMT, G, 1, 2, 1, XLDS, 1> Stream;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), W_ = blockDim.x >> 6;
   const int lane = threadIdx.x & 63, r16 = lane & 15, q = lane >> 4;
   const int pair = blockIdx.y, t = pair / a.K, k = pair - t * a.K, j0 = blockIdx.x * 16;
@@ -199,18 +202,19 @@ __global__ __launch_bounds__(256) void k_dw4_up_pair(DecW4 a) {
 template <int FMT, int G, bool XLDS>
 __global__ __launch_bounds__(1024) void k_dw4_down_pair(DecW4 a, int splits) {
   extern __shared__ __attribute__((aligned(16))) char dw_lds[];
-  typedef W4Stream<FMT, G, 1, 1, 1, XLDS, FMT == W4_INT && G < 128 ? 1 : 2> Stream;
+  typedef W4Stream<FMT, G, 1, 1, 1, XLDS, 1> Stream;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int lane = threadIdx.x & 63, r16 = lane & 15, q = lane >> 4;
   const int t = blockIdx.y, c0 = blockIdx.x * 16, k = wave / splits, part = wave - k * splits;
-  const int32_t* idx = a.topk_idx + (int64_t)t * a.K;
-  const int e = idx[k];
+  const int64_t choice = (int64_t)t * a.K + min(lane, a.K - 1);
+  const int ids = a.topk_idx[choice];
+  const float weights = a.topk_w[choice];
   const bf16* x = a.act + ((int64_t)t * a.K + k) * a.n;
   bf16* xl = reinterpret_cast<bf16*>(dw_lds) + (int64_t)k * a.n;
   const int nb = w4_blocks(a.n), b0 = nb * part / splits, b1 = nb * (part + 1) / splits;
   W4Stage<FMT, 4> stage;
   if constexpr (XLDS) stage.request(x, xl, b0 * W4_BLOCK, min(b1 * W4_BLOCK, a.n));
-  const int64_t row = (int64_t)__builtin_amdgcn_readfirstlane(e) * a.d + c0 + r16;
+  const int64_t row = (int64_t)__builtin_amdgcn_readlane(ids, k) * a.d + c0 + r16;
   Stream ws;
   ws.w[0] = a.down + row * (a.n / 2) + 16 * q;
   ws.s[0] = a.s_down + (FMT == W4_INT ? row * 2 : row * 4 + q);
@@ -226,18 +230,18 @@ __global__ __launch_bounds__(1024) void k_dw4_down_pair(DecW4 a, int splits) {
   float* res = reinterpret_cast<float*>(dw_lds);  // [wave][16]
   if (q == 0) res[wave * 16 + r16] = acc[0][0][0];
   __syncthreads();
-  if (threadIdx.x < 16) {
+  if (wave == 0) {
     int order[16];
-    dw_order(idx, a.K, order);
+    dw_order(ids, a.K, order);
     float o = 0.0f;
 #pragma unroll
     for (int r = 0; r < 16; ++r)
       if (r < a.K) {
         float y = 0.0f;
-        for (int s = 0; s < splits; ++s) y += res[(order[r] * splits + s) * 16 + threadIdx.x];
-        o = fmaf(a.topk_w[(int64_t)t * a.K + order[r]], y, o);
+        for (int s = 0; s < splits; ++s) y += res[(order[r] * splits + s) * 16 + r16];
+        o = fmaf(__uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(weights), order[r])), y, o);
       }
-    a.out[(int64_t)t * a.d + c0 + threadIdx.x] = from_f32<bf16>(o);
+    if (lane < 16) a.out[(int64_t)t * a.d + c0 + lane] = from_f32<bf16>(o);
   }
 }
 
@@ -249,26 +253,27 @@ __global__ __launch_bounds__(256) void k_dw4_topk(DecW4 a) {
   if (lane < a.K) a.list[(int64_t)e * a.T + atomicAdd(&a.cnt[e], 1)] = t * a.K + lane;  // (a token picks an expert at most once)
 }
 
-// A tile of an expert against groups of 16 of its tokens, the waves sharing the reduction.  UP: 16 gate rows
-// and their up rows -> act; else 32 rows of W_down -> y.
+// A tile of an expert against groups of 16 of its tokens, the waves sharing the reduction.  UP: 8 RT gate rows
+// and their up rows -> act; else 16 RT rows of W_down -> y.
+constexpr int DW_RT = 4, DW_EXPERT_WAVES = 4;
 template <int FMT, int G, bool UP>
 __global__ __launch_bounds__(512) void k_dw4_expert(DecW4 a) {
   extern __shared__ __attribute__((aligned(16))) char dw_lds[];
-  constexpr int RT = 2, TILE = 256;
+  constexpr int RT = DW_RT, H = RT / 2, TILE = 256;
   typedef W4Stream<FMT, G, 1, RT, 4, false, 1> Stream;
   const int e = blockIdx.y, c = __builtin_amdgcn_readfirstlane(a.cnt[e]);
   if (c == 0) return;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), W_ = blockDim.x >> 6;
   const int lane = threadIdx.x & 63, r16 = lane & 15, q = lane >> 4;
-  const int rows = UP ? a.n : a.d, K = UP ? a.d : a.n;  // of an expert
-  const int c0 = blockIdx.x * (UP ? 16 : 32);
+  const int rows = UP ? a.n : a.d, K = UP ? a.d : a.n;  // of an expert; multiples of 64, as the tiles' columns divide
+  const int c0 = blockIdx.x * (UP ? 16 * H : 16 * RT);
   const int32_t* lst = a.list + (int64_t)e * a.T;
   Stream ws;
 #pragma unroll
   for (int r = 0; r < RT; ++r) {
-    const int64_t row = (int64_t)e * rows + c0 + r16 + (UP ? 0 : 16 * r);  // (n and d are multiples of 64)
-    const uint8_t* w = UP ? (r == 0 ? a.gate : a.up) : a.down;
-    const uint8_t* s = UP ? (r == 0 ? a.s_gate : a.s_up) : a.s_down;
+    const int64_t row = (int64_t)e * rows + c0 + 16 * (UP ? r % H : r) + r16;
+    const uint8_t* w = UP ? (r < H ? a.gate : a.up) : a.down;
+    const uint8_t* s = UP ? (r < H ? a.s_gate : a.s_up) : a.s_down;
     ws.w[r] = w + row * (K / 2) + 16 * q;
     ws.s[r] = s + (FMT == W4_INT ? row * 2 : row * 4 + q);
   }
@@ -279,7 +284,9 @@ __global__ __launch_bounds__(512) void k_dw4_expert(DecW4 a) {
   for (int g0 = 0; g0 < c; g0 += 16) {
     const int pair = lst[min(g0 + r16, c - 1)];
     ws.x[0] = (UP ? a.X + (int64_t)(pair / a.K) * a.d : a.act + (int64_t)pair * a.n) + Stream::XQ * q;
-    f32x4 acc[RT][1] = {{{0.0f, 0.0f, 0.0f, 0.0f}}, {{0.0f, 0.0f, 0.0f, 0.0f}}};
+    f32x4 acc[RT][1];
+#pragma unroll
+    for (int r = 0; r < RT; ++r) acc[r][0] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
     if (b0 < b1) ws.run(b0, b1, acc);
     __syncthreads();  // (the last group's results have been read)
 #pragma unroll
@@ -291,19 +298,19 @@ __global__ __launch_bounds__(512) void k_dw4_expert(DecW4 a) {
       for (int w = 1; w < W_; ++w) v += *reinterpret_cast<const f32x4*>(p + w * RT * TILE);
       return v;
     };
-    constexpr int QUADS = UP ? 4 : 8;
+    constexpr int QUADS = UP ? 4 * H : 4 * RT;  // of a token's columns
     for (int it = threadIdx.x; it < 16 * QUADS; it += blockDim.x) {
-      const int quad = it % QUADS, tok = it / QUADS, col = c0 + 4 * quad;
+      const int quad = it % QUADS, tok = it / QUADS, col = c0 + 4 * quad, r = quad >> 2, at = tok * 16 + 4 * (quad & 3);
       if (g0 + tok >= c) continue;
       const int64_t to = lst[g0 + tok];
       if constexpr (UP) {
-        const f32x4 g = total(0, tok * 16 + 4 * quad), u = total(1, tok * 16 + 4 * quad);
+        const f32x4 g = total(r, at), u = total(r + H, at);
         f32x4 h;
 #pragma unroll
         for (int i = 0; i < 4; ++i) h[i] = g[i] * sigmoid_f32(g[i]) * u[i];
         dec_store4<bf16>(a.act + to * a.n + col, h);
       } else {
-        *reinterpret_cast<f32x4*>(a.y + to * a.d + col) = total(quad >> 2, tok * 16 + 4 * (quad & 3));
+        *reinterpret_cast<f32x4*>(a.y + to * a.d + col) = total(r, at);
       }
     }
   }
@@ -312,7 +319,7 @@ __global__ __launch_bounds__(512) void k_dw4_expert(DecW4 a) {
 __global__ __launch_bounds__(256) void k_dw4_combine(DecW4 a) {
   const int t = blockIdx.y, c = (blockIdx.x * 256 + threadIdx.x) * 4;
   int order[16];
-  dw_order(a.topk_idx + (int64_t)t * a.K, a.K, order);
+  dw_order(a.topk_idx[(int64_t)t * a.K + min((int)threadIdx.x & 63, a.K - 1)], a.K, order);
   if (c >= a.d) return;
   f32x4 yv[16];
   float wv[16];
@@ -332,12 +339,20 @@ __global__ __launch_bounds__(256) void k_dw4_combine(DecW4 a) {
 
 constexpr int64_t DW_LDS = 65536;
 
-// Whether the call goes by pairs.
-static bool dw4_pairs(int64_t T, int E, int K) { return T == 1 || T * K * 2 <= E; }
+// Whether the call goes by pairs: that saves two launches, and reads an expert again for every further pair
+// that chose it (from the caches, mostly).  Where half as many pairs as experts at most are routed both take
+// the same (d = 7168, n = 2048, E = 64, T = 4: 164 and 167 us), beyond that the expected repeated bytes decide: d =
+// 1536, n = 256, E = 128, K = 8 takes 28 and 35 us at T = 9, 40 and 43 at 16 (28 MB), 55 and 47 at 24 (54 MB); d =
+// 7168, n = 2048, E = 64 309 and 228 at T = 8 (520 MB).
+static bool dw4_pairs(const Shape& s) {
+  const double P = (double)s.T * s.K, E = s.E;
+  if (P > 1024) return false;
+  const double again = P - E * (1.0 - pow(1.0 - 1.0 / E, P));
+  return s.T == 1 || 2 * P <= E || again * 1.5 * (double)s.n * (double)s.d <= 28e6;
+}
 
 template <int FMT, int G>
-static hipError_t dw4_run(const DecW4& a, hipStream_t st) {
-  const bool pairs = dw4_pairs(a.T, a.E, a.K);
+static hipError_t dw4_run(const DecW4& a, bool pairs, hipStream_t st) {
   const dim3 lg((unsigned)cdiv(a.E, 16), (unsigned)cdiv(a.T, 16 * DW_NG), (unsigned)a.slices);
   k_dw4_logits<<<lg, DW_LOGIT_WAVES * 64, 0, st>>>(a, !pairs);
   hipError_t e = hipGetLastError();
@@ -366,15 +381,15 @@ static hipError_t dw4_run(const DecW4& a, hipStream_t st) {
   e = hipGetLastError();
   if (e != hipSuccess) return e;
   auto waves_of = [](int K) {
-    int w = 8;
+    int w = DW_EXPERT_WAVES;
     while (w > 1 && w4_blocks(K) / w < 2) w /= 2;
     return w;
   };
-  const int wu = waves_of(a.d), wd = waves_of(a.n);
-  k_dw4_expert<FMT, G, true><<<dim3((unsigned)(a.n / 16), (unsigned)a.E), wu * 64, wu * 2048, st>>>(a);
+  const int wu = waves_of(a.d), wd = waves_of(a.n), lds = DW_RT * 1024;  // per wave
+  k_dw4_expert<FMT, G, true><<<dim3((unsigned)(a.n / (8 * DW_RT)), (unsigned)a.E), wu * 64, wu * lds, st>>>(a);
   e = hipGetLastError();
   if (e != hipSuccess) return e;
-  k_dw4_expert<FMT, G, false><<<dim3((unsigned)(a.d / 32), (unsigned)a.E), wd * 64, wd * 2048, st>>>(a);
+  k_dw4_expert<FMT, G, false><<<dim3((unsigned)(a.d / (16 * DW_RT)), (unsigned)a.E), wd * 64, wd * lds, st>>>(a);
   e = hipGetLastError();
   if (e != hipSuccess) return e;
   k_dw4_combine<<<dim3((unsigned)cdiv(a.d, 1024), (unsigned)a.T), 256, 0, st>>>(a);
@@ -410,14 +425,15 @@ hipError_t launch_decode_w4(const Shape& s, const void* X, const void* W_r, cons
   a.y = reinterpret_cast<float*>(w);
   // slices of the logits lie where y will be written, by pairs over the unused lists too; each has at least 8
   // steps of the reduction
-  a.part = dw4_pairs(s.T, s.E, s.K) ? reinterpret_cast<float*>(a.list) : a.y;
-  const int64_t room = (int64_t)s.K * s.d + (dw4_pairs(s.T, s.E, s.K) ? s.E : 0);  // floats per token
+  const bool pairs = dw4_pairs(s);
+  a.part = pairs ? reinterpret_cast<float*>(a.list) : a.y;
+  const int64_t room = (int64_t)s.K * s.d + (pairs ? s.E : 0);  // floats per token
   a.slices = 1;
   while (a.slices < DW_SLICES && s.d / 32 / (a.slices * 2) >= 8 && (int64_t)s.E * a.slices * 2 <= room) a.slices *= 2;
-  if (W_gate.format == W4_FP) return dw4_run<W4_FP, 32>(a, st);
-  if (W_gate.group == 32) return dw4_run<W4_INT, 32>(a, st);
-  if (W_gate.group == 64) return dw4_run<W4_INT, 64>(a, st);
-  return dw4_run<W4_INT, 128>(a, st);
+  if (W_gate.format == W4_FP) return dw4_run<W4_FP, 32>(a, pairs, st);
+  if (W_gate.group == 32) return dw4_run<W4_INT, 32>(a, pairs, st);
+  if (W_gate.group == 64) return dw4_run<W4_INT, 64>(a, pairs, st);
+  return dw4_run<W4_INT, 128>(a, pairs, st);
 }
 
 }  // namespace moe

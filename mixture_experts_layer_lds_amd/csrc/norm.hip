@@ -13,45 +13,67 @@
 
 namespace moe {
 
+// How rows are accessed: element by element; in 16-byte accesses with a part of a chunk at the end; in 16-byte
+// accesses throughout.
+enum { NORM_ANY = 0, NORM_PART = 1, NORM_WHOLE = 2 };
+
 // Element i of a thread's chunk j lies in column norm_col(j, i): 8 neighbours per chunk where rows are
 // 16-byte aligned, else neighbours in neighbouring threads, which keeps 2- and 4-byte accesses coalesced.
-template <bool ALIGNED>
+template <int MODE>
 __device__ __forceinline__ int norm_col(int j, int i, int tpr, int t) {
-  return ALIGNED ? (j * tpr + t) * 8 + i : (j * 8 + i) * tpr + t;
+  return MODE != NORM_ANY ? (j * tpr + t) * 8 + i : (j * 8 + i) * tpr + t;
 }
 
 // 8 elements as they lie in memory.
 template <typename T> struct Raw8 { u32x4 v[8 / Vec<T>::N]; };
 
-template <typename T, int NC, bool ALIGNED>
-__device__ __forceinline__ void norm_load(const T* p, int cols, int tpr, int t, Raw8<T> (&r)[NC]) {
+// Columns behind the row hold zeros.
+template <typename T, int MODE>
+__device__ __forceinline__ Raw8<T> norm_load1(const T* p, int cols, int tpr, int t, int j) {
+  constexpr int NV = 8 / Vec<T>::N;
+  const int c = norm_col<MODE>(j, 0, tpr, t);
+  Raw8<T> r;
+  if constexpr (MODE == NORM_WHOLE) {
 #pragma unroll
-  for (int j = 0; j < NC; ++j) {
-    const int c = norm_col<ALIGNED>(j, 0, tpr, t);
-    if (ALIGNED && c + 8 <= cols) {
+    for (int v = 0; v < NV; ++v) r.v[v] = u32x4{0u, 0u, 0u, 0u};
+    if (c < cols) {
 #pragma unroll
-      for (int v = 0; v < 8 / Vec<T>::N; ++v) r[j].v[v] = ld16_nt(p + c + v * Vec<T>::N);
-    } else {
-      float f[8];
+      for (int v = 0; v < NV; ++v) r.v[v] = ld16_nt(p + c + v * Vec<T>::N);
+    }
+    return r;
+  }
+  if (MODE == NORM_PART && c + 8 <= cols) {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const int ci = norm_col<ALIGNED>(j, i, tpr, t);
-        f[i] = ci < cols ? to_f32(p[ci]) : 0.0f;
-      }
+    for (int v = 0; v < NV; ++v) r.v[v] = ld16_nt(p + c + v * Vec<T>::N);
+    return r;
+  }
+  float f[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+  if (c < cols) {
 #pragma unroll
-      for (int v = 0; v < 8 / Vec<T>::N; ++v) r[j].v[v] = pack16<T>(f + v * Vec<T>::N);
+    for (int i = 0; i < 8; ++i) {
+      const int ci = norm_col<MODE>(j, i, tpr, t);
+      if (ci < cols) f[i] = to_f32(p[ci]);
     }
   }
+#pragma unroll
+  for (int v = 0; v < NV; ++v) r.v[v] = pack16<T>(f + v * Vec<T>::N);
+  return r;
+}
+template <typename T, int NC, int MODE>
+__device__ __forceinline__ void norm_load(const T* p, int cols, int tpr, int t, Raw8<T> (&r)[NC]) {
+#pragma unroll
+  for (int j = 0; j < NC; ++j) r[j] = norm_load1<T, MODE>(p, cols, tpr, t, j);
 }
 template <typename T>
 __device__ __forceinline__ void norm_unpack(const Raw8<T>& r, float* f) {
 #pragma unroll
   for (int v = 0; v < 8 / Vec<T>::N; ++v) unpack16<T>(r.v[v], f + v * Vec<T>::N);
 }
-template <typename T, bool ALIGNED>
+template <typename T, int MODE>
 __device__ __forceinline__ void norm_store(T* p, int cols, int tpr, int t, int j, const Raw8<T>& r) {
-  const int c = norm_col<ALIGNED>(j, 0, tpr, t);
-  if (ALIGNED && c + 8 <= cols) {
+  const int c = norm_col<MODE>(j, 0, tpr, t);
+  if (c >= cols) return;
+  if (MODE == NORM_WHOLE || (MODE == NORM_PART && c + 8 <= cols)) {
 #pragma unroll
     for (int v = 0; v < 8 / Vec<T>::N; ++v) st16_nt(p + c + v * Vec<T>::N, r.v[v]);
   } else {
@@ -59,7 +81,7 @@ __device__ __forceinline__ void norm_store(T* p, int cols, int tpr, int t, int j
     norm_unpack<T>(r, f);
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      const int ci = norm_col<ALIGNED>(j, i, tpr, t);
+      const int ci = norm_col<MODE>(j, i, tpr, t);
       if (ci < cols) p[ci] = from_f32<T>(f[i]);
     }
   }
@@ -72,32 +94,58 @@ __device__ __forceinline__ Raw8<T> norm_pack(const float* f) {
   return r;
 }
 
-// Weight or bias of a thread's columns (null: the value `none`).
-template <int NC, bool ALIGNED>
-__device__ __forceinline__ void norm_vector(const void* p, bool wbf16, float none, int cols, int tpr, int t, float (&w)[NC * 8]) {
+// Weight or bias of a thread's chunk j (null: the value `none`).
+template <int MODE>
+__device__ __forceinline__ void norm_vector(const void* p, bool wbf16, float none, int cols, int tpr, int t, int j, float* w) {
+  const int c0 = norm_col<MODE>(j, 0, tpr, t);
 #pragma unroll
-  for (int j = 0; j < NC; ++j)
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const int c = norm_col<ALIGNED>(j, i, tpr, t);
-      float v = none;
-      if (p && c < cols) v = wbf16 ? to_f32(static_cast<const bf16*>(p)[c]) : static_cast<const float*>(p)[c];
-      w[j * 8 + i] = v;
+  for (int i = 0; i < 8; ++i) w[i] = none;
+  if (!p || c0 >= cols) return;
+  if (MODE != NORM_ANY && c0 + 8 <= cols) {
+    if (wbf16) {
+      unpack16<bf16>(ld16(static_cast<const bf16*>(p) + c0), w);
+    } else {
+      unpack16<float>(ld16(static_cast<const float*>(p) + c0), w);
+      unpack16<float>(ld16(static_cast<const float*>(p) + c0 + 4), w + 4);
     }
+    return;
+  }
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const int c = norm_col<MODE>(j, i, tpr, t);
+    if (c < cols) w[i] = wbf16 ? to_f32(static_cast<const bf16*>(p)[c]) : static_cast<const float*>(p)[c];
+  }
 }
 
-// Sums of a row's values over its threads, in every one of them: shuffles inside a wave, then (tpr > 64:
+// Sum of v over groups of `tpr` neighbouring lanes (a power of two, 8 .. 64), in every lane: mirrored and
+// swapped lanes, no trip through LDS.
+template <int CTRL> __device__ __forceinline__ float norm_dpp(float v) {
+  return v + __uint_as_float(dpp_src<CTRL, 0xf, 0xf>(__float_as_uint(v)));
+}
+__device__ __forceinline__ float norm_lane_sum(float v, int tpr) {
+  v = norm_dpp<0xb1>(v);   // quad_perm 1 0 3 2
+  v = norm_dpp<0x4e>(v);   // quad_perm 2 3 0 1
+  v = norm_dpp<0x141>(v);  // row_half_mirror
+  if (tpr >= 16) v = norm_dpp<0x140>(v);  // row_mirror
+  if (tpr >= 32) {
+    auto s = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+    v = __uint_as_float(s[0]) + __uint_as_float(s[1]);
+  }
+  if (tpr >= 64) {
+    auto s = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+    v = __uint_as_float(s[0]) + __uint_as_float(s[1]);
+  }
+  return v;
+}
+
+// Sums of a row's values over its threads, in every one of them: inside a wave, then (tpr > 64:
 // the row's threads are the workgroup) the waves' sums through LDS in wave order.  The two halves of `red`
 // alternate, so that a reduction writes what no wave still reads: between its write and the last read of
 // the same half lies the other half's barrier.
 template <int N>
 __device__ __forceinline__ void norm_row_sum(float (&v)[N], int tpr, float (*red)[N][16], int& half) {
 #pragma unroll
-  for (int o = 32; o > 0; o >>= 1)
-    if (o < tpr) {
-#pragma unroll
-      for (int k = 0; k < N; ++k) v[k] += __shfl_xor(v[k], o, WAVE);
-    }
+  for (int k = 0; k < N; ++k) v[k] = norm_lane_sum(v[k], tpr);
   if (tpr <= WAVE) return;
   const int waves = tpr >> 6;
   if ((threadIdx.x & 63) == 0) {
@@ -124,37 +172,48 @@ struct NormFwd {
   bool wbf16, rms;
 };
 
-template <typename T, int NC, bool ALIGNED, int THREADS>
+template <typename T, int NC, int MODE, int THREADS>
 __global__ __launch_bounds__(THREADS) void k_norm(NormFwd a) {
   __shared__ float red[2][1][16];
   const int tpr = a.tpr, t = threadIdx.x & (tpr - 1), rpb = blockDim.x / tpr, cols = a.cols;
   const float inv = 1.0f / (float)cols;
+  const bool res = a.res != nullptr;
   int half = 0;
+  const int64_t step = (int64_t)gridDim.x * rpb;
+  int64_t row = (int64_t)blockIdx.x * rpb + threadIdx.x / tpr;
+  constexpr bool AHEAD = THREADS < 1024 || NC == 1;  // (128 registers do not hold the next row too)
+  Raw8<T> raw[NC], rr[NC];
+  auto load = [&](int64_t r) {
+    if (r >= a.rows) return;
+    norm_load<T, NC, MODE>(static_cast<const T*>(a.x) + r * a.ldx, cols, tpr, t, raw);
+    if (res) norm_load<T, NC, MODE>(static_cast<const T*>(a.res) + r * a.ldr, cols, tpr, t, rr);
+  };
+  if constexpr (AHEAD) load(row);
   float w[NC * 8], b[NC * 8];
-  norm_vector<NC, ALIGNED>(a.w, a.wbf16, 1.0f, cols, tpr, t, w);
-  norm_vector<NC, ALIGNED>(a.b, a.wbf16, 0.0f, cols, tpr, t, b);
+#pragma unroll
+  for (int j = 0; j < NC; ++j) {
+    norm_vector<MODE>(a.w, a.wbf16, 1.0f, cols, tpr, t, j, w + j * 8);
+    norm_vector<MODE>(a.b, a.wbf16, 0.0f, cols, tpr, t, j, b + j * 8);
+  }
   // (with tpr > 64 a row is the workgroup's, so the barriers inside are reached by all of it; with several
   // rows a workgroup there are none)
-  for (int64_t row = (int64_t)blockIdx.x * rpb + threadIdx.x / tpr; row < a.rows; row += (int64_t)gridDim.x * rpb) {
-    Raw8<T> raw[NC];
-    norm_load<T, NC, ALIGNED>(static_cast<const T*>(a.x) + row * a.ldx, cols, tpr, t, raw);
+  for (; row < a.rows; row += step) {
+    if constexpr (!AHEAD) load(row);
     float f[NC * 8];
-    if (a.res) {
-      Raw8<T> rr[NC];
-      norm_load<T, NC, ALIGNED>(static_cast<const T*>(a.res) + row * a.ldr, cols, tpr, t, rr);
 #pragma unroll
-      for (int j = 0; j < NC; ++j) {
-        float u[8], v[8];
-        norm_unpack<T>(raw[j], u);
+    for (int j = 0; j < NC; ++j) {
+      norm_unpack<T>(raw[j], f + j * 8);
+      if (res) {
+        float v[8];
         norm_unpack<T>(rr[j], v);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) u[i] += v[i];
-        raw[j] = norm_pack<T>(u);  // what is normalised is the rounded sum, which the backward reads
-        if (a.sum) norm_store<T, ALIGNED>(static_cast<T*>(a.sum) + row * a.lds, cols, tpr, t, j, raw[j]);
+        for (int i = 0; i < 8; ++i) f[j * 8 + i] += v[i];
+        const Raw8<T> sum = norm_pack<T>(f + j * 8);  // what is normalised is the rounded sum, which the backward reads
+        if (a.sum) norm_store<T, MODE>(static_cast<T*>(a.sum) + row * a.lds, cols, tpr, t, j, sum);
+        norm_unpack<T>(sum, f + j * 8);
       }
     }
-#pragma unroll
-    for (int j = 0; j < NC; ++j) norm_unpack<T>(raw[j], f + j * 8);
+    if constexpr (AHEAD) load(row + step);  // the next row arrives while this one is reduced
     float mu = 0.0f;
     if (!a.rms) {
       float s[1] = {0.0f};
@@ -168,7 +227,7 @@ __global__ __launch_bounds__(THREADS) void k_norm(NormFwd a) {
     for (int j = 0; j < NC; ++j)
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        const float d = norm_col<ALIGNED>(j, i, tpr, t) < cols ? f[j * 8 + i] - mu : 0.0f;
+        const float d = norm_col<MODE>(j, i, tpr, t) < cols ? f[j * 8 + i] - mu : 0.0f;
         f[j * 8 + i] = d;
         q[0] = fmaf(d, d, q[0]);
       }
@@ -183,7 +242,74 @@ __global__ __launch_bounds__(THREADS) void k_norm(NormFwd a) {
     for (int j = 0; j < NC; ++j) {
 #pragma unroll
       for (int i = 0; i < 8; ++i) f[j * 8 + i] = fmaf(f[j * 8 + i] * rstd, w[j * 8 + i], b[j * 8 + i]);
-      norm_store<T, ALIGNED>(y, cols, tpr, t, j, norm_pack<T>(f + j * 8));
+      norm_store<T, MODE>(y, cols, tpr, t, j, norm_pack<T>(f + j * 8));
+    }
+  }
+}
+
+// Rows that the registers do not hold: 1024 threads a row, which is read three times (for the mean, the squares
+// and the result; after the first from the caches, mostly), as the vectors are for each row.
+template <typename T, int MODE>
+__global__ __launch_bounds__(1024) void k_norm_long(NormFwd a) {
+  __shared__ float red[2][1][16];
+  const int tpr = 1024, t = threadIdx.x, cols = a.cols, nc = (cols + 8191) / 8192;
+  const float inv = 1.0f / (float)cols;
+  int half = 0;
+  for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x) {
+    const T* x = static_cast<const T*>(a.x) + row * a.ldx;
+    const T* r = a.res ? static_cast<const T*>(a.res) + row * a.ldr : nullptr;
+    T* sum = a.sum ? static_cast<T*>(a.sum) + row * a.lds : nullptr;
+    T* y = static_cast<T*>(a.y) + row * a.ldy;
+    // chunk j of x + r, rounded
+    auto added = [&](int j, float (&f)[8]) {
+      norm_unpack<T>(norm_load1<T, MODE>(x, cols, tpr, t, j), f);
+      if (!r) return;
+      float v[8];
+      norm_unpack<T>(norm_load1<T, MODE>(r, cols, tpr, t, j), v);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) f[i] += v[i];
+      const Raw8<T> s = norm_pack<T>(f);
+      norm_unpack<T>(s, f);
+    };
+    // the same once more: from sum where it is kept, as sum may lie where x or r was
+    auto again = [&](int j, float (&f)[8]) {
+      if (sum) norm_unpack<T>(norm_load1<T, MODE>(sum, cols, tpr, t, j), f);
+      else added(j, f);
+    };
+    float s[1] = {0.0f};
+    for (int j = 0; j < nc; ++j) {
+      float f[8];
+      added(j, f);
+      if (sum) norm_store<T, MODE>(sum, cols, tpr, t, j, norm_pack<T>(f));
+#pragma unroll
+      for (int i = 0; i < 8; ++i) s[0] += f[i];
+    }
+    norm_row_sum<1>(s, tpr, red, half);
+    const float mu = a.rms ? 0.0f : s[0] * inv;
+    float q[1] = {0.0f};
+    for (int j = 0; j < nc; ++j) {
+      float f[8];
+      again(j, f);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const float d = norm_col<MODE>(j, i, tpr, t) < cols ? f[i] - mu : 0.0f;
+        q[0] = fmaf(d, d, q[0]);
+      }
+    }
+    norm_row_sum<1>(q, tpr, red, half);
+    const float rstd = 1.0f / sqrtf(fmaf(q[0], inv, a.eps));
+    if (t == 0) {
+      if (a.mean) a.mean[row] = mu;
+      if (a.rstd) a.rstd[row] = rstd;
+    }
+    for (int j = 0; j < nc; ++j) {
+      float f[8], w[8], b[8];
+      again(j, f);
+      norm_vector<MODE>(a.w, a.wbf16, 1.0f, cols, tpr, t, j, w);
+      norm_vector<MODE>(a.b, a.wbf16, 0.0f, cols, tpr, t, j, b);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) f[i] = fmaf((f[i] - mu) * rstd, w[i], b[i]);
+      norm_store<T, MODE>(y, cols, tpr, t, j, norm_pack<T>(f));
     }
   }
 }
@@ -200,24 +326,42 @@ struct NormBwd {
 
 // Every thread keeps its columns' parts of dw and db over the rows it takes; a workgroup adds those of
 // its row groups in LDS and writes one partial row, which k_norm_wgrad adds up in a fixed order.
-template <typename T, int NC, bool ALIGNED, int THREADS>
+template <typename T, int NC, int MODE, int THREADS>
 __global__ __launch_bounds__(THREADS) void k_norm_bwd(NormBwd a) {
   __shared__ float red[2][2][16];
   __shared__ float add[THREADS <= 256 ? 256 * 8 : 1];
   const int tpr = a.tpr, t = threadIdx.x & (tpr - 1), rpb = blockDim.x / tpr, cols = a.cols;
   const float inv = 1.0f / (float)cols;
+  const bool has_dsum = a.dsum && a.dx;
   int half = 0;
+  const int64_t step = (int64_t)gridDim.x * rpb;
+  int64_t row = (int64_t)blockIdx.x * rpb + threadIdx.x / tpr;
+  Raw8<T> ndy[NC], ns[NC], nd[NC];
+  float nmu = 0.0f, nrstd = 0.0f;
+  auto load = [&](int64_t r) {
+    if (r >= a.rows) return;
+    norm_load<T, NC, MODE>(static_cast<const T*>(a.dy) + r * a.ldy, cols, tpr, t, ndy);
+    norm_load<T, NC, MODE>(static_cast<const T*>(a.s) + r * a.lds, cols, tpr, t, ns);
+    if (has_dsum) norm_load<T, NC, MODE>(static_cast<const T*>(a.dsum) + r * a.ldr, cols, tpr, t, nd);
+    nmu = a.rms ? 0.0f : a.mean[r];
+    nrstd = a.rstd[r];
+  };
+  load(row);
   float w[NC * 8], dw[NC * 8], db[NC * 8];
-  norm_vector<NC, ALIGNED>(a.w, a.wbf16, 1.0f, cols, tpr, t, w);
+#pragma unroll
+  for (int j = 0; j < NC; ++j) norm_vector<MODE>(a.w, a.wbf16, 1.0f, cols, tpr, t, j, w + j * 8);
 #pragma unroll
   for (int i = 0; i < NC * 8; ++i) dw[i] = db[i] = 0.0f;
-  for (int64_t row = (int64_t)blockIdx.x * rpb + threadIdx.x / tpr; row < a.rows; row += (int64_t)gridDim.x * rpb) {
+  for (; row < a.rows; row += step) {
     Raw8<T> rdy[NC], rs[NC], rd[NC];
-    norm_load<T, NC, ALIGNED>(static_cast<const T*>(a.dy) + row * a.ldy, cols, tpr, t, rdy);
-    norm_load<T, NC, ALIGNED>(static_cast<const T*>(a.s) + row * a.lds, cols, tpr, t, rs);
-    const bool has_dsum = a.dsum && a.dx;
-    if (has_dsum) norm_load<T, NC, ALIGNED>(static_cast<const T*>(a.dsum) + row * a.ldr, cols, tpr, t, rd);
-    const float mu = a.rms ? 0.0f : a.mean[row], rstd = a.rstd[row];
+#pragma unroll
+    for (int j = 0; j < NC; ++j) {
+      rdy[j] = ndy[j];
+      rs[j] = ns[j];
+      if (has_dsum) rd[j] = nd[j];
+    }
+    const float mu = nmu, rstd = nrstd;
+    load(row + step);  // the next row arrives while this one is reduced
     float v[2] = {0.0f, 0.0f};
 #pragma unroll
     for (int j = 0; j < NC; ++j) {
@@ -227,7 +371,7 @@ __global__ __launch_bounds__(THREADS) void k_norm_bwd(NormBwd a) {
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         const int k = j * 8 + i;
-        const float xh = norm_col<ALIGNED>(j, i, tpr, t) < cols ? (x[i] - mu) * rstd : 0.0f;
+        const float xh = norm_col<MODE>(j, i, tpr, t) < cols ? (x[i] - mu) * rstd : 0.0f;
         dw[k] = fmaf(g[i], xh, dw[k]);
         db[k] += g[i];
         const float gw = g[i] * w[k];
@@ -250,7 +394,7 @@ __global__ __launch_bounds__(THREADS) void k_norm_bwd(NormBwd a) {
         const float xh = (x[i] - mu) * rstd;
         d[i] = fmaf(rstd, fmaf(-xh, m2, fmaf(g[i], w[j * 8 + i], -m1)), d[i]);
       }
-      norm_store<T, ALIGNED>(dx, cols, tpr, t, j, norm_pack<T>(d));
+      norm_store<T, MODE>(dx, cols, tpr, t, j, norm_pack<T>(d));
     }
   }
   if (!a.part) return;
@@ -278,11 +422,79 @@ __global__ __launch_bounds__(THREADS) void k_norm_bwd(NormBwd a) {
       if ((int)threadIdx.x < tpr) {
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-          const int c = norm_col<ALIGNED>(j, i, tpr, t);
+          const int c = norm_col<MODE>(j, i, tpr, t);
           if (c < cols) part[k * cols + c] = v[i];
         }
       }
     }
+}
+
+// dx of rows that the registers do not hold: 1024 threads a row, which is read twice (the second time from the
+// caches, mostly), as the weights are.
+template <typename T, int MODE>
+__global__ __launch_bounds__(1024) void k_norm_bwd_long(NormBwd a) {
+  __shared__ float red[2][2][16];
+  const int tpr = 1024, t = threadIdx.x, cols = a.cols, nc = (cols + 8191) / 8192;
+  const float inv = 1.0f / (float)cols;
+  int half = 0;
+  for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x) {
+    const T* dy = static_cast<const T*>(a.dy) + row * a.ldy;
+    const T* s = static_cast<const T*>(a.s) + row * a.lds;
+    const T* ds = a.dsum ? static_cast<const T*>(a.dsum) + row * a.ldr : nullptr;
+    T* dx = static_cast<T*>(a.dx) + row * a.ldx;
+    const float mu = a.rms ? 0.0f : a.mean[row], rstd = a.rstd[row];
+    float v[2] = {0.0f, 0.0f};
+    auto chunk = [&](int j, float (&gw)[8], float (&xh)[8]) {
+      norm_unpack<T>(norm_load1<T, MODE>(dy, cols, tpr, t, j), gw);
+      norm_unpack<T>(norm_load1<T, MODE>(s, cols, tpr, t, j), xh);
+      float w[8];
+      norm_vector<MODE>(a.w, a.wbf16, 1.0f, cols, tpr, t, j, w);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        gw[i] *= w[i];
+        xh[i] = norm_col<MODE>(j, i, tpr, t) < cols ? (xh[i] - mu) * rstd : 0.0f;
+      }
+    };
+    for (int j = 0; j < nc; ++j) {
+      float gw[8], xh[8];
+      chunk(j, gw, xh);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        v[0] += gw[i];
+        v[1] = fmaf(gw[i], xh[i], v[1]);
+      }
+    }
+    norm_row_sum<2>(v, tpr, red, half);
+    const float m1 = a.rms ? 0.0f : v[0] * inv, m2 = v[1] * inv;
+    for (int j = 0; j < nc; ++j) {
+      float gw[8], xh[8], d[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+      chunk(j, gw, xh);
+      if (ds) norm_unpack<T>(norm_load1<T, MODE>(ds, cols, tpr, t, j), d);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) d[i] = fmaf(rstd, fmaf(-xh[i], m2, gw[i] - m1), d[i]);
+      norm_store<T, MODE>(dx, cols, tpr, t, j, norm_pack<T>(d));
+    }
+  }
+}
+
+// dw and db of rows too long for k_norm_bwd's registers: one column a thread, a run of rows a workgroup.
+template <typename T>
+__global__ __launch_bounds__(256) void k_norm_cols(NormBwd a) {
+  const int c = blockIdx.x * 256 + threadIdx.x;
+  if (c >= a.cols) return;
+  const int64_t r0 = a.rows * blockIdx.y / gridDim.y, r1 = a.rows * (blockIdx.y + 1) / gridDim.y;
+  const T* dy = static_cast<const T*>(a.dy) + c;
+  const T* s = static_cast<const T*>(a.s) + c;
+  float dw = 0.0f, db = 0.0f;
+#pragma unroll 8
+  for (int64_t r = r0; r < r1; ++r) {
+    const float g = to_f32(dy[r * a.ldy]), x = to_f32(s[r * a.lds]);
+    dw = fmaf(g, (x - (a.rms ? 0.0f : a.mean[r])) * a.rstd[r], dw);
+    db += g;
+  }
+  float* part = a.part + (int64_t)blockIdx.y * 2 * a.cols;
+  part[c] = dw;
+  part[a.cols + c] = db;
 }
 
 // dw and db: the workgroups' partial rows added in fp64, 8 runs of them per column, then the runs.
@@ -308,51 +520,76 @@ __global__ __launch_bounds__(256) void k_norm_wgrad(const float* __restrict__ pa
   }
 }
 
-// Threads per row: NC = ceil(cols / (8 tpr)) chunks each.
+// Threads per row and with them the chunks of 8 columns per thread: a few rows take as many threads as there
+// are chunks; many rows up to three chunks a thread (two with 512 threads), so that the lanes are busy, a row's sums
+// cross few waves and the registers still hold the next row.
 static int norm_tpr(int64_t cols, int64_t rows) {
   const int64_t chunks = cdiv(cols, 8);
   int tpr = 8;
-  const int most = rows >= 1024 ? 4 : 1;  // few rows: as many threads as there are chunks
-  while (tpr < 1024 && cdiv(chunks, tpr) > (tpr < 64 ? 1 : most)) tpr *= 2;
+  while (tpr < 1024 && cdiv(chunks, tpr) > (rows < 1024 || tpr < 64 ? 1 : tpr <= 256 ? 3 : 2)) tpr *= 2;
   return tpr;
 }
-static int norm_threads(int tpr) { return tpr > 256 ? tpr : tpr > 64 ? tpr : 256; }
-static int norm_grid(int64_t rows, int tpr, int most) {
-  const int64_t need = cdiv(rows, norm_threads(tpr) / tpr);
+static int norm_threads(int tpr) { return tpr > 64 ? tpr : 256; }
+// Workgroups: eight waves a CU, which walk the rows; more of them only spread the accesses over more of memory's
+// pages (32768 x 7168 forward 327 us with 256 of 512 threads, 345 with 512; 16384 x 4096 89 us with 512 of 256
+// threads, 93 with 1024).
+static int norm_grid(int64_t rows, int tpr) {
+  const int threads = norm_threads(tpr);
+  const int64_t most = threads >= 512 ? 256 : 512, need = cdiv(rows, threads / tpr);
   return (int)(need < most ? need : most);
 }
-constexpr int NORM_FWD_GRID = 2048, NORM_BWD_GRID = 1024;  // workgroups
+// Rows that the registers of 1024 threads do not hold: of the forward, and of the backward, where the vectors'
+// gradients are held too.
+static bool norm_fwd_long(int64_t cols) { return cols > 16 * 1024; }
+static bool norm_bwd_long(int64_t cols) { return cols > 8 * 1024; }
 
-template <typename T, int NC, bool ALIGNED>
+template <typename T, int NC, int MODE>
 static void norm_go(const NormFwd& a, int grid, int threads, hipStream_t st) {
-  if constexpr (NC <= 4)  // (more chunks only with 1024 threads a row)
-    if (threads <= 256) return k_norm<T, NC, ALIGNED, 256><<<grid, threads, 0, st>>>(a);
-  k_norm<T, NC, ALIGNED, 1024><<<grid, threads, 0, st>>>(a);
+  if (threads <= 256) k_norm<T, NC, MODE, 256><<<grid, threads, 0, st>>>(a);
+  else if constexpr (NC <= 2) {
+    if (threads <= 512) k_norm<T, NC, MODE, 512><<<grid, threads, 0, st>>>(a);
+    else k_norm<T, NC, MODE, 1024><<<grid, threads, 0, st>>>(a);
+  }
 }
-template <typename T, int NC, bool ALIGNED>
+template <typename T, int NC, int MODE>
 static void norm_go(const NormBwd& a, int grid, int threads, hipStream_t st) {
-  if constexpr (NC <= 4)
-    if (threads <= 256) return k_norm_bwd<T, NC, ALIGNED, 256><<<grid, threads, 0, st>>>(a);
-  k_norm_bwd<T, NC, ALIGNED, 1024><<<grid, threads, 0, st>>>(a);
+  if (threads <= 256) k_norm_bwd<T, NC, MODE, 256><<<grid, threads, 0, st>>>(a);
+  else if constexpr (NC <= 2) {
+    if (threads <= 512) k_norm_bwd<T, NC, MODE, 512><<<grid, threads, 0, st>>>(a);
+    else if constexpr (NC == 1) k_norm_bwd<T, NC, MODE, 1024><<<grid, threads, 0, st>>>(a);
+  }
 }
-template <typename T, bool ALIGNED, class Args>
+template <typename T, int MODE>
+static bool norm_go_long(const NormFwd& a, int grid, hipStream_t st) {
+  if (!norm_fwd_long(a.cols)) return false;
+  k_norm_long<T, MODE><<<grid, 1024, 0, st>>>(a);
+  return true;
+}
+template <typename T, int MODE>
+static bool norm_go_long(const NormBwd& a, int grid, hipStream_t st) {
+  if (!norm_bwd_long(a.cols)) return false;
+  k_norm_bwd_long<T, MODE><<<grid, 1024, 0, st>>>(a);
+  return true;
+}
+template <typename T, int MODE, class Args>
 static void norm_chunks(const Args& a, int grid, int threads, hipStream_t st) {
+  if (norm_go_long<T, MODE>(a, grid, st)) return;
   const int nc = (int)cdiv(a.cols, 8 * a.tpr);
-  if (nc <= 1) norm_go<T, 1, ALIGNED>(a, grid, threads, st);
-  else if (nc <= 2) norm_go<T, 2, ALIGNED>(a, grid, threads, st);
-  else if (nc <= 3) norm_go<T, 3, ALIGNED>(a, grid, threads, st);
-  else if (nc <= 4) norm_go<T, 4, ALIGNED>(a, grid, threads, st);
-  else norm_go<T, 8, ALIGNED>(a, grid, threads, st);
+  if (nc <= 1) norm_go<T, 1, MODE>(a, grid, threads, st);
+  else if (nc <= 2) norm_go<T, 2, MODE>(a, grid, threads, st);
+  else norm_go<T, 3, MODE>(a, grid, threads, st);
 }
 template <class Args>
 static hipError_t norm_launch(const Args& a, bool is_bf16, bool aligned, int grid, hipStream_t st) {
-  const int threads = norm_threads(a.tpr);
+  const int threads = norm_threads(a.tpr), mode = !aligned ? NORM_ANY : a.cols % 8 ? NORM_PART : NORM_WHOLE;
   if (is_bf16) {
-    if (aligned) norm_chunks<bf16, true>(a, grid, threads, st);
-    else norm_chunks<bf16, false>(a, grid, threads, st);
+    if (mode == NORM_WHOLE) norm_chunks<bf16, NORM_WHOLE>(a, grid, threads, st);
+    else if (mode == NORM_PART) norm_chunks<bf16, NORM_PART>(a, grid, threads, st);
+    else norm_chunks<bf16, NORM_ANY>(a, grid, threads, st);
   } else {
-    if (aligned) norm_chunks<float, true>(a, grid, threads, st);
-    else norm_chunks<float, false>(a, grid, threads, st);
+    if (mode == NORM_WHOLE) norm_chunks<float, NORM_WHOLE>(a, grid, threads, st);
+    else if (mode == NORM_PART) norm_chunks<float, NORM_PART>(a, grid, threads, st);
+    else norm_chunks<float, NORM_ANY>(a, grid, threads, st);
   }
   return hipGetLastError();
 }
@@ -369,18 +606,18 @@ hipError_t launch_norm(const NormShape& s, const void* x, const void* residual, 
   a.eps = s.eps; a.wbf16 = s.wbf16; a.rms = s.rms;
   const int64_t vec = s.bf16 ? 8 : 4;
   const bool aligned = s.ldx % vec == 0 && s.ldy % vec == 0 && (!residual || s.ldr % vec == 0) && (!sum || s.lds % vec == 0);
-  return norm_launch(a, s.bf16, aligned, norm_grid(s.rows, a.tpr, NORM_FWD_GRID), st);
+  return norm_launch(a, s.bf16, aligned, norm_grid(s.rows, a.tpr), st);
 }
 
 size_t norm_bwd_workspace_bytes(const NormShape& s) {
   const int tpr = norm_tpr(s.cols, s.rows);
-  return (size_t)norm_grid(s.rows, tpr, NORM_BWD_GRID) * 2 * s.cols * sizeof(float);
+  return (size_t)norm_grid(s.rows, tpr) * 2 * s.cols * sizeof(float);
 }
 
 hipError_t launch_norm_bwd(const NormShape& s, const void* dy, const void* sum, const void* weight, const float* mean,
                            const float* rstd, const void* dsum, void* dx, float* dweight, float* dbias, void* ws,
                            hipStream_t st) {
-  const int tpr = norm_tpr(s.cols, s.rows), grid = norm_grid(s.rows, tpr, NORM_BWD_GRID);
+  const int tpr = norm_tpr(s.cols, s.rows), grid = norm_grid(s.rows, tpr);
   const bool vectors = dweight || dbias;
   float* part = static_cast<float*>(ws);
   if (s.rows > 0) {
@@ -391,7 +628,15 @@ hipError_t launch_norm_bwd(const NormShape& s, const void* dy, const void* sum, 
     a.cols = (int)s.cols; a.tpr = tpr; a.wbf16 = s.wbf16; a.rms = s.rms;
     const int64_t vec = s.bf16 ? 8 : 4;
     const bool aligned = s.ldy % vec == 0 && s.lds % vec == 0 && (!dx || s.ldx % vec == 0) && (!dsum || s.ldr % vec == 0);
-    const hipError_t e = norm_launch(a, s.bf16, aligned, grid, st);
+    const bool long_rows = norm_bwd_long(s.cols);
+    hipError_t e = hipSuccess;
+    if (vectors && long_rows) {  // (first: dx may take the place of dy or s)
+      const dim3 cols((unsigned)cdiv(s.cols, 256), (unsigned)grid);
+      if (s.bf16) k_norm_cols<bf16><<<cols, 256, 0, st>>>(a);
+      else k_norm_cols<float><<<cols, 256, 0, st>>>(a);
+      e = hipGetLastError();
+    }
+    if (e == hipSuccess && (dx || !long_rows)) e = norm_launch(a, s.bf16, aligned, grid, st);
     if (e != hipSuccess) return e;
   }
   if (!vectors) return hipSuccess;
