@@ -431,9 +431,9 @@ moe_status moe_norm_backward(const moe_norm_dims* dims, const void* dy, const vo
                              float* dweight, float* dbias, void* ws, size_t ws_bytes, void* stream);
 
 /* One gradient tensor (host struct): n consecutive elements of dtype at src (n >= 0).  dst: where
- * moe_grad_clip writes the scaled ones: src itself (in place; also meant by NULL) or n elements that
- * overlap no tensor of the list.  src and dst need only the element's own alignment; those on 16-byte
- * borders move in 16-byte accesses.  reserved: 0. */
+ * moe_grad_clip writes the scaled ones: src itself (in place; also meant by NULL) or other n elements.
+ * src and dst need only the element's own alignment; those on 16-byte borders move in 16-byte accesses.
+ * reserved: 0. */
 typedef struct moe_grad {
   const void* src;
   void* dst;
@@ -442,16 +442,32 @@ typedef struct moe_grad {
   int32_t reserved;
 } moe_grad;
 
-/* Host: workspace bytes for a list of count tensors (count 0 .. 2^16; 0 for an invalid count). */
-size_t moe_grad_workspace_bytes(int32_t count);
+/* The list that the calls below take (host struct).  A program makes it once for tensors that stay where they
+ * are: moe_grad_table() fills a host buffer and this struct, the caller copies the buffer to device memory
+ * (16-byte aligned) and sets table to it. */
+typedef struct moe_grad_list {
+  const void* table; /* device */
+  int32_t count;
+  int32_t chunks;
+} moe_grad_list;
+
+/* Host: bytes of the table of a list (count 0 .. 2^16; 0 if the list is invalid, with moe_last_error() set). */
+size_t moe_grad_table_bytes(const moe_grad* grads, int32_t count);
+
+/* Host: checks the tensors and writes their table to host_table (16-byte aligned, `bytes` long) and count and
+ * chunks to list (table: NULL).  No two tensors may share memory, sources and destinations alike, but for a
+ * tensor's own src and dst in the same place: else MOE_EINVAL. */
+moe_status moe_grad_table(const moe_grad* grads, int32_t count, void* host_table, size_t bytes,
+                          moe_grad_list* list);
+
+/* Host: workspace bytes of the calls below. */
+size_t moe_grad_workspace_bytes(void);
 
 /* moe_grad_norm — norm [1] fp32 = sqrt(sum of squares over all tensors), summed in fp64 in a fixed
- * order, so that it is exact to its rounding for any fp32 values.  Infinities and NaN reach it.
- * grads: host array, read during the call only.  It may hold any mix of sizes and types; one
- * tensor must not stand in it twice (it would count twice).  No tensors: 0.
- * ws: moe_grad_workspace_bytes(count) bytes. */
-moe_status moe_grad_norm(const moe_grad* grads, int32_t count, float* norm, void* ws, size_t ws_bytes,
-                         void* stream);
+ * order, so that it is exact to its rounding for any fp32 values.  Infinities and NaN reach it.  No
+ * tensors: 0.
+ * ws: moe_grad_workspace_bytes() bytes. */
+moe_status moe_grad_norm(const moe_grad_list* grads, float* norm, void* ws, size_t ws_bytes, void* stream);
 
 /* moe_grad_clip — dst = c src with c = max_norm / norm where norm > max_norm, else 1; products in
  * fp32, rounded once.  max_norm >= 0 (infinity: never cut).
@@ -459,8 +475,8 @@ moe_status moe_grad_norm(const moe_grad* grads, int32_t count, float* norm, void
  *  norm_in [1] fp32, device: the norm to use, e.g. joined over ranks; norm is then unused and may be NULL,
  *  as may ws.
  *  A norm that is infinite or NaN leaves c = 1: the caller sees it in norm and skips the step. */
-moe_status moe_grad_clip(const moe_grad* grads, int32_t count, double max_norm, const float* norm_in,
-                         float* norm, void* ws, size_t ws_bytes, void* stream);
+moe_status moe_grad_clip(const moe_grad_list* grads, double max_norm, const float* norm_in, float* norm,
+                         void* ws, size_t ws_bytes, void* stream);
 
 /* 4-bit weights with group scales, for serving: each row of K elements is cut into groups of consecutive
  * elements with one scale each.

@@ -39,7 +39,8 @@ EXPORTS = ["moe_max_rows", "moe_workspace_bytes", "moe_route", "moe_permute", "m
            "moe_backward_aux", "moe_router_loss", "moe_router_loss_backward",
            "moe_router_loss_workspace_bytes", "moe_dropout", "moe_combine_dropout", "moe_linear",
            "moe_linear_backward", "moe_linear_workspace_bytes", "moe_linear_plan",
-           "moe_norm", "moe_norm_workspace_bytes", "moe_norm_backward", "moe_grad_workspace_bytes", "moe_grad_norm",
+           "moe_norm", "moe_norm_workspace_bytes", "moe_norm_backward", "moe_grad_table_bytes", "moe_grad_table",
+           "moe_grad_workspace_bytes", "moe_grad_norm",
            "moe_grad_clip", "moe_w4_scale_bytes", "moe_quantize_w4", "moe_dequantize_w4", "moe_linear_w4_workspace_bytes",
            "moe_linear_w4", "moe_decode_w4",
            "moe_version", "moe_timing_enable", "moe_timing_read"]
@@ -76,6 +77,10 @@ class NormDims(ctypes.Structure):
 class GradStruct(ctypes.Structure):
     _fields_ = [("src", ctypes.c_void_p), ("dst", ctypes.c_void_p), ("n", ctypes.c_int64), ("dtype", ctypes.c_int32),
                 ("reserved", ctypes.c_int32)]
+
+
+class GradListStruct(ctypes.Structure):
+    _fields_ = [("table", ctypes.c_void_p), ("count", ctypes.c_int32), ("chunks", ctypes.c_int32)]
 
 
 class W4Struct(ctypes.Structure):
@@ -142,9 +147,12 @@ def lib():
         L.moe_norm.argtypes = [pn, vp, vp, vp, vp, vp, vp, vp, vp, vp]
         L.moe_norm_workspace_bytes.argtypes, L.moe_norm_workspace_bytes.restype = [pn], sz
         L.moe_norm_backward.argtypes = [pn, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp]
-        L.moe_grad_workspace_bytes.argtypes, L.moe_grad_workspace_bytes.restype = [i32], sz
-        L.moe_grad_norm.argtypes = [pg, i32, vp, vp, sz, vp]
-        L.moe_grad_clip.argtypes = [pg, i32, ctypes.c_double, vp, vp, vp, sz, vp]
+        po = ctypes.POINTER(GradListStruct)
+        L.moe_grad_table_bytes.argtypes, L.moe_grad_table_bytes.restype = [pg, i32], sz
+        L.moe_grad_table.argtypes = [pg, i32, vp, sz, po]
+        L.moe_grad_workspace_bytes.argtypes, L.moe_grad_workspace_bytes.restype = [], sz
+        L.moe_grad_norm.argtypes = [po, vp, vp, sz, vp]
+        L.moe_grad_clip.argtypes = [po, ctypes.c_double, vp, vp, vp, sz, vp]
         pw, ci = ctypes.POINTER(W4Struct), ctypes.c_int
         L.moe_w4_scale_bytes.argtypes, L.moe_w4_scale_bytes.restype = [i64, i64, i32, i32], i64
         L.moe_quantize_w4.argtypes = [i64, i64, ci, vp, pw, vp]
@@ -152,7 +160,7 @@ def lib():
         L.moe_linear_w4_workspace_bytes.argtypes, L.moe_linear_w4_workspace_bytes.restype = [pl], sz
         L.moe_linear_w4.argtypes = [pl, vp, pw, vp, vp, vp, vp, sz, vp]
         L.moe_decode_w4.argtypes = [pd, vp, vp, vp, pw, pw, pw, vp, vp, vp, vp, vp, sz, vp]
-        for f in ("moe_norm", "moe_norm_backward", "moe_grad_norm", "moe_grad_clip", "moe_quantize_w4", "moe_dequantize_w4",
+        for f in ("moe_norm", "moe_norm_backward", "moe_grad_table", "moe_grad_norm", "moe_grad_clip", "moe_quantize_w4", "moe_dequantize_w4",
                   "moe_linear_w4", "moe_decode_w4"):
             getattr(L, f).restype = st
         for f in ("moe_backward_aux", "moe_router_loss", "moe_router_loss_backward", "moe_dropout",
@@ -202,12 +210,19 @@ def _stream(stream=None):
     return (stream if stream is not None else torch.cuda.current_stream()).cuda_stream
 
 
+def _gp(t, dev):
+    """Address of a tensor that GPU ``dev`` can read (None and addresses pass)."""
+    if t is None or t.__class__ is int:
+        return t
+    if t.get_device() != dev:
+        raise MoEError(-1, "a tensor is on %s: it must be on the current GPU, cuda:%d" % (t.device, dev))
+    return t.data_ptr()
+
+
 def _on_gpu(*tensors):
-    """Refuses tensors that the current GPU's kernels could not read (None and addresses pass)."""
     dev = torch.cuda.current_device()
     for t in tensors:
-        if t is not None and not isinstance(t, int) and t.get_device() != dev:
-            raise MoEError(-1, "a tensor is on %s: it must be on the current GPU, cuda:%d" % (t.device, dev))
+        _gp(t, dev)
 
 
 def _check(status):
@@ -502,9 +517,9 @@ def norm_workspace(dims, device="cuda"):
 def moe_norm(dims, x, residual, weight, bias, sum, y, mean, rstd, stream=None):
     """sum = x + residual, y = norm(sum) weight + bias, with the rows' mean and 1 / deviation; residual, weight,
     bias, sum, mean and rstd may be None."""
-    _on_gpu(x, residual, weight, bias, sum, y, mean, rstd)
-    status = lib().moe_norm(ctypes.byref(dims), _p(x), _p(residual), _p(weight), _p(bias), _p(sum), _p(y), _p(mean),
-                            _p(rstd), _stream(stream))
+    d = torch.cuda.current_device()
+    status = lib().moe_norm(ctypes.byref(dims), _gp(x, d), _gp(residual, d), _gp(weight, d), _gp(bias, d), _gp(sum, d),
+                            _gp(y, d), _gp(mean, d), _gp(rstd, d), _stream(stream))
     if status:
         _check(status)
 
@@ -512,22 +527,24 @@ def moe_norm(dims, x, residual, weight, bias, sum, y, mean, rstd, stream=None):
 def moe_norm_backward(dims, dy, s, weight, mean, rstd, dsum, dx, dweight, dbias, ws, ws_bytes, stream=None):
     """Gradients of moe_norm from dy and the normalised sum s (x without a residual); dsum: the gradient that
     reaches s directly, or None; dx, dweight and dbias may be None."""
-    _on_gpu(dy, s, weight, mean, rstd, dsum, dx, dweight, dbias, ws)
-    _check(lib().moe_norm_backward(ctypes.byref(dims), _p(dy), _p(s), _p(weight), _p(mean), _p(rstd), _p(dsum), _p(dx),
-                                   _p(dweight), _p(dbias), _p(ws), ws_bytes, _stream(stream)))
+    d = torch.cuda.current_device()
+    _check(lib().moe_norm_backward(ctypes.byref(dims), _gp(dy, d), _gp(s, d), _gp(weight, d), _gp(mean, d), _gp(rstd, d),
+                                   _gp(dsum, d), _gp(dx, d), _gp(dweight, d), _gp(dbias, d), _gp(ws, d), ws_bytes,
+                                   _stream(stream)))
 
 
 class Gradients:
     """A list of gradient tensors (contiguous, bf16 or fp32, on one GPU) and where moe_grad_clip writes the
-    scaled ones: ``dst``, tensors of the same sizes and types, or in place without it."""
+    scaled ones: ``dst``, tensors of the same sizes and types, or in place without it.  Holds the tensors and
+    the device table that the kernels read; made once for tensors that stay where they are."""
 
     def __init__(self, src, dst=None):
-        self.src, self.dst = list(src), list(src if dst is None else dst)
+        self.src = list(src)
+        self.dst = self.src if dst is None else list(dst)
         if len(self.src) != len(self.dst):
             raise MoEError(-1, "%d gradients but %d destinations" % (len(self.src), len(self.dst)))
         self.count = len(self.src)
         self.array = (GradStruct * max(self.count, 1))()
-        spans = []
         for i, (s, d) in enumerate(zip(self.src, self.dst)):
             if s.dtype not in (torch.bfloat16, torch.float32):
                 raise MoEError(-2, "gradient %d: dtype %s not supported" % (i, s.dtype))
@@ -537,35 +554,36 @@ class Gradients:
                 raise MoEError(-1, "gradient %d must be contiguous" % i)
             if s.device != self.src[0].device or d.device != s.device:
                 raise MoEError(-1, "gradient %d is on another device" % i)
-            n = s.numel()
-            self.array[i] = GradStruct(s.data_ptr(), d.data_ptr(), n, MOE_BF16 if s.dtype is torch.bfloat16 else MOE_F32, 0)
-            if n:
-                spans.append((s.data_ptr(), s.data_ptr() + n * s.element_size(), i))
-                if d.data_ptr() != s.data_ptr():
-                    spans.append((d.data_ptr(), d.data_ptr() + n * s.element_size(), i))
-        spans.sort()
-        for (_, end, i), (start, _, j) in zip(spans, spans[1:]):
-            if start < end:
-                raise MoEError(-1, "gradients %d and %d share memory" % (i, j))
+            self.array[i] = GradStruct(s.data_ptr(), d.data_ptr(), s.numel(),
+                                       MOE_BF16 if s.dtype is torch.bfloat16 else MOE_F32, 0)
+        nbytes = lib().moe_grad_table_bytes(self.array, self.count)
+        if nbytes == 0:
+            raise MoEError(-1, lib().moe_last_error().decode())
+        host = torch.empty(nbytes + 16, dtype=torch.uint8)
+        host = host[-host.data_ptr() % 16:][:nbytes]
+        self.struct = GradListStruct()
+        _check(lib().moe_grad_table(self.array, self.count, host.data_ptr(), nbytes, ctypes.byref(self.struct)))
+        self.table = host.to(self.src[0].device) if self.count else host
+        self.struct.table = self.table.data_ptr()
+        self._ref = ctypes.byref(self.struct)
 
 
 def grad_workspace(grads, device="cuda"):
-    nbytes = lib().moe_grad_workspace_bytes(grads.count)
-    return torch.empty(max(nbytes, 256), dtype=torch.uint8, device=device), nbytes
+    nbytes = lib().moe_grad_workspace_bytes()
+    return torch.empty(nbytes, dtype=torch.uint8, device=device), nbytes
 
 
 def moe_grad_norm(grads, norm, ws, ws_bytes, stream=None):
     """The global norm (fp32 [1]) of a list of gradients."""
-    _on_gpu(*grads.src[:1], norm, ws)
-    _check(lib().moe_grad_norm(grads.array, grads.count, _p(norm), _p(ws), ws_bytes, _stream(stream)))
+    _on_gpu(grads.table if grads.count else None, norm, ws)
+    _check(lib().moe_grad_norm(grads._ref, _p(norm), _p(ws), ws_bytes, _stream(stream)))
 
 
 def moe_grad_clip(grads, max_norm, norm_in, norm, ws, ws_bytes, stream=None):
     """Gradients scaled down to a global norm of max_norm.  norm_in (fp32 [1]): the norm to use; None: it is
     computed and written to norm."""
-    _on_gpu(*grads.src[:1], norm_in, norm, ws)
-    _check(lib().moe_grad_clip(grads.array, grads.count, float(max_norm), _p(norm_in), _p(norm), _p(ws), ws_bytes,
-                               _stream(stream)))
+    _on_gpu(grads.table if grads.count else None, norm_in, norm, ws)
+    _check(lib().moe_grad_clip(grads._ref, max_norm, _p(norm_in), _p(norm), _p(ws), ws_bytes, _stream(stream)))
 
 
 class W4:
@@ -634,9 +652,10 @@ def _w4_rows(w4, rows, K, name):
 def moe_linear_w4(dims, X, W, bias, residual, out, ws, ws_bytes, stream=None):
     """out = residual + act(X W^T + bias) with 4-bit weights W (a W4); bias and residual may be None."""
     _w4_rows(W, 2 * dims.N if dims.act == ACTS["swiglu"] else dims.N, dims.K, "W")
-    _on_gpu(X, W.codes, bias, residual, out, ws)
-    status = lib().moe_linear_w4(ctypes.byref(dims), _p(X), W._ref, _p(bias), _p(residual), _p(out), _p(ws), ws_bytes,
-                                 _stream(stream))
+    d = torch.cuda.current_device()
+    _gp(W.codes, d)
+    status = lib().moe_linear_w4(ctypes.byref(dims), _gp(X, d), W._ref, _gp(bias, d), _gp(residual, d), _gp(out, d), _gp(ws, d),
+                                 ws_bytes, _stream(stream))
     if status:
         _check(status)
 

@@ -2,40 +2,22 @@
 //
 //   N = sqrt(sum over tensors and elements of g^2),  c = max_norm / N where N > max_norm, else 1,  out = c g
 //
-// The tensors' addresses and lengths travel in the kernels' arguments, GRAD_TENSORS of them a launch, so a
-// call needs no table in device memory and a captured graph holds its own.  Tensors are cut into chunks of
-// GRAD_CHUNK elements; a fixed grid of workgroups walks them, each thread adding its squares in fp64
-// (whose squares neither overflow nor vanish for any fp32 value), and leaves one partial sum per workgroup.
-// The scaling kernel's workgroups each add the partial sums, all in the same order, so no launch stands
-// between the two passes.
+// The tensors are described by a table that the host makes once (GradEntry per tensor, then the tensor of each
+// chunk of GRAD_CHUNK elements), so that a pass over any number of them is one launch.  A fixed grid of workgroups
+// walks the chunks, each thread adding its squares in fp64 (which neither overflow nor vanish for any fp32
+// value), and leaves one partial sum per workgroup.  The scaling kernel's workgroups each add the partial sums,
+// all in the same order, so no launch stands between the two passes.
+#include <algorithm>
+#include <memory>
+#include <new>
+
 #include "internal.h"
 
 namespace moe {
 
-constexpr int GRAD_TENSORS = 112;   // per launch: 3.4 KB of kernel arguments
-constexpr int GRAD_CHUNK = 8192;    // elements
-constexpr int GRAD_GRID = 2048;     // workgroups over all launches of a pass (more where launches are many)
+constexpr int GRAD_GRID = 1024;     // workgroups
 
-struct GradTable {
-  const void* src[GRAD_TENSORS];
-  void* dst[GRAD_TENSORS];
-  int64_t n[GRAD_TENSORS];
-  int32_t first[GRAD_TENSORS + 1];  // first chunk of each tensor, and the number of chunks
-  uint8_t kind[GRAD_TENSORS];       // GRAD_BF16 | GRAD_ALIGNED
-  int32_t count;
-};
 enum { GRAD_BF16 = 1, GRAD_ALIGNED = 2 };
-
-// The tensor that chunk c belongs to: the last one whose first chunk is not behind it.
-__device__ __forceinline__ int grad_find(const GradTable& g, int c) {
-  int lo = 0, hi = g.count - 1;
-  while (lo < hi) {
-    const int mid = (lo + hi + 1) >> 1;
-    if (g.first[mid] <= c) lo = mid;
-    else hi = mid - 1;
-  }
-  return lo;
-}
 
 __device__ __forceinline__ double grad_block_sum(double v, double* red) {
 #pragma unroll
@@ -114,26 +96,25 @@ __device__ __forceinline__ void grad_scale(const T* p, T* o, int n, bool aligned
   for (int k = i + threadIdx.x; k < n; k += 256) o[k] = from_f32<T>(to_f32(p[k]) * c);
 }
 
-// f(tensor, first element of the chunk, elements in it)
+// f(entry, first element of the chunk, elements in it)
 template <class F>
-__device__ __forceinline__ void grad_chunks(const GradTable& g, F f) {
-  const int chunks = g.first[g.count];
-  int t = -1;
+__device__ __forceinline__ void grad_chunks(const GradEntry* __restrict__ table, const int32_t* __restrict__ tensor, int chunks, F f) {
+  int next = (int)blockIdx.x < chunks ? tensor[blockIdx.x] : 0;
   for (int c = blockIdx.x; c < chunks; c += gridDim.x) {
-    if (t < 0 || c >= g.first[t + 1]) t = grad_find(g, c);
-    const int64_t at = (int64_t)(c - g.first[t]) * GRAD_CHUNK;
-    const int64_t left = g.n[t] - at;
-    f(t, at, (int)(left < GRAD_CHUNK ? left : GRAD_CHUNK));
+    const GradEntry g = table[__builtin_amdgcn_readfirstlane(next)];
+    if (c + (int)gridDim.x < chunks) next = tensor[c + gridDim.x];
+    const int64_t at = (int64_t)(c - g.first) * GRAD_CHUNK, left = g.n - at;
+    f(g, at, (int)(left < GRAD_CHUNK ? left : GRAD_CHUNK));
   }
 }
 
-__global__ __launch_bounds__(256) void k_grad_square(GradTable g, double* part) {
+__global__ __launch_bounds__(256) void k_grad_square(const GradEntry* table, const int32_t* tensor, int chunks, double* part) {
   __shared__ double red[4];
   double v = 0.0;
-  grad_chunks(g, [&](int t, int64_t at, int n) {
-    const bool al = g.kind[t] & GRAD_ALIGNED;
-    if (g.kind[t] & GRAD_BF16) v += grad_square<bf16>(static_cast<const bf16*>(g.src[t]) + at, n, al);
-    else v += grad_square<float>(static_cast<const float*>(g.src[t]) + at, n, al);
+  grad_chunks(table, tensor, chunks, [&](const GradEntry& g, int64_t at, int n) {
+    const bool al = g.kind & GRAD_ALIGNED;
+    if (g.kind & GRAD_BF16) v += grad_square<bf16>(static_cast<const bf16*>(g.src) + at, n, al);
+    else v += grad_square<float>(static_cast<const float*>(g.src) + at, n, al);
   });
   v = grad_block_sum(v, red);
   if (threadIdx.x == 0) part[blockIdx.x] = v;
@@ -142,7 +123,11 @@ __global__ __launch_bounds__(256) void k_grad_square(GradTable g, double* part) 
 // The sum of the partial sums, in one order in every workgroup.
 __device__ __forceinline__ double grad_total(const double* part, int parts, double* red) {
   double v = 0.0;
-  for (int i = threadIdx.x; i < parts; i += 256) v += part[i];
+#pragma unroll
+  for (int i = 0; i < GRAD_GRID / 256; ++i) {
+    const int k = threadIdx.x + 256 * i;
+    v += k < parts ? part[k] : 0.0;
+  }
   return grad_block_sum(v, red);
 }
 
@@ -152,94 +137,92 @@ __global__ __launch_bounds__(256) void k_grad_norm(const double* part, int parts
   if (threadIdx.x == 0) *norm = (float)sqrt(v);
 }
 
-__global__ __launch_bounds__(256) void k_grad_scale(GradTable g, const double* part, int parts, const float* norm_in, float* norm,
-                                                    double max_norm) {
+__global__ __launch_bounds__(256) void k_grad_scale(const GradEntry* table, const int32_t* tensor, int chunks, const double* part,
+                                                    int parts, const float* norm_in, float* norm, double max_norm) {
   __shared__ double red[4];
   const double n = part ? sqrt(grad_total(part, parts, red)) : (double)*norm_in;
-  if (norm && blockIdx.x == 0 && threadIdx.x == 0) *norm = (float)n;
+  if (part && blockIdx.x == 0 && threadIdx.x == 0) *norm = (float)n;
   // a norm that is not a finite fp32 number (as the caller sees it) leaves the values as they are
   const bool cut = n > max_norm && (float)n < __builtin_inff();
   const float c = cut ? (float)(max_norm / n) : 1.0f;
-  grad_chunks(g, [&](int t, int64_t at, int m) {
-    if (!cut && g.src[t] == g.dst[t]) return;
-    const bool al = g.kind[t] & GRAD_ALIGNED;
-    if (g.kind[t] & GRAD_BF16)
-      grad_scale<bf16>(static_cast<const bf16*>(g.src[t]) + at, static_cast<bf16*>(g.dst[t]) + at, m, al, c);
-    else
-      grad_scale<float>(static_cast<const float*>(g.src[t]) + at, static_cast<float*>(g.dst[t]) + at, m, al, c);
+  grad_chunks(table, tensor, chunks, [&](const GradEntry& g, int64_t at, int m) {
+    if (!cut && g.src == g.dst) return;
+    const bool al = g.kind & GRAD_ALIGNED;
+    if (g.kind & GRAD_BF16) grad_scale<bf16>(static_cast<const bf16*>(g.src) + at, static_cast<bf16*>(g.dst) + at, m, al, c);
+    else grad_scale<float>(static_cast<const float*>(g.src) + at, static_cast<float*>(g.dst) + at, m, al, c);
   });
 }
 
-// Launches of a pass over the list: f(table, grid) for every GRAD_TENSORS tensors that have elements.
-static int grad_launches(int count) { return (int)cdiv(count, GRAD_TENSORS); }
-static int grad_grid(int chunks, int count) {
-  const int share = (int)cdiv(GRAD_GRID, grad_launches(count));
-  const int most = share < 256 ? 256 : share;
-  return chunks < most ? chunks : most;
-}
-template <class F>
-static hipError_t grad_pass(const GradTensor* list, int count, F f) {
-  for (int i = 0; i < count; i += GRAD_TENSORS) {
-    GradTable g;
-    g.count = 0;
-    int chunks = 0;
-    for (int k = i; k < count && k < i + GRAD_TENSORS; ++k) {
-      if (list[k].n == 0) continue;
-      const int q = g.count++;
-      const uintptr_t both = reinterpret_cast<uintptr_t>(list[k].src) | reinterpret_cast<uintptr_t>(list[k].dst);
-      g.src[q] = list[k].src;
-      g.dst[q] = list[k].dst;
-      g.n[q] = list[k].n;
-      g.first[q] = chunks;
-      g.kind[q] = (uint8_t)((list[k].bf16 ? GRAD_BF16 : 0) | (both % 16 == 0 ? GRAD_ALIGNED : 0));
-      chunks += (int)cdiv(list[k].n, GRAD_CHUNK);
-    }
-    if (g.count == 0) continue;
-    g.first[g.count] = chunks;
-    f(g, grad_grid(chunks, count));
-    const hipError_t e = hipGetLastError();
-    if (e != hipSuccess) return e;
+static int grad_grid(int chunks) { return chunks < GRAD_GRID ? chunks : GRAD_GRID; }
+
+size_t grad_workspace_bytes() { return GRAD_GRID * sizeof(double); }
+
+int grad_table(const GradTensor* list, int count, void* host) {
+  GradEntry* e = static_cast<GradEntry*>(host);
+  int32_t* tensor = reinterpret_cast<int32_t*>(e + count);
+  int chunks = 0;
+  for (int i = 0; i < count; ++i) {
+    const uintptr_t both = reinterpret_cast<uintptr_t>(list[i].src) | reinterpret_cast<uintptr_t>(list[i].dst);
+    e[i] = GradEntry{list[i].src, list[i].dst, list[i].n, chunks, (list[i].bf16 ? GRAD_BF16 : 0) | (both % 16 == 0 ? GRAD_ALIGNED : 0)};
+    for (int64_t c = cdiv(list[i].n, GRAD_CHUNK); c > 0; --c) tensor[chunks++] = i;
   }
-  return hipSuccess;
+  return chunks;
 }
 
-size_t grad_workspace_bytes(int count) {
-  const int per = grad_grid(0x7fffffff, count < 1 ? 1 : count);
-  return (size_t)per * (count < 1 ? 1 : grad_launches(count)) * sizeof(double);
+// Two tensors (sources or destinations, but for one's own two in the same place) that share bytes.
+bool grad_overlap(const GradTensor* list, int count, int* first, int* second) {
+  struct Span {
+    uintptr_t a, b;
+    int i;
+  };
+  const std::unique_ptr<Span[]> s(new (std::nothrow) Span[2 * (size_t)count + 1]);
+  if (!s) return false;
+  size_t n = 0;
+  for (int i = 0; i < count; ++i) {
+    const uintptr_t bytes = (uintptr_t)list[i].n * (list[i].bf16 ? 2 : 4);
+    if (bytes == 0) continue;
+    const uintptr_t src = reinterpret_cast<uintptr_t>(list[i].src), dst = reinterpret_cast<uintptr_t>(list[i].dst);
+    s[n++] = Span{src, src + bytes, i};
+    if (dst != src) s[n++] = Span{dst, dst + bytes, i};
+  }
+  std::sort(s.get(), s.get() + n, [](const Span& x, const Span& y) { return x.a < y.a; });
+  for (size_t k = 1; k < n; ++k)
+    if (s[k].a < s[k - 1].b) {
+      *first = s[k - 1].i;
+      *second = s[k].i;
+      return true;
+    }
+  return false;
 }
 
-static hipError_t grad_squares(const GradTensor* list, int count, double* part, int* parts, hipStream_t st) {
-  *parts = 0;
-  return grad_pass(list, count, [&](const GradTable& g, int grid) {
-    k_grad_square<<<grid, 256, 0, st>>>(g, part + *parts);
-    *parts += grid;
-  });
+static const int32_t* grad_tensors(const void* table, int count) {
+  return reinterpret_cast<const int32_t*>(static_cast<const GradEntry*>(table) + count);
 }
 
-hipError_t launch_grad_norm(const GradTensor* list, int count, float* norm, void* ws, hipStream_t st) {
-  double* part = static_cast<double*>(ws);
-  int parts = 0;
-  const hipError_t e = grad_squares(list, count, part, &parts, st);
-  if (e != hipSuccess) return e;
-  k_grad_norm<<<1, 256, 0, st>>>(part, parts, norm);
+static hipError_t grad_squares(const void* table, int count, int chunks, double* part, hipStream_t st) {
+  if (chunks == 0) return hipSuccess;
+  k_grad_square<<<grad_grid(chunks), 256, 0, st>>>(static_cast<const GradEntry*>(table), grad_tensors(table, count), chunks, part);
   return hipGetLastError();
 }
 
-hipError_t launch_grad_clip(const GradTensor* list, int count, double max_norm, const float* norm_in, float* norm, void* ws,
+hipError_t launch_grad_norm(const void* table, int count, int chunks, float* norm, void* ws, hipStream_t st) {
+  double* part = static_cast<double*>(ws);
+  const hipError_t e = grad_squares(table, count, chunks, part, st);
+  if (e != hipSuccess) return e;
+  k_grad_norm<<<1, 256, 0, st>>>(part, grad_grid(chunks), norm);
+  return hipGetLastError();
+}
+
+hipError_t launch_grad_clip(const void* table, int count, int chunks, double max_norm, const float* norm_in, float* norm, void* ws,
                             hipStream_t st) {
+  if (chunks == 0) return norm_in ? hipSuccess : launch_grad_norm(table, count, 0, norm, ws, st);
   double* part = norm_in ? nullptr : static_cast<double*>(ws);
-  int parts = 0;
   if (!norm_in) {
-    const hipError_t e = grad_squares(list, count, part, &parts, st);
+    const hipError_t e = grad_squares(table, count, chunks, part, st);
     if (e != hipSuccess) return e;
   }
-  bool first = true;
-  const hipError_t e = grad_pass(list, count, [&](const GradTable& g, int grid) {
-    k_grad_scale<<<grid, 256, 0, st>>>(g, part, parts, norm_in, first && !norm_in ? norm : nullptr, max_norm);
-    first = false;
-  });
-  if (e != hipSuccess || !first || norm_in) return e;
-  k_grad_norm<<<1, 256, 0, st>>>(part, 0, norm);  // no elements at all
+  const int grid = grad_grid(chunks);
+  k_grad_scale<<<grid, 256, 0, st>>>(static_cast<const GradEntry*>(table), grad_tensors(table, count), chunks, part, grid, norm_in, norm, max_norm);
   return hipGetLastError();
 }
 

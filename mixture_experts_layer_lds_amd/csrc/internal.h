@@ -150,16 +150,27 @@ hipError_t launch_norm_bwd(const NormShape& s, const void* dy, const void* sum, 
                            hipStream_t st);
 
 // ---- gradient norm and clipping (grads.hip) ----
+constexpr int GRAD_CHUNK = 8192;  // elements
 struct GradTensor {
   const void* src;
   void* dst;
   int64_t n;
   bool bf16;
 };
-size_t grad_workspace_bytes(int count);
-hipError_t launch_grad_norm(const GradTensor* list, int count, float* norm, void* ws, hipStream_t st);
+// Table in device memory: an entry per tensor, then the tensor of each chunk (int32).
+struct GradEntry {
+  const void* src;
+  void* dst;
+  int64_t n;
+  int32_t first;  // first chunk
+  int32_t kind;
+};
+size_t grad_workspace_bytes();
+int grad_table(const GradTensor* list, int count, void* host);  // returns the number of chunks
+bool grad_overlap(const GradTensor* list, int count, int* first, int* second);
+hipError_t launch_grad_norm(const void* table, int count, int chunks, float* norm, void* ws, hipStream_t st);
 // norm_in (device) or, where it is null, the norm computed first and written to norm
-hipError_t launch_grad_clip(const GradTensor* list, int count, double max_norm, const float* norm_in, float* norm, void* ws,
+hipError_t launch_grad_clip(const void* table, int count, int chunks, double max_norm, const float* norm_in, float* norm, void* ws,
                             hipStream_t st);
 
 // ---- router losses (router_loss.hip) ----

@@ -951,7 +951,8 @@ moe_status moe_norm_backward(const moe_norm_dims* dims, const void* dy, const vo
 
 // ---- gradient norm and clipping ----
 constexpr int32_t kMaxGrads = 1 << 16;
-static moe_status check_grads(const moe_grad* g, int32_t count, GradTensor* out) {
+static moe_status check_grads(const moe_grad* g, int32_t count, GradTensor* out, int64_t* chunks) {
+  *chunks = 0;
   for (int32_t i = 0; i < count; ++i) {
     if (g[i].dtype != MOE_F32 && g[i].dtype != MOE_BF16) return fail(MOE_ENOTSUP, "tensor %d: dtype %d not supported", i, g[i].dtype);
     if (g[i].n < 0 || g[i].n > ((int64_t)1 << 36)) return fail(MOE_EINVAL, "tensor %d: n=%lld out of range [0, 2^36]", i, (long long)g[i].n);
@@ -964,52 +965,75 @@ static moe_status check_grads(const moe_grad* g, int32_t count, GradTensor* out)
     const uintptr_t both = reinterpret_cast<uintptr_t>(t.src) | reinterpret_cast<uintptr_t>(t.dst);
     if (t.n > 0 && !t.src) return fail(MOE_EINVAL, "tensor %d: src is NULL", i);
     if (t.n > 0 && both % (t.bf16 ? 2 : 4)) return fail(MOE_EINVAL, "tensor %d is not aligned to its elements", i);
+    *chunks += cdiv(t.n, GRAD_CHUNK);
     out[i] = t;
   }
+  if (*chunks > 0x7fffffffll) return fail(MOE_ENOTSUP, "the tensors hold more than 2^31 chunks of %d elements", GRAD_CHUNK);
   return MOE_OK;
 }
-static moe_status check_grad_list(const moe_grad* g, int32_t count) {
+static size_t grad_table_bytes(int32_t count, int64_t chunks) { return (size_t)count * sizeof(GradEntry) + (size_t)chunks * 4; }
+static moe_status grad_list(const moe_grad* g, int32_t count, std::unique_ptr<GradTensor[]>* out, int64_t* chunks) {
   if (count < 0 || count > kMaxGrads) return fail(MOE_EINVAL, "count=%d out of range [0, 2^16]", count);
   if (count > 0 && !g) return fail(MOE_EINVAL, "grads is NULL");
+  out->reset(new (std::nothrow) GradTensor[count + 1]);
+  if (!*out) return fail(MOE_EINVAL, "no host memory for %d tensors", count);
+  return check_grads(g, count, out->get(), chunks);
+}
+
+size_t moe_grad_table_bytes(const moe_grad* grads, int32_t count) {
+  std::unique_ptr<GradTensor[]> list;
+  int64_t chunks = 0;
+  if (grad_list(grads, count, &list, &chunks) != MOE_OK) return 0;
+  const size_t bytes = grad_table_bytes(count, chunks);
+  return bytes ? bytes : sizeof(GradEntry);
+}
+
+moe_status moe_grad_table(const moe_grad* grads, int32_t count, void* host_table, size_t bytes, moe_grad_list* out) {
+  std::unique_ptr<GradTensor[]> list;
+  int64_t chunks = 0;
+  MOE_TRY(grad_list(grads, count, &list, &chunks));
+  if (!out) return fail(MOE_EINVAL, "list is NULL");
+  MOE_TRY(need_ptr(host_table, "host_table"));
+  if (bytes < grad_table_bytes(count, chunks))
+    return fail(MOE_EWORKSPACE, "table of %zu bytes < %zu needed", bytes, grad_table_bytes(count, chunks));
+  int a = 0, b = 0;
+  if (grad_overlap(list.get(), count, &a, &b)) return fail(MOE_EINVAL, "tensors %d and %d share memory", a, b);
+  out->table = nullptr;
+  out->count = count;
+  out->chunks = grad_table(list.get(), count, host_table);
   return MOE_OK;
 }
-static moe_status check_grad_ws(int32_t count, void* ws, size_t ws_bytes) {
-  const size_t need = grad_workspace_bytes(count);
+
+static moe_status check_grad_call(const moe_grad_list* g, void* ws, size_t ws_bytes, bool needs_ws) {
+  if (!g) return fail(MOE_EINVAL, "grads is NULL");
+  if (g->count < 0 || g->count > kMaxGrads || g->chunks < 0)
+    return fail(MOE_EINVAL, "count=%d / chunks=%d out of range", g->count, g->chunks);
+  if (g->chunks > 0) MOE_TRY(need_ptr(g->table, "table"));
+  if (!needs_ws) return MOE_OK;
+  const size_t need = grad_workspace_bytes();
   if (ws_bytes < need) return fail(MOE_EWORKSPACE, "workspace of %zu bytes < %zu needed", ws_bytes, need);
   return need_ptr(ws, "ws");
 }
 
-size_t moe_grad_workspace_bytes(int32_t count) {
-  if (count < 0 || count > kMaxGrads) return fail(MOE_EINVAL, "count=%d out of range [0, 2^16]", count), 0;
-  return grad_workspace_bytes(count);
-}
+size_t moe_grad_workspace_bytes(void) { return grad_workspace_bytes(); }
 
-moe_status moe_grad_norm(const moe_grad* grads, int32_t count, float* norm, void* ws, size_t ws_bytes, void* stream) {
-  MOE_TRY(check_grad_list(grads, count));
-  const std::unique_ptr<GradTensor[]> list(new (std::nothrow) GradTensor[count + 1]);
-  if (!list) return fail(MOE_EINVAL, "no host memory for %d tensors", count);
-  MOE_TRY(check_grads(grads, count, list.get()));
+moe_status moe_grad_norm(const moe_grad_list* grads, float* norm, void* ws, size_t ws_bytes, void* stream) {
+  MOE_TRY(check_grad_call(grads, ws, ws_bytes, true));
   MOE_TRY(need_ptr(norm, "norm"));
-  MOE_TRY(check_grad_ws(count, ws, ws_bytes));
   hipStream_t st = static_cast<hipStream_t>(stream);
-  MOE_STAGE(MOE_STAGE_GRAD, st, launch_grad_norm(list.get(), count, norm, ws, st), "gradient norm");
+  MOE_STAGE(MOE_STAGE_GRAD, st, launch_grad_norm(grads->table, grads->count, grads->chunks, norm, ws, st), "gradient norm");
   return MOE_OK;
 }
 
-moe_status moe_grad_clip(const moe_grad* grads, int32_t count, double max_norm, const float* norm_in, float* norm,
-                         void* ws, size_t ws_bytes, void* stream) {
-  MOE_TRY(check_grad_list(grads, count));
+moe_status moe_grad_clip(const moe_grad_list* grads, double max_norm, const float* norm_in, float* norm, void* ws,
+                         size_t ws_bytes, void* stream) {
+  MOE_TRY(check_grad_call(grads, ws, ws_bytes, !norm_in));
   if (!(max_norm >= 0.0)) return fail(MOE_EINVAL, "max_norm=%g must be >= 0", max_norm);
-  const std::unique_ptr<GradTensor[]> list(new (std::nothrow) GradTensor[count + 1]);
-  if (!list) return fail(MOE_EINVAL, "no host memory for %d tensors", count);
-  MOE_TRY(check_grads(grads, count, list.get()));
   MOE_TRY(opt_ptr(norm_in, "norm_in"));
-  if (!norm_in) {
-    MOE_TRY(need_ptr(norm, "norm"));
-    MOE_TRY(check_grad_ws(count, ws, ws_bytes));
-  }
+  if (!norm_in) MOE_TRY(need_ptr(norm, "norm"));
   hipStream_t st = static_cast<hipStream_t>(stream);
-  MOE_STAGE(MOE_STAGE_GRAD, st, launch_grad_clip(list.get(), count, max_norm, norm_in, norm, ws, st), "gradient clipping");
+  MOE_STAGE(MOE_STAGE_GRAD, st,
+            launch_grad_clip(grads->table, grads->count, grads->chunks, max_norm, norm_in, norm, ws, st), "gradient clipping");
   return MOE_OK;
 }
 

@@ -76,27 +76,50 @@ def grads(*items):
     return a
 
 
-def test_gradient_refusals(lib):
-    ok = grads((FAKE, FAKE, 10, 0))
-    need = lib.moe_grad_workspace_bytes(1)
-    assert need > 0 and lib.moe_grad_workspace_bytes(-1) == 0 and lib.moe_grad_workspace_bytes((1 << 16) + 1) == 0
-    nrm = lambda g=ok, count=1, norm_=FAKE, ws=FAKE, nb=need: lib.moe_grad_norm(g, count, norm_, ws, nb, None)  # noqa: E731
-    clp = lambda g=ok, count=1, m=1.0, ni=None, norm_=FAKE, ws=FAKE, nb=need: lib.moe_grad_clip(g, count, m, ni, norm_, ws, nb, None)  # noqa: E731
+def test_gradient_table_refusals(lib):
+    host = (ctypes.c_uint64 * 64)()
+    at = (ctypes.addressof(host) + 15) // 16 * 16
+    out = B.GradListStruct()
+    tab = lambda g, count=1, table=at, nb=400, o=ctypes.byref(out): lib.moe_grad_table(g, count, table, nb, o)  # noqa: E731
+    ok = grads((FAKE, None, 8193, 0))
+    need = lib.moe_grad_table_bytes(ok, 1)
+    assert need == 32 + 2 * 4 and tab(ok) == 0 and (out.table, out.count, out.chunks) == (None, 1, 2)
+    assert tab(ok, nb=need) == 0 and tab(ok, nb=need - 1) == -3
+    assert tab(ok, table=None) == -1 and tab(ok, table=at + 8) == -1 and tab(ok, o=None) == -1
+    for count in (-1, (1 << 16) + 1):
+        assert tab(ok, count=count) == -1 and lib.moe_grad_table_bytes(ok, count) == 0
+    assert tab(None) == -1 and lib.moe_grad_table_bytes(None, 1) == 0
+    for item, status in (((FAKE, FAKE, -1, 0), -1), ((FAKE, FAKE, (1 << 36) + 1, 0), -1), ((None, FAKE, 3, 0), -1), ((FAKE + 2, FAKE, 3, 0), -1),
+                         ((FAKE, FAKE + 2, 3, 0), -1), ((FAKE + 1, FAKE, 3, 1), -1), ((FAKE, FAKE, 3, 2), -2)):
+        assert tab(grads(item)) == status, item
+        assert b"tensor 0" in lib.moe_last_error() and lib.moe_grad_table_bytes(grads(item), 1) == 0
+    bad = grads((FAKE, FAKE, 10, 0))
+    bad[0].reserved = 1
+    assert tab(bad) == -1
+    # shared memory: the same tensor twice, parts of one, a destination over another's source
+    for two in (((FAKE, None, 10, 0), (FAKE, None, 10, 0)), ((FAKE, None, 10, 0), (FAKE + 36, None, 2, 0)), ((FAKE, FAKE * 2, 10, 0), (FAKE * 2 + 20, None, 4, 1)),
+                ((FAKE, FAKE * 2, 10, 0), (FAKE * 3, FAKE * 2, 10, 0)), ((FAKE, FAKE + 4, 10, 0), (FAKE * 3, None, 1, 0))):
+        assert tab(grads(*two), count=2) == -1 and b"share memory" in lib.moe_last_error()
+    assert tab(grads((FAKE, None, 10, 0), (FAKE + 40, None, 10, 0)), count=2) == 0 and out.chunks == 2
+    assert tab(grads(), count=0) == 0 and (out.count, out.chunks) == (0, 0) and lib.moe_grad_table_bytes(None, 0) > 0
+
+
+def test_gradient_call_refusals(lib):
+    need = lib.moe_grad_workspace_bytes()
+    assert need > 0
+    glist = lambda **kw: B.GradListStruct(**dict(dict(table=FAKE, count=1, chunks=1), **kw))  # noqa: E731
+    nrm = lambda g=glist(), norm_=FAKE, ws=FAKE, nb=need: lib.moe_grad_norm(ctypes.byref(g), norm_, ws, nb, None)  # noqa: E731
+    clp = lambda g=glist(), m=1.0, ni=None, norm_=FAKE, ws=FAKE, nb=need: lib.moe_grad_clip(ctypes.byref(g), m, ni, norm_, ws, nb, None)  # noqa: E731
     for f in (nrm, clp):
-        assert f(count=-1) == -1 and f(count=(1 << 16) + 1) == -1 and f(g=None) == -1
+        for kw in (dict(table=None), dict(table=FAKE + 8), dict(count=-1), dict(count=(1 << 16) + 1), dict(chunks=-1)):
+            assert f(g=glist(**kw)) == -1, kw
         assert f(norm_=None) == -1 and f(norm_=FAKE + 4) == -1 and f(ws=None) == -1 and f(ws=FAKE + 8) == -1 and f(nb=need - 1) == -3
-        for item, status in (((FAKE, FAKE, -1, 0), -1), ((FAKE, FAKE, (1 << 36) + 1, 0), -1), ((None, FAKE, 3, 0), -1), ((FAKE + 2, FAKE, 3, 0), -1),
-                             ((FAKE, FAKE + 2, 3, 0), -1), ((FAKE + 1, FAKE, 3, 1), -1), ((FAKE, FAKE, 3, 2), -2)):
-            assert f(g=grads(item)) == status, item
-            assert b"tensor 0" in lib.moe_last_error()
-        bad = grads((FAKE, FAKE, 10, 0))
-        bad[0].reserved = 1
-        assert f(g=bad) == -1
+    assert lib.moe_grad_norm(None, FAKE, FAKE, need, None) == -1 and lib.moe_grad_clip(None, 1.0, None, FAKE, FAKE, need, None) == -1
     for m in (-1.0, float("nan"), float("-inf")):
         assert clp(m=m) == -1 and b"max_norm" in lib.moe_last_error()
     assert clp(ni=FAKE + 4) == -1
     # with a norm given and nothing to scale there is nothing to do
-    assert clp(g=grads((None, None, 0, 0)), ni=FAKE, norm_=None, ws=None, nb=0) == 0
+    assert clp(g=glist(table=None, count=0, chunks=0), ni=FAKE, norm_=None, ws=None, nb=0) == 0
 
 
 def test_gradient_list_checks_tensors():
@@ -111,4 +134,4 @@ def test_gradient_list_checks_tensors():
     with pytest.raises(B.MoEError, match="share memory"):
         B.Gradients([both[:40], both[40:80]], [torch.zeros(40), both[:40]])
     g = B.Gradients([both[:40], both[40:80], both[80:80]])
-    assert g.count == 3 and g.array[1].n == 40
+    assert g.count == 3 and g.array[1].n == 40 and g.struct.chunks == 2
