@@ -512,13 +512,16 @@ moe_status moe_quantize_w4(int64_t rows, int64_t K, int dtype, const void* src, 
 moe_status moe_dequantize_w4(int64_t rows, int64_t K, int dtype, const moe_w4* w, void* out, void* stream);
 
 /* moe_linear_w4 — moe_linear without Z, on 4-bit weights W (N' rows of K): out = residual + act(X W^T + bias).
- *  dims.dtype must be MOE_BF16 (X, residual, out); K a multiple of the group.  Up to 64 rows the codes are
- *  streamed, products are exact and sums fp32 (INT4: a group's sum is multiplied by its scale in
- *  fp32); with more rows W is expanded to bf16 in the workspace first, where an INT4 value is rounded to
- *  bf16 (half a step, 2^-9 of it).
- *  An infinite element of X may make its row's results NaN where the exact sum is infinite (INT4).
+ *  dims.dtype must be MOE_BF16 (X, residual, out); K a multiple of the group.  All sums are fp32.  A product goes
+ *  one of three ways, by dims alone (moe_linear_w4_plan): STREAMED (up to 64 rows always), where products are exact
+ *  and an INT4 group's sum is multiplied by its scale in fp32; TILED (some hundred rows) and EXPANDED (many), where
+ *  an INT4 value is rounded to bf16 before it is multiplied (half a step, 2^-9 of it; FP4 values are exact).
+ *  An infinite element of X may make its row's results NaN where the exact sum is infinite.
  *  residual may be out (with the same stride).  M = 0 does nothing.
  *  ws: moe_linear_w4_workspace_bytes(dims) bytes. */
+enum { MOE_W4_STREAMED = 0, MOE_W4_TILED = 1, MOE_W4_EXPANDED = 2 };
+/* Host: the way of a product, for measurement tools and tests, or a negative moe_status. */
+int moe_linear_w4_plan(const moe_linear_dims* dims);
 size_t moe_linear_w4_workspace_bytes(const moe_linear_dims* dims);
 moe_status moe_linear_w4(const moe_linear_dims* dims, const void* X, const moe_w4* W, const float* bias,
                          const void* residual, void* out, void* ws, size_t ws_bytes, void* stream);

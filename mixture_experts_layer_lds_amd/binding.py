@@ -25,6 +25,7 @@ OP_ROUTE, OP_PERMUTE, OP_FFN, OP_COMBINE, OP_FORWARD, OP_BACKWARD, OP_DECODE, OP
 FP8_E4M3, FP8_E5M2 = 0, 1
 ACTS = {"none": 0, "relu": 1, "gelu": 2, "silu": 3, "swiglu": 4}
 LINEAR_FORWARD, LINEAR_BACKWARD = 0, 1
+W4_WAYS = ["streamed", "tiled", "expanded"]
 W4_FORMATS = {"int4": 0, "fp4": 1}
 NORM_KINDS = {"layer": 0, "rms": 1}
 LINEAR_OUT, LINEAR_DX, LINEAR_DW = 0, 1, 2
@@ -42,7 +43,7 @@ EXPORTS = ["moe_max_rows", "moe_workspace_bytes", "moe_route", "moe_permute", "m
            "moe_norm", "moe_norm_workspace_bytes", "moe_norm_backward", "moe_grad_table_bytes", "moe_grad_table",
            "moe_grad_workspace_bytes", "moe_grad_norm",
            "moe_grad_clip", "moe_w4_scale_bytes", "moe_quantize_w4", "moe_dequantize_w4", "moe_linear_w4_workspace_bytes",
-           "moe_linear_w4", "moe_decode_w4",
+           "moe_linear_w4_plan", "moe_linear_w4", "moe_decode_w4",
            "moe_version", "moe_timing_enable", "moe_timing_read"]
 STAGES = ["router_gemm", "route", "tiles", "up_gemm", "down_gemm", "permute", "combine", "dact_gemm",
           "dw_down_gemm", "dw_gu_gemm", "dx_gemm", "router_bwd", "dwr_gemm", "decode", "fp8_quant",
@@ -158,6 +159,7 @@ def lib():
         L.moe_quantize_w4.argtypes = [i64, i64, ci, vp, pw, vp]
         L.moe_dequantize_w4.argtypes = [i64, i64, ci, pw, vp, vp]
         L.moe_linear_w4_workspace_bytes.argtypes, L.moe_linear_w4_workspace_bytes.restype = [pl], sz
+        L.moe_linear_w4_plan.argtypes, L.moe_linear_w4_plan.restype = [pl], ci
         L.moe_linear_w4.argtypes = [pl, vp, pw, vp, vp, vp, vp, sz, vp]
         L.moe_decode_w4.argtypes = [pd, vp, vp, vp, pw, pw, pw, vp, vp, vp, vp, vp, sz, vp]
         for f in ("moe_norm", "moe_norm_backward", "moe_grad_table", "moe_grad_norm", "moe_grad_clip", "moe_quantize_w4", "moe_dequantize_w4",
@@ -642,6 +644,14 @@ def moe_dequantize_w4(w4, out, stream=None):
 def linear_w4_workspace(dims, device="cuda"):
     nbytes = lib().moe_linear_w4_workspace_bytes(ctypes.byref(dims))
     return torch.empty(max(nbytes, 256), dtype=torch.uint8, device=device), nbytes
+
+
+def moe_linear_w4_plan(dims):
+    """How a product on 4-bit weights goes: "streamed", "tiled" or "expanded"."""
+    way = lib().moe_linear_w4_plan(ctypes.byref(dims))
+    if way < 0:
+        _check(way)
+    return W4_WAYS[way]
 
 
 def _w4_rows(w4, rows, K, name):

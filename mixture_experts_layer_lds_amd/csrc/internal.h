@@ -212,6 +212,8 @@ hipError_t launch_quant_w4(const void* src, bool is_bf16, int format, int group,
                            void* scales, hipStream_t st);
 hipError_t launch_expand_w4(const W4View& w, int64_t rows, int64_t K, bool is_bf16, void* out, hipStream_t st);
 size_t linear_w4_workspace_bytes(const LinShape& s);
+enum { W4_STREAMED = 0, W4_TILED = 1, W4_EXPANDED = 2 };
+int linear_w4_plan(const LinShape& s);
 hipError_t launch_linear_w4(const LinShape& s, const void* X, const W4View& w, const float* bias, const void* residual, void* out,
                             void* ws, hipStream_t st);
 // launch_decode with the experts' weights in 4 bits (one format and group for the three)

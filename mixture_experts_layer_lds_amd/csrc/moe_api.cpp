@@ -1039,6 +1039,7 @@ moe_status moe_grad_clip(const moe_grad_list* grads, double max_norm, const floa
 
 // ---- 4-bit weights ----
 static_assert((int)MOE_W4_INT4 == W4_INT && (int)MOE_W4_FP4 == W4_FP, "format codes");
+static_assert((int)MOE_W4_STREAMED == W4_STREAMED && (int)MOE_W4_TILED == W4_TILED && (int)MOE_W4_EXPANDED == W4_EXPANDED, "ways");
 static moe_status check_w4_format(int64_t K, int32_t format, int32_t group) {
   if (format != MOE_W4_INT4 && format != MOE_W4_FP4) return fail(MOE_EINVAL, "4-bit format %d invalid", format);
   if (format == MOE_W4_FP4 ? group != 32 : group != 32 && group != 64 && group != 128)
@@ -1131,6 +1132,12 @@ static moe_status check_linear_w4(const moe_linear_dims* dims, LinShape* s) {
 size_t moe_linear_w4_workspace_bytes(const moe_linear_dims* dims) {
   LinShape s;
   return check_linear_w4(dims, &s) == MOE_OK ? linear_w4_workspace_bytes(s) : 0;
+}
+
+int moe_linear_w4_plan(const moe_linear_dims* dims) {
+  LinShape s;
+  MOE_TRY(check_linear_w4(dims, &s));
+  return linear_w4_plan(s);
 }
 
 moe_status moe_linear_w4(const moe_linear_dims* dims, const void* X, const moe_w4* W, const float* bias,

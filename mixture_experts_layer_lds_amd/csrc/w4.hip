@@ -1,8 +1,9 @@
 // 4-bit weights with group scales (w4.h has the formats): quantisation, expansion, and the dense
 // projection on them, out = residual + act(X W^T + bias) with bf16 X.
 //
-// Few rows: the codes are streamed from memory straight into registers (k_w4_rows).  More rows: W expanded to
-// bf16 in the workspace, then the dense projection's own tiles.
+// Few rows: the codes are streamed from memory straight into registers (k_w4_rows).  Some hundred: tiles with X in
+// LDS (k_w4_tile).  More: W expanded to bf16 in the workspace, then the dense projection's own tiles.
+#include "gemm_core.h"
 #include "internal.h"
 #include "lin_epi.h"
 #include "w4.h"
@@ -180,8 +181,222 @@ __global__ __launch_bounds__(512) void k_w4_rows(const bf16* __restrict__ X, int
   }
 }
 
-// Rows up to which the codes are streamed; more go through an expanded copy of W.
-constexpr int W4_STREAM_ROWS = 64;
+// ---- some hundred rows ----
+// X through LDS, W straight from its codes: a workgroup of four waves takes 128 tokens and 64 RT rows of W.  Blocks
+// of 128 elements of the tokens (32 KB) arrive in two slots of LDS in turn by direct loads; each wave expands the codes
+// of its own 16 RT rows into the products' B operand, where no other wave needs them, so that W never passes through
+// LDS or memory as bf16.  INT4 values are rounded to bf16 here (half a step, 2^-9 of them; s (c - 8) itself is exact in
+// fp32): eight token groups per tile leave no time for a scale per group and result.
+//   X in LDS: [128 tokens][256 bytes], 16-byte chunk c of token t in slot c ^ (t & 15): the 16 tokens that are
+// read together lie in different banks.  Each slot is an array of its own, so that the compiler sees that reading
+// one does not wait for the loads into the other.
+//   Bound by LDS: every wave reads the whole block of X, 32 KB against 64 MFMAs of 16 cycles (RT = 2).  Two
+// workgroups a CU hide each other's waits: eight waves on a ring of four slots, one workgroup a CU, took 26 us where
+// this takes 19 (256 x 2048 -> 7168).  777 x 2048 -> 7168 36.5 us (625 TFLOP/s); expanding W first 42.5.
+constexpr int W4G_TOK = 128, W4G_NG = W4G_TOK / 16, W4G_WAVES = 4, W4G_SLOT = W4G_TOK * 256;
+constexpr int W4G_DMA = W4G_SLOT / 1024 / W4G_WAVES;  // direct loads of a wave per block
+
+template <int FMT>
+__device__ __forceinline__ u32x4 w4_expand8(uint32_t w, float s, float s8) {
+  if constexpr (FMT == W4_FP) {
+    (void)s8;
+    return w4_unpack_fp(w, s);
+  } else {
+    const uint32_t lo = w & 0x0f0f0f0fu, hi = (w >> 4) & 0x0f0f0f0fu;  // elements 0 2 4 6 and 1 3 5 7
+    u32x4 r;
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      r[k] = pack_bf16x2(fmaf((float)((lo >> (8 * k)) & 255u), s, s8), fmaf((float)((hi >> (8 * k)) & 255u), s, s8));
+    return r;
+  }
+}
+
+template <int FMT, int RT, int OUT>
+__global__ __launch_bounds__(W4G_WAVES * 64, 2) void k_w4_tile(const bf16* __restrict__ X, int64_t ldx,
+                                                            const uint8_t* __restrict__ codes, const uint8_t* __restrict__ scales,
+                                                            int64_t plane, int group_shift, int m, int n, int K,
+                                                            float* __restrict__ part, LinEpi<bf16> ep) {
+  __shared__ __attribute__((aligned(1024))) char l0[W4G_SLOT], l1[W4G_SLOT];
+  constexpr bool GLU = OUT == W4_GLU, INT = FMT == W4_INT;
+  constexpr int COLS = GLU ? 8 * RT : 16 * RT;  // output columns of a wave
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), r16 = lane & 15, q = lane >> 4;
+  const int c0 = (blockIdx.x * W4G_WAVES + wave) * COLS, t0 = blockIdx.y * W4G_TOK;
+  const int nb = w4_blocks(K);
+  const int b0 = (int)((int64_t)nb * blockIdx.z / gridDim.z), b1 = (int)((int64_t)nb * (blockIdx.z + 1) / gridDim.z);
+  // the wave's rows of W (behind the last one: that one, unused): SwiGLU's tiles hold gate rows, then up rows
+  const uint8_t *wp[RT], *sp[RT];
+#pragma unroll
+  for (int r = 0; r < RT; ++r) {
+    const int i = 16 * r + r16, col = GLU && i >= COLS ? i - COLS : i;
+    const int64_t row = (GLU && i >= COLS ? n : 0) + min(c0 + col, n - 1);
+    wp[r] = codes + row * (K / 2) + 16 * q;
+    sp[r] = scales + (INT ? row * 2 : row * 4 + q);
+  }
+  // direct loads: instruction i of the wave fills tokens 16 i + 4 wave + 0 .. 3, lane l slot l % 16 of token l / 16
+  const int tl = 4 * wave + (lane >> 4), chunk = (lane & 15) ^ (tl & 15);
+  const char* xt = reinterpret_cast<const char*>(X + (int64_t)t0 * ldx);
+  uint32_t xo[W4G_DMA];
+#pragma unroll
+  for (int i = 0; i < W4G_DMA; ++i) xo[i] = (uint32_t)min(16 * i + tl, m - 1 - t0) * (uint32_t)(ldx * 2);  // (below 2^31)
+  u32x4 cw[2][RT];
+  uint32_t cs[2][RT];
+  auto fetch = [&](int b, char* slot, u32x4 (&c)[RT], uint32_t (&s)[RT]) {
+    // (chunks behind the row repeat its last: they meet weights of zero)
+    const uint32_t at = (uint32_t)b * 256u + 16u * (uint32_t)min(chunk, (K - b * W4_BLOCK) / 8 - 1);
+#pragma unroll
+    for (int i = 0; i < W4G_DMA; ++i) dma16(xt + xo[i] + at, slot + i * 4096 + wave * 1024);
+    const bool in = b * W4_BLOCK + 32 * q < K;
+    const int64_t pl = INT ? (b * W4_BLOCK + (in ? 32 * q : 0)) >> group_shift : b;
+#pragma unroll
+    for (int r = 0; r < RT; ++r) {
+      c[r] = ld16(wp[r] + (int64_t)b * (W4_BLOCK / 2) - (in ? 0 : 16 * q));
+      if constexpr (INT) s[r] = *reinterpret_cast<const uint16_t*>(sp[r] + pl * plane);
+      else s[r] = sp[r][pl * plane];  // (a byte behind the row is not used)
+    }
+  };
+  f32x4 acc[RT][W4G_NG];
+#pragma unroll
+  for (int r = 0; r < RT; ++r)
+#pragma unroll
+    for (int g = 0; g < W4G_NG; ++g) acc[r][g] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+  auto products = [&](int b, const char* slot, const u32x4 (&c)[RT], const uint32_t (&s)[RT]) {
+    const bool in = b * W4_BLOCK + 32 * q < K;
+    const char* xb = slot + r16 * 256;
+    float f[RT], f8[RT];
+#pragma unroll
+    for (int r = 0; r < RT; ++r) {
+      if constexpr (INT) f[r] = in ? __uint_as_float(s[r] << 16) : 0.0f;
+      else f[r] = !in ? 1.0f : __uint_as_float(s[r] ? s[r] << 23 : 0x00400000u);
+      f8[r] = -8.0f * f[r];
+    }
+    u32x4 x[2][W4G_NG];
+    auto read = [&](int j) {
+      const char* xj = xb + 16 * ((4 * q + j) ^ r16);
+#pragma unroll
+      for (int g = 0; g < W4G_NG; ++g) x[j & 1][g] = *reinterpret_cast<const u32x4*>(xj + g * 4096);
+    };
+    read(0);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      if (j < 3) read(j + 1);
+      u32x4 w[RT];
+#pragma unroll
+      for (int r = 0; r < RT; ++r) w[r] = w4_expand8<FMT>(INT || in ? c[r][j] : 0u, f[r], f8[r]);
+#pragma unroll
+      for (int g = 0; g < W4G_NG; ++g)
+#pragma unroll
+        for (int r = 0; r < RT; ++r) acc[r][g] = w4_mfma(x[j & 1][g], w[r], acc[r][g]);
+      __builtin_amdgcn_sched_barrier(0);
+    }
+  };
+  // block b from `slot`; the next one goes where the block before was (behind the last one: that one once more,
+  // unread, so that the loop needs no case of its own)
+  auto step = [&](int b, const char* slot, const u32x4 (&c)[RT], const uint32_t (&s)[RT], char* free, u32x4 (&cf)[RT], uint32_t (&sf)[RT]) {
+    wait_vmcnt<0>();
+    ring_barrier();
+    fetch(min(b + 1, b1 - 1), free, cf, sf);
+    products(b, slot, c, s);
+  };
+  if (b0 < b1) {
+    fetch(b0, l0, cw[0], cs[0]);
+    int b = b0;
+    for (; b + 2 <= b1; b += 2) {
+      step(b, l0, cw[0], cs[0], l1, cw[1], cs[1]);
+      step(b + 1, l1, cw[1], cs[1], l0, cw[0], cs[0]);
+    }
+    if (b < b1) step(b, l0, cw[0], cs[0], l1, cw[1], cs[1]);
+  }
+  wait_vmcnt<0>();  // the direct loads still under way end before the slots are used again
+  __syncthreads();
+  // 16 tokens at a time through the wave's own part of LDS: [token][16 RT values], a lane takes a quarter of a
+  // token's columns
+  constexpr int PITCH = 16 * RT + 4, QUADS = COLS / 4;
+  float* res = reinterpret_cast<float*>(l0) + wave * (16 * PITCH);
+  const int tok = lane >> 2;
+#pragma unroll
+  for (int g = 0; g < W4G_NG; ++g) {
+#pragma unroll
+    for (int r = 0; r < RT; ++r)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) res[(4 * q + i) * PITCH + 16 * r + r16] = acc[r][g][i];
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "workgroup");
+    __builtin_amdgcn_wave_barrier();
+    const int t = t0 + 16 * g + tok;
+#pragma unroll
+    for (int k = 0; k < (QUADS + 3) / 4; ++k) {
+      const int at = 4 * ((lane & 3) + 4 * k), c = c0 + at;
+      if (at < COLS && t < m && c < n) {
+        const f32x4 z = *reinterpret_cast<const f32x4*>(res + tok * PITCH + at);
+        if constexpr (GLU) {
+          const f32x4 up = *reinterpret_cast<const f32x4*>(res + tok * PITCH + COLS + at);
+          lin_epi4(ep, (int64_t)t, c, n, true, z, up);
+        } else if constexpr (OUT == W4_OUT) {
+          lin_epi4(ep, (int64_t)t, c, n, false, z, z);
+        } else {
+          *reinterpret_cast<f32x4*>(part + ((int64_t)blockIdx.z * m + t) * n + c) = z;
+        }
+      }
+    }
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "workgroup");
+    __builtin_amdgcn_wave_barrier();
+  }
+}
+
+struct W4TilePlan {
+  int rt, slices;
+  double us;
+};
+// Row tiles per wave and slices by a model of measured times: a block of the loop takes 1.1 us (RT = 2: 1.45) with one
+// workgroup a CU and 1.7 (2.3) with two; joining slices 3 us and their bytes at 4 TB/s.
+static W4TilePlan w4_tile_plan(const LinShape& s) {
+  const int64_t rows = s.act == LIN_SWIGLU ? 2 * s.N : s.N, groups = cdiv(s.M, W4G_TOK), blocks = w4_blocks((int)s.K);
+  W4TilePlan best{1, 1, 0.0};
+  for (int rt = 1; rt <= 2; ++rt)
+    for (int slices = 1; slices <= 4 && (slices == 1 || blocks / slices >= 2); slices *= 2) {
+      const int64_t wgs = cdiv(rows, 16 * W4G_WAVES * rt) * groups * slices, rest = wgs % 512;
+      const double one = rt == 1 ? 1.1 : 1.45, two = rt == 1 ? 1.7 : 2.3;
+      double us = (double)cdiv(blocks, slices) * ((double)(wgs / 512) * two + (rest == 0 ? 0.0 : rest <= 256 ? one : two));
+      us += 1.5;  // the launch and the first block
+      if (slices > 1) us += 3.0 + (double)slices * (double)s.M * (double)rows * 8.0 / 4e6;
+      if (best.us == 0.0 || us < best.us) best = W4TilePlan{rt, slices, us};
+    }
+  return best;
+}
+
+// Which way a product goes.  Up to 64 rows the codes are streamed; up to 1024 the quicker of streaming (4 us and 7.5
+// ps per row, row of W and element, 32 rows at a time: 256 x 1024 -> 1024 5.5 us, tiles 9) and tiles; beyond, W
+// is expanded (2048 x 2048 -> 7168 63 us, tiles 70; 1024 rows 45 and 38).
+constexpr int W4_STREAM_ROWS = 64, W4_TILE_ROWS = 1024;
+int linear_w4_plan(const LinShape& s) {
+  if (s.M <= W4_STREAM_ROWS) return W4_STREAMED;
+  if (s.M > W4_TILE_ROWS) return W4_EXPANDED;
+  const double rows = (double)(s.act == LIN_SWIGLU ? 2 * s.N : s.N);
+  const double stream = 4.0 + 7.5e-9 * (double)(cdiv(s.M, 32) * 32) * rows * (double)s.K;
+  return stream < w4_tile_plan(s).us ? W4_STREAMED : W4_TILED;
+}
+template <int FMT, int RT>
+static void w4_tile_rt(const LinShape& s, const W4TilePlan& p, const W4View& w, const bf16* X, const LinEpi<bf16>& ep, float* part,
+                       hipStream_t st) {
+  const bool glu = s.act == LIN_SWIGLU;
+  const int64_t rows = glu ? 2 * s.N : s.N;
+  const dim3 grid((unsigned)cdiv(rows, 16 * W4G_WAVES * RT), (unsigned)cdiv(s.M, W4G_TOK), (unsigned)p.slices);
+  const uint8_t* sc = static_cast<const uint8_t*>(w.scales);
+  const int64_t plane = rows * (FMT == W4_INT ? 2 : 4);
+  const int m = (int)s.M, K = (int)s.K, shift = w.group == 32 ? 5 : w.group == 64 ? 6 : 7, T = W4G_WAVES * 64;
+  if (p.slices > 1) k_w4_tile<FMT, RT, W4_PART><<<grid, T, 0, st>>>(X, s.ldx, w.codes, sc, plane, shift, m, (int)rows, K, part, ep);
+  else if (glu) k_w4_tile<FMT, RT, W4_GLU><<<grid, T, 0, st>>>(X, s.ldx, w.codes, sc, plane, shift, m, (int)s.N, K, part, ep);
+  else k_w4_tile<FMT, RT, W4_OUT><<<grid, T, 0, st>>>(X, s.ldx, w.codes, sc, plane, shift, m, (int)s.N, K, part, ep);
+}
+template <int FMT>
+static hipError_t w4_tile(const LinShape& s, const W4View& w, const bf16* X, const LinEpi<bf16>& ep, float* part, hipStream_t st) {
+  const W4TilePlan p = w4_tile_plan(s);
+  if (p.rt == 2) w4_tile_rt<FMT, 2>(s, p, w, X, ep, part, st);
+  else w4_tile_rt<FMT, 1>(s, p, w, X, ep, part, st);
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess || p.slices == 1) return e;
+  return launch_lin_finish(part, p.slices, (int)s.M, (int)s.N, (int)(s.act == LIN_SWIGLU ? 2 * s.N : s.N), ep, st);
+}
+
 constexpr int64_t W4_LDS = 65536;
 
 // How a product is cut: by the shape alone, so that the workspace is known without the weights.
@@ -276,8 +491,9 @@ static size_t w4_expanded_bytes(const LinShape& s) {
   return align_up((size_t)(s.act == LIN_SWIGLU ? 2 * s.N : s.N) * s.K * sizeof(bf16), 256);
 }
 size_t linear_w4_workspace_bytes(const LinShape& s) {
-  if (s.M > W4_STREAM_ROWS) return w4_expanded_bytes(s) + linear_fwd_workspace_bytes(s);
-  const int slices = s.M > 0 ? w4_plan(s).slices : 1;
+  const int way = linear_w4_plan(s);
+  if (way == W4_EXPANDED) return w4_expanded_bytes(s) + linear_fwd_workspace_bytes(s);
+  const int slices = way == W4_TILED ? w4_tile_plan(s).slices : s.M > 0 ? w4_plan(s).slices : 1;
   return slices > 1 ? (size_t)slices * s.M * (s.act == LIN_SWIGLU ? 2 * s.N : s.N) * sizeof(float) : 0;
 }
 
@@ -317,7 +533,8 @@ hipError_t launch_expand_w4(const W4View& w, int64_t rows, int64_t K, bool is_bf
 hipError_t launch_linear_w4(const LinShape& s, const void* X, const W4View& w, const float* bias, const void* residual, void* out,
                             void* ws, hipStream_t st) {
   if (s.M == 0) return hipSuccess;
-  if (s.M > W4_STREAM_ROWS) {
+  const int way = linear_w4_plan(s);
+  if (way == W4_EXPANDED) {
     const hipError_t e = launch_expand_w4(w, s.act == LIN_SWIGLU ? 2 * s.N : s.N, s.K, true, ws, st);
     if (e != hipSuccess) return e;
     return launch_linear(s, X, ws, bias, residual, nullptr, out, static_cast<char*>(ws) + w4_expanded_bytes(s), st);
@@ -325,6 +542,7 @@ hipError_t launch_linear_w4(const LinShape& s, const void* X, const W4View& w, c
   const LinEpi<bf16> ep{bias, static_cast<const bf16*>(residual), s.ldr, nullptr, 0, static_cast<bf16*>(out), s.ldy, s.act};
   const bf16* x = static_cast<const bf16*>(X);
   float* part = static_cast<float*>(ws);
+  if (way == W4_TILED) return w.format == W4_FP ? w4_tile<W4_FP>(s, w, x, ep, part, st) : w4_tile<W4_INT>(s, w, x, ep, part, st);
   if (w.format == W4_FP) return w4_stream<W4_FP, 32>(s, w, x, ep, part, st);
   if (w.group == 32) return w4_stream<W4_INT, 32>(s, w, x, ep, part, st);
   if (w.group == 64) return w4_stream<W4_INT, 64>(s, w, x, ep, part, st);

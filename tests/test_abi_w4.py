@@ -74,8 +74,11 @@ def test_linear_refusals(lib):
     for kw in (dict(X=None), dict(out=None), dict(W=None), dict(X=FAKE + 2), dict(bias=FAKE + 4), dict(res=FAKE + 2), dict(out=FAKE)):
         assert lin(ldims(), **kw) == -1, kw
     assert lin(ldims(ldr=72), res=FAKE * 2) == -1 and b"stride" in lib.moe_last_error()
-    need = lib.moe_linear_w4_workspace_bytes(ref(ldims()))
-    assert need >= 64 * 256 * 2 and lin(ldims(), nb=need - 1) == -3 and lin(ldims(), ws=None) == -1
+    many = ldims(M=1100)
+    need = lib.moe_linear_w4_workspace_bytes(ref(many))
+    assert need >= 64 * 256 * 2 and lin(many, nb=need - 1) == -3 and lin(many, ws=None) == -1
+    assert B.moe_linear_w4_plan(many) == "expanded" and B.moe_linear_w4_plan(ldims(M=64)) == "streamed"
+    assert lib.moe_linear_w4_plan(ref(ldims(N=100))) == -2 and lib.moe_linear_w4_plan(None) == -1
     assert lin(ldims(M=0), X=None, W=None, out=None, ws=None, nb=0) == 0
 
 

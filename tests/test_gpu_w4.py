@@ -12,7 +12,6 @@ from oracle import w4 as ow
 pytestmark = pytest.mark.gpu
 
 FORMATS = [("fp4", 32), ("int4", 32), ("int4", 64), ("int4", 128)]
-EXPANDED = 64  # more rows than these go through weights expanded to bf16
 
 
 @pytest.fixture(autouse=True)
@@ -97,14 +96,14 @@ def test_every_fp4_code_and_scale_byte():
         assert ok.sum() > 200 * 32 and np.array_equal(got[ok[:, k0:k0 + 16]], V[:, k0:k0 + 16][ok[:, k0:k0 + 16]])
 
 
-def linear_bounds(X, codes, s, V, fmt, group, M):
+def linear_bounds(X, codes, s, V, fmt, group, streamed):
     """|z - exact z| of the streaming kernel: exact products, fp32 sums.  INT4: within a group 33 additions per
     32 elements of terms up to 16 s |x| (1 + c / 16 + 1.5), then one addition per group in each of at least 1
     (K < 2048) or 4 waves, 8 waves at most; FP4: one addition per element.  Expanded weights: one per element."""
     K = X.shape[1]
     ax = np.abs(X)
-    if fmt == "fp4" or M > EXPANDED:
-        chain = (K if K < 2048 else K // 4) + 16 if M <= EXPANDED else K + 64
+    if fmt == "fp4" or not streamed:
+        chain = (K if K < 2048 else K // 4) + 16 if streamed else K + 64
         return chain * U32 * (ax @ np.abs(V).T)
     groups = K // group
     sg = np.abs(s)                                                       # [rows, groups]
@@ -127,10 +126,11 @@ def check_linear(M, N, K, fmt, group, act, bias, residual, pad, seed=0):
     B.moe_linear_w4(dims, x, w, b, res, out, ws, nb)
     torch.cuda.synchronize()
     X = f64(x)
-    if M > EXPANDED:
+    streamed = B.moe_linear_w4_plan(dims) == "streamed"
+    if not streamed:
         V = ow.bf16(V.astype(np.float32))  # (exact products of 4 and 8 bits, rounded once)
     z = X @ V.T + (f64(b) if bias else 0.0)
-    ez = linear_bounds(X, codes, s, V, fmt, group, M) + 2 * U32 * np.abs(z)
+    ez = linear_bounds(X, codes, s, V, fmt, group, streamed) + 2 * U32 * np.abs(z)
     y = ob.activation(z, act)
     if act == "swiglu":
         a, u, ea, eu = z[:, :N], z[:, N:], ez[:, :N], ez[:, N:]
@@ -157,6 +157,11 @@ def check_linear(M, N, K, fmt, group, act, bias, residual, pad, seed=0):
     (1, 1000, 160, "gelu", True, False, 8), (16, 56, 2144, "swiglu", True, True, 24), (17, 72, 4192, "none", False, True, 0), (1, 264, 7168, "swiglu", False, False, 0),
     (13, 4096, 512, "none", True, True, 0), (31, 200, 1120, "gelu", False, True, 8), (33, 104, 864, "swiglu", True, True, 0), (64, 48, 352, "none", False, False, 8),
     (65, 136, 416, "none", True, True, 0), (200, 264, 1088, "swiglu", True, True, 8), (300, 512, 2048, "relu", False, False, 0), (3, 8, 16384, "none", False, False, 0),
+    # tiles: one and two row tiles a wave, slices, ragged tokens, rows and blocks, SwiGLU on both
+    (129, 4104, 2080, "none", True, True, 8), (255, 1992, 1056, "swiglu", True, False, 0), (700, 4104, 416, "gelu", False, True, 0), (1024, 2056, 288, "swiglu", False, True, 8),
+    (129, 7168, 2048, "relu", True, True, 0), (100, 2048, 4096, "swiglu", True, False, 0), (1000, 4096, 160, "none", False, False, 0), (66, 3976, 4192, "silu", False, False, 0), (513, 8, 8192, "relu", True, True, 0),
+    # expanded
+    (1025, 136, 416, "none", True, True, 0), (1100, 72, 1088, "swiglu", True, True, 8), (1300, 264, 32, "relu", False, False, 0),
 ])
 @pytest.mark.parametrize("fmt,group", FORMATS)
 def test_linear_matches_oracle(M, N, K, act, bias, residual, pad, fmt, group):
@@ -201,9 +206,32 @@ def test_no_rows_and_no_weights():
     B.moe_dequantize_w4(empty, torch.empty(0, 128, device="cuda"))
 
 
-@pytest.mark.parametrize("M", [1, 100])
+def test_every_way_is_taken():
+    way = lambda M, N, K, act="none": B.moe_linear_w4_plan(B.make_linear_dims(M, N, K, "bf16", act))  # noqa: E731
+    assert {way(M, 7168, 2048) for M in (1, 5, 16, 17, 64)} == {"streamed"} and way(200, 512, 512) == "streamed"
+    assert {way(M, 7168, 2048) for M in (129, 256, 777, 1024)} == {"tiled"} and way(700, 4104, 416) == way(1024, 2056, 288, "swiglu") == "tiled"
+    assert way(1025, 8, 32) == way(5000, 4096, 4096) == "expanded"
+
+
+@pytest.mark.parametrize("fmt,group", FORMATS)
+def test_tiles_hold_infinities_and_nans_in_their_rows(fmt, group):
+    M, N, K = 300, 4096, 2048 + 128
+    w = random_w4(N, K, fmt, group, 5)[0]
+    dims = B.make_linear_dims(M, N, K)
+    assert B.moe_linear_w4_plan(dims) == "tiled"
+    x = torch.randn(M, K, generator=torch.Generator().manual_seed(1)).bfloat16().cuda()
+    y, z = (torch.empty(M, N, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    ws, nb = B.linear_w4_workspace(dims)
+    B.moe_linear_w4(dims, x, w, None, None, y, ws, nb)
+    x[3, 5], x[140, 2100], x[299, K - 1] = float("nan"), float("inf"), float("-inf")
+    B.moe_linear_w4(dims, x, w, None, None, z, ws, nb)
+    keep = [t for t in range(M) if t not in (3, 140, 299)]
+    assert torch.equal(z[keep], y[keep]) and bool(z[3].isnan().all()) and not bool(z[140].isfinite().any()) and not bool(z[299].isfinite().any())
+
+
+@pytest.mark.parametrize("M", [1, 24, 300, 1100])
 def test_graph_replays_match_eager(M):
-    N, K = 264, 1024
+    N, K = 1800, 2048
     w = random_w4(2 * N, K, "int4", 64, 2)[0]
     x = torch.randn(M, K, device="cuda").bfloat16()
     out = torch.empty(M, N, dtype=torch.bfloat16, device="cuda")
