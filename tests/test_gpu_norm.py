@@ -56,6 +56,7 @@ SHAPES = [
     (1, 1, 0), (1, 8, 0), (3, 7, 0), (5, 9, 7), (2, 63, 1), (1, 7168, 0), (4, 64, 0), (33, 264, 8), (257, 1003, 5),
     (64, 1024, 0), (7, 4096, 0), (2, 8200, 0), (3, 16385, 3), (2, 65536, 0), (2, 65535, 0), (1030, 136, 0), (2100, 520, 8),
     (1100, 1536, 0), (1025, 2049, 0), (1024, 7168, 0), (1030, 40, 4), (5000, 3, 0),
+    (600, 8200, 0), (300, 16390, 2),  # workgroups of 1024 threads that take several rows
 ]
 
 
