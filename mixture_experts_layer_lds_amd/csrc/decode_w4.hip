@@ -154,7 +154,7 @@ template <int FMT, int G, bool XLDS>
 __global__ __launch_bounds__(256) void k_dw4_up_pair(DecW4 a) {
   extern __shared__ __attribute__((aligned(16))) char dw_lds[];
   __shared__ int chosen;
-  typedef W4Stream<FMT, G, 1, 2, 1, XLDS, 1> Stream;
+  typedef W4Stream<FMT, G, 1, 2, 1, XLDS ? W4_XLDS : W4_XMEM, 1> Stream;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), W_ = blockDim.x >> 6;
   const int lane = threadIdx.x & 63, r16 = lane & 15, q = lane >> 4;
   const int pair = blockIdx.y, t = pair / a.K, k = pair - t * a.K, j0 = blockIdx.x * 16;
@@ -202,7 +202,7 @@ __global__ __launch_bounds__(256) void k_dw4_up_pair(DecW4 a) {
 template <int FMT, int G, bool XLDS>
 __global__ __launch_bounds__(1024) void k_dw4_down_pair(DecW4 a, int splits) {
   extern __shared__ __attribute__((aligned(16))) char dw_lds[];
-  typedef W4Stream<FMT, G, 1, 1, 1, XLDS, 1> Stream;
+  typedef W4Stream<FMT, G, 1, 1, 1, XLDS ? W4_XLDS : W4_XMEM, 1> Stream;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int lane = threadIdx.x & 63, r16 = lane & 15, q = lane >> 4;
   const int t = blockIdx.y, c0 = blockIdx.x * 16, k = wave / splits, part = wave - k * splits;
@@ -260,7 +260,8 @@ template <int FMT, int G, bool UP>
 __global__ __launch_bounds__(512) void k_dw4_expert(DecW4 a) {
   extern __shared__ __attribute__((aligned(16))) char dw_lds[];
   constexpr int RT = DW_RT, H = RT / 2, TILE = 256;
-  typedef W4Stream<FMT, G, 1, RT, 4, false, 1> Stream;
+  typedef W4Stream<FMT, G, 1, RT, 4, W4_XLINE, 1> Stream;
+  static_assert(RT * TILE * 4 == W4_XSLOT, "a wave's tokens and results take the same place");
   const int e = blockIdx.y, c = __builtin_amdgcn_readfirstlane(a.cnt[e]);
   if (c == 0) return;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), W_ = blockDim.x >> 6;
@@ -280,15 +281,20 @@ __global__ __launch_bounds__(512) void k_dw4_expert(DecW4 a) {
   ws.plane = (int64_t)a.E * rows * (FMT == W4_INT ? 2 : 4);
   ws.K = K;
   const int nb = w4_blocks(K), b0 = nb * wave / W_, b1 = nb * (wave + 1) / W_;
+  ws.xb = reinterpret_cast<const char*>(UP ? a.X : a.act);
+  ws.xs = dw_lds + wave * W4_XSLOT;
   float* res = reinterpret_cast<float*>(dw_lds);  // [wave][RT][token][16]
   for (int g0 = 0; g0 < c; g0 += 16) {
-    const int pair = lst[min(g0 + r16, c - 1)];
-    ws.x[0] = (UP ? a.X + (int64_t)(pair / a.K) * a.d : a.act + (int64_t)pair * a.n) + Stream::XQ * q;
+    if (g0 > 0) __syncthreads();  // (the last group's results, where the waves put their tokens, have been read)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int pair = lst[min(g0 + 4 * i + q, c - 1)];
+      ws.xo[0][i] = (uint32_t)(UP ? pair / a.K : pair) * (uint32_t)(K * 2) + 16 * r16;  // (below 2^31: T <= 1024, K <= 16)
+    }
     f32x4 acc[RT][1];
 #pragma unroll
     for (int r = 0; r < RT; ++r) acc[r][0] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
     if (b0 < b1) ws.run(b0, b1, acc);
-    __syncthreads();  // (the last group's results have been read)
 #pragma unroll
     for (int r = 0; r < RT; ++r) w4_put<4>(res + (wave * RT + r) * TILE, acc[r][0]);
     __syncthreads();

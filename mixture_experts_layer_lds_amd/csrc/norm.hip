@@ -503,9 +503,10 @@ __global__ __launch_bounds__(256) void k_norm_cols(NormBwd a) {
   part[a.cols + c] = db;
 }
 
-// dw and db: the workgroups' partial rows added in fp64, 8 runs of them per column, then the runs.
-constexpr int NORM_WG_COLS = 32, NORM_WG_RUNS = 8;
-__global__ __launch_bounds__(256) void k_norm_wgrad(const float* __restrict__ part, int parts, int cols, float* dw, float* db) {
+// dw and db: the workgroups' partial rows added in fp64, 32 runs of them per column, then the runs (512 rows of 1003:
+// 2 us less than 8 runs, whose trips to memory follow one another).
+constexpr int NORM_WG_COLS = 32, NORM_WG_RUNS = 32;
+__global__ __launch_bounds__(NORM_WG_COLS * NORM_WG_RUNS) void k_norm_wgrad(const float* __restrict__ part, int parts, int cols, float* dw, float* db) {
   __shared__ double red[NORM_WG_RUNS][NORM_WG_COLS + 1];
   const int cl = threadIdx.x % NORM_WG_COLS, run = threadIdx.x / NORM_WG_COLS;
   const int c = blockIdx.x * NORM_WG_COLS + cl;
@@ -530,10 +531,13 @@ __global__ __launch_bounds__(256) void k_norm_wgrad(const float* __restrict__ pa
 // are chunks (two a thread with 512 threads: one row of 7168 3.8 us, 4.1 with 1024); many rows up to three chunks
 // a thread (two with 512 threads), so that the lanes are busy, a row's sums cross few waves and the registers still
 // hold the next row.  So 256 threads go with 1 to 3 chunks, 512 with 1 or 2, 1024 (rows over 8192, forward) with 2.
-static int norm_tpr(int64_t cols, int64_t rows) {
+// `many`: in the forward 256 rows (999 x 1536 bf16 4.6 us, one chunk a thread 5.3), in the backward 1024 (14.1 us,
+// three chunks 17.4: fewer threads hold a row's sums of the vectors' gradients).
+constexpr int NORM_FWD_MANY = 256, NORM_BWD_MANY = 1024;
+static int norm_tpr(int64_t cols, int64_t rows, int many) {
   const int64_t chunks = cdiv(cols, 8);
   int tpr = 8;
-  while (tpr < 1024 && cdiv(chunks, tpr) > (tpr == 512 ? 2 : rows < 1024 || tpr < 64 ? 1 : 3)) tpr *= 2;
+  while (tpr < 1024 && cdiv(chunks, tpr) > (tpr == 512 ? 2 : rows < many || tpr < 64 ? 1 : 3)) tpr *= 2;
   return tpr;
 }
 static int norm_threads(int tpr) { return tpr > 64 ? tpr : 256; }
@@ -606,7 +610,7 @@ hipError_t launch_norm(const NormShape& s, const void* x, const void* residual, 
   a.sum = sum; a.y = y; a.mean = s.rms ? nullptr : mean; a.rstd = rstd;
   a.rows = s.rows; a.ldx = s.ldx; a.ldr = s.ldr; a.lds = s.lds; a.ldy = s.ldy;
   a.cols = (int)s.cols;
-  a.tpr = norm_tpr(s.cols, s.rows);
+  a.tpr = norm_tpr(s.cols, s.rows, NORM_FWD_MANY);
   a.eps = s.eps; a.wbf16 = s.wbf16; a.rms = s.rms;
   const int64_t vec = s.bf16 ? 8 : 4;
   const bool aligned = s.ldx % vec == 0 && s.ldy % vec == 0 && (!residual || s.ldr % vec == 0) && (!sum || s.lds % vec == 0);
@@ -614,14 +618,14 @@ hipError_t launch_norm(const NormShape& s, const void* x, const void* residual, 
 }
 
 size_t norm_bwd_workspace_bytes(const NormShape& s) {
-  const int tpr = norm_tpr(s.cols, s.rows);
+  const int tpr = norm_tpr(s.cols, s.rows, NORM_BWD_MANY);
   return (size_t)norm_grid(s.rows, tpr) * 2 * s.cols * sizeof(float);
 }
 
 hipError_t launch_norm_bwd(const NormShape& s, const void* dy, const void* sum, const void* weight, const float* mean,
                            const float* rstd, const void* dsum, void* dx, float* dweight, float* dbias, void* ws,
                            hipStream_t st) {
-  const int tpr = norm_tpr(s.cols, s.rows), grid = norm_grid(s.rows, tpr);
+  const int tpr = norm_tpr(s.cols, s.rows, NORM_BWD_MANY), grid = norm_grid(s.rows, tpr);
   const bool vectors = dweight || dbias;
   float* part = static_cast<float*>(ws);
   if (s.rows > 0) {
@@ -644,7 +648,7 @@ hipError_t launch_norm_bwd(const NormShape& s, const void* dy, const void* sum, 
     if (e != hipSuccess) return e;
   }
   if (!vectors) return hipSuccess;
-  k_norm_wgrad<<<dim3((unsigned)cdiv(s.cols, NORM_WG_COLS), 2), 256, 0, st>>>(part, s.rows > 0 ? grid : 0, (int)s.cols, dweight, dbias);
+  k_norm_wgrad<<<dim3((unsigned)cdiv(s.cols, NORM_WG_COLS), 2), NORM_WG_COLS * NORM_WG_RUNS, 0, st>>>(part, s.rows > 0 ? grid : 0, (int)s.cols, dweight, dbias);
   return hipGetLastError();
 }
 

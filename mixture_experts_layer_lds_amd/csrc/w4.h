@@ -60,11 +60,19 @@ __device__ __forceinline__ u32x4 w4_unpack_fp(uint32_t w, float s) {
                __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, s, 3))};
 }
 
+// Where a stream's tokens come from: memory, each lane the elements that its products take (one token, which all
+// lanes of a group read); LDS (W4Stage), in the order that the steps take them; memory by whole lines, which the
+// wave turns in its own part of LDS.  The last is for groups of 16 tokens, where reading a lane's 16 bytes from a
+// token each costs more in the caches than the bytes do: 32 x 14336 -> 4096 int4 21.6 us, by lines 19.5; 13 x 2048 ->
+// 7168 7.0 and 6.4.
+enum { W4_XMEM = 0, W4_XLDS = 1, W4_XLINE = 2 };
+constexpr int W4_XSLOT = 16 * 256;  // bytes of LDS per wave and group with W4_XLINE: [token][chunk ^ token]
+
 // One wave's stream over blocks of RT tiles of 16 weight rows against NG groups of tokens.
-// XLDS: the tokens lie in LDS (w4_stage), in the order that the steps take them; else in memory.
 // U: blocks per batch of loads.
-template <int FMT, int G, int NG, int RT, int NI, bool XLDS, int U>
+template <int FMT, int G, int NG, int RT, int NI, int XMODE, int U>
 struct W4Stream {
+  static constexpr bool XLDS = XMODE == W4_XLDS, XLINE = XMODE == W4_XLINE;
   static constexpr bool INT = FMT == W4_INT;
   static constexpr bool TR = INT && G < W4_BLOCK;     // blocks are transposed
   static constexpr int GS = INT ? G / 32 : 1;         // steps per group
@@ -75,6 +83,10 @@ struct W4Stream {
   const uint8_t* s[RT];  // INT: its scales' first bytes; FP: its scale byte of group lane / 16
   int64_t plane;         // bytes between scale planes (INT: per group; FP: per block)
   const bf16* x[NG];     // lane's token, at element XQ (lane / 16); XLDS: in LDS
+  // XLINE: lane's chunk lane % 16 of tokens 4 i + lane / 16, and the wave's LDS (NG W4_XSLOT)
+  const char* xb;
+  uint32_t xo[NG][4];
+  char* xs;
   int K;
 
   struct Codes {
@@ -104,14 +116,39 @@ struct W4Stream {
       }
     }
   }
-  __device__ __forceinline__ void load_x(u32x4 (&v)[NG][4], int blk) const {
+  // the tokens' elements of a block; of its first `left` (a multiple of 32), zeros behind
+  __device__ __forceinline__ void load_x(u32x4 (&v)[NG][4], int blk, int left = W4_BLOCK) const {
+    const int lane = threadIdx.x & 63;
+    const u32x4 zero = {0u, 0u, 0u, 0u};
 #pragma unroll
     for (int g = 0; g < NG; ++g)
 #pragma unroll
-      for (int j = 0; j < 4; ++j) v[g][j] = ld16(x[g] + blk * W4_BLOCK + j * XS);
+      for (int j = 0; j < 4; ++j) {
+        const int at = XLINE ? 8 * (lane & 15) : TR ? 32 * j : 32 * (lane >> 4);
+        const bool in = left == W4_BLOCK || at < left;
+        if constexpr (XLINE) v[g][j] = in ? ld16(xb + (xo[g][j] + (uint32_t)blk * (2 * W4_BLOCK))) : zero;
+        else v[g][j] = in ? ld16(x[g] + blk * W4_BLOCK + j * XS) : zero;
+      }
+  }
+  // XLINE: a block's elements from the order of memory to LDS, and the lane's of a step from there (the wave's LDS
+  // accesses stay in order)
+  __device__ __forceinline__ void put(const u32x4 (&v)[NG][4]) const {
+    const int lane = threadIdx.x & 63;
+#pragma unroll
+    for (int g = 0; g < NG; ++g)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int t = 4 * i + (lane >> 4);
+        st16(xs + g * W4_XSLOT + t * 256 + 16 * ((lane & 15) ^ t), INT ? w4_order_int(v[g][i]) : v[g][i]);
+      }
+  }
+  __device__ __forceinline__ u32x4 get(int g, int j) const {
+    const int lane = threadIdx.x & 63, r16 = lane & 15, q = lane >> 4;
+    return ld16(xs + g * W4_XSLOT + r16 * 256 + 16 * ((TR ? 4 * j + q : 4 * q + j) ^ r16));
   }
   // the first `steps` steps of a block
-  __device__ __forceinline__ void mma(Codes& b, const u32x4 (&xv)[NG][4], int steps, f32x4 (&acc)[RT][NG]) const {
+  __device__ __forceinline__ void mma(Codes& b, u32x4 (&xv)[NG][4], int steps, f32x4 (&acc)[RT][NG]) const {
+    if constexpr (XLINE) put(xv);
     if constexpr (INT) {
       constexpr uint32_t NEG = 0xbfc0bfc0u;  // -1.5, twice
       const u32x4 neg = {NEG, NEG, NEG, NEG};
@@ -122,15 +159,15 @@ struct W4Stream {
 #pragma unroll
       for (int h = 0; h < NS; ++h) {
         if (h * GS >= steps) break;
-        u32x4 xo[NG][GS];
+        u32x4 xi[NG][GS];
         f32x4 part[RT][NG];
 #pragma unroll
         for (int g = 0; g < NG; ++g) {
           f32x4 corr = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
           for (int j = 0; j < GS; ++j) {
-            xo[g][j] = XLDS ? xv[g][h * GS + j] : w4_order_int(xv[g][h * GS + j]);
-            corr = w4_mfma(xo[g][j], neg, corr);
+            xi[g][j] = XLINE ? get(g, h * GS + j) : XLDS ? xv[g][h * GS + j] : w4_order_int(xv[g][h * GS + j]);
+            corr = w4_mfma(xi[g][j], neg, corr);
           }
 #pragma unroll
           for (int r = 0; r < RT; ++r) part[r][g] = corr;
@@ -141,7 +178,7 @@ struct W4Stream {
           for (int j = 0; j < GS; ++j) {
             const u32x4 c = w4_unpack_int(b.c[r][h * GS + j]);
 #pragma unroll
-            for (int g = 0; g < NG; ++g) part[r][g] = w4_mfma(xo[g][j], c, part[r][g]);
+            for (int g = 0; g < NG; ++g) part[r][g] = w4_mfma(xi[g][j], c, part[r][g]);
           }
           const float f = __uint_as_float(b.s[r][h] << 16);
 #pragma unroll
@@ -152,6 +189,12 @@ struct W4Stream {
       }
     } else {
       (void)steps;  // (lanes behind the row have zeros in xv)
+      if constexpr (XLINE) {
+#pragma unroll
+        for (int g = 0; g < NG; ++g)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) xv[g][j] = get(g, j);
+      }
 #pragma unroll
       for (int r = 0; r < RT; ++r) {
         // 2^(e - 127); e = 0 is below the normal range
@@ -222,18 +265,11 @@ struct W4Stream {
   __device__ __forceinline__ void run(int a, int b, f32x4 (&acc)[RT][NG]) const { run(a, b, acc, [] {}); }
   // the part of a last block: K - 128 blk = 32, 64 or 96 elements
   __device__ __forceinline__ void tail(int blk, f32x4 (&acc)[RT][NG]) const {
-    const int q = (threadIdx.x & 63) >> 4, left = K - blk * W4_BLOCK;
+    const int left = K - blk * W4_BLOCK;
     Codes c;
     u32x4 v[NG][4];
     load_codes(c, blk, left);
-    const u32x4 zero = {0u, 0u, 0u, 0u};
-#pragma unroll
-    for (int g = 0; g < NG; ++g)
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const bool in = TR ? 32 * j < left : 32 * q < left;
-        v[g][j] = in ? ld16(x[g] + blk * W4_BLOCK + j * XS) : zero;
-      }
+    load_x(v, blk, left);
     mma(c, v, left / 32, acc);
   }
 };

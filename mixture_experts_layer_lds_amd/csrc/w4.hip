@@ -11,6 +11,7 @@
 namespace moe {
 
 // ---- quantisation ----
+// Bound by memory: reads the weights once, writes 9/32 (bf16) of their bytes.
 // One wave per row, one lane per 32 elements; a group's lanes (1, 2 or 4 neighbours) share its maximum.
 template <typename T, int FMT>
 __global__ __launch_bounds__(256) void k_quant_w4(const T* __restrict__ src, int64_t rows, int K, int group,
@@ -95,15 +96,20 @@ enum { W4_OUT = 0, W4_GLU = 1, W4_PART = 2 };  // the epilogue; SwiGLU's; partia
 //
 // Up to 4 tokens (NI = 1) each wave copies its run of X to LDS, in the order that the products take it, so that
 // the memory path carries little but codes.  With more, X (16 tokens of a block: 4 KB for a tile's 1 KB of
-// codes) comes from L2, which bounds the kernel unless a wave takes several tiles of rows with each block of X:
-// 13 x 14336 -> 4096 took 17.3 us with RT = 1 and the whole reduction in a workgroup, 11.7 with RT = 4 and four
-// slices (to which joining them adds about 2.5).
-template <int FMT, int G, int NG, int RT, int NI, bool XLDS, int U, int OUT>
+// codes) comes from L2 by whole lines, which bounds the kernel unless a wave takes several tiles of rows with each
+// block of X: 13 x 14336 -> 4096 took 17.3 us with RT = 1 and the whole reduction in a workgroup, 11.2 with RT = 4 and
+// four slices (to which joining them adds about 2).  What bounds it then is how short the work is: each wave has
+// 3 or 4 blocks, so asking for the first (about 2 us) and the waves' sums are half of its time; two blocks more under way
+// gave nothing.
+//   One token: the codes alone.  7168 -> 2048 SwiGLU fp4 (15.6 MB) 6.6 us a call, 2.4 TB/s, 14336 columns (62 MB) 16.1,
+// 3.9 TB/s: launch, first load and sums are some 3 us of either.
+template <int FMT, int G, int NG, int RT, int NI, int XMODE, int U, int OUT>
 __global__ __launch_bounds__(512) void k_w4_rows(const bf16* __restrict__ X, int64_t ldx, const uint8_t* __restrict__ codes,
                                                  const uint8_t* __restrict__ scales, int64_t plane, int m, int n, int K,
                                                  float* __restrict__ part, LinEpi<bf16> ep) {
   extern __shared__ __attribute__((aligned(16))) char w4_lds[];
-  typedef W4Stream<FMT, G, NG, RT, NI, XLDS, U> Stream;
+  typedef W4Stream<FMT, G, NG, RT, NI, XMODE, U> Stream;
+  constexpr bool XLDS = XMODE == W4_XLDS;
   constexpr int TOK = w4_tokens<NI>();
   constexpr bool GLU = OUT == W4_GLU;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), W_ = blockDim.x >> 6;
@@ -126,10 +132,16 @@ __global__ __launch_bounds__(512) void k_w4_rows(const bf16* __restrict__ X, int
   const int a = z0 + (z1 - z0) * wave / W_, b = z0 + (z1 - z0) * (wave + 1) / W_;
   bf16* xl = reinterpret_cast<bf16*>(w4_lds);
   const int xp = K + 8;  // LDS pitch of a token
+  if constexpr (XLDS) {
+    ws.x[0] = xl + min(w4_token<NI>(), m - 1) * xp + Stream::XQ * q;
+  } else {
+    ws.xb = reinterpret_cast<const char*>(X + (int64_t)t0 * ldx);
+    ws.xs = w4_lds + wave * (NG * W4_XSLOT);
 #pragma unroll
-  for (int g = 0; g < NG; ++g) {
-    const int t = min(t0 + g * TOK + w4_token<NI>(), m - 1);
-    ws.x[g] = (XLDS ? xl + t * xp : X + (int64_t)t * ldx) + Stream::XQ * q;
+    for (int g = 0; g < NG; ++g)
+#pragma unroll
+      for (int i = 0; i < 4; ++i)  // (below 2^29)
+        ws.xo[g][i] = (uint32_t)min(16 * g + 4 * i + q, m - 1 - t0) * (uint32_t)(ldx * 2) + 16 * r16;
   }
   W4Stage<FMT, 2> first;
   if constexpr (XLDS) first.request(X, xl, a * W4_BLOCK, min(b * W4_BLOCK, K));
@@ -149,7 +161,7 @@ __global__ __launch_bounds__(512) void k_w4_rows(const bf16* __restrict__ X, int
         }
       }
     });
-  if constexpr (XLDS) __syncthreads();  // (the results take the tokens' place)
+  if constexpr (XLDS || RT < 4) __syncthreads();  // (the results take the tokens' place: with RT = 4 the wave's own)
   float* res = reinterpret_cast<float*>(w4_lds);
   constexpr int TILE = TOK * 16;
 #pragma unroll
@@ -363,15 +375,15 @@ static W4TilePlan w4_tile_plan(const LinShape& s) {
   return best;
 }
 
-// Which way a product goes.  Up to 64 rows the codes are streamed; up to 1024 the quicker of streaming (4 us and 7.5
-// ps per row, row of W and element, 32 rows at a time: 256 x 1024 -> 1024 5.5 us, tiles 9) and tiles; beyond, W
-// is expanded (2048 x 2048 -> 7168 63 us, tiles 70; 1024 rows 45 and 38).
+// Which way a product goes.  Up to 64 rows the codes are streamed; up to 1024 the quicker of streaming (4 us and 6.5
+// fs per row, row of W and element, 32 rows at a time: 256 x 1024 -> 1024 4.9 us, tiles 9.2; 256 x 2048 -> 7168 29 and
+// 18) and tiles; beyond, W is expanded (2048 x 2048 -> 7168 63 us, tiles 70; 1024 rows 45 and 38).
 constexpr int W4_STREAM_ROWS = 64, W4_TILE_ROWS = 1024;
 int linear_w4_plan(const LinShape& s) {
   if (s.M <= W4_STREAM_ROWS) return W4_STREAMED;
   if (s.M > W4_TILE_ROWS) return W4_EXPANDED;
   const double rows = (double)(s.act == LIN_SWIGLU ? 2 * s.N : s.N);
-  const double stream = 4.0 + 7.5e-9 * (double)(cdiv(s.M, 32) * 32) * rows * (double)s.K;
+  const double stream = 4.0 + 6.5e-9 * (double)(cdiv(s.M, 32) * 32) * rows * (double)s.K;
   return stream < w4_tile_plan(s).us ? W4_STREAMED : W4_TILED;
 }
 template <int FMT, int RT>
@@ -423,10 +435,10 @@ static W4Plan w4_plan(const LinShape& s) {
     while (p.waves > 1 && blocks / p.waves < 4) p.waves /= 2;
     return p;
   }
-  // X costs its bytes once per workgroup, at about 13 TB/s over all L2s; fewer, taller workgroups need
-  // slices to fill the chip, and a second launch of about 2.5 us to join them
+  // X costs its bytes once per workgroup, at about 26 TB/s over all L2s; fewer, taller workgroups need slices to fill
+  // the chip, and a second launch of about 2.5 us to join them (64 x 7168 -> 2048 SwiGLU 12.4 us whole, 13.9 sliced)
   const int64_t groups = cdiv(s.M, 16 * p.ng);
-  const double x_us = 32.0 * p.ng * s.K * groups / 13e6;  // per row tile of a workgroup
+  const double x_us = 32.0 * p.ng * s.K * groups / 26e6;  // per row tile of a workgroup
   int best = 1;
   for (int rt : {4, 2}) {
     if (cdiv(rows, 16 * rt) * groups >= 200) {
@@ -446,40 +458,40 @@ static W4Plan w4_plan(const LinShape& s) {
   return p;
 }
 
-template <int FMT, int G, int NG, int RT, int NI, bool XLDS, int U>
+template <int FMT, int G, int NG, int RT, int NI, int XMODE, int U>
 static void w4_rows(const LinShape& s, const W4Plan& p, const W4View& w, const bf16* X, const LinEpi<bf16>& ep, float* part,
                     hipStream_t st) {
   const bool glu = s.act == LIN_SWIGLU;
   const int64_t rows = glu ? 2 * s.N : s.N;
   constexpr int TOK = w4_tokens<NI>();
   size_t lds = (size_t)p.waves * RT * NG * TOK * 16 * sizeof(float);
-  const size_t xl = XLDS ? (size_t)s.M * (s.K + 8) * sizeof(bf16) : 0;
+  const size_t xl = XMODE == W4_XLDS ? (size_t)s.M * (s.K + 8) * sizeof(bf16) : (size_t)p.waves * NG * W4_XSLOT;
   if (xl > lds) lds = xl;
   const dim3 grid((unsigned)cdiv(rows, 16 * RT), (unsigned)cdiv(s.M, TOK * NG), (unsigned)p.slices);
   const uint8_t* sc = static_cast<const uint8_t*>(w.scales);
   const int64_t plane = rows * (FMT == W4_INT ? 2 : 4);
   const int m = (int)s.M, K = (int)s.K, threads = p.waves * 64;
   if (p.slices > 1) {
-    if constexpr (!XLDS && RT == 4)
-      k_w4_rows<FMT, G, NG, RT, NI, XLDS, U, W4_PART><<<grid, threads, lds, st>>>(X, s.ldx, w.codes, sc, plane, m, (int)rows, K, part, ep);
+    if constexpr (RT == 4)
+      k_w4_rows<FMT, G, NG, RT, NI, XMODE, U, W4_PART><<<grid, threads, lds, st>>>(X, s.ldx, w.codes, sc, plane, m, (int)rows, K, part, ep);
   } else if (glu) {
-    k_w4_rows<FMT, G, NG, RT, NI, XLDS, U, W4_GLU><<<grid, threads, lds, st>>>(X, s.ldx, w.codes, sc, plane, m, (int)s.N, K, part, ep);
+    k_w4_rows<FMT, G, NG, RT, NI, XMODE, U, W4_GLU><<<grid, threads, lds, st>>>(X, s.ldx, w.codes, sc, plane, m, (int)s.N, K, part, ep);
   } else {
-    k_w4_rows<FMT, G, NG, RT, NI, XLDS, U, W4_OUT><<<grid, threads, lds, st>>>(X, s.ldx, w.codes, sc, plane, m, (int)s.N, K, part, ep);
+    k_w4_rows<FMT, G, NG, RT, NI, XMODE, U, W4_OUT><<<grid, threads, lds, st>>>(X, s.ldx, w.codes, sc, plane, m, (int)s.N, K, part, ep);
   }
 }
 template <int FMT, int G, int NG>
 static void w4_rows_rt(const LinShape& s, const W4Plan& p, const W4View& w, const bf16* X, const LinEpi<bf16>& ep, float* part,
                        hipStream_t st) {
-  if (p.rt == 4) w4_rows<FMT, G, NG, 4, 4, false, 1>(s, p, w, X, ep, part, st);
-  else if (p.rt == 2) w4_rows<FMT, G, NG, 2, 4, false, 1>(s, p, w, X, ep, part, st);
-  else w4_rows<FMT, G, NG, 1, 4, false, 1>(s, p, w, X, ep, part, st);
+  if (p.rt == 4) w4_rows<FMT, G, NG, 4, 4, W4_XLINE, 1>(s, p, w, X, ep, part, st);
+  else if (p.rt == 2) w4_rows<FMT, G, NG, 2, 4, W4_XLINE, 1>(s, p, w, X, ep, part, st);
+  else w4_rows<FMT, G, NG, 1, 4, W4_XLINE, 1>(s, p, w, X, ep, part, st);
 }
 template <int FMT, int G>
 static hipError_t w4_stream(const LinShape& s, const W4View& w, const bf16* X, const LinEpi<bf16>& ep, float* part, hipStream_t st) {
   const W4Plan p = w4_plan(s);
   // (small groups leave no registers for two blocks a batch)
-  if (p.lds) w4_rows<FMT, G, 1, 1, 1, true, FMT == W4_INT && G < 128 ? 1 : 2>(s, p, w, X, ep, part, st);
+  if (p.lds) w4_rows<FMT, G, 1, 1, 1, W4_XLDS, FMT == W4_INT && G < 128 ? 1 : 2>(s, p, w, X, ep, part, st);
   else if (p.ng == 1) w4_rows_rt<FMT, G, 1>(s, p, w, X, ep, part, st);
   else w4_rows_rt<FMT, G, 2>(s, p, w, X, ep, part, st);
   const hipError_t e = hipGetLastError();
