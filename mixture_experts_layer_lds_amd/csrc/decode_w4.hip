@@ -127,25 +127,17 @@ __device__ __forceinline__ int dw_choose(const DecW4& a, int t, int K) {
   return dw_choose_ej<16, WRITE>(a, t, K);
 }
 
-// The ranks of a token's choices by expert id: order[r] is the choice of the r-th smallest expert.  mine: lane
-// k holds the k-th choice.
+// A token's choices by expert id: order[r] is the choice of the r-th smallest expert.  mine: lane k holds the k-th
+// choice; no two are the same.
 __device__ __forceinline__ void dw_order(int mine, int K, int (&order)[16]) {
-  int ids[16];
+  const int lane = threadIdx.x & 63;
+  int rank = 0;
 #pragma unroll
-  for (int k = 0; k < 16; ++k) ids[k] = k < K ? __builtin_amdgcn_readlane(mine, k) : 0x7fffffff;
-  int prev = -1;
+  for (int k = 0; k < 16; ++k)
+    if (k < K) rank += __builtin_amdgcn_readlane(mine, k) < mine ? 1 : 0;
 #pragma unroll
-  for (int r = 0; r < 16; ++r) {
-    int best = 0x7fffffff, b = 0;
-#pragma unroll
-    for (int k = 0; k < 16; ++k)
-      if (ids[k] > prev && ids[k] < best) {
-        best = ids[k];
-        b = k;
-      }
-    order[r] = b;
-    prev = best;
-  }
+  for (int r = 0; r < 16; ++r)
+    order[r] = r < K ? (int)__builtin_ctzll(__builtin_amdgcn_ballot_w64(lane < K && rank == r) | (1ull << 63)) : 0;
 }
 
 // ---- by pairs ----
