@@ -11,10 +11,11 @@
 // difference of large sums.  All sums are fp32.
 //
 // Bound by memory: the forward reads x and r and writes s and y once, the backward reads dy, s and dsum and
-// writes dx.  32768 x 7168 bf16: forward 1.88 GB in 328 us (5.7 TB/s), backward 1.88 GB in 314 us (6.0 TB/s); 32768 x
-// 1536 backward 82 us (4.9 TB/s: the last rows, the partial rows and the second launch are a fifth of it).  What brought them there: the next row requested
-// while one is reduced (368 -> 340 us), a grid that just fills the chip (norm_grid), lane sums by DPP.  One row of 7168
-// is a launch: 3.8 us on the GPU, of which the rows' two trips to memory are about half.
+// writes dx.  32768 x 7168 bf16: forward 1.88 GB in 327 us (5.7 TB/s), backward 1.88 GB in 314 us (6.0 TB/s); 32768 x
+// 1536 backward 79 us (5.1 TB/s: the partial rows and the second launch are 5 us of it).  What brought them there: the
+// next row requested while one is reduced, a grid that just fills the chip (norm_grid), lane sums by DPP.  One row of
+// 7168 is a launch: 3.3 us on the GPU.  A backward of some hundred rows is bound by its chain of launch, row, sums and
+// second launch: 999 x 1003 fp32 12.8 us, 3 at the rate of a copy.
 #include "internal.h"
 
 namespace moe {
@@ -324,9 +325,9 @@ struct NormBwd {
   const void *dy, *s, *w, *dsum;
   const float *mean, *rstd;
   void* dx;       // may be null
-  float* part;    // [workgroups][dw, db][cols], or null
+  float* part;    // [workgroups][dw, db][pitch], or null
   int64_t rows, ldy, lds, ldr, ldx;
-  int cols, tpr;
+  int cols, tpr, pitch;
   bool wbf16, rms;
 };
 
@@ -404,7 +405,7 @@ __global__ __launch_bounds__(THREADS) void k_norm_bwd(NormBwd a) {
     }
   }
   if (!a.part) return;
-  float* part = a.part + (int64_t)blockIdx.x * 2 * cols;
+  float* part = a.part + (int64_t)blockIdx.x * 2 * a.pitch;
 #pragma unroll
   for (int j = 0; j < NC; ++j)
 #pragma unroll
@@ -425,11 +426,18 @@ __global__ __launch_bounds__(THREADS) void k_norm_bwd(NormBwd a) {
           }
         }
       }
-      if ((int)threadIdx.x < tpr) {
+      if ((int)threadIdx.x >= tpr) continue;
+      if constexpr (MODE != NORM_ANY) {  // (a partial row is whole chunks)
+        const int c = norm_col<MODE>(j, 0, tpr, t);
+        if (c < cols) {
+          st16(part + k * a.pitch + c, pack16<float>(v));
+          st16(part + k * a.pitch + c + 4, pack16<float>(v + 4));
+        }
+      } else {
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
           const int c = norm_col<MODE>(j, i, tpr, t);
-          if (c < cols) part[k * cols + c] = v[i];
+          if (c < cols) part[k * a.pitch + c] = v[i];
         }
       }
     }
@@ -498,15 +506,15 @@ __global__ __launch_bounds__(256) void k_norm_cols(NormBwd a) {
     dw = fmaf(g, (x - (a.rms ? 0.0f : a.mean[r])) * a.rstd[r], dw);
     db += g;
   }
-  float* part = a.part + (int64_t)blockIdx.y * 2 * a.cols;
+  float* part = a.part + (int64_t)blockIdx.y * 2 * a.pitch;
   part[c] = dw;
-  part[a.cols + c] = db;
+  part[a.pitch + c] = db;
 }
 
 // dw and db: the workgroups' partial rows added in fp64, 32 runs of them per column, then the runs (512 rows of 1003:
 // 2 us less than 8 runs, whose trips to memory follow one another).
 constexpr int NORM_WG_COLS = 32, NORM_WG_RUNS = 32;
-__global__ __launch_bounds__(NORM_WG_COLS * NORM_WG_RUNS) void k_norm_wgrad(const float* __restrict__ part, int parts, int cols, float* dw, float* db) {
+__global__ __launch_bounds__(NORM_WG_COLS * NORM_WG_RUNS) void k_norm_wgrad(const float* __restrict__ part, int parts, int cols, int pitch, float* dw, float* db) {
   __shared__ double red[NORM_WG_RUNS][NORM_WG_COLS + 1];
   const int cl = threadIdx.x % NORM_WG_COLS, run = threadIdx.x / NORM_WG_COLS;
   const int c = blockIdx.x * NORM_WG_COLS + cl;
@@ -514,9 +522,9 @@ __global__ __launch_bounds__(NORM_WG_COLS * NORM_WG_RUNS) void k_norm_wgrad(cons
   if (!out) return;  // (uniform)
   double v = 0.0;
   if (c < cols) {
-    const float* p = part + (int64_t)blockIdx.y * cols + c;
+    const float* p = part + (int64_t)blockIdx.y * pitch + c;
 #pragma unroll 8
-    for (int q = run; q < parts; q += NORM_WG_RUNS) v += (double)p[(int64_t)q * 2 * cols];
+    for (int q = run; q < parts; q += NORM_WG_RUNS) v += (double)p[(int64_t)q * 2 * pitch];
   }
   red[run][cl] = v;
   __syncthreads();
@@ -531,8 +539,8 @@ __global__ __launch_bounds__(NORM_WG_COLS * NORM_WG_RUNS) void k_norm_wgrad(cons
 // are chunks (two a thread with 512 threads: one row of 7168 3.8 us, 4.1 with 1024); many rows up to three chunks
 // a thread (two with 512 threads), so that the lanes are busy, a row's sums cross few waves and the registers still
 // hold the next row.  So 256 threads go with 1 to 3 chunks, 512 with 1 or 2, 1024 (rows over 8192, forward) with 2.
-// `many`: in the forward 256 rows (999 x 1536 bf16 4.6 us, one chunk a thread 5.3), in the backward 1024 (14.1 us,
-// three chunks 17.4: fewer threads hold a row's sums of the vectors' gradients).
+// `many`: in the forward 256 rows (999 x 1536 bf16 4.6 us, one chunk a thread 5.3), in the backward 1024 (999 x
+// 1003 fp32 14.9 us, with three chunks 17.4: fewer threads hold the sums of the vectors' gradients).
 constexpr int NORM_FWD_MANY = 256, NORM_BWD_MANY = 1024;
 static int norm_tpr(int64_t cols, int64_t rows, int many) {
   const int64_t chunks = cdiv(cols, 8);
@@ -617,9 +625,10 @@ hipError_t launch_norm(const NormShape& s, const void* x, const void* residual, 
   return norm_launch(a, s.bf16, aligned, norm_grid(s.rows, a.tpr), st);
 }
 
+static int norm_pitch(int64_t cols) { return (int)align_up((size_t)cols, 8); }
 size_t norm_bwd_workspace_bytes(const NormShape& s) {
   const int tpr = norm_tpr(s.cols, s.rows, NORM_BWD_MANY);
-  return (size_t)norm_grid(s.rows, tpr) * 2 * s.cols * sizeof(float);
+  return (size_t)norm_grid(s.rows, tpr) * 2 * norm_pitch(s.cols) * sizeof(float);
 }
 
 hipError_t launch_norm_bwd(const NormShape& s, const void* dy, const void* sum, const void* weight, const float* mean,
@@ -633,7 +642,7 @@ hipError_t launch_norm_bwd(const NormShape& s, const void* dy, const void* sum, 
     a.dy = dy; a.s = sum; a.w = weight; a.dsum = dsum; a.mean = mean; a.rstd = rstd;
     a.dx = dx; a.part = vectors ? part : nullptr;
     a.rows = s.rows; a.ldy = s.ldy; a.lds = s.lds; a.ldr = s.ldr; a.ldx = s.ldx;
-    a.cols = (int)s.cols; a.tpr = tpr; a.wbf16 = s.wbf16; a.rms = s.rms;
+    a.cols = (int)s.cols; a.tpr = tpr; a.pitch = norm_pitch(s.cols); a.wbf16 = s.wbf16; a.rms = s.rms;
     const int64_t vec = s.bf16 ? 8 : 4;
     const bool aligned = s.ldy % vec == 0 && s.lds % vec == 0 && (!dx || s.ldx % vec == 0) && (!dsum || s.ldr % vec == 0);
     const bool long_rows = norm_bwd_long(s.cols);
@@ -648,7 +657,7 @@ hipError_t launch_norm_bwd(const NormShape& s, const void* dy, const void* sum, 
     if (e != hipSuccess) return e;
   }
   if (!vectors) return hipSuccess;
-  k_norm_wgrad<<<dim3((unsigned)cdiv(s.cols, NORM_WG_COLS), 2), NORM_WG_COLS * NORM_WG_RUNS, 0, st>>>(part, s.rows > 0 ? grid : 0, (int)s.cols, dweight, dbias);
+  k_norm_wgrad<<<dim3((unsigned)cdiv(s.cols, NORM_WG_COLS), 2), NORM_WG_COLS * NORM_WG_RUNS, 0, st>>>(part, s.rows > 0 ? grid : 0, (int)s.cols, norm_pitch(s.cols), dweight, dbias);
   return hipGetLastError();
 }
 
