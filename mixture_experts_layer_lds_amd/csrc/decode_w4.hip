@@ -11,9 +11,12 @@
 //      one workgroup of a token writes its logits, choices and weights;
 //   3. down: a workgroup takes 16 output columns of a token, its waves the token's experts; their results are
 //      added in ascending expert order with their weights, in LDS.
+// DeepSeek-V3-shaped layer, T = 1, fp4: 4.8 + 32 + 18 us for 191 MB (up at 3.9 TB/s, down at 3.7: each launch has
+// some 3 us of choosing, first loads and sums in which no codes arrive); fine-grained layer, T = 8: 3.7 + 11 + 7.
 // By experts (more tokens): five launches.  1. router logits, which also clear the experts' counters; 2. top-K,
 // each pair appended to its expert's list (the order inside a list reaches no value); 3. gate/up and
 // 4. down on groups of 16 of an expert's tokens; 5. combine in ascending expert order.
+// d = 7168, n = 2048, E = 64, T = 16, fp4: 304 us for 1.24 GB, 4.1 TB/s.
 #include <cmath>
 
 #include "internal.h"
@@ -153,15 +156,13 @@ __global__ __launch_bounds__(256) void k_dw4_up_pair(DecW4 a) {
   const bf16* x = a.X + (int64_t)t * a.d;
   bf16* xl = reinterpret_cast<bf16*>(dw_lds);
   const int nb = w4_blocks(a.d), b0 = nb * wave / W_, b1 = nb * (wave + 1) / W_;
+  W4Stage<FMT, 1> stage;
+  if constexpr (XLDS) stage.request(x, xl, b0 * W4_BLOCK, min(b1 * W4_BLOCK, a.d));
   if (wave == 0) {
     const int e = blockIdx.x == 0 && k == 0 ? dw_choose<true>(a, t, a.K) : dw_choose<false>(a, t, k + 1);
     if (lane == k) chosen = e;
   }
-  if constexpr (XLDS) {
-    W4Stage<FMT, 1> stage;
-    stage.request(x, xl, b0 * W4_BLOCK, min(b1 * W4_BLOCK, a.d));
-    stage.write();
-  }
+  if constexpr (XLDS) stage.write();
   __syncthreads();
   const int e = __builtin_amdgcn_readfirstlane(chosen);
   const int64_t row = (int64_t)e * a.n + j0 + r16;
@@ -338,15 +339,15 @@ __global__ __launch_bounds__(256) void k_dw4_combine(DecW4 a) {
 constexpr int64_t DW_LDS = 65536;
 
 // Whether the call goes by pairs: that saves two launches, and reads an expert again for every further pair
-// that chose it (from the caches, mostly).  Where half as many pairs as experts at most are routed both take
-// the same (d = 7168, n = 2048, E = 64, T = 4: 164 and 167 us), beyond that the expected repeated bytes decide: d =
-// 1536, n = 256, E = 128, K = 8 takes 28 and 35 us at T = 9, 40 and 43 at 16 (28 MB), 55 and 47 at 24 (54 MB); d =
-// 7168, n = 2048, E = 64 309 and 228 at T = 8 (520 MB).
+// that chose it (from the caches, mostly).  Where half as many pairs as experts at most are routed pairs are never
+// slower (d = 7168, n = 2048, E = 64, T = 4: 154 and 161 us), beyond that the expected repeated bytes decide: d =
+// 1536, n = 256, E = 128, K = 8 int4 takes 32 and 41 us at T = 16 (28 MB), 42 and 45 at 24 (54 MB), 50 and 46 at 32
+// (86 MB); d = 7168, n = 2048, E = 64 289 and 259 at T = 8 (514 MB).
 static bool dw4_pairs(const Shape& s) {
   const double P = (double)s.T * s.K, E = s.E;
   if (P > 1024) return false;
   const double again = P - E * (1.0 - pow(1.0 - 1.0 / E, P));
-  return s.T == 1 || 2 * P <= E || again * 1.5 * (double)s.n * (double)s.d <= 28e6;
+  return s.T == 1 || 2 * P <= E || again * 1.5 * (double)s.n * (double)s.d <= 64e6;
 }
 
 template <int FMT, int G>

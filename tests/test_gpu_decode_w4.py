@@ -63,12 +63,13 @@ class Layer:
 
 
 # reductions of whole blocks of 128 and of one half; one to many tokens an expert (over 16 and 32: several passes);
-# by pairs (T = 1, 2 T K <= E, or small weights) and by experts (over 1024 pairs, or over 28 MB read again)
+# by pairs (T = 1, 2 T K <= E, or small weights) and by experts (over 1024 pairs, or over 64 MB read again)
 @pytest.mark.parametrize("T,d,n,E,K,skew", [
     (2, 256, 128, 8, 2, 0.0), (4, 320, 192, 40, 5, 0.0), (1, 128, 64, 16, 16, 0.0), (7, 1088, 448, 256, 8, 0.0), (1, 64, 2048, 1024, 3, 0.0), (1, 192, 128, 3, 2, 0.0),
     (49, 128, 64, 130, 2, 0.0), (300, 64, 64, 5, 4, 0.2), (1024, 128, 64, 40, 2, 0.0), (520, 192, 448, 3, 2, 0.0), (1, 40960, 64, 2, 1, 0.0), (1, 64, 40960, 2, 1, 0.0),
     (1, 64, 64, 4, 1, 0.0), (1, 1536, 256, 16, 8, 0.0), (8, 320, 192, 12, 2, 0.0), (3, 128, 64, 1, 1, 0.0), (40, 192, 128, 5, 2, 0.5),
     (100, 256, 320, 6, 3, 1.0), (17, 2048, 128, 8, 4, 0.0), (64, 448, 704, 8, 2, 0.3),
+    (100, 256, 640, 6, 3, 1.0), (64, 1088, 704, 8, 2, 0.3), (33, 704, 1088, 5, 5, 0.0), (512, 128, 64, 3, 2, 0.0),
 ])
 @pytest.mark.parametrize("fmt,group", FORMATS)
 def test_decode_matches_oracle(T, d, n, E, K, skew, fmt, group):
