@@ -538,7 +538,8 @@ def moe_norm_backward(dims, dy, s, weight, mean, rstd, dsum, dx, dweight, dbias,
 class Gradients:
     """A list of gradient tensors (contiguous, bf16 or fp32, on one GPU) and where moe_grad_clip writes the
     scaled ones: ``dst``, tensors of the same sizes and types, or in place without it.  Holds the tensors and
-    the device table that the kernels read; made once for tensors that stay where they are."""
+    the device table that the kernels read; made once for tensors that stay where they are, and kept until the calls
+    on it have run (a captured graph: as long as it is replayed)."""
 
     def __init__(self, src, dst=None):
         self.src = list(src)
