@@ -501,7 +501,7 @@ typedef struct moe_w4 {
 int64_t moe_w4_scale_bytes(int64_t rows, int64_t K, int32_t format, int32_t group);
 
 /* moe_quantize_w4 — codes and scales of src [rows, K] dtype (MOE_BF16 or MOE_F32), finite values, into
- * the arrays of w.  INT4: s = max|group| / 7 rounded to bf16 (1 for a group of zeros), c the nearest integer
+ * the arrays of w.  INT4: s = max|group| / 7 rounded to bf16 (1 where that is 0), c the nearest integer
  * to x / s, ties to even, plus 8 (1 .. 15).  FP4: the smallest power of two s with max|group| / s <= 6, within
  * 2^-127 .. 2^127 (1 for zeros), c the nearest value to x / s, ties to the even code.  rows >= 0. */
 moe_status moe_quantize_w4(int64_t rows, int64_t K, int dtype, const void* src, const moe_w4* w, void* stream);

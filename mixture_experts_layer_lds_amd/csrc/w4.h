@@ -311,7 +311,7 @@ __device__ __forceinline__ void w4_put(float* p, f32x4 v) {
 #pragma unroll
   for (int i = 0; i < NI; ++i) p[(NI * q + i) * 16 + r16] = v[i];
 }
-// A lane's token in a group: of the 16 rows of A.
-template <int NI> __device__ __forceinline__ int w4_token() { return NI == 1 ? (threadIdx.x & 15) >> 2 : threadIdx.x & 15; }
+// With NI = 1, a lane's token: of A's 16 rows every fourth counts.
+__device__ __forceinline__ int w4_token() { return (threadIdx.x & 15) >> 2; }
 
 }  // namespace moe

@@ -133,7 +133,7 @@ __global__ __launch_bounds__(512) void k_w4_rows(const bf16* __restrict__ X, int
   bf16* xl = reinterpret_cast<bf16*>(w4_lds);
   const int xp = K + 8;  // LDS pitch of a token
   if constexpr (XLDS) {
-    ws.x[0] = xl + min(w4_token<NI>(), m - 1) * xp + Stream::XQ * q;
+    ws.x[0] = xl + min(w4_token(), m - 1) * xp + Stream::XQ * q;
   } else {
     ws.xb = reinterpret_cast<const char*>(X + (int64_t)t0 * ldx);
     ws.xs = w4_lds + wave * (NG * W4_XSLOT);

@@ -127,3 +127,69 @@ def test_quantised_layer_end_to_end():
         assert float((v - w.float()).norm() / w.float().norm()) < 0.15
     L.check()
     assert ow.E2M1[7] == 6.0
+
+
+@pytest.mark.parametrize("T,K,E", [(2, 2, 520), (600, 2, 520)])
+def test_code_offsets_past_32_bits(T, K, E):
+    """4.4e9 bytes of codes a matrix, every token on the last two experts, by pairs and by experts."""
+    d = n = 4096
+    g = torch.Generator(device="cuda").manual_seed(5)
+
+    def weights(rows, k):
+        codes = torch.randint(0, 256, (rows, k // 2), dtype=torch.uint8, device="cuda", generator=g)
+        scales = torch.randint(118, 121, (k // 128, rows, 4), dtype=torch.uint8, device="cuda", generator=g)
+        return B.W4(codes, scales, "fp4", 32)
+
+    def values(w, rows):  # of the last two experts
+        v = torch.empty(2, rows, w.K, device="cuda")
+        B.moe_dequantize_w4(B.W4(w.codes[-2 * rows:].contiguous(), w.scales[:, -2 * rows:].contiguous(), "fp4", 32), v)
+        return v.double()
+
+    gate, up, down = weights(E * n, d), weights(E * n, d), weights(E * d, n)
+    assert gate.codes.numel() > 1 << 32
+    X = torch.randn(T, d, device="cuda", generator=g).bfloat16()
+    W_r = torch.zeros(E, d, dtype=torch.bfloat16, device="cuda")
+    bias = torch.zeros(E, device="cuda")
+    bias[-2:] = torch.tensor([3.0, 3.5])
+    dims = B.make_dims(T, d, n, E, K)
+    logits, idx = torch.empty(T, E, device="cuda"), torch.empty(T, K, dtype=torch.int32, device="cuda")
+    w, out = torch.empty(T, K, device="cuda"), torch.empty(T, d, dtype=torch.bfloat16, device="cuda")
+    B.moe_decode_w4(dims, X, W_r, bias, gate, up, down, logits, idx, w, out, *B.workspace(dims, B.OP_DECODE))
+    assert torch.equal(idx, torch.tensor([E - 1, E - 2], dtype=torch.int32, device="cuda").expand(T, 2))
+    x, Vg, Vu, Vd = X.double(), values(gate, n), values(up, n), values(down, d)
+    ref = sum(w[:, 1 - e:2 - e].double() * ((torch.nn.functional.silu(x @ Vg[e].T) * (x @ Vu[e].T)) @ Vd[e].T) for e in range(2))
+    assert_close("out", f64(out), f64(ref), TOL["bf16"])
+
+
+@pytest.mark.parametrize("T", [3, 200])
+def test_a_token_that_is_not_finite_stays_alone(T):
+    L = Layer(T, 256, 640, 6, 3, "int4", 64)
+    L.step()
+    want = [t.clone() for t in (L.logits, L.idx, L.w, L.out)]
+    L.X[1, 7] = float("nan")
+    L.step()
+    keep = [t for t in range(T) if t != 1]
+    for got, ref in zip((L.logits, L.idx, L.w, L.out), want):
+        assert torch.equal(got[keep], ref[keep])
+    assert bool(L.logits[1].isnan().all()) and bool(L.out[1].isnan().all())
+    assert sorted(set(L.idx[1].tolist())) == [0, 1, 2]  # (of equal keys the lowest ids)
+
+
+@pytest.mark.parametrize("T", [2, 200])
+def test_calls_on_two_streams_with_their_own_workspaces(T):
+    layers = [Layer(T, 256, 640, 6, 3, "fp4", 32, seed=k) for k in (1, 2)]
+    for L in layers:
+        L.step()
+    torch.cuda.synchronize()
+    want = [L.out.clone() for L in layers]
+    streams = [torch.cuda.Stream() for _ in layers]
+    for _ in range(5):
+        for L in layers:
+            L.out.zero_()
+        torch.cuda.synchronize()
+        for L, s in zip(layers, streams):
+            with torch.cuda.stream(s):
+                L.step()
+        torch.cuda.synchronize()
+        for L, o in zip(layers, want):
+            assert torch.equal(L.out, o)

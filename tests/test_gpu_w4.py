@@ -261,3 +261,31 @@ def test_code_offsets_past_32_bits():
     B.moe_dequantize_w4(B.W4(again.codes[-64:].contiguous(), again.scales[:, -64:].contiguous(), "int4", 128), back)
     # the last group's largest value is -4 = -8 x 0.5: s = bf16(4 / 7), its values are off by at most half of it
     assert torch.equal(back[:-1], out[:-1]) and bool(((back[-1].float() - out[-1].float()).abs() <= 2 / 7 * 1.01).all())
+
+
+@pytest.mark.parametrize("M,N,K", [(1, 520, 1024), (16, 264, 14336), (130, 2056, 4096), (1100, 264, 512)])
+def test_calls_on_two_streams_with_their_own_workspaces(M, N, K):
+    w = random_w4(N, K, "int4", 128, 9)[0]
+    dims = B.make_linear_dims(M, N, K)
+    g = torch.Generator().manual_seed(M)
+    runs = [dict(x=torch.randn(M, K, generator=g).bfloat16().cuda(), out=torch.empty(M, N, dtype=torch.bfloat16, device="cuda"), ws=B.linear_w4_workspace(dims))
+            for _ in range(2)]
+
+    def step(r):
+        B.moe_linear_w4(dims, r["x"], w, None, None, r["out"], *r["ws"])
+
+    for r in runs:
+        step(r)
+    torch.cuda.synchronize()
+    want = [r["out"].clone() for r in runs]
+    streams = [torch.cuda.Stream() for _ in runs]
+    for _ in range(5):
+        for r in runs:
+            r["out"].zero_()
+        torch.cuda.synchronize()
+        for r, s in zip(runs, streams):
+            with torch.cuda.stream(s):
+                step(r)
+        torch.cuda.synchronize()
+        for r, o in zip(runs, want):
+            assert torch.equal(r["out"], o)
