@@ -354,37 +354,111 @@ __global__ __launch_bounds__(W4G_WAVES * 64, 2) void k_w4_tile(const bf16* __res
   }
 }
 
+constexpr int64_t W4_LDS = 65536;
+
+// How a product is cut: by the shape alone, so that the workspace is known without the weights.
+struct W4Plan {
+  bool lds;         // up to 4 tokens, which lie in LDS
+  int ng, rt;       // token groups of 16 and row tiles of a workgroup
+  int slices, waves;
+  double us;        // more than 16 rows: the model's time
+};
+static int w4_waves(int blocks) {  // of a workgroup: at least two blocks each
+  int waves = 8;
+  while (waves > 1 && blocks / waves < 2) waves /= 2;
+  return waves;
+}
+static W4Plan w4_plan(const LinShape& s) {
+  const bool glu = s.act == LIN_SWIGLU;
+  const int64_t rows = glu ? 2 * s.N : s.N;
+  const int blocks = w4_blocks((int)s.K);
+  W4Plan p;
+  p.lds = s.M <= 4 && s.M * (s.K + 8) * 2 <= W4_LDS;
+  p.ng = s.M <= 16 ? 1 : 2;
+  p.rt = 1;
+  p.slices = 1;
+  p.us = 0.0;
+  if (p.lds) {
+    // 8 waves where the grid would not fill the chip otherwise (2 x 2048 x 7168: 5.9 us, 6.6 with 4;
+    // 2 x 14336 x 4096: 14.8, 14.0)
+    const int64_t tiles = rows / 16;
+    p.waves = 4;
+    while (p.waves < 8 && tiles * p.waves < 2048) p.waves *= 2;
+    while (p.waves > 1 && blocks / p.waves < 4) p.waves /= 2;
+    return p;
+  }
+  const int64_t groups = cdiv(s.M, 16 * p.ng);
+  if (p.ng == 1) {
+    // X costs its bytes once per workgroup, at about 26 TB/s over all L2s; fewer, taller workgroups need slices to fill
+    // the chip, and a second launch of about 2.5 us to join them
+    const double x_us = 32.0 * s.K / 26e6;  // per row tile of a workgroup
+    int best = 1;
+    for (int rt : {4, 2}) {
+      if (cdiv(rows, 16 * rt) >= 200) {
+        best = rt;
+        break;
+      }
+    }
+    const double whole = x_us * cdiv(rows, 16 * best), sliced = x_us * cdiv(rows, 64) + 2.5;
+    p.rt = best;
+    if (best < 4 && sliced < whole) {
+      p.rt = 4;
+      while (p.slices < 8 && cdiv(rows, 64) * p.slices < 200 && blocks / (2 * p.slices) >= 8) p.slices *= 2;
+      if (p.slices == 1) p.rt = best;
+    }
+    p.waves = w4_waves(blocks / p.slices);
+    return p;
+  }
+  // 32 tokens a workgroup: by a model of measured times.  A round of 256 workgroups of eight waves, b blocks of 128 a
+  // wave, takes 3 + 2 b us with four row tiles and 2.4 + 1.15 b with two; with one, where two workgroups share a
+  // CU, each round adds 1.5 + 0.68 b to 2 + 0.42 b (96 x 7168 -> 2048 SwiGLU fp4 17.1, 21.8 and 22.7 us, 64 rows 16.8, 12.3
+  // and 16.7, 32 rows 16.4, 12.0 and 10.6).
+  for (int rt : {4, 2, 1})
+    for (int slices = 1; slices <= (rt == 4 ? 8 : 1) && (slices == 1 || blocks / slices >= 16); slices *= 2) {
+      const int waves = w4_waves(blocks / slices);
+      const double b = (double)blocks / slices / 8.0;
+      const double rounds = (double)cdiv(cdiv(rows, 16 * rt) * groups * slices * waves, 8 * 256);
+      double us = rt == 4 ? 2.5 + rounds * (3.0 + 2.0 * b) : rt == 2 ? 2.0 + rounds * (2.4 + 1.15 * b) : 2.0 + 0.42 * b + rounds * (1.5 + 0.68 * b);
+      if (slices > 1) us += 3.0 + (double)slices * (double)s.M * (double)rows * 8.0 / 4e6;  // joining them
+      if (p.us == 0.0 || us < p.us) {
+        p.us = us;
+        p.rt = rt;
+        p.slices = slices;
+        p.waves = waves;
+      }
+    }
+  return p;
+}
+
 struct W4TilePlan {
   int rt, slices;
   double us;
 };
-// Row tiles per wave and slices by a model of measured times: a block of the loop takes 1.1 us (RT = 2: 1.45) with one
-// workgroup a CU and 1.7 (2.3) with two; joining slices 3 us and their bytes at 4 TB/s.
+// Row tiles per wave and slices by a model of measured times: a block of the loop takes 1 us (RT = 2: 1.45) with one
+// workgroup a CU and 1.7 (2.3) with two; joining slices takes 1.5 us and their bytes at 6 TB/s.
 static W4TilePlan w4_tile_plan(const LinShape& s) {
   const int64_t rows = s.act == LIN_SWIGLU ? 2 * s.N : s.N, groups = cdiv(s.M, W4G_TOK), blocks = w4_blocks((int)s.K);
   W4TilePlan best{1, 1, 0.0};
   for (int rt = 1; rt <= 2; ++rt)
     for (int slices = 1; slices <= 4 && (slices == 1 || blocks / slices >= 2); slices *= 2) {
       const int64_t wgs = cdiv(rows, 16 * W4G_WAVES * rt) * groups * slices, rest = wgs % 512;
-      const double one = rt == 1 ? 1.1 : 1.45, two = rt == 1 ? 1.7 : 2.3;
+      const double one = rt == 1 ? 1.0 : 1.45, two = rt == 1 ? 1.7 : 2.3;
       double us = (double)cdiv(blocks, slices) * ((double)(wgs / 512) * two + (rest == 0 ? 0.0 : rest <= 256 ? one : two));
       us += 1.5;  // the launch and the first block
-      if (slices > 1) us += 3.0 + (double)slices * (double)s.M * (double)rows * 8.0 / 4e6;
+      if (slices > 1) us += 1.5 + (double)slices * (double)s.M * (double)rows * 8.0 / 6e6;
       if (best.us == 0.0 || us < best.us) best = W4TilePlan{rt, slices, us};
     }
   return best;
 }
 
-// Which way a product goes.  Up to 64 rows the codes are streamed; up to 1024 the quicker of streaming (4 us and 6.5
-// fs per row, row of W and element, 32 rows at a time: 256 x 1024 -> 1024 4.9 us, tiles 9.2; 256 x 2048 -> 7168 29 and
-// 18) and tiles; beyond, W is expanded (2048 x 2048 -> 7168 63 us, tiles 70; 1024 rows 45 and 38).
+// Which way a product goes.  Up to 64 rows the codes are streamed; up to 1024 the quicker of streaming and tiles by the
+// models above (256 x 1024 -> 1024 4.9 us, tiles 9.2; 256 x 2048 -> 7168 30 and 18); beyond, W is expanded (2048 x
+// 2048 -> 7168 63 us, tiles 70; 1024 rows 45 and 38).
 constexpr int W4_STREAM_ROWS = 64, W4_TILE_ROWS = 1024;
 int linear_w4_plan(const LinShape& s) {
   if (s.M <= W4_STREAM_ROWS) return W4_STREAMED;
   if (s.M > W4_TILE_ROWS) return W4_EXPANDED;
-  const double rows = (double)(s.act == LIN_SWIGLU ? 2 * s.N : s.N);
-  const double stream = 4.0 + 6.5e-9 * (double)(cdiv(s.M, 32) * 32) * rows * (double)s.K;
-  return stream < w4_tile_plan(s).us ? W4_STREAMED : W4_TILED;
+  return w4_plan(s).us < w4_tile_plan(s).us ? W4_STREAMED : W4_TILED;
 }
 template <int FMT, int RT>
 static void w4_tile_rt(const LinShape& s, const W4TilePlan& p, const W4View& w, const bf16* X, const LinEpi<bf16>& ep, float* part,
@@ -407,55 +481,6 @@ static hipError_t w4_tile(const LinShape& s, const W4View& w, const bf16* X, con
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess || p.slices == 1) return e;
   return launch_lin_finish(part, p.slices, (int)s.M, (int)s.N, (int)(s.act == LIN_SWIGLU ? 2 * s.N : s.N), ep, st);
-}
-
-constexpr int64_t W4_LDS = 65536;
-
-// How a product is cut: by the shape alone, so that the workspace is known without the weights.
-struct W4Plan {
-  bool lds;         // up to 4 tokens, which lie in LDS
-  int ng, rt;       // token groups of 16 and row tiles of a workgroup
-  int slices, waves;
-};
-static W4Plan w4_plan(const LinShape& s) {
-  const bool glu = s.act == LIN_SWIGLU;
-  const int64_t rows = glu ? 2 * s.N : s.N;
-  const int blocks = w4_blocks((int)s.K);
-  W4Plan p;
-  p.lds = s.M <= 4 && s.M * (s.K + 8) * 2 <= W4_LDS;
-  p.ng = s.M <= 16 ? 1 : 2;
-  p.rt = 1;
-  p.slices = 1;
-  if (p.lds) {
-    // 8 waves where the grid would not fill the chip otherwise (2 x 2048 x 7168: 5.9 us, 6.6 with 4;
-    // 2 x 14336 x 4096: 14.8, 14.0)
-    const int64_t tiles = rows / 16;
-    p.waves = 4;
-    while (p.waves < 8 && tiles * p.waves < 2048) p.waves *= 2;
-    while (p.waves > 1 && blocks / p.waves < 4) p.waves /= 2;
-    return p;
-  }
-  // X costs its bytes once per workgroup, at about 26 TB/s over all L2s; fewer, taller workgroups need slices to fill
-  // the chip, and a second launch of about 2.5 us to join them (64 x 7168 -> 2048 SwiGLU 12.4 us whole, 13.9 sliced)
-  const int64_t groups = cdiv(s.M, 16 * p.ng);
-  const double x_us = 32.0 * p.ng * s.K * groups / 26e6;  // per row tile of a workgroup
-  int best = 1;
-  for (int rt : {4, 2}) {
-    if (cdiv(rows, 16 * rt) * groups >= 200) {
-      best = rt;
-      break;
-    }
-  }
-  const double whole = x_us * cdiv(rows, 16 * best), sliced = x_us * cdiv(rows, 64) + 2.5;
-  p.rt = best;
-  if (best < 4 && sliced < whole) {
-    p.rt = 4;
-    while (p.slices < 8 && cdiv(rows, 64) * groups * p.slices < 200 && blocks / (2 * p.slices) >= 8) p.slices *= 2;
-    if (p.slices == 1) p.rt = best;
-  }
-  p.waves = 8;
-  while (p.waves > 1 && blocks / p.slices / p.waves < 2) p.waves /= 2;
-  return p;
 }
 
 template <int FMT, int G, int NG, int RT, int NI, int XMODE, int U>
