@@ -37,7 +37,7 @@ struct DecW4 {
   bf16* out;
   int32_t* cnt;   // [E]
   int32_t* list;  // [E][T] pair ids t * K + k
-  bf16* act;      // [T * K][n]
+  bf16* act;      // [T * K][n], the activation rounded as in the layer's other forms: the MFMAs of down take bf16
   float* y;       // [T * K][d]
   float* part;    // [slices][T][E] sums of slices of the router logits (one slice: they are the logits)
   int T, d, n, E, K, slices;

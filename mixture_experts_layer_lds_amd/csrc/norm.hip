@@ -514,7 +514,8 @@ __global__ __launch_bounds__(256) void k_norm_cols(NormBwd a) {
 // dw and db: the workgroups' partial rows added in fp64, 32 runs of them per column, then the runs (512 rows of 1003:
 // 2 us less than 8 runs, whose trips to memory follow one another).
 constexpr int NORM_WG_COLS = 32, NORM_WG_RUNS = 32;
-__global__ __launch_bounds__(NORM_WG_COLS * NORM_WG_RUNS) void k_norm_wgrad(const float* __restrict__ part, int parts, int cols, int pitch, float* dw, float* db) {
+__global__ __launch_bounds__(NORM_WG_COLS * NORM_WG_RUNS) void k_norm_wgrad(const float* __restrict__ part, int parts, int cols,
+                                                                           int pitch, float* dw, float* db) {
   __shared__ double red[NORM_WG_RUNS][NORM_WG_COLS + 1];
   const int cl = threadIdx.x % NORM_WG_COLS, run = threadIdx.x / NORM_WG_COLS;
   const int c = blockIdx.x * NORM_WG_COLS + cl;
@@ -657,7 +658,8 @@ hipError_t launch_norm_bwd(const NormShape& s, const void* dy, const void* sum, 
     if (e != hipSuccess) return e;
   }
   if (!vectors) return hipSuccess;
-  k_norm_wgrad<<<dim3((unsigned)cdiv(s.cols, NORM_WG_COLS), 2), NORM_WG_COLS * NORM_WG_RUNS, 0, st>>>(part, s.rows > 0 ? grid : 0, (int)s.cols, norm_pitch(s.cols), dweight, dbias);
+  k_norm_wgrad<<<dim3((unsigned)cdiv(s.cols, NORM_WG_COLS), 2), NORM_WG_COLS * NORM_WG_RUNS, 0, st>>>(
+      part, s.rows > 0 ? grid : 0, (int)s.cols, norm_pitch(s.cols), dweight, dbias);
   return hipGetLastError();
 }
 

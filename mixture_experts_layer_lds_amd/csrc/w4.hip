@@ -11,7 +11,7 @@
 namespace moe {
 
 // ---- quantisation ----
-// Bound by memory: reads the weights once, writes 9/32 (bf16) of their bytes.
+// Bound by memory: 16384 x 7168 bf16 80 to 89 us (3.3 to 3.7 TB/s), fp32 119 to 138 (3.9 to 4.5).
 // One wave per row, one lane per 32 elements; a group's lanes (1, 2 or 4 neighbours) share its maximum.
 template <typename T, int FMT>
 __global__ __launch_bounds__(256) void k_quant_w4(const T* __restrict__ src, int64_t rows, int K, int group,
@@ -59,6 +59,7 @@ __global__ __launch_bounds__(256) void k_quant_w4(const T* __restrict__ src, int
 }
 
 // ---- expansion: a thread takes 8 codes of a word, so that a wave writes whole lines ----
+// 16384 x 7168 to bf16 63 us with groups of 128 (4.7 TB/s), 82 to 89 with 32, whose scales lie in planes of their own.
 template <typename T, int FMT>
 __global__ __launch_bounds__(256) void k_expand_w4(const uint8_t* __restrict__ codes, const void* __restrict__ scales, int64_t rows,
                                                    int K, int group, T* __restrict__ out) {
@@ -418,7 +419,9 @@ static W4Plan w4_plan(const LinShape& s) {
       const int waves = w4_waves(blocks / slices);
       const double b = (double)blocks / slices / 8.0;
       const double rounds = (double)cdiv(cdiv(rows, 16 * rt) * groups * slices * waves, 8 * 256);
-      double us = rt == 4 ? 2.5 + rounds * (3.0 + 2.0 * b) : rt == 2 ? 2.0 + rounds * (2.4 + 1.15 * b) : 2.0 + 0.42 * b + rounds * (1.5 + 0.68 * b);
+      double us = rt == 4   ? 2.5 + rounds * (3.0 + 2.0 * b)
+                  : rt == 2 ? 2.0 + rounds * (2.4 + 1.15 * b)
+                            : 2.0 + 0.42 * b + rounds * (1.5 + 0.68 * b);
       if (slices > 1) us += 3.0 + (double)slices * (double)s.M * (double)rows * 8.0 / 4e6;  // joining them
       if (p.us == 0.0 || us < p.us) {
         p.us = us;
