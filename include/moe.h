@@ -386,7 +386,7 @@ typedef enum { MOE_NORM_LAYER = 0, MOE_NORM_RMS = 1 } moe_norm_kind;
 
 /* Shape (host struct).  rows (0 .. 2^31 - 1) of cols elements (1 .. 65536, any number).  ldx: row stride
  * in elements of x and dx; ldr: of residual and dsum; lds: of sum; ldy: of y and dy (>= cols, at most
- * 2^40; 0 = dense; rows whose strides keep 16-byte alignment move in 16-byte accesses).
+ * 2^40; 0 = dense; strides that keep 16-byte alignment are the quickest).
  * dtype: type of x, residual, sum, y and of the gradients dy, dsum, dx.  wtype: type of weight and bias
  * (their gradients are fp32).  kind: a moe_norm_kind.  eps: finite, >= 0.  flags: reserved, must be 0. */
 typedef struct moe_norm_dims {

@@ -20,16 +20,17 @@
 
 namespace moe {
 
-// How rows are accessed: element by element; in 16-byte accesses with a part of a chunk at the end; in 16-byte
-// accesses throughout.
-enum { NORM_ANY = 0, NORM_PART = 1, NORM_WHOLE = 2 };
-
-// Element i of a thread's chunk j lies in column norm_col(j, i): 8 neighbours per chunk where rows are
-// 16-byte aligned, else neighbours in neighbouring threads, which keeps 2- and 4-byte accesses coalesced.
-template <int MODE>
-__device__ __forceinline__ int norm_col(int j, int i, int tpr, int t) {
-  return MODE != NORM_ANY ? (j * tpr + t) * 8 + i : (j * 8 + i) * tpr + t;
+// Rows are accessed in 16 bytes whatever their alignment (their strides may be any; 30000 x 1600 bf16 of stride
+// 1603 by elements took 704 us, so 103): with a part of a chunk at the row's end, or in whole chunks throughout.
+enum { NORM_PART = 0, NORM_WHOLE = 1 };
+typedef u32x4 __attribute__((aligned(2))) u32x4_any;
+__device__ __forceinline__ u32x4 norm_ld16(const void* p) {
+  return __builtin_nontemporal_load(static_cast<const u32x4_any*>(p));
 }
+__device__ __forceinline__ void norm_st16(void* p, u32x4 v) { __builtin_nontemporal_store(v, static_cast<u32x4_any*>(p)); }
+
+// The first column of a thread's chunk j, 8 neighbours.
+__device__ __forceinline__ int norm_col(int j, int tpr, int t) { return (j * tpr + t) * 8; }
 
 // 8 elements as they lie in memory.
 template <typename T> struct Raw8 { u32x4 v[8 / Vec<T>::N]; };
@@ -38,27 +39,27 @@ template <typename T> struct Raw8 { u32x4 v[8 / Vec<T>::N]; };
 template <typename T, int MODE>
 __device__ __forceinline__ Raw8<T> norm_load1(const T* p, int cols, int tpr, int t, int j) {
   constexpr int NV = 8 / Vec<T>::N;
-  const int c = norm_col<MODE>(j, 0, tpr, t);
+  const int c = norm_col(j, tpr, t);
   Raw8<T> r;
   if constexpr (MODE == NORM_WHOLE) {
 #pragma unroll
     for (int v = 0; v < NV; ++v) r.v[v] = u32x4{0u, 0u, 0u, 0u};
     if (c < cols) {
 #pragma unroll
-      for (int v = 0; v < NV; ++v) r.v[v] = ld16_nt(p + c + v * Vec<T>::N);
+      for (int v = 0; v < NV; ++v) r.v[v] = norm_ld16(p + c + v * Vec<T>::N);
     }
     return r;
   }
-  if (MODE == NORM_PART && c + 8 <= cols) {
+  if (c + 8 <= cols) {
 #pragma unroll
-    for (int v = 0; v < NV; ++v) r.v[v] = ld16_nt(p + c + v * Vec<T>::N);
+    for (int v = 0; v < NV; ++v) r.v[v] = norm_ld16(p + c + v * Vec<T>::N);
     return r;
   }
   float f[8] = {0, 0, 0, 0, 0, 0, 0, 0};
   if (c < cols) {
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      const int ci = norm_col<MODE>(j, i, tpr, t);
+      const int ci = norm_col(j, tpr, t) + i;
       if (ci < cols) f[i] = to_f32(p[ci]);
     }
   }
@@ -78,17 +79,17 @@ __device__ __forceinline__ void norm_unpack(const Raw8<T>& r, float* f) {
 }
 template <typename T, int MODE>
 __device__ __forceinline__ void norm_store(T* p, int cols, int tpr, int t, int j, const Raw8<T>& r) {
-  const int c = norm_col<MODE>(j, 0, tpr, t);
+  const int c = norm_col(j, tpr, t);
   if (c >= cols) return;
   if (MODE == NORM_WHOLE || (MODE == NORM_PART && c + 8 <= cols)) {
 #pragma unroll
-    for (int v = 0; v < 8 / Vec<T>::N; ++v) st16_nt(p + c + v * Vec<T>::N, r.v[v]);
+    for (int v = 0; v < 8 / Vec<T>::N; ++v) norm_st16(p + c + v * Vec<T>::N, r.v[v]);
   } else {
     float f[8];
     norm_unpack<T>(r, f);
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      const int ci = norm_col<MODE>(j, i, tpr, t);
+      const int ci = norm_col(j, tpr, t) + i;
       if (ci < cols) p[ci] = from_f32<T>(f[i]);
     }
   }
@@ -104,11 +105,11 @@ __device__ __forceinline__ Raw8<T> norm_pack(const float* f) {
 // Weight or bias of a thread's chunk j (null: the value `none`).
 template <int MODE>
 __device__ __forceinline__ void norm_vector(const void* p, bool wbf16, float none, int cols, int tpr, int t, int j, float* w) {
-  const int c0 = norm_col<MODE>(j, 0, tpr, t);
+  const int c0 = norm_col(j, tpr, t);
 #pragma unroll
   for (int i = 0; i < 8; ++i) w[i] = none;
   if (!p || c0 >= cols) return;
-  if (MODE != NORM_ANY && c0 + 8 <= cols) {
+  if (MODE == NORM_WHOLE || c0 + 8 <= cols) {
     if (wbf16) {
       unpack16<bf16>(ld16(static_cast<const bf16*>(p) + c0), w);
     } else {
@@ -119,7 +120,7 @@ __device__ __forceinline__ void norm_vector(const void* p, bool wbf16, float non
   }
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
-    const int c = norm_col<MODE>(j, i, tpr, t);
+    const int c = norm_col(j, tpr, t) + i;
     if (c < cols) w[i] = wbf16 ? to_f32(static_cast<const bf16*>(p)[c]) : static_cast<const float*>(p)[c];
   }
 }
@@ -234,7 +235,7 @@ __global__ __launch_bounds__(THREADS) void k_norm(NormFwd a) {
     for (int j = 0; j < NC; ++j)
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        const float d = norm_col<MODE>(j, i, tpr, t) < cols ? f[j * 8 + i] - mu : 0.0f;
+        const float d = norm_col(j, tpr, t) + i < cols ? f[j * 8 + i] - mu : 0.0f;
         f[j * 8 + i] = d;
         q[0] = fmaf(d, d, q[0]);
       }
@@ -299,7 +300,7 @@ __global__ __launch_bounds__(1024) void k_norm_long(NormFwd a) {
       again(j, f);
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        const float d = norm_col<MODE>(j, i, tpr, t) < cols ? f[i] - mu : 0.0f;
+        const float d = norm_col(j, tpr, t) + i < cols ? f[i] - mu : 0.0f;
         q[0] = fmaf(d, d, q[0]);
       }
     }
@@ -378,7 +379,7 @@ __global__ __launch_bounds__(THREADS) void k_norm_bwd(NormBwd a) {
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         const int k = j * 8 + i;
-        const float xh = norm_col<MODE>(j, i, tpr, t) < cols ? (x[i] - mu) * rstd : 0.0f;
+        const float xh = norm_col(j, tpr, t) + i < cols ? (x[i] - mu) * rstd : 0.0f;
         dw[k] = fmaf(g[i], xh, dw[k]);
         db[k] += g[i];
         const float gw = g[i] * w[k];
@@ -427,18 +428,10 @@ __global__ __launch_bounds__(THREADS) void k_norm_bwd(NormBwd a) {
         }
       }
       if ((int)threadIdx.x >= tpr) continue;
-      if constexpr (MODE != NORM_ANY) {  // (a partial row is whole chunks)
-        const int c = norm_col<MODE>(j, 0, tpr, t);
-        if (c < cols) {
-          st16(part + k * a.pitch + c, pack16<float>(v));
-          st16(part + k * a.pitch + c + 4, pack16<float>(v + 4));
-        }
-      } else {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const int c = norm_col<MODE>(j, i, tpr, t);
-          if (c < cols) part[k * a.pitch + c] = v[i];
-        }
+      const int c = norm_col(j, tpr, t);
+      if (c < cols) {  // (a partial row is whole chunks)
+        st16(part + k * a.pitch + c, pack16<float>(v));
+        st16(part + k * a.pitch + c + 4, pack16<float>(v + 4));
       }
     }
 }
@@ -466,7 +459,7 @@ __global__ __launch_bounds__(1024) void k_norm_bwd_long(NormBwd a) {
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         gw[i] *= w[i];
-        xh[i] = norm_col<MODE>(j, i, tpr, t) < cols ? (xh[i] - mu) * rstd : 0.0f;
+        xh[i] = norm_col(j, tpr, t) + i < cols ? (xh[i] - mu) * rstd : 0.0f;
       }
     };
     for (int j = 0; j < nc; ++j) {
@@ -597,16 +590,14 @@ static void norm_chunks(const Args& a, int grid, int threads, hipStream_t st) {
   else norm_go<T, 3, MODE>(a, grid, threads, st);
 }
 template <class Args>
-static hipError_t norm_launch(const Args& a, bool is_bf16, bool aligned, int grid, hipStream_t st) {
-  const int threads = norm_threads(a.tpr), mode = !aligned ? NORM_ANY : a.cols % 8 ? NORM_PART : NORM_WHOLE;
+static hipError_t norm_launch(const Args& a, bool is_bf16, int grid, hipStream_t st) {
+  const int threads = norm_threads(a.tpr), mode = a.cols % 8 ? NORM_PART : NORM_WHOLE;
   if (is_bf16) {
     if (mode == NORM_WHOLE) norm_chunks<bf16, NORM_WHOLE>(a, grid, threads, st);
-    else if (mode == NORM_PART) norm_chunks<bf16, NORM_PART>(a, grid, threads, st);
-    else norm_chunks<bf16, NORM_ANY>(a, grid, threads, st);
+    else norm_chunks<bf16, NORM_PART>(a, grid, threads, st);
   } else {
     if (mode == NORM_WHOLE) norm_chunks<float, NORM_WHOLE>(a, grid, threads, st);
-    else if (mode == NORM_PART) norm_chunks<float, NORM_PART>(a, grid, threads, st);
-    else norm_chunks<float, NORM_ANY>(a, grid, threads, st);
+    else norm_chunks<float, NORM_PART>(a, grid, threads, st);
   }
   return hipGetLastError();
 }
@@ -621,9 +612,7 @@ hipError_t launch_norm(const NormShape& s, const void* x, const void* residual, 
   a.cols = (int)s.cols;
   a.tpr = norm_tpr(s.cols, s.rows, NORM_FWD_MANY);
   a.eps = s.eps; a.wbf16 = s.wbf16; a.rms = s.rms;
-  const int64_t vec = s.bf16 ? 8 : 4;
-  const bool aligned = s.ldx % vec == 0 && s.ldy % vec == 0 && (!residual || s.ldr % vec == 0) && (!sum || s.lds % vec == 0);
-  return norm_launch(a, s.bf16, aligned, norm_grid(s.rows, a.tpr), st);
+  return norm_launch(a, s.bf16, norm_grid(s.rows, a.tpr), st);
 }
 
 static int norm_pitch(int64_t cols) { return (int)align_up((size_t)cols, 8); }
@@ -644,8 +633,6 @@ hipError_t launch_norm_bwd(const NormShape& s, const void* dy, const void* sum, 
     a.dx = dx; a.part = vectors ? part : nullptr;
     a.rows = s.rows; a.ldy = s.ldy; a.lds = s.lds; a.ldr = s.ldr; a.ldx = s.ldx;
     a.cols = (int)s.cols; a.tpr = tpr; a.pitch = norm_pitch(s.cols); a.wbf16 = s.wbf16; a.rms = s.rms;
-    const int64_t vec = s.bf16 ? 8 : 4;
-    const bool aligned = s.ldy % vec == 0 && s.lds % vec == 0 && (!dx || s.ldx % vec == 0) && (!dsum || s.ldr % vec == 0);
     const bool long_rows = norm_bwd_long(s.cols);
     hipError_t e = hipSuccess;
     if (vectors && long_rows) {  // (first: dx may take the place of dy or s)
@@ -654,7 +641,7 @@ hipError_t launch_norm_bwd(const NormShape& s, const void* dy, const void* sum, 
       else k_norm_cols<float><<<cols, 256, 0, st>>>(a);
       e = hipGetLastError();
     }
-    if (e == hipSuccess && (dx || !long_rows)) e = norm_launch(a, s.bf16, aligned, grid, st);
+    if (e == hipSuccess && (dx || !long_rows)) e = norm_launch(a, s.bf16, grid, st);
     if (e != hipSuccess) return e;
   }
   if (!vectors) return hipSuccess;
