@@ -432,7 +432,7 @@ moe_status moe_norm_backward(const moe_norm_dims* dims, const void* dy, const vo
 
 /* One gradient tensor (host struct): n consecutive elements of dtype at src (n >= 0).  dst: where
  * moe_grad_clip writes the scaled ones: src itself (in place; also meant by NULL) or other n elements.
- * src and dst need only the element's own alignment; those on 16-byte borders move in 16-byte accesses.
+ * src and dst need only the element's own alignment.
  * reserved: 0. */
 typedef struct moe_grad {
   const void* src;

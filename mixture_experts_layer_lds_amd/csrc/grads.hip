@@ -20,7 +20,15 @@ namespace moe {
 
 constexpr int GRAD_GRID = 1024;     // workgroups
 
-enum { GRAD_BF16 = 1, GRAD_ALIGNED = 2 };
+enum { GRAD_BF16 = 1 };
+
+// 16 bytes of any tensor: they need no more than an element's alignment.
+typedef u32x4 __attribute__((aligned(2))) u32x4_any;
+__device__ __forceinline__ u32x4 grad_ld16(const void* p) { return *static_cast<const u32x4_any*>(p); }
+__device__ __forceinline__ u32x4 grad_ld16_nt(const void* p) {
+  return __builtin_nontemporal_load(static_cast<const u32x4_any*>(p));
+}
+__device__ __forceinline__ void grad_st16_nt(void* p, u32x4 v) { __builtin_nontemporal_store(v, static_cast<u32x4_any*>(p)); }
 
 __device__ __forceinline__ double grad_block_sum(double v, double* red) {
 #pragma unroll
@@ -33,70 +41,62 @@ __device__ __forceinline__ double grad_block_sum(double v, double* red) {
 }
 
 template <typename T>
-__device__ __forceinline__ double grad_square(const T* p, int n, bool aligned) {
+__device__ __forceinline__ double grad_square(const T* p, int n) {
   constexpr int VEC = Vec<T>::N, U = 4;
   double v = 0.0;
-  int i = 0;
-  if (aligned) {
-    const int step = 256 * VEC;
-    int k = threadIdx.x * VEC;
-    for (; k + (U - 1) * step + VEC <= n; k += U * step) {
-      u32x4 r[U];
+  const int step = 256 * VEC;
+  int k = threadIdx.x * VEC;
+  for (; k + (U - 1) * step + VEC <= n; k += U * step) {
+    u32x4 r[U];
 #pragma unroll
-      for (int u = 0; u < U; ++u) r[u] = ld16(p + k + u * step);
+    for (int u = 0; u < U; ++u) r[u] = grad_ld16(p + k + u * step);
 #pragma unroll
-      for (int u = 0; u < U; ++u) {
-        float f[VEC];
-        unpack16<T>(r[u], f);
-#pragma unroll
-        for (int q = 0; q < VEC; ++q) v = fma((double)f[q], (double)f[q], v);
-      }
-    }
-    for (; k + VEC <= n; k += step) {
+    for (int u = 0; u < U; ++u) {
       float f[VEC];
-      unpack16<T>(ld16(p + k), f);
+      unpack16<T>(r[u], f);
 #pragma unroll
       for (int q = 0; q < VEC; ++q) v = fma((double)f[q], (double)f[q], v);
     }
-    i = n / VEC * VEC;
   }
-  for (int k = i + threadIdx.x; k < n; k += 256) {
-    const double x = (double)to_f32(p[k]);
+  for (; k + VEC <= n; k += step) {
+    float f[VEC];
+    unpack16<T>(grad_ld16(p + k), f);
+#pragma unroll
+    for (int q = 0; q < VEC; ++q) v = fma((double)f[q], (double)f[q], v);
+  }
+  for (int i = n / VEC * VEC + threadIdx.x; i < n; i += 256) {
+    const double x = (double)to_f32(p[i]);
     v = fma(x, x, v);
   }
   return v;
 }
 
 template <typename T>
-__device__ __forceinline__ void grad_scale(const T* p, T* o, int n, bool aligned, float c) {
+__device__ __forceinline__ void grad_scale(const T* p, T* o, int n, float c) {
   constexpr int VEC = Vec<T>::N, U = 4;
-  int i = 0;
-  if (aligned) {
-    const int step = 256 * VEC;
-    int k = threadIdx.x * VEC;
-    for (; k + (U - 1) * step + VEC <= n; k += U * step) {
-      u32x4 r[U];
+  const int step = 256 * VEC;
+  int k = threadIdx.x * VEC;
+  for (; k + (U - 1) * step + VEC <= n; k += U * step) {
+    u32x4 r[U];
 #pragma unroll
-      for (int u = 0; u < U; ++u) r[u] = ld16_nt(p + k + u * step);
+    for (int u = 0; u < U; ++u) r[u] = grad_ld16_nt(p + k + u * step);
 #pragma unroll
-      for (int u = 0; u < U; ++u) {
-        float f[VEC];
-        unpack16<T>(r[u], f);
-#pragma unroll
-        for (int q = 0; q < VEC; ++q) f[q] *= c;
-        st16_nt(o + k + u * step, pack16<T>(f));
-      }
-    }
-    for (; k + VEC <= n; k += step) {
+    for (int u = 0; u < U; ++u) {
       float f[VEC];
-      unpack16<T>(ld16_nt(p + k), f);
+      unpack16<T>(r[u], f);
 #pragma unroll
       for (int q = 0; q < VEC; ++q) f[q] *= c;
-      st16_nt(o + k, pack16<T>(f));
+      grad_st16_nt(o + k + u * step, pack16<T>(f));
     }
-    i = n / VEC * VEC;
   }
-  for (int k = i + threadIdx.x; k < n; k += 256) o[k] = from_f32<T>(to_f32(p[k]) * c);
+  for (; k + VEC <= n; k += step) {
+    float f[VEC];
+    unpack16<T>(grad_ld16_nt(p + k), f);
+#pragma unroll
+    for (int q = 0; q < VEC; ++q) f[q] *= c;
+    grad_st16_nt(o + k, pack16<T>(f));
+  }
+  for (int i = n / VEC * VEC + threadIdx.x; i < n; i += 256) o[i] = from_f32<T>(to_f32(p[i]) * c);
 }
 
 // f(entry, first element of the chunk, elements in it)
@@ -115,9 +115,8 @@ __global__ __launch_bounds__(256) void k_grad_square(const GradEntry* table, con
   __shared__ double red[4];
   double v = 0.0;
   grad_chunks(table, tensor, chunks, [&](const GradEntry& g, int64_t at, int n) {
-    const bool al = g.kind & GRAD_ALIGNED;
-    if (g.kind & GRAD_BF16) v += grad_square<bf16>(static_cast<const bf16*>(g.src) + at, n, al);
-    else v += grad_square<float>(static_cast<const float*>(g.src) + at, n, al);
+    if (g.kind & GRAD_BF16) v += grad_square<bf16>(static_cast<const bf16*>(g.src) + at, n);
+    else v += grad_square<float>(static_cast<const float*>(g.src) + at, n);
   });
   v = grad_block_sum(v, red);
   if (threadIdx.x == 0) part[blockIdx.x] = v;
@@ -150,9 +149,8 @@ __global__ __launch_bounds__(256) void k_grad_scale(const GradEntry* table, cons
   const float c = cut ? (float)(max_norm / n) : 1.0f;
   grad_chunks(table, tensor, chunks, [&](const GradEntry& g, int64_t at, int m) {
     if (!cut && g.src == g.dst) return;
-    const bool al = g.kind & GRAD_ALIGNED;
-    if (g.kind & GRAD_BF16) grad_scale<bf16>(static_cast<const bf16*>(g.src) + at, static_cast<bf16*>(g.dst) + at, m, al, c);
-    else grad_scale<float>(static_cast<const float*>(g.src) + at, static_cast<float*>(g.dst) + at, m, al, c);
+    if (g.kind & GRAD_BF16) grad_scale<bf16>(static_cast<const bf16*>(g.src) + at, static_cast<bf16*>(g.dst) + at, m, c);
+    else grad_scale<float>(static_cast<const float*>(g.src) + at, static_cast<float*>(g.dst) + at, m, c);
   });
 }
 
@@ -165,8 +163,7 @@ int grad_table(const GradTensor* list, int count, void* host) {
   int32_t* tensor = reinterpret_cast<int32_t*>(e + count);
   int chunks = 0;
   for (int i = 0; i < count; ++i) {
-    const uintptr_t both = reinterpret_cast<uintptr_t>(list[i].src) | reinterpret_cast<uintptr_t>(list[i].dst);
-    e[i] = GradEntry{list[i].src, list[i].dst, list[i].n, chunks, (list[i].bf16 ? GRAD_BF16 : 0) | (both % 16 == 0 ? GRAD_ALIGNED : 0)};
+    e[i] = GradEntry{list[i].src, list[i].dst, list[i].n, chunks, list[i].bf16 ? GRAD_BF16 : 0};
     for (int64_t c = cdiv(list[i].n, GRAD_CHUNK); c > 0; --c) tensor[chunks++] = i;
   }
   return chunks;
