@@ -516,7 +516,9 @@ moe_status moe_dequantize_w4(int64_t rows, int64_t K, int dtype, const moe_w4* w
  *  one of three ways, by dims alone (moe_linear_w4_plan): STREAMED (up to 64 rows always), where products are exact
  *  and an INT4 group's sum is multiplied by its scale in fp32; TILED (some hundred rows) and EXPANDED (many), where
  *  an INT4 value is rounded to bf16 before it is multiplied (half a step, 2^-9 of it; FP4 values are exact).
- *  An infinite element of X may make its row's results NaN where the exact sum is infinite.
+ *  Any finite X is in range: a result is lost to infinity only where a weight, an INT4 group's sum times its scale, a
+ *  partial sum of those or the result itself is beyond its type, and an element whose weight is zero adds nothing, however large.  An
+ *  infinite element of X may make its row's results NaN where the exact sum is infinite.
  *  residual may be out (with the same stride).  M = 0 does nothing.
  *  ws: moe_linear_w4_workspace_bytes(dims) bytes. */
 enum { MOE_W4_STREAMED = 0, MOE_W4_TILED = 1, MOE_W4_EXPANDED = 2 };

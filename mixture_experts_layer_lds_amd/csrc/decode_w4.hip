@@ -156,7 +156,7 @@ __global__ __launch_bounds__(256) void k_dw4_up_pair(DecW4 a) {
   const bf16* x = a.X + (int64_t)t * a.d;
   bf16* xl = reinterpret_cast<bf16*>(dw_lds);
   const int nb = w4_blocks(a.d), b0 = nb * wave / W_, b1 = nb * (wave + 1) / W_;
-  W4Stage<FMT, 1> stage;
+  W4Stage<1> stage;
   if constexpr (XLDS) stage.request(x, xl, b0 * W4_BLOCK, min(b1 * W4_BLOCK, a.d));
   if (wave == 0) {
     const int e = blockIdx.x == 0 && k == 0 ? dw_choose<true>(a, t, a.K) : dw_choose<false>(a, t, k + 1);
@@ -205,7 +205,7 @@ __global__ __launch_bounds__(1024) void k_dw4_down_pair(DecW4 a, int splits) {
   const bf16* x = a.act + ((int64_t)t * a.K + k) * a.n;
   bf16* xl = reinterpret_cast<bf16*>(dw_lds) + (int64_t)k * a.n;
   const int nb = w4_blocks(a.n), b0 = nb * part / splits, b1 = nb * (part + 1) / splits;
-  W4Stage<FMT, 4> stage;
+  W4Stage<4> stage;
   if constexpr (XLDS) stage.request(x, xl, b0 * W4_BLOCK, min(b1 * W4_BLOCK, a.n));
   const int64_t row = (int64_t)__builtin_amdgcn_readlane(ids, k) * a.d + c0 + r16;
   Stream ws;

@@ -10,11 +10,14 @@
 //
 // INT (value (c - 8) s, s bf16 per group of G = 32, 64 or 128): a group has to be whole steps, since its
 // scale multiplies their sum.  With G = 128 the block is one group and steps are as above; with less, four
-// lane swaps transpose the block so that step j holds elements 32 j .. 32 j + 31.  A code is put into the
-// mantissa of 1.0 (1 + c / 16: one shift and one and-or for two codes) and the excess of 1.5 is taken off by
-// a product of the tokens with -1.5, from which the group's sum starts: all products are exact, sums fp32,
-// and the weights are never rounded.  Two codes that share a register are four apart; the tokens' elements
-// are put into the same order, 0 4 1 5 2 6 3 7, by four byte permutations.
+// lane swaps transpose the block so that step j holds elements 32 j .. 32 j + 31.  c - 8 = 4 h + l with the digits
+// h = -2 .. 1 and l = 0 .. 3, each of which is an E2M1 value (h / 2 and l / 2): six bit operations make both digits of
+// eight codes, the same conversions as for FP make them bf16, and a product is two MFMAs.  All products are exact, sums
+// fp32, the weights are never rounded, and a weight of zero adds nothing however large the token's element is.
+// (Codes as 1 + c / 16 and a product of the tokens with -1.5 to take the excess off are eight operations and fewer
+// MFMAs, 14.1 us for 13 x 14336 -> 4096 with groups of 128 where this takes 14.9 and level for one token, but every sum
+// carries rounding errors of 24 |x| s, and overflows for large finite x.)  The digits are scaled by 2^-12, which the end
+// takes back: 128 products of any finite x stay in range.
 //
 // With the weights as B a lane's results all belong to one weight row, so a group costs one scale conversion
 // and NI multiply-adds a lane: 4 for up to 16 tokens, 1 for up to 4, which then lie in every fourth row of A.
@@ -44,15 +47,6 @@ __device__ __forceinline__ void w4_transpose(u32x4& c) {
   c = u32x4{x[0], x[1], y[0], y[1]};
 }
 
-// Eight codes of a word as 1 + c / 16 in bf16, elements 0 4 1 5 2 6 3 7.
-__device__ __forceinline__ u32x4 w4_unpack_int(uint32_t w) {
-  constexpr uint32_t M = 0x00780078u, ONE = 0x3f803f80u;
-  return u32x4{((w << 3) & M) | ONE, ((w >> 1) & M) | ONE, ((w >> 5) & M) | ONE, ((w >> 9) & M) | ONE};
-}
-__device__ __forceinline__ u32x4 w4_order_int(u32x4 x) {
-  return u32x4{__builtin_amdgcn_perm(x[2], x[0], 0x05040100u), __builtin_amdgcn_perm(x[2], x[0], 0x07060302u),
-               __builtin_amdgcn_perm(x[3], x[1], 0x05040100u), __builtin_amdgcn_perm(x[3], x[1], 0x07060302u)};
-}
 __device__ __forceinline__ u32x4 w4_unpack_fp(uint32_t w, float s) {
   return u32x4{__builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, s, 0)),
                __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, s, 1)),
@@ -60,9 +54,18 @@ __device__ __forceinline__ u32x4 w4_unpack_fp(uint32_t w, float s) {
                __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, s, 3))};
 }
 
+// The digits of eight INT codes as E2M1 codes: l / 2 (its code is l) and h / 2 (-1, -0.5, 0, 0.5 for the code's upper two
+// bits 0 .. 3).
+__device__ __forceinline__ uint32_t w4_low_digits(uint32_t w) { return w & 0x33333333u; }
+__device__ __forceinline__ uint32_t w4_high_digits(uint32_t w) {
+  const uint32_t t = w >> 2;  // the upper two bits of a code in the lower two of its place
+  return (~w & 0x88888888u) | (~((w >> 1) | t) & 0x22222222u) | (t & 0x11111111u);
+}
+constexpr float W4_LOW = 0x1p-11f, W4_HIGH = 0x1p-9f;  // 2 and 8, times 2^-12
+constexpr float W4_INT_UNIT = 0x1p12f;
+
 // Where a stream's tokens come from: memory, each lane the elements that its products take (one token, which all
-// lanes of a group read); LDS (W4Stage), in the order that the steps take them; memory by whole lines, which the
-// wave turns in its own part of LDS.  The last is for groups of 16 tokens, where reading a lane's 16 bytes from a
+// lanes of a group read); LDS (W4Stage); memory by whole lines, which the wave turns in its own part of LDS.  The last is for groups of 16 tokens, where reading a lane's 16 bytes from a
 // token each costs more in the caches than the bytes do: 32 x 14336 -> 4096 int4 21.6 us, by lines 19.5; 13 x 2048 ->
 // 7168 7.0 and 6.4.
 enum { W4_XMEM = 0, W4_XLDS = 1, W4_XLINE = 2 };
@@ -139,7 +142,7 @@ struct W4Stream {
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const int t = 4 * i + (lane >> 4);
-        st16(xs + g * W4_XSLOT + t * 256 + 16 * ((lane & 15) ^ t), INT ? w4_order_int(v[g][i]) : v[g][i]);
+        st16(xs + g * W4_XSLOT + t * 256 + 16 * ((lane & 15) ^ t), v[g][i]);
       }
   }
   __device__ __forceinline__ u32x4 get(int g, int j) const {
@@ -150,8 +153,6 @@ struct W4Stream {
   __device__ __forceinline__ void mma(Codes& b, u32x4 (&xv)[NG][4], int steps, f32x4 (&acc)[RT][NG]) const {
     if constexpr (XLINE) put(xv);
     if constexpr (INT) {
-      constexpr uint32_t NEG = 0xbfc0bfc0u;  // -1.5, twice
-      const u32x4 neg = {NEG, NEG, NEG, NEG};
       if constexpr (TR) {
 #pragma unroll
         for (int r = 0; r < RT; ++r) w4_transpose(b.c[r]);
@@ -160,31 +161,29 @@ struct W4Stream {
       for (int h = 0; h < NS; ++h) {
         if (h * GS >= steps) break;
         u32x4 xi[NG][GS];
-        f32x4 part[RT][NG];
 #pragma unroll
-        for (int g = 0; g < NG; ++g) {
-          f32x4 corr = {0.0f, 0.0f, 0.0f, 0.0f};
+        for (int g = 0; g < NG; ++g)
 #pragma unroll
-          for (int j = 0; j < GS; ++j) {
-            xi[g][j] = XLINE ? get(g, h * GS + j) : XLDS ? xv[g][h * GS + j] : w4_order_int(xv[g][h * GS + j]);
-            corr = w4_mfma(xi[g][j], neg, corr);
-          }
-#pragma unroll
-          for (int r = 0; r < RT; ++r) part[r][g] = corr;
-        }
+          for (int j = 0; j < GS; ++j) xi[g][j] = XLINE ? get(g, h * GS + j) : xv[g][h * GS + j];
 #pragma unroll
         for (int r = 0; r < RT; ++r) {
+          f32x4 part[NG];
+#pragma unroll
+          for (int g = 0; g < NG; ++g) part[g] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
           for (int j = 0; j < GS; ++j) {
-            const u32x4 c = w4_unpack_int(b.c[r][h * GS + j]);
+            const uint32_t w8 = b.c[r][h * GS + j];
+            const u32x4 lo = w4_unpack_fp(w4_low_digits(w8), W4_LOW), hi = w4_unpack_fp(w4_high_digits(w8), W4_HIGH);
 #pragma unroll
-            for (int g = 0; g < NG; ++g) part[r][g] = w4_mfma(xi[g][j], c, part[r][g]);
+            for (int g = 0; g < NG; ++g) part[g] = w4_mfma(xi[g][j], lo, part[g]);
+#pragma unroll
+            for (int g = 0; g < NG; ++g) part[g] = w4_mfma(xi[g][j], hi, part[g]);
           }
           const float f = __uint_as_float(b.s[r][h] << 16);
 #pragma unroll
           for (int g = 0; g < NG; ++g)
 #pragma unroll
-            for (int i = 0; i < NI; ++i) acc[r][g][i] = fmaf(f, part[r][g][i], acc[r][g][i]);
+            for (int i = 0; i < NI; ++i) acc[r][g][i] = fmaf(f, part[g][i], acc[r][g][i]);
         }
       }
     } else {
@@ -259,7 +258,7 @@ struct W4Stream {
 #pragma unroll
       for (int r = 0; r < RT; ++r)
 #pragma unroll
-        for (int g = 0; g < NG; ++g) acc[r][g] *= 16.0f;  // codes went in as c / 16
+        for (int g = 0; g < NG; ++g) acc[r][g] *= W4_INT_UNIT;
     }
   }
   __device__ __forceinline__ void run(int a, int b, f32x4 (&acc)[RT][NG]) const { run(a, b, acc, [] {}); }
@@ -274,10 +273,9 @@ struct W4Stream {
   }
 };
 
-// Copies elements [k0, k1) (multiples of 32) of a token to LDS, for the calling wave's own use: INT in the
-// order of the codes.  The first 64 x 8 R elements pass through registers, so that other loads can be
-// issued between request() and write().
-template <int FMT, int R>
+// Copies elements [k0, k1) (multiples of 32) of a token to LDS, for the calling wave's own use.  The first 64 x 8 R
+// elements pass through registers, so that other loads can be issued between request() and write().
+template <int R>
 struct W4Stage {
   u32x4 v[R];
   const bf16* x;
@@ -295,11 +293,8 @@ struct W4Stage {
   __device__ __forceinline__ void write() const {
 #pragma unroll
     for (int i = 0; i < R; ++i)
-      if (k0 + 512 * i < k1) st16(lds + k0 + 512 * i, FMT == W4_INT ? w4_order_int(v[i]) : v[i]);
-    for (int k = k0 + 512 * R; k < k1; k += 512) {
-      const u32x4 u = ld16(x + k);
-      st16(lds + k, FMT == W4_INT ? w4_order_int(u) : u);
-    }
+      if (k0 + 512 * i < k1) st16(lds + k0 + 512 * i, v[i]);
+    for (int k = k0 + 512 * R; k < k1; k += 512) st16(lds + k, ld16(x + k));
   }
 };
 

@@ -95,8 +95,8 @@ enum { W4_OUT = 0, W4_GLU = 1, W4_PART = 2 };  // the epilogue; SwiGLU's; partia
 // reduction, which its waves share: blocks of 128 elements in contiguous runs.  The waves' results meet in LDS,
 // [wave][RT][NG][token][16], are added in wave order, and the epilogue runs on four columns of a token a thread.
 //
-// Up to 4 tokens (NI = 1) each wave copies its run of X to LDS, in the order that the products take it, so that
-// the memory path carries little but codes.  With more, X (16 tokens of a block: 4 KB for a tile's 1 KB of
+// Up to 4 tokens (NI = 1) each wave copies its run of X to LDS, so that the memory path carries little but
+// codes.  With more, X (16 tokens of a block: 4 KB for a tile's 1 KB of
 // codes) comes from L2 by whole lines, which bounds the kernel unless a wave takes several tiles of rows with each
 // block of X: 13 x 14336 -> 4096 took 17.3 us with RT = 1 and the whole reduction in a workgroup, 11.2 with RT = 4 and
 // four slices (to which joining them adds about 2).  What bounds it then is how short the work is: each wave has
@@ -144,7 +144,7 @@ __global__ __launch_bounds__(512) void k_w4_rows(const bf16* __restrict__ X, int
       for (int i = 0; i < 4; ++i)  // (below 2^29)
         ws.xo[g][i] = (uint32_t)min(16 * g + 4 * i + q, m - 1 - t0) * (uint32_t)(ldx * 2) + 16 * r16;
   }
-  W4Stage<FMT, 2> first;
+  W4Stage<2> first;
   if constexpr (XLDS) first.request(X, xl, a * W4_BLOCK, min(b * W4_BLOCK, K));
   f32x4 acc[RT][NG];
 #pragma unroll
@@ -156,7 +156,7 @@ __global__ __launch_bounds__(512) void k_w4_rows(const bf16* __restrict__ X, int
       if constexpr (XLDS) {
         first.write();
         for (int t = 1; t < m; ++t) {
-          W4Stage<FMT, 1> s;
+          W4Stage<1> s;
           s.request(X + t * ldx, xl + t * xp, a * W4_BLOCK, min(b * W4_BLOCK, K));
           s.write();
         }
@@ -278,7 +278,8 @@ __global__ __launch_bounds__(W4G_WAVES * 64, 2) void k_w4_tile(const bf16* __res
     float f[RT], f8[RT];
 #pragma unroll
     for (int r = 0; r < RT; ++r) {
-      if constexpr (INT) f[r] = in ? __uint_as_float(s[r] << 16) : 0.0f;
+      // (INT: a sixteenth of the scale, as 8 s may be beyond the range where 7 s is not; the end takes it back)
+      if constexpr (INT) f[r] = in ? 0.0625f * __uint_as_float(s[r] << 16) : 0.0f;
       else f[r] = !in ? 1.0f : __uint_as_float(s[r] ? s[r] << 23 : 0x00400000u);
       f8[r] = -8.0f * f[r];
     }
@@ -331,7 +332,7 @@ __global__ __launch_bounds__(W4G_WAVES * 64, 2) void k_w4_tile(const bf16* __res
 #pragma unroll
     for (int r = 0; r < RT; ++r)
 #pragma unroll
-      for (int i = 0; i < 4; ++i) res[(4 * q + i) * PITCH + 16 * r + r16] = acc[r][g][i];
+      for (int i = 0; i < 4; ++i) res[(4 * q + i) * PITCH + 16 * r + r16] = acc[r][g][i] * (INT ? 16.0f : 1.0f);
     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "workgroup");
     __builtin_amdgcn_wave_barrier();
     const int t = t0 + 16 * g + tok;
