@@ -288,6 +288,7 @@ __global__ __launch_bounds__(512) void k_dw4_expert(DecW4 a) {
 #pragma unroll
     for (int r = 0; r < RT; ++r) acc[r][0] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
     if (b0 < b1) ws.run(b0, b1, acc);
+    w4_lds_order();
 #pragma unroll
     for (int r = 0; r < RT; ++r) w4_put<4>(res + (wave * RT + r) * TILE, acc[r][0]);
     __syncthreads();

@@ -15,7 +15,7 @@
 // eight codes, the same conversions as for FP make them bf16, and a product is two MFMAs.  All products are exact, sums
 // fp32, the weights are never rounded, and a weight of zero adds nothing however large the token's element is.
 // (Codes as 1 + c / 16 and a product of the tokens with -1.5 to take the excess off are eight operations and fewer
-// MFMAs, 14.1 us for 13 x 14336 -> 4096 with groups of 128 where this takes 14.9 and level for one token, but every sum
+// MFMAs, 14.1 us for 13 x 14336 -> 4096 with groups of 128 where this takes 14.4 and level for one token, but every sum
 // carries rounding errors of 24 |x| s, and overflows for large finite x.)  The digits are scaled by 2^-12, which the end
 // takes back: 128 products of any finite x stay in range.
 //
@@ -36,6 +36,13 @@ __host__ __device__ __forceinline__ int w4_blocks(int K) { return (K + W4_BLOCK 
 // a: tokens, b: weights
 __device__ __forceinline__ f32x4 w4_mfma(u32x4 a, u32x4 b, f32x4 c) {
   return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
+}
+
+// Between LDS accesses of a wave's lanes to one another's places.  The LDS takes a wave's accesses in their order, so
+// nothing has to be waited for: this keeps the compiler from changing that order.
+__device__ __forceinline__ void w4_lds_order() {
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  __builtin_amdgcn_wave_barrier();
 }
 
 // Word j of lane group i becomes word i of lane group j (lane groups: lane / 16).
@@ -133,10 +140,11 @@ struct W4Stream {
         else v[g][j] = in ? ld16(x[g] + blk * W4_BLOCK + j * XS) : zero;
       }
   }
-  // XLINE: a block's elements from the order of memory to LDS, and the lane's of a step from there (the wave's LDS
-  // accesses stay in order)
+  // XLINE: a block's elements from the order of memory to LDS, where the lanes have read the last block's, and the
+  // lane's of a step from there
   __device__ __forceinline__ void put(const u32x4 (&v)[NG][4]) const {
     const int lane = threadIdx.x & 63;
+    w4_lds_order();
 #pragma unroll
     for (int g = 0; g < NG; ++g)
 #pragma unroll
@@ -144,6 +152,7 @@ struct W4Stream {
         const int t = 4 * i + (lane >> 4);
         st16(xs + g * W4_XSLOT + t * 256 + 16 * ((lane & 15) ^ t), v[g][i]);
       }
+    w4_lds_order();
   }
   __device__ __forceinline__ u32x4 get(int g, int j) const {
     const int lane = threadIdx.x & 63, r16 = lane & 15, q = lane >> 4;
@@ -295,6 +304,7 @@ struct W4Stage {
     for (int i = 0; i < R; ++i)
       if (k0 + 512 * i < k1) st16(lds + k0 + 512 * i, v[i]);
     for (int k = k0 + 512 * R; k < k1; k += 512) st16(lds + k, ld16(x + k));
+    w4_lds_order();
   }
 };
 

@@ -162,7 +162,9 @@ __global__ __launch_bounds__(512) void k_w4_rows(const bf16* __restrict__ X, int
         }
       }
     });
-  if constexpr (XLDS || RT < 4) __syncthreads();  // (the results take the tokens' place: with RT = 4 the wave's own)
+  // (the results take the tokens' place: with RT = 4 the wave's own)
+  if constexpr (XLDS || RT < 4) __syncthreads();
+  else w4_lds_order();
   float* res = reinterpret_cast<float*>(w4_lds);
   constexpr int TILE = TOK * 16;
 #pragma unroll
