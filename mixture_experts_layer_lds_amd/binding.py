@@ -212,6 +212,11 @@ def _stream(stream=None):
     return (stream if stream is not None else torch.cuda.current_stream()).cuda_stream
 
 
+def _stream_on(dev, stream):
+    """As _stream, where the current device is known."""
+    return _raw_stream(dev) if stream is None and _raw_stream is not None else _stream(stream)
+
+
 def _gp(t, dev):
     """Address of a tensor that GPU ``dev`` can read (None and addresses pass)."""
     if t is None or t.__class__ is int:
@@ -225,6 +230,64 @@ def _on_gpu(*tensors):
     dev = torch.cuda.current_device()
     for t in tensors:
         _gp(t, dev)
+
+
+_TYPES = {MOE_F32: torch.float32, MOE_BF16: torch.bfloat16}
+
+
+# The tensors that a call takes (None and addresses pass): what is as expected leaves by the first return, for 0.15 us of a
+# call's 6 each.
+def _gv(t, dev, dtype, n, name):
+    """Address of a contiguous tensor of at least n elements of dtype that GPU ``dev`` can read."""
+    if t is None or t.__class__ is int:
+        return t
+    if t.dtype is dtype and t.get_device() == dev and t.numel() >= n and t.is_contiguous():
+        return t.data_ptr()
+    _check_type(t, dtype, name)
+    if t.numel() < n or not t.is_contiguous():
+        raise MoEError(-1, "%s has %d elements (contiguous: %s), %d contiguous ones expected" % (name, t.numel(), t.is_contiguous(), n))
+    return _gp(t, dev)
+
+
+def _gm(t, dev, dtype, rows, cols, ld, name):
+    """Address of a tensor of ``rows`` rows of cols elements of dtype, ld elements apart (0: cols), as _gv."""
+    if t is None or t.__class__ is int:
+        return t
+    if t.dtype is dtype and t.get_device() == dev and t.numel() == rows * cols and (not ld or ld == cols) and t.is_contiguous():
+        return t.data_ptr()
+    _check_type(t, dtype, name)
+    _check_rows(t, rows, cols, ld or cols, name)
+    return _gp(t, dev)
+
+
+def _check_type(t, dtype, name):
+    if t.dtype is not dtype:
+        raise MoEError(-1, "%s is %s, %s expected" % (name, t.dtype, dtype))
+
+
+def _check_rows(t, rows, cols, ld, name):
+    size, step, dim = t.shape, t.stride(), t.dim()
+    if rows <= 0 or dim == 2 and step == (ld, 1) and size[0] >= rows and size[1] >= cols:
+        return
+    if dim and cols > 1 and size[-1] > 1 and step[-1] != 1:
+        raise MoEError(-1, "%s: neighbours in a row lie %d elements apart" % (name, step[-1]))
+    if dim > 1 and rows > 1 and size[-2] > 1 and step[-2] != ld and size[-1] > 1:
+        raise MoEError(-1, "%s: its rows lie %d elements apart, by the dims %d" % (name, step[-2], ld))
+    if dim > 2 and not t.is_contiguous() and any(step[i] != step[i + 1] * size[i + 1] for i in range(dim - 2) if size[i] > 1):
+        raise MoEError(-1, "%s: its rows do not lie at one distance" % name)
+    # (a view of the first columns of longer rows ends before the last row's stride does)
+    room = t.untyped_storage().nbytes() // t.element_size() - t.storage_offset()
+    if t.numel() < rows * cols or room < (rows - 1) * ld + cols:
+        raise MoEError(-1, "%s has %d elements, %d rows of %d (%d apart) expected" % (name, t.numel(), rows, cols, ld))
+
+
+def _gw(ws, dev, ws_bytes):
+    """Address of a workspace tensor of at least ws_bytes bytes, as _gv."""
+    if ws is None or ws.__class__ is int:
+        return ws
+    if ws.numel() * ws.element_size() < ws_bytes or not ws.is_contiguous():
+        raise MoEError(-1, "the workspace has %d bytes, not ws_bytes=%d" % (ws.numel() * ws.element_size(), ws_bytes))
+    return _gp(ws, dev)
 
 
 def _check(status):
@@ -519,9 +582,11 @@ def norm_workspace(dims, device="cuda"):
 def moe_norm(dims, x, residual, weight, bias, sum, y, mean, rstd, stream=None):
     """sum = x + residual, y = norm(sum) weight + bias, with the rows' mean and 1 / deviation; residual, weight,
     bias, sum, mean and rstd may be None."""
-    d = torch.cuda.current_device()
-    status = lib().moe_norm(ctypes.byref(dims), _gp(x, d), _gp(residual, d), _gp(weight, d), _gp(bias, d), _gp(sum, d),
-                            _gp(y, d), _gp(mean, d), _gp(rstd, d), _stream(stream))
+    d, t, w, n, c = torch.cuda.current_device(), _TYPES.get(dims.dtype), _TYPES.get(dims.wtype), dims.rows, dims.cols
+    status = lib().moe_norm(ctypes.byref(dims), _gm(x, d, t, n, c, dims.ldx, "x"), _gm(residual, d, t, n, c, dims.ldr, "residual"),
+                            _gv(weight, d, w, c, "weight"), _gv(bias, d, w, c, "bias"), _gm(sum, d, t, n, c, dims.lds, "sum"),
+                            _gm(y, d, t, n, c, dims.ldy, "y"), _gv(mean, d, torch.float32, n, "mean"),
+                            _gv(rstd, d, torch.float32, n, "rstd"), _stream_on(d, stream))
     if status:
         _check(status)
 
@@ -529,10 +594,13 @@ def moe_norm(dims, x, residual, weight, bias, sum, y, mean, rstd, stream=None):
 def moe_norm_backward(dims, dy, s, weight, mean, rstd, dsum, dx, dweight, dbias, ws, ws_bytes, stream=None):
     """Gradients of moe_norm from dy and the normalised sum s (x without a residual); dsum: the gradient that
     reaches s directly, or None; dx, dweight and dbias may be None."""
-    d = torch.cuda.current_device()
-    _check(lib().moe_norm_backward(ctypes.byref(dims), _gp(dy, d), _gp(s, d), _gp(weight, d), _gp(mean, d), _gp(rstd, d),
-                                   _gp(dsum, d), _gp(dx, d), _gp(dweight, d), _gp(dbias, d), _gp(ws, d), ws_bytes,
-                                   _stream(stream)))
+    d, t, w, n, c = torch.cuda.current_device(), _TYPES.get(dims.dtype), _TYPES.get(dims.wtype), dims.rows, dims.cols
+    f = torch.float32
+    _check(lib().moe_norm_backward(ctypes.byref(dims), _gm(dy, d, t, n, c, dims.ldy, "dy"), _gm(s, d, t, n, c, dims.lds, "s"),
+                                   _gv(weight, d, w, c, "weight"), _gv(mean, d, f, n, "mean"), _gv(rstd, d, f, n, "rstd"),
+                                   _gm(dsum, d, t, n, c, dims.ldr, "dsum"), _gm(dx, d, t, n, c, dims.ldx, "dx"),
+                                   _gv(dweight, d, f, c, "dweight"), _gv(dbias, d, f, c, "dbias"), _gw(ws, d, ws_bytes), ws_bytes,
+                                   _stream_on(d, stream)))
 
 
 class Gradients:
@@ -578,15 +646,18 @@ def grad_workspace(grads, device="cuda"):
 
 def moe_grad_norm(grads, norm, ws, ws_bytes, stream=None):
     """The global norm (fp32 [1]) of a list of gradients."""
-    _on_gpu(grads.table if grads.count else None, norm, ws)
-    _check(lib().moe_grad_norm(grads._ref, _p(norm), _p(ws), ws_bytes, _stream(stream)))
+    d = torch.cuda.current_device()
+    _gp(grads.table if grads.count else None, d)
+    _check(lib().moe_grad_norm(grads._ref, _gv(norm, d, torch.float32, 1, "norm"), _gw(ws, d, ws_bytes), ws_bytes, _stream_on(d, stream)))
 
 
 def moe_grad_clip(grads, max_norm, norm_in, norm, ws, ws_bytes, stream=None):
     """Gradients scaled down to a global norm of max_norm.  norm_in (fp32 [1]): the norm to use; None: it is
     computed and written to norm."""
-    _on_gpu(grads.table if grads.count else None, norm_in, norm, ws)
-    _check(lib().moe_grad_clip(grads._ref, max_norm, _p(norm_in), _p(norm), _p(ws), ws_bytes, _stream(stream)))
+    d = torch.cuda.current_device()
+    _gp(grads.table if grads.count else None, d)
+    _check(lib().moe_grad_clip(grads._ref, max_norm, _gv(norm_in, d, torch.float32, 1, "norm_in"),
+                               _gv(norm, d, torch.float32, 1, "norm"), _gw(ws, d, ws_bytes), ws_bytes, _stream_on(d, stream)))
 
 
 class W4:
@@ -663,10 +734,11 @@ def _w4_rows(w4, rows, K, name):
 def moe_linear_w4(dims, X, W, bias, residual, out, ws, ws_bytes, stream=None):
     """out = residual + act(X W^T + bias) with 4-bit weights W (a W4); bias and residual may be None."""
     _w4_rows(W, 2 * dims.N if dims.act == ACTS["swiglu"] else dims.N, dims.K, "W")
-    d = torch.cuda.current_device()
+    d, t, m, n = torch.cuda.current_device(), torch.bfloat16, dims.M, dims.N
     _gp(W.codes, d)
-    status = lib().moe_linear_w4(ctypes.byref(dims), _gp(X, d), W._ref, _gp(bias, d), _gp(residual, d), _gp(out, d), _gp(ws, d),
-                                 ws_bytes, _stream(stream))
+    status = lib().moe_linear_w4(ctypes.byref(dims), _gm(X, d, t, m, dims.K, dims.ldx, "X"), W._ref,
+                                 _gv(bias, d, torch.float32, W.rows, "bias"), _gm(residual, d, t, m, n, dims.ldr, "residual"),
+                                 _gm(out, d, t, m, n, dims.ldy, "out"), _gw(ws, d, ws_bytes), ws_bytes, _stream_on(d, stream))
     if status:
         _check(status)
 
@@ -676,9 +748,13 @@ def moe_decode_w4(dims, X, W_r, bias, W_gate, W_up, W_down, logits, topk_idx, to
     _w4_rows(W_gate, dims.E * dims.n, dims.d, "W_gate")
     _w4_rows(W_up, dims.E * dims.n, dims.d, "W_up")
     _w4_rows(W_down, dims.E * dims.d, dims.n, "W_down")
-    _on_gpu(X, W_r, bias, W_gate.codes, W_up.codes, W_down.codes, logits, topk_idx, topk_w, out, ws)
-    _check(lib().moe_decode_w4(ctypes.byref(dims), _p(X), _p(W_r), _p(bias), W_gate._ref, W_up._ref, W_down._ref, _p(logits),
-                               _p(topk_idx), _p(topk_w), _p(out), _p(ws), ws_bytes, _stream(stream)))
+    d, T, E, K, w, b, f = torch.cuda.current_device(), dims.T, dims.E, dims.K, dims.d, torch.bfloat16, torch.float32
+    for part in (W_gate, W_up, W_down):
+        _gp(part.codes, d)
+    _check(lib().moe_decode_w4(ctypes.byref(dims), _gv(X, d, b, T * w, "X"), _gv(W_r, d, b, E * w, "W_r"), _gv(bias, d, f, E, "bias"),
+                               W_gate._ref, W_up._ref, W_down._ref, _gv(logits, d, f, T * E, "logits"),
+                               _gv(topk_idx, d, torch.int32, T * K, "topk_idx"), _gv(topk_w, d, f, T * K, "topk_w"),
+                               _gv(out, d, b, T * w, "out"), _gw(ws, d, ws_bytes), ws_bytes, _stream_on(d, stream)))
 
 
 def moe_timing_enable(on):
