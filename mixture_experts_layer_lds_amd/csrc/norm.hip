@@ -543,12 +543,17 @@ static int norm_tpr(int64_t cols, int64_t rows, int many) {
   return tpr;
 }
 static int norm_threads(int tpr) { return tpr > 64 ? tpr : 256; }
-// Workgroups: eight waves a CU, which walk the rows; more of them only spread the accesses over more of memory's
-// pages (32768 x 7168 forward 327 us with 256 of 512 threads, 345 with 512; 16384 x 4096 89 us with 512 of 256
-// threads, 93 with 1024).
-static int norm_grid(int64_t rows, int tpr) {
+// Workgroups, which walk the rows: eight waves a CU, or sixteen where a row takes 1024 threads; more of them only spread the
+// accesses over more of memory's pages (32768 x 7168 forward 327 us with 256 of 512 threads, 345 with 512; 16384 x 4096
+// 89 us with 512 of 256 threads, 93 with 1024).  128 threads (many rows of over 1536 columns) are two waves: bf16 rows take 1024
+// workgroups (32768 x 2048 88 us, backward 98; with 512 109 and 118), fp32 rows, twice the bytes, 512 (16384 x 2048 104 us,
+// backward 104; with 1024 112 and 113), and so does a backward with less than four rows for each of 1024, since each
+// leaves a partial row of the vectors' gradients (2048 x 2048 bf16 17.7 us; with 1024 21.8).
+static int norm_grid(int64_t rows, int tpr, bool is_bf16, bool backward) {
   const int threads = norm_threads(tpr);
-  const int64_t most = threads >= 512 ? 256 : 512, need = cdiv(rows, threads / tpr);
+  int64_t most = threads >= 512 ? 256 : 512;
+  if (threads == 128 && is_bf16 && (!backward || rows >= 4 * 1024)) most = 1024;
+  const int64_t need = cdiv(rows, threads / tpr);
   return (int)(need < most ? need : most);
 }
 // Rows that the registers of 1024 threads do not hold: of the forward, and of the backward, where the vectors'
@@ -612,19 +617,19 @@ hipError_t launch_norm(const NormShape& s, const void* x, const void* residual, 
   a.cols = (int)s.cols;
   a.tpr = norm_tpr(s.cols, s.rows, NORM_FWD_MANY);
   a.eps = s.eps; a.wbf16 = s.wbf16; a.rms = s.rms;
-  return norm_launch(a, s.bf16, norm_grid(s.rows, a.tpr), st);
+  return norm_launch(a, s.bf16, norm_grid(s.rows, a.tpr, s.bf16, false), st);
 }
 
 static int norm_pitch(int64_t cols) { return (int)align_up((size_t)cols, 8); }
 size_t norm_bwd_workspace_bytes(const NormShape& s) {
   const int tpr = norm_tpr(s.cols, s.rows, NORM_BWD_MANY);
-  return (size_t)norm_grid(s.rows, tpr) * 2 * norm_pitch(s.cols) * sizeof(float);
+  return (size_t)norm_grid(s.rows, tpr, s.bf16, true) * 2 * norm_pitch(s.cols) * sizeof(float);
 }
 
 hipError_t launch_norm_bwd(const NormShape& s, const void* dy, const void* sum, const void* weight, const float* mean,
                            const float* rstd, const void* dsum, void* dx, float* dweight, float* dbias, void* ws,
                            hipStream_t st) {
-  const int tpr = norm_tpr(s.cols, s.rows, NORM_BWD_MANY), grid = norm_grid(s.rows, tpr);
+  const int tpr = norm_tpr(s.cols, s.rows, NORM_BWD_MANY), grid = norm_grid(s.rows, tpr, s.bf16, true);
   const bool vectors = dweight || dbias;
   float* part = static_cast<float*>(ws);
   if (s.rows > 0) {
