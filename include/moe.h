@@ -524,6 +524,10 @@ moe_status moe_dequantize_w4(int64_t rows, int64_t K, int dtype, const moe_w4* w
 enum { MOE_W4_STREAMED = 0, MOE_W4_TILED = 1, MOE_W4_EXPANDED = 2 };
 /* Host: the way of a product, for measurement tools and tests, or a negative moe_status. */
 int moe_linear_w4_plan(const moe_linear_dims* dims);
+/* Host: the same, and how the product is cut: row_tiles, the tiles of 16 rows of W that a workgroup (STREAMED) or wave
+ * (TILED) takes; token_groups, the groups of 16 tokens that it takes with them (0: up to 4 tokens, kept in LDS); slices
+ * of K that are joined afterwards.  EXPANDED: zeros.  Each pointer may be NULL. */
+int moe_linear_w4_cut(const moe_linear_dims* dims, int32_t* row_tiles, int32_t* token_groups, int32_t* slices);
 size_t moe_linear_w4_workspace_bytes(const moe_linear_dims* dims);
 moe_status moe_linear_w4(const moe_linear_dims* dims, const void* X, const moe_w4* W, const float* bias,
                          const void* residual, void* out, void* ws, size_t ws_bytes, void* stream);

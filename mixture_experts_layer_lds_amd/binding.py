@@ -43,7 +43,7 @@ EXPORTS = ["moe_max_rows", "moe_workspace_bytes", "moe_route", "moe_permute", "m
            "moe_norm", "moe_norm_workspace_bytes", "moe_norm_backward", "moe_grad_table_bytes", "moe_grad_table",
            "moe_grad_workspace_bytes", "moe_grad_norm",
            "moe_grad_clip", "moe_w4_scale_bytes", "moe_quantize_w4", "moe_dequantize_w4", "moe_linear_w4_workspace_bytes",
-           "moe_linear_w4_plan", "moe_linear_w4", "moe_decode_w4",
+           "moe_linear_w4_plan", "moe_linear_w4_cut", "moe_linear_w4", "moe_decode_w4",
            "moe_version", "moe_timing_enable", "moe_timing_read"]
 STAGES = ["router_gemm", "route", "tiles", "up_gemm", "down_gemm", "permute", "combine", "dact_gemm",
           "dw_down_gemm", "dw_gu_gemm", "dx_gemm", "router_bwd", "dwr_gemm", "decode", "fp8_quant",
@@ -154,12 +154,13 @@ def lib():
         L.moe_grad_workspace_bytes.argtypes, L.moe_grad_workspace_bytes.restype = [], sz
         L.moe_grad_norm.argtypes = [po, vp, vp, sz, vp]
         L.moe_grad_clip.argtypes = [po, ctypes.c_double, vp, vp, vp, sz, vp]
-        pw, ci = ctypes.POINTER(W4Struct), ctypes.c_int
+        pw, ci, pi = ctypes.POINTER(W4Struct), ctypes.c_int, ctypes.POINTER(i32)
         L.moe_w4_scale_bytes.argtypes, L.moe_w4_scale_bytes.restype = [i64, i64, i32, i32], i64
         L.moe_quantize_w4.argtypes = [i64, i64, ci, vp, pw, vp]
         L.moe_dequantize_w4.argtypes = [i64, i64, ci, pw, vp, vp]
         L.moe_linear_w4_workspace_bytes.argtypes, L.moe_linear_w4_workspace_bytes.restype = [pl], sz
         L.moe_linear_w4_plan.argtypes, L.moe_linear_w4_plan.restype = [pl], ci
+        L.moe_linear_w4_cut.argtypes, L.moe_linear_w4_cut.restype = [pl, pi, pi, pi], ci
         L.moe_linear_w4.argtypes = [pl, vp, pw, vp, vp, vp, vp, sz, vp]
         L.moe_decode_w4.argtypes = [pd, vp, vp, vp, pw, pw, pw, vp, vp, vp, vp, vp, sz, vp]
         for f in ("moe_norm", "moe_norm_backward", "moe_grad_table", "moe_grad_norm", "moe_grad_clip", "moe_quantize_w4", "moe_dequantize_w4",
@@ -724,6 +725,15 @@ def moe_linear_w4_plan(dims):
     if way < 0:
         _check(way)
     return W4_WAYS[way]
+
+
+def moe_linear_w4_cut(dims):
+    """(way, row tiles, token groups, slices) of a product on 4-bit weights."""
+    n = [ctypes.c_int32() for _ in range(3)]
+    way = lib().moe_linear_w4_cut(ctypes.byref(dims), *[ctypes.byref(v) for v in n])
+    if way < 0:
+        _check(way)
+    return (W4_WAYS[way],) + tuple(v.value for v in n)
 
 
 def _w4_rows(w4, rows, K, name):

@@ -202,7 +202,7 @@ hipError_t launch_linear_bwd(const LinShape& s, const void* dY, const void* X, c
 // dX += dL W_r for dense logit gradients dL [T][E_pad] in the element type
 hipError_t launch_logit_dx(const Shape& s, const void* dL, int E_pad, const void* W_r, void* dX, hipStream_t st);
 
-// ---- 4-bit weights (w4.hip, decode.hip) ----
+// ---- 4-bit weights (w4.hip, decode_w4.hip) ----
 struct W4View {
   const uint8_t* codes;
   const void* scales;
@@ -214,6 +214,10 @@ hipError_t launch_expand_w4(const W4View& w, int64_t rows, int64_t K, bool is_bf
 size_t linear_w4_workspace_bytes(const LinShape& s);
 enum { W4_STREAMED = 0, W4_TILED = 1, W4_EXPANDED = 2 };
 int linear_w4_plan(const LinShape& s);
+struct W4Cut {
+  int row_tiles, token_groups, slices;  // (token_groups 0: the tokens lie in LDS)
+};
+W4Cut linear_w4_cut(const LinShape& s);
 hipError_t launch_linear_w4(const LinShape& s, const void* X, const W4View& w, const float* bias, const void* residual, void* out,
                             void* ws, hipStream_t st);
 // launch_decode with the experts' weights in 4 bits (one format and group for the three)

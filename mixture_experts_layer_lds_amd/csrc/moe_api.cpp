@@ -1140,6 +1140,16 @@ int moe_linear_w4_plan(const moe_linear_dims* dims) {
   return linear_w4_plan(s);
 }
 
+int moe_linear_w4_cut(const moe_linear_dims* dims, int32_t* row_tiles, int32_t* token_groups, int32_t* slices) {
+  LinShape s;
+  MOE_TRY(check_linear_w4(dims, &s));
+  const W4Cut c = linear_w4_cut(s);
+  if (row_tiles) *row_tiles = c.row_tiles;
+  if (token_groups) *token_groups = c.token_groups;
+  if (slices) *slices = c.slices;
+  return linear_w4_plan(s);
+}
+
 moe_status moe_linear_w4(const moe_linear_dims* dims, const void* X, const moe_w4* W, const float* bias,
                          const void* residual, void* out, void* ws, size_t ws_bytes, void* stream) {
   LinShape s;

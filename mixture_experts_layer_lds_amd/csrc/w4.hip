@@ -466,6 +466,16 @@ int linear_w4_plan(const LinShape& s) {
   if (s.M > W4_TILE_ROWS) return W4_EXPANDED;
   return w4_plan(s).us < w4_tile_plan(s).us ? W4_STREAMED : W4_TILED;
 }
+W4Cut linear_w4_cut(const LinShape& s) {
+  const int way = linear_w4_plan(s);
+  if (way == W4_EXPANDED || s.M == 0) return W4Cut{0, 0, 0};
+  if (way == W4_TILED) {
+    const W4TilePlan t = w4_tile_plan(s);
+    return W4Cut{t.rt, W4G_NG, t.slices};
+  }
+  const W4Plan p = w4_plan(s);
+  return W4Cut{p.rt, p.lds ? 0 : p.ng, p.slices};
+}
 template <int FMT, int RT>
 static void w4_tile_rt(const LinShape& s, const W4TilePlan& p, const W4View& w, const bf16* X, const LinEpi<bf16>& ep, float* part,
                        hipStream_t st) {
