@@ -71,8 +71,9 @@ __device__ __forceinline__ double grad_square(const T* p, int n) {
   return v;
 }
 
+// o = p c[0] c[1]
 template <typename T>
-__device__ __forceinline__ void grad_scale(const T* p, T* o, int n, float c) {
+__device__ __forceinline__ void grad_scale(const T* p, T* o, int n, const float (&c)[2]) {
   constexpr int VEC = Vec<T>::N, U = 4;
   const int step = 256 * VEC;
   int k = threadIdx.x * VEC;
@@ -85,7 +86,7 @@ __device__ __forceinline__ void grad_scale(const T* p, T* o, int n, float c) {
       float f[VEC];
       unpack16<T>(r[u], f);
 #pragma unroll
-      for (int q = 0; q < VEC; ++q) f[q] *= c;
+      for (int q = 0; q < VEC; ++q) f[q] = f[q] * c[0] * c[1];
       grad_st16_nt(o + k + u * step, pack16<T>(f));
     }
   }
@@ -93,10 +94,10 @@ __device__ __forceinline__ void grad_scale(const T* p, T* o, int n, float c) {
     float f[VEC];
     unpack16<T>(grad_ld16_nt(p + k), f);
 #pragma unroll
-    for (int q = 0; q < VEC; ++q) f[q] *= c;
+    for (int q = 0; q < VEC; ++q) f[q] = f[q] * c[0] * c[1];
     grad_st16_nt(o + k, pack16<T>(f));
   }
-  for (int i = n / VEC * VEC + threadIdx.x; i < n; i += 256) o[i] = from_f32<T>(to_f32(p[i]) * c);
+  for (int i = n / VEC * VEC + threadIdx.x; i < n; i += 256) o[i] = from_f32<T>(to_f32(p[i]) * c[0] * c[1]);
 }
 
 // f(entry, first element of the chunk, elements in it)
@@ -146,7 +147,11 @@ __global__ __launch_bounds__(256) void k_grad_scale(const GradEntry* table, cons
   if (part && blockIdx.x == 0 && threadIdx.x == 0) *norm = (float)n;
   // a norm that is not a finite fp32 number (as the caller sees it) leaves the values as they are
   const bool cut = n > max_norm && (float)n < __builtin_inff();
-  const float c = cut ? (float)(max_norm / n) : 1.0f;
+  // a factor below fp32's normal range (a norm of 1e36 cut to 1e-6) would lose its digits: then it goes in two, the first a
+  // power of two
+  const double f = cut ? max_norm / n : 1.0;
+  const bool two = f < 0x1p-126;
+  const float c[2] = {two ? 0x1p-126f : 1.0f, (float)(two ? f * 0x1p126 : f)};
   grad_chunks(table, tensor, chunks, [&](const GradEntry& g, int64_t at, int m) {
     if (!cut && g.src == g.dst) return;
     if (g.kind & GRAD_BF16) grad_scale<bf16>(static_cast<const bf16*>(g.src) + at, static_cast<bf16*>(g.dst) + at, m, c);
