@@ -170,6 +170,23 @@ __device__ __forceinline__ void norm_row_sum(float (&v)[N], int tpr, float (*red
   half ^= 1;
 }
 
+// 1 / sqrt(q / n + eps) for a row's sum of squares q, inv = 1 / n.  Squares that leave fp32's range (elements over
+// 2^64, or of 2^-50 and less with an eps that does not hide them) are summed once more, as squares(s) of elements times
+// a power of two s: any finite row has its deviation.  v is the same in all threads of a row.
+template <class Squares>
+__device__ __forceinline__ float norm_rstd(float q, float inv, float eps, Squares squares) {
+  const float v = fmaf(q, inv, eps);
+  if (v >= 0x1p-100f && v <= 3.4028235e38f) return 1.0f / sqrtf(v);
+  const float s = v < 1.0f ? 0x1p100f : 0x1p-76f;
+  return s / sqrtf(fmaf(squares(s), inv, eps * s * s));
+}
+// A row's mean from its sum s; where that left fp32's range, from sum(2^-20), the sum of elements times 2^-20.
+template <class Sum>
+__device__ __forceinline__ float norm_mean(float s, float inv, Sum sum) {
+  if (fabsf(s) <= 3.4028235e38f) return s * inv;
+  return sum(0x1p-20f) * inv * 0x1p20f;
+}
+
 struct NormFwd {
   const void *x, *res, *w, *b;
   void *sum, *y;
@@ -228,7 +245,13 @@ __global__ __launch_bounds__(THREADS) void k_norm(NormFwd a) {
 #pragma unroll
       for (int i = 0; i < NC * 8; ++i) s[0] += f[i];  // (columns past the row hold zeros)
       norm_row_sum<1>(s, tpr, red, half);
-      mu = s[0] * inv;
+      mu = norm_mean(s[0], inv, [&](float scale) {
+        float z[1] = {0.0f};
+#pragma unroll
+        for (int i = 0; i < NC * 8; ++i) z[0] = fmaf(f[i], scale, z[0]);
+        norm_row_sum<1>(z, tpr, red, half);
+        return z[0];
+      });
     }
     float q[1] = {0.0f};
 #pragma unroll
@@ -240,7 +263,13 @@ __global__ __launch_bounds__(THREADS) void k_norm(NormFwd a) {
         q[0] = fmaf(d, d, q[0]);
       }
     norm_row_sum<1>(q, tpr, red, half);
-    const float rstd = 1.0f / sqrtf(fmaf(q[0], inv, a.eps));
+    const float rstd = norm_rstd(q[0], inv, a.eps, [&](float scale) {
+      float z[1] = {0.0f};
+#pragma unroll
+      for (int i = 0; i < NC * 8; ++i) z[0] = fmaf(f[i] * scale, f[i] * scale, z[0]);
+      norm_row_sum<1>(z, tpr, red, half);
+      return z[0];
+    });
     if (t == 0) {
       if (a.mean) a.mean[row] = mu;
       if (a.rstd) a.rstd[row] = rstd;
@@ -293,19 +322,32 @@ __global__ __launch_bounds__(1024) void k_norm_long(NormFwd a) {
       for (int i = 0; i < 8; ++i) s[0] += f[i];
     }
     norm_row_sum<1>(s, tpr, red, half);
-    const float mu = a.rms ? 0.0f : s[0] * inv;
-    float q[1] = {0.0f};
-    for (int j = 0; j < nc; ++j) {
-      float f[8];
-      again(j, f);
+    const float mu = a.rms ? 0.0f : norm_mean(s[0], inv, [&](float scale) {
+      float z[1] = {0.0f};
+      for (int j = 0; j < nc; ++j) {
+        float f[8];
+        again(j, f);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const float d = norm_col(j, tpr, t) + i < cols ? f[i] - mu : 0.0f;
-        q[0] = fmaf(d, d, q[0]);
+        for (int i = 0; i < 8; ++i) z[0] = fmaf(f[i], scale, z[0]);
       }
-    }
-    norm_row_sum<1>(q, tpr, red, half);
-    const float rstd = 1.0f / sqrtf(fmaf(q[0], inv, a.eps));
+      norm_row_sum<1>(z, tpr, red, half);
+      return z[0];
+    });
+    auto squares = [&](float scale) {
+      float z[1] = {0.0f};
+      for (int j = 0; j < nc; ++j) {
+        float f[8];
+        again(j, f);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const float d = norm_col(j, tpr, t) + i < cols ? (f[i] - mu) * scale : 0.0f;
+          z[0] = fmaf(d, d, z[0]);
+        }
+      }
+      norm_row_sum<1>(z, tpr, red, half);
+      return z[0];
+    };
+    const float rstd = norm_rstd(squares(1.0f), inv, a.eps, squares);
     if (t == 0) {
       if (a.mean) a.mean[row] = mu;
       if (a.rstd) a.rstd[row] = rstd;

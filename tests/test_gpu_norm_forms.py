@@ -130,3 +130,40 @@ def test_eps(cols, eps, dtype, kind):
     if eps == 0.0:  # rows of zeros have no direction
         B.moe_norm(dims, torch.zeros_like(x), None, None, None, None, y, None, None)
         assert bool(y.isnan().all())
+
+
+# rows in 8 lanes, in waves, in workgroups, of two chunks a thread of 1024, re-read
+@pytest.mark.parametrize("kind", ["layer", "rms"])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("cols", [5, 60, 264, 520, 1003, 1100, 7168, 9000, 16390])
+def test_rows_of_any_finite_size(cols, dtype, kind):
+    """Rows whose squares or sums leave fp32's range, up and down, beside rows that stay in it."""
+    sizes = [1.0, 1e19, 1e25, 1e37, 1e-12, 1e-20, 1e-30, 3.0, 1e30, 1e-36, 1e-3]
+    rows = 3 * len(sizes)
+    g = torch.Generator().manual_seed(cols)
+    x = torch.randn(rows, cols, generator=g, dtype=torch.float64).clamp_(-4, 4)
+    x[::3] += 2.0  # (means far from zero: the sum of 16390 elements of 2e37 is beyond the range, their mean is not)
+    x *= torch.tensor(sizes, dtype=torch.float64).repeat(3)[:, None]
+    x = x.to(DT[dtype]).cuda()
+    assert bool(x.isfinite().all())
+    w, b = torch.linspace(0.5, 1.5, cols, device="cuda"), torch.linspace(-1, 1, cols, device="cuda")
+    for eps in (0.0, 1e-30, 1e-5):
+        dims = B.make_norm_dims(rows, cols, dtype, kind, eps)
+        y, mean, rstd = torch.empty_like(x), torch.zeros(rows, device="cuda"), torch.empty(rows, device="cuda")
+        B.moe_norm(dims, x, None, w, b, None, y, mean, rstd)
+        X, e = f64(x), float(np.float32(eps))
+        rm, rr = ob.norm_stats(X, e, kind)
+        bm, br = tn.stat_bounds(X, rm, rr, e)
+        assert_within("mean", f64(mean), rm, bm + U32 * np.abs(rm))
+        # (below the normal range a step is 2^-149)
+        assert_within("rstd", f64(rstd), rr, br * rr + 2.0 ** -149)
+        ref = ob.norm(X, f64(w), f64(b), e, kind)
+        tiny = 2.0 ** -149 / rr[:, None] * np.abs(ref - f64(b))  # (rstd's last step, relative, and its part of y)
+        assert_within("y", f64(y), ref, tn.forward_bound(X, f64(w), f64(b), rm, rr, e, dtype, ref) + tiny)
+        # every row alone is the same: none reaches another
+        for r in range(0, rows, 7):
+            one = B.make_norm_dims(1, cols, dtype, kind, eps)
+            y1 = torch.empty(1, cols, dtype=DT[dtype], device="cuda")
+            B.moe_norm(one, x[r:r + 1].clone(), None, w, b, None, y1, None, None)
+            ok = tn.forward_bound(X[r:r + 1], f64(w), f64(b), rm[r:r + 1], rr[r:r + 1], e, dtype, ref[r:r + 1]) + tiny[r:r + 1]
+            assert_within("row %d alone" % r, f64(y1), ref[r:r + 1], ok)
