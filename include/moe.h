@@ -407,9 +407,9 @@ typedef struct moe_norm_dims {
  *  sum [rows,cols] or NULL (NULL without a residual): s rounded to dtype, for the next residual and the
  *  backward.  What is normalised is the rounded s, whether sum is given or not.
  *  y [rows,cols]; mean (LAYER; unused for RMS) and rstd [rows] fp32, or NULL where no backward follows.
- *  fp32 arithmetic, y is rounded once; rows of any finite size (with eps = 0 of zeros: NaN).  sum and y may each be x or residual (with the same stride), but
- *  not one another.  A row with infinities or NaN has NaN in y; other rows are untouched by it.  rows = 0
- *  does nothing. */
+ *  fp32 arithmetic, y is rounded once; rows of any finite size (with eps = 0, of zeros: NaN).  sum and y may each
+ *  be x or residual (with the same stride), but not one another.  A row with infinities or NaN has NaN in y; other
+ *  rows are untouched by it.  rows = 0 does nothing. */
 moe_status moe_norm(const moe_norm_dims* dims, const void* x, const void* residual, const void* weight,
                     const void* bias, void* sum, void* y, float* mean, float* rstd, void* stream);
 
@@ -515,10 +515,11 @@ moe_status moe_dequantize_w4(int64_t rows, int64_t K, int dtype, const moe_w4* w
  *  dims.dtype must be MOE_BF16 (X, residual, out); K a multiple of the group.  All sums are fp32.  A product goes
  *  one of three ways, by dims alone (moe_linear_w4_plan): STREAMED (up to 64 rows always), where products are exact
  *  and an INT4 group's sum is multiplied by its scale in fp32; TILED (some hundred rows) and EXPANDED (many), where
- *  an INT4 value is rounded to bf16 before it is multiplied (half a step, 2^-9 of it; FP4 values are exact).
+ *  an INT4 value is rounded to bf16 before it is multiplied (half a step, 2^-9 of it; FP4 values are exact): a caller
+ *  to whom that matters passes up to 64 rows a call.
  *  Any finite X is in range: a result is lost to infinity only where a weight, an INT4 group's sum times its scale, a
- *  partial sum of those or the result itself is beyond its type, and an element whose weight is zero adds nothing, however large.  An
- *  infinite element of X may make its row's results NaN where the exact sum is infinite.
+ *  partial sum of those or the result itself is beyond its type, and an element whose weight is zero adds nothing, however
+ *  large.  An infinite element of X may make its row's results NaN where the exact sum is infinite.
  *  residual may be out (with the same stride).  M = 0 does nothing.
  *  ws: moe_linear_w4_workspace_bytes(dims) bytes. */
 enum { MOE_W4_STREAMED = 0, MOE_W4_TILED = 1, MOE_W4_EXPANDED = 2 };
@@ -568,9 +569,9 @@ moe_status moe_decode(const moe_dims* dims, const void* X, const void* W_r, cons
 /* moe_decode_w4 — moe_decode with the experts' weights in 4 bits: W_gate, W_up (E n rows of d) and W_down
  * (E d rows of n), all three of one format and group.  dims.dtype must be MOE_BF16 (X, W_r, out); d and n
  * multiples of the group; plain top-K, T <= 1024.  Products are exact and sums fp32, as in moe_linear_w4's
- * streaming form; the SwiGLU activation is rounded to bf16 between the projections.  Routing is the same
- * function of the logits as moe_decode's.  It is a chain of three to five launches without grid-wide
- * barriers, so nothing has to be resident at once and there is no status to ask for.
+ * streaming form; the SwiGLU activation is rounded to bf16 between the projections, as moe_decode rounds it.
+ * Routing is the same function of the logits as moe_decode's.  It is a chain of three to five launches without
+ * grid-wide barriers, so nothing has to be resident at once and there is no status to ask for.
  *  ws: moe_workspace_bytes(dims, MOE_OP_DECODE) bytes, contents on entry unused. */
 moe_status moe_decode_w4(const moe_dims* dims, const void* X, const void* W_r, const float* bias,
                          const moe_w4* W_gate, const moe_w4* W_up, const moe_w4* W_down, float* logits,

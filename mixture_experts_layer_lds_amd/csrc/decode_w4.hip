@@ -12,11 +12,11 @@
 //   3. down: a workgroup takes 16 output columns of a token, its waves the token's experts; their results are
 //      added in ascending expert order with their weights, in LDS.
 // DeepSeek-V3-shaped layer, T = 1, fp4: 4.8 + 32 + 18 us for 191 MB (up at 3.9 TB/s, down at 3.7: each launch has
-// some 3 us of choosing, first loads and sums in which no codes arrive); fine-grained layer, T = 8: 3.7 + 11 + 7.
+// some 3 us of choosing, first loads and sums in which no codes arrive); fine-grained layer, T = 8, int4/64: 3.7 + 12 + 7.
 // By experts (more tokens): five launches.  1. router logits, which also clear the experts' counters; 2. top-K,
 // each pair appended to its expert's list (the order inside a list reaches no value); 3. gate/up and
 // 4. down on groups of 16 of an expert's tokens; 5. combine in ascending expert order.
-// d = 7168, n = 2048, E = 64, T = 16, fp4: 304 us for 1.24 GB, 4.1 TB/s.
+// d = 7168, n = 2048, E = 64, T = 16, fp4: 312 us for 1.33 GB, 4.3 TB/s.
 #include <cmath>
 
 #include "internal.h"

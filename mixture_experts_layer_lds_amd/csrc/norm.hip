@@ -11,8 +11,8 @@
 // difference of large sums.  All sums are fp32.
 //
 // Bound by memory: the forward reads x and r and writes s and y once, the backward reads dy, s and dsum and
-// writes dx.  32768 x 7168 bf16: forward 1.88 GB in 327 us (5.7 TB/s), backward 1.88 GB in 314 us (6.0 TB/s); 32768 x
-// 1536 backward 79 us (5.1 TB/s: the partial rows and the second launch are 5 us of it).  What brought them there: the
+// writes dx.  32768 x 7168 bf16: forward 1.88 GB in 327 us (5.7 TB/s), backward 1.88 GB in 319 us (5.9 TB/s); 32768 x
+// 1536 backward 78 us (5.1 TB/s: the partial rows and the second launch are 5 us of it).  What brought them there: the
 // next row requested while one is reduced, a grid that just fills the chip (norm_grid), lane sums by DPP.  One row of
 // 7168 is a launch: 3.3 us on the GPU.  A backward of some hundred rows is bound by its chain of launch, row, sums and
 // second launch: 999 x 1003 fp32 12.8 us, 3 at the rate of a copy.
@@ -21,7 +21,7 @@
 namespace moe {
 
 // Rows are accessed in 16 bytes whatever their alignment (their strides may be any; 30000 x 1600 bf16 of stride
-// 1603 by elements took 704 us, so 103): with a part of a chunk at the row's end, or in whole chunks throughout.
+// 1603 by elements took 704 us, so 89, dense ones 70): with a part of a chunk at the row's end, or in whole chunks throughout.
 enum { NORM_PART = 0, NORM_WHOLE = 1 };
 typedef u32x4 __attribute__((aligned(2))) u32x4_any;
 __device__ __forceinline__ u32x4 norm_ld16(const void* p) {

@@ -72,9 +72,9 @@ constexpr float W4_LOW = 0x1p-11f, W4_HIGH = 0x1p-9f;  // 2 and 8, times 2^-12
 constexpr float W4_INT_UNIT = 0x1p12f;
 
 // Where a stream's tokens come from: memory, each lane the elements that its products take (one token, which all
-// lanes of a group read); LDS (W4Stage); memory by whole lines, which the wave turns in its own part of LDS.  The last is for groups of 16 tokens, where reading a lane's 16 bytes from a
-// token each costs more in the caches than the bytes do: 32 x 14336 -> 4096 int4 21.6 us, by lines 19.5; 13 x 2048 ->
-// 7168 7.0 and 6.4.
+// lanes of a group read); LDS (W4Stage); memory by whole lines, which the wave turns in its own part of LDS.  The
+// last is for groups of 16 tokens, where reading a lane's 16 bytes from a token each costs more in the caches than the
+// bytes do: a tenth of the whole with 32 x 14336 -> 4096 and 13 x 2048 -> 7168.
 enum { W4_XMEM = 0, W4_XLDS = 1, W4_XLINE = 2 };
 constexpr int W4_XSLOT = 16 * 256;  // bytes of LDS per wave and group with W4_XLINE: [token][chunk ^ token]
 

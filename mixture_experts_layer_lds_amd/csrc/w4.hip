@@ -98,8 +98,8 @@ enum { W4_OUT = 0, W4_GLU = 1, W4_PART = 2 };  // the epilogue; SwiGLU's; partia
 // Up to 4 tokens (NI = 1) each wave copies its run of X to LDS, so that the memory path carries little but
 // codes.  With more, X (16 tokens of a block: 4 KB for a tile's 1 KB of
 // codes) comes from L2 by whole lines, which bounds the kernel unless a wave takes several tiles of rows with each
-// block of X: 13 x 14336 -> 4096 took 17.3 us with RT = 1 and the whole reduction in a workgroup, 11.2 with RT = 4 and
-// four slices (to which joining them adds about 2).  What bounds it then is how short the work is: each wave has
+// block of X: 13 x 14336 -> 4096 int4 took 17.3 us with RT = 1 and the whole reduction in a workgroup where RT = 4 and
+// four slices took 11.2 (12 since a code goes in as two digits; joining the slices adds about 2).  What bounds it then is how short the work is: each wave has
 // 3 or 4 blocks, so asking for the first (about 2 us) and the waves' sums are half of its time; two blocks more under way
 // gave nothing.
 //   One token: the codes alone.  7168 -> 2048 SwiGLU fp4 (15.6 MB) 6.6 us a call, 2.4 TB/s, 14336 columns (62 MB) 16.1,
@@ -207,7 +207,7 @@ __global__ __launch_bounds__(512) void k_w4_rows(const bf16* __restrict__ X, int
 // one does not wait for the loads into the other.
 //   Bound by LDS: every wave reads the whole block of X, 32 KB against 64 MFMAs of 16 cycles (RT = 2).  Two
 // workgroups a CU hide each other's waits: eight waves on a ring of four slots, one workgroup a CU, took 26 us where
-// this takes 19 (256 x 2048 -> 7168).  777 x 2048 -> 7168 36.5 us (625 TFLOP/s); expanding W first 42.5.
+// this takes 19 (256 x 2048 -> 7168).  777 x 2048 -> 7168 int4/32 40 us (570 TFLOP/s), int4/128 38, fp4 33.
 constexpr int W4G_TOK = 128, W4G_NG = W4G_TOK / 16, W4G_WAVES = 4, W4G_SLOT = W4G_TOK * 256;
 constexpr int W4G_DMA = W4G_SLOT / 1024 / W4G_WAVES;  // direct loads of a wave per block
 
