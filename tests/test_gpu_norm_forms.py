@@ -135,7 +135,7 @@ def test_eps(cols, eps, dtype, kind):
 # rows in 8 lanes, in waves, in workgroups, of two chunks a thread of 1024, re-read
 @pytest.mark.parametrize("kind", ["layer", "rms"])
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
-@pytest.mark.parametrize("cols", [5, 60, 264, 520, 1003, 1100, 7168, 9000, 16390])
+@pytest.mark.parametrize("cols", [5, 60, 100, 200, 264, 520, 1003, 1100, 7168, 9000, 16390])
 def test_rows_of_any_finite_size(cols, dtype, kind):
     """Rows whose squares or sums leave fp32's range, up and down, beside rows that stay in it."""
     sizes = [1.0, 1e19, 1e25, 1e37, 1e-12, 1e-20, 1e-30, 3.0, 1e30, 1e-36, 1e-3]

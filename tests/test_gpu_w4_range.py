@@ -76,19 +76,19 @@ def test_a_large_element_on_weights_of_zero_adds_nothing(M, N, K, fmt, group):
 @pytest.mark.parametrize("M,K", [(1, 256), (4, 256), (13, 256), (40, 256), (300, 2048), (1100, 256)])
 @pytest.mark.parametrize("group", [32, 64, 128])
 def test_int4_products_over_the_finite_range(M, K, group):
-    """The codes that quantisation gives times its largest scales with small tokens, and the largest tokens under small
-    scales: where (c - 8) s and its product with x are finite numbers, that is the result."""
+    """The codes that quantisation gives times its largest scales with small tokens, the largest tokens under small scales
+    and the smallest ones (subnormal digit products) under large scales: where (c - 8) s and its product with x are finite numbers, that is the result."""
     N = 4096
     codes = np.full((N, K), 8, np.uint8)
     row = np.arange(N)
     codes[row, row % K] = 1 + (row + row // K) % 15  # one element a row that counts, in every place of a block in turn
-    for scale, x0 in ((4.8e37, 2.0 ** -40), (-4.8e37, 3.0 * 2.0 ** -50), (2.0 ** -10, 3.3e38), (-(2.0 ** -10), -3.3e38)):
+    for scale, x0 in ((4.8e37, 2.0 ** -40), (-4.8e37, 3.0 * 2.0 ** -50), (2.0 ** -10, 3.3e38), (-(2.0 ** -10), -3.3e38), (2.0 ** 60, 2.0 ** -126)):
         s = ow.bf16(np.full((N, K // group), scale, np.float32))
         (w,) = pack(codes, s, "int4", group)
         x = torch.full((M, K), x0).bfloat16()
         got, _ = linear(x.cuda(), w, N)
         ref = f64(x) @ ow.values(codes, s, "int4").T   # (one product that is not zero: exact)
-        assert np.abs(ref).max() > 1e20
+        assert np.abs(ref).max() > 2.0 ** -70
         # (7 s and the like are rounded to bf16 beyond 64 rows)
         assert_within("scale %g, x %g" % (scale, x0), f64(got), ref, 2.01 * HALF["bf16"] * np.abs(ref))
 
